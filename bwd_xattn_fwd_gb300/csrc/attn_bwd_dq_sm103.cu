@@ -16,6 +16,8 @@
 //   dS = P (dP - D_i)                          are registers) -> bf16 into TMEM
 //   dQ_m += dS K_n            (A = dS from TMEM, B = K_n from shared memory)
 // dQ = scale * accumulator (the softmax scale is applied once, at the end).
+// Window with sinks (kWin): query i sees key j <= i only if i - j < window or j < sinks;
+// the CTA walks the sink tiles and the tiles from the first one its window reaches.
 #include "sm103_ptx.cuh"
 #include "xattn_internal.h"
 
@@ -62,13 +64,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
 // S and dP are each released (s_free, dp_free) as soon as both groups have loaded their
 // columns, so the next tile's products overlap this tile's arithmetic; the dS slot is
 // rewritten only after dQ(n-1) has read it (dq_done).
-template <int HD>
+template <int HD, bool kWin>
 __global__ void __maxnreg__(168)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                        const float *__restrict__ lse, const float *__restrict__ Dvec,
                        __nv_bfloat16 *__restrict__ dq, int B, int S, int nh, int nkv, float scale,
-                       int *status, unsigned long long timeout_ns) {
+                       int window, int sinks, int *status, unsigned long long timeout_ns) {
   using L = DqLayout<HD>;
   constexpr int kDqStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -83,7 +85,12 @@ __global__ void __maxnreg__(168)
   const int bh = static_cast<int>(blockIdx.x) % BH;
   const int b = bh / nh, h = bh % nh;
   const int kvh = h / (nh / nkv);
-  const int T = m + 1;                      // key tiles n = 0 .. m
+  // Key tiles: n = 0 .. m, or (kWin) `heads` sink tiles and then lo .. m; a role's counter
+  // n indexes this list, tile_at gives the key tile.
+  const int lo = kWin ? max(m * kTileRows - window + 1, 0) / kTileRows : 0;
+  const int heads = kWin ? min((sinks + kTileRows - 1) / kTileRows, lo) : 0;
+  const int T = heads + m - lo + 1;
+  auto tile_at = [heads, lo](int n) { return kWin && n >= heads ? n - heads + lo : n; };
 
   const uint32_t sQ = smem_u32(smem + L::kQ);
   const uint32_t sdO = smem_u32(smem + L::kdO);
@@ -160,8 +167,8 @@ __global__ void __maxnreg__(168)
       if (!warp_wait(empty(s), (use & 1) ^ 1, ctl)) break;
       mbar_expect_tx_elect(full(s), 2 * L::kTileBytes);
       XATTN_DCHECK(kvh < nkv && s < kDqStages, status);
-      load_tile(sK + s * L::kTileBytes, &mk, full(s), kvh, n * kTileRows, b);
-      load_tile(sV + s * L::kTileBytes, &mv, full(s), kvh, n * kTileRows, b);
+      load_tile(sK + s * L::kTileBytes, &mk, full(s), kvh, tile_at(n) * kTileRows, b);
+      load_tile(sV + s * L::kTileBytes, &mv, full(s), kvh, tile_at(n) * kTileRows, b);
       issued = n + 1;
       if (++s == kDqStages) { s = 0; ++use; }
     }
@@ -245,7 +252,12 @@ __global__ void __maxnreg__(168)
     const float nD = ig < S ? -Dvec[row] : 0.f;
     bool ok = true;
     for (int n = 0; n < T; ++n) {
-      const bool diag = (n == m);
+      const int kt = tile_at(n);                      // key tile
+      // Edge tiles (the diagonal; kWin: also the window's far edge and sink tiles behind
+      // it): this row sees key columns far .. near of the tile, and those before sk.
+      const bool diag = kt == m || (kWin && min(m * kTileRows + kTileRows, S) - kt * kTileRows > window && (kt + 1) * kTileRows > sinks);
+      const int near = kt == m ? i : kTileRows - 1;
+      const int far = kWin ? (m - kt) * kTileRows + i - window + 1 : 0, sk = kWin ? sinks - kt * kTileRows : 0;
       // P = exp2(S scale log2e - LSE log2e) for this group's 64 columns, in fp32.
       if (!warp_wait(s_full, n & 1, ctl)) { ok = false; break; }
       tc_fence_after();
@@ -262,9 +274,10 @@ __global__ void __maxnreg__(168)
         ffma2(x0, x1, __uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]), scale_log2, scale_log2,
               nlse2, nlse2);
         float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        if (diag) {                                   // key c0 + c > query i is masked
-          if (c0 + 2 * e > i) p0 = 0.f;
-          if (c0 + 2 * e + 1 > i) p1 = 0.f;
+        if (diag) {
+          const int c = c0 + 2 * e;
+          if (c > near || (kWin && c < far && c >= sk)) p0 = 0.f;
+          if (c + 1 > near || (kWin && c + 1 < far && c + 1 >= sk)) p1 = 0.f;
         }
         p[2 * e] = __float_as_uint(p0);
         p[2 * e + 1] = __float_as_uint(p1);
@@ -336,19 +349,34 @@ __global__ void __maxnreg__(168)
   }
 }
 
-template <int HD>
+template <int HD, bool kWin>
 cudaError_t launch_dq_hd(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                          const CUtensorMap &mdo, const float *lse, const float *D, __nv_bfloat16 *dq,
-                         int B, int S, int nh, int nkv, float scale, int *status, uint64_t timeout_ns,
-                         cudaStream_t stream) {
+                         int B, int S, int nh, int nkv, float scale, int window, int sinks, int *status,
+                         uint64_t timeout_ns, cudaStream_t stream) {
   using L = DqLayout<HD>;
-  cudaError_t err = cudaFuncSetAttribute(attn_bwd_dq_kernel<HD>,
+  cudaError_t err = cudaFuncSetAttribute(attn_bwd_dq_kernel<HD, kWin>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynBytes);
   if (err != cudaSuccess) return err;
   const int num_m = (S + kTileRows - 1) / kTileRows;
   const unsigned grid = static_cast<unsigned>(B) * nh * num_m;
-  return launch_pdl(attn_bwd_dq_kernel<HD>, grid, kDqThreads, L::kDynBytes, stream, mq, mk, mv, mdo, lse, D, dq,
-                    B, S, nh, nkv, scale, status, timeout_ns);
+  return launch_pdl(attn_bwd_dq_kernel<HD, kWin>, grid, kDqThreads, L::kDynBytes, stream, mq, mk, mv, mdo, lse, D, dq,
+                    B, S, nh, nkv, scale, window, sinks, status, timeout_ns);
+}
+
+template <bool kWin>
+cudaError_t launch_dq(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mdo,
+                      const float *lse, const float *D, __nv_bfloat16 *dq, int B, int S, int nh, int nkv, int hd,
+                      float scale, int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream) {
+#define XATTN_DQ_HD(HD)                                                                                            \
+  if (hd == HD)                                                                                                    \
+    return launch_dq_hd<HD, kWin>(mq, mk, mv, mdo, lse, D, dq, B, S, nh, nkv, scale, window, sinks, status,        \
+                                  timeout_ns, stream)
+  XATTN_DQ_HD(64);
+  XATTN_DQ_HD(32);
+  XATTN_DQ_HD(128);
+#undef XATTN_DQ_HD
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -357,13 +385,15 @@ cudaError_t launch_bwd_dq_bf16(const CUtensorMap &mq, const CUtensorMap &mk, con
                                const CUtensorMap &mdo, const float *lse, const BwdWorkspace &ws,
                                __nv_bfloat16 *dq, int B, int S, int nh, int nkv, int hd, float scale,
                                int *status, uint64_t timeout_ns, cudaStream_t stream) {
-  if (hd == 64)
-    return launch_dq_hd<64>(mq, mk, mv, mdo, lse, ws.D, dq, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  if (hd == 32)
-    return launch_dq_hd<32>(mq, mk, mv, mdo, lse, ws.D, dq, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  if (hd == 128)
-    return launch_dq_hd<128>(mq, mk, mv, mdo, lse, ws.D, dq, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  return cudaErrorInvalidValue;
+  return launch_dq<false>(mq, mk, mv, mdo, lse, ws.D, dq, B, S, nh, nkv, hd, scale, 0, 0, status, timeout_ns, stream);
+}
+
+cudaError_t launch_window_bwd_dq_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                      const CUtensorMap &mdo, const float *lse, const BwdWorkspace &ws,
+                                      __nv_bfloat16 *dq, int B, int S, int nh, int nkv, int hd, float scale,
+                                      int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream) {
+  return launch_dq<true>(mq, mk, mv, mdo, lse, ws.D, dq, B, S, nh, nkv, hd, scale, window, sinks, status, timeout_ns,
+                         stream);
 }
 
 }  // namespace xattn

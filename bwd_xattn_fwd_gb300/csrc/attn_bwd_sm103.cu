@@ -253,15 +253,38 @@ __device__ __forceinline__ uint32_t ds_offset(int j, int i) {
 // pass, and dQ is reproducible. dq: the bf16 output (resident mode only).
 //
 // kDsTmem (fused dQ, not resident): dK reads dS^T from TMEM (see below).
-template <int HD, bool kFusedDq, bool kResident = false, bool kDsTmem = false>
+//
+// kWin: query i sees key j <= i only if i - j < window or j < sinks. Key tile n then
+// meets the query tiles m = n .. last_query_tile(n), and a tile that holds a sink all of
+// them up to the last: its walk is cut into parts of win.part_tiles query tiles, each a
+// unit of its own, or one (batch, kv head)'s sink tile would be the longest chain of the
+// launch by far. A part writes its dV and dK sums in fp32 to win.parts, and
+// window_parts_kernel adds the parts in order (no atomics; the result is reproducible).
+struct WinArgs {
+  int window, sinks;       // 1 <= window <= S, 0 <= sinks <= S
+  int nparts, part_tiles;  // parts of a sink tile's walk (1: written straight to dv, dk)
+  float *parts;            // [B nkv, sink tiles, nparts, dV / dK, 128 rows, hd]
+};
+
+__host__ __device__ inline int window_sink_tiles(int sinks) { return (sinks + kTileRows - 1) / kTileRows; }
+
+// Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 31);
+  return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
+template <int HD, bool kFusedDq, bool kResident = false, bool kDsTmem = false, bool kWin = false>
 __global__ void __maxnreg__(168)
     attn_bwd_main_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                          const __grid_constant__ CUtensorMap maux, const __grid_constant__ CUtensorMap mdq,
                          __nv_bfloat16 *__restrict__ dk,
                          __nv_bfloat16 *__restrict__ dv, __nv_bfloat16 *__restrict__ dq, int B, int S, int nh,
-                         int nkv, float scale, int *status, unsigned long long timeout_ns) {
+                         int nkv, float scale, const WinArgs win, int *status, unsigned long long timeout_ns) {
   static_assert(kFusedDq || !kResident, "the resident dQ is a fused-dQ mode");
+  static_assert(!kWin || !kResident, "the resident dQ takes whole heads");
   using L = BwdLayout<HD, kFusedDq>;
   constexpr int kQS = L::kQStages, kOS = L::kOStages;
   // kDsTmem (fused dQ, not resident): the dS warps also write dS^T in bf16 over the
@@ -292,7 +315,10 @@ __global__ void __maxnreg__(168)
   const int num_m = (S + kTileRows - 1) / kTileRows;
   const int BK = B * nkv;
   const int group = nh / nkv;
-  const int num_units = num_m * BK;
+  const int sink_tiles = kWin ? window_sink_tiles(win.sinks) : 0;
+  // Units of one (batch, kv head): its key tiles, the sink tiles once per part.
+  const int per_bk = kWin ? sink_tiles * win.nparts + num_m - sink_tiles : num_m;
+  const int num_units = per_bk * BK;
   const bool head_major = kResident || group == 1;
   const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
   // Resident dQ: CTA c takes heads c, c + G, ... and each head's key tiles in order.
@@ -301,12 +327,24 @@ __global__ void __maxnreg__(168)
     return k * G + ((k & 1) ? G - 1 - cta : cta);
   };
   int n = 0, b = 0, kvh = 0, per_head = 0, T = 0;
+  int m0 = 0, part = 0;                   // kWin: first query tile; part of the sink tile's walk
   auto set_unit = [&](int u) {
-    const int bk = head_major ? u / num_m : u % BK;
-    n = head_major ? u % num_m : u / BK;
+    const int bk = head_major ? u / per_bk : u % BK;
+    n = head_major ? u % per_bk : u / BK;
     b = bk / nkv;
     kvh = bk % nkv;
-    per_head = num_m - n;                 // query tiles m = n .. num_m-1
+    if constexpr (kWin) {
+      const int split = sink_tiles * win.nparts, e = n;
+      n = e < split ? e / win.nparts : e - split + sink_tiles;
+      part = e < split ? e % win.nparts : 0;
+      m0 = e < split ? n + part * win.part_tiles : n;
+      const int m1 = e < split ? min(m0 + win.part_tiles, num_m)
+                               : min((n * kTileRows + kTileRows - 1 + win.window - 1) / kTileRows + 1, num_m);
+      per_head = max(m1 - m0, 0);         // a part past the end has nothing to do
+    } else {
+      m0 = n;
+      per_head = num_m - n;               // query tiles m = n .. num_m-1
+    }
     T = group * per_head;                 // iterations (r, m)
   };
 
@@ -436,6 +474,18 @@ __global__ void __maxnreg__(168)
     }
   };
 
+  // kWin: columns c .. c + 15 of row j of this part's dV (which = 0) or dK (1) sums, fp32.
+  auto store_part = [&](int which, int j, int c, const uint32_t *v, float mult) {
+    const size_t slot = (static_cast<size_t>(b * nkv + kvh) * sink_tiles + n) * win.nparts + part;
+    float4 *dst = reinterpret_cast<float4 *>(win.parts + ((2 * slot + which) * kTileRows + j) * HD + c);
+    XATTN_DCHECK(slot < static_cast<size_t>(BK) * sink_tiles * win.nparts, status);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      dst[e] = make_float4(__uint_as_float(v[4 * e]) * mult, __uint_as_float(v[4 * e + 1]) * mult,
+                           __uint_as_float(v[4 * e + 2]) * mult, __uint_as_float(v[4 * e + 3]) * mult);
+  };
+  (void)store_part;
+
   if (warp == 0) {
     // ---------------- TMA producer (converged warp, one elected lane issues) ----------------
     // The Q / dO rings run on across units. A unit's first kOStages ring loads only need
@@ -446,7 +496,7 @@ __global__ void __maxnreg__(168)
     int issued_q = 0, issued_o = 0, units = 0;
     int g = 0, sq = 0, uq = 0, so = 0, uo = 0;
     auto load_ring = [&](int t) -> bool {
-      const int h = kvh * group + t / per_head, m = n + t % per_head;
+      const int h = kvh * group + t / per_head, m = m0 + t % per_head;
       if (!warp_wait(q_empty(sq), (uq & 1) ^ 1, ctl)) return false;
       mbar_expect_tx_elect(q_full(sq), L::kTileBytes + L::kAuxTileBytes);
       load_tile(sQ + sq * L::kTileBytes, &mq, q_full(sq), h, m * kTileRows, b);
@@ -468,6 +518,7 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       set_unit(u);
+      if (kWin && T == 0) continue;
       const int pre = T < kOS ? T : kOS;
       for (int t = 0; ok && t < pre; ++t) ok = load_ring(t);
       if (!ok || !warp_wait(acc_done, (units - 1) & 1, ctl)) break;
@@ -554,6 +605,7 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       set_unit(u);
+      if (kWin && T == 0) continue;
       // The unit's first score product: K and V have landed, and this side's warps have
       // read the previous score tile (the last one of the previous unit).
       // kDsTmem, dS side: the previous dP^T columns hold the last dS^T, which this warp's
@@ -631,7 +683,7 @@ __global__ void __maxnreg__(168)
               // product waits for the previous head's dQ read-out.
               if (n == 0 && t == 0 && !warp_wait(dqt_free, (heads - 1) & 1, ctl)) { ok = false; break; }
               tc_fence_after();
-              const uint32_t col = static_cast<uint32_t>(((t / per_head) * num_m + n + t % per_head) * HD);
+              const uint32_t col = static_cast<uint32_t>(((t / per_head) * num_m + m0 + t % per_head) * HD);
               XATTN_DCHECK(col + HD <= 64u, status);     // the resident dQ tiles fit columns [448, 512)
               if (elect_one()) {
 #pragma unroll
@@ -686,11 +738,12 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       set_unit(u);
+      if (kWin && T == 0) continue;
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
         if (!warp_wait(dqs_full(g % L::kdSTiles), (g / L::kdSTiles) & 1, ctl)) { ok = false; break; }
         if (lane == 0) {
-          const int h = kvh * group + t / per_head, m = n + t % per_head;
+          const int h = kvh * group + t / per_head, m = m0 + t % per_head;
           const uint32_t src = smem_u32(sdS_ptr + (g % L::kdSTiles) * L::kdSBytes);
           // fp32 box: the innermost coordinates 0 and HD/2 are 16-byte multiples.
           XATTN_DCHECK(h < nh && m < num_m && (HD / 2) % 4 == 0 && src >= sdS &&
@@ -718,10 +771,20 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       set_unit(u);
+      if (kWin && T == 0) continue;
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
-        const int m = n + t % per_head;
-        const bool diag = (m == n);
+        const int m = m0 + t % per_head;
+        // kWin: the masked copy also takes the tiles at the window's far edge and what a sink
+        // tile has behind it. Key row j sees the query columns lo_col .. hi_col.
+        const bool diag = kWin ? (m == n || (min(m * kTileRows + kTileRows, S) - n * kTileRows > win.window &&
+                                             (n + 1) * kTileRows > win.sinks))
+                               : (m == n);
+        const int lo_col = m == n ? j : 0;
+        const int hi_col = (kWin && n * kTileRows + j >= win.sinks) ? win.window - 1 + j - (m - n) * kTileRows
+                                                                    : kTileRows - 1;
+        (void)lo_col;
+        (void)hi_col;
         if (!warp_wait(s_full, g & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         // The whole row of S^T(t) comes into registers with one TMEM read and the buffer is
@@ -741,6 +804,16 @@ __global__ void __maxnreg__(168)
         // i < key row j is masked (P = 0); the common body has no mask.
         auto chunk = [&](auto masked, auto chunk_index, uint32_t *pk) {
           constexpr int c = decltype(chunk_index)::value;
+          uint32_t vis = 0;
+          if constexpr (kWin && decltype(masked)::value) {
+            vis = bit_range(lo_col - 32 * c, hi_col - 32 * c);
+            if (!__any_sync(0xffffffffu, vis != 0u)) {   // no key row of the warp is seen
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+              return;
+            }
+          }
+          (void)vis;
           float xs[32];
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
@@ -751,7 +824,7 @@ __global__ void __maxnreg__(168)
           if constexpr (decltype(masked)::value) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * c + e < j) xs[e] = 0.f;
+              if (kWin ? ((vis >> e) & 1u) == 0u : 32 * c + e < j) xs[e] = 0.f;
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(xs[2 * e], xs[2 * e + 1]);
@@ -790,7 +863,9 @@ __global__ void __maxnreg__(168)
         tmem_ld_x16(tdV + lane_off + c, v);
         tmem_wait_ld();
         reg_fence<16>(v);
-        if (jg < S) {
+        if (kWin && n < sink_tiles && win.nparts > 1) {
+          store_part(0, j, c, v, 1.f);
+        } else if (jg < S) {
           uint4 *dst = reinterpret_cast<uint4 *>(dv + row_off + c);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
@@ -845,6 +920,7 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       set_unit(u);
+      if (kWin && T == 0) continue;
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
         if (!warp_wait(p_full, g & 1, ctl) || !warp_wait(dp_full, g & 1, ctl)) { ok = false; break; }
@@ -961,7 +1037,9 @@ __global__ void __maxnreg__(168)
         tmem_ld_x16(tdK + lane_off + c, v);
         tmem_wait_ld();
         reg_fence<16>(v);
-        if (jg < S) {
+        if (kWin && n < sink_tiles && win.nparts > 1) {
+          store_part(1, j, c, v, scale);
+        } else if (jg < S) {
           float f[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(v[e]) * scale;
@@ -1025,13 +1103,45 @@ __global__ void __maxnreg__(168)
   }
 }
 
-template <int HD, bool kFusedDq, bool kResident = false, bool kDsTmem = false>
+// Adds the parts of the sink tiles' dV and dK in order and rounds once. One thread per 4
+// elements of one tensor; part p of key tile n exists when n + p part_tiles < num_m.
+template <int HD>
+__global__ void __launch_bounds__(256) window_parts_kernel(const float *__restrict__ parts,
+                                                           __nv_bfloat16 *__restrict__ dk,
+                                                           __nv_bfloat16 *__restrict__ dv, int BK, int S, int nkv,
+                                                           int sink_tiles, int nparts, int part_tiles) {
+  grid_dep_launch();
+  grid_dep_wait();
+  constexpr int kQuads = kTileRows * HD / 4;
+  const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long tile = t / (2 * kQuads);                 // (batch, kv head, sink tile)
+  if (tile >= static_cast<long long>(BK) * sink_tiles) return;
+  const int e = static_cast<int>(t % (2 * kQuads)), which = e / kQuads, quad = e % kQuads;
+  const int bk = static_cast<int>(tile / sink_tiles), n = static_cast<int>(tile % sink_tiles);
+  const int j = quad / (HD / 4), c = quad % (HD / 4) * 4, jg = n * kTileRows + j;
+  if (jg >= S) return;
+  const int num_m = (S + kTileRows - 1) / kTileRows;
+  const int used = min(nparts, (num_m - n + part_tiles - 1) / part_tiles);
+  const float4 *src = reinterpret_cast<const float4 *>(parts + (2 * tile * nparts + which) * (kTileRows * HD)) + quad;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < used; ++p) {
+    const float4 x = src[static_cast<size_t>(p) * 2 * kQuads];
+    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+  }
+  __nv_bfloat16 *dst = (which ? dk : dv) +
+                       ((static_cast<size_t>(bk / nkv) * S + jg) * nkv + static_cast<size_t>(bk % nkv)) * HD + c;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+}
+
+template <int HD, bool kFusedDq, bool kResident = false, bool kDsTmem = false, bool kWin = false>
 cudaError_t launch_main_hd(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                            const CUtensorMap &mdo, const CUtensorMap &maux, const CUtensorMap &mdq,
                            __nv_bfloat16 *dk, __nv_bfloat16 *dv, __nv_bfloat16 *dq, int B, int S, int nh,
-                           int nkv, float scale, int *status, uint64_t timeout_ns, cudaStream_t stream) {
+                           int nkv, float scale, int *status, uint64_t timeout_ns, cudaStream_t stream,
+                           const WinArgs &win = WinArgs{}) {
   using L = BwdLayout<HD, kFusedDq>;
-  auto kernel = attn_bwd_main_kernel<HD, kFusedDq, kResident, kDsTmem>;
+  auto kernel = attn_bwd_main_kernel<HD, kFusedDq, kResident, kDsTmem, kWin>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynBytes);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM, or one per unit (resident dQ: per head) when there are
@@ -1039,10 +1149,18 @@ cudaError_t launch_main_hd(const CUtensorMap &mq, const CUtensorMap &mk, const C
   int dev = 0, sms = 0;
   if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
   if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
-  const long long units = static_cast<long long>(B) * nkv * (kResident ? 1 : (S + kTileRows - 1) / kTileRows);
+  const int num_m = (S + kTileRows - 1) / kTileRows;
+  const int sink_tiles = window_sink_tiles(win.sinks);
+  const int per_bk = kWin ? sink_tiles * win.nparts + num_m - sink_tiles : num_m;
+  const long long units = static_cast<long long>(B) * nkv * (kResident ? 1 : per_bk);
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
-  return launch_pdl(kernel, grid, kBwdThreads, L::kDynBytes, stream, mq, mk, mv, mdo, maux, mdq, dk, dv, dq, B, S,
-                    nh, nkv, scale, status, timeout_ns);
+  err = launch_pdl(kernel, grid, kBwdThreads, L::kDynBytes, stream, mq, mk, mv, mdo, maux, mdq, dk, dv, dq, B, S,
+                   nh, nkv, scale, win, status, timeout_ns);
+  if (!kWin || err != cudaSuccess || sink_tiles == 0 || win.nparts == 1) return err;
+  const long long quads = static_cast<long long>(B) * nkv * sink_tiles * 2 * (kTileRows * HD / 4);
+  return launch_pdl(window_parts_kernel<HD>, static_cast<unsigned>((quads + 255) / 256), 256, 0, stream,
+                    static_cast<const float *>(win.parts), dk, dv, B * nkv, S, nkv, sink_tiles, win.nparts,
+                    win.part_tiles);
 }
 
 // 3. dq convert (fused dQ): 8 elements per thread (two 16-byte loads, one 16-byte
@@ -1113,6 +1231,50 @@ cudaError_t launch_bwd_main_bf16(const CUtensorMap &mq, const CUtensorMap &mk,
                : launch_main_hd<32, false>(mq, mk, mv, mdo, maux, md, dk, dv, nullptr, B, S, nh, nkv, scale, status, timeout_ns, stream);
   if (hd == 128 && !mdq)
     return launch_main_hd<128, false>(mq, mk, mv, mdo, maux, md, dk, dv, nullptr, B, S, nh, nkv, scale, status, timeout_ns, stream);
+  return cudaErrorInvalidValue;
+}
+
+// A sink tile's walk is cut into parts of as many query tiles as a key tile of the window
+// meets (at least 4), so that no unit is longer than the others.
+WindowSplit window_bwd_split(int S, int window, int sinks) {
+  const int num_m = (S + kTileRows - 1) / kTileRows;
+  WindowSplit w;
+  w.sink_tiles = window_sink_tiles(sinks);
+  const int meets = (window + kTileRows - 2) / kTileRows + 1;
+  w.part_tiles = meets < 4 ? 4 : meets;
+  w.nparts = (num_m + w.part_tiles - 1) / w.part_tiles;
+  return w;
+}
+
+size_t window_parts_bytes(int B, int S, int nkv, int hd, int window, int sinks) {
+  const WindowSplit w = window_bwd_split(S, window, sinks);
+  if (w.nparts == 1) return 0;
+  return static_cast<size_t>(B) * nkv * w.sink_tiles * w.nparts * 2 * kTileRows * hd * sizeof(float);
+}
+
+cudaError_t launch_window_bwd_main_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                        const CUtensorMap &mdo, const CUtensorMap &maux, const CUtensorMap *mdq,
+                                        __nv_bfloat16 *dk, __nv_bfloat16 *dv, int B, int S, int nh, int nkv, int hd,
+                                        float scale, int window, int sinks, float *parts, int *status,
+                                        uint64_t timeout_ns, cudaStream_t stream) {
+  const WindowSplit w = window_bwd_split(S, window, sinks);
+  const WinArgs win{window, sinks, w.nparts, w.part_tiles, parts};
+  const CUtensorMap &md = mdq ? *mdq : maux;
+#define XATTN_WIN_MAIN(HD, FUSED, DSTMEM)                                                                            \
+  return launch_main_hd<HD, FUSED, false, DSTMEM, true>(mq, mk, mv, mdo, maux, md, dk, dv, nullptr, B, S, nh, nkv,   \
+                                                        scale, status, timeout_ns, stream, win)
+  if (hd == 64) {
+    if (!mdq) XATTN_WIN_MAIN(64, false, false);
+    if (nh != nkv) XATTN_WIN_MAIN(64, true, true);
+    XATTN_WIN_MAIN(64, true, false);
+  }
+  if (hd == 32) {
+    if (!mdq) XATTN_WIN_MAIN(32, false, false);
+    if (nh != nkv) XATTN_WIN_MAIN(32, true, true);
+    XATTN_WIN_MAIN(32, true, false);
+  }
+  if (hd == 128 && !mdq) XATTN_WIN_MAIN(128, false, false);
+#undef XATTN_WIN_MAIN
   return cudaErrorInvalidValue;
 }
 

@@ -27,6 +27,8 @@
 // than 2^8 (the stale max is exact because the final normalisation uses the same max).
 // Epilogue: O / l in bf16, LSE = (m + log2 l) ln 2.
 // Causal tile skipping: tile m visits key tiles 0..m.
+// Window with sinks (kWin): tile m visits the key tiles that hold a sink and those from
+// the first one its window reaches; both kinds of tile edge are masked (step below).
 // TMEM columns: S_A [0,128) S_B [128,256) fp32 | O_A [256,256+HD) O_B [320,320+HD) fp32 |
 //               P_A [384,448) P_B [448,512) bf16 pairs; at hd = 128: O_A [256,384),
 //               O_B [384,512), and P_X in the first 64 columns of S_X.
@@ -106,14 +108,26 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok);
 }
 
+// Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 31);
+  return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
 // kNegScale: scale < 0, so the row maximum of the scaled scores is the scaled minimum of
 // the raw ones.
-template <int HD, bool kNegScale, int kRing>
+// kWin: query i sees key j <= i only if i - j < window or j < sinks. A unit then walks a
+// list of key tiles: `heads` sink tiles 0 .. heads - 1, then tiles loA .. n_last (loA =
+// the first tile that A's window reaches). A uses all of them but tile mB; B all but the
+// list's entry `skip` (tile loA when it lies behind B's window and holds no sink). Every
+// role counts a unit's tiles by their index in the list.
+template <int HD, bool kNegScale, int kRing, bool kWin>
 __global__ void __maxnreg__(168)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, __nv_bfloat16 *__restrict__ o,
                     float *__restrict__ lse, int B, int S, int nh, int nkv, float scale_log2,
-                    int *status, unsigned long long timeout_ns) {
+                    int window, int sinks, int *status, unsigned long long timeout_ns) {
   using L = FwdLayout<HD, kRing>;
   constexpr int kFwdStages = L::kStages;
   constexpr int kQBufs = L::kQBufs;
@@ -134,6 +148,12 @@ __global__ void __maxnreg__(168)
   const int num_units = num_pairs * BH;
   const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
   auto unit_at = [G, cta](int k) { return k * G + ((k & 1) ? G - 1 - cta : cta); };
+  // kWin: the first key tile that the window of query tile m's first row reaches, and the
+  // tiles that hold a sink. (window <= S, so the difference stays in range.)
+  auto first_tile = [window](int m) { return max(m * kTileRows - window + 1, 0) / kTileRows; };
+  const int sink_tiles = kWin ? (sinks + kTileRows - 1) / kTileRows : 0;
+  (void)first_tile;
+  (void)sink_tiles;
 // Fields of unit u, as constants of the role loop that processes it.
 #define XATTN_FWD_UNIT(u)                                       \
   const int jp = num_pairs - 1 - (u) / BH;                      \
@@ -142,8 +162,15 @@ __global__ void __maxnreg__(168)
   const int mA = 2 * jp, mB = 2 * jp + 1;                       \
   const bool hasB = mB < num_m;                                 \
   const int n_last = hasB ? mB : mA; /* last key tile */        \
+  const int loA = kWin ? first_tile(mA) : 0;                    \
+  const int loB = kWin ? first_tile(mB) : 0;                    \
+  const int heads = kWin ? min(sink_tiles, loA) : 0;            \
+  const int count = heads + n_last - loA + 1;                   \
+  const int skip = (kWin && loB > loA && loA >= sink_tiles) ? heads : -1; \
   (void)b;                                                      \
   (void)kvh;                                                    \
+  (void)count;                                                  \
+  (void)skip;                                                   \
   (void)n_last
 
   const uint32_t sQ = smem_u32(smem + L::kQ);
@@ -253,7 +280,7 @@ __global__ void __maxnreg__(168)
       if (hasB) load_tile(sQb + L::kTileBytes, &mq, q_full(qb), h, mB * kTileRows, b);
       ++units;
 #pragma unroll 1
-      for (int n = 0; ok && n <= n_last; ++n) ok = load_kv(n, kvh, b);
+      for (int i = 0; ok && i < count; ++i) ok = load_kv(kWin && i >= heads ? i - heads + loA : i, kvh, b);
     }
     // Let every copy in flight land before the CTA can exit.
     for (int j = (units > kQBufs ? units - kQBufs : 0); j < units; ++j)
@@ -334,44 +361,62 @@ __global__ void __maxnreg__(168)
       // its mma_final arrival below can never count towards an earlier use of the buffer.
       if (!warp_wait(q_full(qb), (units / kQBufs) & 1, ctl)) break;
       if (x == 0 || hasB) {
-        // The unit's first scores: key tile 0 landed, and S_X of the previous unit read;
-        // its first PV overwrites O_X, which the previous epilogue has read.
-        ok = warp_wait(full(ring_stage(R)), ring_phase(R), ctl) && warp_wait(s_free(x), (gx - 1) & 1, ctl);
+        // The unit's first scores: its first key tile landed, and S_X of the previous unit
+        // read; its first PV overwrites O_X, which the previous epilogue has read.
+        // n counts the unit's list of key tiles (without a window, the key tiles): this
+        // tile's entries are n0 .. n_end - 1, for B without `skip`.
+        const int skip_x = (kWin && x == 1) ? skip : -1;
+        const int n0 = (kWin && skip_x == 0) ? 1 : 0;
+        const int n_end = kWin ? (x == 0 && hasB ? count - 1 : count) : mX + 1;
+        auto after = [skip_x](int n) { return (kWin && n + 1 == skip_x) ? n + 2 : n + 1; };
+        if (kWin && n0 == 1) ok = warp_wait(full(ring_stage(R)), ring_phase(R), ctl);
+        ok = ok && warp_wait(full(ring_stage(R + n0)), ring_phase(R + n0), ctl) &&
+             warp_wait(s_free(x), (gx - 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        issue_qk(ring_stage(R), qb);
+        issue_qk(ring_stage(R + n0), qb);
         if (!warp_wait(o_free(x), (unitsx - 1) & 1, ctl)) { ok = false; break; }
 #pragma unroll 1
-        for (int n = 0; n <= mX; ++n, ++gx) {
-          const bool shared_tile = x == 0 ? hasB : n <= mA;
+        for (int n = n0; n < n_end; n = after(n), ++gx) {
+          const int n1 = after(n);
+          // A tile this side does not use still has to land before the next wait on its
+          // stage: a barrier tells only its last two phases apart.
+          if (kWin && n1 == n + 2 && !warp_wait(full(ring_stage(R + n + 1)), ring_phase(R + n + 1), ctl)) {
+            ok = false;
+            break;
+          }
+          const bool shared_tile = kWin ? (x == 0 ? hasB && n != skip : n + 1 < count)
+                                        : (x == 0 ? hasB : n <= mA);
           if constexpr (!L::kAliasP) {
-            if (n + 1 <= mX) {
+            if (n1 < n_end) {
               if (!warp_wait(s_free(x), gx & 1, ctl) ||
-                  !warp_wait(full(ring_stage(R + n + 1)), ring_phase(R + n + 1), ctl)) { ok = false; break; }
+                  !warp_wait(full(ring_stage(R + n1)), ring_phase(R + n1), ctl)) { ok = false; break; }
               tc_fence_after();
-              issue_qk(ring_stage(R + n + 1), qb);
+              issue_qk(ring_stage(R + n1), qb);
             }
             if (!warp_wait(p_full(x), gx & 1, ctl)) { ok = false; break; }
             tc_fence_after();
-            issue_pv(ring_stage(R + n), n == 0, !shared_tile);
+            issue_pv(ring_stage(R + n), n == n0, !shared_tile);
           } else {
             // P_X(n) sits in S_X's columns: PV_X(n) first, then S_X(n+1) over them.
             if (!warp_wait(p_full(x), gx & 1, ctl)) { ok = false; break; }
             tc_fence_after();
-            issue_pv(ring_stage(R + n), n == 0, !shared_tile);
-            if (n + 1 <= mX) {
-              if (!warp_wait(full(ring_stage(R + n + 1)), ring_phase(R + n + 1), ctl)) { ok = false; break; }
+            issue_pv(ring_stage(R + n), n == n0, !shared_tile);
+            if (n1 < n_end) {
+              if (!warp_wait(full(ring_stage(R + n1)), ring_phase(R + n1), ctl)) { ok = false; break; }
               tc_fence_after();
-              issue_qk(ring_stage(R + n + 1), qb);
+              issue_qk(ring_stage(R + n1), qb);
             }
           }
         }
+        if (kWin && ok && x == 0 && hasB)
+          ok = warp_wait(full(ring_stage(R + count - 1)), ring_phase(R + count - 1), ctl);
         if (!ok) break;
         ++unitsx;
       }
       if (elect_one()) mma_commit(mma_final(qb));  // covers every MMA of this unit
       __syncwarp();
-      R += n_last + 1;
+      R += kWin ? count : n_last + 1;
       ++units;
     }
     if (units > 0) mbar_drain(mma_final((units - 1) % kQBufs), ((units - 1) / kQBufs) & 1, ctl);
@@ -397,8 +442,26 @@ __global__ void __maxnreg__(168)
       // are wholly visible, chunk q is masked per lane (key column > row), chunks above q
       // are wholly masked (P = 0 without exponentials); q is warp-uniform, so each chunk
       // takes one branch-free path.
-      auto step = [&](auto masked, int n) -> bool {
+      // With a window the masked copy also takes the tiles at the window's far edge and the
+      // sink tiles behind it. vis: the row's visible columns, a word per 32-column chunk;
+      // per chunk the warp takes the unmasked path (every row sees all 32), no path (P = 0,
+      // no row sees any) or the masked one, and a row may see nothing of a whole tile.
+      auto step = [&](auto masked, int n, bool first) -> bool {
         constexpr bool kDiag = decltype(masked)::value;
+        uint32_t vis[4] = {};
+        if constexpr (kWin && kDiag) {
+          const int far = (mX - n) * kTileRows + row - window + 1;   // first column in the window
+          const int near = n == mX ? row : kTileRows - 1, sk = min(sinks - n * kTileRows - 1, near);
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+            vis[cc] = bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc);
+        }
+        // Chunk cc of this warp's rows: 0 none visible, 1 all, 2 mixed.
+        auto kind = [&](int cc) {
+          if constexpr (kWin && kDiag)
+            return __all_sync(0xffffffffu, vis[cc] == 0xffffffffu) ? 1 : __any_sync(0xffffffffu, vis[cc] != 0u) ? 2 : 0;
+          return (!kDiag || cc < quarter) ? 1 : (cc == quarter ? 2 : 0);
+        };
         if (!warp_wait(s_full(x), gx & 1, ctl)) return false;
         tc_fence_after();
         // The whole row of S_X(n) comes into registers with one TMEM read, and the buffer
@@ -414,13 +477,17 @@ __global__ void __maxnreg__(168)
         // (scale >= 0) or their scaled minimum (scale < 0); masked columns do not count.
         constexpr float kFill = kNegScale ? INFINITY : -INFINITY;
         float mx4[4] = {kFill, kFill, kFill, kFill};
+        auto hidden = [&](int c) {
+          if constexpr (kWin) return ((vis[c >> 5] >> (c & 31)) & 1u) == 0u;
+          return c > row;
+        };
         auto max_chunk = [&](auto mask_chunk, int c32) {
 #pragma unroll
           for (int c = c32; c < c32 + 32; c += 2) {
             float v0 = __uint_as_float(r[c]), v1 = __uint_as_float(r[c + 1]);
             if (decltype(mask_chunk)::value) {
-              if (c > row) v0 = kFill;
-              if (c + 1 > row) v1 = kFill;
+              if (hidden(c)) v0 = kFill;
+              if (hidden(c + 1)) v1 = kFill;
             }
             float &a = mx4[(c >> 1) & 3];
             a = kNegScale ? fmin3(a, v0, v1) : fmax3(a, v0, v1);
@@ -428,8 +495,9 @@ __global__ void __maxnreg__(168)
         };
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
-          if (!kDiag || cc < quarter) max_chunk(std::false_type{}, 32 * cc);
-          else if (cc == quarter) max_chunk(std::true_type{}, 32 * cc);
+          const int kc = kind(cc);
+          if (kc == 1) max_chunk(std::false_type{}, 32 * cc);
+          else if (kc == 2) max_chunk(std::true_type{}, 32 * cc);
         }
         const float mx = (kNegScale ? fmin3(mx4[0], mx4[1], fminf(mx4[2], mx4[3]))
                                     : fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]))) * scale_log2;
@@ -443,6 +511,7 @@ __global__ void __maxnreg__(168)
         // exponentials on the shared unit).
         float alpha = 1.f;
         if (rescale) alpha = ex2_approx(mrow - mnew);
+        if (kWin && mnew == -INFINITY) alpha = 1.f;   // a row that has seen no key yet
         const float neg_m = -m_use;
         // Exponents, the causal mask on them (-inf -> exact zeros for any scale, 0
         // included), the exponentials, row sums and bf16 P, packed in place into r[0, 64).
@@ -461,8 +530,8 @@ __global__ void __maxnreg__(168)
             ffma2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), scale_log2, scale_log2,
                   neg_m, neg_m);
             if (decltype(mask_chunk)::value) {
-              if (c > row) x0 = -INFINITY;
-              if (c + 1 > row) x1 = -INFINITY;
+              if (hidden(c)) x0 = -INFINITY;
+              if (hidden(c + 1)) x1 = -INFINITY;
             }
             float p0, p1;
             if (!kDiag && !decltype(mask_chunk)::value && (e & 7) == 7) {
@@ -477,9 +546,10 @@ __global__ void __maxnreg__(168)
           }
         };
         auto chunk = [&](int cc) {
-          if (!kDiag || cc < quarter) {
+          const int kc = kind(cc);
+          if (kc == 1) {
             exp_chunk(std::false_type{}, 32 * cc);
-          } else if (cc == quarter) {
+          } else if (kc == 2) {
             exp_chunk(std::true_type{}, 32 * cc);
           } else {
 #pragma unroll
@@ -495,7 +565,7 @@ __global__ void __maxnreg__(168)
         tmem_st_x16(tPx + 32, r + 32);
         chunk(3);
         tmem_st_x16(tPx + 48, r + 48);
-        if (rescale && n > 0) {
+        if (rescale && !first) {
 #pragma unroll
           for (int c = 0; c < HD; c += 32) {
             uint32_t ov[32];
@@ -514,13 +584,29 @@ __global__ void __maxnreg__(168)
         mbar_arrive(p_full(x));
         return true;
       };
+      if constexpr (kWin) {
+        const int n_end = (x == 0 && hasB) ? count - 1 : count;
+        bool first = true;
 #pragma unroll 1
-      for (int n = 0; n < mX; ++n, ++gx) {
-        if (!step(std::false_type{}, n)) { ok = false; break; }
-      }
-      if (ok) {
-        if (!step(std::true_type{}, mX)) ok = false;
-        ++gx;
+        for (int i = 0; i < n_end; ++i) {
+          if (x == 1 && i == skip) continue;
+          const int n = i < heads ? i : i - heads + loA;
+          // Some row below S of the tile does not see some key of tile n.
+          const bool edge = n == mX || (min(mX * kTileRows + kTileRows, S) - n * kTileRows > window &&
+                                        (n + 1) * kTileRows > sinks);
+          if (!(edge ? step(std::true_type{}, n, first) : step(std::false_type{}, n, first))) { ok = false; break; }
+          first = false;
+          ++gx;
+        }
+      } else {
+#pragma unroll 1
+        for (int n = 0; n < mX; ++n, ++gx) {
+          if (!step(std::false_type{}, n, n == 0)) { ok = false; break; }
+        }
+        if (ok) {
+          if (!step(std::true_type{}, mX, mX == 0)) ok = false;
+          ++gx;
+        }
       }
       if (!ok) break;
       // Epilogue: O / l in bf16 and the LSE; then O_X is free for the next unit.
@@ -564,12 +650,12 @@ __global__ void __maxnreg__(168)
 }
 #undef XATTN_FWD_UNIT
 
-template <int HD, bool kNegScale, int kRing>
+template <int HD, bool kNegScale, int kRing, bool kWin>
 cudaError_t launch_fwd_sign(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                             __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, float scale,
-                            int *status, uint64_t timeout_ns, cudaStream_t stream) {
+                            int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream) {
   using L = FwdLayout<HD, kRing>;
-  cudaError_t err = cudaFuncSetAttribute(attn_fwd_kernel<HD, kNegScale, kRing>,
+  cudaError_t err = cudaFuncSetAttribute(attn_fwd_kernel<HD, kNegScale, kRing, kWin>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynBytes);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM, or one per unit when there are fewer units.
@@ -579,24 +665,41 @@ cudaError_t launch_fwd_sign(const CUtensorMap &mq, const CUtensorMap &mk, const 
   const int num_m = (S + kTileRows - 1) / kTileRows;
   const long long units = static_cast<long long>(B) * nh * ((num_m + 1) / 2);
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
-  return launch_pdl(attn_fwd_kernel<HD, kNegScale, kRing>, grid, kFwdThreads, L::kDynBytes, stream, mq, mk, mv, o,
-                    lse, B, S, nh, nkv, scale * kLog2e, status, timeout_ns);
+  return launch_pdl(attn_fwd_kernel<HD, kNegScale, kRing, kWin>, grid, kFwdThreads, L::kDynBytes, stream, mq, mk, mv,
+                    o, lse, B, S, nh, nkv, scale * kLog2e, window, sinks, status, timeout_ns);
 }
 
-template <int HD>
+template <int HD, bool kWin>
 cudaError_t launch_fwd_hd(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                           __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, float scale,
-                          int *status, uint64_t timeout_ns, cudaStream_t stream) {
+                          int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream) {
   constexpr int kRingGroups = FwdLayout<HD>::kStages;
   constexpr int kRingMha = HD == 128 ? kRingGroups : 4;
+#define XATTN_FWD(NEG, RING)                                                                                  \
+  return launch_fwd_sign<HD, NEG, RING, kWin>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, window, sinks, status, \
+                                              timeout_ns, stream)
   if (nh == nkv) {
-    if (scale < 0.f)
-      return launch_fwd_sign<HD, true, kRingMha>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
-    return launch_fwd_sign<HD, false, kRingMha>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
+    if (scale < 0.f) XATTN_FWD(true, kRingMha);
+    XATTN_FWD(false, kRingMha);
   }
-  if (scale < 0.f)
-    return launch_fwd_sign<HD, true, kRingGroups>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  return launch_fwd_sign<HD, false, kRingGroups>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
+  if (scale < 0.f) XATTN_FWD(true, kRingGroups);
+  XATTN_FWD(false, kRingGroups);
+#undef XATTN_FWD
+}
+
+template <bool kWin>
+cudaError_t launch_fwd(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, __nv_bfloat16 *o,
+                       float *lse, int B, int S, int nh, int nkv, int hd, float scale, int window, int sinks,
+                       int *status, uint64_t timeout_ns, cudaStream_t stream) {
+#define XATTN_FWD_HD(HD)                                                                                       \
+  if (hd == HD)                                                                                                \
+    return launch_fwd_hd<HD, kWin>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, window, sinks, status, timeout_ns, \
+                                   stream)
+  XATTN_FWD_HD(64);
+  XATTN_FWD_HD(32);
+  XATTN_FWD_HD(128);
+#undef XATTN_FWD_HD
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -604,13 +707,13 @@ cudaError_t launch_fwd_hd(const CUtensorMap &mq, const CUtensorMap &mk, const CU
 cudaError_t launch_fwd_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                             __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, int hd,
                             float scale, int *status, uint64_t timeout_ns, cudaStream_t stream) {
-  if (hd == 64)
-    return launch_fwd_hd<64>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  if (hd == 32)
-    return launch_fwd_hd<32>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  if (hd == 128)
-    return launch_fwd_hd<128>(mq, mk, mv, o, lse, B, S, nh, nkv, scale, status, timeout_ns, stream);
-  return cudaErrorInvalidValue;
+  return launch_fwd<false>(mq, mk, mv, o, lse, B, S, nh, nkv, hd, scale, 0, 0, status, timeout_ns, stream);
+}
+
+cudaError_t launch_window_fwd_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                   __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, int hd, float scale,
+                                   int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream) {
+  return launch_fwd<true>(mq, mk, mv, o, lse, B, S, nh, nkv, hd, scale, window, sinks, status, timeout_ns, stream);
 }
 
 }  // namespace xattn

@@ -195,6 +195,16 @@ xattn_status cuda_status(cudaError_t e) {
     if (st_ != XATTN_OK) return st_;             \
   } while (0)
 
+// Window and sinks of a window call; on success *w and *s are clipped to S (a window of S
+// or more keeps every key, sinks beyond S mean all of them).
+xattn_status check_window(int S, int window, int sinks, int *w, int *s) {
+  if (window < 1 || sinks < 0) return XATTN_ERR_WINDOW;
+  if (S > (1 << 30)) return XATTN_ERR_BAD_SHAPE;   // tile sums stay inside int32
+  *w = window < S ? window : S;
+  *s = sinks < S ? sinks : S;
+  return XATTN_OK;
+}
+
 xattn_status bf16_device(DeviceInfo **dev) {
   XATTN_TRY(device_info(dev));
   if (!(*dev)->sm103) return XATTN_ERR_NO_DEVICE_SUPPORT;
@@ -414,6 +424,105 @@ xattn_status xattn_bwd_deterministic(const void *q, const void *k, const void *v
   return r;
 }
 
+xattn_status xattn_window_fwd(const void *q, const void *k, const void *v, int B, int S, int nh, int nkv, int hd,
+                              int window, int sinks, float scale, void *o, float *lse, void *stream) {
+  if (!q || !k || !v || !o || !lse) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
+  int w = 0, s = 0;
+  XATTN_TRY(check_window(S, window, sinks, &w, &s));
+  XATTN_TRY(check_bf16_fwd(hd));
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  CUtensorMap mq, mk, mv;
+  XATTN_TRY(make_map(&mq, q, B, S, nh, hd));
+  XATTN_TRY(make_map(&mk, k, B, S, nkv, hd));
+  XATTN_TRY(make_map(&mv, v, B, S, nkv, hd));
+  return cuda_status(launch_window_fwd_bf16(mq, mk, mv, static_cast<__nv_bfloat16 *>(o), lse, B, S, nh, nkv, hd,
+                                            scale, w, s, dev->status, wait_limit_ns(),
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+xattn_status xattn_window_bwd(const void *q, const void *k, const void *v, const void *o, const void *dO,
+                              const float *lse, int B, int S, int nh, int nkv, int hd, int window, int sinks,
+                              float scale, int deterministic, void *dq, void *dk, void *dv, void *stream) {
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
+  int w = 0, s = 0;
+  XATTN_TRY(check_window(S, window, sinks, &w, &s));
+  XATTN_TRY(check_bwd_scale(scale));
+  XATTN_TRY(check_bf16_fwd(hd));
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  // dQ: added across key tiles by the main kernel, or (deterministic, and at hd = 128, where
+  // its accumulator does not fit the tensor memory) from the query-stationary kernel.
+  const bool fused = !deterministic && hd != 128;
+  CUtensorMap mq, mk, mv, mdo, maux, mdq;
+  XATTN_TRY(make_map(&mq, q, B, S, nh, hd));
+  XATTN_TRY(make_map(&mk, k, B, S, nkv, hd));
+  XATTN_TRY(make_map(&mv, v, B, S, nkv, hd));
+  XATTN_TRY(make_map(&mdo, dO, B, S, nh, hd));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t base_bytes = (bwd_workspace_bytes(B, S, nh, hd, fused) + 255) / 256 * 256;
+  void *base = nullptr;
+  if (cudaMallocAsync(&base, base_bytes + window_parts_bytes(B, S, nkv, hd, w, s), st) != cudaSuccess) {
+    cudaGetLastError();   // do not leave the failure for the caller's next error check
+    return XATTN_ERR_CUDA;
+  }
+  float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(base) + base_bytes);
+  const BwdWorkspace ws = bwd_workspace_carve(base, B, S, nh, hd);
+  xattn_status r = make_map_aux(&maux, ws.aux, B, S, nh);
+  if (r == XATTN_OK && fused) r = make_map_dq(&mdq, ws.dqacc, B, S, nh, hd);
+  if (r == XATTN_OK)
+    r = cuda_status(launch_bwd_preprocess(static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(dO),
+                                          lse, B, S, nh, hd, scale, ws, fused, st));
+  if (r == XATTN_OK)
+    r = cuda_status(launch_window_bwd_main_bf16(mq, mk, mv, mdo, maux, fused ? &mdq : nullptr,
+                                                static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dv), B,
+                                                S, nh, nkv, hd, scale, w, s, parts, dev->status, wait_limit_ns(), st));
+  if (r == XATTN_OK && fused)
+    r = cuda_status(launch_dq_convert(ws.dqacc, static_cast<__nv_bfloat16 *>(dq), static_cast<size_t>(B) * S * nh * hd,
+                                      scale, st));
+  else if (r == XATTN_OK)
+    r = cuda_status(launch_window_bwd_dq_bf16(mq, mk, mv, mdo, lse, ws, static_cast<__nv_bfloat16 *>(dq), B, S, nh,
+                                              nkv, hd, scale, w, s, dev->status, wait_limit_ns(), st));
+  const cudaError_t fe = cudaFreeAsync(base, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
+}
+
+xattn_status xattn_window_fwd_f32(const float *q, const float *k, const float *v, int B, int S, int nh, int nkv,
+                                  int hd, int window, int sinks, float scale, float *o, float *lse, void *stream) {
+  if (!q || !k || !v || !o || !lse) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
+  int w = 0, s = 0;
+  XATTN_TRY(check_window(S, window, sinks, &w, &s));
+  if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  return cuda_status(launch_window_fwd_f32(q, k, v, o, lse, B, S, nh, nkv, hd, scale, w, s,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+xattn_status xattn_window_bwd_f32(const float *q, const float *k, const float *v, const float *o, const float *dO,
+                                  const float *lse, int B, int S, int nh, int nkv, int hd, int window, int sinks,
+                                  float scale, float *dq, float *dk, float *dv, void *stream) {
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
+  int w = 0, s = 0;
+  XATTN_TRY(check_window(S, window, sinks, &w, &s));
+  if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  return cuda_status(launch_window_bwd_f32(q, k, v, o, dO, lse, dq, dk, dv, B, S, nh, nkv, hd, scale, w, s,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
 xattn_status xattn_fwd_f32(const float *q, const float *k, const float *v, int B, int S, int nh,
                            int nkv, int hd, float scale, float *o, float *lse, void *stream) {
   if (!q || !k || !v || !o || !lse) return XATTN_ERR_NULL_PTR;
@@ -452,6 +561,7 @@ const char *xattn_status_string(xattn_status s) {
     case XATTN_ERR_WORKSPACE: return "workspace is NULL, not 256-byte aligned, or too small";
     case XATTN_ERR_SCRATCH_LIMIT:
       return "these sizes need more scratch than xattn_bwd_noalloc's fixed array holds";
+    case XATTN_ERR_WINDOW: return "window must be positive and sinks not negative";
     case XATTN_ERR_DEVICE_BOUNDS:
       return "an on-device bounds check failed (debug build)";
   }

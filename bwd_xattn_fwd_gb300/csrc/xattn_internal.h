@@ -120,4 +120,31 @@ cudaError_t launch_bwd_f32(const float *q, const float *k, const float *v, const
                            int B, int S, int nh, int nkv, int hd, float scale,
                            cudaStream_t stream);
 
+// Window attention with sinks: the forward and backward above with query i seeing key
+// j <= i only if i - j < window or j < sinks (1 <= window <= S, 0 <= sinks <= S). The main
+// backward kernel cuts each sink tile's walk over the query tiles into nparts parts of
+// part_tiles tiles; with nparts > 1 `parts` holds window_parts_bytes() bytes of fp32 sums.
+struct WindowSplit {
+  int sink_tiles, nparts, part_tiles;
+};
+WindowSplit window_bwd_split(int S, int window, int sinks);
+size_t window_parts_bytes(int B, int S, int nkv, int hd, int window, int sinks);
+cudaError_t launch_window_fwd_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                   __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, int hd, float scale,
+                                   int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream);
+cudaError_t launch_window_bwd_main_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                        const CUtensorMap &mdo, const CUtensorMap &maux, const CUtensorMap *mdq,
+                                        __nv_bfloat16 *dk, __nv_bfloat16 *dv, int B, int S, int nh, int nkv, int hd,
+                                        float scale, int window, int sinks, float *parts, int *status,
+                                        uint64_t timeout_ns, cudaStream_t stream);
+cudaError_t launch_window_bwd_dq_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                      const CUtensorMap &mdo, const float *lse, const BwdWorkspace &ws,
+                                      __nv_bfloat16 *dq, int B, int S, int nh, int nkv, int hd, float scale,
+                                      int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream);
+cudaError_t launch_window_fwd_f32(const float *q, const float *k, const float *v, float *o, float *lse, int B, int S,
+                                  int nh, int nkv, int hd, float scale, int window, int sinks, cudaStream_t stream);
+cudaError_t launch_window_bwd_f32(const float *q, const float *k, const float *v, const float *o, const float *dO,
+                                  const float *lse, float *dq, float *dk, float *dv, int B, int S, int nh, int nkv,
+                                  int hd, float scale, int window, int sinks, cudaStream_t stream);
+
 }  // namespace xattn

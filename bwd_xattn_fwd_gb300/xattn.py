@@ -43,6 +43,8 @@ class Status(enum.IntEnum):
     ERR_BAD_SCALE = 9
     ERR_WORKSPACE = 10
     ERR_SCRATCH_LIMIT = 11
+    ERR_DEVICE_BOUNDS = 12
+    ERR_WINDOW = 13
 
 
 class XattnError(RuntimeError):
@@ -67,6 +69,10 @@ _SIGS = {
     "xattn_fwd_f32": [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp],
     "xattn_bwd_f32": [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp],
     "xattn_decode": [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp],
+    "xattn_window_fwd": [_vp] * 3 + [_i] * 7 + [_f] + [_vp] * 3,
+    "xattn_window_bwd": [_vp] * 6 + [_i] * 7 + [_f, _i] + [_vp] * 4,
+    "xattn_window_fwd_f32": [_vp] * 3 + [_i] * 7 + [_f] + [_vp] * 3,
+    "xattn_window_bwd_f32": [_vp] * 6 + [_i] * 7 + [_f] + [_vp] * 4,
     "xattn_check_device_status": [_vp],
 }
 for _name, _args in _SIGS.items():
@@ -86,6 +92,7 @@ _lib.xattn_build_flags.restype = ctypes.c_int
 _lib.xattn_selftest_bounds_check.argtypes = [_vp]
 _lib.xattn_selftest_bounds_check.restype = ctypes.c_int
 
+NO_WINDOW = 0x7FFFFFFF              # XATTN_NO_WINDOW in xattn.h
 BWD_FUSED_DQ, BWD_RESIDENT_DQ, BWD_QUERY_DQ = 0, 1, 2
 BUILD_DEVICE_CHECKS = 1             # xattn_build_flags bit: on-device bounds checks compiled in
 ERR_DEVICE_TIMEOUT, ERR_DEVICE_BOUNDS = 8, 12
@@ -197,6 +204,27 @@ def xattn_decode(q, k_cache, v_cache, B, T, nh, nkv, hd, scale, o, lse, stream=N
           _addr(lse), _stream(stream))
 
 
+def xattn_window_fwd(q, k, v, B, S, nh, nkv, hd, window, sinks, scale, o, lse, stream=None):
+    _call("xattn_window_fwd", _addr(q), _addr(k), _addr(v), B, S, nh, nkv, hd, window, sinks, scale, _addr(o),
+          _addr(lse), _stream(stream))
+
+
+def xattn_window_bwd(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, deterministic, dq, dk, dv,
+                     stream=None):
+    _call("xattn_window_bwd", _addr(q), _addr(k), _addr(v), _addr(o), _addr(dO), _addr(lse), B, S, nh, nkv, hd,
+          window, sinks, scale, int(bool(deterministic)), _addr(dq), _addr(dk), _addr(dv), _stream(stream))
+
+
+def xattn_window_fwd_f32(q, k, v, B, S, nh, nkv, hd, window, sinks, scale, o, lse, stream=None):
+    _call("xattn_window_fwd_f32", _addr(q), _addr(k), _addr(v), B, S, nh, nkv, hd, window, sinks, scale, _addr(o),
+          _addr(lse), _stream(stream))
+
+
+def xattn_window_bwd_f32(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, dq, dk, dv, stream=None):
+    _call("xattn_window_bwd_f32", _addr(q), _addr(k), _addr(v), _addr(o), _addr(dO), _addr(lse), B, S, nh, nkv, hd,
+          window, sinks, scale, _addr(dq), _addr(dk), _addr(dv), _stream(stream))
+
+
 def xattn_selftest_wait_timeout(limit_ns, stream=None):
     fn = _lib.xattn_selftest_wait_timeout
     fn.argtypes = [ctypes.c_ulonglong, _vp]
@@ -278,3 +306,94 @@ def attention_decode(q, k_cache, v_cache, scale=None, stream=None):
     lse = torch.empty((B, nh), dtype=torch.float32, device=q.device)
     xattn_decode(q, k_cache, v_cache, B, T, nh, nkv, hd, scale, o, lse, stream)
     return o, lse
+
+
+def _check(tensors):
+    """Raises unless each (name, tensor, shape, dtype) is a contiguous tensor of that shape and
+    type on the first one's GPU. Returns that device."""
+    device = tensors[0][1].device
+    if device.type != "cuda":
+        raise ValueError(f"{tensors[0][0]} must be a CUDA tensor, not on {device}")
+    for name, t, shape, dtype in tensors:
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {device}")
+    return device
+
+
+class _On:
+    """Makes `device` current, and the given stream (a torch stream or a raw handle) the one
+    that torch allocates outputs on; .stream is the handle to launch on."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._guards = []
+        if torch.cuda.current_device() != device.index:
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self._guards.append(torch.cuda.stream(stream))
+            self.stream = stream.cuda_stream
+        else:
+            self.stream = torch.cuda.current_stream(device).cuda_stream
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _window_dims(q, k, v):
+    import torch
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,S,nh,hd] and k, v [B,S,nkv,hd]")
+    B, S, nh, hd = q.shape
+    nkv = k.shape[2]
+    return B, S, nh, nkv, hd, (("q", q, (B, S, nh, hd), q.dtype), ("k", k, (B, S, nkv, hd), q.dtype),
+                               ("v", v, (B, S, nkv, hd), q.dtype))
+
+
+def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
+    """(o, lse) of causal attention in which query i sees key j only if i - j < window or
+    j < sinks; tensors as for attention_fwd (bf16 or fp32)."""
+    import torch
+    B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
+    device = _check(tensors)
+    scale = float(hd ** -0.5 if scale is None else scale)
+    with _On(device, stream) as handle:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, S, nh), dtype=torch.float32, device=device)
+        fn = xattn_window_fwd if q.dtype == torch.bfloat16 else xattn_window_fwd_f32
+        fn(q, k, v, B, S, nh, nkv, hd, window, sinks, scale, o, lse, handle)
+    return o, lse
+
+
+def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, stream=None, deterministic=False):
+    """(dq, dk, dv) for the tensors of attention_window_fwd and the output gradient dO.
+    deterministic (bf16): dQ bit-reproducible as well, from a second recompute."""
+    import torch
+    B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
+    device = _check((*tensors, ("o", o, q.shape, q.dtype), ("dO", dO, q.shape, q.dtype),
+                     ("lse", lse, (B, S, nh), torch.float32)))
+    scale = float(hd ** -0.5 if scale is None else scale)
+    with _On(device, stream) as handle:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        if q.dtype == torch.bfloat16:
+            xattn_window_bwd(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, deterministic, dq, dk, dv,
+                             handle)
+        else:
+            xattn_window_bwd_f32(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, dq, dk, dv, handle)
+    return dq, dk, dv

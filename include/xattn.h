@@ -67,8 +67,9 @@ typedef enum {
                                          0 < |scale| < 2^-64) */
     XATTN_ERR_WORKSPACE = 10,         /* workspace pointer NULL/misaligned or too small */
     XATTN_ERR_SCRATCH_LIMIT = 11,     /* xattn_bwd_noalloc: sizes need more than its fixed scratch */
-    XATTN_ERR_DEVICE_BOUNDS = 12      /* debug builds only: an on-device bounds check failed
+    XATTN_ERR_DEVICE_BOUNDS = 12,     /* debug builds only: an on-device bounds check failed
                                          (reported later, like a timeout) */
+    XATTN_ERR_WINDOW = 13             /* window < 1 or sinks < 0 */
 } xattn_status;
 
 /*
@@ -203,7 +204,42 @@ xattn_status xattn_bwd_f32(const float *q, const float *k, const float *v, const
                            int hd, float scale, float *dq, float *dk, float *dv,
                            void *stream);
 
-/* Static text for a status code (never NULL). */
+/*
+ * Window attention with sinks: causal attention in which query i sees key j <= i only if
+ *     i - j < window   (the query itself and the window - 1 keys before it)   or
+ *     j < sinks        (the sequence's first keys, which stay visible).
+ * Every query sees itself, so no row is empty. The pages have no windowed attention; the
+ * operation is otherwise that of xattn_fwd / xattn_bwd, with their layouts, arithmetic,
+ * alignment (lse 4-byte) and scale rules. window >= 1 and sinks >= 0 (else
+ * XATTN_ERR_WINDOW); both are clipped to S, so XATTN_NO_WINDOW gives the causal op.
+ * S <= 2^30 (else XATTN_ERR_BAD_SHAPE). Key and query tiles that hold no visible pair are
+ * neither loaded nor computed.
+ *   xattn_window_fwd      : hd in {32, 64, 128}.
+ *   xattn_window_bwd      : hd in {32, 64, 128}; deterministic == 0: dQ added across key
+ *                           tiles with fp32 reduce-adds (hd 32 / 64; its last bits may vary
+ *                           from run to run; dK and dV do not); deterministic != 0, and
+ *                           hd = 128: every output reproducible. Scratch (the causal
+ *                           backward's, and fp32 partial sums of the sink tiles' dK and dV)
+ *                           is taken with cudaMallocAsync on `stream` and released with
+ *                           cudaFreeAsync on it.
+ *   xattn_window_*_f32    : IEEE fp32 on the CUDA cores, hd in [1, 128], no scratch.
+ */
+#define XATTN_NO_WINDOW 0x7fffffff
+xattn_status xattn_window_fwd(const void *q, const void *k, const void *v, int B, int S, int nh,
+                              int nkv, int hd, int window, int sinks, float scale, void *o,
+                              float *lse, void *stream);
+xattn_status xattn_window_bwd(const void *q, const void *k, const void *v, const void *o,
+                              const void *dO, const float *lse, int B, int S, int nh, int nkv,
+                              int hd, int window, int sinks, float scale, int deterministic,
+                              void *dq, void *dk, void *dv, void *stream);
+xattn_status xattn_window_fwd_f32(const float *q, const float *k, const float *v, int B, int S,
+                                  int nh, int nkv, int hd, int window, int sinks, float scale,
+                                  float *o, float *lse, void *stream);
+xattn_status xattn_window_bwd_f32(const float *q, const float *k, const float *v, const float *o,
+                                  const float *dO, const float *lse, int B, int S, int nh,
+                                  int nkv, int hd, int window, int sinks, float scale, float *dq,
+                                  float *dk, float *dv, void *stream);
+
 /*
  * Decode attention, bf16 (xtrain docs/evolution.md, post-training milestones M2a-M2c):
  * one new query per sequence against that sequence's cached keys and values -- equal to
@@ -246,6 +282,7 @@ xattn_status xattn_decode(const void *q, const void *k_cache, const void *v_cach
  */
 int xattn_decode_runs(int B, int T, int nh, int nkv, int hd, int num_sms);
 
+/* Static text for a status code (never NULL). */
 const char *xattn_status_string(xattn_status status);
 
 /*

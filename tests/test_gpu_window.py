@@ -1,0 +1,161 @@
+"""Window attention with sinks through the binding, against its definition in 64 bits (every
+element within a bound derived from the roundings, tests/window_ref.py), on windows and sinks
+that end inside, at and across tiles; against the causal op; gradients against differences;
+graphs, streams and run-to-run reproducibility."""
+import pytest
+import torch
+
+from bwd_xattn_fwd_gb300 import workloads as W
+from window_ref import check, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from bwd_xattn_fwd_gb300 import xattn  # noqa: F401  (fails loudly if not built)
+
+
+def _inputs(B, S, nh, nkv, hd, dtype, seed=0):
+    w = W.Workload("window", B, S, nh, nkv, hd, dtype, qkv_scale=0.5)
+    return {n: t.cuda() for n, t in W.make_inputs(w, seed=seed).items()}
+
+
+def _run(x, window, sinks, scale, deterministic=False):
+    from bwd_xattn_fwd_gb300 import xattn
+    q, k, v, dO = (x[n] for n in ("q", "k", "v", "dO"))
+    o, lse = xattn.attention_window_fwd(q, k, v, window, sinks, scale)
+    dq, dk, dv = xattn.attention_window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic=deterministic)
+    torch.cuda.synchronize()
+    assert xattn.xattn_check_device_status() == 0
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+
+# (B, S, nh, nkv, hd, window, sinks): lengths 1, below, at and past tiles; windows of one key,
+# ending inside and at tiles, spanning several, and beyond the sequence; no sinks, a few, a
+# tile's worth, more than one tile, all keys; query groups and one head per kv head
+SHAPES = [
+    (1, 1, 1, 1, 64, 1, 0),
+    (2, 5, 2, 1, 32, 2, 1),
+    (1, 128, 2, 2, 64, 1, 0),
+    (1, 129, 2, 2, 64, 128, 0),
+    (1, 300, 4, 2, 64, 1, 1),
+    (2, 300, 4, 2, 64, 7, 3),
+    (1, 640, 4, 4, 64, 129, 0),
+    (1, 700, 4, 1, 64, 128, 4),
+    (2, 1000, 4, 2, 64, 130, 4),
+    (1, 1100, 8, 2, 64, 257, 128),
+    (1, 1500, 4, 2, 64, 64, 129),
+    (1, 1500, 4, 2, 64, 300, 260),
+    (1, 900, 4, 2, 64, 2000, 3),
+    (1, 900, 4, 2, 64, 100, 2000),
+    (1, 900, 2, 1, 64, 899, 0),
+    (2, 515, 6, 3, 32, 60, 4),
+    (1, 1300, 4, 4, 32, 200, 17),
+    (1, 257, 2, 1, 128, 100, 0),
+    (1, 1290, 4, 2, 128, 300, 4),
+    (1, 1290, 2, 2, 128, 33, 140),
+    (24, 520, 8, 2, 64, 140, 4),       # several units per CTA
+    (3, 2100, 12, 12, 32, 500, 4),
+    (2, 4000, 4, 1, 64, 256, 4),       # sink tiles cut into many parts
+    (1, 3500, 8, 2, 128, 150, 130),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("deterministic", [False, True])
+def test_bf16(shape, deterministic):
+    B, S, nh, nkv, hd, window, sinks = shape
+    x = _inputs(B, S, nh, nkv, hd, "bf16", seed=S)
+    scale = hd ** -0.5
+    check(_run(x, window, sinks, scale, deterministic), reference(x, window, sinks, scale, True), str(shape))
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 1, 0), (2, 70, 4, 2, 24, 9, 0), (1, 130, 2, 2, 64, 33, 5),
+                                   (1, 260, 2, 1, 128, 64, 70), (1, 90, 3, 3, 33, 500, 0), (1, 90, 3, 1, 5, 1, 200)],
+                         ids=str)
+def test_f32(shape):
+    B, S, nh, nkv, hd, window, sinks = shape
+    x = _inputs(B, S, nh, nkv, hd, "f32", seed=S)
+    scale = hd ** -0.5
+    check(_run(x, window, sinks, scale), reference(x, window, sinks, scale, False), str(shape))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_scales(scale):
+    x = _inputs(1, 700, 4, 2, 64, "bf16", seed=3)
+    check(_run(x, 200, 4, scale), reference(x, 200, 4, scale, True), f"scale {scale}")
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_a_window_of_everything_is_the_causal_op(hd):
+    """The forward does the causal op's arithmetic in its order: bit for bit the same."""
+    from bwd_xattn_fwd_gb300 import xattn
+    x = _inputs(2, 700, 4, 2, hd, "bf16", seed=1)
+    q, k, v = (x[n] for n in ("q", "k", "v"))
+    o, lse = xattn.attention_window_fwd(q, k, v, xattn.NO_WINDOW)
+    ro, rl = xattn.attention_fwd(q, k, v)
+    assert torch.equal(o, ro) and torch.equal(lse, rl)
+
+
+def test_gradients_against_differences():
+    """Directional differences of L = sum(dO * o) in fp32 mode, taken in 64 bits of the
+    definition: (L(x + h d) - L(x - h d)) / 2h against <grad, d>. With h = 1e-4 the difference's
+    own error is O(h^2) ~ 1e-8 of the third derivative (unit-size inputs), far below 1e-4."""
+    shape = (1, 150, 4, 2, 32)
+    x = _inputs(*shape, "f32", seed=9)
+    window, sinks, scale = 40, 3, 32 ** -0.5
+    got = _run(x, window, sinks, scale)
+    g = torch.Generator("cuda").manual_seed(1)
+
+    def loss(y):
+        o = reference({**x, **y}, window, sinks, scale, False)["o"][0]
+        return float((x["dO"].double() * o).sum())
+
+    for name in ("q", "k", "v"):
+        d = torch.randn(x[name].shape, generator=g, device="cuda", dtype=torch.float64)
+        h = 1e-4
+        slope = (loss({name: x[name].double() + h * d}) - loss({name: x[name].double() - h * d})) / (2 * h)
+        dot = float((got["d" + name].double() * d).sum())
+        assert abs(dot - slope) <= 1e-4 * float((got["d" + name].double() * d).abs().sum()), (name, dot, slope)
+
+
+def test_reproducible():
+    """o, lse, dk and dv are bit for bit the same from run to run, dq too when asked for."""
+    x = _inputs(2, 2000, 8, 2, 64, "bf16", seed=4)
+    a, b = (_run(x, 300, 5, 0.125) for _ in range(2))
+    c, d = (_run(x, 300, 5, 0.125, deterministic=True) for _ in range(2))
+    for n in ("o", "lse", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
+    for n in c:
+        assert torch.equal(c[n], d[n]), n
+
+
+def test_graph_replay_and_streams():
+    """Forward and backward captured on a side stream, replayed on new inputs."""
+    from bwd_xattn_fwd_gb300 import xattn
+    x = _inputs(2, 600, 4, 2, 64, "bf16", seed=5)
+    scale = 0.125
+    _run(x, 100, 4, scale)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    q, k, v, dO = (x[n] for n in ("q", "k", "v", "dO"))
+    with torch.cuda.graph(graph, stream=side):
+        o, lse = xattn.attention_window_fwd(q, k, v, 100, 4, scale)
+        dq, dk, dv = xattn.attention_window_bwd(q, k, v, o, dO, lse, 100, 4, scale)
+    y = _inputs(2, 600, 4, 2, 64, "bf16", seed=6)
+    for n in x:
+        x[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert xattn.xattn_check_device_status() == 0
+    check({"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, reference(y, 100, 4, scale, True), "replay")
+    # an explicit stream, its outputs allocated for it
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    o2, lse2 = xattn.attention_window_fwd(q, k, v, 100, 4, scale, stream=other)
+    other.synchronize()
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)

@@ -1,0 +1,97 @@
+"""Window attention's argument checks, and its 64-bit reference against differences, without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from window_ref import reference
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from bwd_xattn_fwd_gb300 import build
+    return ctypes.CDLL(build.build())
+
+
+P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+
+
+def _fwd(lib, name="xattn_window_fwd", q=16, k=32, v=48, B=1, S=4, nh=2, nkv=1, hd=64, window=2, sinks=0,
+         scale=0.125, o=64, lse=80):
+    f = getattr(lib, name)
+    f.restype, f.argtypes = I, [P] * 3 + [I] * 7 + [F] + [P] * 3
+    return f(q, k, v, B, S, nh, nkv, hd, window, sinks, scale, o, lse, None)
+
+
+def _bwd(lib, name="xattn_window_bwd", q=16, hd=64, S=4, nh=2, nkv=1, window=2, sinks=0, scale=0.125, lse=96, dq=112):
+    f = getattr(lib, name)
+    f.restype = I
+    f.argtypes = [P] * 6 + [I] * 7 + [F] + ([I] if name == "xattn_window_bwd" else []) + [P] * 4
+    det = (0,) if name == "xattn_window_bwd" else ()
+    return f(q, 32, 48, 64, 80, lse, 1, S, nh, nkv, hd, window, sinks, scale, *det, dq, 128, 144, None)
+
+
+@pytest.mark.parametrize("name", ["xattn_window_fwd", "xattn_window_fwd_f32"])
+def test_forward_checks(lib, name):
+    assert _fwd(lib, name, q=None) == 1
+    assert _fwd(lib, name, lse=None) == 1
+    assert _fwd(lib, name, B=0) == 2
+    assert _fwd(lib, name, S=0) == 2
+    assert _fwd(lib, name, S=(1 << 30) + 1) == 2
+    assert _fwd(lib, name, nh=3, nkv=2) == 3
+    assert _fwd(lib, name, scale=float("nan")) == 9
+    assert _fwd(lib, name, window=0) == 13
+    assert _fwd(lib, name, window=-5) == 13
+    assert _fwd(lib, name, sinks=-1) == 13
+    assert _fwd(lib, name, hd=129) == 4
+    if name == "xattn_window_fwd":
+        assert _fwd(lib, hd=48) == 4
+        assert _fwd(lib, q=18) == 5
+        assert _fwd(lib, lse=82) == 5
+
+
+@pytest.mark.parametrize("name", ["xattn_window_bwd", "xattn_window_bwd_f32"])
+def test_backward_checks(lib, name):
+    assert _bwd(lib, name, q=None) == 1
+    assert _bwd(lib, name, S=-1) == 2
+    assert _bwd(lib, name, nh=3, nkv=2) == 3
+    assert _bwd(lib, name, window=0) == 13
+    assert _bwd(lib, name, sinks=-1) == 13
+    assert _bwd(lib, name, hd=130) == 4
+    assert _bwd(lib, name, scale=float("inf")) == 9
+    if name == "xattn_window_bwd":
+        assert _bwd(lib, scale=1e-30) == 9
+        assert _bwd(lib, dq=120) == 5
+        assert _bwd(lib, lse=98) == 5
+
+
+def test_accepted_sizes_reach_the_device(lib):
+    if not torch.cuda.is_available():
+        assert _fwd(lib, window=0x7FFFFFFF, sinks=0x7FFFFFFF) == 6
+        assert _bwd(lib, hd=128, window=0x7FFFFFFF, sinks=0x7FFFFFFF) == 6
+
+
+def test_helpers_refuse_what_they_cannot_read():
+    from bwd_xattn_fwd_gb300 import xattn
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):                                   # not on a GPU
+        xattn.attention_window_fwd(q, q, q, 2)
+    with pytest.raises(TypeError):
+        xattn.attention_window_fwd(q.half(), q.half(), q.half(), 2)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (3, 2), (20, 0), (4, 20)])
+def test_reference_gradients_against_differences(window, sinks):
+    g = torch.Generator().manual_seed(0)
+    x = {n: torch.randn(1, 12, h, 8, generator=g, dtype=torch.float64)
+         for n, h in (("q", 4), ("k", 2), ("v", 2), ("dO", 4))}
+    ref = reference(x, window, sinks, 0.3, False)
+
+    def loss(y):
+        return float((x["dO"] * reference({**x, **y}, window, sinks, 0.3, False)["o"][0]).sum())
+
+    for name in ("q", "k", "v"):
+        d = torch.randn(x[name].shape, generator=g, dtype=torch.float64)
+        h = 1e-5
+        slope = (loss({name: x[name] + h * d}) - loss({name: x[name] - h * d})) / (2 * h)
+        assert abs(float((ref["d" + name][0] * d).sum()) - slope) <= 1e-7 * (1 + abs(slope))
