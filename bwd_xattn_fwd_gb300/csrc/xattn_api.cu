@@ -24,7 +24,9 @@ struct DeviceInfo {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
   bool sm103 = false;
+  int sms = 0;
   int *status = nullptr;
+  cudaMemPool_t pool = nullptr;   // scratch_alloc's
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -84,11 +86,33 @@ xattn_status device_info(DeviceInfo **out) {
     d.err = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     d.sm103 = (major == 10 && minor == 3);
+    if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (d.err == cudaSuccess) {
+      cudaMemPoolProps props = {};
+      props.allocType = cudaMemAllocationTypePinned;
+      props.location.type = cudaMemLocationTypeDevice;
+      props.location.id = dev;
+      d.err = cudaMemPoolCreate(&d.pool, &props);
+    }
+    if (d.err == cudaSuccess) {
+      unsigned long long keep = ~0ull;
+      d.err = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    }
     if (d.err == cudaSuccess) d.err = cudaGetSymbolAddress(reinterpret_cast<void **>(&d.status), g_device_status);
   });
   if (d.err != cudaSuccess) return XATTN_ERR_CUDA;
   *out = &d;
   return XATTN_OK;
+}
+
+// Scratch of one call on `stream`, released with cudaFreeAsync on it. It comes from a pool of
+// the library's own that keeps what it has grown to: the default pool gives its memory back
+// at every synchronisation, and the next call would map it again (step of B8 S2048, each
+// call waited for: 471 us with the default pool against 134 us back to back).
+xattn_status scratch_alloc(const DeviceInfo &d, size_t bytes, cudaStream_t stream, void **out) {
+  if (cudaMallocFromPoolAsync(out, bytes, d.pool, stream) == cudaSuccess) return XATTN_OK;
+  cudaGetLastError();   // do not leave the failure for the caller's next error check
+  return XATTN_ERR_CUDA;
 }
 
 xattn_status get_encode() {
@@ -203,6 +227,42 @@ xattn_status check_window(int S, int window, int sinks, int *w, int *s) {
   *w = window < S ? window : S;
   *s = sinks < S ? sinks : S;
   return XATTN_OK;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes of a paged cache [num_pages, page_size, nkv, hd] and a table of max_pages entries a
+// sequence, for n new tokens a sequence.
+xattn_status check_pages(int B, int n, int nkv, int hd, int num_pages, int page_size, int max_pages) {
+  if (B <= 0 || n <= 0 || nkv <= 0 || hd <= 0 || num_pages <= 0 || max_pages <= 0) return XATTN_ERR_BAD_SHAPE;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && (page_size <= 0 || page_size % 128 != 0))
+    return XATTN_ERR_PAGES;
+  const long long most = 1ll << 30;   // positions and rows of one sequence's table stay far inside int32
+  if (page_size > most || static_cast<long long>(max_pages) * page_size > most ||
+      n > static_cast<long long>(max_pages) * page_size)
+    return XATTN_ERR_PAGES;
+  // Element offsets stay inside int64, grids inside int32.
+  if (static_cast<double>(num_pages) * page_size * nkv * hd > 0x1p60 ||
+      static_cast<double>(B) * n * nkv * hd > 0x1p38 || static_cast<double>(B) * max_pages > 0x1p40)
+    return XATTN_ERR_BAD_SHAPE;
+  return XATTN_OK;
+}
+
+// 4-D map over a pool [num_pages, page_size, nkv, hd]: box = up to 128 rows of one kv head in
+// one page (64 columns at hd = 128). Pages outside the pool read as zeros.
+xattn_status make_map_pages(CUtensorMap *map, const void *ptr, int num_pages, int page_size, int nkv, int hd) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(nkv),
+                              static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(hd) * 2;
+  const cuuint64_t strides[3] = {row, row * nkv, row * nkv * page_size};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(hd > 64 ? 64 : hd), 1,
+                             static_cast<cuuint32_t>(page_size < kTileRows ? page_size : kTileRows), 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
+                              strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              hd == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
 xattn_status bf16_device(DeviceInfo **dev) {
@@ -376,6 +436,83 @@ xattn_status xattn_decode(const void *q, const void *k_cache, const void *v_cach
   return r;
 }
 
+xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v_pages, const int *page_table,
+                               const int *ctx_lens, const unsigned long long *tree, int B, int n, int nh, int nkv,
+                               int hd, int num_pages, int page_size, int max_pages, int window, int sinks,
+                               float scale, void *o, float *lse, void *stream) {
+  if (!q || !k_pages || !v_pages || !page_table || !ctx_lens || !o || !lse) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_shape(B, n, nh, nkv, hd, scale));
+  XATTN_TRY(check_pages(B, n, nkv, hd, num_pages, page_size, max_pages));
+  if (n > XATTN_TREE_MAX) return XATTN_ERR_BAD_SHAPE;
+  if (window < n || sinks < 0) return XATTN_ERR_WINDOW;
+  if (hd != 32 && hd != 64 && hd != 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(lse) ||
+      !aligned4(page_table) || !aligned4(ctx_lens) || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  CUtensorMap mk, mv;
+  XATTN_TRY(make_map_pages(&mk, k_pages, num_pages, page_size, nkv, hd));
+  XATTN_TRY(make_map_pages(&mv, v_pages, num_pages, page_size, nkv, hd));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = tree_grid(B, n, nh, nkv, hd, page_size, max_pages, dev->sms);
+  TreeArgs a = {};
+  a.rec_rows = tree_record_rows(n, nh, nkv);
+  void *ws = nullptr;
+  XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.page_table = page_table;
+  a.ctx_lens = ctx_lens;
+  a.tree = tree;
+  a.o = static_cast<__nv_bfloat16 *>(o);
+  a.lse = lse;
+  a.ws_o = static_cast<float *>(ws);
+  a.ws_ml = a.ws_o + static_cast<size_t>(grid) * 2 * a.rec_rows * hd;
+  a.B = B, a.n = n, a.nh = nh, a.nkv = nkv;
+  a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
+  a.window = window < (1 << 30) ? window : (1 << 30);   // a table holds at most 2^30 positions
+  a.sinks = sinks < (1 << 30) ? sinks : (1 << 30);
+  a.scale_log2 = scale * kLog2e;
+  a.status = dev->status;
+  a.timeout_ns = wait_limit_ns();
+  xattn_status r = cuda_status(launch_tree_bf16(mk, mv, a, hd, grid, st));
+  const cudaError_t fe = cudaFreeAsync(ws, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
+}
+
+xattn_status xattn_cache_append(const void *k_new, const void *v_new, void *k_pages, void *v_pages,
+                                const int *page_table, const int *ctx_lens, int B, int n, int nkv, int hd,
+                                int num_pages, int page_size, int max_pages, void *stream) {
+  if (!k_new || !v_new || !k_pages || !v_pages || !page_table || !ctx_lens) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_pages(B, n, nkv, hd, num_pages, page_size, max_pages));
+  if (hd % 8 != 0) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) ||
+      !aligned4(ctx_lens))
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const PageArgs a = {static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), page_table, ctx_lens, B, n,
+                      nkv * hd / 8, num_pages, page_size, max_pages};
+  return cuda_status(launch_cache_append(a, k_new, v_new, static_cast<cudaStream_t>(stream)));
+}
+
+xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_table, const int *ctx_lens,
+                                 const int *path, const int *accepted, int B, int n, int nkv, int hd, int num_pages,
+                                 int page_size, int max_pages, void *stream) {
+  if (!k_pages || !v_pages || !page_table || !ctx_lens || !path || !accepted) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_pages(B, n, nkv, hd, num_pages, page_size, max_pages));
+  if (hd % 8 != 0) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) || !aligned4(ctx_lens) || !aligned4(path) ||
+      !aligned4(accepted))
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const PageArgs a = {static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), page_table, ctx_lens, B, n,
+                      nkv * hd / 8, num_pages, page_size, max_pages};
+  return cuda_status(launch_cache_compact(a, path, accepted, static_cast<cudaStream_t>(stream)));
+}
+
 xattn_status xattn_bwd_deterministic(const void *q, const void *k, const void *v, const void *o,
                                      const void *dO, const float *lse, int B, int S, int nh,
                                      int nkv, int hd, float scale, void *dq, void *dk, void *dv,
@@ -470,10 +607,7 @@ xattn_status xattn_window_bwd(const void *q, const void *k, const void *v, const
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t base_bytes = (bwd_workspace_bytes(B, S, nh, hd, fused) + 255) / 256 * 256;
   void *base = nullptr;
-  if (cudaMallocAsync(&base, base_bytes + window_parts_bytes(B, S, nkv, hd, w, s), st) != cudaSuccess) {
-    cudaGetLastError();   // do not leave the failure for the caller's next error check
-    return XATTN_ERR_CUDA;
-  }
+  XATTN_TRY(scratch_alloc(*dev, base_bytes + window_parts_bytes(B, S, nkv, hd, w, s), st, &base));
   float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(base) + base_bytes);
   const BwdWorkspace ws = bwd_workspace_carve(base, B, S, nh, hd);
   xattn_status r = make_map_aux(&maux, ws.aux, B, S, nh);
@@ -561,7 +695,9 @@ const char *xattn_status_string(xattn_status s) {
     case XATTN_ERR_WORKSPACE: return "workspace is NULL, not 256-byte aligned, or too small";
     case XATTN_ERR_SCRATCH_LIMIT:
       return "these sizes need more scratch than xattn_bwd_noalloc's fixed array holds";
-    case XATTN_ERR_WINDOW: return "window must be positive and sinks not negative";
+    case XATTN_ERR_WINDOW: return "window must be positive (xattn_tree_decode: at least n) and sinks not negative";
+    case XATTN_ERR_PAGES:
+      return "page_size must be 16, 32, 64 or a multiple of 128, and the table hold n to 2^30 positions a sequence";
     case XATTN_ERR_DEVICE_BOUNDS:
       return "an on-device bounds check failed (debug build)";
   }

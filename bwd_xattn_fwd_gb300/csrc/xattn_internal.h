@@ -147,4 +147,34 @@ cudaError_t launch_window_bwd_f32(const float *q, const float *k, const float *v
                                   const float *lse, float *dq, float *dk, float *dv, int B, int S, int nh, int nkv,
                                   int hd, float scale, int window, int sinks, cudaStream_t stream);
 
+// Attention of n new tokens per sequence over a paged cache (attn_tree.cu). mk, mv: maps over
+// the pools [num_pages, page_size, nkv, hd] with boxes of min(page_size, 128) rows of one kv
+// head (64 columns at hd = 128). ws_o, ws_ml: tree_workspace_bytes(grid, rec_rows, hd) bytes,
+// ws_ml after the 2 grid rec_rows hd floats of ws_o.
+struct TreeArgs {
+  const __nv_bfloat16 *q;
+  const int *page_table, *ctx_lens;
+  const unsigned long long *tree;      // null: token i sees new tokens 0 .. i
+  __nv_bfloat16 *o;
+  float *lse, *ws_o, *ws_ml;
+  int B, n, nh, nkv, num_pages, page_size, max_pages, window, sinks, rec_rows;
+  float scale_log2;
+  int *status;
+  unsigned long long timeout_ns;
+};
+int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_pages, int sms);
+int tree_record_rows(int n, int nh, int nkv);
+size_t tree_workspace_bytes(int grid, int rec_rows, int hd);
+cudaError_t launch_tree_bf16(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int hd, int grid,
+                             cudaStream_t stream);
+
+// Rows of a paged cache (cache_pages.cu); row_vecs: 16-byte vectors of a row, nkv hd / 8.
+struct PageArgs {
+  uint4 *k_pages, *v_pages;
+  const int *page_table, *ctx_lens;
+  int B, n, row_vecs, num_pages, page_size, max_pages;
+};
+cudaError_t launch_cache_append(const PageArgs &a, const void *k_new, const void *v_new, cudaStream_t stream);
+cudaError_t launch_cache_compact(const PageArgs &a, const int *path, const int *accepted, cudaStream_t stream);
+
 }  // namespace xattn

@@ -45,6 +45,7 @@ class Status(enum.IntEnum):
     ERR_SCRATCH_LIMIT = 11
     ERR_DEVICE_BOUNDS = 12
     ERR_WINDOW = 13
+    ERR_PAGES = 14
 
 
 class XattnError(RuntimeError):
@@ -73,6 +74,9 @@ _SIGS = {
     "xattn_window_bwd": [_vp] * 6 + [_i] * 7 + [_f, _i] + [_vp] * 4,
     "xattn_window_fwd_f32": [_vp] * 3 + [_i] * 7 + [_f] + [_vp] * 3,
     "xattn_window_bwd_f32": [_vp] * 6 + [_i] * 7 + [_f] + [_vp] * 4,
+    "xattn_tree_decode": [_vp] * 6 + [_i] * 10 + [_f] + [_vp] * 3,
+    "xattn_cache_append": [_vp] * 6 + [_i] * 7 + [_vp],
+    "xattn_cache_compact": [_vp] * 6 + [_i] * 7 + [_vp],
     "xattn_check_device_status": [_vp],
 }
 for _name, _args in _SIGS.items():
@@ -92,6 +96,7 @@ _lib.xattn_build_flags.restype = ctypes.c_int
 _lib.xattn_selftest_bounds_check.argtypes = [_vp]
 _lib.xattn_selftest_bounds_check.restype = ctypes.c_int
 
+TREE_MAX = 64                       # XATTN_TREE_MAX in xattn.h
 NO_WINDOW = 0x7FFFFFFF              # XATTN_NO_WINDOW in xattn.h
 BWD_FUSED_DQ, BWD_RESIDENT_DQ, BWD_QUERY_DQ = 0, 1, 2
 BUILD_DEVICE_CHECKS = 1             # xattn_build_flags bit: on-device bounds checks compiled in
@@ -223,6 +228,25 @@ def xattn_window_fwd_f32(q, k, v, B, S, nh, nkv, hd, window, sinks, scale, o, ls
 def xattn_window_bwd_f32(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, dq, dk, dv, stream=None):
     _call("xattn_window_bwd_f32", _addr(q), _addr(k), _addr(v), _addr(o), _addr(dO), _addr(lse), B, S, nh, nkv, hd,
           window, sinks, scale, _addr(dq), _addr(dk), _addr(dv), _stream(stream))
+
+
+def xattn_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, B, n, nh, nkv, hd, num_pages, page_size,
+                      max_pages, window, sinks, scale, o, lse, stream=None):
+    _call("xattn_tree_decode", _addr(q), _addr(k_pages), _addr(v_pages), _addr(page_table), _addr(ctx_lens),
+          _addr(tree), B, n, nh, nkv, hd, num_pages, page_size, max_pages, window, sinks, scale, _addr(o), _addr(lse),
+          _stream(stream))
+
+
+def xattn_cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, B, n, nkv, hd, num_pages, page_size,
+                       max_pages, stream=None):
+    _call("xattn_cache_append", _addr(k_new), _addr(v_new), _addr(k_pages), _addr(v_pages), _addr(page_table),
+          _addr(ctx_lens), B, n, nkv, hd, num_pages, page_size, max_pages, _stream(stream))
+
+
+def xattn_cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, B, n, nkv, hd, num_pages, page_size,
+                        max_pages, stream=None):
+    _call("xattn_cache_compact", _addr(k_pages), _addr(v_pages), _addr(page_table), _addr(ctx_lens), _addr(path),
+          _addr(accepted), B, n, nkv, hd, num_pages, page_size, max_pages, _stream(stream))
 
 
 def xattn_selftest_wait_timeout(limit_ns, stream=None):
@@ -397,3 +421,74 @@ def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, strea
         else:
             xattn_window_bwd_f32(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, dq, dk, dv, handle)
     return dq, dk, dv
+
+
+def _pool(k_pages, v_pages, page_table, ctx_lens):
+    """The checks of a paged cache's tensors, and its sizes."""
+    import torch
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages, v_pages must be [num_pages,page_size,nkv,hd] and page_table [B,max_pages]")
+    B, max_pages = page_table.shape
+    return B, max_pages, (("k_pages", k_pages, k_pages.shape, torch.bfloat16),
+                          ("v_pages", v_pages, k_pages.shape, torch.bfloat16),
+                          ("page_table", page_table, page_table.shape, torch.int32),
+                          ("ctx_lens", ctx_lens, (B,), torch.int32))
+
+
+def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, window=None, sinks=0, scale=None,
+                          stream=None):
+    """(o [B,n,nh,hd], lse [B,n,nh]) of n <= 64 new tokens a sequence over a paged cache: q
+    [B,n,nh,hd] against the pools [num_pages,page_size,nkv,hd] (bf16), through page_table
+    [B,max_pages] and ctx_lens [B] (int32); the new tokens' K and V are already at positions
+    ctx_lens .. ctx_lens + n - 1 (cache_append). tree [B,n] (int64): bit j of word i lets token
+    i see new token j; None: token i sees new tokens 0 .. i (n = 1: the decode step). window
+    (None: no window) and sinks as in attention_window_fwd."""
+    import torch
+    B, max_pages, tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
+    if q.dim() != 4:
+        raise ValueError("q must be [B,n,nh,hd]")
+    n, nh = int(q.shape[1]), int(q.shape[2])
+    num_pages, page_size, nkv, hd = k_pages.shape
+    tensors = (("q", q, (B, n, nh, hd), torch.bfloat16), *tensors)
+    if tree is not None:
+        tensors = (*tensors, ("tree", tree, (B, n), torch.int64))
+    device = _check(tensors)
+    scale = float(hd ** -0.5 if scale is None else scale)
+    window = NO_WINDOW if window is None else window
+    with _On(device, stream) as handle:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, n, nh), dtype=torch.float32, device=device)
+        xattn_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, B, n, nh, nkv, hd, num_pages, page_size,
+                          max_pages, window, sinks, scale, o, lse, handle)
+    return o, lse
+
+
+def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=None):
+    """Writes the rows k_new, v_new [B,n,nkv,hd] to positions ctx_lens .. ctx_lens + n - 1 of each
+    sequence's pages (in place)."""
+    import torch
+    B, max_pages, tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
+    num_pages, page_size, nkv, hd = k_pages.shape
+    if k_new.dim() != 4:
+        raise ValueError("k_new and v_new must be [B,n,nkv,hd]")
+    n = int(k_new.shape[1])
+    device = _check((*tensors, ("k_new", k_new, (B, n, nkv, hd), torch.bfloat16),
+                     ("v_new", v_new, (B, n, nkv, hd), torch.bfloat16)))
+    with _On(device, stream) as handle:
+        xattn_cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, B, n, nkv, hd, num_pages, page_size,
+                           max_pages, handle)
+
+
+def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream=None):
+    """Moves the rows of positions ctx_lens + path[:, i], i < accepted, down to ctx_lens + i (in
+    place): path [B,n] (int32, ascending over its accepted entries), accepted [B] (int32)."""
+    import torch
+    B, max_pages, tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
+    num_pages, page_size, nkv, hd = k_pages.shape
+    if path.dim() != 2:
+        raise ValueError("path must be [B,n]")
+    n = int(path.shape[1])
+    device = _check((*tensors, ("path", path, (B, n), torch.int32), ("accepted", accepted, (B,), torch.int32)))
+    with _On(device, stream) as handle:
+        xattn_cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, B, n, nkv, hd, num_pages,
+                            page_size, max_pages, handle)

@@ -69,7 +69,8 @@ typedef enum {
     XATTN_ERR_SCRATCH_LIMIT = 11,     /* xattn_bwd_noalloc: sizes need more than its fixed scratch */
     XATTN_ERR_DEVICE_BOUNDS = 12,     /* debug builds only: an on-device bounds check failed
                                          (reported later, like a timeout) */
-    XATTN_ERR_WINDOW = 13             /* window < 1 or sinks < 0 */
+    XATTN_ERR_WINDOW = 13,            /* window < 1 (xattn_tree_decode: < n) or sinks < 0 */
+    XATTN_ERR_PAGES = 14              /* page_size or the page table's width out of range */
 } xattn_status;
 
 /*
@@ -281,6 +282,70 @@ xattn_status xattn_decode(const void *q, const void *k_cache, const void *v_cach
  * GPU model.
  */
 int xattn_decode_runs(int B, int T, int nh, int nkv, int hd, int num_sms);
+
+/*
+ * A paged K/V cache: two pools k_pages, v_pages [num_pages, page_size, nkv, hd] (bf16) and a
+ * table page_table [B, max_pages] (int) of page numbers. Position p of sequence b is row
+ * p % page_size of page page_table[b][p / page_size]; ctx_lens [B] (int) counts its committed
+ * positions. page_size is 16, 32, 64 or a multiple of 128, and max_pages * page_size at most
+ * 2^30 (else XATTN_ERR_PAGES). The table and the lengths are read on the device when the call
+ * runs, so a captured graph follows their contents. A table entry outside [0, num_pages) is
+ * no page: its positions are not visible, and rows for them are dropped. Lengths are taken
+ * within [0, max_pages * page_size - n] by xattn_tree_decode. The pools, tables and lengths
+ * of the three calls below are the same; the pages have no counterpart for them.
+ */
+
+/*
+ * Attention of n new tokens per sequence over its paged cache, bf16. The new tokens' K and V
+ * are already in the cache, at positions ctx_b .. ctx_b + n - 1 (xattn_cache_append).
+ *   q     [B, n, nh, hd] bf16;  o [B, n, nh, hd] bf16 out;  lse [B, n, nh] float out
+ *   tree  [B, n] 64-bit words, 8-byte aligned, or NULL. Bit j of word i: new token i sees new
+ *         token j (a token's own bit is the caller's too); bits n .. 63 are ignored. NULL:
+ *         token i sees new tokens 0 .. i (a run of tokens, or with n = 1 the decode step).
+ * With depth_i = (bits of word i) - 1 (at least 0), token i stands at ctx_b + depth_i and
+ * sees committed position p when ctx_b + depth_i - p < window or p < sinks.
+ * A token that sees nothing gives o = 0 and lse = -infinity. Positions that no token of the
+ * sequence sees are never used and may hold anything, NaN included; K and V at positions
+ * that some token sees must be finite.
+ * n <= XATTN_TREE_MAX (else XATTN_ERR_BAD_SHAPE); hd in {32, 64, 128}; nh a multiple of nkv
+ * (any group); window >= n (so that a window never ends inside the tree) and sinks >= 0
+ * (else XATTN_ERR_WINDOW; XATTN_NO_WINDOW for none); any finite scale. q, k_pages, v_pages
+ * and o 16-byte aligned, the int and float arrays 4-byte.
+ * Arithmetic as in xattn_fwd: tensor-core products on the bf16 inputs with fp32 accumulation,
+ * P rounded to bf16 before the P.V product, softmax statistics in fp32. Scratch is stream-
+ * ordered (allocated and freed on `stream`). The result is bit-for-bit reproducible for given
+ * lengths, sizes and SM count.
+ */
+#define XATTN_TREE_MAX 64
+xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v_pages,
+                               const int *page_table, const int *ctx_lens,
+                               const unsigned long long *tree, int B, int n, int nh, int nkv,
+                               int hd, int num_pages, int page_size, int max_pages, int window,
+                               int sinks, float scale, void *o, float *lse, void *stream);
+
+/*
+ * Writes n new tokens' rows k_new, v_new [B, n, nkv, hd] to positions ctx_b .. ctx_b + n - 1 of
+ * each sequence. Positions outside the table, or whose entry is no page, are dropped; no
+ * other row is touched. Two sequences must not append to one page. hd a multiple of 8 (else
+ * XATTN_ERR_UNSUPPORTED_HD); any n that the table can hold. No scratch.
+ */
+xattn_status xattn_cache_append(const void *k_new, const void *v_new, void *k_pages,
+                                void *v_pages, const int *page_table, const int *ctx_lens, int B,
+                                int n, int nkv, int hd, int num_pages, int page_size,
+                                int max_pages, void *stream);
+
+/*
+ * Keeps the accepted path of a tree of n drafted tokens: moves the rows of positions
+ * ctx_b + path[b][i], i < accepted[b], to ctx_b + i, in place. path [B, n] (int) ascends over
+ * its first accepted[b] entries (so path[b][i] >= i); accepted [B] (int) is taken within
+ * [0, n]. An entry that is not above its index stays where it is; one beyond n - 1, or whose
+ * row or place is no page, is not moved. Rows behind the accepted ones keep what they held. hd
+ * a multiple of 8 (else XATTN_ERR_UNSUPPORTED_HD). No scratch.
+ */
+xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_table,
+                                 const int *ctx_lens, const int *path, const int *accepted,
+                                 int B, int n, int nkv, int hd, int num_pages, int page_size,
+                                 int max_pages, void *stream);
 
 /* Static text for a status code (never NULL). */
 const char *xattn_status_string(xattn_status status);

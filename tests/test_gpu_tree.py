@@ -1,0 +1,325 @@
+"""Tree attention over a paged cache and the cache's page operations through the binding,
+against plain forms (tests/paged_ref.py): ragged and empty caches, pages that end inside tiles,
+rows that hold NaN wherever no token looks, freed pages, windows and sinks, words that see
+nothing, odd groups; a turn of drafted decoding as a program runs it; graphs and streams."""
+import math
+import random
+
+import pytest
+import torch
+
+from paged_ref import (append_reference, check_tree, compact_reference, paged_state, random_words, signed,
+                       tree_reference)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from bwd_xattn_fwd_gb300 import xattn  # noqa: F401  (fails loudly if not built)
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _q(B, n, nh, hd, seed):
+    g = torch.Generator().manual_seed(seed + 1000)
+    return (torch.randn(B, n, nh, hd, generator=g) * 0.5).to(torch.bfloat16).cuda()
+
+
+def _attend(q, k, v, table, lens, words, window, sinks, scale=None):
+    from bwd_xattn_fwd_gb300 import xattn
+    tree = None if words is None else torch.tensor(signed(words), device="cuda")
+    o, lse = xattn.attention_tree_decode(q, k, v, _i32(table), _i32(lens), tree=tree, window=window, sinks=sinks,
+                                         scale=scale)
+    torch.cuda.synchronize()
+    assert xattn.xattn_check_device_status() == 0
+    return o, lse
+
+
+def _lens(B, top, seed):
+    rng = random.Random(seed)
+    return [rng.choice([0, 1, top, rng.randint(0, top)]) for _ in range(B)]
+
+
+BIG = 2**31 - 1
+# (B, n, nh, nkv, hd, page, longest cache, window, sinks)
+CASES = [
+    (1, 1, 1, 1, 64, 16, 0, BIG, 0),
+    (1, 1, 4, 1, 64, 16, 5, BIG, 0),
+    (3, 1, 8, 2, 64, 64, 300, BIG, 0),
+    (2, 5, 8, 2, 64, 16, 127, BIG, 0),
+    (2, 3, 4, 4, 32, 32, 128, BIG, 0),
+    (4, 8, 16, 4, 64, 128, 700, BIG, 0),
+    (2, 7, 6, 2, 128, 16, 500, BIG, 0),
+    (2, 64, 4, 4, 64, 16, 333, BIG, 0),
+    (2, 64, 16, 2, 64, 64, 600, BIG, 0),       # 512 rows a kv head: four row tiles
+    (2, 27, 14, 2, 32, 16, 450, BIG, 0),       # a group of 7: rows end inside a tile
+    (2, 61, 8, 1, 128, 256, 700, BIG, 0),      # pages wider than a tile
+    (1, 2, 2, 1, 64, 384, 1000, BIG, 0),
+    (3, 1, 8, 2, 64, 16, 900, 1, 0),           # a window of the token alone
+    (3, 4, 8, 2, 64, 16, 900, 4, 3),
+    (3, 1, 8, 2, 128, 16, 1500, 129, 4),
+    (2, 16, 8, 2, 64, 32, 2000, 300, 130),
+    (2, 9, 4, 2, 32, 64, 1200, 128, 128),
+    (3, 5, 4, 2, 64, 16, 600, 200, 5000),      # more sinks than positions
+    (70, 2, 8, 2, 64, 16, 400, BIG, 0),        # more sequences than a warp scans at once
+    (200, 1, 4, 4, 32, 32, 900, 256, 4),
+    (1, 4, 4, 1, 64, 64, 30000, BIG, 0),       # one long cache over every CTA
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+@pytest.mark.parametrize("shape", ["tree", "run"])
+def test_tree_attention(case, shape):
+    B, n, nh, nkv, hd, page, top, window, sinks = case
+    lens = _lens(B, top, seed=top + n)
+    lens[0] = top
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=7, device="cuda")
+    words = random_words(B, n, seed=3) if shape == "tree" else None
+    q = _q(B, n, nh, hd, seed=n)
+    o, lse = _attend(q, k, v, table, lens, words, window, sinks)
+    check_tree(o, lse, tree_reference(q, k, v, table, lens, words, window, sinks, hd ** -0.5), f"{case} {shape}")
+
+
+def test_words_that_see_nothing():
+    """With an empty cache a word of zero sees nothing: o = 0, lse = -inf; arbitrary words
+    (without the token's own bit, with bits past n) mean what their bits say."""
+    B, n, nh, nkv, hd, page = 4, 6, 8, 2, 64, 16
+    lens = [0, 0, 50, 200]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=1, device="cuda")
+    words = [[0, 0, 0, 0, 0, 0], [0, 1, 0, 0b100000, 0b111, ~0 & (2**64 - 1)], [0] * 6, [2, 1, 0, 5 << 40, 63, 8]]
+    q = _q(B, n, nh, hd, seed=2)
+    o, lse = _attend(q, k, v, table, lens, words, BIG, 0)
+    check_tree(o, lse, tree_reference(q, k, v, table, lens, words, BIG, 0, hd ** -0.5), "words")
+    assert bool((o[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+
+
+@pytest.mark.parametrize("hd,page", [(64, 16), (128, 32), (32, 128)])
+def test_missing_pages_and_lengths_out_of_range(hd, page):
+    """Entries outside the pool hold no positions (-1, the pool's size, the extremes of int32);
+    lengths are taken within what the table holds."""
+    B, n, nh, nkv = 5, 3, 4, 2
+    lens = [400, 130, 390, 64, 256]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=5, device="cuda")
+    num_pages = k.shape[0]
+    table[0][1] = -1
+    table[1][0] = num_pages
+    table[2] = [-(2**31)] * len(table[2])
+    table[3][0] = 2**31 - 1
+    q = _q(B, n, nh, hd, seed=8)
+    for words in (None, random_words(B, n, 1)):
+        o, lse = _attend(q, k, v, table, lens, words, BIG, 0)
+        check_tree(o, lse, tree_reference(q, k, v, table, lens, words, BIG, 0, hd ** -0.5), "missing pages")
+    k, v, table = paged_state(2, n, nkv, hd, page, [200, 300], seed=5, device="cuda")
+    cap = len(table[0]) * page
+    k.nan_to_num_(nan=0.25)
+    v.nan_to_num_(nan=0.25)
+    q = _q(2, n, nh, hd, seed=8)
+    wild = [-5, cap + 1000]
+    o, lse = _attend(q, k, v, table, wild, None, BIG, 0)
+    check_tree(o, lse, tree_reference(q, k, v, table, wild, None, BIG, 0, hd ** -0.5), "lengths")
+
+
+@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("sinks", [0, 4])
+def test_pages_behind_the_window_may_be_freed(n, sinks):
+    """The answer does not change when pages that no token sees are freed (-1) or point at a page
+    that now holds NaN."""
+    B, nh, nkv, hd, page, window = 3, 8, 2, 64, 16, 200
+    lens = [1000, 450, 777]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=4, device="cuda")
+    q = _q(B, n, nh, hd, seed=4)
+    o, lse = _attend(q, k, v, table, lens, None, window, sinks)
+    check_tree(o, lse, tree_reference(q, k, v, table, lens, None, window, sinks, hd ** -0.5), "kept")
+    stale = k.shape[0]
+    k2 = torch.cat([k, torch.full_like(k[:1], math.nan)])
+    v2 = torch.cat([v, torch.full_like(v[:1], math.nan)])
+    for b in range(B):
+        for e in range(len(table[b])):
+            if e * page >= sinks and (e + 1) * page <= lens[b] - window + 1:
+                table[b][e] = -1 if e % 2 else stale
+    o2, lse2 = _attend(q, k2, v2, table, lens, None, window, sinks)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.5, 3.0])
+def test_scales(scale):
+    B, n, nh, nkv, hd, page, lens = 2, 4, 4, 2, 64, 32, [300, 90]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=2, device="cuda")
+    q, words = _q(B, n, nh, hd, 1), random_words(B, n, 2)
+    o, lse = _attend(q, k, v, table, lens, words, BIG, 0, scale=scale)
+    check_tree(o, lse, tree_reference(q, k, v, table, lens, words, BIG, 0, scale), f"scale {scale}")
+
+
+def test_shared_pages_and_the_contiguous_decode():
+    """Sequences that share their prefix's pages; and a cache laid out in order agrees with
+    xattn_decode within both bounds (bf16 rounding of o and of P: 2^-7 of sum p |v| <= max |v|)."""
+    from bwd_xattn_fwd_gb300 import xattn
+    B, nh, nkv, hd, page, T = 4, 8, 2, 64, 64, 640
+    k, v, table = paged_state(B, 1, nkv, hd, page, [T - 1] * B, seed=6, device="cuda", spare=0)
+    for b in range(1, B):
+        table[b][:4] = table[0][:4]
+    q = _q(B, 1, nh, hd, 3)
+    lens = [T - 1] * B
+    o, lse = _attend(q, k, v, table, lens, None, BIG, 0)
+    check_tree(o, lse, tree_reference(q, k, v, table, lens, None, BIG, 0, hd ** -0.5), "shared")
+    idx = torch.tensor(table, device="cuda")
+    kc, vc = (p[idx].view(B, T, nkv, hd).contiguous() for p in (k, v))
+    oc, lc = xattn.attention_decode(q[:, 0].contiguous(), kc, vc)
+    assert float((oc.float() - o[:, 0].float()).abs().max()) <= 2 * 2.0 ** -7 * float(vc.float().abs().max())
+    assert float((lc - lse[:, 0]).abs().max()) <= 2.0 ** -8
+
+
+def test_reproducible_and_rows_of_other_sequences_do_not_matter():
+    B, n, nh, nkv, hd, page = 9, 4, 8, 2, 64, 16
+    lens = _lens(B, 800, 5)
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=9, device="cuda")
+    q, words = _q(B, n, nh, hd, 5), random_words(B, n, 5)
+    a = _attend(q, k, v, table, lens, words, 300, 4)
+    b = _attend(q, k, v, table, lens, words, 300, 4)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+PAGE_CASES = [(1, 1, 1, 8, 16, [0]), (3, 1, 2, 64, 16, [5, 0, 31]), (2, 37, 4, 32, 32, [0, 63]),
+              (5, 16, 1, 128, 64, [1, 64, 100, 7, 0]), (2, 300, 3, 24, 128, [17, 250]), (4, 64, 8, 128, 16, [9, 0, 3, 200])]
+
+
+@pytest.mark.parametrize("case", PAGE_CASES, ids=str)
+def test_append(case):
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nkv, hd, page, lens = case
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=n, device="cuda")
+    k.nan_to_num_(nan=7.0)
+    v.nan_to_num_(nan=9.0)
+    if B > 2:
+        table[1][lens[1] // page] = -1               # rows without a page are dropped
+        table[2][lens[2] // page] = k.shape[0]
+    g = torch.Generator().manual_seed(n)
+    kn, vn = (torch.randn(B, n, nkv, hd, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    rk, rv = append_reference(kn, vn, k, v, table, lens)
+    xattn.cache_append(kn, vn, k, v, _i32(table), _i32(lens))
+    assert torch.equal(k, rk) and torch.equal(v, rv)
+    # past the table's end, and before position 0: the rows that have no place are dropped
+    far = [len(table[0]) * page - (n + 1) // 2] * B
+    far[-1] = -(n // 2)
+    rk, rv = append_reference(vn, kn, k, v, table, far)
+    xattn.cache_append(vn, kn, k, v, _i32(table), _i32(far))
+    assert torch.equal(k, rk) and torch.equal(v, rv)
+
+
+@pytest.mark.parametrize("case", [c for c in PAGE_CASES if c[1] <= 64], ids=str)
+def test_compact(case):
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nkv, hd, page, lens = case
+    rng = random.Random(n)
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=n, device="cuda")
+    k.nan_to_num_(nan=7.0)
+    v.nan_to_num_(nan=9.0)
+    for accepted in ([n] * B, [min(n, rng.randint(0, 12)) for _ in range(B)], [0] * B, [n + 5] + [-3] * (B - 1)):
+        path = [sorted(rng.sample(range(n), min(max(a, 0), n))) + [0] * (n - min(max(a, 0), n)) for a in accepted]
+        rk, rv = compact_reference(k, v, table, lens, path, accepted)
+        xattn.cache_compact(k, v, _i32(table), _i32(lens), _i32(path), _i32(accepted))
+        assert torch.equal(k, rk) and torch.equal(v, rv), accepted
+    # a path that skips far ahead, an entry past n, one below its place
+    path = [[min(n - 1, i + n // 2) for i in range(n)] for _ in range(B)]
+    path[0] = [n + 3] * n
+    accepted = [min(n, n // 2 + 1)] * B
+    if B > 2:
+        table[2][lens[2] // page] = -1
+    rk, rv = compact_reference(k, v, table, lens, path, accepted)
+    xattn.cache_compact(k, v, _i32(table), _i32(lens), _i32(path), _i32(accepted))
+    assert torch.equal(k, rk) and torch.equal(v, rv)
+
+
+def test_a_turn_of_drafted_decoding():
+    """A windowed model's program: a prompt through the window forward and into the pages, a tree
+    drafted and attended, its accepted path kept, then one more token; each token's output equals
+    the window forward's of the sequence that was accepted (both within bf16's bounds of the
+    definition, which the reference is)."""
+    from bwd_xattn_fwd_gb300 import xattn
+    from window_ref import reference
+    B, P, n, nh, nkv, hd, page, window, sinks = 2, 150, 6, 8, 2, 64, 16, 70, 3
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *s: (torch.randn(*s, generator=g) * 0.5).to(torch.bfloat16).cuda()  # noqa: E731
+    k, v, table = paged_state(B, 20, nkv, hd, page, [P] * B, seed=1, device="cuda")
+    k.fill_(math.nan)
+    v.fill_(math.nan)
+    tb, zero = _i32(table), _i32([0] * B)
+    qp, kp, vp = rnd(B, P, nh, hd), rnd(B, P, nkv, hd), rnd(B, P, nkv, hd)
+    xattn.attention_window_fwd(qp, kp, vp, window, sinks)
+    xattn.cache_append(kp, vp, k, v, tb, zero)
+    # tree: 0 -> {1, 2}, 2 -> {3, 4}, 4 -> 5; accepted: 0, 2, 4
+    words = [[0b1, 0b11, 0b101, 0b1101, 0b10101, 0b110101]] * B
+    path = [0, 2, 4]
+    lens = _i32([P] * B)
+    qd, kd, vd = rnd(B, n, nh, hd), rnd(B, n, nkv, hd), rnd(B, n, nkv, hd)
+    xattn.cache_append(kd, vd, k, v, tb, lens)
+    o, lse = xattn.attention_tree_decode(qd, k, v, tb, lens, tree=torch.tensor(words, device="cuda"), window=window,
+                                         sinks=sinks)
+    xattn.cache_compact(k, v, tb, lens, _i32([path + [0] * 3] * B), _i32([3] * B))
+    lens = lens + 3
+    q1, k1, v1 = rnd(B, 1, nh, hd), rnd(B, 1, nkv, hd), rnd(B, 1, nkv, hd)
+    xattn.cache_append(k1, v1, k, v, tb, lens)
+    o1, lse1 = xattn.attention_tree_decode(q1, k, v, tb, lens, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert xattn.xattn_check_device_status() == 0
+    seq = {"q": torch.cat([qp, qd[:, path], q1], 1), "k": torch.cat([kp, kd[:, path], k1], 1),
+           "v": torch.cat([vp, vd[:, path], v1], 1)}
+    seq["dO"] = torch.zeros_like(seq["q"])
+    ref = reference(seq, window, sinks, hd ** -0.5, True)
+    got_o, got_l = torch.cat([o[:, path], o1], 1).double(), torch.cat([lse[:, path], lse1], 1).double()
+    val, err = ref["o"]
+    assert float(((got_o - val[:, P:]).abs() / err[:, P:]).max()) <= 1.0
+    assert float((got_l - ref["lse"][0][:, P:]).abs().max()) <= float(ref["lse"][1].max())
+
+
+def test_graphs_follow_lengths_and_two_graphs_do_not_meet():
+    """Two captured turns on two streams replayed together, after the lengths and the table have
+    changed under them."""
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nh, nkv, hd, page = 3, 4, 8, 2, 64, 16
+    states = []
+    for seed in (1, 2):
+        k, v, table = paged_state(B, n, nkv, hd, page, [900, 50, 400], seed=seed, device="cuda")
+        words = random_words(B, n, seed)
+        s = dict(k=k, v=v, table=table, tb=_i32(table), lens=_i32([5, 50, 100]), q=_q(B, n, nh, hd, seed), words=words,
+                 tree=torch.tensor(signed(words), device="cuda"), stream=torch.cuda.Stream(),
+                 graph=torch.cuda.CUDAGraph())
+        states.append(s)
+    call = lambda s: xattn.attention_tree_decode(s["q"], s["k"], s["v"], s["tb"], s["lens"], tree=s["tree"])  # noqa: E731
+    call(states[0])
+    torch.cuda.synchronize()
+    for s in states:
+        with torch.cuda.graph(s["graph"], stream=s["stream"]):
+            s["o"], s["lse"] = call(s)
+    new = [900, 50, 400]
+    for s in states:
+        s["lens"].copy_(_i32(new))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s in states:
+            with torch.cuda.stream(s["stream"]):
+                s["graph"].replay()
+    torch.cuda.synchronize()
+    assert xattn.xattn_check_device_status() == 0
+    for s in states:
+        check_tree(s["o"], s["lse"], tree_reference(s["q"], s["k"], s["v"], s["table"], new, s["words"], BIG, 0,
+                                                    hd ** -0.5), "graph")
+
+
+def test_explicit_streams_by_object_and_handle():
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nh, nkv, hd, page, lens = 2, 4, 4, 2, 64, 16, [100, 60]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=2, device="cuda")
+    q, tb, ln = _q(B, n, nh, hd, 1), _i32(table), _i32(lens)
+    ref, rl = xattn.attention_tree_decode(q, k, v, tb, ln)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        o, lse = xattn.attention_tree_decode(q, k, v, tb, ln, stream=stream)
+        side.synchronize()
+        assert torch.equal(o, ref) and torch.equal(lse, rl)
