@@ -355,8 +355,8 @@ cudaError_t launch_dq_hd(const CUtensorMap &mq, const CUtensorMap &mk, const CUt
                          int B, int S, int nh, int nkv, float scale, int window, int sinks, int *status,
                          uint64_t timeout_ns, cudaStream_t stream) {
   using L = DqLayout<HD>;
-  cudaError_t err = cudaFuncSetAttribute(attn_bwd_dq_kernel<HD, kWin>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t err = allow_smem(attn_bwd_dq_kernel<HD, kWin>, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
   const int num_m = (S + kTileRows - 1) / kTileRows;
   const unsigned grid = static_cast<unsigned>(B) * nh * num_m;

@@ -1142,7 +1142,8 @@ cudaError_t launch_main_hd(const CUtensorMap &mq, const CUtensorMap &mk, const C
                            const WinArgs &win = WinArgs{}) {
   using L = BwdLayout<HD, kFusedDq>;
   auto kernel = attn_bwd_main_kernel<HD, kFusedDq, kResident, kDsTmem, kWin>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t err = allow_smem(kernel, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM, or one per unit (resident dQ: per head) when there are
   // fewer.

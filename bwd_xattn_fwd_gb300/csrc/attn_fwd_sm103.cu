@@ -655,8 +655,8 @@ cudaError_t launch_fwd_sign(const CUtensorMap &mq, const CUtensorMap &mk, const 
                             __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, float scale,
                             int window, int sinks, int *status, uint64_t timeout_ns, cudaStream_t stream) {
   using L = FwdLayout<HD, kRing>;
-  cudaError_t err = cudaFuncSetAttribute(attn_fwd_kernel<HD, kNegScale, kRing, kWin>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t err = allow_smem(attn_fwd_kernel<HD, kNegScale, kRing, kWin>, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
   // Persistent CTAs: one per SM, or one per unit when there are fewer units.
   int dev = 0, sms = 0;

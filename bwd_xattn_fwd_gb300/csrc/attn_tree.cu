@@ -9,8 +9,13 @@
 //
 // GB300 mapping. The cache is read once, so HBM bounds the operation: a visible position is
 // 4 hd bytes of K and V against 4 hd n group flops. The n x group query rows that share a kv
-// head are packed into tiles of 128 rows (row = token * group + head of the group), one TMEM
-// lane each, and the cache streams past them in 128-position tiles.
+// head are packed into tiles (row = token * group + head of the group), one TMEM lane each,
+// and the cache streams past them in 128-position tiles.
+//   * Few rows: a product has 128 rows whether they are used or not, so up to 32 (64) rows are
+//     put in the tile kSplit = 4 (2) times. Copy c of a row takes the columns [c, c + 1) 128 /
+//     kSplit of every tile, with its own maximum, sum and O (its P is zero elsewhere, written
+//     once), and the copies are merged at the end: the softmax of a tile, which is what a CTA
+//     waits for, takes a quarter (half) of the time and all four warps.
 //   * Work: a unit is (sequence, kv head, row tile) with the position tiles it can see; the
 //     units' tiles in order form one line that is cut into equal runs, one per resident CTA,
 //     so ragged lengths and windows balance without a plan from the host (the lengths are
@@ -22,6 +27,8 @@
 //     outside the pool: the TMA unit writes zeros and reads nothing.
 // Warps: 0 TMA producer; 1 TMEM owner and MMA issuer; 2-5 softmax, one query row a thread.
 // TMEM: S [0,128) fp32 | P [128,192) bf16 pairs | O [192, 192 + hd).
+#include <type_traits>
+
 #include "sm103_ptx.cuh"
 #include "xattn_internal.h"
 
@@ -46,10 +53,17 @@ struct TreeLayout {
   static constexpr uint32_t kK = kTileBytes;
   static constexpr uint32_t kV = kK + kSlots * kTileBytes;
   static constexpr uint32_t kBars = kV + kSlots * kTileBytes;
-  static constexpr int kNumBars = 4 * kSlots + 5;
+  static constexpr int kNumBars = 4 * kSlots + 6;
   static constexpr uint32_t kPages = kBars + 8 * kNumBars;      // per V slot: boxes that hold a page
   static constexpr uint32_t kMisc = (kPages + 4 * kSlots + 15) / 16 * 16;
-  static constexpr uint32_t kUsed = kMisc + 32;
+  // At a piece's end: kPartCols columns of O of up to 96 lanes (the copies beyond the first),
+  // and every lane's (max, sum); in the Q tile, free by then, or at hd 32, where it is too
+  // small, behind the rest.
+  static constexpr int kPartCols = HD == 128 ? 64 : 32;
+  static constexpr uint32_t kPart = HD == 32 ? (kMisc + 32 + 127) / 128 * 128 : kQ;
+  static constexpr uint32_t kStat = kPart + 96 * kPartCols * 4;
+  static constexpr uint32_t kUsed = HD == 32 ? kStat + kTileRows * 8 : kMisc + 32;
+  static_assert(HD == 32 || kStat + kTileRows * 8 <= kK, "the hand-over fits the Q tile");
   // The tiles start at the next multiple of 1024; the base is at least 256-byte aligned.
   static constexpr uint32_t kDynBytes = kUsed + 768 > 80 * 1024 ? kUsed + 768 : 80 * 1024;
   static constexpr uint32_t kTmemCols = HD == 128 ? 512 : 256;
@@ -61,6 +75,19 @@ struct TreeLayout {
 __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
   const bool ok = mbar_wait(bar, parity, ctl);
   return __all_sync(0xffffffffu, ok);
+}
+
+// The line that holds p into L2. While the rings keep HBM busy a load that misses L2 takes
+// about 4 us; what the next piece will read is asked for at the start of the current one.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// One arrival for the whole warp, after what every lane has done (128 arrivals of single
+// lanes take some 500 cycles).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 // Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
@@ -90,6 +117,23 @@ __device__ __forceinline__ Sight sight_of(const TreeArgs &a, int b) {
   return s;
 }
 
+// a / b for 0 <= a, 0 < b, in 32 bits where that will do.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// The line of `length` tiles in `runs` runs: the first length % runs have one tile more.
+__device__ __forceinline__ long long run_start(long long length, long long runs, long long c) {
+  const long long each = quotient(length, runs);
+  return c * each + min(c, length - each * runs);
+}
+__device__ __forceinline__ long long run_of(long long length, long long runs, long long pos) {
+  const long long each = quotient(length, runs), more = length - each * runs;
+  const long long head = more * (each + 1);
+  return pos < head ? quotient(pos, each + 1) : more + quotient(pos - head, each);
+}
+
 // A run of the line of tiles, walked piece by piece; warp-uniform, every warp of every role
 // walks the same pieces. All counts in 64 bits.
 struct Walk {
@@ -99,35 +143,45 @@ struct Walk {
   Sight s;
 };
 
-// Tiles of all sequences, and (for the warp's target tile) the sequence that holds it.
-__device__ __forceinline__ long long line_length(const TreeArgs &a, int units, int lane) {
-  long long t = 0;
-  for (int b = lane; b < a.B; b += 32) t += sight_of(a, b).count;
+// Tiles of all sequences and units: the line's length. And the sequence that holds tile
+// `target` of it, with the line's tiles before that sequence. counts: tiles of the lane's
+// first four sequences (lane, lane + 32, ..), loaded together.
+__device__ __forceinline__ long long line_length(const TreeArgs &a, int units, int lane, int *counts) {
+  // A sequence has at most 2^23 tiles (2^30 positions): a lane's four, and 32 lanes of one,
+  // fit 32 bits.
+  int four = 0;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  return t * units;
+  for (int k = 0; k < 4; ++k) {
+    counts[k] = 32 * k + lane < a.B ? sight_of(a, 32 * k + lane).count : 0;
+    four += counts[k];
+  }
+  long long total = __reduce_add_sync(0xffffffffu, four);
+  for (int b0 = 128; b0 < a.B; b0 += 32)
+    total += __reduce_add_sync(0xffffffffu, b0 + lane < a.B ? sight_of(a, b0 + lane).count : 0);
+  return total * units;
 }
 
-__device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane, long long target, int *b_out,
-                                          long long *first_out) {
+__device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane, const int *counts, long long target,
+                                          int *b_out, long long *first_out) {
   long long base = 0;
+  int next[4] = {counts[0], counts[1], counts[2], counts[3]};
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    const long long mine = b < a.B ? static_cast<long long>(sight_of(a, b).count) * units : 0;
-    long long incl = mine;
+    const int mine = b0 < 128 ? next[0] : (b0 + lane < a.B ? sight_of(a, b0 + lane).count : 0);
+    next[0] = next[1], next[1] = next[2], next[2] = next[3];
+    int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, off);
+      const int up = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += up;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, b < a.B && base + incl > target);
+    const unsigned past = __ballot_sync(0xffffffffu, base + static_cast<long long>(incl) * units > target);
     if (past) {
       const int l = __ffs(past) - 1;
       *b_out = b0 + l;
-      *first_out = base + __shfl_sync(0xffffffffu, incl - mine, l);
+      *first_out = base + static_cast<long long>(__shfl_sync(0xffffffffu, incl - mine, l)) * units;
       return;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    base += static_cast<long long>(__shfl_sync(0xffffffffu, incl, 31)) * units;
   }
   *b_out = a.B;
   *first_out = base;
@@ -141,8 +195,8 @@ __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units
     w.s = sight_of(a, ++w.b);
     at = 0;
   }
-  w.unit = static_cast<int>(at / w.s.count);
-  w.e0 = static_cast<int>(at % w.s.count);
+  w.unit = static_cast<int>(quotient(at, w.s.count));
+  w.e0 = static_cast<int>(at - static_cast<long long>(w.unit) * w.s.count);
   w.e1 = static_cast<int>(min(static_cast<long long>(w.s.count), w.e0 + (w.stop - w.pos)));
   w.pos += w.e1 - w.e0;
   return true;
@@ -150,7 +204,7 @@ __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units
 
 // Record of a cut unit's piece: CTA c's piece that starts inside a unit is record 2c, the one
 // that starts it record 2c + 1. Layout: [records][rows][hd] O, then [records][rows] (max, sum).
-template <int HD>
+template <int HD, int kSplit>
 __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
     tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = TreeLayout<HD>;
@@ -167,6 +221,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
   auto v_empty = [&](int s) { return bar(3 * L::kSlots + s); };
   const uint32_t s_full = bar(4 * L::kSlots), s_free = bar(4 * L::kSlots + 1), p_full = bar(4 * L::kSlots + 2);
   const uint32_t o_done = bar(4 * L::kSlots + 3), q_full = bar(4 * L::kSlots + 4);
+  const uint32_t meet = bar(4 * L::kSlots + 5);              // the softmax warps among themselves
+  constexpr int kRows = kTileRows / kSplit, kCols = kTileRows / kSplit;
   volatile uint32_t *pages = reinterpret_cast<volatile uint32_t *>(smem + L::kPages);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
@@ -177,10 +233,11 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
     *abort_flag = 0;
     for (int s = 0; s < 4 * L::kSlots; ++s) mbar_init(bar(s), 1);
     mbar_init(s_full, 1);
-    mbar_init(s_free, 128);
-    mbar_init(p_full, 128);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
     mbar_init(o_done, 1);
-    mbar_init(q_full, 128);
+    mbar_init(q_full, 4);
+    mbar_init(meet, 4);
     fence_mbar_init();
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
@@ -199,60 +256,90 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
 
   // This CTA's run of the line.
   const int group = a.nh / a.nkv, rows_all = a.n * group;
-  const int row_tiles = (rows_all + kTileRows - 1) / kTileRows;
+  const int row_tiles = (rows_all + kRows - 1) / kRows;
   const int units = a.nkv * row_tiles;
-  const long long length = line_length(a, units, lane);
+  int counts[4];
+  const long long length = line_length(a, units, lane, counts);
   const long long runs = min(static_cast<long long>(gridDim.x), length);
   Walk walk;
   walk.pos = walk.stop = 0;
   if (blockIdx.x < runs) {
-    walk.pos = blockIdx.x * length / runs;
-    walk.stop = (blockIdx.x + 1) * length / runs;
-    line_find(a, units, lane, walk.pos, &walk.b, &walk.first);
+    walk.pos = run_start(length, runs, blockIdx.x);
+    walk.stop = run_start(length, runs, blockIdx.x + 1);
+    line_find(a, units, lane, counts, walk.pos, &walk.b, &walk.first);
     walk.s = sight_of(a, walk.b);
   }
 
   if (warp == 0) {
-    // ---------------- TMA producer: lane l loads box l of each tile ----------------
+    // ---------------- TMA producer: lane l finds box l of each tile ----------------
     const int box_rows = min(a.page_size, kTileRows), boxes = kTileRows / box_rows;
     int R = 0, issued_k = 0, issued_v = 0;
-    bool ok = true;
-    while (ok && walk_piece(walk, a, units)) {
-      const int kvh = walk.unit / row_tiles;
-      const int *table = a.page_table + static_cast<size_t>(walk.b) * a.max_pages;
+    bool ok = true, have = walk_piece(walk, a, units);
+    // The table entries of a piece, 8 to a 32-byte sector.
+    auto prefetch_table = [&](const Walk &w) {
+      const int *table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+      const int t0 = w.e0 < w.s.heads ? w.e0 : w.e0 - w.s.heads + w.s.lo;
+      const int t1 = w.e1 - 1 < w.s.heads ? w.e1 - 1 : w.e1 - 1 - w.s.heads + w.s.lo;
+      const int last = min(t1 * kTileRows + kTileRows - 1, w.s.end - 1) / a.page_size;
+      for (int at = t0 * kTileRows / a.page_size + 8 * lane; at <= last + 7; at += 256) prefetch_l2(table + min(at, last));
+    };
+    // A tile's boxes: their pages come to every lane first, then one elected lane issues the
+    // copies back to back from uniform registers (box by box, with a shuffle or a branch per
+    // box, took 75 cycles each: at 16-row pages as long as the bytes themselves take). Only
+    // pages of more than 128 rows have a row to start at, and those are one box.
+    auto load_boxes = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int kvh, int row, int page) {
+      int pg[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) pg[x] = __shfl_sync(0xffffffffu, page, x);
+      const int rw = __shfl_sync(0xffffffffu, row, 0);
+      const uint32_t box_bytes = box_rows * L::kAtomBytes;
+      if (elect_one()) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (x < boxes) {
+#pragma unroll
+            for (int c = 0; c < L::kSubTiles; ++c)
+              tma_load_4d(dst + c * L::kSubBytes + x * box_bytes, map, full, 64 * c, kvh, x == 0 ? rw : 0, pg[x]);
+          }
+      }
+      __syncwarp();
+    };
+    if (have) prefetch_table(walk);
+    while (ok && have) {
+      const Walk here = walk;
+      have = walk_piece(walk, a, units);
+      if (have) prefetch_table(walk);
+      const int kvh = here.unit / row_tiles;
+      const int *table = a.page_table + static_cast<size_t>(here.b) * a.max_pages;
+      // This lane's box of entry e: its table entry (-1 when no row can see the box) and its
+      // row in the page. Read one tile ahead, so that no tile waits for the table.
+      auto box_of = [&](int e, int *row) -> int {
+        const int tile = e < here.s.heads ? e : e - here.s.heads + here.s.lo;
+        const int p0 = tile * kTileRows + lane * box_rows, at = p0 / a.page_size;
+        *row = p0 - at * a.page_size;
+        if (lane >= boxes || e >= here.e1 || p0 >= here.s.end || (p0 + box_rows <= here.s.far && p0 >= a.sinks)) return -1;
+        return __ldg(table + at);                               // p0 < end <= max_pages * page_size
+      };
+      int row_next = 0, id_next = box_of(here.e0, &row_next);
 #pragma unroll 1
-      for (int e = walk.e0; e < walk.e1; ++e, ++R) {
-        const int tile = e < walk.s.heads ? e : e - walk.s.heads + walk.s.lo;
-        // The box's page, or num_pages (outside the pool) when it holds nothing to see.
-        const int p0 = tile * kTileRows + lane * box_rows;
-        int page = a.num_pages, row = 0;
-        if (lane < boxes && p0 < walk.s.end && (p0 + box_rows > walk.s.far || p0 < a.sinks)) {
-          const int id = table[p0 / a.page_size];               // p0 < end <= max_pages * page_size
-          if (id >= 0 && id < a.num_pages) page = id, row = p0 % a.page_size;
-        }
+      for (int e = here.e0; e < here.e1; ++e, ++R) {
+        // Outside the pool (num_pages) there is nothing to read: the box is zeros.
+        const int row = row_next, page = id_next >= 0 && id_next < a.num_pages ? id_next : a.num_pages;
+        id_next = box_of(e + 1, &row_next);
         const unsigned held = __ballot_sync(0xffffffffu, page != a.num_pages);
         const int s = R % L::kSlots;
         const uint32_t ph = static_cast<uint32_t>((R / L::kSlots) & 1) ^ 1u;
         if (!tree_wait(k_empty(s), ph, ctl)) { ok = false; break; }
-        if (lane == 0) mbar_expect_tx(k_full(s), L::kTileBytes);
-        __syncwarp();
-        if (lane < boxes)
-#pragma unroll
-          for (int c = 0; c < L::kSubTiles; ++c)
-            tma_load_4d(sK + s * L::kTileBytes + c * L::kSubBytes + lane * box_rows * L::kAtomBytes, &mk, k_full(s),
-                        64 * c, kvh, row, page);
+        mbar_expect_tx_elect(k_full(s), L::kTileBytes);
+        load_boxes(sK + s * L::kTileBytes, &mk, k_full(s), kvh, row, page);
         issued_k = R + 1;
         if (!tree_wait(v_empty(s), ph, ctl)) { ok = false; break; }
-        if (lane == 0) {
+        if (elect_one()) {
           pages[s] = held;                 // read by the softmax warps before P V frees the slot
           mbar_expect_tx(v_full(s), L::kTileBytes);
         }
         __syncwarp();
-        if (lane < boxes)
-#pragma unroll
-          for (int c = 0; c < L::kSubTiles; ++c)
-            tma_load_4d(sV + s * L::kTileBytes + c * L::kSubBytes + lane * box_rows * L::kAtomBytes, &mv, v_full(s),
-                        64 * c, kvh, row, page);
+        load_boxes(sV + s * L::kTileBytes, &mv, v_full(s), kvh, row, page);
         issued_v = R + 1;
       }
     }
@@ -321,131 +408,139 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
     if (scored > 0) mbar_drain(s_full, (scored - 1) & 1, ctl);
     if (R > 0) mbar_drain(o_done, (R - 1) & 1, ctl);
   } else {
-    // ---------------- softmax: thread = query row of the tile ----------------
-    const int quarter = warp & 3, row = quarter * 32 + lane;
+    // ---------------- softmax: thread = one copy of a query row ----------------
+    const int quarter = warp & 3, lane_row = quarter * 32 + lane;     // TMEM lane
+    const int row = lane_row % kRows, copy = lane_row / kRows;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tSx = tS + lane_off, tPx = tP + lane_off, tOx = tO + lane_off;
+    const uint32_t tSx = tS + lane_off + copy * kCols, tPx = tP + lane_off + copy * (kCols / 2), tOx = tO + lane_off;
     const int box_rows = min(a.page_size, kTileRows);
     const unsigned all_boxes = box_rows == kTileRows ? 1u : (1u << (kTileRows / box_rows)) - 1u;
-    int R = 0;
+    float2 *stat = reinterpret_cast<float2 *>(smem + L::kStat);
+    if constexpr (kSplit > 1) {
+      // P of the columns that the other copies take.
+      uint32_t zero[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) zero[i] = 0u;
+      tmem_st_x32(tP + lane_off, zero);
+      tmem_st_x32(tP + lane_off + 32, zero);
+      tmem_wait_st();
+    }
+    int R = 0, meets = 0;
     bool ok = true;
-    while (ok && walk_piece(walk, a, units)) {
+    // All softmax warps have come this far (bounded, like every wait).
+    auto meet_all = [&]() -> bool {
+      warp_arrive(meet, lane);
+      return tree_wait(meet, meets++ & 1, ctl);
+    };
+    // A piece's query row and word: into L2 while the piece before it runs, into registers
+    // before that piece's result is written, and put in place after it.
+    uint4 xq[HD / 8];
+    unsigned long long word = 0;
+    auto load_rows = [&](bool ahead) {
+      const int row0 = (walk.unit % row_tiles) * kRows, rho = row0 + row;
+      const bool mine = rho < rows_all;
+      const int token = mine ? rho / group : 0;
+      const size_t at = static_cast<size_t>(walk.b) * a.n + token;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          a.q + (at * a.nh + static_cast<size_t>(walk.unit / row_tiles) * group + (mine ? rho - token * group : 0)) * HD);
+      if (ahead) {
+        if (mine && copy == 0) {
+#pragma unroll
+          for (int c = 0; c < HD / 8; c += 8) prefetch_l2(src + c);
+          if (a.tree) prefetch_l2(a.tree + at);
+        }
+        return;
+      }
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c) xq[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      // Bits past the last new token mean nothing.
+      word = !mine ? 0 : (a.tree ? __ldg(a.tree + at) : (2ull << token) - 1) & (a.n == 64 ? ~0ull : (1ull << a.n) - 1);
+    };
+    bool have = walk_piece(walk, a, units);
+    if (have) load_rows(false);
+    else if (warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
+    while (ok && have) {
       const Sight s = walk.s;
-      const int kvh = walk.unit / row_tiles, row0 = (walk.unit % row_tiles) * kTileRows;
-      const int rows = min(rows_all - row0, kTileRows);
-      const bool live = quarter * 32 < rows;                 // the warp has a row
-      const int rho = row0 + row, token = rho / group;
+      const int b = walk.b, e0 = walk.e0, e1 = walk.e1;
+      const int kvh = walk.unit / row_tiles, row0 = (walk.unit % row_tiles) * kRows;
+      const int unit = walk.unit;
+      // From here on `walk` is the next piece.
+      have = walk_piece(walk, a, units);
+      if (have) load_rows(true);
+      // A run that ends inside the unit it started last says so to the combine.
+      if (!have && warp == 2 && lane == 0) {
+        const long long start = walk.stop - (e1 - e0);
+        const bool cut = e0 == 0 && e1 < s.count;
+        a.plan[blockIdx.x] = make_int4(b, unit, cut ? static_cast<int>(run_of(length, runs, start + s.count - 1)) : 0, cut);
+      }
+      const int rows = min(rows_all - row0, kRows);
+      const bool live = kSplit > 1 || quarter * 32 < rows;    // the warp has a row
       const bool mine = row < rows;
-      const size_t out = (static_cast<size_t>(walk.b) * a.n + token) * a.nh + static_cast<size_t>(kvh) * group +
-                         rho % group;                         // row of q, o and lse
-      // The row's query into the Q tile, swizzled as TMA would (dead rows of a live warp: 0).
+      // The rows into the Q tile, swizzled as TMA would (0 past the last).
       if (live) {
         constexpr int kChunks = static_cast<int>(L::kAtomBytes / 16);
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (mine ? out : 0) * HD);
 #pragma unroll
         for (int c = 0; c < HD / 8; ++c) {
-          const uint4 x = mine ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-          const int ch = c % kChunks, sw = L::kAtomBytes == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
-          *reinterpret_cast<uint4 *>(smem + L::kQ + (c / kChunks) * L::kSubBytes + row * L::kAtomBytes + (sw << 4)) = x;
+          const int ch = c % kChunks, sw = L::kAtomBytes == 128 ? (ch ^ (lane_row & 7)) : (ch ^ ((lane_row >> 1) & 3));
+          *reinterpret_cast<uint4 *>(smem + L::kQ + (c / kChunks) * L::kSubBytes + lane_row * L::kAtomBytes +
+                                     (sw << 4)) = xq[c];
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(q_full);
-      // The row's ancestors, its position, and how far its window reaches.
-      unsigned long long word = 0;
-      if (mine) {
-        const unsigned long long all = a.n == 64 ? ~0ull : (1ull << a.n) - 1;
-        word = a.tree ? a.tree[static_cast<size_t>(walk.b) * a.n + token] & all : (2ull << token) - 1;
-      }
-      const int pos = s.ctx + max(__popcll(word) - 1, 0);
-      const int far = pos - a.window + 1;
+      warp_arrive(q_full, lane);
+      // The row's ancestors and how far its window reaches.
+      const unsigned long long seen = word;
+      const int far = s.ctx + max(__popcll(seen) - 1, 0) - a.window + 1;
       float mrow = -INFINITY, lrow = 0.f;
-#pragma unroll 1
-      for (int e = walk.e0; e < walk.e1; ++e, ++R) {
-        const int tile = e < s.heads ? e : e - s.heads + s.lo, t0 = tile * kTileRows;
-        const int slot = R % L::kSlots;
-        // V has landed (so pages[slot] is there to read; its slot is not loaded again before
-        // this tile's P V), and the scores.
-        if (!tree_wait(v_full(slot), (R / L::kSlots) & 1, ctl) || !tree_wait(s_full, R & 1, ctl)) { ok = false; break; }
-        tc_fence_after();
-        const unsigned held = pages[slot];
-        // Positions that some row does not see: new ones, those behind a window, missing pages.
-        const bool edge = t0 + kTileRows > s.ctx || held != all_boxes ||
-                          (t0 <= s.end - 1 - a.window && t0 + kTileRows > a.sinks);
-        uint32_t vis[4];
-        if (edge) {
+      // One tile: this copy's kCols columns. The masked form is compiled apart, so that the
+      // tiles every row sees whole carry no mask. vis: a word per 32 columns.
+      auto step = [&](auto masked, const uint32_t *vis, bool first) -> bool {
+        float x[kCols];
+        uint32_t *xr = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int base = t0 + 32 * w, off = base - s.ctx;
-            uint32_t m = word_range(0, s.ctx - 1 - base) & (word_range(far - base, 31) | word_range(0, a.sinks - 1 - base));
-            if (off >= 0) {
-              if (off < 64) m |= static_cast<uint32_t>(word >> off);
-            } else if (off > -32) {
-              m |= static_cast<uint32_t>(word << -off);
-            }
-            uint32_t there = 0;
-            if (box_rows >= 32)
-              there = (held >> (32 * w / box_rows)) & 1u ? 0xffffffffu : 0u;
-            else
-              there = ((held >> (2 * w)) & 1u ? 0x0000ffffu : 0u) | ((held >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
-            vis[w] = m & there;
-          }
-          // V rows that no row sees may hold anything: they are zeroed before P V, in which
-          // their P is 0 (0 x NaN would not be). Missing pages were loaded as zeros.
-          const int p = t0 + row;
-          if (p >= s.end || (p < s.far && p >= a.sinks)) {
-#pragma unroll
-            for (int c = 0; c < L::kSubTiles; ++c)
-#pragma unroll
-              for (uint32_t x = 0; x < L::kAtomBytes; x += 16)
-                *reinterpret_cast<uint4 *>(smem + L::kV + slot * L::kTileBytes + c * L::kSubBytes +
-                                           row * L::kAtomBytes + x) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        if (!live) {
-          mbar_arrive(s_free);
-          // P of the previous tile has been read before anyone moves on.
-          if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
-          mbar_arrive(p_full);
-          continue;
-        }
-        uint32_t r[128];
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld_x32(tSx + c, r + c);
+        for (int c = 0; c < kCols; c += 32) tmem_ld_x32(tSx + c, xr + c);
         tmem_wait_ld();
-        reg_fence<128>(r);
+        reg_fence<kCols>(xr);
         tc_fence_before();
-        mbar_arrive(s_free);
-        // Scaled, masked scores in place (the log2 domain), their maximum, P and its sum.
+        warp_arrive(s_free, lane);
+        // Scaled scores (log2 domain) and their maximum.
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) {
-          float x = __uint_as_float(r[c]) * a.scale_log2;
-          if (edge && ((vis[c >> 5] >> (c & 31)) & 1u) == 0u) x = -INFINITY;
-          r[c] = __float_as_uint(x);
-          mx[c & 3] = fmaxf(mx[c & 3], x);
+        for (int c = 0; c < kCols; c += 2) {
+          fmul2(x[c], x[c + 1], x[c], x[c + 1], a.scale_log2, a.scale_log2);
+          if constexpr (decltype(masked)::value) {
+            if (((vis[c >> 5] >> (c & 31)) & 1u) == 0u) x[c] = -INFINITY;
+            if (((vis[c >> 5] >> ((c + 1) & 31)) & 1u) == 0u) x[c + 1] = -INFINITY;
+          }
+          float &m = mx[(c >> 1) & 3];
+          m = fmax3(m, x[c], x[c + 1]);
         }
-        const float mnew = fmaxf(mrow, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        const float mnew = fmax3(fmaxf(mrow, mx[0]), mx[1], fmaxf(mx[2], mx[3]));
         // O is rescaled only when some row's maximum grew by more than 2^8.
         const bool rescale = __any_sync(0xffffffffu, mnew > mrow + 8.0f);
         const float m_use = rescale ? mnew : mrow;
-        const float alpha = (rescale && mnew > mrow) ? ex2_approx(mrow - mnew) : 1.f;
-        const float base = m_use == -INFINITY ? 0.f : m_use;       // a row that has seen nothing yet
+        float alpha = 1.f;
+        if (rescale && mnew > mrow) alpha = ex2_approx(mrow - mnew);
+        const float base = m_use == -INFINITY ? 0.f : -m_use;         // a row that has seen nothing yet
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const float p0 = ex2_approx(__uint_as_float(r[2 * c]) - base);
-          const float p1 = ex2_approx(__uint_as_float(r[2 * c + 1]) - base);
-          ps[(c & 1) * 2] += p0;
-          ps[(c & 1) * 2 + 1] += p1;
-          r[c] = pack_bf16x2(p0, p1);
+        for (int c = 0; c < kCols; c += 2) {
+          float p0, p1;
+          fadd2(p0, p1, x[c], x[c + 1], base, base);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          const int e = (c >> 1) & 1;
+          fadd2(ps[2 * e], ps[2 * e + 1], ps[2 * e], ps[2 * e + 1], p0, p1);
+          pk[c / 2] = pack_bf16x2(p0, p1);
         }
-        if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
+        if (!tree_wait(o_done, (R - 1) & 1, ctl)) return false;
         tc_fence_after();
-        tmem_st_x32(tPx, r);
-        tmem_st_x32(tPx + 32, r + 32);
-        if (rescale && e > walk.e0) {
+        if constexpr (kCols == 32) tmem_st_x16(tPx, pk);
+        if constexpr (kCols >= 64)
+#pragma unroll
+          for (int c = 0; c < kCols / 2; c += 32) tmem_st_x32(tPx + c, pk + c);
+        if (rescale && !first) {
 #pragma unroll
           for (int c = 0; c < HD; c += 32) {
             uint32_t ov[32];
@@ -461,41 +556,156 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
         mrow = m_use;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full);
+        warp_arrive(p_full, lane);
+        return true;
+      };
+#pragma unroll 1
+      for (int e = e0; e < e1; ++e, ++R) {
+        const int tile = e < s.heads ? e : e - s.heads + s.lo, t0 = tile * kTileRows;
+        const int slot = R % L::kSlots;
+        // V has landed (so pages[slot] is there to read; its slot is not loaded again before
+        // this tile's P V), and the scores.
+        if (!tree_wait(v_full(slot), (R / L::kSlots) & 1, ctl) || !tree_wait(s_full, R & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        const unsigned held = pages[slot];
+        // Positions that some row does not see: new ones, those behind a window, missing pages.
+        const bool edge = t0 + kTileRows > s.ctx || held != all_boxes ||
+                          (t0 <= s.end - 1 - a.window && t0 + kTileRows > a.sinks);
+        uint32_t vis[kCols / 32];
+        if (edge) {
+#pragma unroll
+          for (int w = 0; w < kCols / 32; ++w) {
+            const int col = copy * kCols + 32 * w, base = t0 + col, off = base - s.ctx;
+            uint32_t m = word_range(0, s.ctx - 1 - base) & (word_range(far - base, 31) | word_range(0, a.sinks - 1 - base));
+            if (off >= 0) {
+              if (off < 64) m |= static_cast<uint32_t>(seen >> off);
+            } else if (off > -32) {
+              m |= static_cast<uint32_t>(seen << -off);
+            }
+            uint32_t there = 0;
+            if (box_rows >= 32)
+              there = (held >> (col / box_rows)) & 1u ? 0xffffffffu : 0u;
+            else
+              there = ((held >> (col / 16)) & 1u ? 0x0000ffffu : 0u) | ((held >> (col / 16 + 1)) & 1u ? 0xffff0000u : 0u);
+            vis[w] = m & there;
+          }
+          // V rows that no row sees may hold anything: they are zeroed before P V, in which
+          // their P is 0 (0 x NaN would not be). Missing pages were loaded as zeros.
+          const int p = t0 + lane_row;
+          if (p >= s.end || (p < s.far && p >= a.sinks)) {
+#pragma unroll
+            for (int c = 0; c < L::kSubTiles; ++c)
+#pragma unroll
+              for (uint32_t x = 0; x < L::kAtomBytes; x += 16)
+                *reinterpret_cast<uint4 *>(smem + L::kV + slot * L::kTileBytes + c * L::kSubBytes +
+                                           lane_row * L::kAtomBytes + x) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!live) {
+          warp_arrive(s_free, lane);
+          // P of the previous tile has been read before anyone moves on.
+          if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
+          warp_arrive(p_full, lane);
+          continue;
+        }
+        if (!(edge ? step(std::true_type{}, vis, e == e0) : step(std::false_type{}, vis, e == e0))) {
+          ok = false;
+          break;
+        }
       }
       if (!ok) break;
-      // The piece's result: O and the LSE of a whole unit, else a record.
+      if (have) load_rows(false);
+      // The piece's result: O and the LSE of a whole unit, else a record (its O not divided by
+      // its sum).
       if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
-      if (!live) continue;
       tc_fence_after();
-      const bool whole = walk.e0 == 0 && walk.e1 == s.count;
-      const size_t rec = 2 * static_cast<size_t>(blockIdx.x) + (walk.e0 == 0 ? 1 : 0);
-      const float inv = lrow > 0.f ? 1.f / lrow : 0.f;
-      float *ws_o = a.ws_o + (rec * a.rec_rows + row) * HD;
+      const bool whole = e0 == 0 && e1 == s.count;
+      const size_t rec = (2 * static_cast<size_t>(blockIdx.x) + (e0 == 0 ? 1 : 0)) * a.rec_rows + row;
+      XATTN_DCHECK(rec / a.rec_rows < 2 * static_cast<size_t>(gridDim.x) && rows <= a.rec_rows, a.status);
+      const int rho = row0 + row;
+      const size_t out = (static_cast<size_t>(b) * a.n + rho / group) * a.nh + static_cast<size_t>(kvh) * group + rho % group;
+      // Copies beyond the first hand their O (kPart columns at a time) and statistics to the
+      // first through shared memory, which weighs and adds them in order.
+      constexpr int kPart = kSplit == 1 ? 32 : L::kPartCols, kPieces = kPart / 4;
+      float4 *part = reinterpret_cast<float4 *>(smem + L::kPart);
+      auto piece = [](int l, int i) { return l * kPieces + (i ^ (l & 7)); };   // against bank conflicts
+      float weight[kSplit], M = mrow, sum = lrow;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += kPart) {
+        uint32_t ov[kPart];
+        if (live)
 #pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t ov[32];
-        tmem_ld_x32(tOx + c, ov);
+          for (int x = 0; x < kPart; x += 32) tmem_ld_x32(tOx + c + x, ov + x);
         tmem_wait_ld();
-        reg_fence<32>(ov);
-        if (mine && whole) {
-          // A row that sees nothing gives 0, whatever its O columns hold.
-          uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * HD + c);
-          auto val = [&](int i) { return lrow > 0.f ? __uint_as_float(ov[i]) * inv : 0.f; };
+        reg_fence<kPart>(ov);
+        if constexpr (kSplit > 1) {
+          if (copy > 0) {
+            if (c == 0) stat[lane_row] = make_float2(mrow, lrow);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pack_bf16x2(val(8 * i), val(8 * i + 1)), pack_bf16x2(val(8 * i + 2), val(8 * i + 3)),
-                                pack_bf16x2(val(8 * i + 4), val(8 * i + 5)), pack_bf16x2(val(8 * i + 6), val(8 * i + 7)));
-        } else if (mine) {
-          XATTN_DCHECK(rec < 2 * static_cast<size_t>(gridDim.x) && row < a.rec_rows, a.status);
-          uint4 *dst = reinterpret_cast<uint4 *>(ws_o + c);
+            for (int i = 0; i < kPieces; ++i)
+              part[piece(lane_row - kRows, i)] =
+                  make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                              __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+          }
+          if (!meet_all()) { ok = false; break; }
+          if (copy == 0) {
+            if (c == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+              for (int k = 1; k < kSplit; ++k) M = fmaxf(M, stat[k * kRows + row].x);
+              weight[0] = lrow > 0.f ? ex2_approx(mrow - M) : 0.f;
+              sum = lrow * weight[0];
+#pragma unroll
+              for (int k = 1; k < kSplit; ++k) {
+                const float2 ml = stat[k * kRows + row];
+                weight[k] = ml.y > 0.f ? ex2_approx(ml.x - M) : 0.f;
+                sum = fmaf(ml.y, weight[k], sum);
+              }
+            }
+            // A copy that saw nothing counts 0, whatever its O holds.
+#pragma unroll
+            for (int i = 0; i < kPart; ++i)
+              ov[i] = weight[0] > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * weight[0]) : 0u;
+#pragma unroll
+            for (int k = 1; k < kSplit; ++k)
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) {
+                const float4 z = part[piece((k - 1) * kRows + row, i)];
+                if (weight[k] > 0.f) {
+                  ov[4 * i] = __float_as_uint(fmaf(z.x, weight[k], __uint_as_float(ov[4 * i])));
+                  ov[4 * i + 1] = __float_as_uint(fmaf(z.y, weight[k], __uint_as_float(ov[4 * i + 1])));
+                  ov[4 * i + 2] = __float_as_uint(fmaf(z.z, weight[k], __uint_as_float(ov[4 * i + 2])));
+                  ov[4 * i + 3] = __float_as_uint(fmaf(z.w, weight[k], __uint_as_float(ov[4 * i + 3])));
+                }
+              }
+          }
+        }
+        if (mine && copy == 0) {
+          if (whole) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            auto val = [&](int i) { return sum > 0.f ? __uint_as_float(ov[i]) * inv : 0.f; };
+            uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * HD + c);
+#pragma unroll
+            for (int i = 0; i < kPart / 8; ++i)
+              dst[i] = make_uint4(pack_bf16x2(val(8 * i), val(8 * i + 1)), pack_bf16x2(val(8 * i + 2), val(8 * i + 3)),
+                                  pack_bf16x2(val(8 * i + 4), val(8 * i + 5)), pack_bf16x2(val(8 * i + 6), val(8 * i + 7)));
+          } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.ws_o + rec * HD + c);
+#pragma unroll
+            for (int i = 0; i < kPart / 4; ++i)
+              dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+          }
         }
         __syncwarp();
+        // The hand-over's shared memory is read before the next columns, or queries, go there.
+        if (kSplit > 1 && !meet_all()) { ok = false; break; }
       }
-      if (mine && whole) a.lse[out] = lrow > 0.f ? (mrow + __log2f(lrow)) * kLn2 : -INFINITY;
-      if (mine && !whole) *reinterpret_cast<float2 *>(a.ws_ml + 2 * (rec * a.rec_rows + row)) = make_float2(mrow, lrow);
+      if (mine && copy == 0) {
+        if (whole)
+          a.lse[out] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+        else
+          *reinterpret_cast<float2 *>(a.ws_ml + 2 * rec) = make_float2(M, sum);
+      }
       tc_fence_before();
     }
   }
@@ -508,94 +718,123 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
   }
 }
 
-// One warp per (sequence, token, head): merges the records of its unit if a run's end cut it.
+// Merges the records of the cut units: block (c, y) takes rows of the unit that run c starts
+// and does not finish, if there is one (plan[c]: sequence, unit, last run, yes). HD / 4 lanes
+// hold a row, four columns each. Up to 8 records are added by one warp; more (a long cache
+// over many runs) by the block's warps, every eighth record each, and then in order.
 template <int HD>
-__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeArgs a, int runs_max) {
-  constexpr int kPerLane = HD / 32;
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
+  constexpr int kLanes = HD / 4, kSub = 32 / kLanes, kWarps = 8;
+  __shared__ float4 part[kWarps][32];
+  __shared__ float2 part_ml[kWarps][32];
   grid_dep_launch();
   grid_dep_wait();
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<long long>(a.B) * a.n * a.nh) return;
-  const int h = static_cast<int>(w % a.nh), token = static_cast<int>(w / a.nh % a.n);
-  const int b = static_cast<int>(w / a.nh / a.n);
-  const int group = a.nh / a.nkv, kvh = h / group, rho = token * group + h % group;
-  const int row_tiles = (a.n * group + kTileRows - 1) / kTileRows, units = a.nkv * row_tiles;
-  // The unit's place on the line.
-  long long before = 0, length = 0;
-  for (int i = lane; i < a.B; i += 32) {
-    const long long c = static_cast<long long>(sight_of(a, i).count) * units;
-    length += c;
-    if (i < b) before += c;
+  const int c0 = blockIdx.x;
+  const int4 plan = a.plan[c0];
+  if (!plan.w) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane % kLanes, sub = lane / kLanes;
+  const int group = a.nh / a.nkv, rows_all = a.n * group;
+  const int row_tiles = (rows_all + a.tile_rows - 1) / a.tile_rows;
+  const int kvh = plan.y / row_tiles, row0 = (plan.y % row_tiles) * a.tile_rows;
+  const int rows = min(rows_all - row0, a.tile_rows);
+  const int records = plan.z - c0 + 1;
+  const bool wide = records > kWarps;
+  const int first = wide ? warp : 0, step = wide ? kWarps : 1;
+  const int stride = kSub * static_cast<int>(gridDim.y) * (wide ? 1 : kWarps);
+  for (int rb = (wide ? blockIdx.y : blockIdx.y * kWarps + warp) * kSub; rb < rows; rb += stride) {
+    const int row = min(rb + sub, rows - 1);                // (a spare lane repeats the last row)
+    auto rec_of = [&](int k) { return static_cast<size_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * a.rec_rows + row; };
+    float M = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = first; k < records; k += step) M = fmaxf(M, a.ws_ml[2 * rec_of(k)]);
+#pragma unroll 4
+    for (int k = first; k < records; k += step) {
+      const size_t rec = rec_of(k);
+      const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + 2 * rec);
+      const float4 x = *reinterpret_cast<const float4 *>(a.ws_o + rec * HD + 4 * i);
+      if (ml.y > 0.f) {                                     // (a record that saw nothing holds anything)
+        const float w = ex2_approx(ml.x - M);
+        sum = fmaf(ml.y, w, sum);
+        acc.x = fmaf(x.x, w, acc.x), acc.y = fmaf(x.y, w, acc.y);
+        acc.z = fmaf(x.z, w, acc.z), acc.w = fmaf(x.w, w, acc.w);
+      }
+    }
+    if (wide) {
+      part[warp][lane] = acc;
+      part_ml[warp][lane] = make_float2(M, sum);
+      __syncthreads();
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      M = -INFINITY, sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_ml[w][lane].x);
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = part_ml[w][lane];
+        const float4 x = part[w][lane];
+        const float f = ml.y > 0.f ? ex2_approx(ml.x - M) : 0.f;
+        sum = fmaf(ml.y, f, sum);
+        acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
+        acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
+      }
+      __syncthreads();                                      // before the next rows overwrite part
+    }
+    if (rb + sub < rows && (!wide || warp == 0)) {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int rho = row0 + row;
+      const size_t out =
+          (static_cast<size_t>(plan.x) * a.n + rho / group) * a.nh + static_cast<size_t>(kvh) * group + rho % group;
+      *reinterpret_cast<uint2 *>(a.o + out * HD + 4 * i) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (i == 0) a.lse[out] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+    }
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    length += __shfl_xor_sync(0xffffffffu, length, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-  }
-  const int count = sight_of(a, b).count;
-  const long long u0 = before + static_cast<long long>(kvh * row_tiles + rho / kTileRows) * count, u1 = u0 + count;
-  const long long runs = min(static_cast<long long>(runs_max), length);
-  const long long c0 = ((u0 + 1) * runs - 1) / length, c1 = (u1 * runs - 1) / length;   // first and last run
-  if (c0 == c1) return;                                   // in one piece: already written
-  const int row = rho % kTileRows;
-  auto record = [&](long long c) { return (static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * a.rec_rows + row); };
-  float M = -INFINITY;
-  for (long long c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ws_ml[2 * record(c)]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float base = M == -INFINITY ? 0.f : M;
-  float sum = 0.f, acc[kPerLane];
-#pragma unroll
-  for (int e = 0; e < kPerLane; ++e) acc[e] = 0.f;
-  for (long long c = c0; c <= c1; ++c) {
-    const size_t rec = record(c);
-    const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + 2 * rec);
-    if (!(ml.y > 0.f)) continue;                          // saw nothing
-    const float wgt = ex2_approx(ml.x - base);
-    sum = fmaf(ml.y, wgt, sum);
-#pragma unroll
-    for (int e = 0; e < kPerLane; ++e) acc[e] = fmaf(a.ws_o[rec * HD + lane * kPerLane + e], wgt, acc[e]);
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int e = 0; e < kPerLane; ++e)
-    a.o[static_cast<size_t>(w) * HD + lane * kPerLane + e] = __float2bfloat16_rn(acc[e] * inv);
-  if (lane == 0) a.lse[w] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int HD, int kSplit>
+cudaError_t launch_tree_split(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
+                              cudaStream_t stream) {
+  using L = TreeLayout<HD>;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t err = allow_smem(tree_kernel<HD, kSplit>, L::kDynBytes, allowed);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(tree_kernel<HD, kSplit>, static_cast<unsigned>(grid), kTreeThreads, L::kDynBytes, stream, mk, mv, a);
+  if (err != cudaSuccess || grid == 1) return err;
+  // A block for the rows that 8 warps hold at once; where a unit spans many runs (few units),
+  // one for each warp's rows.
+  const int rows_once = 128 / HD * (static_cast<long long>(a.B) * a.nkv * 8 > grid ? 8 : 1);
+  const dim3 blocks(static_cast<unsigned>(grid - 1), static_cast<unsigned>((a.rec_rows + rows_once - 1) / rows_once));
+  return launch_pdl(tree_combine_kernel<HD>, blocks, 256, 0, stream, a);
 }
 
 template <int HD>
 cudaError_t launch_tree_hd(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
                            cudaStream_t stream) {
-  using L = TreeLayout<HD>;
-  cudaError_t err = cudaFuncSetAttribute(tree_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(L::kDynBytes));
-  if (err != cudaSuccess) return err;
-  err = launch_pdl(tree_kernel<HD>, static_cast<unsigned>(grid), kTreeThreads, L::kDynBytes, stream, mk, mv, a);
-  if (err != cudaSuccess || grid == 1) return err;
-  const long long warps = static_cast<long long>(a.B) * a.n * a.nh;
-  return launch_pdl(tree_combine_kernel<HD>, static_cast<unsigned>((warps + 3) / 4), 128, 0, stream, a, grid);
+  if (a.tile_rows == 32) return launch_tree_split<HD, 4>(mk, mv, a, grid, stream);
+  if (a.tile_rows == 64) return launch_tree_split<HD, 2>(mk, mv, a, grid, stream);
+  return launch_tree_split<HD, 1>(mk, mv, a, grid, stream);
 }
 
 }  // namespace
+
+// Rows of a row tile: the smallest of 32, 64 and 128 that holds every row of a kv head, else
+// 128 (and several tiles).
+int tree_tile_rows(int n, int nh, int nkv) {
+  const long long rows = static_cast<long long>(n) * (nh / nkv);
+  return rows <= 32 ? 32 : (rows <= 64 ? 64 : kTileRows);
+}
 
 // CTAs of a call on a GPU with `sms` SMs: one resident wave, or one per tile of the longest
 // line that the table allows when that is shorter.
 int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_pages, int sms) {
   const long long tiles = (static_cast<long long>(max_pages) * page_size + kTileRows - 1) / kTileRows;
-  const long long row_tiles = (static_cast<long long>(n) * (nh / nkv) + kTileRows - 1) / kTileRows;
-  const long long most = tiles * B * nkv * row_tiles;
+  const int tile_rows = tree_tile_rows(n, nh, nkv);
+  const long long row_tiles = (static_cast<long long>(n) * (nh / nkv) + tile_rows - 1) / tile_rows;
+  const double most = static_cast<double>(tiles) * B * nkv * row_tiles;
   const int resident = sms * (hd == 128 ? TreeLayout<128>::kCtas : TreeLayout<64>::kCtas);
-  return static_cast<int>(most < resident ? most : resident);
-}
-
-int tree_record_rows(int n, int nh, int nkv) {
-  const long long rows = static_cast<long long>(n) * (nh / nkv);
-  return rows < kTileRows ? static_cast<int>(rows) : kTileRows;
+  return most < resident ? static_cast<int>(most) : resident;
 }
 
 size_t tree_workspace_bytes(int grid, int rec_rows, int hd) {
-  return static_cast<size_t>(grid) * 2 * rec_rows * (static_cast<size_t>(hd) + 2) * sizeof(float);
+  return static_cast<size_t>(grid) * (sizeof(int4) + 2 * rec_rows * (static_cast<size_t>(hd) + 2) * sizeof(float));
 }
 
 cudaError_t launch_tree_bf16(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int hd, int grid,

@@ -457,7 +457,8 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int grid = tree_grid(B, n, nh, nkv, hd, page_size, max_pages, dev->sms);
   TreeArgs a = {};
-  a.rec_rows = tree_record_rows(n, nh, nkv);
+  a.tile_rows = tree_tile_rows(n, nh, nkv);
+  a.rec_rows = n * (nh / nkv) < a.tile_rows ? n * (nh / nkv) : a.tile_rows;
   void *ws = nullptr;
   XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
   a.q = static_cast<const __nv_bfloat16 *>(q);
@@ -466,7 +467,8 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   a.tree = tree;
   a.o = static_cast<__nv_bfloat16 *>(o);
   a.lse = lse;
-  a.ws_o = static_cast<float *>(ws);
+  a.plan = static_cast<int4 *>(ws);
+  a.ws_o = reinterpret_cast<float *>(a.plan + grid);
   a.ws_ml = a.ws_o + static_cast<size_t>(grid) * 2 * a.rec_rows * hd;
   a.B = B, a.n = n, a.nh = nh, a.nkv = nkv;
   a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;

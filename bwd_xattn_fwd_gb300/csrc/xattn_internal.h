@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace xattn {
 
 constexpr int kTileRows = 128;                  // rows of Q / K / V per tile
@@ -33,6 +35,20 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned threads, si
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+}
+
+// Allows `kernel` its dynamic shared memory on the current device, once per device: `done`
+// holds a bit for each device where that has happened (a call sets it again if two race).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel *kernel, size_t bytes, std::atomic<unsigned long long> &done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 
 // Rows of the per-(batch, head) workspace vectors, padded to whole tiles.
@@ -149,21 +165,23 @@ cudaError_t launch_window_bwd_f32(const float *q, const float *k, const float *v
 
 // Attention of n new tokens per sequence over a paged cache (attn_tree.cu). mk, mv: maps over
 // the pools [num_pages, page_size, nkv, hd] with boxes of min(page_size, 128) rows of one kv
-// head (64 columns at hd = 128). ws_o, ws_ml: tree_workspace_bytes(grid, rec_rows, hd) bytes,
-// ws_ml after the 2 grid rec_rows hd floats of ws_o.
+// head (64 columns at hd = 128). The scratch, tree_workspace_bytes(grid, rec_rows, hd) bytes:
+// plan, then the 2 grid rec_rows hd floats of ws_o, then ws_ml.
 struct TreeArgs {
   const __nv_bfloat16 *q;
   const int *page_table, *ctx_lens;
   const unsigned long long *tree;      // null: token i sees new tokens 0 .. i
   __nv_bfloat16 *o;
   float *lse, *ws_o, *ws_ml;
-  int B, n, nh, nkv, num_pages, page_size, max_pages, window, sinks, rec_rows;
+  int4 *plan;                          // [grid] what each run leaves to the combine
+  int B, n, nh, nkv, num_pages, page_size, max_pages, window, sinks;
+  int tile_rows, rec_rows;             // rows of a row tile (tree_tile_rows), and of a record
   float scale_log2;
   int *status;
   unsigned long long timeout_ns;
 };
 int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_pages, int sms);
-int tree_record_rows(int n, int nh, int nkv);
+int tree_tile_rows(int n, int nh, int nkv);
 size_t tree_workspace_bytes(int grid, int rec_rows, int hd);
 cudaError_t launch_tree_bf16(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int hd, int grid,
                              cudaStream_t stream);

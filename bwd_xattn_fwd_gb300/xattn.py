@@ -16,6 +16,8 @@ import ctypes
 import enum
 import os
 
+import torch
+
 from . import build as _build
 
 # XATTN_LIBRARY may name another build of libxattn (for example an instrumented one).
@@ -332,45 +334,52 @@ def attention_decode(q, k_cache, v_cache, scale=None, stream=None):
     return o, lse
 
 
-def _check(tensors):
-    """Raises unless each (name, tensor, shape, dtype) is a contiguous tensor of that shape and
-    type on the first one's GPU. Returns that device."""
-    device = tensors[0][1].device
+# ---- tensor-level helpers that check their tensors ---------------------------------------
+#
+# Small calls are bound by the host: these helpers look the C functions up once, pass
+# pointers themselves, and enter a device or stream guard only when one is needed (a
+# decode step's append: 13.0 us through the generic wrappers, 6 us this way).
+
+_window_fwd, _window_fwd_f32 = _lib.xattn_window_fwd, _lib.xattn_window_fwd_f32
+_window_bwd, _window_bwd_f32 = _lib.xattn_window_bwd, _lib.xattn_window_bwd_f32
+_tree_decode = _lib.xattn_tree_decode
+_append, _compact = _lib.xattn_cache_append, _lib.xattn_cache_compact
+
+
+def _refuse(name, t, shape, dtype, device):
+    """Says what is wrong with a tensor that is not as expected."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, not {type(t).__name__}")
     if device.type != "cuda":
-        raise ValueError(f"{tensors[0][0]} must be a CUDA tensor, not on {device}")
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check(device, tensors):
+    """Raises unless every (name, tensor, shape, dtype) is a contiguous tensor of that shape and
+    type on the GPU `device`."""
+    on_gpu = device.type == "cuda"
     for name, t, shape, dtype in tensors:
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {device}")
-    return device
+        if not (on_gpu and isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.device == device and t.is_contiguous()):
+            _refuse(name, t, shape, dtype, device)
 
 
-class _On:
-    """Makes `device` current, and the given stream (a torch stream or a raw handle) the one
-    that torch allocates outputs on; .stream is the handle to launch on."""
+class _Guards:
+    """A stack of context managers."""
 
-    def __init__(self, device, stream):
-        import torch
-        self._guards = []
-        if torch.cuda.current_device() != device.index:
-            self._guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self._guards.append(torch.cuda.stream(stream))
-            self.stream = stream.cuda_stream
-        else:
-            self.stream = torch.cuda.current_stream(device).cuda_stream
+    def __init__(self, *guards):
+        self._guards = guards
 
     def __enter__(self):
         for g in self._guards:
             g.__enter__()
-        return self.stream
 
     def __exit__(self, *exc):
         for g in reversed(self._guards):
@@ -378,61 +387,85 @@ class _On:
         return False
 
 
+_nothing = _Guards()
+
+
+def _on(device, stream):
+    """(guard, handle): within the guard `device` is current and torch allocates outputs for the
+    given stream (a torch stream, a raw handle, or None: the device's current stream), whose
+    handle is what to launch on."""
+    here = torch.cuda.current_device() == device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        return (_nothing if here else _Guards(torch.cuda.device(device))), handle
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return _Guards(torch.cuda.device(device), torch.cuda.stream(stream)), stream.cuda_stream
+
+
 def _window_dims(q, k, v):
-    import torch
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported dtype {q.dtype}")
+    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported q: {getattr(q, 'dtype', type(q))}")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,S,nh,hd] and k, v [B,S,nkv,hd]")
     B, S, nh, hd = q.shape
     nkv = k.shape[2]
-    return B, S, nh, nkv, hd, (("q", q, (B, S, nh, hd), q.dtype), ("k", k, (B, S, nkv, hd), q.dtype),
-                               ("v", v, (B, S, nkv, hd), q.dtype))
+    kv = (B, S, nkv, hd)
+    return B, S, nh, nkv, hd, (("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype))
 
 
 def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
     """(o, lse) of causal attention in which query i sees key j only if i - j < window or
     j < sinks; tensors as for attention_fwd (bf16 or fp32)."""
-    import torch
     B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
-    device = _check(tensors)
-    scale = float(hd ** -0.5 if scale is None else scale)
-    with _On(device, stream) as handle:
+    device = q.device
+    _check(device, tensors)
+    scale = hd ** -0.5 if scale is None else float(scale)
+    window, sinks = min(window, NO_WINDOW), min(sinks, NO_WINDOW)
+    guard, handle = _on(device, stream)
+    with guard:
         o = torch.empty_like(q)
         lse = torch.empty((B, S, nh), dtype=torch.float32, device=device)
-        fn = xattn_window_fwd if q.dtype == torch.bfloat16 else xattn_window_fwd_f32
-        fn(q, k, v, B, S, nh, nkv, hd, window, sinks, scale, o, lse, handle)
+        fn = _window_fwd if q.dtype is torch.bfloat16 else _window_fwd_f32
+        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, nh, nkv, hd, window, sinks, scale, o.data_ptr(),
+                lse.data_ptr(), handle)
+    if rc:
+        raise XattnError(rc, "attention_window_fwd")
     return o, lse
 
 
 def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, stream=None, deterministic=False):
     """(dq, dk, dv) for the tensors of attention_window_fwd and the output gradient dO.
     deterministic (bf16): dQ bit-reproducible as well, from a second recompute."""
-    import torch
     B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
-    device = _check((*tensors, ("o", o, q.shape, q.dtype), ("dO", dO, q.shape, q.dtype),
-                     ("lse", lse, (B, S, nh), torch.float32)))
-    scale = float(hd ** -0.5 if scale is None else scale)
-    with _On(device, stream) as handle:
+    device, dtype = q.device, q.dtype
+    _check(device, (*tensors, ("o", o, q.shape, dtype), ("dO", dO, q.shape, dtype),
+                    ("lse", lse, (B, S, nh), torch.float32)))
+    scale = hd ** -0.5 if scale is None else float(scale)
+    window, sinks = min(window, NO_WINDOW), min(sinks, NO_WINDOW)
+    guard, handle = _on(device, stream)
+    with guard:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        if q.dtype == torch.bfloat16:
-            xattn_window_bwd(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, deterministic, dq, dk, dv,
-                             handle)
-        else:
-            xattn_window_bwd_f32(q, k, v, o, dO, lse, B, S, nh, nkv, hd, window, sinks, scale, dq, dk, dv, handle)
+        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(), B, S, nh, nkv,
+                hd, window, sinks, scale)
+        outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), handle)
+        rc = (_window_bwd(*args, 1 if deterministic else 0, *outs) if dtype is torch.bfloat16
+              else _window_bwd_f32(*args, *outs))
+    if rc:
+        raise XattnError(rc, "attention_window_bwd")
     return dq, dk, dv
 
 
 def _pool(k_pages, v_pages, page_table, ctx_lens):
-    """The checks of a paged cache's tensors, and its sizes."""
-    import torch
+    """Sizes of a paged cache, and its tensors to check."""
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_pages, v_pages must be [num_pages,page_size,nkv,hd] and page_table [B,max_pages]")
     B, max_pages = page_table.shape
-    return B, max_pages, (("k_pages", k_pages, k_pages.shape, torch.bfloat16),
-                          ("v_pages", v_pages, k_pages.shape, torch.bfloat16),
-                          ("page_table", page_table, page_table.shape, torch.int32),
-                          ("ctx_lens", ctx_lens, (B,), torch.int32))
+    shape = k_pages.shape
+    return B, max_pages, shape, (("k_pages", k_pages, shape, torch.bfloat16),
+                                 ("v_pages", v_pages, shape, torch.bfloat16),
+                                 ("page_table", page_table, (B, max_pages), torch.int32),
+                                 ("ctx_lens", ctx_lens, (B,), torch.int32))
 
 
 def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, window=None, sinks=0, scale=None,
@@ -443,52 +476,59 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
     ctx_lens .. ctx_lens + n - 1 (cache_append). tree [B,n] (int64): bit j of word i lets token
     i see new token j; None: token i sees new tokens 0 .. i (n = 1: the decode step). window
     (None: no window) and sinks as in attention_window_fwd."""
-    import torch
-    B, max_pages, tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
+    B, max_pages, (num_pages, page_size, nkv, hd), tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
     if q.dim() != 4:
         raise ValueError("q must be [B,n,nh,hd]")
-    n, nh = int(q.shape[1]), int(q.shape[2])
-    num_pages, page_size, nkv, hd = k_pages.shape
-    tensors = (("q", q, (B, n, nh, hd), torch.bfloat16), *tensors)
+    n, nh = q.shape[1], q.shape[2]
+    device = q.device
+    _check(device, (("q", q, (B, n, nh, hd), torch.bfloat16), *tensors))
+    words = None
     if tree is not None:
-        tensors = (*tensors, ("tree", tree, (B, n), torch.int64))
-    device = _check(tensors)
-    scale = float(hd ** -0.5 if scale is None else scale)
-    window = NO_WINDOW if window is None else window
-    with _On(device, stream) as handle:
+        _check(device, (("tree", tree, (B, n), torch.int64),))
+        words = tree.data_ptr()
+    scale = hd ** -0.5 if scale is None else float(scale)
+    window, sinks = NO_WINDOW if window is None else min(window, NO_WINDOW), min(sinks, NO_WINDOW)
+    guard, handle = _on(device, stream)
+    with guard:
         o = torch.empty_like(q)
         lse = torch.empty((B, n, nh), dtype=torch.float32, device=device)
-        xattn_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, B, n, nh, nkv, hd, num_pages, page_size,
-                          max_pages, window, sinks, scale, o, lse, handle)
+        rc = _tree_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                          ctx_lens.data_ptr(), words, B, n, nh, nkv, hd, num_pages, page_size, max_pages,
+                          window, sinks, scale, o.data_ptr(), lse.data_ptr(), handle)
+    if rc:
+        raise XattnError(rc, "attention_tree_decode")
     return o, lse
 
 
 def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=None):
     """Writes the rows k_new, v_new [B,n,nkv,hd] to positions ctx_lens .. ctx_lens + n - 1 of each
     sequence's pages (in place)."""
-    import torch
-    B, max_pages, tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
-    num_pages, page_size, nkv, hd = k_pages.shape
+    B, max_pages, (num_pages, page_size, nkv, hd), tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
     if k_new.dim() != 4:
         raise ValueError("k_new and v_new must be [B,n,nkv,hd]")
-    n = int(k_new.shape[1])
-    device = _check((*tensors, ("k_new", k_new, (B, n, nkv, hd), torch.bfloat16),
-                     ("v_new", v_new, (B, n, nkv, hd), torch.bfloat16)))
-    with _On(device, stream) as handle:
-        xattn_cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, B, n, nkv, hd, num_pages, page_size,
-                           max_pages, handle)
+    n = k_new.shape[1]
+    device, rows = k_pages.device, (B, n, nkv, hd)
+    _check(device, (*tensors, ("k_new", k_new, rows, torch.bfloat16), ("v_new", v_new, rows, torch.bfloat16)))
+    guard, handle = _on(device, stream)
+    with guard:
+        rc = _append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                     page_table.data_ptr(), ctx_lens.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, handle)
+    if rc:
+        raise XattnError(rc, "cache_append")
 
 
 def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream=None):
     """Moves the rows of positions ctx_lens + path[:, i], i < accepted, down to ctx_lens + i (in
     place): path [B,n] (int32, ascending over its accepted entries), accepted [B] (int32)."""
-    import torch
-    B, max_pages, tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
-    num_pages, page_size, nkv, hd = k_pages.shape
+    B, max_pages, (num_pages, page_size, nkv, hd), tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
     if path.dim() != 2:
         raise ValueError("path must be [B,n]")
-    n = int(path.shape[1])
-    device = _check((*tensors, ("path", path, (B, n), torch.int32), ("accepted", accepted, (B,), torch.int32)))
-    with _On(device, stream) as handle:
-        xattn_cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, B, n, nkv, hd, num_pages,
-                            page_size, max_pages, handle)
+    n = path.shape[1]
+    device = k_pages.device
+    _check(device, (*tensors, ("path", path, (B, n), torch.int32), ("accepted", accepted, (B,), torch.int32)))
+    guard, handle = _on(device, stream)
+    with guard:
+        rc = _compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(),
+                      path.data_ptr(), accepted.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, handle)
+    if rc:
+        raise XattnError(rc, "cache_compact")
