@@ -42,26 +42,11 @@ __device__ __forceinline__ void load_row(float (&x)[kMaxSlots], const float *row
   }
 }
 
-// Keys that query i sees: j = 0 .. i, or (kWin) those with i - j < window or j < sinks,
-// taken as [0, heads) and [lo, i]. key_after steps over the gap; a key j is seen by the
-// queries i = j .. last_query.
-template <bool kWin>
-struct Seen {
-  int window, sinks;
-  __device__ int lo(int i) const { return kWin ? max(i - window + 1, 0) : 0; }
-  __device__ int first(int i) const { return kWin && sinks == 0 ? lo(i) : 0; }
-  __device__ int after(int j, int i) const { return kWin && j + 1 >= sinks ? max(j + 1, lo(i)) : j + 1; }
-  __device__ int last_query(int j, int S) const {
-    return kWin && j >= sinks && window < S - j ? j + window - 1 : S - 1;
-  }
-};
-
-// Forward: warp per (b, i, h). Online softmax over the keys that query i sees.
-template <bool kWin>
+// Forward: warp per (b, i, h). Online softmax over keys j <= i.
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     fwd_f32_kernel(const float *__restrict__ q, const float *__restrict__ k,
                    const float *__restrict__ v, float *__restrict__ o, float *__restrict__ lse,
-                   int B, int S, int nh, int nkv, int hd, float scale, const Seen<kWin> seen) {
+                   int B, int S, int nh, int nkv, int hd, float scale) {
   const long long w = static_cast<long long>(blockIdx.x) * kWarpsPerBlock + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (w >= static_cast<long long>(B) * S * nh) return;
@@ -72,7 +57,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   float qi[kMaxSlots], acc[kMaxSlots] = {0.f, 0.f, 0.f, 0.f};
   load_row(qi, q + w * hd, hd, lane);
   float mrow = -INFINITY, lrow = 0.f;
-  for (int j = seen.first(i); j <= i; j = seen.after(j, i)) {
+  for (int j = 0; j <= i; ++j) {
     const size_t kv_row = ((static_cast<size_t>(b) * S + j) * nkv + kvh) * hd;
     const float s = scale * row_dot(qi, k + kv_row, hd, lane);
     const float mnew = fmaxf(mrow, s);
@@ -95,15 +80,12 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   if (lane == 0) lse[w] = mrow + logf(lrow);
 }
 
-// dQ: warp per query row (b, i, h). dQ_i = scale sum_j P_ij (dO_i.v_j - D_i) k_j over the
-// keys that query i sees.
-template <bool kWin>
+// dQ: warp per query row (b, i, h). dQ_i = scale sum_{j<=i} P_ij (dO_i.v_j - D_i) k_j.
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     bwd_dq_f32_kernel(const float *__restrict__ q, const float *__restrict__ k,
                       const float *__restrict__ v, const float *__restrict__ o,
                       const float *__restrict__ dO, const float *__restrict__ lse,
-                      float *__restrict__ dq, int B, int S, int nh, int nkv, int hd, float scale,
-                      const Seen<kWin> seen) {
+                      float *__restrict__ dq, int B, int S, int nh, int nkv, int hd, float scale) {
   const long long w = static_cast<long long>(blockIdx.x) * kWarpsPerBlock + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (w >= static_cast<long long>(B) * S * nh) return;
@@ -120,7 +102,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   for (int s = 0; s < kMaxSlots; ++s) Di = fmaf(doi[s], oi[s], Di);
   Di = warp_sum(Di);
   const float L = lse[w];
-  for (int j = seen.first(i); j <= i; j = seen.after(j, i)) {
+  for (int j = 0; j <= i; ++j) {
     const size_t kv_row = ((static_cast<size_t>(b) * S + j) * nkv + kvh) * hd;
     const float p = expf(scale * row_dot(qi, k + kv_row, hd, lane) - L);
     const float dp = row_dot(doi, v + kv_row, hd, lane);
@@ -139,14 +121,13 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 }
 
 // dK, dV: warp per key row (b, j, kvh); loops over the query group r = 0.. in order
-// and over the queries i >= j that see key j.
-template <bool kWin>
+// and over queries i >= j.
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     bwd_dkdv_f32_kernel(const float *__restrict__ q, const float *__restrict__ k,
                         const float *__restrict__ v, const float *__restrict__ o,
                         const float *__restrict__ dO, const float *__restrict__ lse,
                         float *__restrict__ dk, float *__restrict__ dv, int B, int S, int nh,
-                        int nkv, int hd, float scale, const Seen<kWin> seen) {
+                        int nkv, int hd, float scale) {
   const long long w = static_cast<long long>(blockIdx.x) * kWarpsPerBlock + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (w >= static_cast<long long>(B) * S * nkv) return;
@@ -160,8 +141,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
   load_row(vj, v + w * hd, hd, lane);
   for (int r = 0; r < group; ++r) {
     const int h = kvh * group + r;
-    const int last = seen.last_query(j, S);
-    for (int i = j; i <= last; ++i) {
+    for (int i = j; i < S; ++i) {
       const size_t qrow = ((static_cast<size_t>(b) * S + i) * nh + h);
       const float *dOi = dO + qrow * hd;
       const float *oi = o + qrow * hd;
@@ -206,50 +186,24 @@ cudaError_t launch_fwd_f32(const float *q, const float *k, const float *v, float
                            int B, int S, int nh, int nkv, int hd, float scale,
                            cudaStream_t stream) {
   const long long rows = static_cast<long long>(B) * S * nh;
-  fwd_f32_kernel<false><<<warps_grid(rows), kWarpsPerBlock * 32, 0, stream>>>(
-      q, k, v, o, lse, B, S, nh, nkv, hd, scale, Seen<false>{});
+  fwd_f32_kernel<<<warps_grid(rows), kWarpsPerBlock * 32, 0, stream>>>(q, k, v, o, lse, B, S, nh,
+                                                                        nkv, hd, scale);
   return cudaGetLastError();
 }
-
-cudaError_t launch_window_fwd_f32(const float *q, const float *k, const float *v, float *o, float *lse, int B, int S,
-                                  int nh, int nkv, int hd, float scale, int window, int sinks, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(B) * S * nh;
-  fwd_f32_kernel<true><<<warps_grid(rows), kWarpsPerBlock * 32, 0, stream>>>(
-      q, k, v, o, lse, B, S, nh, nkv, hd, scale, Seen<true>{window, sinks});
-  return cudaGetLastError();
-}
-
-namespace {
-
-template <bool kWin>
-cudaError_t launch_bwd(const float *q, const float *k, const float *v, const float *o, const float *dO,
-                       const float *lse, float *dq, float *dk, float *dv, int B, int S, int nh, int nkv, int hd,
-                       float scale, const Seen<kWin> &seen, cudaStream_t stream) {
-  const long long qrows = static_cast<long long>(B) * S * nh;
-  const long long krows = static_cast<long long>(B) * S * nkv;
-  bwd_dq_f32_kernel<kWin><<<warps_grid(qrows), kWarpsPerBlock * 32, 0, stream>>>(q, k, v, o, dO, lse, dq, B, S, nh,
-                                                                                 nkv, hd, scale, seen);
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  bwd_dkdv_f32_kernel<kWin><<<warps_grid(krows), kWarpsPerBlock * 32, 0, stream>>>(q, k, v, o, dO, lse, dk, dv, B, S,
-                                                                                   nh, nkv, hd, scale, seen);
-  return cudaGetLastError();
-}
-
-}  // namespace
 
 cudaError_t launch_bwd_f32(const float *q, const float *k, const float *v, const float *o,
                            const float *dO, const float *lse, float *dq, float *dk, float *dv,
                            int B, int S, int nh, int nkv, int hd, float scale,
                            cudaStream_t stream) {
-  return launch_bwd<false>(q, k, v, o, dO, lse, dq, dk, dv, B, S, nh, nkv, hd, scale, Seen<false>{}, stream);
-}
-
-cudaError_t launch_window_bwd_f32(const float *q, const float *k, const float *v, const float *o, const float *dO,
-                                  const float *lse, float *dq, float *dk, float *dv, int B, int S, int nh, int nkv,
-                                  int hd, float scale, int window, int sinks, cudaStream_t stream) {
-  return launch_bwd<true>(q, k, v, o, dO, lse, dq, dk, dv, B, S, nh, nkv, hd, scale, Seen<true>{window, sinks},
-                          stream);
+  const long long qrows = static_cast<long long>(B) * S * nh;
+  const long long krows = static_cast<long long>(B) * S * nkv;
+  bwd_dq_f32_kernel<<<warps_grid(qrows), kWarpsPerBlock * 32, 0, stream>>>(q, k, v, o, dO, lse, dq,
+                                                                           B, S, nh, nkv, hd, scale);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  bwd_dkdv_f32_kernel<<<warps_grid(krows), kWarpsPerBlock * 32, 0, stream>>>(
+      q, k, v, o, dO, lse, dk, dv, B, S, nh, nkv, hd, scale);
+  return cudaGetLastError();
 }
 
 }  // namespace xattn

@@ -265,6 +265,11 @@ xattn_status make_map_pages(CUtensorMap *map, const void *ptr, int num_pages, in
   return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
+// The fp32 window kernels' largest grid: four blocks per 32 rows of a head.
+bool window_f32_grid_ok(int B, int S, int nh) {
+  return static_cast<double>(B) * nh * ((S + 31) / 32) * 4 < 0x1p31;
+}
+
 xattn_status bf16_device(DeviceInfo **dev) {
   XATTN_TRY(device_info(dev));
   if (!(*dev)->sm103) return XATTN_ERR_NO_DEVICE_SUPPORT;
@@ -639,6 +644,7 @@ xattn_status xattn_window_fwd_f32(const float *q, const float *k, const float *v
   int w = 0, s = 0;
   XATTN_TRY(check_window(S, window, sinks, &w, &s));
   if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!window_f32_grid_ok(B, S, nh)) return XATTN_ERR_BAD_SHAPE;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
   return cuda_status(launch_window_fwd_f32(q, k, v, o, lse, B, S, nh, nkv, hd, scale, w, s,
@@ -653,10 +659,17 @@ xattn_status xattn_window_bwd_f32(const float *q, const float *k, const float *v
   int w = 0, s = 0;
   XATTN_TRY(check_window(S, window, sinks, &w, &s));
   if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!window_f32_grid_ok(B, S, nh)) return XATTN_ERR_BAD_SHAPE;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
-  return cuda_status(launch_window_bwd_f32(q, k, v, o, dO, lse, dq, dk, dv, B, S, nh, nkv, hd, scale, w, s,
-                                           static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void *D = nullptr;
+  XATTN_TRY(scratch_alloc(*dev, static_cast<size_t>(B) * S * nh * sizeof(float), st, &D));
+  xattn_status r = cuda_status(launch_window_bwd_f32(q, k, v, o, dO, lse, dq, dk, dv, static_cast<float *>(D), B, S, nh,
+                                                     nkv, hd, scale, w, s, st));
+  const cudaError_t fe = cudaFreeAsync(D, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
 }
 
 xattn_status xattn_fwd_f32(const float *q, const float *k, const float *v, int B, int S, int nh,

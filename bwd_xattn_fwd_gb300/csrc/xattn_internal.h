@@ -160,8 +160,8 @@ cudaError_t launch_window_bwd_dq_bf16(const CUtensorMap &mq, const CUtensorMap &
 cudaError_t launch_window_fwd_f32(const float *q, const float *k, const float *v, float *o, float *lse, int B, int S,
                                   int nh, int nkv, int hd, float scale, int window, int sinks, cudaStream_t stream);
 cudaError_t launch_window_bwd_f32(const float *q, const float *k, const float *v, const float *o, const float *dO,
-                                  const float *lse, float *dq, float *dk, float *dv, int B, int S, int nh, int nkv,
-                                  int hd, float scale, int window, int sinks, cudaStream_t stream);
+                                  const float *lse, float *dq, float *dk, float *dv, float *D, int B, int S, int nh,
+                                  int nkv, int hd, float scale, int window, int sinks, cudaStream_t stream);   // D: [B, S, nh] scratch
 
 // Attention of n new tokens per sequence over a paged cache (attn_tree.cu). mk, mv: maps over
 // the pools [num_pages, page_size, nkv, hd] with boxes of min(page_size, 128) rows of one kv

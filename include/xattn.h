@@ -223,7 +223,9 @@ xattn_status xattn_bwd_f32(const float *q, const float *k, const float *v, const
  *                           backward's, and fp32 partial sums of the sink tiles' dK and dV)
  *                           is taken with cudaMallocAsync on `stream` and released with
  *                           cudaFreeAsync on it.
- *   xattn_window_*_f32    : IEEE fp32 on the CUDA cores, hd in [1, 128], no scratch.
+ *   xattn_window_*_f32    : IEEE fp32 on the CUDA cores, hd in [1, 128], every output
+ *                           reproducible; the backward takes B * S * nh floats of scratch
+ *                           in the same way.
  */
 #define XATTN_NO_WINDOW 0x7fffffff
 xattn_status xattn_window_fwd(const void *q, const void *k, const void *v, int B, int S, int nh,
