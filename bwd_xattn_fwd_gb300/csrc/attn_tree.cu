@@ -22,6 +22,9 @@
 //     read on the device: a captured graph follows them).
 //   * A run's end cuts a unit: such pieces write (max, sum, unnormalised O) records, and
 //     tree_combine_kernel merges each cut unit's records in order.
+//   * Short caches (a table of at most kWholeTiles tiles a sequence): runs of whole units, so
+//     there is nothing to merge: no records, no scratch and no second kernel, which at that
+//     length cost more than the tiles that a CTA takes more.
 //   * Pages: a tile is loaded box by box (one TMA box per page, or per 128 rows of a larger
 //     one). A box that no row can see, or whose table entry is no page, is loaded from
 //     outside the pool: the TMA unit writes zeros and reads nothing.
@@ -135,9 +138,9 @@ __device__ __forceinline__ long long run_of(long long length, long long runs, lo
 }
 
 // A run of the line of tiles, walked piece by piece; warp-uniform, every warp of every role
-// walks the same pieces. All counts in 64 bits.
+// walks the same pieces. All counts in 64 bits. With whole units the line's steps are units.
 struct Walk {
-  long long pos, stop;     // next tile and end of the run, on the line
+  long long pos, stop;     // next tile (unit) and end of the run, on the line
   long long first;         // where sequence b starts on it
   int b, e0, e1, unit;     // piece: sequence, entries [e0, e1) of its list, unit within it
   Sight s;
@@ -189,6 +192,15 @@ __device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane
 
 __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units) {
   if (w.pos >= w.stop) return false;
+  if (a.whole) {
+    w.b = static_cast<int>(quotient(w.pos, units));
+    w.unit = static_cast<int>(w.pos - static_cast<long long>(w.b) * units);
+    w.s = sight_of(a, w.b);
+    w.e0 = 0;
+    w.e1 = w.s.count;
+    ++w.pos;
+    return true;
+  }
   long long at = w.pos - w.first;
   if (at >= static_cast<long long>(w.s.count) * units) {       // the next sequence
     w.first += static_cast<long long>(w.s.count) * units;
@@ -259,13 +271,15 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
   const int row_tiles = (rows_all + kRows - 1) / kRows;
   const int units = a.nkv * row_tiles;
   int counts[4];
-  const long long length = line_length(a, units, lane, counts);
+  const long long length = a.whole ? static_cast<long long>(a.B) * units : line_length(a, units, lane, counts);
   const long long runs = min(static_cast<long long>(gridDim.x), length);
   Walk walk;
   walk.pos = walk.stop = 0;
   if (blockIdx.x < runs) {
     walk.pos = run_start(length, runs, blockIdx.x);
     walk.stop = run_start(length, runs, blockIdx.x + 1);
+  }
+  if (!a.whole && walk.pos < walk.stop) {
     line_find(a, units, lane, counts, walk.pos, &walk.b, &walk.first);
     walk.s = sight_of(a, walk.b);
   }
@@ -304,11 +318,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       }
       __syncwarp();
     };
-    if (have) prefetch_table(walk);
     while (ok && have) {
       const Walk here = walk;
-      have = walk_piece(walk, a, units);
-      if (have) prefetch_table(walk);
       const int kvh = here.unit / row_tiles;
       const int *table = a.page_table + static_cast<size_t>(here.b) * a.max_pages;
       // This lane's box of entry e: its table entry (-1 when no row can see the box) and its
@@ -321,8 +332,16 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
         return __ldg(table + at);                               // p0 < end <= max_pages * page_size
       };
       int row_next = 0, id_next = box_of(here.e0, &row_next);
+      const bool first = R == 0;
+      have = false;
 #pragma unroll 1
       for (int e = here.e0; e < here.e1; ++e, ++R) {
+        // Looking ahead waits until the run's first copies are on their way.
+        if (e == min(here.e0 + (first ? 1 : 0), here.e1 - 1)) {
+          if (first) prefetch_table(here);
+          have = walk_piece(walk, a, units);
+          if (have) prefetch_table(walk);
+        }
         // Outside the pool (num_pages) there is nothing to read: the box is zeros.
         const int row = row_next, page = id_next >= 0 && id_next < a.num_pages ? id_next : a.num_pages;
         id_next = box_of(e + 1, &row_next);
@@ -453,12 +472,11 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       }
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c) xq[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      // Bits past the last new token mean nothing.
-      word = !mine ? 0 : (a.tree ? __ldg(a.tree + at) : (2ull << token) - 1) & (a.n == 64 ? ~0ull : (1ull << a.n) - 1);
+      word = !mine ? 0 : (a.tree ? __ldg(a.tree + at) : (2ull << token) - 1);   // (not used here: no wait)
     };
     bool have = walk_piece(walk, a, units);
     if (have) load_rows(false);
-    else if (warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
+    else if (!a.whole && warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
     while (ok && have) {
       const Sight s = walk.s;
       const int b = walk.b, e0 = walk.e0, e1 = walk.e1;
@@ -468,7 +486,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       have = walk_piece(walk, a, units);
       if (have) load_rows(true);
       // A run that ends inside the unit it started last says so to the combine.
-      if (!have && warp == 2 && lane == 0) {
+      if (!have && !a.whole && warp == 2 && lane == 0) {
         const long long start = walk.stop - (e1 - e0);
         const bool cut = e0 == 0 && e1 < s.count;
         a.plan[blockIdx.x] = make_int4(b, unit, cut ? static_cast<int>(run_of(length, runs, start + s.count - 1)) : 0, cut);
@@ -489,7 +507,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       fence_proxy_async_smem();
       warp_arrive(q_full, lane);
       // The row's ancestors and how far its window reaches.
-      const unsigned long long seen = word;
+      // Bits past the last new token mean nothing.
+      const unsigned long long seen = word & (a.n == 64 ? ~0ull : (1ull << a.n) - 1);
       const int far = s.ctx + max(__popcll(seen) - 1, 0) - a.window + 1;
       float mrow = -INFINITY, lrow = 0.f;
       // One tile: this copy's kCols columns. The masked form is compiled apart, so that the
@@ -797,7 +816,7 @@ cudaError_t launch_tree_split(const CUtensorMap &mk, const CUtensorMap &mv, cons
   cudaError_t err = allow_smem(tree_kernel<HD, kSplit>, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
   err = launch_pdl(tree_kernel<HD, kSplit>, static_cast<unsigned>(grid), kTreeThreads, L::kDynBytes, stream, mk, mv, a);
-  if (err != cudaSuccess || grid == 1) return err;
+  if (err != cudaSuccess || grid == 1 || a.whole) return err;
   // A block for the rows that 8 warps hold at once; where a unit spans many runs (few units),
   // one for each warp's rows.
   const int rows_once = 128 / HD * (static_cast<long long>(a.B) * a.nkv * 8 > grid ? 8 : 1);
@@ -822,10 +841,18 @@ int tree_tile_rows(int n, int nh, int nkv) {
   return rows <= 32 ? 32 : (rows <= 64 ? 64 : kTileRows);
 }
 
-// CTAs of a call on a GPU with `sms` SMs: one resident wave, or one per tile of the longest
-// line that the table allows when that is shorter.
+// Runs are whole units when no sequence can have more tiles than this (see the head of the
+// file; TREE_WHOLE_MEASURED).
+constexpr int kWholeTiles = 8;
+bool tree_whole(int page_size, int max_pages) {
+  return static_cast<long long>(max_pages) * page_size <= kWholeTiles * kTileRows;
+}
+
+// CTAs of a call on a GPU with `sms` SMs: one resident wave, or one per tile (whole unit) of
+// the longest line that the table allows when that is shorter.
 int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_pages, int sms) {
-  const long long tiles = (static_cast<long long>(max_pages) * page_size + kTileRows - 1) / kTileRows;
+  const long long tiles =
+      tree_whole(page_size, max_pages) ? 1 : (static_cast<long long>(max_pages) * page_size + kTileRows - 1) / kTileRows;
   const int tile_rows = tree_tile_rows(n, nh, nkv);
   const long long row_tiles = (static_cast<long long>(n) * (nh / nkv) + tile_rows - 1) / tile_rows;
   const double most = static_cast<double>(tiles) * B * nkv * row_tiles;

@@ -249,7 +249,9 @@ xattn_status check_pages(int B, int n, int nkv, int hd, int num_pages, int page_
 }
 
 // 4-D map over a pool [num_pages, page_size, nkv, hd]: box = up to 128 rows of one kv head in
-// one page (64 columns at hd = 128). Pages outside the pool read as zeros.
+// one page (64 columns at hd = 128). Pages outside the pool read as zeros. L2 fetches as much
+// as a head's row has: at hd = 64 fetches of 256 bytes, half of them the next head's row, made
+// a batch of trees 4 % slower (that row's reader comes after it has left L2).
 xattn_status make_map_pages(CUtensorMap *map, const void *ptr, int num_pages, int page_size, int nkv, int hd) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(nkv),
                               static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(num_pages)};
@@ -261,7 +263,8 @@ xattn_status make_map_pages(CUtensorMap *map, const void *ptr, int num_pages, in
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
                               strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               hd == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              hd == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                        : (hd == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
@@ -464,17 +467,20 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   TreeArgs a = {};
   a.tile_rows = tree_tile_rows(n, nh, nkv);
   a.rec_rows = n * (nh / nkv) < a.tile_rows ? n * (nh / nkv) : a.tile_rows;
+  a.whole = tree_whole(page_size, max_pages) ? 1 : 0;
   void *ws = nullptr;
-  XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
+  if (!a.whole) XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.page_table = page_table;
   a.ctx_lens = ctx_lens;
   a.tree = tree;
   a.o = static_cast<__nv_bfloat16 *>(o);
   a.lse = lse;
-  a.plan = static_cast<int4 *>(ws);
-  a.ws_o = reinterpret_cast<float *>(a.plan + grid);
-  a.ws_ml = a.ws_o + static_cast<size_t>(grid) * 2 * a.rec_rows * hd;
+  if (!a.whole) {
+    a.plan = static_cast<int4 *>(ws);
+    a.ws_o = reinterpret_cast<float *>(a.plan + grid);
+    a.ws_ml = a.ws_o + static_cast<size_t>(grid) * 2 * a.rec_rows * hd;
+  }
   a.B = B, a.n = n, a.nh = nh, a.nkv = nkv;
   a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
   a.window = window < (1 << 30) ? window : (1 << 30);   // a table holds at most 2^30 positions
@@ -483,6 +489,7 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   a.status = dev->status;
   a.timeout_ns = wait_limit_ns();
   xattn_status r = cuda_status(launch_tree_bf16(mk, mv, a, hd, grid, st));
+  if (a.whole) return r;
   const cudaError_t fe = cudaFreeAsync(ws, st);
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
   return r;

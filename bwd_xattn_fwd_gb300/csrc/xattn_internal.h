@@ -175,6 +175,7 @@ struct TreeArgs {
   float *lse, *ws_o, *ws_ml;
   int4 *plan;                          // [grid] what each run leaves to the combine
   int B, n, nh, nkv, num_pages, page_size, max_pages, window, sinks;
+  int whole;                           // runs of whole units (tree_whole): no plan, no records
   int tile_rows, rec_rows;             // rows of a row tile (tree_tile_rows), and of a record
   float scale_log2;
   int *status;
@@ -182,6 +183,7 @@ struct TreeArgs {
 };
 int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_pages, int sms);
 int tree_tile_rows(int n, int nh, int nkv);
+bool tree_whole(int page_size, int max_pages);
 size_t tree_workspace_bytes(int grid, int rec_rows, int hd);
 cudaError_t launch_tree_bf16(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int hd, int grid,
                              cudaStream_t stream);

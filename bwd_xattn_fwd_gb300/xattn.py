@@ -337,8 +337,8 @@ def attention_decode(q, k_cache, v_cache, scale=None, stream=None):
 # ---- tensor-level helpers that check their tensors ---------------------------------------
 #
 # Small calls are bound by the host: these helpers look the C functions up once, pass
-# pointers themselves, and enter a device or stream guard only when one is needed (a
-# decode step's append: 13.0 us through the generic wrappers, 6 us this way).
+# pointers themselves, and make a device or stream current only when that is needed (a decode
+# step's append: 13.0 us through the generic wrappers, HOST_APPEND us this way).
 
 _window_fwd, _window_fwd_f32 = _lib.xattn_window_fwd, _lib.xattn_window_fwd_f32
 _window_bwd, _window_bwd_f32 = _lib.xattn_window_bwd, _lib.xattn_window_bwd_f32
@@ -364,18 +364,21 @@ def _refuse(name, t, shape, dtype, device):
 def _check(device, tensors):
     """Raises unless every (name, tensor, shape, dtype) is a contiguous tensor of that shape and
     type on the GPU `device`."""
-    on_gpu = device.type == "cuda"
+    index = device.index if device.type == "cuda" else -1
     for name, t, shape, dtype in tensors:
-        if not (on_gpu and isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-                and t.device == device and t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+                and t.shape == shape) or index < 0:
             _refuse(name, t, shape, dtype, device)
 
 
-class _Guards:
-    """A stack of context managers."""
+class _Elsewhere:
+    """Makes `device` current, and the given stream (a torch stream, a raw handle, or None: the
+    device's current one) the one that torch allocates on and that calls launch on."""
 
-    def __init__(self, *guards):
-        self._guards = guards
+    def __init__(self, device, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        self._guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
         for g in self._guards:
@@ -387,20 +390,8 @@ class _Guards:
         return False
 
 
-_nothing = _Guards()
-
-
-def _on(device, stream):
-    """(guard, handle): within the guard `device` is current and torch allocates outputs for the
-    given stream (a torch stream, a raw handle, or None: the device's current stream), whose
-    handle is what to launch on."""
-    here = torch.cuda.current_device() == device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-        return (_nothing if here else _Guards(torch.cuda.device(device))), handle
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    return _Guards(torch.cuda.device(device), torch.cuda.stream(stream)), stream.cuda_stream
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _window_dims(q, k, v):
@@ -420,15 +411,16 @@ def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
     B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
     device = q.device
     _check(device, tensors)
+    if stream is not None or _current_device() != device.index:
+        with _Elsewhere(device, stream):
+            return attention_window_fwd(q, k, v, window, sinks, scale)
     scale = hd ** -0.5 if scale is None else float(scale)
     window, sinks = min(window, NO_WINDOW), min(sinks, NO_WINDOW)
-    guard, handle = _on(device, stream)
-    with guard:
-        o = torch.empty_like(q)
-        lse = torch.empty((B, S, nh), dtype=torch.float32, device=device)
-        fn = _window_fwd if q.dtype is torch.bfloat16 else _window_fwd_f32
-        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, nh, nkv, hd, window, sinks, scale, o.data_ptr(),
-                lse.data_ptr(), handle)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, S, nh), dtype=torch.float32, device=device)
+    fn = _window_fwd if q.dtype is torch.bfloat16 else _window_fwd_f32
+    rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, nh, nkv, hd, window, sinks, scale, o.data_ptr(),
+            lse.data_ptr(), _raw_stream(device.index))
     if rc:
         raise XattnError(rc, "attention_window_fwd")
     return o, lse
@@ -441,16 +433,17 @@ def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, strea
     device, dtype = q.device, q.dtype
     _check(device, (*tensors, ("o", o, q.shape, dtype), ("dO", dO, q.shape, dtype),
                     ("lse", lse, (B, S, nh), torch.float32)))
+    if stream is not None or _current_device() != device.index:
+        with _Elsewhere(device, stream):
+            return attention_window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic=deterministic)
     scale = hd ** -0.5 if scale is None else float(scale)
     window, sinks = min(window, NO_WINDOW), min(sinks, NO_WINDOW)
-    guard, handle = _on(device, stream)
-    with guard:
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(), B, S, nh, nkv,
-                hd, window, sinks, scale)
-        outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), handle)
-        rc = (_window_bwd(*args, 1 if deterministic else 0, *outs) if dtype is torch.bfloat16
-              else _window_bwd_f32(*args, *outs))
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(), B, S, nh, nkv,
+            hd, window, sinks, scale)
+    outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _raw_stream(device.index))
+    rc = (_window_bwd(*args, 1 if deterministic else 0, *outs) if dtype is torch.bfloat16
+          else _window_bwd_f32(*args, *outs))
     if rc:
         raise XattnError(rc, "attention_window_bwd")
     return dq, dk, dv
@@ -486,15 +479,16 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
     if tree is not None:
         _check(device, (("tree", tree, (B, n), torch.int64),))
         words = tree.data_ptr()
+    if stream is not None or _current_device() != device.index:
+        with _Elsewhere(device, stream):
+            return attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window, sinks, scale)
     scale = hd ** -0.5 if scale is None else float(scale)
     window, sinks = NO_WINDOW if window is None else min(window, NO_WINDOW), min(sinks, NO_WINDOW)
-    guard, handle = _on(device, stream)
-    with guard:
-        o = torch.empty_like(q)
-        lse = torch.empty((B, n, nh), dtype=torch.float32, device=device)
-        rc = _tree_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                          ctx_lens.data_ptr(), words, B, n, nh, nkv, hd, num_pages, page_size, max_pages,
-                          window, sinks, scale, o.data_ptr(), lse.data_ptr(), handle)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, n, nh), dtype=torch.float32, device=device)
+    rc = _tree_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                      ctx_lens.data_ptr(), words, B, n, nh, nkv, hd, num_pages, page_size, max_pages, window, sinks,
+                      scale, o.data_ptr(), lse.data_ptr(), _raw_stream(device.index))
     if rc:
         raise XattnError(rc, "attention_tree_decode")
     return o, lse
@@ -509,10 +503,11 @@ def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=No
     n = k_new.shape[1]
     device, rows = k_pages.device, (B, n, nkv, hd)
     _check(device, (*tensors, ("k_new", k_new, rows, torch.bfloat16), ("v_new", v_new, rows, torch.bfloat16)))
-    guard, handle = _on(device, stream)
-    with guard:
-        rc = _append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                     page_table.data_ptr(), ctx_lens.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, handle)
+    if stream is not None or _current_device() != device.index:
+        with _Elsewhere(device, stream):
+            return cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens)
+    rc = _append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                 ctx_lens.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(device.index))
     if rc:
         raise XattnError(rc, "cache_append")
 
@@ -526,9 +521,10 @@ def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream
     n = path.shape[1]
     device = k_pages.device
     _check(device, (*tensors, ("path", path, (B, n), torch.int32), ("accepted", accepted, (B,), torch.int32)))
-    guard, handle = _on(device, stream)
-    with guard:
-        rc = _compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(),
-                      path.data_ptr(), accepted.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, handle)
+    if stream is not None or _current_device() != device.index:
+        with _Elsewhere(device, stream):
+            return cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted)
+    rc = _compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
+                  accepted.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(device.index))
     if rc:
         raise XattnError(rc, "cache_compact")
