@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       return tree_wait(meet, meets++ & 1, ctl);
     };
     // A piece's query row and word: into L2 while the piece before it runs, into registers
-    // before that piece's result is written, and put in place after it.
+    // before that piece's result is written (kSplit = 1, whose rows of 128 scores leave none:
+    // after it), and then put in place.
     uint4 xq[HD / 8];
     unsigned long long word = 0;
     auto load_rows = [&](bool ahead) {
@@ -475,13 +476,15 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       word = !mine ? 0 : (a.tree ? __ldg(a.tree + at) : (2ull << token) - 1);   // (not used here: no wait)
     };
     bool have = walk_piece(walk, a, units);
-    if (have) load_rows(false);
-    else if (!a.whole && warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (have) {
+      if (kSplit > 1) load_rows(false);
+    } else if (!a.whole && warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
     while (ok && have) {
       const Sight s = walk.s;
       const int b = walk.b, e0 = walk.e0, e1 = walk.e1;
       const int kvh = walk.unit / row_tiles, row0 = (walk.unit % row_tiles) * kRows;
       const int unit = walk.unit;
+      if (kSplit == 1) load_rows(false);
       // From here on `walk` is the next piece.
       have = walk_piece(walk, a, units);
       if (have) load_rows(true);
@@ -513,26 +516,52 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       float mrow = -INFINITY, lrow = 0.f;
       // One tile: this copy's kCols columns. The masked form is compiled apart, so that the
       // tiles every row sees whole carry no mask. vis: a word per 32 columns.
+      // kSplit = 1 with two CTAs an SM: the columns come from TMEM 32 at a time and twice, for
+      // the maximum and for P. A row of 128 scores held in 168 registers spilled (B8 n64 hd 64
+      // over 8192 positions: 63.4 us, this way 55.7); where there are 255 (hd 128) or fewer
+      // columns the row stays in registers (hd 128: 46.2 us, read twice 50.6).
       auto step = [&](auto masked, const uint32_t *vis, bool first) -> bool {
-        float x[kCols];
-        uint32_t *xr = reinterpret_cast<uint32_t *>(x);
+        constexpr int kChunks = kCols / 32;
+        constexpr bool kKeep = kSplit > 1 || HD == 128;
+        float x[kKeep ? kChunks : 2][32];
+        auto fetch = [&](int k, float *to) { tmem_ld_x32(tSx + 32 * k, reinterpret_cast<uint32_t *>(to)); };
+        // Scaled and masked scores (log2 domain) of chunk k.
+        auto ready = [&](int k, float *y) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) tmem_ld_x32(tSx + c, xr + c);
-        tmem_wait_ld();
-        reg_fence<kCols>(xr);
-        tc_fence_before();
-        warp_arrive(s_free, lane);
-        // Scaled scores (log2 domain) and their maximum.
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-          fmul2(x[c], x[c + 1], x[c], x[c + 1], a.scale_log2, a.scale_log2);
-          if constexpr (decltype(masked)::value) {
-            if (((vis[c >> 5] >> (c & 31)) & 1u) == 0u) x[c] = -INFINITY;
-            if (((vis[c >> 5] >> ((c + 1) & 31)) & 1u) == 0u) x[c + 1] = -INFINITY;
+          for (int c = 0; c < 32; c += 2) {
+            fmul2(y[c], y[c + 1], y[c], y[c + 1], a.scale_log2, a.scale_log2);
+            if constexpr (decltype(masked)::value) {
+              if (((vis[k] >> c) & 1u) == 0u) y[c] = -INFINITY;
+              if (((vis[k] >> (c + 1)) & 1u) == 0u) y[c + 1] = -INFINITY;
+            }
           }
-          float &m = mx[(c >> 1) & 3];
-          m = fmax3(m, x[c], x[c + 1]);
+        };
+        auto read_done = [&]() {
+          tc_fence_before();
+          warp_arrive(s_free, lane);
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (kKeep) {
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) fetch(k, x[k]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) reg_fence<32>(reinterpret_cast<uint32_t *>(x[k]));
+          read_done();
+        } else {
+          fetch(0, x[0]);
+        }
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          float *y = x[kKeep ? k : k & 1];
+          if constexpr (!kKeep) {
+            tmem_wait_ld();
+            reg_fence<32>(reinterpret_cast<uint32_t *>(y));
+            fetch((k + 1) % kChunks, x[(k + 1) & 1]);    // behind the last chunk: the first again
+          }
+          ready(k, y);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], y[c], y[c + 1]);
         }
         const float mnew = fmax3(fmaxf(mrow, mx[0]), mx[1], fmaxf(mx[2], mx[3]));
         // O is rescaled only when some row's maximum grew by more than 2^8.
@@ -542,23 +571,46 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
         if (rescale && mnew > mrow) alpha = ex2_approx(mrow - mnew);
         const float base = m_use == -INFINITY ? 0.f : -m_use;         // a row that has seen nothing yet
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[kCols / 2];
+        // P, over the last tile's, which its P V has read then (o_done).
+        uint32_t pk[kKeep ? kChunks : 1][16];
+        auto p_free = [&]() -> bool {
+          if (!tree_wait(o_done, (R - 1) & 1, ctl)) return false;
+          tc_fence_after();
+          return true;
+        };
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-          float p0, p1;
-          fadd2(p0, p1, x[c], x[c + 1], base, base);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          const int e = (c >> 1) & 1;
-          fadd2(ps[2 * e], ps[2 * e + 1], ps[2 * e], ps[2 * e + 1], p0, p1);
-          pk[c / 2] = pack_bf16x2(p0, p1);
+        for (int k = 0; k < kChunks; ++k) {
+          float *y = x[kKeep ? k : k & 1];
+          if constexpr (!kKeep) {
+            tmem_wait_ld();
+            reg_fence<32>(reinterpret_cast<uint32_t *>(y));
+            if (k + 1 < kChunks) fetch(k + 1, x[(k + 1) & 1]);
+            else read_done();
+            ready(k, y);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float p0, p1;
+            fadd2(p0, p1, y[c], y[c + 1], base, base);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            const int e = (c >> 1) & 1;
+            fadd2(ps[2 * e], ps[2 * e + 1], ps[2 * e], ps[2 * e + 1], p0, p1);
+            pk[kKeep ? k : 0][c / 2] = pack_bf16x2(p0, p1);
+          }
+          if constexpr (!kKeep) {
+            if (k == 0 && !p_free()) {
+              tmem_wait_ld();                            // the next chunk's read is still in flight
+              return false;
+            }
+            tmem_st_x16(tPx + 16 * k, pk[0]);
+          }
         }
-        if (!tree_wait(o_done, (R - 1) & 1, ctl)) return false;
-        tc_fence_after();
-        if constexpr (kCols == 32) tmem_st_x16(tPx, pk);
-        if constexpr (kCols >= 64)
+        if constexpr (kKeep) {
+          if (!p_free()) return false;
 #pragma unroll
-          for (int c = 0; c < kCols / 2; c += 32) tmem_st_x32(tPx + c, pk + c);
+          for (int k = 0; k < kChunks; ++k) tmem_st_x16(tPx + 16 * k, pk[k]);
+        }
         if (rescale && !first) {
 #pragma unroll
           for (int c = 0; c < HD; c += 32) {
@@ -634,7 +686,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
         }
       }
       if (!ok) break;
-      if (have) load_rows(false);
+      if (kSplit > 1 && have) load_rows(false);
       // The piece's result: O and the LSE of a whole unit, else a record (its O not divided by
       // its sum).
       if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
