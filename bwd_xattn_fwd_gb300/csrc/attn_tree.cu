@@ -40,11 +40,11 @@ namespace {
 
 constexpr int kTreeThreads = 192;
 
-// K and V rings of one 128-position tile per slot. hd 32 and 64 take two CTAs an SM (256 TMEM
-// columns each), hd 128 one; the bytes are chosen so that no more fit.
+// K and V rings of one 128-position tile per slot. At hd 32 and 64 two CTAs fit an SM (256 TMEM
+// columns each; the bytes are chosen so that no more do), at hd 128 one.
 template <int HD>
 struct TreeLayout {
-  static constexpr int kCtas = HD == 128 ? 1 : 2;               // resident per SM
+  static constexpr int kCtas = HD == 128 ? 1 : 2;               // resident per SM that fit
   static constexpr int kSlots = HD == 32 ? 4 : 3;               // of K, and of V
   static constexpr uint32_t kRowBytes = HD * 2;
   static constexpr uint32_t kTileBytes = kTileRows * kRowBytes;
@@ -216,8 +216,18 @@ __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units
 
 // Record of a cut unit's piece: CTA c's piece that starts inside a unit is record 2c, the one
 // that starts it record 2c + 1. Layout: [records][rows][hd] O, then [records][rows] (max, sum).
+// CTAs an SM: with few rows two (where they fit), so that one streams while the other ends a
+// unit (B64 n16 hd 64: 46.8 us, one with twice the slots 48.4; n 1 over 1000 positions 38.7
+// against 52.3). A tile of 128 rows is bound by its softmax and wants the registers of one: a
+// row of 128 scores in the 168 registers of two spilled (B8 n64 hd 64 over 8192 positions:
+// 63.4 us, read from TMEM twice instead 55.7, one CTA 33.6).
 template <int HD, int kSplit>
-__global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
+constexpr int tree_ctas() {
+  return kSplit == 1 ? 1 : TreeLayout<HD>::kCtas;
+}
+
+template <int HD, int kSplit>
+__global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = TreeLayout<HD>;
   extern __shared__ uint8_t tree_smem_raw[];
@@ -452,8 +462,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       return tree_wait(meet, meets++ & 1, ctl);
     };
     // A piece's query row and word: into L2 while the piece before it runs, into registers
-    // before that piece's result is written (kSplit = 1, whose rows of 128 scores leave none:
-    // after it), and then put in place.
+    // before that piece's result is written (after it with kSplit = 1, whose rows of 128 scores
+    // leave none: hd 128 48.7 against 45.2 us), and then put in place.
     uint4 xq[HD / 8];
     unsigned long long word = 0;
     auto load_rows = [&](bool ahead) {
@@ -516,52 +526,26 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
       float mrow = -INFINITY, lrow = 0.f;
       // One tile: this copy's kCols columns. The masked form is compiled apart, so that the
       // tiles every row sees whole carry no mask. vis: a word per 32 columns.
-      // kSplit = 1 with two CTAs an SM: the columns come from TMEM 32 at a time and twice, for
-      // the maximum and for P. A row of 128 scores held in 168 registers spilled (B8 n64 hd 64
-      // over 8192 positions: 63.4 us, this way 55.7); where there are 255 (hd 128) or fewer
-      // columns the row stays in registers (hd 128: 46.2 us, read twice 50.6).
       auto step = [&](auto masked, const uint32_t *vis, bool first) -> bool {
-        constexpr int kChunks = kCols / 32;
-        constexpr bool kKeep = kSplit > 1 || HD == 128;
-        float x[kKeep ? kChunks : 2][32];
-        auto fetch = [&](int k, float *to) { tmem_ld_x32(tSx + 32 * k, reinterpret_cast<uint32_t *>(to)); };
-        // Scaled and masked scores (log2 domain) of chunk k.
-        auto ready = [&](int k, float *y) {
+        float x[kCols];
+        uint32_t *xr = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            fmul2(y[c], y[c + 1], y[c], y[c + 1], a.scale_log2, a.scale_log2);
-            if constexpr (decltype(masked)::value) {
-              if (((vis[k] >> c) & 1u) == 0u) y[c] = -INFINITY;
-              if (((vis[k] >> (c + 1)) & 1u) == 0u) y[c + 1] = -INFINITY;
-            }
-          }
-        };
-        auto read_done = [&]() {
-          tc_fence_before();
-          warp_arrive(s_free, lane);
-        };
+        for (int c = 0; c < kCols; c += 32) tmem_ld_x32(tSx + c, xr + c);
+        tmem_wait_ld();
+        reg_fence<kCols>(xr);
+        tc_fence_before();
+        warp_arrive(s_free, lane);
+        // Scaled scores (log2 domain) and their maximum.
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (kKeep) {
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) fetch(k, x[k]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) reg_fence<32>(reinterpret_cast<uint32_t *>(x[k]));
-          read_done();
-        } else {
-          fetch(0, x[0]);
-        }
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          float *y = x[kKeep ? k : k & 1];
-          if constexpr (!kKeep) {
-            tmem_wait_ld();
-            reg_fence<32>(reinterpret_cast<uint32_t *>(y));
-            fetch((k + 1) % kChunks, x[(k + 1) & 1]);    // behind the last chunk: the first again
+        for (int c = 0; c < kCols; c += 2) {
+          fmul2(x[c], x[c + 1], x[c], x[c + 1], a.scale_log2, a.scale_log2);
+          if constexpr (decltype(masked)::value) {
+            if (((vis[c >> 5] >> (c & 31)) & 1u) == 0u) x[c] = -INFINITY;
+            if (((vis[c >> 5] >> ((c + 1) & 31)) & 1u) == 0u) x[c + 1] = -INFINITY;
           }
-          ready(k, y);
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], y[c], y[c + 1]);
+          float &m = mx[(c >> 1) & 3];
+          m = fmax3(m, x[c], x[c + 1]);
         }
         const float mnew = fmax3(fmaxf(mrow, mx[0]), mx[1], fmaxf(mx[2], mx[3]));
         // O is rescaled only when some row's maximum grew by more than 2^8.
@@ -571,46 +555,22 @@ __global__ void __launch_bounds__(kTreeThreads, TreeLayout<HD>::kCtas)
         if (rescale && mnew > mrow) alpha = ex2_approx(mrow - mnew);
         const float base = m_use == -INFINITY ? 0.f : -m_use;         // a row that has seen nothing yet
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
-        // P, over the last tile's, which its P V has read then (o_done).
-        uint32_t pk[kKeep ? kChunks : 1][16];
-        auto p_free = [&]() -> bool {
-          if (!tree_wait(o_done, (R - 1) & 1, ctl)) return false;
-          tc_fence_after();
-          return true;
-        };
+        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          float *y = x[kKeep ? k : k & 1];
-          if constexpr (!kKeep) {
-            tmem_wait_ld();
-            reg_fence<32>(reinterpret_cast<uint32_t *>(y));
-            if (k + 1 < kChunks) fetch(k + 1, x[(k + 1) & 1]);
-            else read_done();
-            ready(k, y);
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float p0, p1;
-            fadd2(p0, p1, y[c], y[c + 1], base, base);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            const int e = (c >> 1) & 1;
-            fadd2(ps[2 * e], ps[2 * e + 1], ps[2 * e], ps[2 * e + 1], p0, p1);
-            pk[kKeep ? k : 0][c / 2] = pack_bf16x2(p0, p1);
-          }
-          if constexpr (!kKeep) {
-            if (k == 0 && !p_free()) {
-              tmem_wait_ld();                            // the next chunk's read is still in flight
-              return false;
-            }
-            tmem_st_x16(tPx + 16 * k, pk[0]);
-          }
+        for (int c = 0; c < kCols; c += 2) {
+          float p0, p1;
+          fadd2(p0, p1, x[c], x[c + 1], base, base);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          const int e = (c >> 1) & 1;
+          fadd2(ps[2 * e], ps[2 * e + 1], ps[2 * e], ps[2 * e + 1], p0, p1);
+          pk[c / 2] = pack_bf16x2(p0, p1);
         }
-        if constexpr (kKeep) {
-          if (!p_free()) return false;
+        // P over the last tile's, which its P V has read then.
+        if (!tree_wait(o_done, (R - 1) & 1, ctl)) return false;
+        tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) tmem_st_x16(tPx + 16 * k, pk[k]);
-        }
+        for (int c = 0; c < kCols / 2; c += 16) tmem_st_x16(tPx + c, pk + c);
         if (rescale && !first) {
 #pragma unroll
           for (int c = 0; c < HD; c += 32) {
@@ -893,8 +853,9 @@ int tree_tile_rows(int n, int nh, int nkv) {
   return rows <= 32 ? 32 : (rows <= 64 ? 64 : kTileRows);
 }
 
-// Runs are whole units when no sequence can have more tiles than this (see the head of the
-// file; TREE_WHOLE_MEASURED).
+// Runs are whole units when no sequence can have more tiles than this. At 1000 positions (8
+// tiles; n 8, hd 64, 4 kv heads) whole against cut units: 64 sequences 14.5 and 24.9 us; one
+// sequence 12.2 and 11.1 us on the GPU, 20.6 and 25.1 us with the host's part of a call.
 constexpr int kWholeTiles = 8;
 bool tree_whole(int page_size, int max_pages) {
   return static_cast<long long>(max_pages) * page_size <= kWholeTiles * kTileRows;
@@ -908,7 +869,7 @@ int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_page
   const int tile_rows = tree_tile_rows(n, nh, nkv);
   const long long row_tiles = (static_cast<long long>(n) * (nh / nkv) + tile_rows - 1) / tile_rows;
   const double most = static_cast<double>(tiles) * B * nkv * row_tiles;
-  const int resident = sms * (hd == 128 ? TreeLayout<128>::kCtas : TreeLayout<64>::kCtas);
+  const int resident = sms * (tile_rows == kTileRows || hd == 128 ? 1 : tree_ctas<64, 2>());
   return most < resident ? static_cast<int>(most) : resident;
 }
 
