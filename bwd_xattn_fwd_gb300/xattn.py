@@ -346,29 +346,33 @@ _tree_decode = _lib.xattn_tree_decode
 _append, _compact = _lib.xattn_cache_append, _lib.xattn_cache_compact
 
 
-def _refuse(name, t, shape, dtype, device):
-    """Says what is wrong with a tensor that is not as expected."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor, not {type(t).__name__}")
-    if device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    raise ValueError(f"{name} must be contiguous")
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
-def _check(device, tensors):
-    """Raises unless every (name, tensor, shape, dtype) is a contiguous tensor of that shape and
-    type on the GPU `device`."""
-    index = device.index if device.type == "cuda" else -1
+def _refuse(tensors):
+    """Raises what is wrong with the first of the (name, tensor, shape, dtype) that is not a
+    contiguous tensor of that shape and type on the first one's GPU."""
+    device = None
     for name, t, shape, dtype in tensors:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
-                and t.shape == shape) or index < 0:
-            _refuse(name, t, shape, dtype, device)
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor, not {type(t).__name__}")
+        device = device or t.device
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a CUDA tensor, not on {t.device}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("inconsistent tensors")
+
+
+def _fits(t, shape, dtype, index):
+    """A contiguous tensor of this shape and type on GPU `index`."""
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
 
 
 class _Elsewhere:
@@ -394,33 +398,32 @@ _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _window_dims(q, k, v):
-    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported q: {getattr(q, 'dtype', type(q))}")
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be [B,S,nh,hd] and k, v [B,S,nkv,hd]")
-    B, S, nh, hd = q.shape
-    nkv = k.shape[2]
-    kv = (B, S, nkv, hd)
-    return B, S, nh, nkv, hd, (("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype))
+def _four(**tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a tensor of four dimensions")
 
 
 def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
     """(o, lse) of causal attention in which query i sees key j only if i - j < window or
     j < sinks; tensors as for attention_fwd (bf16 or fp32)."""
-    B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
-    device = q.device
-    _check(device, tensors)
-    if stream is not None or _current_device() != device.index:
-        with _Elsewhere(device, stream):
+    _four(q=q, k=k)
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    B, S, nh, hd = shape
+    nkv = k.shape[2]
+    kv = (B, S, nkv, hd)
+    if not (index >= 0 and (dtype is _BF16 or dtype is _F32) and q.is_contiguous() and _fits(k, kv, dtype, index)
+            and _fits(v, kv, dtype, index)):
+        _refuse((("q", q, shape, dtype if dtype in (_BF16, _F32) else _BF16), ("k", k, kv, dtype), ("v", v, kv, dtype)))
+    if stream is not None or _current_device() != index:
+        with _Elsewhere(q.device, stream):
             return attention_window_fwd(q, k, v, window, sinks, scale)
     scale = hd ** -0.5 if scale is None else float(scale)
-    window, sinks = min(window, NO_WINDOW), min(sinks, NO_WINDOW)
     o = torch.empty_like(q)
-    lse = torch.empty((B, S, nh), dtype=torch.float32, device=device)
-    fn = _window_fwd if q.dtype is torch.bfloat16 else _window_fwd_f32
-    rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, nh, nkv, hd, window, sinks, scale, o.data_ptr(),
-            lse.data_ptr(), _raw_stream(device.index))
+    lse = torch.empty((B, S, nh), dtype=_F32, device=q.device)
+    rc = (_window_fwd if dtype is _BF16 else _window_fwd_f32)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, nh, nkv, hd, min(window, NO_WINDOW), min(sinks, NO_WINDOW),
+        scale, o.data_ptr(), lse.data_ptr(), _raw_stream(index))
     if rc:
         raise XattnError(rc, "attention_window_fwd")
     return o, lse
@@ -429,36 +432,47 @@ def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
 def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, stream=None, deterministic=False):
     """(dq, dk, dv) for the tensors of attention_window_fwd and the output gradient dO.
     deterministic (bf16): dQ bit-reproducible as well, from a second recompute."""
-    B, S, nh, nkv, hd, tensors = _window_dims(q, k, v)
-    device, dtype = q.device, q.dtype
-    _check(device, (*tensors, ("o", o, q.shape, dtype), ("dO", dO, q.shape, dtype),
-                    ("lse", lse, (B, S, nh), torch.float32)))
-    if stream is not None or _current_device() != device.index:
-        with _Elsewhere(device, stream):
+    _four(q=q, k=k)
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    B, S, nh, hd = shape
+    nkv = k.shape[2]
+    kv, rows = (B, S, nkv, hd), (B, S, nh)
+    if not (index >= 0 and (dtype is _BF16 or dtype is _F32) and q.is_contiguous() and _fits(k, kv, dtype, index)
+            and _fits(v, kv, dtype, index) and _fits(o, shape, dtype, index) and _fits(dO, shape, dtype, index)
+            and _fits(lse, rows, _F32, index)):
+        _refuse((("q", q, shape, dtype if dtype in (_BF16, _F32) else _BF16), ("k", k, kv, dtype), ("v", v, kv, dtype),
+                 ("o", o, shape, dtype), ("dO", dO, shape, dtype), ("lse", lse, rows, _F32)))
+    if stream is not None or _current_device() != index:
+        with _Elsewhere(q.device, stream):
             return attention_window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic=deterministic)
     scale = hd ** -0.5 if scale is None else float(scale)
-    window, sinks = min(window, NO_WINDOW), min(sinks, NO_WINDOW)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(), B, S, nh, nkv,
-            hd, window, sinks, scale)
-    outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _raw_stream(device.index))
-    rc = (_window_bwd(*args, 1 if deterministic else 0, *outs) if dtype is torch.bfloat16
-          else _window_bwd_f32(*args, *outs))
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(), B, S, nh, nkv, hd,
+            min(window, NO_WINDOW), min(sinks, NO_WINDOW), scale)
+    outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _raw_stream(index))
+    rc = _window_bwd(*args, 1 if deterministic else 0, *outs) if dtype is _BF16 else _window_bwd_f32(*args, *outs)
     if rc:
         raise XattnError(rc, "attention_window_bwd")
     return dq, dk, dv
 
 
 def _pool(k_pages, v_pages, page_table, ctx_lens):
-    """Sizes of a paged cache, and its tensors to check."""
-    if k_pages.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("k_pages, v_pages must be [num_pages,page_size,nkv,hd] and page_table [B,max_pages]")
+    """Sizes of a paged cache ([num_pages,page_size,nkv,hd] pools, [B,max_pages] table, [B]
+    lengths), its GPU, and whether its tensors fit each other."""
+    _four(k_pages=k_pages)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a tensor [B,max_pages]")
+    shape, index = k_pages.shape, k_pages.get_device()
     B, max_pages = page_table.shape
-    shape = k_pages.shape
-    return B, max_pages, shape, (("k_pages", k_pages, shape, torch.bfloat16),
-                                 ("v_pages", v_pages, shape, torch.bfloat16),
-                                 ("page_table", page_table, (B, max_pages), torch.int32),
-                                 ("ctx_lens", ctx_lens, (B,), torch.int32))
+    fits = (index >= 0 and k_pages.dtype is _BF16 and k_pages.is_contiguous() and _fits(v_pages, shape, _BF16, index)
+            and page_table.dtype is _I32 and page_table.get_device() == index and page_table.is_contiguous()
+            and _fits(ctx_lens, (B,), _I32, index))
+    return B, max_pages, shape, index, fits
+
+
+def _pool_names(k_pages, v_pages, page_table, ctx_lens):
+    return (("k_pages", k_pages, k_pages.shape, _BF16), ("v_pages", v_pages, k_pages.shape, _BF16),
+            ("page_table", page_table, page_table.shape, _I32), ("ctx_lens", ctx_lens, page_table.shape[:1], _I32))
 
 
 def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, window=None, sinks=0, scale=None,
@@ -469,26 +483,22 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
     ctx_lens .. ctx_lens + n - 1 (cache_append). tree [B,n] (int64): bit j of word i lets token
     i see new token j; None: token i sees new tokens 0 .. i (n = 1: the decode step). window
     (None: no window) and sinks as in attention_window_fwd."""
-    B, max_pages, (num_pages, page_size, nkv, hd), tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
-    if q.dim() != 4:
-        raise ValueError("q must be [B,n,nh,hd]")
+    B, max_pages, (num_pages, page_size, nkv, hd), index, fits = _pool(k_pages, v_pages, page_table, ctx_lens)
+    _four(q=q)
     n, nh = q.shape[1], q.shape[2]
-    device = q.device
-    _check(device, (("q", q, (B, n, nh, hd), torch.bfloat16), *tensors))
-    words = None
-    if tree is not None:
-        _check(device, (("tree", tree, (B, n), torch.int64),))
-        words = tree.data_ptr()
-    if stream is not None or _current_device() != device.index:
-        with _Elsewhere(device, stream):
+    if not (fits and _fits(q, (B, n, nh, hd), _BF16, index) and (tree is None or _fits(tree, (B, n), _I64, index))):
+        _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("q", q, (B, n, nh, hd), _BF16),
+                 *([] if tree is None else [("tree", tree, (B, n), _I64)])))
+    if stream is not None or _current_device() != index:
+        with _Elsewhere(q.device, stream):
             return attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window, sinks, scale)
     scale = hd ** -0.5 if scale is None else float(scale)
-    window, sinks = NO_WINDOW if window is None else min(window, NO_WINDOW), min(sinks, NO_WINDOW)
     o = torch.empty_like(q)
-    lse = torch.empty((B, n, nh), dtype=torch.float32, device=device)
+    lse = torch.empty((B, n, nh), dtype=_F32, device=q.device)
     rc = _tree_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                      ctx_lens.data_ptr(), words, B, n, nh, nkv, hd, num_pages, page_size, max_pages, window, sinks,
-                      scale, o.data_ptr(), lse.data_ptr(), _raw_stream(device.index))
+                      ctx_lens.data_ptr(), None if tree is None else tree.data_ptr(), B, n, nh, nkv, hd, num_pages,
+                      page_size, max_pages, NO_WINDOW if window is None else min(window, NO_WINDOW),
+                      min(sinks, NO_WINDOW), scale, o.data_ptr(), lse.data_ptr(), _raw_stream(index))
     if rc:
         raise XattnError(rc, "attention_tree_decode")
     return o, lse
@@ -497,17 +507,18 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
 def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=None):
     """Writes the rows k_new, v_new [B,n,nkv,hd] to positions ctx_lens .. ctx_lens + n - 1 of each
     sequence's pages (in place)."""
-    B, max_pages, (num_pages, page_size, nkv, hd), tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
-    if k_new.dim() != 4:
-        raise ValueError("k_new and v_new must be [B,n,nkv,hd]")
+    B, max_pages, (num_pages, page_size, nkv, hd), index, fits = _pool(k_pages, v_pages, page_table, ctx_lens)
+    _four(k_new=k_new)
     n = k_new.shape[1]
-    device, rows = k_pages.device, (B, n, nkv, hd)
-    _check(device, (*tensors, ("k_new", k_new, rows, torch.bfloat16), ("v_new", v_new, rows, torch.bfloat16)))
-    if stream is not None or _current_device() != device.index:
-        with _Elsewhere(device, stream):
+    rows = (B, n, nkv, hd)
+    if not (fits and _fits(k_new, rows, _BF16, index) and _fits(v_new, rows, _BF16, index)):
+        _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("k_new", k_new, rows, _BF16),
+                 ("v_new", v_new, rows, _BF16)))
+    if stream is not None or _current_device() != index:
+        with _Elsewhere(k_pages.device, stream):
             return cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens)
     rc = _append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                 ctx_lens.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(device.index))
+                 ctx_lens.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(index))
     if rc:
         raise XattnError(rc, "cache_append")
 
@@ -515,16 +526,17 @@ def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=No
 def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream=None):
     """Moves the rows of positions ctx_lens + path[:, i], i < accepted, down to ctx_lens + i (in
     place): path [B,n] (int32, ascending over its accepted entries), accepted [B] (int32)."""
-    B, max_pages, (num_pages, page_size, nkv, hd), tensors = _pool(k_pages, v_pages, page_table, ctx_lens)
-    if path.dim() != 2:
-        raise ValueError("path must be [B,n]")
+    B, max_pages, (num_pages, page_size, nkv, hd), index, fits = _pool(k_pages, v_pages, page_table, ctx_lens)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be a tensor [B,n]")
     n = path.shape[1]
-    device = k_pages.device
-    _check(device, (*tensors, ("path", path, (B, n), torch.int32), ("accepted", accepted, (B,), torch.int32)))
-    if stream is not None or _current_device() != device.index:
-        with _Elsewhere(device, stream):
+    if not (fits and _fits(path, (B, n), _I32, index) and _fits(accepted, (B,), _I32, index)):
+        _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("path", path, (B, n), _I32),
+                 ("accepted", accepted, (B,), _I32)))
+    if stream is not None or _current_device() != index:
+        with _Elsewhere(k_pages.device, stream):
             return cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted)
     rc = _compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
-                  accepted.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(device.index))
+                  accepted.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(index))
     if rc:
         raise XattnError(rc, "cache_compact")
