@@ -1236,19 +1236,29 @@ cudaError_t launch_bwd_main_bf16(const CUtensorMap &mq, const CUtensorMap &mk,
 }
 
 // A sink tile's walk is cut into parts of as many query tiles as a key tile of the window
-// meets (at least 4), so that no unit is longer than the others.
-WindowSplit window_bwd_split(int S, int window, int sinks) {
+// meets (at least 4), so that no unit is longer than the others (B8 S2048 8 heads on 2,
+// window 512: the main kernel takes 304 units of 20 iterations, 2 a CTA; uncut the sink tiles'
+// units would have 64) -- but into no more than kSinkUnits units over all heads: many sink
+// tiles, or many heads, are parallel enough, and the parts' sums stay below 160 MB.
+constexpr int kSinkUnits = 1216;   // 8 per SM
+WindowSplit window_bwd_split(int B, int S, int nkv, int window, int sinks) {
   const int num_m = (S + kTileRows - 1) / kTileRows;
   WindowSplit w;
   w.sink_tiles = window_sink_tiles(sinks);
   const int meets = (window + kTileRows - 2) / kTileRows + 1;
   w.part_tiles = meets < 4 ? 4 : meets;
   w.nparts = (num_m + w.part_tiles - 1) / w.part_tiles;
+  const long long tiles = static_cast<long long>(B) * nkv * w.sink_tiles;
+  const long long most = tiles < kSinkUnits && tiles > 0 ? kSinkUnits / tiles : 1;
+  if (w.nparts > most) {
+    w.part_tiles = static_cast<int>((num_m + most - 1) / most);
+    w.nparts = (num_m + w.part_tiles - 1) / w.part_tiles;
+  }
   return w;
 }
 
 size_t window_parts_bytes(int B, int S, int nkv, int hd, int window, int sinks) {
-  const WindowSplit w = window_bwd_split(S, window, sinks);
+  const WindowSplit w = window_bwd_split(B, S, nkv, window, sinks);
   if (w.nparts == 1) return 0;
   return static_cast<size_t>(B) * nkv * w.sink_tiles * w.nparts * 2 * kTileRows * hd * sizeof(float);
 }
@@ -1258,7 +1268,7 @@ cudaError_t launch_window_bwd_main_bf16(const CUtensorMap &mq, const CUtensorMap
                                         __nv_bfloat16 *dk, __nv_bfloat16 *dv, int B, int S, int nh, int nkv, int hd,
                                         float scale, int window, int sinks, float *parts, int *status,
                                         uint64_t timeout_ns, cudaStream_t stream) {
-  const WindowSplit w = window_bwd_split(S, window, sinks);
+  const WindowSplit w = window_bwd_split(B, S, nkv, window, sinks);
   const WinArgs win{window, sinks, w.nparts, w.part_tiles, parts};
   const CUtensorMap &md = mdq ? *mdq : maux;
 #define XATTN_WIN_MAIN(HD, FUSED, DSTMEM)                                                                            \

@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       for (int x = 0; x < 8; ++x) pg[x] = __shfl_sync(0xffffffffu, page, x);
       const int rw = __shfl_sync(0xffffffffu, row, 0);
       const uint32_t box_bytes = box_rows * L::kAtomBytes;
+      XATTN_DCHECK(kvh < a.nkv && page >= 0 && page <= a.num_pages && row >= 0 && row + box_rows <= a.page_size &&
+                       boxes <= 8 && dst >= sK && dst + L::kTileBytes <= smem_u32(smem + L::kBars),
+                   a.status);
       if (elect_one()) {
 #pragma unroll
         for (int x = 0; x < 8; ++x)
@@ -599,6 +602,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
         if (!tree_wait(v_full(slot), (R / L::kSlots) & 1, ctl) || !tree_wait(s_full, R & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         const unsigned held = pages[slot];
+        XATTN_DCHECK(t0 >= 0 && t0 < s.end && s.end <= a.max_pages * a.page_size, a.status);
         // Positions that some row does not see: new ones, those behind a window, missing pages.
         const bool edge = t0 + kTileRows > s.ctx || held != all_boxes ||
                           (t0 <= s.end - 1 - a.window && t0 + kTileRows > a.sinks);
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       tc_fence_after();
       const bool whole = e0 == 0 && e1 == s.count;
       const size_t rec = (2 * static_cast<size_t>(blockIdx.x) + (e0 == 0 ? 1 : 0)) * a.rec_rows + row;
-      XATTN_DCHECK(rec / a.rec_rows < 2 * static_cast<size_t>(gridDim.x) && rows <= a.rec_rows, a.status);
+      XATTN_DCHECK(!mine || (rec < 2 * static_cast<size_t>(gridDim.x) * a.rec_rows && rows <= a.rec_rows), a.status);
       const int rho = row0 + row;
       const size_t out = (static_cast<size_t>(b) * a.n + rho / group) * a.nh + static_cast<size_t>(kvh) * group + rho % group;
       // Copies beyond the first hand their O (kPart columns at a time) and statistics to the
@@ -711,6 +715,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
               }
           }
         }
+        XATTN_DCHECK(!mine || out < static_cast<size_t>(a.B) * a.n * a.nh, a.status);
+        XATTN_DCHECK(kSplit == 1 || copy == 0 || piece(lane_row - kRows, kPieces - 1) < 96 * kPieces, a.status);
         if (mine && copy == 0) {
           if (whole) {
             const float inv = sum > 0.f ? 1.f / sum : 0.f;

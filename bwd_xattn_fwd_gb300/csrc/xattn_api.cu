@@ -242,7 +242,7 @@ xattn_status check_pages(int B, int n, int nkv, int hd, int num_pages, int page_
       n > static_cast<long long>(max_pages) * page_size)
     return XATTN_ERR_PAGES;
   // Element offsets stay inside int64, grids inside int32.
-  if (static_cast<double>(num_pages) * page_size * nkv * hd > 0x1p60 ||
+  if (static_cast<double>(nkv) * hd > 0x1p30 || static_cast<double>(num_pages) * page_size * nkv * hd > 0x1p60 ||
       static_cast<double>(B) * n * nkv * hd > 0x1p38 || static_cast<double>(B) * max_pages > 0x1p40)
     return XATTN_ERR_BAD_SHAPE;
   return XATTN_OK;

@@ -143,7 +143,7 @@ cudaError_t launch_bwd_f32(const float *q, const float *k, const float *v, const
 struct WindowSplit {
   int sink_tiles, nparts, part_tiles;
 };
-WindowSplit window_bwd_split(int S, int window, int sinks);
+WindowSplit window_bwd_split(int B, int S, int nkv, int window, int sinks);
 size_t window_parts_bytes(int B, int S, int nkv, int hd, int window, int sinks);
 cudaError_t launch_window_fwd_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                    __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, int hd, float scale,

@@ -36,6 +36,9 @@
  *   - A kernel that waits on an on-chip barrier longer than a bounded time (about
  *     two seconds) gives up, records XATTN_ERR_DEVICE_TIMEOUT in a device status word
  *     and finishes; xattn_check_device_status reports it.
+ *   - Scratch is stream-ordered: taken on `stream` and released on it when the call's work
+ *     is enqueued. The window, tree and fp32 window calls take it from a memory pool of the
+ *     library's own (one per device), which keeps what it has grown to until the process ends.
  *   - CUDA graphs: the calls may be captured on a stream and replayed, once the device
  *     has seen one ordinary call (the first call on a device looks up its device
  *     status word; make that call outside the capture). Entry points that take

@@ -61,6 +61,8 @@ SHAPES = [
     (3, 2100, 12, 12, 32, 500, 4),
     (2, 4000, 4, 1, 64, 256, 4),       # sink tiles cut into many parts
     (1, 3500, 8, 2, 128, 150, 130),
+    (1, 5000, 2, 1, 64, 40, 1500),     # many sink tiles
+    (40, 700, 8, 8, 32, 30, 200),      # many heads: sink tiles uncut
 ]
 
 
