@@ -490,10 +490,11 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       for (int c = 0; c < HD / 8; ++c) xq[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
       word = !mine ? 0 : (a.tree ? __ldg(a.tree + at) : (2ull << token) - 1);   // (not used here: no wait)
     };
+    // Nothing for the combine until the run's end says otherwise (a run that gives up says
+    // nothing).
+    if (!a.whole && warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
     bool have = walk_piece(walk, a, units);
-    if (have) {
-      if (kSplit > 1) load_rows(false);
-    } else if (!a.whole && warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (kSplit > 1 && have) load_rows(false);
     while (ok && have) {
       const Sight s = walk.s;
       const int b = walk.b, e0 = walk.e0, e1 = walk.e1;
@@ -506,8 +507,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       // A run that ends inside the unit it started last says so to the combine.
       if (!have && !a.whole && warp == 2 && lane == 0) {
         const long long start = walk.stop - (e1 - e0);
-        const bool cut = e0 == 0 && e1 < s.count;
-        a.plan[blockIdx.x] = make_int4(b, unit, cut ? static_cast<int>(run_of(length, runs, start + s.count - 1)) : 0, cut);
+        if (e0 == 0 && e1 < s.count)
+          a.plan[blockIdx.x] = make_int4(b, unit, static_cast<int>(run_of(length, runs, start + s.count - 1)), 1);
       }
       const int rows = min(rows_all - row0, kRows);
       const bool live = kSplit > 1 || quarter * 32 < rows;    // the warp has a row

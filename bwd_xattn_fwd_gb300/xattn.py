@@ -16,7 +16,10 @@ import ctypes
 import enum
 import os
 
-import torch
+try:
+    import torch
+except ImportError:      # the C entry points take raw addresses and stream handles without it
+    torch = None
 
 from . import build as _build
 
@@ -346,7 +349,7 @@ _tree_decode = _lib.xattn_tree_decode
 _append, _compact = _lib.xattn_cache_append, _lib.xattn_cache_compact
 
 
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_BF16, _F32, _I32, _I64 = (torch.bfloat16, torch.float32, torch.int32, torch.int64) if torch else (None,) * 4
 
 
 def _refuse(tensors):
@@ -394,8 +397,8 @@ class _Elsewhere:
         return False
 
 
-_current_device = torch.cuda.current_device
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The handle of a device's current stream, without the Stream object around it (2 us less).
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
 
 
 def _four(**tensors):
@@ -415,7 +418,7 @@ def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
     if not (index >= 0 and (dtype is _BF16 or dtype is _F32) and q.is_contiguous() and _fits(k, kv, dtype, index)
             and _fits(v, kv, dtype, index)):
         _refuse((("q", q, shape, dtype if dtype in (_BF16, _F32) else _BF16), ("k", k, kv, dtype), ("v", v, kv, dtype)))
-    if stream is not None or _current_device() != index:
+    if stream is not None or torch.cuda.current_device() != index:
         with _Elsewhere(q.device, stream):
             return attention_window_fwd(q, k, v, window, sinks, scale)
     scale = hd ** -0.5 if scale is None else float(scale)
@@ -442,7 +445,7 @@ def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, strea
             and _fits(lse, rows, _F32, index)):
         _refuse((("q", q, shape, dtype if dtype in (_BF16, _F32) else _BF16), ("k", k, kv, dtype), ("v", v, kv, dtype),
                  ("o", o, shape, dtype), ("dO", dO, shape, dtype), ("lse", lse, rows, _F32)))
-    if stream is not None or _current_device() != index:
+    if stream is not None or torch.cuda.current_device() != index:
         with _Elsewhere(q.device, stream):
             return attention_window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic=deterministic)
     scale = hd ** -0.5 if scale is None else float(scale)
@@ -489,7 +492,7 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
     if not (fits and _fits(q, (B, n, nh, hd), _BF16, index) and (tree is None or _fits(tree, (B, n), _I64, index))):
         _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("q", q, (B, n, nh, hd), _BF16),
                  *([] if tree is None else [("tree", tree, (B, n), _I64)])))
-    if stream is not None or _current_device() != index:
+    if stream is not None or torch.cuda.current_device() != index:
         with _Elsewhere(q.device, stream):
             return attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window, sinks, scale)
     scale = hd ** -0.5 if scale is None else float(scale)
@@ -514,7 +517,7 @@ def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=No
     if not (fits and _fits(k_new, rows, _BF16, index) and _fits(v_new, rows, _BF16, index)):
         _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("k_new", k_new, rows, _BF16),
                  ("v_new", v_new, rows, _BF16)))
-    if stream is not None or _current_device() != index:
+    if stream is not None or torch.cuda.current_device() != index:
         with _Elsewhere(k_pages.device, stream):
             return cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens)
     rc = _append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
@@ -533,7 +536,7 @@ def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream
     if not (fits and _fits(path, (B, n), _I32, index) and _fits(accepted, (B,), _I32, index)):
         _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("path", path, (B, n), _I32),
                  ("accepted", accepted, (B,), _I32)))
-    if stream is not None or _current_device() != index:
+    if stream is not None or torch.cuda.current_device() != index:
         with _Elsewhere(k_pages.device, stream):
             return cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted)
     rc = _compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),

@@ -65,6 +65,12 @@ def test_backward_checks(lib, name):
         assert _bwd(lib, lse=98) == 5
 
 
+def test_status_strings_of_the_new_codes(lib):
+    lib.xattn_status_string.restype = ctypes.c_char_p
+    texts = {lib.xattn_status_string(code).decode() for code in (0, 12, 13, 14)}
+    assert len(texts) == 4 and "unknown xattn status" not in texts
+
+
 def test_accepted_sizes_reach_the_device(lib):
     if not torch.cuda.is_available():
         assert _fwd(lib, window=0x7FFFFFFF, sinks=0x7FFFFFFF) == 6
