@@ -4,16 +4,22 @@ Each .cu file compiles in parallel to an object; the objects link into one share
 library with the CUDA runtime linked statically (so the library loads on a machine
 without a GPU driver; the driver is reached at the first CUDA call).
 
+csrc/xattn_torch.cpp, the native part of the binding's tensor-level calls, compiles beside them
+against the installed torch (its file carries torch's version: another torch builds another).
+
 `--debug` (build(debug=True)) builds the same library with XATTN_DEBUG -- on-device bounds
 checks that report XATTN_ERR_DEVICE_BOUNDS -- into _build_debug/ (load it by pointing
 XATTN_LIBRARY at it).
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -33,6 +39,37 @@ def nvcc() -> str:
     if not os.path.exists(cand):
         raise RuntimeError("nvcc not found (needed to build libxattn)")
     return cand
+
+
+TORCH_SRC = os.path.join(CSRC, "xattn_torch.cpp")
+
+
+def torch_dir():
+    """Where torch is installed (found without importing it), or None."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def torch_lib() -> str:
+    """The native part of the tensor-level calls for the installed torch ("" without torch)."""
+    return os.path.join(BUILD, f"xattn_torch-{importlib.metadata.version('torch')}.so") if torch_dir() else ""
+
+
+def _torch_current() -> bool:
+    lib = torch_lib()
+    if not lib:
+        return True
+    deps = (TORCH_SRC, os.path.join(INCLUDE, "xattn.h"))
+    return os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps)
+
+
+def _torch_command(out: str):
+    t = torch_dir()
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-I{INCLUDE}",
+            f"-I{os.path.join(t, 'include')}", f"-I{os.path.join(t, 'include', 'torch', 'csrc', 'api', 'include')}",
+            f"-I{os.path.join(cuda, 'include')}", f"-I{sysconfig.get_paths()['include']}", TORCH_SRC, "-o", out,
+            f"-L{os.path.join(t, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def sources():
@@ -55,13 +92,20 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     build_dir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     if debug:
         extra = (*extra, "-DXATTN_DEBUG")
-    if not force and up_to_date(lib):
+    torch_tmp = ""
+    procs = []
+    if force or not _torch_current():
+        os.makedirs(BUILD, exist_ok=True)
+        torch_tmp = torch_lib() + f".tmp{os.getpid()}"
+        procs.append((TORCH_SRC, subprocess.Popen(_torch_command(torch_tmp), stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
+    current = not force and up_to_date(lib)
+    if current and not procs:
         return lib
     os.makedirs(build_dir, exist_ok=True)
     nv = nvcc()
-    procs = []
     objs = []
-    for src in sources():
+    for src in [] if current else sources():
         obj = os.path.join(build_dir, os.path.basename(src)[:-3] + ".o")
         cmd = [nv, *ARCH, *CFLAGS, *extra, "-c", src, "-o", obj]
         if verbose:
@@ -78,7 +122,11 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
             print(text, flush=True)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"the compiler failed:\n{msg}")
+    if torch_tmp:
+        os.replace(torch_tmp, torch_lib())
+    if current:
+        return lib
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nv, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs]
     if verbose:

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import importlib.util
 import os
 
 try:
@@ -337,52 +338,31 @@ def attention_decode(q, k_cache, v_cache, scale=None, stream=None):
     return o, lse
 
 
-# ---- tensor-level helpers that check their tensors ---------------------------------------
-#
-# Small calls are bound by the host: these helpers look the C functions up once, pass
-# pointers themselves, and make a device or stream current only when that is needed (a decode
-# step's append: 13.0 us through the generic wrappers, 9 us this way).
+# ---- tensor-level calls that check their tensors (csrc/xattn_torch.cpp) ------------------
 
-_window_fwd, _window_fwd_f32 = _lib.xattn_window_fwd, _lib.xattn_window_fwd_f32
-_window_bwd, _window_bwd_f32 = _lib.xattn_window_bwd, _lib.xattn_window_bwd_f32
-_tree_decode = _lib.xattn_tree_decode
-_append, _compact = _lib.xattn_cache_append, _lib.xattn_cache_compact
-
-
-_BF16, _F32, _I32, _I64 = (torch.bfloat16, torch.float32, torch.int32, torch.int64) if torch else (None,) * 4
-
-
-def _refuse(tensors):
-    """Raises what is wrong with the first of the (name, tensor, shape, dtype) that is not a
-    contiguous tensor of that shape and type on the first one's GPU."""
-    device = None
-    for name, t, shape, dtype in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a tensor, not {type(t).__name__}")
-        device = device or t.device
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be a CUDA tensor, not on {t.device}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, {tensors[0][0]} on {device}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    raise ValueError("inconsistent tensors")
+def _load_calls():
+    """The native part of the calls below, bound to this library's entry points."""
+    path = _build.torch_lib()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built: run `python bwd_xattn_fwd_gb300/build.py` first")
+    spec = importlib.util.spec_from_file_location("xattn_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
+                  ("xattn_window_fwd", "xattn_window_fwd_f32", "xattn_window_bwd", "xattn_window_bwd_f32",
+                   "xattn_tree_decode", "xattn_cache_append", "xattn_cache_compact")))
+    return module
 
 
-def _fits(t, shape, dtype, index):
-    """A contiguous tensor of this shape and type on GPU `index`."""
-    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+_calls = _load_calls() if torch else None
 
 
 class _Elsewhere:
-    """Makes `device` current, and the given stream (a torch stream, a raw handle, or None: the
-    device's current one) the one that torch allocates on and that calls launch on."""
+    """Makes a tensor's device current, and the given stream (a torch stream, a raw handle, or
+    None: the device's current one) the one that torch allocates on and that calls launch on."""
 
-    def __init__(self, device, stream):
+    def __init__(self, t, stream):
+        device = t.device
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         self._guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
@@ -397,85 +377,78 @@ class _Elsewhere:
         return False
 
 
-# The handle of a device's current stream, without the Stream object around it (2 us less).
-_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+def _again(name, status, call, where, stream, tensors):
+    """What a native call that returned no outputs asks for: raises its status; or, when the
+    tensors do not fit, says what is wrong with the first that does not; or, when they are
+    all on another device than the current one, makes that one current and calls again."""
+    if status is not None:
+        raise XattnError(status, name)
+    device = None
+    for label, t, shape, dtype in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: {label} must be a tensor, not {type(t).__name__}")
+        device = device or t.device
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: {label}: expected {dtype}, got {t.dtype}")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}: {label} must be a CUDA tensor, not on {t.device}")
+        if t.device != device:
+            raise ValueError(f"{name}: {label} is on {t.device}, {tensors[0][0]} on {device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {label}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: {label} must be contiguous")
+    if torch.cuda.current_device() == device.index:
+        raise ValueError(f"{name}: a dimension is beyond 2^31 - 1")
+    with _Elsewhere(where, stream):
+        return call()
 
 
-def _four(**tensors):
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{name} must be a tensor of four dimensions")
+def _need_dims(name, **tensors):
+    for label, (t, dims) in tensors.items():
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name}: {label} must be a tensor of {dims} dimensions")
 
 
 def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
     """(o, lse) of causal attention in which query i sees key j only if i - j < window or
     j < sinks; tensors as for attention_fwd (bf16 or fp32)."""
-    _four(q=q, k=k)
-    shape, dtype, index = q.shape, q.dtype, q.get_device()
-    B, S, nh, hd = shape
-    nkv = k.shape[2]
-    kv = (B, S, nkv, hd)
-    if not (index >= 0 and (dtype is _BF16 or dtype is _F32) and q.is_contiguous() and _fits(k, kv, dtype, index)
-            and _fits(v, kv, dtype, index)):
-        _refuse((("q", q, shape, dtype if dtype in (_BF16, _F32) else _BF16), ("k", k, kv, dtype), ("v", v, kv, dtype)))
-    if stream is not None or torch.cuda.current_device() != index:
-        with _Elsewhere(q.device, stream):
+    if stream is not None:
+        with _Elsewhere(q, stream):
             return attention_window_fwd(q, k, v, window, sinks, scale)
-    scale = hd ** -0.5 if scale is None else float(scale)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, S, nh), dtype=_F32, device=q.device)
-    rc = (_window_fwd if dtype is _BF16 else _window_fwd_f32)(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, nh, nkv, hd, min(window, NO_WINDOW), min(sinks, NO_WINDOW),
-        scale, o.data_ptr(), lse.data_ptr(), _raw_stream(index))
-    if rc:
-        raise XattnError(rc, "attention_window_fwd")
-    return o, lse
+    out = _calls.window_fwd(q, k, v, window, sinks, scale)
+    if type(out) is tuple:
+        return out
+    name = "attention_window_fwd"
+    _need_dims(name, q=(q, 4), k=(k, 4))
+    kv, dtype = (*q.shape[:2], k.shape[2], q.shape[3]), q.dtype if q.dtype == torch.float32 else torch.bfloat16
+    return _again(name, out, lambda: attention_window_fwd(q, k, v, window, sinks, scale), q, None,
+                  (("q", q, q.shape, dtype), ("k", k, kv, dtype), ("v", v, kv, dtype)))
 
 
 def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, stream=None, deterministic=False):
     """(dq, dk, dv) for the tensors of attention_window_fwd and the output gradient dO.
     deterministic (bf16): dQ bit-reproducible as well, from a second recompute."""
-    _four(q=q, k=k)
-    shape, dtype, index = q.shape, q.dtype, q.get_device()
-    B, S, nh, hd = shape
-    nkv = k.shape[2]
-    kv, rows = (B, S, nkv, hd), (B, S, nh)
-    if not (index >= 0 and (dtype is _BF16 or dtype is _F32) and q.is_contiguous() and _fits(k, kv, dtype, index)
-            and _fits(v, kv, dtype, index) and _fits(o, shape, dtype, index) and _fits(dO, shape, dtype, index)
-            and _fits(lse, rows, _F32, index)):
-        _refuse((("q", q, shape, dtype if dtype in (_BF16, _F32) else _BF16), ("k", k, kv, dtype), ("v", v, kv, dtype),
-                 ("o", o, shape, dtype), ("dO", dO, shape, dtype), ("lse", lse, rows, _F32)))
-    if stream is not None or torch.cuda.current_device() != index:
-        with _Elsewhere(q.device, stream):
+    if stream is not None:
+        with _Elsewhere(q, stream):
             return attention_window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic=deterministic)
-    scale = hd ** -0.5 if scale is None else float(scale)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dO.data_ptr(), lse.data_ptr(), B, S, nh, nkv, hd,
-            min(window, NO_WINDOW), min(sinks, NO_WINDOW), scale)
-    outs = (dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _raw_stream(index))
-    rc = _window_bwd(*args, 1 if deterministic else 0, *outs) if dtype is _BF16 else _window_bwd_f32(*args, *outs)
-    if rc:
-        raise XattnError(rc, "attention_window_bwd")
-    return dq, dk, dv
+    out = _calls.window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic)
+    if type(out) is tuple:
+        return out
+    name = "attention_window_bwd"
+    _need_dims(name, q=(q, 4), k=(k, 4))
+    kv, dtype = (*q.shape[:2], k.shape[2], q.shape[3]), q.dtype if q.dtype == torch.float32 else torch.bfloat16
+    return _again(name, out, lambda: attention_window_bwd(q, k, v, o, dO, lse, window, sinks, scale,
+                                                          deterministic=deterministic), q, None,
+                  (("q", q, q.shape, dtype), ("k", k, kv, dtype), ("v", v, kv, dtype), ("o", o, q.shape, dtype),
+                   ("dO", dO, q.shape, dtype), ("lse", lse, q.shape[:3], torch.float32)))
 
 
-def _pool(k_pages, v_pages, page_table, ctx_lens):
-    """Sizes of a paged cache ([num_pages,page_size,nkv,hd] pools, [B,max_pages] table, [B]
-    lengths), its GPU, and whether its tensors fit each other."""
-    _four(k_pages=k_pages)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be a tensor [B,max_pages]")
-    shape, index = k_pages.shape, k_pages.get_device()
-    B, max_pages = page_table.shape
-    fits = (index >= 0 and k_pages.dtype is _BF16 and k_pages.is_contiguous() and _fits(v_pages, shape, _BF16, index)
-            and page_table.dtype is _I32 and page_table.get_device() == index and page_table.is_contiguous()
-            and _fits(ctx_lens, (B,), _I32, index))
-    return B, max_pages, shape, index, fits
-
-
-def _pool_names(k_pages, v_pages, page_table, ctx_lens):
-    return (("k_pages", k_pages, k_pages.shape, _BF16), ("v_pages", v_pages, k_pages.shape, _BF16),
-            ("page_table", page_table, page_table.shape, _I32), ("ctx_lens", ctx_lens, page_table.shape[:1], _I32))
+def _pool(name, k_pages, v_pages, page_table, ctx_lens):
+    _need_dims(name, k_pages=(k_pages, 4), page_table=(page_table, 2))
+    return (("k_pages", k_pages, k_pages.shape, torch.bfloat16), ("v_pages", v_pages, k_pages.shape, torch.bfloat16),
+            ("page_table", page_table, page_table.shape, torch.int32),
+            ("ctx_lens", ctx_lens, page_table.shape[:1], torch.int32))
 
 
 def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, window=None, sinks=0, scale=None,
@@ -486,60 +459,52 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
     ctx_lens .. ctx_lens + n - 1 (cache_append). tree [B,n] (int64): bit j of word i lets token
     i see new token j; None: token i sees new tokens 0 .. i (n = 1: the decode step). window
     (None: no window) and sinks as in attention_window_fwd."""
-    B, max_pages, (num_pages, page_size, nkv, hd), index, fits = _pool(k_pages, v_pages, page_table, ctx_lens)
-    _four(q=q)
-    n, nh = q.shape[1], q.shape[2]
-    if not (fits and _fits(q, (B, n, nh, hd), _BF16, index) and (tree is None or _fits(tree, (B, n), _I64, index))):
-        _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("q", q, (B, n, nh, hd), _BF16),
-                 *([] if tree is None else [("tree", tree, (B, n), _I64)])))
-    if stream is not None or torch.cuda.current_device() != index:
-        with _Elsewhere(q.device, stream):
+    if stream is not None:
+        with _Elsewhere(q, stream):
             return attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window, sinks, scale)
-    scale = hd ** -0.5 if scale is None else float(scale)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, n, nh), dtype=_F32, device=q.device)
-    rc = _tree_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                      ctx_lens.data_ptr(), None if tree is None else tree.data_ptr(), B, n, nh, nkv, hd, num_pages,
-                      page_size, max_pages, NO_WINDOW if window is None else min(window, NO_WINDOW),
-                      min(sinks, NO_WINDOW), scale, o.data_ptr(), lse.data_ptr(), _raw_stream(index))
-    if rc:
-        raise XattnError(rc, "attention_tree_decode")
-    return o, lse
+    out = _calls.tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window, sinks, scale)
+    if type(out) is tuple:
+        return out
+    name = "attention_tree_decode"
+    tensors = _pool(name, k_pages, v_pages, page_table, ctx_lens)
+    _need_dims(name, q=(q, 4))
+    B, n = page_table.shape[0], q.shape[1]
+    return _again(name, out, lambda: attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window,
+                                                           sinks, scale), q, None,
+                  (*tensors, ("q", q, (B, n, q.shape[2], k_pages.shape[3]), torch.bfloat16),
+                   *([] if tree is None else [("tree", tree, (B, n), torch.int64)])))
 
 
 def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=None):
     """Writes the rows k_new, v_new [B,n,nkv,hd] to positions ctx_lens .. ctx_lens + n - 1 of each
     sequence's pages (in place)."""
-    B, max_pages, (num_pages, page_size, nkv, hd), index, fits = _pool(k_pages, v_pages, page_table, ctx_lens)
-    _four(k_new=k_new)
-    n = k_new.shape[1]
-    rows = (B, n, nkv, hd)
-    if not (fits and _fits(k_new, rows, _BF16, index) and _fits(v_new, rows, _BF16, index)):
-        _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("k_new", k_new, rows, _BF16),
-                 ("v_new", v_new, rows, _BF16)))
-    if stream is not None or torch.cuda.current_device() != index:
-        with _Elsewhere(k_pages.device, stream):
+    if stream is not None:
+        with _Elsewhere(k_pages, stream):
             return cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens)
-    rc = _append(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                 ctx_lens.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(index))
-    if rc:
-        raise XattnError(rc, "cache_append")
+    out = _calls.cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens)
+    if out is True:
+        return None
+    name = "cache_append"
+    tensors = _pool(name, k_pages, v_pages, page_table, ctx_lens)
+    _need_dims(name, k_new=(k_new, 4))
+    rows = (page_table.shape[0], k_new.shape[1], *k_pages.shape[2:])
+    return _again(name, out, lambda: cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens), k_pages, None,
+                  (*tensors, ("k_new", k_new, rows, torch.bfloat16), ("v_new", v_new, rows, torch.bfloat16)))
 
 
 def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream=None):
     """Moves the rows of positions ctx_lens + path[:, i], i < accepted, down to ctx_lens + i (in
     place): path [B,n] (int32, ascending over its accepted entries), accepted [B] (int32)."""
-    B, max_pages, (num_pages, page_size, nkv, hd), index, fits = _pool(k_pages, v_pages, page_table, ctx_lens)
-    if not isinstance(path, torch.Tensor) or path.dim() != 2:
-        raise ValueError("path must be a tensor [B,n]")
-    n = path.shape[1]
-    if not (fits and _fits(path, (B, n), _I32, index) and _fits(accepted, (B,), _I32, index)):
-        _refuse((*_pool_names(k_pages, v_pages, page_table, ctx_lens), ("path", path, (B, n), _I32),
-                 ("accepted", accepted, (B,), _I32)))
-    if stream is not None or torch.cuda.current_device() != index:
-        with _Elsewhere(k_pages.device, stream):
+    if stream is not None:
+        with _Elsewhere(k_pages, stream):
             return cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted)
-    rc = _compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
-                  accepted.data_ptr(), B, n, nkv, hd, num_pages, page_size, max_pages, _raw_stream(index))
-    if rc:
-        raise XattnError(rc, "cache_compact")
+    out = _calls.cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted)
+    if out is True:
+        return None
+    name = "cache_compact"
+    tensors = _pool(name, k_pages, v_pages, page_table, ctx_lens)
+    _need_dims(name, path=(path, 2))
+    B = page_table.shape[0]
+    return _again(name, out, lambda: cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted), k_pages,
+                  None, (*tensors, ("path", path, (B, path.shape[1]), torch.int32),
+                         ("accepted", accepted, (B,), torch.int32)))

@@ -323,3 +323,49 @@ def test_explicit_streams_by_object_and_handle():
         o, lse = xattn.attention_tree_decode(q, k, v, tb, ln, stream=stream)
         side.synchronize()
         assert torch.equal(o, ref) and torch.equal(lse, rl)
+
+
+def test_tensors_that_do_not_fit_are_refused_and_nothing_is_written():
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nh, nkv, hd, page, lens = 2, 4, 4, 2, 64, 16, [100, 60]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=2, device="cuda")
+    q, tb, ln = _q(B, n, nh, hd, 1), _i32(table), _i32(lens)
+    words = torch.ones(B, n, dtype=torch.int64, device="cuda")
+    call = xattn.attention_tree_decode
+    for bad in ((q.float(), k, v, tb, ln), (q, k.half(), v, tb, ln), (q, k, v, tb.long(), ln), (q, k, v, tb, ln.float()),
+                ("q", k, v, tb, ln)):
+        with pytest.raises((TypeError, ValueError)):
+            call(*bad)
+    for bad in ((q[:1], k, v, tb, ln), (q, k, v[:-1], tb, ln), (q, k, v, tb, ln[:1]), (q.cpu(), k, v, tb, ln),
+                (q, k, v, tb.cpu(), ln), (q[..., ::2], k, v, tb, ln), (q.transpose(1, 2), k, v, tb, ln),
+                (q, k, v, tb[:, ::2], ln), (q[0], k, v, tb, ln), (q, k[0], v, tb, ln)):
+        with pytest.raises(ValueError):
+            call(*bad)
+    with pytest.raises(ValueError):
+        call(q, k, v, tb, ln, tree=words[:, :2])
+    with pytest.raises(TypeError):
+        call(q, k, v, tb, ln, tree=words.int())
+    with pytest.raises(xattn.XattnError) as err:
+        call(q, k, v, tb, ln, window=3)                               # a window that ends inside the tree
+    assert err.value.status == xattn.Status.ERR_WINDOW
+    with pytest.raises(xattn.XattnError) as err:
+        call(q[:, :, :3].contiguous(), k, v, tb, ln)
+    assert err.value.status == xattn.Status.ERR_GROUP
+    with pytest.raises(xattn.XattnError) as err:
+        call(q, k, v, tb, ln, scale=float("nan"))
+    assert err.value.status == xattn.Status.ERR_BAD_SCALE
+    before = k.clone(), v.clone()
+    new = torch.zeros(B, n, nkv, hd, dtype=torch.bfloat16, device="cuda")
+    for bad in ((new.float(), new), (new, new[:, :2]), (new[..., :32], new[..., :32]), (new.cpu(), new)):
+        with pytest.raises((TypeError, ValueError)):
+            xattn.cache_append(*bad, k, v, tb, ln)
+    path, acc = _i32([[0, 1, 2, 3]] * B), _i32([1, 1])
+    for bad in ((path.long(), acc), (path, acc[:1]), (path[:, ::2], acc), (path[0], acc), (path.cpu(), acc)):
+        with pytest.raises((TypeError, ValueError)):
+            xattn.cache_compact(k, v, tb, ln, *bad)
+    with pytest.raises(xattn.XattnError) as err:                      # more rows than the table holds
+        xattn.cache_append(*(torch.zeros(B, 500, nkv, hd, dtype=torch.bfloat16, device="cuda"),) * 2, k, v, tb, ln)
+    assert err.value.status == xattn.Status.ERR_PAGES
+    torch.cuda.synchronize()
+    assert torch.equal(k.view(torch.int16), before[0].view(torch.int16))
+    assert torch.equal(v.view(torch.int16), before[1].view(torch.int16))
