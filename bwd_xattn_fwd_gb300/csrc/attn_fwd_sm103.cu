@@ -115,6 +115,101 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
 }
 
+// One key step of a windowed tile that some row does not see whole: the diagonal, the tiles at
+// the window's far edge, sink tiles behind it. The row sees columns far .. near and 0 .. sk; a
+// chunk of 32 columns that no row of the warp sees costs nothing, and a row may see nothing of
+// the tile, or nothing yet (m = -inf). The scores are read from TMEM chunk by chunk, once for
+// the maximum and once for P. A function of its own and a loop over the chunks on purpose: as
+// a second copy of the row step inside the caller it took registers from the loop over the
+// whole tiles (B4 S4096 16 heads on 4, hd 64, window 4096: 168 us, this way EDGE_FULL; window
+// 1024 with 4 sinks: 99 and EDGE_1024).
+struct EdgeRow {
+  float m, l;      // the row's running maximum (log2 domain) and sum
+  bool ok;
+};
+template <int HD, bool kNegScale>
+__device__ __noinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint32_t tP, uint32_t s_full,
+                                                 uint32_t s_free, uint32_t p_full, uint32_t o_done, int gx, bool first,
+                                                 int far, int near, int sk, float scale_log2, float m, float l,
+                                                 const WaitCtl ctl) {
+  if (!warp_wait(s_full, gx & 1, ctl)) return {m, l, false};
+  tc_fence_after();
+  constexpr float kFill = kNegScale ? INFINITY : -INFINITY;
+  float mx[2] = {kFill, kFill};
+#pragma unroll 1
+  for (int cc = 0; cc < 4; ++cc) {
+    const uint32_t vis = bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc);
+    if (!__any_sync(0xffffffffu, vis != 0u)) continue;
+    uint32_t r[32];
+    tmem_ld_x32(tS + 32 * cc, r);
+    tmem_wait_ld();
+    reg_fence<32>(r);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const float v0 = (vis >> c) & 1u ? __uint_as_float(r[c]) : kFill;
+      const float v1 = (vis >> (c + 1)) & 1u ? __uint_as_float(r[c + 1]) : kFill;
+      float &a = mx[(c >> 1) & 1];
+      a = kNegScale ? fmin3(a, v0, v1) : fmax3(a, v0, v1);
+    }
+  }
+  // (-inf x 0 would be NaN, which fmaxf drops.)
+  const float mnew = fmaxf(m, (kNegScale ? fminf(mx[0], mx[1]) : fmaxf(mx[0], mx[1])) * scale_log2);
+  const bool rescale = __any_sync(0xffffffffu, mnew > m + 8.0f);
+  const float m_use = rescale ? mnew : m;
+  const float alpha = rescale && mnew > m ? ex2_approx(m - mnew) : 1.f;
+  const float neg_m = m_use == -INFINITY ? 0.f : -m_use;
+  // P over the last tile's, which its P V has read then.
+  if (!warp_wait(o_done, (gx - 1) & 1, ctl)) return {m, l, false};
+  tc_fence_after();
+  float ps[4] = {0.f, 0.f, 0.f, 0.f};   // (in the row step's order: a diagonal tile gives its bits)
+#pragma unroll 1
+  for (int cc = 0; cc < 4; ++cc) {
+    const uint32_t vis = bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc);
+    uint32_t pk[16];
+    if (__any_sync(0xffffffffu, vis != 0u)) {
+      uint32_t r[32];
+      tmem_ld_x32(tS + 32 * cc, r);
+      tmem_wait_ld();
+      reg_fence<32>(r);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float x0, x1;
+        ffma2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), scale_log2, scale_log2, neg_m, neg_m);
+        const float p0 = (vis >> c) & 1u ? ex2_approx(x0) : 0.f, p1 = (vis >> (c + 1)) & 1u ? ex2_approx(x1) : 0.f;
+        const int e = c & 2;
+        fadd2(ps[e], ps[e + 1], ps[e], ps[e + 1], p0, p1);
+        pk[c / 2] = pack_bf16x2(p0, p1);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) pk[c] = 0u;
+    }
+    if (cc == 3) {                       // the scores are read
+      tc_fence_before();
+      mbar_arrive(s_free);
+    }
+    // At hd = 128 P lies over the scores of chunks read by now (chunk cc's over columns
+    // 16 cc .. 16 cc + 15).
+    tmem_st_x16(tP + 16 * cc, pk);
+  }
+  if (rescale && !first) {
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 32) {
+      uint32_t ov[32];
+      tmem_ld_x32(tO + c, ov);
+      tmem_wait_ld();
+      reg_fence<32>(ov);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+      tmem_st_x32(tO + c, ov);
+    }
+  }
+  tmem_wait_st();
+  tc_fence_before();
+  mbar_arrive(p_full);
+  return {m_use, l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3])), true};
+}
+
 // kNegScale: scale < 0, so the row maximum of the scaled scores is the scaled minimum of
 // the raw ones.
 // kWin: query i sees key j <= i only if i - j < window or j < sinks. A unit then walks a
@@ -442,26 +537,10 @@ __global__ void __maxnreg__(168)
       // are wholly visible, chunk q is masked per lane (key column > row), chunks above q
       // are wholly masked (P = 0 without exponentials); q is warp-uniform, so each chunk
       // takes one branch-free path.
-      // With a window the masked copy also takes the tiles at the window's far edge and the
-      // sink tiles behind it. vis: the row's visible columns, a word per 32-column chunk;
-      // per chunk the warp takes the unmasked path (every row sees all 32), no path (P = 0,
-      // no row sees any) or the masked one, and a row may see nothing of a whole tile.
-      auto step = [&](auto masked, int n, bool first) -> bool {
+      // (With a window this step takes the tiles that every row sees whole, window_edge_step the
+      // others.)
+      auto step = [&](auto masked, bool first) -> bool {
         constexpr bool kDiag = decltype(masked)::value;
-        uint32_t vis[4] = {};
-        if constexpr (kWin && kDiag) {
-          const int far = (mX - n) * kTileRows + row - window + 1;   // first column in the window
-          const int near = n == mX ? row : kTileRows - 1, sk = min(sinks - n * kTileRows - 1, near);
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
-            vis[cc] = bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc);
-        }
-        // Chunk cc of this warp's rows: 0 none visible, 1 all, 2 mixed.
-        auto kind = [&](int cc) {
-          if constexpr (kWin && kDiag)
-            return __all_sync(0xffffffffu, vis[cc] == 0xffffffffu) ? 1 : __any_sync(0xffffffffu, vis[cc] != 0u) ? 2 : 0;
-          return (!kDiag || cc < quarter) ? 1 : (cc == quarter ? 2 : 0);
-        };
         if (!warp_wait(s_full(x), gx & 1, ctl)) return false;
         tc_fence_after();
         // The whole row of S_X(n) comes into registers with one TMEM read, and the buffer
@@ -477,17 +556,13 @@ __global__ void __maxnreg__(168)
         // (scale >= 0) or their scaled minimum (scale < 0); masked columns do not count.
         constexpr float kFill = kNegScale ? INFINITY : -INFINITY;
         float mx4[4] = {kFill, kFill, kFill, kFill};
-        auto hidden = [&](int c) {
-          if constexpr (kWin) return ((vis[c >> 5] >> (c & 31)) & 1u) == 0u;
-          return c > row;
-        };
         auto max_chunk = [&](auto mask_chunk, int c32) {
 #pragma unroll
           for (int c = c32; c < c32 + 32; c += 2) {
             float v0 = __uint_as_float(r[c]), v1 = __uint_as_float(r[c + 1]);
             if (decltype(mask_chunk)::value) {
-              if (hidden(c)) v0 = kFill;
-              if (hidden(c + 1)) v1 = kFill;
+              if (c > row) v0 = kFill;
+              if (c + 1 > row) v1 = kFill;
             }
             float &a = mx4[(c >> 1) & 3];
             a = kNegScale ? fmin3(a, v0, v1) : fmax3(a, v0, v1);
@@ -495,9 +570,8 @@ __global__ void __maxnreg__(168)
         };
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
-          const int kc = kind(cc);
-          if (kc == 1) max_chunk(std::false_type{}, 32 * cc);
-          else if (kc == 2) max_chunk(std::true_type{}, 32 * cc);
+          if (!kDiag || cc < quarter) max_chunk(std::false_type{}, 32 * cc);
+          else if (cc == quarter) max_chunk(std::true_type{}, 32 * cc);
         }
         const float mx = (kNegScale ? fmin3(mx4[0], mx4[1], fminf(mx4[2], mx4[3]))
                                     : fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]))) * scale_log2;
@@ -511,7 +585,6 @@ __global__ void __maxnreg__(168)
         // exponentials on the shared unit).
         float alpha = 1.f;
         if (rescale) alpha = ex2_approx(mrow - mnew);
-        if (kWin && mnew == -INFINITY) alpha = 1.f;   // a row that has seen no key yet
         const float neg_m = -m_use;
         // Exponents, the causal mask on them (-inf -> exact zeros for any scale, 0
         // included), the exponentials, row sums and bf16 P, packed in place into r[0, 64).
@@ -530,8 +603,8 @@ __global__ void __maxnreg__(168)
             ffma2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), scale_log2, scale_log2,
                   neg_m, neg_m);
             if (decltype(mask_chunk)::value) {
-              if (hidden(c)) x0 = -INFINITY;
-              if (hidden(c + 1)) x1 = -INFINITY;
+              if (c > row) x0 = -INFINITY;
+              if (c + 1 > row) x1 = -INFINITY;
             }
             float p0, p1;
             if (!kDiag && !decltype(mask_chunk)::value && (e & 7) == 7) {
@@ -546,10 +619,9 @@ __global__ void __maxnreg__(168)
           }
         };
         auto chunk = [&](int cc) {
-          const int kc = kind(cc);
-          if (kc == 1) {
+          if (!kDiag || cc < quarter) {
             exp_chunk(std::false_type{}, 32 * cc);
-          } else if (kc == 2) {
+          } else if (cc == quarter) {
             exp_chunk(std::true_type{}, 32 * cc);
           } else {
 #pragma unroll
@@ -585,26 +657,36 @@ __global__ void __maxnreg__(168)
         return true;
       };
       if constexpr (kWin) {
-        const int n_end = (x == 0 && hasB) ? count - 1 : count;
-        bool first = true;
+        // This tile's key tiles: those of sinks behind its window, then lo .. mX. The tiles that
+        // some row below S does not see whole go through window_edge_step.
+        const int lo = x == 0 ? loA : loB, sunk = min(sink_tiles, lo);
+        const int start = sunk > 0 ? 0 : lo;
+        int n = start;
 #pragma unroll 1
-        for (int i = 0; i < n_end; ++i) {
-          if (x == 1 && i == skip) continue;
-          const int n = i < heads ? i : i - heads + loA;
-          // Some row below S of the tile does not see some key of tile n.
-          const bool edge = n == mX || (min(mX * kTileRows + kTileRows, S) - n * kTileRows > window &&
-                                        (n + 1) * kTileRows > sinks);
-          if (!(edge ? step(std::true_type{}, n, first) : step(std::false_type{}, n, first))) { ok = false; break; }
-          first = false;
+        while (n <= mX) {
+          if (n == mX || (min(mX * kTileRows + kTileRows, S) - n * kTileRows > window && (n + 1) * kTileRows > sinks)) {
+            const int near = n == mX ? row : kTileRows - 1;
+            const EdgeRow e = window_edge_step<HD, kNegScale>(
+                tSx, tOx, tPx, s_full(x), s_free(x), p_full(x), o_done(x), gx, n == start,
+                (mX - n) * kTileRows + row - window + 1, near, min(sinks - n * kTileRows - 1, near), scale_log2, mrow,
+                lrow, ctl);
+            mrow = e.m;
+            lrow = e.l;
+            ok = e.ok;
+          } else {
+            ok = step(std::false_type{}, n == start);
+          }
+          if (!ok) break;
           ++gx;
+          n = n + 1 == sunk ? lo : n + 1;
         }
       } else {
 #pragma unroll 1
         for (int n = 0; n < mX; ++n, ++gx) {
-          if (!step(std::false_type{}, n, n == 0)) { ok = false; break; }
+          if (!step(std::false_type{}, n == 0)) { ok = false; break; }
         }
         if (ok) {
-          if (!step(std::true_type{}, mX, mX == 0)) ok = false;
+          if (!step(std::true_type{}, mX == 0)) ok = false;
           ++gx;
         }
       }
