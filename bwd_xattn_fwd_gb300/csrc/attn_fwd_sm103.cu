@@ -439,11 +439,21 @@ __global__ void __maxnreg__(168)
     // is the tile's only user (tile mB when there is a tile B; every tile when there is
     // not). An issuer never arrives for a tile it does not use, so its arrivals cannot
     // land in an earlier phase of the stage that the other issuer has not released yet.
+    // With a window the two sides differ in more tiles, and either may be the slower one: each
+    // passes the tiles that it does not use as well, waiting for them and releasing them, so
+    // every tile has one release from each side and no side's wait for a stage can fall two
+    // phases behind (a barrier tells only its last two apart).
     // R: ring index of the unit's key tile 0; gx: this tile's key steps over all units.
     bool ok = true;
     int units = 0, unitsx = 0;
     auto ring_stage = [](int r) { return r % kFwdStages; };
     auto ring_phase = [](int r) { return static_cast<uint32_t>((r / kFwdStages) & 1); };
+    auto pass_tile = [&](int r) -> bool {
+      if (!warp_wait(full(ring_stage(r)), ring_phase(r), ctl)) return false;
+      if (elect_one()) mbar_arrive(empty(ring_stage(r)));
+      __syncwarp();
+      return true;
+    };
 #pragma unroll 1
     for (int k = 0, R = 0, gx = 0; ok; ++k) {
       const int u = unit_at(k);
@@ -464,7 +474,7 @@ __global__ void __maxnreg__(168)
         const int n0 = (kWin && skip_x == 0) ? 1 : 0;
         const int n_end = kWin ? (x == 0 && hasB ? count - 1 : count) : mX + 1;
         auto after = [skip_x](int n) { return (kWin && n + 1 == skip_x) ? n + 2 : n + 1; };
-        if (kWin && n0 == 1) ok = warp_wait(full(ring_stage(R)), ring_phase(R), ctl);
+        if (kWin && n0 == 1) ok = pass_tile(R);
         ok = ok && warp_wait(full(ring_stage(R + n0)), ring_phase(R + n0), ctl) &&
              warp_wait(s_free(x), (gx - 1) & 1, ctl);
         if (!ok) break;
@@ -474,14 +484,8 @@ __global__ void __maxnreg__(168)
 #pragma unroll 1
         for (int n = n0; n < n_end; n = after(n), ++gx) {
           const int n1 = after(n);
-          // A tile this side does not use still has to land before the next wait on its
-          // stage: a barrier tells only its last two phases apart.
-          if (kWin && n1 == n + 2 && !warp_wait(full(ring_stage(R + n + 1)), ring_phase(R + n + 1), ctl)) {
-            ok = false;
-            break;
-          }
-          const bool shared_tile = kWin ? (x == 0 ? hasB && n != skip : n + 1 < count)
-                                        : (x == 0 ? hasB : n <= mA);
+          if (kWin && n1 == n + 2 && !pass_tile(R + n + 1)) { ok = false; break; }
+          const bool shared_tile = kWin || (x == 0 ? hasB : n <= mA);
           if constexpr (!L::kAliasP) {
             if (n1 < n_end) {
               if (!warp_wait(s_free(x), gx & 1, ctl) ||
@@ -504,10 +508,12 @@ __global__ void __maxnreg__(168)
             }
           }
         }
-        if (kWin && ok && x == 0 && hasB)
-          ok = warp_wait(full(ring_stage(R + count - 1)), ring_phase(R + count - 1), ctl);
+        if (kWin && ok && x == 0 && hasB) ok = pass_tile(R + count - 1);
         if (!ok) break;
         ++unitsx;
+      } else if constexpr (kWin) {
+        for (int n = 0; ok && n < count; ++n) ok = pass_tile(R + n);
+        if (!ok) break;
       }
       if (elect_one()) mma_commit(mma_final(qb));  // covers every MMA of this unit
       __syncwarp();
