@@ -135,21 +135,31 @@ __device__ __noinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint3
   if (!warp_wait(s_full, gx & 1, ctl)) return {m, l, false};
   tc_fence_after();
   constexpr float kFill = kNegScale ? INFINITY : -INFINITY;
-  float mx[2] = {kFill, kFill};
-#pragma unroll 1
-  for (int cc = 0; cc < 4; ++cc) {
-    const uint32_t vis = bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc);
-    if (!__any_sync(0xffffffffu, vis != 0u)) continue;
-    uint32_t r[32];
-    tmem_ld_x32(tS + 32 * cc, r);
+  auto vis_of = [&](int cc) { return bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc); };
+  // Chunk cc in r[cc & 1], the next one on its way.
+  uint32_t r[2][32];
+  auto fetch = [&](int cc, uint32_t *to) { tmem_ld_x32(tS + 32 * cc, to); };
+  auto landed = [](uint32_t *to) {
     tmem_wait_ld();
-    reg_fence<32>(r);
+    reg_fence<32>(to);
+  };
+  float mx[2] = {kFill, kFill};
+  fetch(0, r[0]);
+#pragma unroll 1
+  for (int c2 = 0; c2 < 4; c2 += 2) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float v0 = (vis >> c) & 1u ? __uint_as_float(r[c]) : kFill;
-      const float v1 = (vis >> (c + 1)) & 1u ? __uint_as_float(r[c + 1]) : kFill;
-      float &a = mx[(c >> 1) & 1];
-      a = kNegScale ? fmin3(a, v0, v1) : fmax3(a, v0, v1);
+    for (int h = 0; h < 2; ++h) {
+      landed(r[h]);
+      fetch((c2 + h + 1) & 3, r[h ^ 1]);               // behind the last chunk: the first again, for P
+      const uint32_t vis = vis_of(c2 + h);
+      if (!__any_sync(0xffffffffu, vis != 0u)) continue;
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const float v0 = (vis >> c) & 1u ? __uint_as_float(r[h][c]) : kFill;
+        const float v1 = (vis >> (c + 1)) & 1u ? __uint_as_float(r[h][c + 1]) : kFill;
+        float &a = mx[(c >> 1) & 1];
+        a = kNegScale ? fmin3(a, v0, v1) : fmax3(a, v0, v1);
+      }
     }
   }
   // (-inf x 0 would be NaN, which fmaxf drops.)
@@ -158,39 +168,45 @@ __device__ __noinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint3
   const float m_use = rescale ? mnew : m;
   const float alpha = rescale && mnew > m ? ex2_approx(m - mnew) : 1.f;
   const float neg_m = m_use == -INFINITY ? 0.f : -m_use;
-  // P over the last tile's, which its P V has read then.
-  if (!warp_wait(o_done, (gx - 1) & 1, ctl)) return {m, l, false};
-  tc_fence_after();
   float ps[4] = {0.f, 0.f, 0.f, 0.f};   // (in the row step's order: a diagonal tile gives its bits)
 #pragma unroll 1
-  for (int cc = 0; cc < 4; ++cc) {
-    const uint32_t vis = bit_range(far - 32 * cc, near - 32 * cc) | bit_range(0, sk - 32 * cc);
-    uint32_t pk[16];
-    if (__any_sync(0xffffffffu, vis != 0u)) {
-      uint32_t r[32];
-      tmem_ld_x32(tS + 32 * cc, r);
-      tmem_wait_ld();
-      reg_fence<32>(r);
+  for (int c2 = 0; c2 < 4; c2 += 2) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float x0, x1;
-        ffma2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), scale_log2, scale_log2, neg_m, neg_m);
-        const float p0 = (vis >> c) & 1u ? ex2_approx(x0) : 0.f, p1 = (vis >> (c + 1)) & 1u ? ex2_approx(x1) : 0.f;
-        const int e = c & 2;
-        fadd2(ps[e], ps[e + 1], ps[e], ps[e + 1], p0, p1);
-        pk[c / 2] = pack_bf16x2(p0, p1);
+    for (int h = 0; h < 2; ++h) {
+      landed(r[h]);
+      if (h == 0 || c2 == 0) {
+        fetch(c2 + h + 1, r[h ^ 1]);
+      } else {                             // the scores are read
+        tc_fence_before();
+        mbar_arrive(s_free);
       }
-    } else {
+      const uint32_t vis = vis_of(c2 + h);
+      uint32_t pk[16];
+      if (__any_sync(0xffffffffu, vis != 0u)) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) pk[c] = 0u;
+        for (int c = 0; c < 32; c += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]), scale_log2, scale_log2, neg_m, neg_m);
+          const float p0 = (vis >> c) & 1u ? ex2_approx(x0) : 0.f, p1 = (vis >> (c + 1)) & 1u ? ex2_approx(x1) : 0.f;
+          const int e = c & 2;
+          fadd2(ps[e], ps[e + 1], ps[e], ps[e + 1], p0, p1);
+          pk[c / 2] = pack_bf16x2(p0, p1);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) pk[c] = 0u;
+      }
+      // P over the last tile's, which its P V has read then. (At hd = 128 P lies over the scores
+      // of chunks read by now: chunk cc's over columns 16 cc .. 16 cc + 15.)
+      if (c2 + h == 0) {
+        if (!warp_wait(o_done, (gx - 1) & 1, ctl)) {
+          tmem_wait_ld();                  // the next chunk's read is still in flight
+          return {m, l, false};
+        }
+        tc_fence_after();
+      }
+      tmem_st_x16(tP + 16 * (c2 + h), pk);
     }
-    if (cc == 3) {                       // the scores are read
-      tc_fence_before();
-      mbar_arrive(s_free);
-    }
-    // At hd = 128 P lies over the scores of chunks read by now (chunk cc's over columns
-    // 16 cc .. 16 cc + 15).
-    tmem_st_x16(tP + 16 * cc, pk);
   }
   if (rescale && !first) {
 #pragma unroll 1
