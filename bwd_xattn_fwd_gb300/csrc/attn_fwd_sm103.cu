@@ -679,28 +679,33 @@ __global__ void __maxnreg__(168)
         return true;
       };
       if constexpr (kWin) {
-        // This tile's key tiles: those of sinks behind its window, then lo .. mX. The tiles that
-        // some row below S does not see whole go through window_edge_step.
+        // This tile's key tiles: those of sinks behind its window, then lo .. mX. Tiles whole ..
+        // mX - 1 are those that every row below S sees whole; window_edge_step takes the others.
         const int lo = x == 0 ? loA : loB, sunk = min(sink_tiles, lo);
         const int start = sunk > 0 ? 0 : lo;
-        int n = start;
+        const int whole = max(lo, (min(mX * kTileRows + kTileRows, S) - window + kTileRows - 1) / kTileRows);
+        auto edge = [&](int n) -> bool {
+          const int near = n == mX ? row : kTileRows - 1;
+          const EdgeRow e = window_edge_step<HD, kNegScale>(
+              tSx, tOx, tPx, s_full(x), s_free(x), p_full(x), o_done(x), gx, n == start,
+              (mX - n) * kTileRows + row - window + 1, near, min(sinks - n * kTileRows - 1, near), scale_log2, mrow,
+              lrow, ctl);
+          mrow = e.m;
+          lrow = e.l;
+          return e.ok;
+        };
 #pragma unroll 1
-        while (n <= mX) {
-          if (n == mX || (min(mX * kTileRows + kTileRows, S) - n * kTileRows > window && (n + 1) * kTileRows > sinks)) {
-            const int near = n == mX ? row : kTileRows - 1;
-            const EdgeRow e = window_edge_step<HD, kNegScale>(
-                tSx, tOx, tPx, s_full(x), s_free(x), p_full(x), o_done(x), gx, n == start,
-                (mX - n) * kTileRows + row - window + 1, near, min(sinks - n * kTileRows - 1, near), scale_log2, mrow,
-                lrow, ctl);
-            mrow = e.m;
-            lrow = e.l;
-            ok = e.ok;
-          } else {
-            ok = step(std::false_type{}, n == start);
-          }
-          if (!ok) break;
+        for (int n = start; n < min(whole, mX); n = n + 1 == sunk ? lo : n + 1, ++gx) {
+          if (!edge(n)) { ok = false; break; }
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int n = whole; n < mX; ++n, ++gx) {
+          if (!step(std::false_type{}, n == start)) { ok = false; break; }
+        }
+        if (ok) {
+          if (!edge(mX)) ok = false;
           ++gx;
-          n = n + 1 == sunk ? lo : n + 1;
         }
       } else {
 #pragma unroll 1
