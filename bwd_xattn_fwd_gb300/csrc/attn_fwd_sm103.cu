@@ -119,16 +119,16 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
 // the window's far edge, sink tiles behind it. The row sees columns far .. near and 0 .. sk; a
 // chunk of 32 columns that no row of the warp sees costs nothing, and a row may see nothing of
 // the tile, or nothing yet (m = -inf). The scores are read from TMEM chunk by chunk, once for
-// the maximum and once for P. A function of its own and a loop over the chunks on purpose: as
-// a second copy of the row step inside the caller it took registers from the loop over the
-// whole tiles (B4 S4096 16 heads on 4, hd 64, window 4096: 168 us, this way EDGE_FULL; window
-// 1024 with 4 sinks: 99 and EDGE_1024).
+// the maximum and once for P, in a loop over the chunks: with the row of 128 scores in registers,
+// as in the row step, its masks took registers from the loop over the whole tiles (B4 S4096, 16
+// heads on 4, hd 64, window 4096: 168 us, this way 134; window 1024 with 4 sinks: 99 and 90;
+// B8 S2048, 8 heads on 2, window 512: 37.4 and 31.2).
 struct EdgeRow {
   float m, l;      // the row's running maximum (log2 domain) and sum
   bool ok;
 };
 template <int HD, bool kNegScale>
-__device__ __noinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint32_t tP, uint32_t s_full,
+__device__ __forceinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint32_t tP, uint32_t s_full,
                                                  uint32_t s_free, uint32_t p_full, uint32_t o_done, int gx, bool first,
                                                  int far, int near, int sk, float scale_log2, float m, float l,
                                                  const WaitCtl ctl) {
@@ -153,6 +153,15 @@ __device__ __noinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint3
       fetch((c2 + h + 1) & 3, r[h ^ 1]);               // behind the last chunk: the first again, for P
       const uint32_t vis = vis_of(c2 + h);
       if (!__any_sync(0xffffffffu, vis != 0u)) continue;
+      if (__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float &a = mx[(c >> 1) & 1];
+          a = kNegScale ? fmin3(a, __uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]))
+                        : fmax3(a, __uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]));
+        }
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
         const float v0 = (vis >> c) & 1u ? __uint_as_float(r[h][c]) : kFill;
@@ -182,7 +191,17 @@ __device__ __noinline__ EdgeRow window_edge_step(uint32_t tS, uint32_t tO, uint3
       }
       const uint32_t vis = vis_of(c2 + h);
       uint32_t pk[16];
-      if (__any_sync(0xffffffffu, vis != 0u)) {
+      if (__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(r[h][c]), __uint_as_float(r[h][c + 1]), scale_log2, scale_log2, neg_m, neg_m);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const int e = c & 2;
+          fadd2(ps[e], ps[e + 1], ps[e], ps[e + 1], p0, p1);
+          pk[c / 2] = pack_bf16x2(p0, p1);
+        }
+      } else if (__any_sync(0xffffffffu, vis != 0u)) {
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           float x0, x1;
@@ -694,18 +713,15 @@ __global__ void __maxnreg__(168)
           lrow = e.l;
           return e.ok;
         };
+        int n = start, edge_end = min(whole, mX);
 #pragma unroll 1
-        for (int n = start; n < min(whole, mX); n = n + 1 == sunk ? lo : n + 1, ++gx) {
-          if (!edge(n)) { ok = false; break; }
-        }
-        if (!ok) break;
+        for (;;) {
 #pragma unroll 1
-        for (int n = whole; n < mX; ++n, ++gx) {
-          if (!step(std::false_type{}, n == start)) { ok = false; break; }
-        }
-        if (ok) {
-          if (!edge(mX)) ok = false;
-          ++gx;
+          for (; ok && n < edge_end; n = n + 1 == sunk ? lo : n + 1, ++gx) ok = edge(n);
+          if (!ok || n > mX) break;
+#pragma unroll 1
+          for (; ok && n < mX; ++n, ++gx) ok = step(std::false_type{}, n == start);
+          edge_end = mX + 1;
         }
       } else {
 #pragma unroll 1
