@@ -802,15 +802,23 @@ __global__ void __maxnreg__(168)
         // needs to keep that unit busy (measured: the exponential chunks take half the
         // time of a per-pair interleaved order). On the diagonal tile, query column
         // i < key row j is masked (P = 0); the common body has no mask.
+        // kOneCopy (windows of grouped heads): one copy of the code for edge tiles and others,
+        // whose chunks branch -- of a warp's four in an edge tile one or two are mixed, the
+        // others whole or not seen (B4 S4096, 16 heads on 4, hd 64, window 1000 with 130 sinks:
+        // 266.9 -> 260.2 us; at hd 128 and with one query head per kv head two copies are
+        // faster: 293.3 against 312.3, 312.5 against 318.6).
+        constexpr bool kOneCopy = kWin && kDsTmem;
         auto chunk = [&](auto masked, auto chunk_index, uint32_t *pk) {
           constexpr int c = decltype(chunk_index)::value;
-          uint32_t vis = 0;
-          if constexpr (kWin && decltype(masked)::value) {
-            vis = bit_range(lo_col - 32 * c, hi_col - 32 * c);
-            if (!__any_sync(0xffffffffu, vis != 0u)) {   // no key row of the warp is seen
+          uint32_t vis = 0xffffffffu;
+          if constexpr (kWin && (kOneCopy || decltype(masked)::value)) {
+            if (!kOneCopy || diag) {
+              vis = bit_range(lo_col - 32 * c, hi_col - 32 * c);
+              if (!__any_sync(0xffffffffu, vis != 0u)) {   // no key row of the warp is seen
 #pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = 0u;
-              return;
+                for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                return;
+              }
             }
           }
           (void)vis;
@@ -821,7 +829,13 @@ __global__ void __maxnreg__(168)
                   scale_log2, scale_log2);
 #pragma unroll
           for (int e = 0; e < 32; ++e) xs[e] = ex2_approx(xs[e]);
-          if constexpr (decltype(masked)::value) {
+          if constexpr (kOneCopy) {
+            if (diag && !__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (((vis >> e) & 1u) == 0u) xs[e] = 0.f;
+            }
+          } else if constexpr (decltype(masked)::value) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (kWin ? ((vis >> e) & 1u) == 0u : 32 * c + e < j) xs[e] = 0.f;
@@ -844,7 +858,8 @@ __global__ void __maxnreg__(168)
           tmem_st_x16(tP + lane_off + 48, pk);
           return true;
         };
-        if (!(diag ? body(std::true_type{}) : body(std::false_type{}))) ok = false;
+        if constexpr (kOneCopy) ok = body(std::false_type{});
+        else if (!(diag ? body(std::true_type{}) : body(std::false_type{}))) ok = false;
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
@@ -1235,25 +1250,27 @@ cudaError_t launch_bwd_main_bf16(const CUtensorMap &mq, const CUtensorMap &mk,
   return cudaErrorInvalidValue;
 }
 
-// A sink tile's walk is cut into parts of as many query tiles as a key tile of the window
-// meets (at least 4), so that no unit is longer than the others (B8 S2048 8 heads on 2,
-// window 512: the main kernel takes 304 units of 20 iterations, 2 a CTA; uncut the sink tiles'
-// units would have 64) -- but into no more than kSinkUnits units over all heads: many sink
-// tiles, or many heads, are parallel enough, and the parts' sums stay below 160 MB.
-constexpr int kSinkUnits = 1216;   // 8 per SM
+// A sink tile's walk over the query tiles is a unit as long as the sequence, a key tile of the
+// window one of `meets` query tiles. It is cut into parts of at least `meets` (and 4) tiles, and
+// of half the work of a CTA, so that the last units to run even out (B8 S2048, 8 heads on 2,
+// window 512: 304 units of 20 iterations, 2 a CTA; uncut the sink tiles' have 64). Many heads, or
+// many sink tiles, need no cuts, which cost a pass over fp32 sums (32 x 1024 x 12 heads, window
+// 512: 355 us cut in 2, 331 uncut); and there are never more than kSinkUnits of the parts,
+// whose sums then stay below 160 MB.
+constexpr int kSms = 152, kSinkUnits = 8 * kSms;
 WindowSplit window_bwd_split(int B, int S, int nkv, int window, int sinks) {
-  const int num_m = (S + kTileRows - 1) / kTileRows;
+  const long long num_m = (S + kTileRows - 1) / kTileRows, heads = static_cast<long long>(B) * nkv;
   WindowSplit w;
   w.sink_tiles = window_sink_tiles(sinks);
-  const int meets = (window + kTileRows - 2) / kTileRows + 1;
-  w.part_tiles = meets < 4 ? 4 : meets;
-  w.nparts = (num_m + w.part_tiles - 1) / w.part_tiles;
-  const long long tiles = static_cast<long long>(B) * nkv * w.sink_tiles;
-  const long long most = tiles < kSinkUnits && tiles > 0 ? kSinkUnits / tiles : 1;
-  if (w.nparts > most) {
-    w.part_tiles = static_cast<int>((num_m + most - 1) / most);
-    w.nparts = (num_m + w.part_tiles - 1) / w.part_tiles;
-  }
+  const long long meets = (static_cast<long long>(window) + kTileRows - 2) / kTileRows + 1;
+  const long long each = heads * (w.sink_tiles * num_m + (num_m - w.sink_tiles) * meets) / kSms;   // a CTA's work
+  const long long sink_units = heads * w.sink_tiles;
+  const long long most = sink_units > 0 && sink_units < kSinkUnits ? kSinkUnits / sink_units : 1;  // parts of one
+  long long part = meets > 4 ? meets : 4;
+  if (part < each / 2) part = each / 2;
+  if (part < (num_m + most - 1) / most) part = (num_m + most - 1) / most;
+  w.part_tiles = static_cast<int>(part < num_m ? part : num_m);
+  w.nparts = static_cast<int>((num_m + w.part_tiles - 1) / w.part_tiles);
   return w;
 }
 
