@@ -268,19 +268,47 @@ __global__ void __maxnreg__(168)
       reg_fence<64>(p);
       tc_fence_before();
       mbar_arrive(s_free);
+      if constexpr (kWin) {
+        // Chunks of 32 columns that no row of the warp sees cost nothing, those that all see no
+        // mask.
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        float x0, x1;
-        ffma2(x0, x1, __uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]), scale_log2, scale_log2,
-              nlse2, nlse2);
-        float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        if (diag) {
-          const int c = c0 + 2 * e;
-          if (c > near || (kWin && c < far && c >= sk)) p0 = 0.f;
-          if (c + 1 > near || (kWin && c + 1 < far && c + 1 >= sk)) p1 = 0.f;
+        for (int half = 0; half < 2; ++half) {
+          const int base = c0 + 32 * half;
+          uint32_t vis = 0xffffffffu;
+          if (diag) vis = bit_range(far - base, near - base) | bit_range(0, min(sk - 1, near) - base);
+          uint32_t *h = p + 32 * half;
+          if (!__any_sync(0xffffffffu, vis != 0u)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) h[e] = 0u;
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(h[e]), __uint_as_float(h[e + 1]), scale_log2, scale_log2, nlse2, nlse2);
+            h[e] = __float_as_uint(ex2_approx(x0));
+            h[e + 1] = __float_as_uint(ex2_approx(x1));
+          }
+          if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (((vis >> e) & 1u) == 0u) h[e] = 0u;
+          }
         }
-        p[2 * e] = __float_as_uint(p0);
-        p[2 * e + 1] = __float_as_uint(p1);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]), scale_log2, scale_log2,
+                nlse2, nlse2);
+          float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          if (diag) {                                   // key c0 + c > query i is masked
+            if (c0 + 2 * e > i) p0 = 0.f;
+            if (c0 + 2 * e + 1 > i) p1 = 0.f;
+          }
+          p[2 * e] = __float_as_uint(p0);
+          p[2 * e + 1] = __float_as_uint(p1);
+        }
       }
       // dS = P (dP - D) in two 32-column halves, bf16 into the dS slot.
       if (!warp_wait(dp_full, n & 1, ctl)) { ok = false; break; }

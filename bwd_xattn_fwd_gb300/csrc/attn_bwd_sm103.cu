@@ -268,13 +268,6 @@ struct WinArgs {
 
 __host__ __device__ inline int window_sink_tiles(int sinks) { return (sinks + kTileRows - 1) / kTileRows; }
 
-// Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 31);
-  return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-}
-
 template <int HD, bool kFusedDq, bool kResident = false, bool kDsTmem = false, bool kWin = false>
 __global__ void __maxnreg__(168)
     attn_bwd_main_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,

@@ -108,13 +108,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok);
 }
 
-// Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 31);
-  return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-}
-
 // One key step of a windowed tile that some row does not see whole: the diagonal, the tiles at
 // the window's far edge, sink tiles behind it. The row sees columns far .. near and 0 .. sk; a
 // chunk of 32 columns that no row of the warp sees costs nothing, and a row may see nothing of

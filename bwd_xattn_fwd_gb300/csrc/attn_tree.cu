@@ -93,13 +93,6 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
-__device__ __forceinline__ uint32_t word_range(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 31);
-  return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-}
-
 // The position tiles that some new token of one sequence can see, as a list: `heads` sink
 // tiles, then the tiles from lo to that of the last new token. Entry e is tile e below heads,
 // else e - heads + lo.
@@ -616,7 +609,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
 #pragma unroll
           for (int w = 0; w < kCols / 32; ++w) {
             const int col = copy * kCols + 32 * w, base = t0 + col, off = base - s.ctx;
-            uint32_t m = word_range(0, s.ctx - 1 - base) & (word_range(far - base, 31) | word_range(0, a.sinks - 1 - base));
+            uint32_t m = bit_range(0, s.ctx - 1 - base) & (bit_range(far - base, 31) | bit_range(0, a.sinks - 1 - base));
             if (off >= 0) {
               if (off < 64) m |= static_cast<uint32_t>(seen >> off);
             } else if (off > -32) {

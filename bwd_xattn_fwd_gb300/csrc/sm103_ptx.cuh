@@ -62,6 +62,13 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
   return d;
 }
 
+// Bits lo..hi of a 32-bit word (clipped to it; none when hi < lo).
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 31);
+  return hi < lo ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
 // Packed fp32 pair arithmetic (.f32x2): one instruction for two lanes of work.
 __device__ __forceinline__ void ffma2(float &d0, float &d1, float a0, float a1, float b0, float b1,
                                       float c0, float c1) {
