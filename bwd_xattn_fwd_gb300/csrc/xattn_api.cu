@@ -26,7 +26,9 @@ struct DeviceInfo {
   bool sm103 = false;
   int sms = 0;
   int *status = nullptr;
-  cudaMemPool_t pool = nullptr;   // scratch_alloc's
+  std::once_flag pool_once;       // scratch_alloc's
+  cudaError_t pool_err = cudaSuccess;
+  cudaMemPool_t pool = nullptr;
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -82,22 +84,12 @@ xattn_status device_info(DeviceInfo **out) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return XATTN_ERR_CUDA;
   DeviceInfo &d = g_dev[dev];
   std::call_once(d.once, [&d, dev] {
+    const OutsideCapture outside;
     int major = 0, minor = 0;
     d.err = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     d.sm103 = (major == 10 && minor == 3);
     if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (d.err == cudaSuccess) {
-      cudaMemPoolProps props = {};
-      props.allocType = cudaMemAllocationTypePinned;
-      props.location.type = cudaMemLocationTypeDevice;
-      props.location.id = dev;
-      d.err = cudaMemPoolCreate(&d.pool, &props);
-    }
-    if (d.err == cudaSuccess) {
-      unsigned long long keep = ~0ull;
-      d.err = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    }
     if (d.err == cudaSuccess) d.err = cudaGetSymbolAddress(reinterpret_cast<void **>(&d.status), g_device_status);
   });
   if (d.err != cudaSuccess) return XATTN_ERR_CUDA;
@@ -109,8 +101,19 @@ xattn_status device_info(DeviceInfo **out) {
 // the library's own that keeps what it has grown to: the default pool gives its memory back
 // at every synchronisation, and the next call would map it again (step of B8 S2048, each
 // call waited for: 471 us with the default pool against 134 us back to back).
-xattn_status scratch_alloc(const DeviceInfo &d, size_t bytes, cudaStream_t stream, void **out) {
-  if (cudaMallocFromPoolAsync(out, bytes, d.pool, stream) == cudaSuccess) return XATTN_OK;
+xattn_status scratch_alloc(DeviceInfo &d, size_t bytes, cudaStream_t stream, void **out) {
+  std::call_once(d.pool_once, [&d] {
+    const OutsideCapture outside;
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = static_cast<int>(&d - g_dev);
+    unsigned long long keep = ~0ull;
+    d.pool_err = cudaMemPoolCreate(&d.pool, &props);
+    if (d.pool_err == cudaSuccess)
+      d.pool_err = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+  });
+  if (d.pool_err == cudaSuccess && cudaMallocFromPoolAsync(out, bytes, d.pool, stream) == cudaSuccess) return XATTN_OK;
   cudaGetLastError();   // do not leave the failure for the caller's next error check
   return XATTN_ERR_CUDA;
 }
@@ -520,6 +523,7 @@ xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_t
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) || !aligned4(ctx_lens) || !aligned4(path) ||
       !aligned4(accepted))
     return XATTN_ERR_MISALIGNED;
+  if (2.0 * B * ((nkv * hd / 8 + 31) / 32) > 0x7fffffff) return XATTN_ERR_BAD_SHAPE;   // its grid
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
   const PageArgs a = {static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), page_table, ctx_lens, B, n,

@@ -37,6 +37,17 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned threads, si
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
 }
 
+// While it lives, calls of this thread that a stream capture would forbid (they take no part in
+// it: looking up a symbol, creating a pool, loading a kernel) are allowed, so that the library's
+// first call on a device may be a captured one.
+struct OutsideCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  OutsideCapture(const OutsideCapture &) = delete;
+  OutsideCapture &operator=(const OutsideCapture &) = delete;
+};
+
 // Allows `kernel` its dynamic shared memory on the current device, once per device: `done`
 // holds a bit for each device where that has happened (a call sets it again if two race).
 template <typename Kernel>
@@ -46,6 +57,7 @@ cudaError_t allow_smem(Kernel *kernel, size_t bytes, std::atomic<unsigned long l
   if (err != cudaSuccess) return err;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  const OutsideCapture outside;
   err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return err;

@@ -365,6 +365,8 @@ class _Elsewhere:
         device = t.device
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         self._guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):

@@ -2,6 +2,11 @@
 element within a bound derived from the roundings, tests/window_ref.py), on windows and sinks
 that end inside, at and across tiles; against the causal op; gradients against differences;
 graphs, streams and run-to-run reproducibility."""
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -178,3 +183,66 @@ def test_graph_replay_and_streams():
     o2, lse2 = xattn.attention_window_fwd(q, k, v, 100, 4, scale, stream=other)
     other.synchronize()
     assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+FIRST_IN_CAPTURE = """
+import torch
+from bwd_xattn_fwd_gb300 import xattn
+g = torch.Generator(device="cuda").manual_seed(0)
+q, k, v, dO = (torch.randn(2, 200, 2, 64, generator=g, device="cuda").bfloat16() for _ in range(4))
+table = torch.arange(8, device="cuda", dtype=torch.int32).view(2, 4)
+lens = torch.tensor([50, 7], device="cuda", dtype=torch.int32)
+pages = torch.randn(8, 128, 2, 64, generator=g, device="cuda").bfloat16()
+def calls():
+    o, lse = xattn.attention_window_fwd(q, k, v, 70, 3)
+    grads = xattn.attention_window_bwd(q, k, v, o, dO, lse, 70, 3, deterministic=True)
+    t, _ = xattn.attention_tree_decode(q[:, :4].contiguous(), pages, pages, table, lens)
+    return o, *grads, t
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+eager = calls()
+torch.cuda.synchronize()
+assert xattn.xattn_check_device_status() == 0
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """The library's first calls in a process (which set up its state for the device) may be
+    captured ones."""
+    run = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads on streams of their own give what they give alone."""
+    cases = [(_inputs(2, 400, 4, 2, 64, "bf16", seed=1), 100, 4), (_inputs(1, 700, 2, 2, 128, "bf16", seed=2), 33, 140)]
+    alone = [_run(x, w, s, 0.125, deterministic=True) for x, w, s in cases]
+    got = [None, None]
+
+    def work(i):
+        x, w, s = cases[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                from bwd_xattn_fwd_gb300 import xattn
+                o, lse = xattn.attention_window_fwd(x["q"], x["k"], x["v"], w, s, 0.125)
+                dq, dk, dv = xattn.attention_window_bwd(x["q"], x["k"], x["v"], o, x["dO"], lse, w, s, 0.125,
+                                                        deterministic=True)
+            torch.cuda.current_stream().synchronize()
+            got[i] = {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(a[n], b[n]) for n in a)

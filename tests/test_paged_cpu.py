@@ -90,6 +90,18 @@ def test_binding_checks():
         xattn.cache_compact(k, k, table, lens, lens, lens)
 
 
+def test_a_compaction_beyond_the_largest_grid(lib):
+    assert _compact(lib, B=2**30, n=1, nkv=1, hd=8) == 2             # two blocks a sequence
+
+
+def test_a_stream_of_another_device():
+    from types import SimpleNamespace
+    from bwd_xattn_fwd_gb300 import xattn
+    t, s = SimpleNamespace(device=torch.device("cuda:0")), SimpleNamespace(device=torch.device("cuda:1"))
+    with pytest.raises(ValueError):
+        xattn._Elsewhere(t, s)
+
+
 def test_the_plain_tree_of_a_run_is_causal_attention():
     """A run of new tokens (no words, or the words 2^(i+1) - 1) over a cache is the last rows of
     causal attention: against a softmax written out over the whole sequence."""
