@@ -59,14 +59,7 @@ struct TreeLayout {
   static constexpr int kNumBars = 4 * kSlots + 6;
   static constexpr uint32_t kPages = kBars + 8 * kNumBars;      // per V slot: boxes that hold a page
   static constexpr uint32_t kMisc = (kPages + 4 * kSlots + 15) / 16 * 16;
-  // At a piece's end: kPartCols columns of O of up to 96 lanes (the copies beyond the first),
-  // and every lane's (max, sum); in the Q tile, free by then, or at hd 32, where it is too
-  // small, behind the rest.
-  static constexpr int kPartCols = HD == 128 ? 64 : 32;
-  static constexpr uint32_t kPart = HD == 32 ? (kMisc + 32 + 127) / 128 * 128 : kQ;
-  static constexpr uint32_t kStat = kPart + 96 * kPartCols * 4;
-  static constexpr uint32_t kUsed = HD == 32 ? kStat + kTileRows * 8 : kMisc + 32;
-  static_assert(HD == 32 || kStat + kTileRows * 8 <= kK, "the hand-over fits the Q tile");
+  static constexpr uint32_t kUsed = kMisc + 32;
   // The tiles start at the next multiple of 1024; the base is at least 256-byte aligned.
   static constexpr uint32_t kDynBytes = kUsed + 768 > 80 * 1024 ? kUsed + 768 : 80 * 1024;
   static constexpr uint32_t kTmemCols = HD == 128 ? 512 : 256;
@@ -442,7 +435,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     const uint32_t tSx = tS + lane_off + copy * kCols, tPx = tP + lane_off + copy * (kCols / 2), tOx = tO + lane_off;
     const int box_rows = min(a.page_size, kTileRows);
     const unsigned all_boxes = box_rows == kTileRows ? 1u : (1u << (kTileRows / box_rows)) - 1u;
-    float2 *stat = reinterpret_cast<float2 *>(smem + L::kStat);
+    float2 *stat = reinterpret_cast<float2 *>(smem + L::kQ);        // every lane's (max, sum), at a piece's end
     if constexpr (kSplit > 1) {
       // P of the columns that the other copies take.
       uint32_t zero[32];
@@ -653,98 +646,175 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
         if (!ok) break;
       }
       if (!ok) break;
-      if (kSplit > 1 && have) load_rows(false);
       // The piece's result: O and the LSE of a whole unit, else a record (its O not divided by
       // its sum).
-      if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
       const bool whole = e0 == 0 && e1 == s.count;
-      const size_t rec = (2 * static_cast<size_t>(blockIdx.x) + (e0 == 0 ? 1 : 0)) * a.rec_rows + row;
-      XATTN_DCHECK(!mine || (rec < 2 * static_cast<size_t>(gridDim.x) * a.rec_rows && rows <= a.rec_rows), a.status);
-      const int rho = row0 + row;
-      const size_t out = (static_cast<size_t>(b) * a.n + rho / group) * a.nh + static_cast<size_t>(kvh) * group + rho % group;
-      // Copies beyond the first hand their O (kPart columns at a time) and statistics to the
-      // first through shared memory, which weighs and adds them in order.
-      constexpr int kPart = kSplit == 1 ? 32 : L::kPartCols, kPieces = kPart / 4;
-      float4 *part = reinterpret_cast<float4 *>(smem + L::kPart);
-      auto piece = [](int l, int i) { return l * kPieces + (i ^ (l & 7)); };   // against bank conflicts
-      float weight[kSplit], M = mrow, sum = lrow;
-#pragma unroll 1
-      for (int c = 0; c < HD; c += kPart) {
-        uint32_t ov[kPart];
-        if (live)
+      const size_t rec0 = (2 * static_cast<size_t>(blockIdx.x) + (e0 == 0 ? 1 : 0)) * a.rec_rows;
+      XATTN_DCHECK(rec0 + rows <= 2 * static_cast<size_t>(gridDim.x) * a.rec_rows || a.whole, a.status);
+      auto out_of = [&](int r) {                              // row r of the tile, in o and lse
+        const int rho = row0 + r;
+        const size_t at = (static_cast<size_t>(b) * a.n + rho / group) * a.nh + static_cast<size_t>(kvh) * group + rho % group;
+        XATTN_DCHECK(r >= rows || at < static_cast<size_t>(a.B) * a.n * a.nh, a.status);
+        return at;
+      };
+      auto put_stats = [&](float M, float sum) {
+        if (whole)
+          a.lse[out_of(row)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+        else
+          *reinterpret_cast<float2 *>(a.ws_ml + 2 * (rec0 + row)) = make_float2(M, sum);
+      };
+      if constexpr (kSplit > 1) {
+        // The copies' (max, sum) meet in the Q tile, which the last scores have read, while the
+        // last P V runs; each copy then weighs its own O, and the copies meet there again. Of
+        // two copies each adds half of the columns. Of four, few rows and many columns, all
+        // warps add, some lanes a row, so that a piece's end goes with its rows: a token's 4 at
+        // hd 128 2600 cycles, 5100 with copy 0's warp adding its lanes' rows (B64 n1 window
+        // 2048: 59.0 -> 55.1 us; B64 n8 hd 64 44.6 -> 41.1; with two copies this way loses, B64
+        // n16 45.2 against 44.0).
+        stat[lane_row] = make_float2(mrow, lrow);
+        warp_arrive(meet, lane);
+        if (have) load_rows(false);
+        if (!tree_wait(meet, meets++ & 1, ctl)) { ok = false; break; }
+        float M = -INFINITY, sum = 0.f, weight = 0.f;
 #pragma unroll
-          for (int x = 0; x < kPart; x += 32) tmem_ld_x32(tOx + c + x, ov + x);
-        tmem_wait_ld();
-        reg_fence<kPart>(ov);
-        if constexpr (kSplit > 1) {
-          if (copy > 0) {
-            if (c == 0) stat[lane_row] = make_float2(mrow, lrow);
+        for (int k = 0; k < kSplit; ++k) M = fmaxf(M, stat[k * kRows + row].x);
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-              part[piece(lane_row - kRows, i)] =
-                  make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
-                              __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
-          }
-          if (!meet_all()) { ok = false; break; }
-          if (copy == 0) {
-            if (c == 0) {
-#pragma unroll
-              for (int k = 1; k < kSplit; ++k) M = fmaxf(M, stat[k * kRows + row].x);
-              weight[0] = lrow > 0.f ? ex2_approx(mrow - M) : 0.f;
-              sum = lrow * weight[0];
-#pragma unroll
-              for (int k = 1; k < kSplit; ++k) {
-                const float2 ml = stat[k * kRows + row];
-                weight[k] = ml.y > 0.f ? ex2_approx(ml.x - M) : 0.f;
-                sum = fmaf(ml.y, weight[k], sum);
-              }
-            }
+        for (int k = 0; k < kSplit; ++k) {
+          const float2 ml = stat[k * kRows + row];
+          const float w = ml.y > 0.f ? ex2_approx(ml.x - M) : 0.f;
+          sum = fmaf(ml.y, w, sum);
+          if (k == copy) weight = w;
+        }
+        if (whole && sum > 0.f) weight /= sum;
+        warp_arrive(meet, lane);
+        if (mine && copy == 0) put_stats(M, sum);
+        if (!tree_wait(o_done, (R - 1) & 1, ctl) || !tree_wait(meet, meets++ & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        float4 *part = reinterpret_cast<float4 *>(smem + L::kQ);
+        if constexpr (kSplit == 2) {
+          // Each copy hands one half of its columns over and adds the other: the Q tile holds a
+          // half of every lane.
+          constexpr int kCols2 = HD / 2, kOnce = kCols2 < 32 ? kCols2 : 32, kPieces = kCols2 / 4;
+          static_assert(kTileRows * kPieces * 16 <= L::kTileBytes, "half of every lane's O fits the Q tile");
+          auto piece = [](int l, int i) { return l * kPieces + (i ^ (l & (kPieces < 8 ? kPieces - 1 : 7))); };
+          auto o_columns = [&](float *x, int c) {            // kOnce weighed columns of this copy's O
+            uint32_t ov[kOnce];
+            if constexpr (kOnce == 32) tmem_ld_x32(tOx + c, ov);
+            else tmem_ld_x16(tOx + c, ov);
+            tmem_wait_ld();
+            reg_fence<kOnce>(ov);
             // A copy that saw nothing counts 0, whatever its O holds.
 #pragma unroll
-            for (int i = 0; i < kPart; ++i)
-              ov[i] = weight[0] > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * weight[0]) : 0u;
+            for (int e = 0; e < kOnce; ++e) x[e] = weight > 0.f ? __uint_as_float(ov[e]) * weight : 0.f;
+          };
+          float x[kOnce];
+#pragma unroll 1
+          for (int c = 0; c < kCols2; c += kOnce) {
+            o_columns(x, (1 - copy) * kCols2 + c);
+            if (mine)
 #pragma unroll
-            for (int k = 1; k < kSplit; ++k)
+              for (int e = 0; e < kOnce; e += 4)
+                part[piece(lane_row, (c + e) / 4)] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            __syncwarp();                                    // (the reads of TMEM are the warp's)
+          }
+          if (!meet_all()) { ok = false; break; }
+          const size_t out = mine ? out_of(row) : 0;
+#pragma unroll 1
+          for (int c = 0; c < kCols2; c += kOnce) {
+            const int col = copy * kCols2 + c;
+            o_columns(x, col);
+            if (mine)
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i) {
-                const float4 z = part[piece((k - 1) * kRows + row, i)];
-                if (weight[k] > 0.f) {
-                  ov[4 * i] = __float_as_uint(fmaf(z.x, weight[k], __uint_as_float(ov[4 * i])));
-                  ov[4 * i + 1] = __float_as_uint(fmaf(z.y, weight[k], __uint_as_float(ov[4 * i + 1])));
-                  ov[4 * i + 2] = __float_as_uint(fmaf(z.z, weight[k], __uint_as_float(ov[4 * i + 2])));
-                  ov[4 * i + 3] = __float_as_uint(fmaf(z.w, weight[k], __uint_as_float(ov[4 * i + 3])));
-                }
+              for (int e = 0; e < kOnce; e += 4) {
+                const float4 z = part[piece(lane_row ^ kRows, (c + e) / 4)];
+                x[e] += z.x, x[e + 1] += z.y, x[e + 2] += z.z, x[e + 3] += z.w;
               }
+            if (mine && whole) {
+              uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * HD + col);
+#pragma unroll
+              for (int e = 0; e < kOnce; e += 8)
+                dst[e / 8] = make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
+                                        pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
+            } else if (mine) {
+              float4 *dst = reinterpret_cast<float4 *>(a.ws_o + (rec0 + row) * HD + col);
+#pragma unroll
+              for (int e = 0; e < kOnce; e += 4) dst[e / 4] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+            __syncwarp();                                    // (the reads of TMEM are the warp's)
+          }
+          if (have && !meet_all()) { ok = false; break; }    // read before the next queries go there
+        } else {
+          // The tile takes every column of up to half of its rows, or half the columns of all.
+          constexpr int kHalf = kRows / 2;
+          static_assert(kSplit * kHalf * HD * 4 <= L::kTileBytes, "half of the copies' O fits the Q tile");
+          const bool few = rows <= kHalf;
+          const int pieces = few ? HD / 4 : HD / 8, at = few ? copy * kHalf + row : lane_row;   // 16 bytes each
+          const bool here = mine && (!few || row < kHalf);
+          auto piece = [&](int l, int i) { return l * pieces + (i ^ (l & min(7, pieces - 1))); };   // against bank conflicts
+          XATTN_DCHECK(!here || (at + 1) * pieces * 16 <= static_cast<int>(L::kTileBytes), a.status);
+#pragma unroll 1
+          for (int p0 = 0; p0 < HD / 4; p0 += pieces) {
+#pragma unroll 1
+            for (int c = p0 / 8 * 8; c < p0 + pieces; c += 8) {
+              uint32_t ov[32];
+              tmem_ld_x32(tOx + 4 * c, ov);
+              tmem_wait_ld();
+              reg_fence<32>(ov);
+              // A copy that saw nothing counts 0, whatever its O holds.
+              auto val = [&](int x) { return weight > 0.f ? __uint_as_float(ov[x]) * weight : 0.f; };
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (here && (HD > 32 || (c + x >= p0 && c + x < p0 + pieces)))
+                  part[piece(at, c + x - p0)] = make_float4(val(4 * x), val(4 * x + 1), val(4 * x + 2), val(4 * x + 3));
+              __syncwarp();                                  // (the reads of TMEM are the warp's)
+            }
+            if (!meet_all()) { ok = false; break; }
+            const int i = lane & (pieces - 1), each = 32 / pieces;
+            for (int r = quarter * each + lane / pieces; r < rows; r += 4 * each) {
+              const int step = few ? kHalf : kRows;
+              float4 x = part[piece(r, i)];
+#pragma unroll
+              for (int k = 1; k < kSplit; ++k) {
+                const float4 z = part[piece(r + k * step, i)];
+                x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
+              }
+              if (whole)
+                *reinterpret_cast<uint2 *>(a.o + out_of(r) * HD + 4 * (p0 + i)) =
+                    make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+              else
+                *reinterpret_cast<float4 *>(a.ws_o + (rec0 + r) * HD + 4 * (p0 + i)) = x;
+            }
+            // The Q tile is read before the next columns, or queries, go there.
+            if ((have || p0 + pieces < HD / 4) && !meet_all()) { ok = false; break; }
           }
         }
-        XATTN_DCHECK(!mine || out < static_cast<size_t>(a.B) * a.n * a.nh, a.status);
-        XATTN_DCHECK(kSplit == 1 || copy == 0 || piece(lane_row - kRows, kPieces - 1) < 96 * kPieces, a.status);
-        if (mine && copy == 0) {
-          if (whole) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            auto val = [&](int i) { return sum > 0.f ? __uint_as_float(ov[i]) * inv : 0.f; };
+        if (!ok) break;
+      } else {
+        if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        const size_t out = mine ? out_of(row) : 0;
+        const float inv = lrow > 0.f ? 1.f / lrow : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t ov[32];
+          if (live) tmem_ld_x32(tOx + c, ov);
+          tmem_wait_ld();
+          reg_fence<32>(ov);
+          if (mine && whole) {
+            auto val = [&](int i) { return lrow > 0.f ? __uint_as_float(ov[i]) * inv : 0.f; };
             uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * HD + c);
 #pragma unroll
-            for (int i = 0; i < kPart / 8; ++i)
+            for (int i = 0; i < 4; ++i)
               dst[i] = make_uint4(pack_bf16x2(val(8 * i), val(8 * i + 1)), pack_bf16x2(val(8 * i + 2), val(8 * i + 3)),
                                   pack_bf16x2(val(8 * i + 4), val(8 * i + 5)), pack_bf16x2(val(8 * i + 6), val(8 * i + 7)));
-          } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(a.ws_o + rec * HD + c);
+          } else if (mine) {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.ws_o + (rec0 + row) * HD + c);
 #pragma unroll
-            for (int i = 0; i < kPart / 4; ++i)
-              dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
           }
+          __syncwarp();
         }
-        __syncwarp();
-        // The hand-over's shared memory is read before the next columns, or queries, go there.
-        if (kSplit > 1 && !meet_all()) { ok = false; break; }
-      }
-      if (mine && copy == 0) {
-        if (whole)
-          a.lse[out] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
-        else
-          *reinterpret_cast<float2 *>(a.ws_ml + 2 * rec) = make_float2(M, sum);
+        if (mine) put_stats(mrow, lrow);
       }
       tc_fence_before();
     }
