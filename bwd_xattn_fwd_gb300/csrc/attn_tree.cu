@@ -106,98 +106,104 @@ __device__ __forceinline__ Sight sight_of(const TreeArgs &a, int b) {
   return s;
 }
 
-// a / b for 0 <= a, 0 < b, in 32 bits where that will do; the long division stays out of the
-// instruction stream.
-__device__ __noinline__ long long long_quotient(long long a, long long b) { return a / b; }
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-  return long_quotient(a, b);
+// a / b for 0 <= a, 0 < b.
+__device__ __forceinline__ int quotient(int a, int b) {
+  return static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(b));
 }
 
-// The line of `length` tiles in `runs` runs: the first length % runs have one tile more.
-__device__ __forceinline__ long long run_start(long long length, long long runs, long long c) {
-  const long long each = quotient(length, runs);
-  return c * each + min(c, length - each * runs);
-}
-__device__ __forceinline__ long long run_of(long long length, long long runs, long long pos) {
-  const long long each = quotient(length, runs), more = length - each * runs;
-  const long long head = more * (each + 1);
-  return pos < head ? quotient(pos, each + 1) : more + quotient(pos - head, each);
-}
+// The line of `length` tiles (at most 2^30) in `runs` runs: the first length % runs have one more.
+struct Runs {
+  int each, more;
+  __device__ Runs(int length, int runs) : each(quotient(length, runs)), more(length - each * runs) {}
+  __device__ int start(int c) const { return c * each + min(c, more); }
+  __device__ int of(int pos) const {                           // the run that holds pos
+    const int head = more * (each + 1);
+    return pos < head ? quotient(pos, each + 1) : more + quotient(pos - head, each);
+  }
+};
 
 // A run of the line of tiles, walked piece by piece; warp-uniform, every warp of every role
-// walks the same pieces. All counts in 64 bits. With whole units the line's steps are units.
+// walks the same pieces. With whole units the line's steps are units.
 struct Walk {
-  long long pos, stop;     // next tile (unit) and end of the run, on the line
-  long long first;         // where sequence b starts on it
+  int pos, stop;           // next tile (unit) and end of the run, on the line
+  int first;               // where sequence b starts on it
   int b, e0, e1, unit;     // piece: sequence, entries [e0, e1) of its list, unit within it
   Sight s;
 };
 
-// Tiles of all sequences and units: the line's length. And the sequence that holds tile
-// `target` of it, with the line's tiles before that sequence. counts: tiles of the lane's
-// first four sequences (lane, lane + 32, ..), loaded together.
-__device__ __forceinline__ long long line_length(const TreeArgs &a, int units, int lane, int *counts) {
-  // A sequence has at most 2^23 tiles (2^30 positions): a lane's four, and 32 lanes of one,
-  // fit 32 bits.
-  int four = 0;
+// Tiles of four sequences (from b on).
+__device__ __forceinline__ int four_counts(const TreeArgs &a, int b, int *counts) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    counts[k] = 32 * k + lane < a.B ? sight_of(a, 32 * k + lane).count : 0;
-    four += counts[k];
+  for (int k = 0; k < 4; ++k) counts[k] = b + k < a.B ? sight_of(a, b + k).count : 0;
+  return (counts[0] + counts[1]) + (counts[2] + counts[3]);
+}
+
+// Tiles of all sequences and units: the line's length. And the sequence that holds tile
+// `target` of it, with the line's tiles before that sequence. Four sequences a lane; counts:
+// those of the first 128, which the one keeps for the other.
+__device__ __forceinline__ int line_length(const TreeArgs &a, int units, int lane, int *counts) {
+  int total = __reduce_add_sync(0xffffffffu, four_counts(a, 4 * lane, counts));
+  for (int b0 = 128; b0 < a.B; b0 += 128) {
+    int more[4];
+    total += __reduce_add_sync(0xffffffffu, four_counts(a, b0 + 4 * lane, more));
   }
-  long long total = __reduce_add_sync(0xffffffffu, four);
-  for (int b0 = 128; b0 < a.B; b0 += 32)
-    total += __reduce_add_sync(0xffffffffu, b0 + lane < a.B ? sight_of(a, b0 + lane).count : 0);
   return total * units;
 }
 
-__device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane, const int *counts, long long target,
-                                          int *b_out, long long *first_out) {
-  long long base = 0;
-  int next[4] = {counts[0], counts[1], counts[2], counts[3]};
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = b0 < 128 ? next[0] : (b0 + lane < a.B ? sight_of(a, b0 + lane).count : 0);
-    next[0] = next[1], next[1] = next[2], next[2] = next[3];
+__device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane, const int *counts, int target,
+                                          int *b_out, int *first_out) {
+  const int want = quotient(target, units);                    // x units > target as x > want
+  int base = 0, c[4] = {counts[0], counts[1], counts[2], counts[3]};
+  int mine = (c[0] + c[1]) + (c[2] + c[3]);
+#pragma unroll 1
+  for (int b0 = 0;;) {
     int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += up;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, base + static_cast<long long>(incl) * units > target);
+    const unsigned past = __ballot_sync(0xffffffffu, base + incl > want);
     if (past) {
       const int l = __ffs(past) - 1;
-      *b_out = b0 + l;
-      *first_out = base + static_cast<long long>(__shfl_sync(0xffffffffu, incl - mine, l)) * units;
+      int before = base + incl - mine, k = 0;
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        if (k == x && before + c[x] <= want) before += c[x], ++k;
+      *b_out = b0 + 4 * l + __shfl_sync(0xffffffffu, k, l);
+      *first_out = __shfl_sync(0xffffffffu, before, l) * units;
       return;
     }
-    base += static_cast<long long>(__shfl_sync(0xffffffffu, incl, 31)) * units;
+    base += __shfl_sync(0xffffffffu, incl, 31);
+    b0 += 128;
+    if (b0 >= a.B) break;                                      // (target is on the line: not reached)
+    mine = four_counts(a, b0 + 4 * lane, c);
   }
-  *b_out = a.B;
-  *first_out = base;
+  *b_out = a.B - 1;
+  *first_out = 0;
 }
 
 __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units) {
   if (w.pos >= w.stop) return false;
   if (a.whole) {
-    w.b = static_cast<int>(quotient(w.pos, units));
-    w.unit = static_cast<int>(w.pos - static_cast<long long>(w.b) * units);
+    w.b = quotient(w.pos, units);
+    w.unit = w.pos - w.b * units;
     w.s = sight_of(a, w.b);
     w.e0 = 0;
     w.e1 = w.s.count;
     ++w.pos;
     return true;
   }
-  long long at = w.pos - w.first;
-  if (at >= static_cast<long long>(w.s.count) * units) {       // the next sequence
-    w.first += static_cast<long long>(w.s.count) * units;
-    w.s = sight_of(a, ++w.b);
+  int at = w.pos - w.first;
+  if (at >= w.s.count * units) {                               // the next sequence
+    w.first += w.s.count * units;
+    if (++w.b >= a.B) return false;                            // (only if the lengths change under the call)
+    w.s = sight_of(a, w.b);
     at = 0;
   }
-  w.unit = static_cast<int>(quotient(at, w.s.count));
-  w.e0 = static_cast<int>(at - static_cast<long long>(w.unit) * w.s.count);
-  w.e1 = static_cast<int>(min(static_cast<long long>(w.s.count), w.e0 + (w.stop - w.pos)));
+  w.unit = quotient(at, w.s.count);
+  w.e0 = at - w.unit * w.s.count;
+  w.e1 = min(w.s.count, w.e0 + (w.stop - w.pos));
   w.pos += w.e1 - w.e0;
   return true;
 }
@@ -265,17 +271,16 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
   const uint32_t tS = tmem, tP = tmem + 128, tO = tmem + 192;
 
   // This CTA's run of the line.
-  const int group = a.nh / a.nkv, rows_all = a.n * group;
-  const int row_tiles = (rows_all + kRows - 1) / kRows;
+  const int group = a.group, rows_all = a.n * group, row_tiles = a.row_tiles;
   const int units = a.nkv * row_tiles;
   int counts[4];
-  const long long length = a.whole ? static_cast<long long>(a.B) * units : line_length(a, units, lane, counts);
-  const long long runs = min(static_cast<long long>(gridDim.x), length);
+  const int length = a.whole ? a.B * units : line_length(a, units, lane, counts);
+  const Runs runs(length, min(static_cast<int>(gridDim.x), length));
   Walk walk;
   walk.pos = walk.stop = 0;
-  if (blockIdx.x < runs) {
-    walk.pos = run_start(length, runs, blockIdx.x);
-    walk.stop = run_start(length, runs, blockIdx.x + 1);
+  if (static_cast<int>(blockIdx.x) < length) {
+    walk.pos = runs.start(blockIdx.x);
+    walk.stop = runs.start(blockIdx.x + 1);
   }
   if (!a.whole && walk.pos < walk.stop) {
     line_find(a, units, lane, counts, walk.pos, &walk.b, &walk.first);
@@ -287,13 +292,14 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     const int box_rows = min(a.page_size, kTileRows), boxes = kTileRows / box_rows;
     int R = 0, issued_k = 0, issued_v = 0;
     bool ok = true, have = walk_piece(walk, a, units);
+    auto page_of = [&](int p) { return a.page_shift >= 0 ? p >> a.page_shift : quotient(p, a.page_size); };
     // The table entries of a piece, 8 to a 32-byte sector.
     auto prefetch_table = [&](const Walk &w) {
       const int *table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
       const int t0 = w.e0 < w.s.heads ? w.e0 : w.e0 - w.s.heads + w.s.lo;
       const int t1 = w.e1 - 1 < w.s.heads ? w.e1 - 1 : w.e1 - 1 - w.s.heads + w.s.lo;
-      const int last = min(t1 * kTileRows + kTileRows - 1, w.s.end - 1) / a.page_size;
-      for (int at = t0 * kTileRows / a.page_size + 8 * lane; at <= last + 7; at += 256) prefetch_l2(table + min(at, last));
+      const int last = page_of(min(t1 * kTileRows + kTileRows - 1, w.s.end - 1));
+      for (int at = page_of(t0 * kTileRows) + 8 * lane; at <= last + 7; at += 256) prefetch_l2(table + min(at, last));
     };
     // A tile's boxes: their pages come to every lane first, then one elected lane issues the
     // copies back to back from uniform registers (box by box, with a shuffle or a branch per
@@ -321,13 +327,13 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     };
     while (ok && have) {
       const Walk here = walk;
-      const int kvh = here.unit / row_tiles;
+      const int kvh = row_tiles == 1 ? here.unit : quotient(here.unit, row_tiles);
       const int *table = a.page_table + static_cast<size_t>(here.b) * a.max_pages;
       // This lane's box of entry e: its table entry (-1 when no row can see the box) and its
       // row in the page. Read one tile ahead, so that no tile waits for the table.
       auto box_of = [&](int e, int *row) -> int {
         const int tile = e < here.s.heads ? e : e - here.s.heads + here.s.lo;
-        const int p0 = tile * kTileRows + lane * box_rows, at = p0 / a.page_size;
+        const int p0 = tile * kTileRows + lane * box_rows, at = page_of(p0);
         *row = p0 - at * a.page_size;
         if (lane >= boxes || e >= here.e1 || p0 >= here.s.end || (p0 + box_rows <= here.s.far && p0 >= a.sinks)) return -1;
         return __ldg(table + at);                               // p0 < end <= max_pages * page_size
@@ -492,9 +498,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       if (have) load_rows(true);
       // A run that ends inside the unit it started last says so to the combine.
       if (!have && !a.whole && warp == 2 && lane == 0) {
-        const long long start = walk.stop - (e1 - e0);
+        const int start = walk.stop - (e1 - e0);
         if (e0 == 0 && e1 < s.count)
-          a.plan[blockIdx.x] = make_int4(b, unit, static_cast<int>(run_of(length, runs, start + s.count - 1)), 1);
+          a.plan[blockIdx.x] = make_int4(b, unit, runs.of(start + s.count - 1), 1);
       }
       const int rows = min(rows_all - row0, kRows);
       const bool live = kSplit > 1 || quarter * 32 < rows;    // the warp has a row
@@ -843,8 +849,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
   const int4 plan = a.plan[c0];
   if (!plan.w) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane % kLanes, sub = lane / kLanes;
-  const int group = a.nh / a.nkv, rows_all = a.n * group;
-  const int row_tiles = (rows_all + a.tile_rows - 1) / a.tile_rows;
+  const int group = a.group, rows_all = a.n * group, row_tiles = a.row_tiles;
   const int kvh = plan.y / row_tiles, row0 = (plan.y % row_tiles) * a.tile_rows;
   const int rows = min(rows_all - row0, a.tile_rows);
   const int records = plan.z - c0 + 1;
@@ -952,15 +957,17 @@ bool tree_whole(int page_size, int max_pages) {
   return static_cast<long long>(max_pages) * page_size <= kWholeTiles * kTileRows;
 }
 
+// The longest line that the table allows, in tiles (whole units).
+double tree_line(const TreeArgs &a) {
+  const long long tiles = a.whole ? 1 : (static_cast<long long>(a.max_pages) * a.page_size + kTileRows - 1) / kTileRows;
+  return static_cast<double>(tiles) * a.B * a.nkv * a.row_tiles;
+}
+
 // CTAs of a call on a GPU with `sms` SMs: one resident wave, or one per tile (whole unit) of
 // the longest line that the table allows when that is shorter.
-int tree_grid(int B, int n, int nh, int nkv, int hd, int page_size, int max_pages, int sms) {
-  const long long tiles =
-      tree_whole(page_size, max_pages) ? 1 : (static_cast<long long>(max_pages) * page_size + kTileRows - 1) / kTileRows;
-  const int tile_rows = tree_tile_rows(n, nh, nkv);
-  const long long row_tiles = (static_cast<long long>(n) * (nh / nkv) + tile_rows - 1) / tile_rows;
-  const double most = static_cast<double>(tiles) * B * nkv * row_tiles;
-  const int resident = sms * (tile_rows == kTileRows || hd == 128 ? 1 : tree_ctas<64, 2>());
+int tree_grid(const TreeArgs &a, int hd, int sms) {
+  const double most = tree_line(a);
+  const int resident = sms * (a.tile_rows == kTileRows || hd == 128 ? 1 : tree_ctas<64, 2>());
   return most < resident ? static_cast<int>(most) : resident;
 }
 

@@ -460,17 +460,25 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned4(lse) ||
       !aligned4(page_table) || !aligned4(ctx_lens) || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
     return XATTN_ERR_MISALIGNED;
+  TreeArgs a = {};
+  a.B = B, a.n = n, a.nh = nh, a.nkv = nkv;
+  a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
+  a.group = nh / nkv;
+  a.tile_rows = tree_tile_rows(n, nh, nkv);
+  const long long rows = static_cast<long long>(n) * a.group;
+  if (rows > (1 << 30)) return XATTN_ERR_BAD_SHAPE;
+  a.row_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
+  a.rec_rows = rows < a.tile_rows ? static_cast<int>(rows) : a.tile_rows;
+  a.whole = tree_whole(page_size, max_pages) ? 1 : 0;
+  a.page_shift = (page_size & (page_size - 1)) ? -1 : __builtin_ctz(page_size);
+  if (tree_line(a) > 0x1p30) return XATTN_ERR_BAD_SHAPE;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
   CUtensorMap mk, mv;
   XATTN_TRY(make_map_pages(&mk, k_pages, num_pages, page_size, nkv, hd));
   XATTN_TRY(make_map_pages(&mv, v_pages, num_pages, page_size, nkv, hd));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = tree_grid(B, n, nh, nkv, hd, page_size, max_pages, dev->sms);
-  TreeArgs a = {};
-  a.tile_rows = tree_tile_rows(n, nh, nkv);
-  a.rec_rows = n * (nh / nkv) < a.tile_rows ? n * (nh / nkv) : a.tile_rows;
-  a.whole = tree_whole(page_size, max_pages) ? 1 : 0;
+  const int grid = tree_grid(a, hd, dev->sms);
   void *ws = nullptr;
   if (!a.whole) XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
   a.q = static_cast<const __nv_bfloat16 *>(q);
@@ -484,8 +492,6 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
     a.ws_o = reinterpret_cast<float *>(a.plan + grid);
     a.ws_ml = a.ws_o + static_cast<size_t>(grid) * 2 * a.rec_rows * hd;
   }
-  a.B = B, a.n = n, a.nh = nh, a.nkv = nkv;
-  a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
   a.window = window < (1 << 30) ? window : (1 << 30);   // a table holds at most 2^30 positions
   a.sinks = sinks < (1 << 30) ? sinks : (1 << 30);
   a.scale_log2 = scale * kLog2e;

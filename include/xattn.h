@@ -312,8 +312,10 @@ int xattn_decode_runs(int B, int T, int nh, int nkv, int hd, int num_sms);
  * A token that sees nothing gives o = 0 and lse = -infinity. Positions that no token of the
  * sequence sees are never used and may hold anything, NaN included; K and V at positions
  * that some token sees must be finite.
- * n <= XATTN_TREE_MAX (else XATTN_ERR_BAD_SHAPE); hd in {32, 64, 128}; nh a multiple of nkv
- * (any group); window >= n (so that a window never ends inside the tree) and sinks >= 0
+ * n <= XATTN_TREE_MAX, and B * nkv * (row tiles of up to 128 of a kv head's n * group rows) *
+ * (128-position tiles of the table) <= 2^30 (else XATTN_ERR_BAD_SHAPE); hd in {32, 64, 128};
+ * nh a multiple of nkv (any group); window >= n (so that a window never ends inside the tree)
+ * and sinks >= 0
  * (else XATTN_ERR_WINDOW; XATTN_NO_WINDOW for none); any finite scale. q, k_pages, v_pages
  * and o 16-byte aligned, the int and float arrays 4-byte.
  * Arithmetic as in xattn_fwd: tensor-core products on the bf16 inputs with fp32 accumulation,

@@ -43,6 +43,7 @@ def test_tree_checks(lib):
         assert _tree(lib, page=page) == 14, page
     assert _tree(lib, width=1, n=17, window=17) == 14             # the table cannot hold the new tokens
     assert _tree(lib, page=128, width=(1 << 23) + 1) == 14
+    assert _tree(lib, page=128, width=1 << 23, B=128) == 2        # 128 sequences x 2 kv heads x 2^23 tiles
     if not torch.cuda.is_available():
         for page in (16, 32, 64, 128, 256, 384):
             assert _tree(lib, page=page, tree=None) == 6          # accepted; fails only for want of a GPU
