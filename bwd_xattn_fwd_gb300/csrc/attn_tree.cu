@@ -24,7 +24,11 @@
 //     tree_combine_kernel merges each cut unit's records in order.
 //   * Short caches (a table of at most kWholeTiles tiles a sequence): runs of whole units, so
 //     there is nothing to merge: no records, no scratch and no second kernel, which at that
-//     length cost more than the tiles that a CTA takes more.
+//     length cost more than the tiles that a CTA takes more. Where a unit a CTA fills the GPU
+//     (`choose`) the lengths decide: whole units unless the longest would keep the call waiting
+//     for more than the 4 us that cutting costs. A CTA takes about 0.85 us a tile, HBM 0.075 ns
+//     a column of one (B64 n16 over 2048 positions 28.8 us cut, 23.7 whole; over 4096 43.6 and
+//     42.6; with more units than CTAs cut is better: B64 n1 at hd 128, window 2048 55.0, 57.0).
 //   * Pages: a tile is loaded box by box (one TMA box per page, or per 128 rows of a larger
 //     one). A box that no row can see, or whose table entry is no page, is loaded from
 //     outside the pool: the TMA unit writes zeros and reads nothing.
@@ -128,6 +132,7 @@ struct Walk {
   int pos, stop;           // next tile (unit) and end of the run, on the line
   int first;               // where sequence b starts on it
   int b, e0, e1, unit;     // piece: sequence, entries [e0, e1) of its list, unit within it
+  bool whole;              // the line's steps are units
   Sight s;
 };
 
@@ -140,13 +145,16 @@ __device__ __forceinline__ int four_counts(const TreeArgs &a, int b, int *counts
 
 // Tiles of all sequences and units: the line's length. And the sequence that holds tile
 // `target` of it, with the line's tiles before that sequence. Four sequences a lane; counts:
-// those of the first 128, which the one keeps for the other.
-__device__ __forceinline__ int line_length(const TreeArgs &a, int units, int lane, int *counts) {
+// those of the first 128, which the one keeps for the other; longest: tiles of a sequence at most.
+__device__ __forceinline__ int line_length(const TreeArgs &a, int units, int lane, int *counts, int *longest) {
   int total = __reduce_add_sync(0xffffffffu, four_counts(a, 4 * lane, counts));
+  int most = max(max(counts[0], counts[1]), max(counts[2], counts[3]));
   for (int b0 = 128; b0 < a.B; b0 += 128) {
     int more[4];
     total += __reduce_add_sync(0xffffffffu, four_counts(a, b0 + 4 * lane, more));
+    most = max(most, max(max(more[0], more[1]), max(more[2], more[3])));
   }
+  if (longest) *longest = __reduce_max_sync(0xffffffffu, most);
   return total * units;
 }
 
@@ -185,7 +193,7 @@ __device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane
 
 __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units) {
   if (w.pos >= w.stop) return false;
-  if (a.whole) {
+  if (w.whole) {
     w.b = quotient(w.pos, units);
     w.unit = w.pos - w.b * units;
     w.s = sight_of(a, w.b);
@@ -274,15 +282,22 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
   const int group = a.group, rows_all = a.n * group, row_tiles = a.row_tiles;
   const int units = a.nkv * row_tiles;
   int counts[4];
-  const int length = a.whole ? a.B * units : line_length(a, units, lane, counts);
-  const Runs runs(length, min(static_cast<int>(gridDim.x), length));
   Walk walk;
+  walk.whole = a.whole;
+  int length = a.B * units, longest = 0;
+  if (!a.whole) {
+    const int tiles = line_length(a, units, lane, counts, a.choose ? &longest : nullptr);
+    if (a.choose)
+      walk.whole = longest * 850.f <= fmaxf(tiles * (HD * 0.075f), tiles * (850.f / gridDim.x)) + 4000.f;
+    if (!walk.whole) length = tiles;
+  }
+  const Runs runs(length, min(static_cast<int>(gridDim.x), length));
   walk.pos = walk.stop = 0;
   if (static_cast<int>(blockIdx.x) < length) {
     walk.pos = runs.start(blockIdx.x);
     walk.stop = runs.start(blockIdx.x + 1);
   }
-  if (!a.whole && walk.pos < walk.stop) {
+  if (!walk.whole && walk.pos < walk.stop) {
     line_find(a, units, lane, counts, walk.pos, &walk.b, &walk.first);
     walk.s = sight_of(a, walk.b);
   }
@@ -992,6 +1007,12 @@ bool tree_whole(int page_size, int max_pages) {
 double tree_line(const TreeArgs &a) {
   const long long tiles = a.whole ? 1 : (static_cast<long long>(a.max_pages) * a.page_size + kTileRows - 1) / kTileRows;
   return static_cast<double>(tiles) * a.B * a.nkv * a.row_tiles;
+}
+
+// A unit a CTA, or nearly: whole units may be faster than cut ones.
+bool tree_choose(const TreeArgs &a, int grid) {
+  const double units = static_cast<double>(a.B) * a.nkv * a.row_tiles;
+  return !a.whole && units <= grid && 2 * units >= grid;
 }
 
 // CTAs of a call on a GPU with `sms` SMs: one resident wave, or one per tile (whole unit) of

@@ -68,7 +68,8 @@ CASES = [
     (3, 5, 4, 2, 64, 16, 600, 200, 5000),      # more sinks than positions
     (70, 2, 8, 2, 64, 16, 400, BIG, 0),        # more sequences than a warp scans at once
     (200, 1, 4, 4, 32, 32, 900, 256, 4),
-    (300, 2, 2, 1, 64, 64, 1900, BIG, 0),      # more than a warp's lanes hold at once, units cut
+    (300, 2, 2, 1, 64, 64, 1900, BIG, 0),      # more sequences than a warp's lanes hold at once
+    (300, 2, 2, 1, 32, 64, 9000, BIG, 0),      # the same with some far longer than most: units cut
     (1, 4, 4, 1, 64, 64, 30000, BIG, 0),       # one long cache over every CTA
     (5, 16, 8, 2, 64, 64, 9000, BIG, 0),       # few units over many CTAs, some short
 ]
