@@ -219,10 +219,10 @@ __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units
 // Record of a cut unit's piece: CTA c's piece that starts inside a unit is record 2c, the one
 // that starts it record 2c + 1. Layout: [records][rows][hd] O, then [records][rows] (max, sum).
 // CTAs an SM: with few rows two (where they fit), so that one streams while the other ends a
-// unit (B64 n16 hd 64: 46.8 us, one with twice the slots 48.4; n 1 over 1000 positions 38.7
-// against 52.3). A tile of 128 rows is bound by its softmax and wants the registers of one: a
-// row of 128 scores in the 168 registers of two spilled (B8 n64 hd 64 over 8192 positions:
-// 63.4 us, read from TMEM twice instead 55.7, one CTA 33.6).
+// unit (B64 n16 hd 64: 43.2 us, one with twice the slots 47.8; 200 sequences of 1000 positions,
+// n 1, 34.2 against 47.0). A tile of 128 rows is bound by its softmax and wants the registers of
+// one: a row of 128 scores spills in the 168 registers of two (B8 n64 hd 64 over 8192 positions:
+// 42.8 us, one CTA 31.9).
 template <int HD, int kSplit>
 constexpr int tree_ctas() {
   return kSplit == 1 ? 1 : TreeLayout<HD>::kCtas;
@@ -996,8 +996,8 @@ int tree_tile_rows(int n, int nh, int nkv) {
 }
 
 // Runs are whole units when no sequence can have more tiles than this. At 1000 positions (8
-// tiles; n 8, hd 64, 4 kv heads) whole against cut units: 64 sequences 14.5 and 24.9 us; one
-// sequence 12.2 and 11.1 us on the GPU, 20.6 and 25.1 us with the host's part of a call.
+// tiles; n 8, hd 64, 4 kv heads) whole against cut units: 64 sequences 12.9 and 21.6 us; one
+// sequence 9.6 and 10.8 us on the GPU, 10.4 and 12.0 us with the host's part of a call.
 constexpr int kWholeTiles = 8;
 bool tree_whole(int page_size, int max_pages) {
   return static_cast<long long>(max_pages) * page_size <= kWholeTiles * kTileRows;
