@@ -25,9 +25,9 @@
 //   * Short caches (a table of at most kWholeTiles tiles a sequence): runs of whole units, so
 //     there is nothing to merge: no records, no scratch and no second kernel, which at that
 //     length cost more than the tiles that a CTA takes more. Where a unit a CTA fills the GPU
-//     (`choose`) the lengths decide: whole units unless the longest would keep the call waiting
-//     for more than the 4 us that cutting costs. A CTA takes about 0.85 us a tile, HBM 0.075 ns
-//     a column of one (B64 n16 over 2048 positions 28.8 us cut, 23.7 whole; over 4096 43.6 and
+//     (`tree_choose`) the lengths decide: whole units unless the longest would keep the call waiting
+//     for more than the 4 us that cutting costs. A CTA takes about 0.9 us a tile, HBM 0.075 ns
+//     a column of one (B64 n16 over 2048 positions 28.8 us cut, 24.1 whole; over 4096 43.6 and
 //     42.6; with more units than CTAs cut is better: B64 n1 at hd 128, window 2048 55.0, 57.0).
 //   * Pages: a tile is loaded box by box (one TMA box per page, or per 128 rows of a larger
 //     one). A box that no row can see, or whose table entry is no page, is loaded from
@@ -132,7 +132,7 @@ struct Walk {
   int pos, stop;           // next tile (unit) and end of the run, on the line
   int first;               // where sequence b starts on it
   int b, e0, e1, unit;     // piece: sequence, entries [e0, e1) of its list, unit within it
-  bool whole;              // the line's steps are units
+  int whole;               // the line's steps are units
   Sight s;
 };
 
@@ -146,6 +146,7 @@ __device__ __forceinline__ int four_counts(const TreeArgs &a, int b, int *counts
 // Tiles of all sequences and units: the line's length. And the sequence that holds tile
 // `target` of it, with the line's tiles before that sequence. Four sequences a lane; counts:
 // those of the first 128, which the one keeps for the other; longest: tiles of a sequence at most.
+template <bool kLongest>
 __device__ __forceinline__ int line_length(const TreeArgs &a, int units, int lane, int *counts, int *longest) {
   int total = __reduce_add_sync(0xffffffffu, four_counts(a, 4 * lane, counts));
   int most = max(max(counts[0], counts[1]), max(counts[2], counts[3]));
@@ -154,7 +155,7 @@ __device__ __forceinline__ int line_length(const TreeArgs &a, int units, int lan
     total += __reduce_add_sync(0xffffffffu, four_counts(a, b0 + 4 * lane, more));
     most = max(most, max(max(more[0], more[1]), max(more[2], more[3])));
   }
-  if (longest) *longest = __reduce_max_sync(0xffffffffu, most);
+  if constexpr (kLongest) *longest = __reduce_max_sync(0xffffffffu, most);
   return total * units;
 }
 
@@ -191,9 +192,10 @@ __device__ __forceinline__ void line_find(const TreeArgs &a, int units, int lane
   *first_out = 0;
 }
 
+template <bool kChoose>
 __device__ __forceinline__ bool walk_piece(Walk &w, const TreeArgs &a, int units) {
   if (w.pos >= w.stop) return false;
-  if (w.whole) {
+  if (kChoose ? w.whole : a.whole) {
     w.b = quotient(w.pos, units);
     w.unit = w.pos - w.b * units;
     w.s = sight_of(a, w.b);
@@ -228,7 +230,9 @@ constexpr int tree_ctas() {
   return kSplit == 1 ? 1 : TreeLayout<HD>::kCtas;
 }
 
-template <int HD, int kSplit>
+// kChoose: a call that tree_choose lets choose (a kernel of its own: the choice in every call
+// cost those that have none 1 %).
+template <int HD, int kSplit, bool kChoose>
 __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = TreeLayout<HD>;
@@ -286,9 +290,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
   walk.whole = a.whole;
   int length = a.B * units, longest = 0;
   if (!a.whole) {
-    const int tiles = line_length(a, units, lane, counts, a.choose ? &longest : nullptr);
-    if (a.choose)
-      walk.whole = longest * 850.f <= fmaxf(tiles * (HD * 0.075f), tiles * (850.f / gridDim.x)) + 4000.f;
+    const int tiles = line_length<kChoose>(a, units, lane, counts, &longest);
+    if constexpr (kChoose)
+      walk.whole = longest * 900.f <= fmaxf(tiles * (HD * 0.075f), tiles * (900.f / gridDim.x)) + 4000.f;
     if (!walk.whole) length = tiles;
   }
   const Runs runs(length, min(static_cast<int>(gridDim.x), length));
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     // ---------------- TMA producer: lane l finds box l of each tile ----------------
     const int box_rows = min(a.page_size, kTileRows), boxes = kTileRows / box_rows;
     int R = 0, issued_k = 0, issued_v = 0;
-    bool ok = true, have = walk_piece(walk, a, units);
+    bool ok = true, have = walk_piece<kChoose>(walk, a, units);
     auto page_of = [&](int p) { return a.page_shift >= 0 ? p >> a.page_shift : quotient(p, a.page_size); };
     // The table entries of a piece, 8 to a 32-byte sector.
     auto prefetch_table = [&](const Walk &w) {
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
         // Looking ahead waits until the run's first copies are on their way.
         if (e == min(here.e0 + (first ? 1 : 0), here.e1 - 1)) {
           if (first) prefetch_table(here);
-          have = walk_piece(walk, a, units);
+          have = walk_piece<kChoose>(walk, a, units);
           if (have) prefetch_table(walk);
         }
         // Outside the pool (num_pages) there is nothing to read: the box is zeros.
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     };
     int R = 0, piece = 0, scored = 0;
     bool ok = true;
-    while (ok && walk_piece(walk, a, units)) {
+    while (ok && walk_piece<kChoose>(walk, a, units)) {
       ok = tree_wait(q_full, piece & 1, ctl) && scores(R);
       if (ok) scored = R + 1;
 #pragma unroll 1
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     // Nothing for the combine until the run's end says otherwise (a run that gives up says
     // nothing).
     if (!a.whole && warp == 2 && lane == 0) a.plan[blockIdx.x] = make_int4(0, 0, 0, 0);
-    bool have = walk_piece(walk, a, units);
+    bool have = walk_piece<kChoose>(walk, a, units);
     if (kSplit > 1 && have) load_rows(false);
     while (ok && have) {
       const Sight s = walk.s;
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       const int unit = walk.unit;
       if (kSplit == 1) load_rows(false);
       // From here on `walk` is the next piece.
-      have = walk_piece(walk, a, units);
+      have = walk_piece<kChoose>(walk, a, units);
       if (have) load_rows(true);
       // A run that ends inside the unit it started last says so to the combine.
       if (!have && !a.whole && warp == 2 && lane == 0) {
@@ -958,14 +962,28 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int
   }
 }
 
-template <int HD, int kSplit>
-cudaError_t launch_tree_split(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
-                              cudaStream_t stream) {
+// A unit a CTA, or nearly: whole units may be faster than cut ones.
+bool tree_choose(const TreeArgs &a, int grid) {
+  const double units = static_cast<double>(a.B) * a.nkv * a.row_tiles;
+  return !a.whole && units <= grid && 2 * units >= grid;
+}
+
+template <int HD, int kSplit, bool kChoose>
+cudaError_t launch_tree_kernel(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
+                               cudaStream_t stream) {
   using L = TreeLayout<HD>;
   static std::atomic<unsigned long long> allowed{0};
-  cudaError_t err = allow_smem(tree_kernel<HD, kSplit>, L::kDynBytes, allowed);
+  cudaError_t err = allow_smem(tree_kernel<HD, kSplit, kChoose>, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(tree_kernel<HD, kSplit>, static_cast<unsigned>(grid), kTreeThreads, L::kDynBytes, stream, mk, mv, a);
+  return launch_pdl(tree_kernel<HD, kSplit, kChoose>, static_cast<unsigned>(grid), kTreeThreads, L::kDynBytes, stream,
+                    mk, mv, a);
+}
+
+template <int HD, int kSplit>
+cudaError_t launch_tree_split(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, bool choose, int grid,
+                              cudaStream_t stream) {
+  const cudaError_t err = choose ? launch_tree_kernel<HD, kSplit, true>(mk, mv, a, grid, stream)
+                                 : launch_tree_kernel<HD, kSplit, false>(mk, mv, a, grid, stream);
   if (err != cudaSuccess || grid == 1 || a.whole) return err;
   // A block for the rows that 8 warps hold at once; where a unit spans many runs (few units),
   // one for each warp's rows.
@@ -981,9 +999,10 @@ cudaError_t launch_tree_split(const CUtensorMap &mk, const CUtensorMap &mv, cons
 template <int HD>
 cudaError_t launch_tree_hd(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
                            cudaStream_t stream) {
-  if (a.tile_rows == 32) return launch_tree_split<HD, 4>(mk, mv, a, grid, stream);
-  if (a.tile_rows == 64) return launch_tree_split<HD, 2>(mk, mv, a, grid, stream);
-  return launch_tree_split<HD, 1>(mk, mv, a, grid, stream);
+  const bool choose = tree_choose(a, grid);
+  if (a.tile_rows == 32) return launch_tree_split<HD, 4>(mk, mv, a, choose, grid, stream);
+  if (a.tile_rows == 64) return launch_tree_split<HD, 2>(mk, mv, a, choose, grid, stream);
+  return launch_tree_split<HD, 1>(mk, mv, a, choose, grid, stream);
 }
 
 }  // namespace
@@ -1007,12 +1026,6 @@ bool tree_whole(int page_size, int max_pages) {
 double tree_line(const TreeArgs &a) {
   const long long tiles = a.whole ? 1 : (static_cast<long long>(a.max_pages) * a.page_size + kTileRows - 1) / kTileRows;
   return static_cast<double>(tiles) * a.B * a.nkv * a.row_tiles;
-}
-
-// A unit a CTA, or nearly: whole units may be faster than cut ones.
-bool tree_choose(const TreeArgs &a, int grid) {
-  const double units = static_cast<double>(a.B) * a.nkv * a.row_tiles;
-  return !a.whole && units <= grid && 2 * units >= grid;
 }
 
 // CTAs of a call on a GPU with `sms` SMs: one resident wave, or one per tile (whole unit) of

@@ -479,7 +479,6 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   XATTN_TRY(make_map_pages(&mv, v_pages, num_pages, page_size, nkv, hd));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int grid = tree_grid(a, hd, dev->sms);
-  a.choose = tree_choose(a, grid) ? 1 : 0;
   void *ws = nullptr;
   if (!a.whole) XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
   a.q = static_cast<const __nv_bfloat16 *>(q);

@@ -188,7 +188,6 @@ struct TreeArgs {
   int4 *plan;                          // [grid] what each run leaves to the combine
   int B, n, nh, nkv, num_pages, page_size, max_pages, window, sinks;
   int whole;                           // runs of whole units (tree_whole): no plan, no records
-  int choose;                          // the kernel chooses between whole and cut units (tree_choose)
   int tile_rows, rec_rows;             // rows of a row tile (tree_tile_rows), and of a record
   int group, row_tiles;                // nh / nkv; row tiles of a kv head
   int page_shift;                      // log2 page_size, or -1 when it is no power of two
@@ -198,7 +197,6 @@ struct TreeArgs {
 };
 double tree_line(const TreeArgs &a);   // at most 2^30
 int tree_grid(const TreeArgs &a, int hd, int sms);
-bool tree_choose(const TreeArgs &a, int grid);
 int tree_tile_rows(int n, int nh, int nkv);
 bool tree_whole(int page_size, int max_pages);
 size_t tree_workspace_bytes(int grid, int rec_rows, int hd);

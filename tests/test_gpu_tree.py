@@ -314,6 +314,29 @@ def test_graphs_follow_lengths_and_two_graphs_do_not_meet():
                                                     hd ** -0.5), "graph")
 
 
+def test_a_graph_whose_lengths_even_out():
+    """200 units of (sequence, kv head): a few long caches among short ones are cut into runs, even
+    ones are not; one captured call takes both, in either order."""
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nh, nkv, hd, page = 50, 2, 4, 4, 64, 64
+    even, uneven = [2000 - b for b in range(B)], [6000 if b % 20 == 3 else b for b in range(B)]
+    k, v, table = paged_state(B, n, nkv, hd, page, [max(x) for x in zip(even, uneven)], seed=5, device="cuda")
+    width = max(len(r) for r in table)
+    table = [r + [-1] * (width - len(r)) for r in table]
+    q, tb, lens = _q(B, n, nh, hd, 3), _i32(table), _i32(even)
+    graph = torch.cuda.CUDAGraph()
+    xattn.attention_tree_decode(q, k, v, tb, lens)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        o, lse = xattn.attention_tree_decode(q, k, v, tb, lens)
+    for now in (even, uneven, even):
+        lens.copy_(_i32(now))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert xattn.xattn_check_device_status() == 0
+        check_tree(o, lse, tree_reference(q, k, v, table, now, None, BIG, 0, hd ** -0.5), "even" if now is even else "uneven")
+
+
 def test_explicit_streams_by_object_and_handle():
     from bwd_xattn_fwd_gb300 import xattn
     B, n, nh, nkv, hd, page, lens = 2, 4, 4, 2, 64, 16, [100, 60]
