@@ -212,7 +212,8 @@ xattn_status xattn_bwd_f32(const float *q, const float *k, const float *v, const
  * Window attention with sinks: causal attention in which query i sees key j <= i only if
  *     i - j < window   (the query itself and the window - 1 keys before it)   or
  *     j < sinks        (the sequence's first keys, which stay visible).
- * Every query sees itself, so no row is empty. The pages have no windowed attention; the
+ * Every query sees itself, so no row is empty. K and V must be finite, as for the causal calls:
+ * a hidden key's weight of 0 meets its V in the products. The pages have no windowed attention; the
  * operation is otherwise that of xattn_fwd / xattn_bwd, with their layouts, arithmetic,
  * alignment (lse 4-byte) and scale rules. window >= 1 and sinks >= 0 (else
  * XATTN_ERR_WINDOW); both are clipped to S, so XATTN_NO_WINDOW gives the causal op.
