@@ -9,7 +9,7 @@
 // FMA pipe, bound a product (8 16-byte reads for 64 FMAs). The two groups of a block take its
 // tiles in turn, and dK/dV a cluster of blocks as well, because the problems this mode serves
 // (gradient checks, small models) are chains of a few tiles on a GPU that they do not fill.
-// Forward and backward of B2 S499 4 heads on 2, hd 64, window 100: 74 us (14.7 + 19.0 + 36.5);
+// Forward and backward of B2 S499 4 heads on 2, hd 64, window 100: 64.5 us (13.4 + 17.8 + 34.4 alone);
 // one group of 128 threads with 2 x 4 pairs (6 reads for 32 FMAs) took 98 us, a warp per row
 // and one key at a time 643 us.
 // Three kernels: the forward, dQ (query tile, walking keys), dK/dV (key tile, walking queries
@@ -88,7 +88,7 @@ __device__ __forceinline__ void products(float (&acc)[4][4], const float *x, con
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[r][j] = 0.f;
   const float *x0 = x + 4 * ty * (HDP + 4), *y0 = y + tx * (HDP + 4);
-#pragma unroll 2
+#pragma unroll 4
   for (int d = 0; d < HDP; d += 4) {
     float4 xv[4], yv[4];
 #pragma unroll
@@ -228,6 +228,7 @@ __host__ __device__ constexpr int query_floats() {
 // Forward: block = (batch, head, query tile).
 template <int HDP>
 __global__ void __launch_bounds__(kF32Threads) window_fwd_f32_kernel(const F32Args a) {
+  grid_dep_wait();
   extern __shared__ __align__(16) float f32_smem[];
   constexpr int kTile = tile_floats<HDP>();
   const Place w(a);
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kF32Threads) window_fwd_f32_kernel(const F32Ar
 // writes D_i = dO_i . o_i for the dK/dV kernel.
 template <int HDP>
 __global__ void __launch_bounds__(kF32Threads) window_dq_f32_kernel(const F32Args a) {
+  grid_dep_wait();
   extern __shared__ __align__(16) float f32_smem[];
   constexpr int kTile = tile_floats<HDP>();
   const Place w(a);
@@ -405,6 +407,7 @@ __host__ __device__ constexpr int key_floats() {
 template <int HDP>
 __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kF32Threads) window_dkdv_f32_kernel(const F32Args a) {
   namespace cg = cooperative_groups;
+  grid_dep_wait();
   extern __shared__ __align__(16) float f32_smem[];
   constexpr int kTile = tile_floats<HDP>();
   const int g = threadIdx.x / kGroup, t = threadIdx.x % kGroup, tx = t % 8, ty = t / 8;
@@ -495,16 +498,16 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kF32Threads) wi
 
 bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Ordinary launches: blocks that start early under programmatic launches pile up on the SMs
-// the kernel before them leaves free (the three kernels 140 us instead of 98 with 2 x 4 pairs).
+// Programmatic launches that no kernel triggers early: a kernel is set up while the one before it
+// ends, but its blocks do not start on the SMs that one leaves free, where they would pile up
+// (the three kernels 140 us instead of 98 with 2 x 4 pairs).
 template <typename Kernel>
 cudaError_t launch(Kernel *kernel, std::atomic<unsigned long long> &allowed, long long blocks, int floats,
                    const F32Args &a, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(floats) * sizeof(float);
   const cudaError_t err = allow_smem(kernel, smem, allowed);
   if (err != cudaSuccess) return err;
-  kernel<<<static_cast<unsigned>(blocks), kF32Threads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kernel, static_cast<unsigned>(blocks), kF32Threads, smem, stream, a);
 }
 
 template <int HDP>
