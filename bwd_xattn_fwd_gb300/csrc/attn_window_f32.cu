@@ -396,7 +396,9 @@ __global__ void __launch_bounds__(kF32Threads) window_dq_f32_kernel(const F32Arg
 // dK, dV: a cluster of kParts blocks = (batch, kv head, key tile); its (head of the group,
 // query tile) pairs go round the 2 kParts groups, so that a sink tile, which every query sees,
 // is not one block's chain; the parts are added in order through distributed shared memory.
-constexpr int kParts = 4;
+// kParts is 4, or 8 where that leaves a block an SM (B1 S200, 14 key tiles: 11.5 us, 16.5 with 4;
+// B4 S300, 80 key tiles: 39.3 and 27.2).
+constexpr int kSms = 152;
 
 // Shared memory: K, V; per group q, dO twice; per group P and dS; per group lse and D of 32 rows.
 template <int HDP>
@@ -404,7 +406,7 @@ __host__ __device__ constexpr int key_floats() {
   return 10 * tile_floats<HDP>() + 4 * kPairs + 4 * kT;
 }
 
-template <int HDP>
+template <int HDP, int kParts>
 __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kF32Threads) window_dkdv_f32_kernel(const F32Args a) {
   namespace cg = cooperative_groups;
   grid_dep_wait();
@@ -519,7 +521,7 @@ cudaError_t launch_fwd(const F32Args &a, cudaStream_t stream) {
 
 template <int HDP>
 cudaError_t launch_bwd(const F32Args &a, float *dk, float *dv, cudaStream_t stream) {
-  static std::atomic<unsigned long long> allowed_q{0}, allowed_kv{0};
+  static std::atomic<unsigned long long> allowed_q{0}, allowed_kv{0}, allowed_kv8{0};
   const long long tiles = (a.S + kT - 1) / kT;
   const cudaError_t err =
       launch(window_dq_f32_kernel<HDP>, allowed_q, tiles * a.B * a.nh, query_floats<HDP, 3>(), a, stream);
@@ -527,7 +529,10 @@ cudaError_t launch_bwd(const F32Args &a, float *dk, float *dv, cudaStream_t stre
   F32Args kv = a;
   kv.out = dk;
   kv.out2 = dv;
-  return launch(window_dkdv_f32_kernel<HDP>, allowed_kv, tiles * a.B * a.nkv * kParts, key_floats<HDP>(), kv, stream);
+  const long long units = tiles * a.B * a.nkv;
+  if (units * 8 <= kSms)
+    return launch(window_dkdv_f32_kernel<HDP, 8>, allowed_kv8, units * 8, key_floats<HDP>(), kv, stream);
+  return launch(window_dkdv_f32_kernel<HDP, 4>, allowed_kv, units * 4, key_floats<HDP>(), kv, stream);
 }
 
 }  // namespace

@@ -81,7 +81,8 @@ def test_bf16(shape, deterministic):
 
 
 @pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 1, 0), (2, 70, 4, 2, 24, 9, 0), (1, 130, 2, 2, 64, 33, 5),
-                                   (1, 260, 2, 1, 128, 64, 70), (1, 90, 3, 3, 33, 500, 0), (1, 90, 3, 1, 5, 1, 200)],
+                                   (1, 260, 2, 1, 128, 64, 70), (1, 90, 3, 3, 33, 500, 0), (1, 90, 3, 1, 5, 1, 200),
+                                   (2, 499, 4, 2, 64, 100, 3), (3, 333, 4, 2, 128, 40, 33), (9, 70, 3, 3, 20, 9, 0)],
                          ids=str)
 def test_f32(shape):
     B, S, nh, nkv, hd, window, sinks = shape
