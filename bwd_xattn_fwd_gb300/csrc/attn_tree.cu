@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
     // before that piece's result is written (after it with kSplit = 1, whose rows of 128 scores
     // leave none: hd 128 48.7 against 45.2 us), and then put in place.
     uint4 xq[HD / 8];
-    unsigned long long word = 0;
+    unsigned long long word = 0, all_words[2] = {0, 0};
     auto load_rows = [&](bool ahead) {
       const int row0 = (walk.unit % row_tiles) * kRows, rho = row0 + row;
       const bool mine = rho < rows_all;
@@ -500,6 +500,12 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c) xq[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
       word = !mine ? 0 : (a.tree ? __ldg(a.tree + at) : (2ull << token) - 1);   // (not used here: no wait)
+      // Tokens lane and lane + 32 of the sequence. (Four copies: the warp's own rows are all of them.)
+      if (kSplit < 4 && a.tree) {
+        const unsigned long long *words = a.tree + static_cast<size_t>(walk.b) * a.n;
+        all_words[0] = lane < a.n ? __ldg(words + lane) : 0;
+        all_words[1] = lane + 32 < a.n ? __ldg(words + lane + 32) : 0;
+      }
     };
     // Nothing for the combine until the run's end says otherwise (a run that gives up says
     // nothing).
@@ -538,8 +544,21 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
       warp_arrive(q_full, lane);
       // The row's ancestors and how far its window reaches.
       // Bits past the last new token mean nothing.
-      const unsigned long long seen = word & (a.n == 64 ? ~0ull : (1ull << a.n) - 1);
-      const int far = s.ctx + max(__popcll(seen) - 1, 0) - a.window + 1;
+      const unsigned long long in_tree = a.n == 64 ? ~0ull : (1ull << a.n) - 1, seen = word & in_tree;
+      auto depth_of = [&](unsigned long long w) { return max(__popcll(w & in_tree) - 1, 0); };
+      const int far = s.ctx + depth_of(word) - a.window + 1;
+      // What some token of the sequence sees: new tokens, and committed positions from far_any on.
+      unsigned long long seen_any = in_tree;
+      int far_any = s.far;
+      if (a.tree) {
+        const unsigned long long x = kSplit == 4 ? seen : (all_words[0] | all_words[1]) & in_tree;
+        seen_any = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(x)) |
+                   static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(x >> 32))) << 32;
+        int depth = 64;
+        if (kSplit == 4 ? mine : lane < a.n) depth = depth_of(kSplit == 4 ? word : all_words[0]);
+        if (kSplit < 4 && lane + 32 < a.n) depth = min(depth, depth_of(all_words[1]));
+        far_any = s.ctx + __reduce_min_sync(0xffffffffu, depth) - a.window + 1;
+      }
       float mrow = -INFINITY, lrow = 0.f;
       // One tile: this copy's kCols columns. vis: a word per 32 columns. With few columns a
       // thread always masks; 128 have a copy without masks for the tiles that every row sees
@@ -640,10 +659,12 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
               there = ((held >> (col / 16)) & 1u ? 0x0000ffffu : 0u) | ((held >> (col / 16 + 1)) & 1u ? 0xffff0000u : 0u);
             vis[w] = m & there;
           }
-          // V rows that no row sees may hold anything: they are zeroed before P V, in which
-          // their P is 0 (0 x NaN would not be). Missing pages were loaded as zeros.
-          const int p = t0 + lane_row;
-          if (p >= s.end || (p < s.far && p >= a.sinks)) {
+          // V rows that no token sees may hold anything -- behind the cache, behind every token's
+          // window, drafted rows that no word names (the spare ones of a smaller tree) -- and are
+          // zeroed before P V, in which their P is 0 (0 x NaN would not be). Missing pages were
+          // loaded as zeros.
+          const int p = t0 + lane_row, off = p - s.ctx;
+          if (off < 0 ? p < far_any && p >= a.sinks : off >= a.n || ((seen_any >> off) & 1u) == 0u) {
 #pragma unroll
             for (int c = 0; c < L::kSubTiles; ++c)
 #pragma unroll

@@ -395,3 +395,59 @@ def test_tensors_that_do_not_fit_are_refused_and_nothing_is_written():
     torch.cuda.synchronize()
     assert torch.equal(k.view(torch.int16), before[0].view(torch.int16))
     assert torch.equal(v.view(torch.int16), before[1].view(torch.int16))
+
+
+def _hide(k, v, table, lens, words, window, sinks, page, n):
+    """NaN in K and V of every position of the sequences that no token sees."""
+    hidden = 0
+    for b, ctx in enumerate(lens):
+        seen = 0
+        for w in words[b]:
+            w &= (1 << n) - 1
+            near = max(ctx + max(bin(w).count("1") - 1, 0) - window + 1, 0)
+            seen |= ((1 << ctx) - 1) & ~((1 << min(near, ctx)) - 1) | (1 << min(sinks, ctx)) - 1 | w << ctx
+        rows = [table[b][p // page] * page + p % page for p in range(ctx + n) if not (seen >> p) & 1]
+        hidden += len(rows)
+        for pool in (k, v):
+            pool.view(-1, *pool.shape[2:])[rows] = math.nan
+    return hidden
+
+
+# (B, n, nh, nkv, hd, page, longest cache, window, sinks): tiles of 32, 64 and 128 rows, and several;
+# whole units (short tables), cut ones, and calls that choose
+UNSEEN_CASES = [
+    (3, 8, 4, 1, 64, 16, 500, BIG, 0),
+    (3, 6, 4, 1, 32, 32, 700, 90, 3),
+    (5, 16, 16, 4, 64, 64, 3000, BIG, 0),
+    (5, 16, 16, 4, 128, 16, 2500, 300, 4),
+    (4, 9, 14, 2, 32, 16, 900, 70, 0),
+    (4, 30, 16, 4, 64, 16, 1500, 200, 100),
+    (3, 64, 8, 2, 64, 128, 600, BIG, 0),
+    (3, 61, 16, 2, 128, 64, 3000, 500, 4),
+    (60, 8, 16, 4, 64, 64, 1800, BIG, 0),
+    (60, 12, 16, 4, 64, 16, 1800, 128, 4),
+]
+
+
+@pytest.mark.parametrize("case", UNSEEN_CASES, ids=str)
+def test_positions_that_no_token_sees_may_hold_nan(case):
+    """A batch of trees of different sizes: spare tokens have words of 0 and rows that nobody wrote;
+    tokens that no word names; and trees without a token of depth 0, whose windows all end before
+    the first token's would."""
+    B, n, nh, nkv, hd, page, top, window, sinks = case
+    rng = random.Random(n)
+    lens = [top - 37 * b % (top // 2) for b in range(B)]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=n, device="cuda")
+    words = random_words(B, n, seed=5)
+    for b in range(B):
+        if b % 3 == 0:                                   # a smaller tree
+            words[b][rng.randint(1, n - 1):] = [0] * n
+            del words[b][n:]
+        elif b % 3 == 1:                                 # token n - 2 named by nobody, not by itself
+            words[b] = [w & ~(1 << (n - 2)) for w in words[b]]
+        else:                                            # every token has at least three ancestors
+            words[b] = [w | 0b1111 for w in words[b]]
+    assert _hide(k, v, table, lens, words, window, sinks, page, n) >= 2
+    q = _q(B, n, nh, hd, seed=n)
+    o, lse = _attend(q, k, v, table, lens, words, window, sinks)
+    check_tree(o, lse, tree_reference(q, k, v, table, lens, words, window, sinks, hd ** -0.5), str(case))
