@@ -703,9 +703,11 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
         XATTN_DCHECK(r >= rows || at < static_cast<size_t>(a.B) * a.n * a.nh, a.status);
         return at;
       };
+      // (Here and in the combine a sum of 0 is a row that saw nothing; NaN, of a query or of scores
+      // that are no numbers, is not 0 and stays.)
       auto put_stats = [&](float M, float sum) {
         if (whole)
-          a.lse[out_of(row)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+          a.lse[out_of(row)] = sum != 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
         else
           *reinterpret_cast<float2 *>(a.ws_ml + 2 * (rec0 + row)) = make_float2(M, sum);
       };
@@ -727,11 +729,11 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
 #pragma unroll
         for (int k = 0; k < kSplit; ++k) {
           const float2 ml = stat[k * kRows + row];
-          const float w = ml.y > 0.f ? ex2_approx(ml.x - M) : 0.f;
+          const float w = ml.y != 0.f ? ex2_approx(ml.x - M) : 0.f;
           sum = fmaf(ml.y, w, sum);
           if (k == copy) weight = w;
         }
-        if (whole && sum > 0.f) weight /= sum;
+        if (whole && sum != 0.f) weight /= sum;
         warp_arrive(meet, lane);
         if (mine && copy == 0) put_stats(M, sum);
         if (!tree_wait(o_done, (R - 1) & 1, ctl) || !tree_wait(meet, meets++ & 1, ctl)) { ok = false; break; }
@@ -751,7 +753,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
             reg_fence<kOnce>(ov);
             // A copy that saw nothing counts 0, whatever its O holds.
 #pragma unroll
-            for (int e = 0; e < kOnce; ++e) x[e] = weight > 0.f ? __uint_as_float(ov[e]) * weight : 0.f;
+            for (int e = 0; e < kOnce; ++e) x[e] = weight != 0.f ? __uint_as_float(ov[e]) * weight : 0.f;
           };
           float x[kOnce];
 #pragma unroll 1
@@ -807,7 +809,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
               tmem_wait_ld();
               reg_fence<32>(ov);
               // A copy that saw nothing counts 0, whatever its O holds.
-              auto val = [&](int x) { return weight > 0.f ? __uint_as_float(ov[x]) * weight : 0.f; };
+              auto val = [&](int x) { return weight != 0.f ? __uint_as_float(ov[x]) * weight : 0.f; };
 #pragma unroll
               for (int x = 0; x < 8; ++x)
                 if (here && (HD > 32 || (c + x >= p0 && c + x < p0 + pieces)))
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
         if (!tree_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         const size_t out = mine ? out_of(row) : 0;
-        const float inv = lrow > 0.f ? 1.f / lrow : 0.f;
+        const float inv = lrow != 0.f ? 1.f / lrow : 0.f;
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           uint32_t ov[32];
@@ -847,7 +849,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas<HD, kSplit>())
           tmem_wait_ld();
           reg_fence<32>(ov);
           if (mine && whole) {
-            auto val = [&](int i) { return lrow > 0.f ? __uint_as_float(ov[i]) * inv : 0.f; };
+            auto val = [&](int i) { return lrow != 0.f ? __uint_as_float(ov[i]) * inv : 0.f; };
             uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * HD + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -944,7 +946,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int
         ml = *reinterpret_cast<const float2 *>(a.ws_ml + 2 * rec);
         x = *reinterpret_cast<const float4 *>(a.ws_o + rec * HD + 4 * i);
       }
-      if (ml_here.y > 0.f) {
+      if (ml_here.y != 0.f) {
         const float m2 = fmaxf(M, ml_here.x), f0 = ex2_approx(M - m2), f1 = ex2_approx(ml_here.x - m2);
         M = m2;
         sum = sum * f0 + ml_here.y * f1;
@@ -964,7 +966,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = part_ml[w][lane];
         const float4 x = part[w][lane];
-        const float f = ml.y > 0.f ? ex2_approx(ml.x - M) : 0.f;
+        const float f = ml.y != 0.f ? ex2_approx(ml.x - M) : 0.f;
         sum = fmaf(ml.y, f, sum);
         acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
         acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
@@ -972,13 +974,13 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int
       __syncthreads();                                      // before the next rows overwrite part
     }
     if (rb + sub < rows && (!wide || warp == 0)) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
       const int rho = row0 + row;
       const size_t out =
           (static_cast<size_t>(plan.x) * a.n + rho / group) * a.nh + static_cast<size_t>(kvh) * group + rho % group;
       *reinterpret_cast<uint2 *>(a.o + out * HD + 4 * i) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (i == 0) a.lse[out] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+      if (i == 0) a.lse[out] = sum != 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
     }
   }
 }

@@ -451,3 +451,27 @@ def test_positions_that_no_token_sees_may_hold_nan(case):
     q = _q(B, n, nh, hd, seed=n)
     o, lse = _attend(q, k, v, table, lens, words, window, sinks)
     check_tree(o, lse, tree_reference(q, k, v, table, lens, words, window, sinks, hd ** -0.5), str(case))
+
+
+@pytest.mark.parametrize("n,nh,hd,top", [(4, 4, 64, 600), (4, 4, 64, 20000), (12, 4, 32, 9000), (40, 4, 128, 9000),
+                                         (40, 4, 64, 700)])
+def test_scores_that_are_no_numbers_are_not_rows_that_see_nothing(n, nh, hd, top):
+    """A query that holds NaN, and one whose scores overflow: o and lse of those rows are NaN, as a
+    softmax in fp32 gives them, and not the 0 and -inf of a row that sees nothing; other rows are
+    as right as without them."""
+    B, nkv, page, lens = 2, 1, 64, [top, top // 3]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=6, device="cuda")
+    q = _q(B, n, nh, hd, seed=6)
+    bad = torch.zeros(B, n, nh, dtype=torch.bool, device="cuda")
+    bad[0, 1, 2] = bad[1, n - 1, 0] = True
+    q[0, 1, 2, 5] = math.nan
+    q[1, n - 1, 0] = 3e38
+    k.masked_fill_(k.isnan(), 0.0)
+    for b in range(B):                                   # one key of large numbers: q . k is +inf for that query
+        k.view(-1, nkv, hd)[table[b][0] * page + 3] = 2.0
+    o, lse = _attend(q, k, v, table, lens, None, BIG, 0)
+    assert bool(o[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    q[bad] = 0.0
+    ref = tree_reference(q, k, v, table, lens, None, BIG, 0, hd ** -0.5)
+    o[bad], lse[bad] = ref[0][0][bad].to(o.dtype), ref[1][0][bad].float()
+    check_tree(o, lse, ref, "the other rows")
