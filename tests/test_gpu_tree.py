@@ -475,3 +475,24 @@ def test_scores_that_are_no_numbers_are_not_rows_that_see_nothing(n, nh, hd, top
     ref = tree_reference(q, k, v, table, lens, None, BIG, 0, hd ** -0.5)
     o[bad], lse[bad] = ref[0][0][bad].to(o.dtype), ref[1][0][bad].float()
     check_tree(o, lse, ref, "the other rows")
+
+
+@pytest.mark.parametrize("case", [(6, 4, 4, 1, 64, 16, 700), (6, 4, 16, 4, 128, 64, 4000), (5, 16, 16, 4, 64, 64, 5000),
+                                  (9, 14, 8, 2, 32, 32, 3000), (5, 48, 16, 2, 64, 16, 2500), (4, 64, 4, 2, 128, 64, 900),
+                                  (70, 8, 8, 2, 64, 64, 1700)], ids=str)
+def test_a_sequence_does_not_depend_on_the_others(case):
+    """Units of different sequences share a CTA's tiles and the records of cut ones: with the lengths
+    as they were, new K, V and queries of all other sequences leave a sequence's bits alone."""
+    B, n, nh, nkv, hd, page, top = case
+    lens = [top - 61 * b % (top // 2) for b in range(B)]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=3, device="cuda")
+    q, words = _q(B, n, nh, hd, 3), random_words(B, n, 3)
+    o, lse = _attend(q, k, v, table, lens, words, BIG, 0)
+    g = torch.Generator("cuda").manual_seed(1)
+    for kept in (0, B // 2, B - 1):
+        pages = torch.tensor([e for e in table[kept] if e >= 0], device="cuda")
+        k2, v2, q2 = (torch.randn(t.shape, generator=g, device="cuda").to(t.dtype) for t in (k, v, q))
+        k2[pages], v2[pages], q2[kept] = k[pages], v[pages], q[kept]
+        o2, lse2 = _attend(q2, k2, v2, table, lens, words, BIG, 0)
+        assert torch.equal(o2[kept], o[kept]) and torch.equal(lse2[kept], lse[kept])
+        assert not torch.equal(o2[kept - 1], o[kept - 1])
