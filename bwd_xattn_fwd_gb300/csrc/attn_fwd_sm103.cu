@@ -467,6 +467,12 @@ __global__ void __maxnreg__(168)
     // is the tile's only user (tile mB when there is a tile B; every tile when there is
     // not). An issuer never arrives for a tile it does not use, so its arrivals cannot
     // land in an earlier phase of the stage that the other issuer has not released yet.
+    // A barrier tells only its last two phases apart: when an issuer waits for a stage whose use
+    // before it skipped, that use's copy has to have landed. It has: the tile r that A skips
+    // (mB) because B releases tile r - 1 only after its wait for r; the units that B skips
+    // (they come first) because A does the same, and because their Q comes after the products of
+    // the unit two before -- but not with three query tiles, whose units without a B have no more
+    // tiles than the ring (launch_fwd_bf16; tests/test_forward_ring.py has the schedule).
     // With a window the two sides differ in more tiles, and either may be the slower one: each
     // passes the tiles that it does not use as well, waiting for them and releasing them, so
     // every tile has one release from each side and no side's wait for a stage can fall two
@@ -825,6 +831,13 @@ cudaError_t launch_fwd(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 cudaError_t launch_fwd_bf16(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                             __nv_bfloat16 *o, float *lse, int B, int S, int nh, int nkv, int hd,
                             float scale, int *status, uint64_t timeout_ns, cudaStream_t stream) {
+  // Three query tiles at hd 32 and 64 (S 257 .. 384): as the window of everything, which gives the
+  // same bits and whose issuers pass the tiles they do not use. There, with the causal kernel's, issuer
+  // B could take a copy of an earlier unit for its own if Q overtook it (at hd 128 the one Q
+  // buffer keeps it from that). B64 S384, 8 heads on 2 / on 8, hd 64: 31.1 / 31.1 us the causal kernel,
+  // 32.1 / 33.7 this way; a wait in the causal kernel cost other lengths 1 to 2 %.
+  if ((S + kTileRows - 1) / kTileRows == 3 && hd != 128)
+    return launch_fwd<true>(mq, mk, mv, o, lse, B, S, nh, nkv, hd, scale, S, 0, status, timeout_ns, stream);
   return launch_fwd<false>(mq, mk, mv, o, lse, B, S, nh, nkv, hd, scale, 0, 0, status, timeout_ns, stream);
 }
 
