@@ -8,7 +8,8 @@ the library has not been built, importing this module raises at once.
 The functions named like the C entry points (``xattn_fwd``, ``xattn_bwd``, ...)
 take the same arguments in the same order; tensor arguments may be torch tensors
 or raw integer addresses. ``attention_fwd`` / ``attention_bwd`` allocate the
-outputs with torch and call them.
+outputs with torch and call them. The C-level functions take raw addresses and stream handles
+without torch.
 """
 from __future__ import annotations
 
@@ -16,11 +17,6 @@ import ctypes
 import enum
 import importlib.util
 import os
-
-try:
-    import torch
-except ImportError:      # the C entry points take raw addresses and stream handles without it
-    torch = None
 
 from . import build as _build
 
@@ -342,6 +338,7 @@ def attention_decode(q, k_cache, v_cache, scale=None, stream=None):
 
 def _load_calls():
     """The native part of the calls below, bound to this library's entry points."""
+    import torch  # noqa: F401  (its libraries)
     path = _build.torch_lib()
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built: run `python bwd_xattn_fwd_gb300/build.py` first")
@@ -354,7 +351,16 @@ def _load_calls():
     return module
 
 
-_calls = _load_calls() if torch else None
+class _Unloaded:
+    """Stands for the native part until the first of the calls below; nothing else needs it."""
+
+    def __getattr__(self, name):
+        global _calls
+        _calls = _load_calls()
+        return getattr(_calls, name)
+
+
+_calls = _Unloaded()
 
 
 class _Elsewhere:
@@ -362,6 +368,7 @@ class _Elsewhere:
     None: the device's current one) the one that torch allocates on and that calls launch on."""
 
     def __init__(self, t, stream):
+        import torch
         device = t.device
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
@@ -383,6 +390,7 @@ def _again(name, status, call, where, stream, tensors):
     """What a native call that returned no outputs asks for: raises its status; or, when the
     tensors do not fit, says what is wrong with the first that does not; or, when they are
     all on another device than the current one, makes that one current and calls again."""
+    import torch
     if status is not None:
         raise XattnError(status, name)
     device = None
@@ -407,6 +415,7 @@ def _again(name, status, call, where, stream, tensors):
 
 
 def _need_dims(name, **tensors):
+    import torch
     for label, (t, dims) in tensors.items():
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             raise ValueError(f"{name}: {label} must be a tensor of {dims} dimensions")
@@ -421,6 +430,7 @@ def attention_window_fwd(q, k, v, window, sinks=0, scale=None, stream=None):
     out = _calls.window_fwd(q, k, v, window, sinks, scale)
     if type(out) is tuple:
         return out
+    import torch
     name = "attention_window_fwd"
     _need_dims(name, q=(q, 4), k=(k, 4))
     kv, dtype = (*q.shape[:2], k.shape[2], q.shape[3]), q.dtype if q.dtype == torch.float32 else torch.bfloat16
@@ -437,6 +447,7 @@ def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, strea
     out = _calls.window_bwd(q, k, v, o, dO, lse, window, sinks, scale, deterministic)
     if type(out) is tuple:
         return out
+    import torch
     name = "attention_window_bwd"
     _need_dims(name, q=(q, 4), k=(k, 4))
     kv, dtype = (*q.shape[:2], k.shape[2], q.shape[3]), q.dtype if q.dtype == torch.float32 else torch.bfloat16
@@ -447,6 +458,7 @@ def attention_window_bwd(q, k, v, o, dO, lse, window, sinks=0, scale=None, strea
 
 
 def _pool(name, k_pages, v_pages, page_table, ctx_lens):
+    import torch
     _need_dims(name, k_pages=(k_pages, 4), page_table=(page_table, 2))
     return (("k_pages", k_pages, k_pages.shape, torch.bfloat16), ("v_pages", v_pages, k_pages.shape, torch.bfloat16),
             ("page_table", page_table, page_table.shape, torch.int32),
@@ -467,6 +479,7 @@ def attention_tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree=None, 
     out = _calls.tree_decode(q, k_pages, v_pages, page_table, ctx_lens, tree, window, sinks, scale)
     if type(out) is tuple:
         return out
+    import torch
     name = "attention_tree_decode"
     tensors = _pool(name, k_pages, v_pages, page_table, ctx_lens)
     _need_dims(name, q=(q, 4))
@@ -486,6 +499,7 @@ def cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens, stream=No
     out = _calls.cache_append(k_new, v_new, k_pages, v_pages, page_table, ctx_lens)
     if out is True:
         return None
+    import torch
     name = "cache_append"
     tensors = _pool(name, k_pages, v_pages, page_table, ctx_lens)
     _need_dims(name, k_new=(k_new, 4))
@@ -503,6 +517,7 @@ def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream
     out = _calls.cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted)
     if out is True:
         return None
+    import torch
     name = "cache_compact"
     tensors = _pool(name, k_pages, v_pages, page_table, ctx_lens)
     _need_dims(name, path=(path, 2))

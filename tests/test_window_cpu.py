@@ -1,5 +1,8 @@
 """Window attention's argument checks, and its 64-bit reference against differences, without a GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -101,3 +104,30 @@ def test_reference_gradients_against_differences(window, sinks):
         h = 1e-5
         slope = (loss({name: x[name] + h * d}) - loss({name: x[name] - h * d})) / (2 * h)
         assert abs(float((ref["d" + name][0] * d).sum()) - slope) <= 1e-7 * (1 + abs(slope))
+
+
+WITHOUT_EXTENSION = """
+import sys
+from bwd_xattn_fwd_gb300 import build
+build.torch_lib = lambda: "/nonexistent/xattn_torch.so"
+from bwd_xattn_fwd_gb300 import xattn
+assert "torch" not in sys.modules
+try:
+    xattn.xattn_window_fwd(0, 32, 48, 1, 4, 2, 1, 64, 2, 0, 0.1, 64, 80, stream=0)
+except xattn.XattnError as err:
+    assert err.status == xattn.Status.ERR_NULL_PTR
+import torch
+q = torch.zeros(1, 4, 2, 64)
+try:
+    xattn.attention_window_fwd(q, q, q, 2)
+except ImportError as err:
+    print("needs", err)
+"""
+
+
+def test_the_c_entry_points_need_neither_torch_nor_the_extension(lib):
+    """The binding imports, and its C-level functions run, before torch and without the native
+    part of the tensor-level calls; the first of those says what is missing."""
+    run = subprocess.run([sys.executable, "-c", WITHOUT_EXTENSION], capture_output=True, text=True,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0 and "/nonexistent/xattn_torch.so is not built" in run.stdout, run.stderr
