@@ -5,7 +5,8 @@ library with the CUDA runtime linked statically (so the library loads on a machi
 without a GPU driver; the driver is reached at the first CUDA call).
 
 csrc/xattn_torch.cpp, the native part of the binding's tensor-level calls, compiles beside them
-against the installed torch (its file carries torch's version: another torch builds another).
+against the installed torch and the running Python (its file carries both versions: another torch
+or Python builds another).
 
 `--debug` (build(debug=True)) builds the same library with XATTN_DEBUG -- on-device bounds
 checks that report XATTN_ERR_DEVICE_BOUNDS -- into _build_debug/ (load it by pointing
@@ -51,8 +52,12 @@ def torch_dir():
 
 
 def torch_lib() -> str:
-    """The native part of the tensor-level calls for the installed torch ("" without torch)."""
-    return os.path.join(BUILD, f"xattn_torch-{importlib.metadata.version('torch')}.so") if torch_dir() else ""
+    """The native part of the tensor-level calls for the installed torch and this Python's ABI
+    ("" without torch)."""
+    if not torch_dir():
+        return ""
+    version = f"{importlib.metadata.version('torch')}.{sysconfig.get_config_var('SOABI')}"
+    return os.path.join(BUILD, f"xattn_torch-{version}.so")
 
 
 def _torch_current() -> bool:

@@ -131,3 +131,14 @@ def test_the_c_entry_points_need_neither_torch_nor_the_extension(lib):
     run = subprocess.run([sys.executable, "-c", WITHOUT_EXTENSION], capture_output=True, text=True,
                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert run.returncode == 0 and "/nonexistent/xattn_torch.so is not built" in run.stdout, run.stderr
+
+
+def test_the_extension_is_one_python_s(monkeypatch):
+    """A Python extension belongs to an ABI as well as to a torch version: its file names both."""
+    import importlib.metadata
+    import sysconfig
+    from bwd_xattn_fwd_gb300 import build
+    here = build.torch_lib()
+    assert importlib.metadata.version("torch") in here and sysconfig.get_config_var("SOABI") in here
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-other")
+    assert build.torch_lib() != here
