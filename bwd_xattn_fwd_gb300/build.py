@@ -6,7 +6,7 @@ without a GPU driver; the driver is reached at the first CUDA call).
 
 csrc/xattn_torch.cpp, the native part of the binding's tensor-level calls, compiles beside them
 against the installed torch and the running Python (its file carries both versions: another torch
-or Python builds another).
+or Python builds another; without a torch for CUDA there is none).
 
 `--debug` (build(debug=True)) builds the same library with XATTN_DEBUG -- on-device bounds
 checks that report XATTN_ERR_DEVICE_BOUNDS -- into _build_debug/ (load it by pointing
@@ -53,8 +53,8 @@ def torch_dir():
 
 def torch_lib() -> str:
     """The native part of the tensor-level calls for the installed torch and this Python's ABI
-    ("" without torch)."""
-    if not torch_dir():
+    ("" without a torch for CUDA)."""
+    if not torch_dir() or not os.path.exists(os.path.join(torch_dir(), "lib", "libc10_cuda.so")):
         return ""
     version = f"{importlib.metadata.version('torch')}.{sysconfig.get_config_var('SOABI')}"
     return os.path.join(BUILD, f"xattn_torch-{version}.so")
@@ -99,7 +99,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
         extra = (*extra, "-DXATTN_DEBUG")
     torch_tmp = ""
     procs = []
-    if force or not _torch_current():
+    if torch_lib() and (force or not _torch_current()):
         os.makedirs(BUILD, exist_ok=True)
         torch_tmp = torch_lib() + f".tmp{os.getpid()}"
         procs.append((TORCH_SRC, subprocess.Popen(_torch_command(torch_tmp), stdout=subprocess.PIPE,

@@ -340,6 +340,8 @@ def _load_calls():
     """The native part of the calls below, bound to this library's entry points."""
     import torch  # noqa: F401  (its libraries)
     path = _build.torch_lib()
+    if not path:
+        raise ImportError("the tensor-level calls need a torch built for CUDA")
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built: run `python bwd_xattn_fwd_gb300/build.py` first")
     spec = importlib.util.spec_from_file_location("xattn_torch", path)

@@ -142,3 +142,15 @@ def test_the_extension_is_one_python_s(monkeypatch):
     assert importlib.metadata.version("torch") in here and sysconfig.get_config_var("SOABI") in here
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-other")
     assert build.torch_lib() != here
+
+
+def test_a_torch_without_cuda_has_no_extension(monkeypatch, tmp_path):
+    """There is nothing to build then, the library is built all the same, and the tensor-level calls
+    say what they lack."""
+    from bwd_xattn_fwd_gb300 import build, xattn
+    (tmp_path / "lib").mkdir()
+    monkeypatch.setattr(build, "torch_dir", lambda: str(tmp_path))
+    assert build.torch_lib() == "" and build._torch_current()
+    assert build.build() == build.LIB
+    with pytest.raises(ImportError, match="CUDA"):
+        xattn._load_calls()
