@@ -100,8 +100,9 @@ xattn_status device_info(DeviceInfo **out) {
 // Scratch of one call on `stream`, released with cudaFreeAsync on it. It comes from a pool of
 // the library's own that keeps what it has grown to: the default pool gives its memory back
 // at every synchronisation, and the next call would map it again (step of B8 S2048, each
-// call waited for: 471 us with the default pool against 134 us back to back).
-xattn_status scratch_alloc(DeviceInfo &d, size_t bytes, cudaStream_t stream, void **out) {
+// call waited for: 471 us with the default pool against 134 us back to back). xattn_trim_scratch
+// gives it back.
+cudaError_t scratch_pool(DeviceInfo &d) {
   std::call_once(d.pool_once, [&d] {
     const OutsideCapture outside;
     cudaMemPoolProps props = {};
@@ -113,7 +114,11 @@ xattn_status scratch_alloc(DeviceInfo &d, size_t bytes, cudaStream_t stream, voi
     if (d.pool_err == cudaSuccess)
       d.pool_err = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
   });
-  if (d.pool_err == cudaSuccess && cudaMallocFromPoolAsync(out, bytes, d.pool, stream) == cudaSuccess) return XATTN_OK;
+  return d.pool_err;
+}
+
+xattn_status scratch_alloc(DeviceInfo &d, size_t bytes, cudaStream_t stream, void **out) {
+  if (scratch_pool(d) == cudaSuccess && cudaMallocFromPoolAsync(out, bytes, d.pool, stream) == cudaSuccess) return XATTN_OK;
   cudaGetLastError();   // do not leave the failure for the caller's next error check
   return XATTN_ERR_CUDA;
 }
@@ -757,6 +762,16 @@ xattn_status xattn_selftest_bounds_check(void *stream) {
   XATTN_TRY(device_info(&dev));
   bounds_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(dev->status, 1);
   return cuda_status(cudaGetLastError());
+}
+
+xattn_status xattn_trim_scratch(size_t keep_bytes) {
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const OutsideCapture outside;
+  cudaError_t err = scratch_pool(*dev);
+  if (err == cudaSuccess) err = cudaMemPoolTrimTo(dev->pool, keep_bytes);
+  if (err != cudaSuccess) cudaGetLastError();   // do not leave the failure for the caller's next error check
+  return cuda_status(err);
 }
 
 xattn_status xattn_check_device_status(void *stream) {

@@ -79,6 +79,7 @@ _SIGS = {
     "xattn_tree_decode": [_vp] * 6 + [_i] * 10 + [_f] + [_vp] * 3,
     "xattn_cache_append": [_vp] * 6 + [_i] * 7 + [_vp],
     "xattn_cache_compact": [_vp] * 6 + [_i] * 7 + [_vp],
+    "xattn_trim_scratch": [_sz],
     "xattn_check_device_status": [_vp],
 }
 for _name, _args in _SIGS.items():
@@ -249,6 +250,12 @@ def xattn_cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, 
                         max_pages, stream=None):
     _call("xattn_cache_compact", _addr(k_pages), _addr(v_pages), _addr(page_table), _addr(ctx_lens), _addr(path),
           _addr(accepted), B, n, nkv, hd, num_pages, page_size, max_pages, _stream(stream))
+
+
+def xattn_trim_scratch(keep_bytes=0):
+    """Gives back what the current device's scratch pool holds beyond keep_bytes and no call still
+    uses."""
+    _call("xattn_trim_scratch", keep_bytes)
 
 
 def xattn_selftest_wait_timeout(limit_ns, stream=None):

@@ -38,7 +38,7 @@
  *     and finishes; xattn_check_device_status reports it.
  *   - Scratch is stream-ordered: taken on `stream` and released on it when the call's work
  *     is enqueued. The window, tree and fp32 window calls take it from a memory pool of the
- *     library's own (one per device), which keeps what it has grown to until the process ends.
+ *     library's own (one per device), which keeps what it has grown to (xattn_trim_scratch).
  *   - CUDA graphs: the calls may be captured on a stream and replayed, once the device
  *     has seen one ordinary call (the first call on a device looks up its device
  *     status word; make that call outside the capture). Entry points that take
@@ -354,6 +354,14 @@ xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_t
                                  const int *ctx_lens, const int *path, const int *accepted,
                                  int B, int n, int nkv, int hd, int num_pages, int page_size,
                                  int max_pages, void *stream);
+
+/*
+ * Gives back to the driver what the library's scratch pool of the current device holds beyond
+ * keep_bytes and no call still uses (a call uses its scratch until its work on its stream is
+ * over: synchronise first to have all of it given back). The next call that takes scratch maps it
+ * again. Memory of captured graphs belongs to the graphs and is not touched.
+ */
+xattn_status xattn_trim_scratch(size_t keep_bytes);
 
 /* Static text for a status code (never NULL). */
 const char *xattn_status_string(xattn_status status);

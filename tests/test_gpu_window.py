@@ -247,3 +247,29 @@ def test_two_threads_at_once():
     torch.cuda.synchronize()
     for a, b in zip(alone, got):
         assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_the_scratch_can_be_given_back():
+    """A backward's scratch (its fp32 dQ accumulator alone is 4 B S nh hd bytes) stays with the
+    library until it is trimmed; the next call takes new scratch and gives the same bits."""
+    from bwd_xattn_fwd_gb300 import xattn
+    B, S, nh, nkv, hd = 4, 4096, 16, 4, 64
+    x = _inputs(B, S, nh, nkv, hd, "bf16", seed=2)
+    a = _run(x, 700, 4, 0.125)
+    used = 4 * B * S * nh * hd
+    xattn.xattn_trim_scratch(1 << 40)                      # beyond what there is: nothing to give back
+    held = torch.cuda.mem_get_info()[0]
+    xattn.xattn_trim_scratch()
+    assert torch.cuda.mem_get_info()[0] - held >= used
+    b = _run(x, 700, 4, 0.125)
+    for n in ("o", "lse", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        c = xattn.attention_window_fwd(x["q"], x["k"], x["v"], 700, 4, 0.125)
+        xattn.xattn_trim_scratch()                         # takes no part in the capture
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c[0], a["o"])

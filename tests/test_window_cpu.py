@@ -154,3 +154,12 @@ def test_a_torch_without_cuda_has_no_extension(monkeypatch, tmp_path):
     assert build.build() == build.LIB
     with pytest.raises(ImportError, match="CUDA"):
         xattn._load_calls()
+
+
+def test_trimming_the_scratch_needs_a_device(lib):
+    from bwd_xattn_fwd_gb300 import xattn
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    with pytest.raises(xattn.XattnError) as err:
+        xattn.xattn_trim_scratch(1 << 20)
+    assert err.value.status == xattn.Status.ERR_CUDA
