@@ -74,6 +74,15 @@ PyObject *result(int status, std::initializer_list<Tensor> outputs) {
   return tuple;
 }
 
+// The calls that write tensors in place say so to autograd, as torch's in-place operations do (a
+// tensor that some backward saved is then refused there). Inference tensors have no version.
+PyObject *written(int status, std::initializer_list<const Tensor *> tensors) {
+  if (status == XATTN_OK)
+    for (const Tensor *t : tensors)
+      if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+  return result(status, {});
+}
+
 // What every call begins with (the number of arguments), and what follows its checks: the
 // tensors' device is the current one, and this is its stream.
 #define XATTN_CALL(count)                                     \
@@ -227,7 +236,7 @@ PyObject *cache_append(PyObject *, PyObject *const *args, Py_ssize_t n) {
   status = g_cache_append(kn, vn, kp, vp, table, lens, p.B, rows, p.nkv, p.hd, p.num_pages, p.page_size, p.max_pages,
                           stream);
   Py_END_ALLOW_THREADS
-  return result(status, {});
+  return written(status, {p.k, p.v});
   END_HANDLE_TH_ERRORS
 }
 
@@ -248,7 +257,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *args, Py_ssize_t n) {
   status = g_cache_compact(kp, vp, table, lens, pp, ap, p.B, rows, p.nkv, p.hd, p.num_pages, p.page_size, p.max_pages,
                            stream);
   Py_END_ALLOW_THREADS
-  return result(status, {});
+  return written(status, {p.k, p.v});
   END_HANDLE_TH_ERRORS
 }
 

@@ -496,3 +496,31 @@ def test_a_sequence_does_not_depend_on_the_others(case):
         o2, lse2 = _attend(q2, k2, v2, table, lens, words, BIG, 0)
         assert torch.equal(o2[kept], o[kept]) and torch.equal(lse2[kept], lse[kept])
         assert not torch.equal(o2[kept - 1], o[kept - 1])
+
+
+def test_page_calls_tell_autograd_that_they_write():
+    """append and compact raise the pools' version counters as in-place operations do; a refused call
+    does not, and inference tensors (which have none) are taken."""
+    from bwd_xattn_fwd_gb300 import xattn
+    B, n, nkv, hd, page, lens = 2, 4, 2, 64, 16, [10, 0]
+    k, v, table = paged_state(B, n, nkv, hd, page, lens, seed=2, device="cuda")
+    new = torch.zeros(B, n, nkv, hd, dtype=torch.bfloat16, device="cuda")
+    tb, ln, path, acc = _i32(table), _i32(lens), _i32([[0, 2, 3, 0]] * B), _i32([3, 1])
+    weight = torch.ones(hd, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    product = weight * k.nan_to_num_(0.0)                          # saves k for its backward
+    at = k._version, v._version
+    with pytest.raises(ValueError):
+        xattn.cache_append(new, new[:, :2], k, v, tb, ln)
+    assert (k._version, v._version) == at
+    xattn.cache_append(new, new, k, v, tb, ln)
+    assert k._version > at[0] and v._version > at[1]
+    at = k._version, v._version
+    xattn.cache_compact(k, v, tb, ln, path, acc)
+    assert k._version > at[0] and v._version > at[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        product.sum().backward()
+    with torch.inference_mode():
+        ki, vi = k.clone(), v.clone()
+        xattn.cache_append(new, new, ki, vi, tb, ln)
+        xattn.cache_compact(ki, vi, tb, ln, path, acc)
+    torch.cuda.synchronize()
