@@ -188,6 +188,10 @@ xattn_status make_map_aux(CUtensorMap *map, void *ptr, int B, int S, int nh) {
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+template <typename... T>
+bool aligned4(const T *...p) {
+  return (((reinterpret_cast<uintptr_t>(p) & 3u) == 0) && ...);
+}
 
 xattn_status check_shape(int B, int S, int nh, int nkv, int hd, float scale) {
   if (B <= 0 || S <= 0 || nh <= 0 || nkv <= 0 || hd <= 0) return XATTN_ERR_BAD_SHAPE;
@@ -236,8 +240,6 @@ xattn_status check_window(int S, int window, int sinks, int *w, int *s) {
   *s = sinks < S ? sinks : S;
   return XATTN_OK;
 }
-
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Sizes of a paged cache [num_pages, page_size, nkv, hd] and a table of max_pages entries a
 // sequence, for n new tokens a sequence.
@@ -305,7 +307,7 @@ xattn_status xattn_fwd(const void *q, const void *k, const void *v, int B, int S
   if (!q || !k || !v || !o || !lse) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
   XATTN_TRY(check_bf16_fwd(hd));
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return XATTN_ERR_MISALIGNED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse)) return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
   CUtensorMap mq, mk, mv;
@@ -344,7 +346,7 @@ xattn_status xattn_bwd_preprocess(const void *o, const void *dO, const float *ls
   XATTN_TRY(check_shape(B, S, nh, nh, hd, scale));
   XATTN_TRY(check_bwd_scale(scale));
   XATTN_TRY(check_bf16(hd));
-  if (!aligned16(o) || !aligned16(dO)) return XATTN_ERR_MISALIGNED;
+  if (!aligned16(o) || !aligned16(dO) || !aligned4(lse)) return XATTN_ERR_MISALIGNED;
   XATTN_TRY(check_workspace(workspace, workspace_bytes, B, S, nh, hd));
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
@@ -405,7 +407,7 @@ xattn_status xattn_bwd(const void *q, const void *k, const void *v, const void *
   XATTN_TRY(check_bwd_scale(scale));
   XATTN_TRY(check_bf16_fwd(hd));
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) ||
-      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
   // hd = 128: dV, dK and a dQ accumulator do not fit in TMEM together, so dQ comes from
   // the query-stationary kernel (the deterministic backward).
@@ -434,7 +436,7 @@ xattn_status xattn_decode(const void *q, const void *k_cache, const void *v_cach
   const long long chunks = (static_cast<long long>(T) + decode_chunk_keys(hd) - 1) / decode_chunk_keys(hd);
   if (static_cast<long long>(B) * nkv * chunks > 0x7fffffffLL) return XATTN_ERR_BAD_SHAPE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+      !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
@@ -551,7 +553,7 @@ xattn_status xattn_bwd_deterministic(const void *q, const void *k, const void *v
   XATTN_TRY(check_bwd_scale(scale));
   XATTN_TRY(check_bf16_fwd(hd));
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) ||
-      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
@@ -598,7 +600,7 @@ xattn_status xattn_window_fwd(const void *q, const void *k, const void *v, int B
   XATTN_TRY(check_window(S, window, sinks, &w, &s));
   XATTN_TRY(check_bf16_fwd(hd));
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+      !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
@@ -621,7 +623,7 @@ xattn_status xattn_window_bwd(const void *q, const void *k, const void *v, const
   XATTN_TRY(check_bwd_scale(scale));
   XATTN_TRY(check_bf16_fwd(hd));
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) ||
-      !aligned16(dk) || !aligned16(dv) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+      !aligned16(dk) || !aligned16(dv) || !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
@@ -666,6 +668,7 @@ xattn_status xattn_window_fwd_f32(const float *q, const float *k, const float *v
   int w = 0, s = 0;
   XATTN_TRY(check_window(S, window, sinks, &w, &s));
   if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned4(q, k, v, o, lse)) return XATTN_ERR_MISALIGNED;
   if (!window_f32_grid_ok(B, S, nh)) return XATTN_ERR_BAD_SHAPE;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
@@ -681,6 +684,7 @@ xattn_status xattn_window_bwd_f32(const float *q, const float *k, const float *v
   int w = 0, s = 0;
   XATTN_TRY(check_window(S, window, sinks, &w, &s));
   if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned4(q, k, v, o, dO, lse, dq, dk, dv)) return XATTN_ERR_MISALIGNED;
   if (!window_f32_grid_ok(B, S, nh)) return XATTN_ERR_BAD_SHAPE;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
@@ -699,6 +703,7 @@ xattn_status xattn_fwd_f32(const float *q, const float *k, const float *v, int B
   if (!q || !k || !v || !o || !lse) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
   if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned4(q, k, v, o, lse)) return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
   return cuda_status(launch_fwd_f32(q, k, v, o, lse, B, S, nh, nkv, hd, scale,
@@ -711,6 +716,7 @@ xattn_status xattn_bwd_f32(const float *q, const float *k, const float *v, const
   if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
   if (hd > 128) return XATTN_ERR_UNSUPPORTED_HD;
+  if (!aligned4(q, k, v, o, dO, lse, dq, dk, dv)) return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(device_info(&dev));
   return cuda_status(launch_bwd_f32(q, k, v, o, dO, lse, dq, dk, dv, B, S, nh, nkv, hd, scale,
@@ -724,7 +730,7 @@ const char *xattn_status_string(xattn_status s) {
     case XATTN_ERR_BAD_SHAPE: return "B, S, nh, nkv and hd must be positive and within size limits";
     case XATTN_ERR_GROUP: return "nh must be a multiple of nkv";
     case XATTN_ERR_UNSUPPORTED_HD: return "unsupported head dimension (bf16: 32, 64 or 128; the backward's stage calls and xattn_bwd_noalloc: 32 or 64; fp32: <= 128)";
-    case XATTN_ERR_MISALIGNED: return "a bf16 tensor pointer is not 16-byte aligned";
+    case XATTN_ERR_MISALIGNED: return "a bf16 tensor pointer is not 16-byte aligned, or a float or int array not 4-byte";
     case XATTN_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case XATTN_ERR_NO_DEVICE_SUPPORT: return "the current device is not compute capability 10.3 (sm_103)";
     case XATTN_ERR_DEVICE_TIMEOUT: return "a bounded on-device wait expired";

@@ -67,6 +67,7 @@ extern "C" xattn_status xattn_bwd_noalloc(const void *q, const void *k, const vo
   for (const void *p : {q, k, v, o, dO, static_cast<const void *>(dq), static_cast<const void *>(dk),
                         static_cast<const void *>(dv)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return XATTN_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return XATTN_ERR_MISALIGNED;
   const size_t need = xattn_bwd_workspace_bytes(B, S, nh, hd);
   if (need == 0) return XATTN_ERR_BAD_SHAPE;
   if (need > static_cast<size_t>(XATTN_NOALLOC_SCRATCH_BYTES)) return XATTN_ERR_SCRATCH_LIMIT;

@@ -62,7 +62,8 @@ typedef enum {
     XATTN_ERR_UNSUPPORTED_HD = 4,     /* bf16: hd not in {32, 64, 128} (the backward's
                                          stage calls and xattn_bwd_noalloc: {32, 64});
                                          fp32: hd > 128 */
-    XATTN_ERR_MISALIGNED = 5,         /* a bf16 tensor pointer is not 16-byte aligned */
+    XATTN_ERR_MISALIGNED = 5,         /* a bf16 tensor pointer is not 16-byte aligned, or a float
+                                         or int array not 4-byte (xattn_tree_decode's words: 8) */
     XATTN_ERR_CUDA = 6,               /* a CUDA runtime or driver call failed */
     XATTN_ERR_NO_DEVICE_SUPPORT = 7,  /* the current device is not compute capability 10.3 */
     XATTN_ERR_DEVICE_TIMEOUT = 8,     /* a bounded on-device wait expired (reported later) */

@@ -163,3 +163,34 @@ def test_trimming_the_scratch_needs_a_device(lib):
     with pytest.raises(xattn.XattnError) as err:
         xattn.xattn_trim_scratch(1 << 20)
     assert err.value.status == xattn.Status.ERR_CUDA
+
+
+def _causal(lib, name, bad):
+    """A causal entry point with pointer number `bad` two bytes off."""
+    f = getattr(lib, name)
+    n_in, n_out = (3, 2) if "fwd" in name else (6, 3)
+    f.restype, f.argtypes = I, [P] * n_in + [I] * 5 + [F] + [P] * n_out + [P]
+    at = [16 * (i + 1) + (2 if i == bad else 0) for i in range(n_in + n_out)]
+    return f(*at[:n_in], 1, 4, 2, 1, 64, 0.125, *at[n_in:], None)
+
+
+def _window_f32(lib, name, bad):
+    f = getattr(lib, name)
+    n_in, n_out = (3, 2) if "fwd" in name else (6, 3)
+    f.restype, f.argtypes = I, [P] * n_in + [I] * 7 + [F] + [P] * n_out + [P]
+    at = [16 * (i + 1) + (2 if i == bad else 0) for i in range(n_in + n_out)]
+    return f(*at[:n_in], 1, 4, 2, 1, 64, 2, 0, 0.125, *at[n_in:], None)
+
+
+def test_misaligned_floats_are_refused(lib):
+    """A float tensor or lse that is not 4-byte aligned would fault on the device."""
+    for name in ("xattn_window_fwd_f32", "xattn_window_bwd_f32"):
+        for bad in range(5 if "fwd" in name else 9):
+            assert _window_f32(lib, name, bad) == 5, (name, bad)
+    for name in ("xattn_fwd_f32", "xattn_bwd_f32", "xattn_fwd", "xattn_bwd", "xattn_bwd_deterministic",
+                 "xattn_bwd_noalloc"):
+        for bad in range(5 if "fwd" in name else 9):
+            assert _causal(lib, name, bad) == 5, (name, bad)
+    f = lib.xattn_bwd_preprocess
+    f.restype, f.argtypes = I, [P] * 3 + [I] * 4 + [F, P, ctypes.c_size_t, P]
+    assert f(16, 32, 50, 1, 4, 2, 64, 0.125, 256, 1 << 20, None) == 5
