@@ -195,9 +195,10 @@ bool aligned4(const T *...p) {
 
 xattn_status check_shape(int B, int S, int nh, int nkv, int hd, float scale) {
   if (B <= 0 || S <= 0 || nh <= 0 || nkv <= 0 || hd <= 0) return XATTN_ERR_BAD_SHAPE;
-  // Keep every element index and grid size well inside their integer types.
-  const long long elems = static_cast<long long>(B) * S * nh * hd;
-  if (elems > (1ll << 40) || static_cast<long long>(B) * nh * ((S + 127) / 128) > (1ll << 31) - 1)
+  // Keep every element index and grid size well inside their integer types (in doubles: the
+  // products of four ints pass 64 bits).
+  const double heads = static_cast<double>(B) * nh;
+  if (heads * S * hd > 0x1p40 || heads * ((static_cast<long long>(S) + 127) / 128) > 0x1p31 - 1)
     return XATTN_ERR_BAD_SHAPE;
   if (nh % nkv != 0) return XATTN_ERR_GROUP;
   if (!std::isfinite(scale)) return XATTN_ERR_BAD_SCALE;

@@ -230,3 +230,16 @@ def test_bwd_dq_mode(lib):
     assert f(128, 2, 2, 64, 1) == 1 and f(129, 2, 2, 64, 1) == 2
     assert f(2048, 8, 2, 64, 1) == 2 and f(4096, 16, 4, 128, 1) == 2
     assert f(256, 6, 4, 32, 0) == -1 and f(0, 2, 2, 32, 1) == -1 and f(256, 2, 2, 48, 0) == -1
+
+
+def test_sizes_whose_products_pass_64_bits(lib):
+    """They are too large, whatever is left of the product in 64 bits."""
+    big = 1 << 30
+    assert _fwd(lib, B=big, S=big, nh=big, nkv=big) == 2
+    assert _fwd(lib, S=2**31 - 1, hd=128, nh=1024, nkv=1) == 2
+    assert _decode(lib, B=big, T=big, nh=big, nkv=big) == 2
+    f = lib.xattn_fwd_f32
+    f.restype = ctypes.c_int
+    f.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int] * 5 + [ctypes.c_float] + [ctypes.c_void_p] * 3
+    assert f(16, 32, 48, big, big, big, big, 64, 0.1, 64, 80, None) == 2
+    assert f(16, 32, 48, 1, 2**31 - 1, 64, 64, 128, 0.1, 64, 80, None) == 2
