@@ -79,6 +79,12 @@ __global__ void bounds_selftest_kernel(int *status, int n) {
   (void)status;
 }
 
+#define XATTN_TRY(expr)                          \
+  do {                                           \
+    const xattn_status st_ = (expr);             \
+    if (st_ != XATTN_OK) return st_;             \
+  } while (0)
+
 xattn_status device_info(DeviceInfo **out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return XATTN_ERR_CUDA;
@@ -205,10 +211,15 @@ xattn_status check_shape(int B, int S, int nh, int nkv, int hd, float scale) {
   return XATTN_OK;
 }
 
+// The bf16 kernels take exponentials to base 2 of scores times scale log2 e, which has to be a number.
+xattn_status check_bf16_scale(float scale) {
+  return std::isfinite(scale * kLog2e) ? XATTN_OK : XATTN_ERR_BAD_SCALE;
+}
+
 // The bf16 backward folds -LSE/scale into a tensor-core operand; it takes scale == 0
 // exactly, and any |scale| >= 2^-64 (so that LSE/scale stays far from overflow).
 xattn_status check_bwd_scale(float scale) {
-  if (!std::isfinite(scale)) return XATTN_ERR_BAD_SCALE;
+  XATTN_TRY(check_bf16_scale(scale));
   if (scale != 0.f && std::fabs(scale) < 0x1p-64f) return XATTN_ERR_BAD_SCALE;
   return XATTN_OK;
 }
@@ -225,12 +236,6 @@ xattn_status cuda_status(cudaError_t e) {
   if (verbose) std::fprintf(stderr, "libxattn: CUDA error %d: %s\n", static_cast<int>(e), cudaGetErrorString(e));
   return XATTN_ERR_CUDA;
 }
-
-#define XATTN_TRY(expr)                          \
-  do {                                           \
-    const xattn_status st_ = (expr);             \
-    if (st_ != XATTN_OK) return st_;             \
-  } while (0)
 
 // Window and sinks of a window call; on success *w and *s are clipped to S (a window of S
 // or more keeps every key, sinks beyond S mean all of them).
@@ -308,6 +313,7 @@ xattn_status xattn_fwd(const void *q, const void *k, const void *v, int B, int S
   if (!q || !k || !v || !o || !lse) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_shape(B, S, nh, nkv, hd, scale));
   XATTN_TRY(check_bf16_fwd(hd));
+  XATTN_TRY(check_bf16_scale(scale));
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse)) return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
@@ -431,6 +437,7 @@ xattn_status xattn_decode(const void *q, const void *k_cache, const void *v_cach
                           int nh, int nkv, int hd, float scale, void *o, float *lse, void *stream) {
   if (!q || !k_cache || !v_cache || !o || !lse) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_shape(B, T, nh, nkv, hd, scale));
+  XATTN_TRY(check_bf16_scale(scale));
   if (nh / nkv > kMaxDecodeGroup) return XATTN_ERR_GROUP;
   if (hd != 32 && hd != 64 && hd != 128) return XATTN_ERR_UNSUPPORTED_HD;
   // One CTA per (batch, kv head, chunk): the grid is one-dimensional.
@@ -461,6 +468,7 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
                                float scale, void *o, float *lse, void *stream) {
   if (!q || !k_pages || !v_pages || !page_table || !ctx_lens || !o || !lse) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_shape(B, n, nh, nkv, hd, scale));
+  XATTN_TRY(check_bf16_scale(scale));
   XATTN_TRY(check_pages(B, n, nkv, hd, num_pages, page_size, max_pages));
   if (n > XATTN_TREE_MAX) return XATTN_ERR_BAD_SHAPE;
   if (window < n || sinks < 0) return XATTN_ERR_WINDOW;
@@ -600,6 +608,7 @@ xattn_status xattn_window_fwd(const void *q, const void *k, const void *v, int B
   int w = 0, s = 0;
   XATTN_TRY(check_window(S, window, sinks, &w, &s));
   XATTN_TRY(check_bf16_fwd(hd));
+  XATTN_TRY(check_bf16_scale(scale));
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
       !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
@@ -735,7 +744,7 @@ const char *xattn_status_string(xattn_status s) {
     case XATTN_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case XATTN_ERR_NO_DEVICE_SUPPORT: return "the current device is not compute capability 10.3 (sm_103)";
     case XATTN_ERR_DEVICE_TIMEOUT: return "a bounded on-device wait expired";
-    case XATTN_ERR_BAD_SCALE: return "scale must be finite";
+    case XATTN_ERR_BAD_SCALE: return "scale (bf16: scale log2 e) must be finite";
     case XATTN_ERR_WORKSPACE: return "workspace is NULL, not 256-byte aligned, or too small";
     case XATTN_ERR_SCRATCH_LIMIT:
       return "these sizes need more scratch than xattn_bwd_noalloc's fixed array holds";

@@ -67,8 +67,8 @@ typedef enum {
     XATTN_ERR_CUDA = 6,               /* a CUDA runtime or driver call failed */
     XATTN_ERR_NO_DEVICE_SUPPORT = 7,  /* the current device is not compute capability 10.3 */
     XATTN_ERR_DEVICE_TIMEOUT = 8,     /* a bounded on-device wait expired (reported later) */
-    XATTN_ERR_BAD_SCALE = 9,          /* scale is not finite (bf16 backward: or
-                                         0 < |scale| < 2^-64) */
+    XATTN_ERR_BAD_SCALE = 9,          /* scale is not finite (bf16: or scale log2 e is not;
+                                         bf16 backward: or 0 < |scale| < 2^-64) */
     XATTN_ERR_WORKSPACE = 10,         /* workspace pointer NULL/misaligned or too small */
     XATTN_ERR_SCRATCH_LIMIT = 11,     /* xattn_bwd_noalloc: sizes need more than its fixed scratch */
     XATTN_ERR_DEVICE_BOUNDS = 12,     /* debug builds only: an on-device bounds check failed

@@ -243,3 +243,12 @@ def test_sizes_whose_products_pass_64_bits(lib):
     f.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int] * 5 + [ctypes.c_float] + [ctypes.c_void_p] * 3
     assert f(16, 32, 48, big, big, big, big, 64, 0.1, 64, 80, None) == 2
     assert f(16, 32, 48, 1, 2**31 - 1, 64, 64, 128, 0.1, 64, 80, None) == 2
+
+
+def test_scales_too_large_for_base_2(lib):
+    """The bf16 kernels use scale log2 e: where that is no number, a score of 0 would give NaN."""
+    for scale in (2.5e38, -3.4e38):
+        assert _fwd(lib, scale=scale) == 9 and _bwd(lib, scale) == 9 and _decode(lib, scale=scale) == 9
+    import torch
+    if not torch.cuda.is_available():
+        assert _fwd(lib, scale=2.3e38) == 6

@@ -150,3 +150,7 @@ def test_random_words_are_trees():
     for row in random_words(3, 64, 1):
         for i, w in enumerate(row):
             assert w >> i == 1                                       # itself, and no later token
+
+
+def test_a_scale_too_large_for_base_2(lib):
+    assert _tree(lib, scale=-2.5e38) == 9

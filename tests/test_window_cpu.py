@@ -194,3 +194,9 @@ def test_misaligned_floats_are_refused(lib):
     f = lib.xattn_bwd_preprocess
     f.restype, f.argtypes = I, [P] * 3 + [I] * 4 + [F, P, ctypes.c_size_t, P]
     assert f(16, 32, 50, 1, 4, 2, 64, 0.125, 256, 1 << 20, None) == 5
+
+
+def test_scales_too_large_for_base_2(lib):
+    assert _fwd(lib, scale=2.5e38) == 9 and _bwd(lib, scale=2.5e38) == 9
+    if not torch.cuda.is_available():
+        assert _fwd(lib, "xattn_window_fwd_f32", scale=2.5e38) == 6
