@@ -39,11 +39,9 @@
  *   - Scratch is stream-ordered: taken on `stream` and released on it when the call's work
  *     is enqueued. The window, tree and fp32 window calls take it from a memory pool of the
  *     library's own (one per device), which keeps what it has grown to (xattn_trim_scratch).
- *   - CUDA graphs: the calls may be captured on a stream and replayed, once the device
- *     has seen one ordinary call (the first call on a device looks up its device
- *     status word; make that call outside the capture). Entry points that take
- *     scratch with cudaMallocAsync record it in the graph as stream-ordered
- *     allocation nodes.
+ *   - CUDA graphs: the calls may be captured on a stream and replayed, a process's first
+ *     call on a device among them (but xattn_bwd_noalloc's, see there). Scratch is recorded
+ *     in the graph as stream-ordered allocation nodes.
  */
 #ifndef XATTN_H
 #define XATTN_H
@@ -226,8 +224,7 @@ xattn_status xattn_bwd_f32(const float *q, const float *k, const float *v, const
  *                           from run to run; dK and dV do not); deterministic != 0, and
  *                           hd = 128: every output reproducible. Scratch (the causal
  *                           backward's, and fp32 partial sums of the sink tiles' dK and dV)
- *                           is taken with cudaMallocAsync on `stream` and released with
- *                           cudaFreeAsync on it.
+ *                           is stream-ordered, from the library's pool.
  *   xattn_window_*_f32    : IEEE fp32 on the CUDA cores, hd in [1, 128], every output
  *                           reproducible; the backward takes B * S * nh floats of scratch
  *                           in the same way.
@@ -348,7 +345,8 @@ xattn_status xattn_cache_append(const void *k_new, const void *v_new, void *k_pa
  * ctx_b + path[b][i], i < accepted[b], to ctx_b + i, in place. path [B, n] (int) ascends over
  * its first accepted[b] entries (so path[b][i] >= i); accepted [B] (int) is taken within
  * [0, n]. An entry that is not above its index stays where it is; one beyond n - 1, or whose
- * row or place is no page, is not moved. Rows behind the accepted ones keep what they held. hd
+ * row or place is no page, is not moved. Rows behind the accepted ones keep what they held. Two
+ * sequences must not share a page that holds positions from ctx_b on. hd
  * a multiple of 8 (else XATTN_ERR_UNSUPPORTED_HD). No scratch.
  */
 xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_table,

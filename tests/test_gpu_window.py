@@ -273,3 +273,46 @@ def test_the_scratch_can_be_given_back():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(c[0], a["o"])
+
+
+EVERY_CALL_FIRST_IN_CAPTURE = """
+import torch
+from bwd_xattn_fwd_gb300 import xattn
+g = torch.Generator(device="cuda").manual_seed(0)
+rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+q, k, v, dO, o = (rnd(2, 200, 2, 64) for _ in range(5))
+qf, kf, vf, dOf, of = (t.float() for t in (q, k, v, dO, o))
+lse = torch.full((2, 200, 2), 5.0, device="cuda")
+one, new = rnd(2, 2, 64), rnd(2, 4, 2, 64)
+i32 = lambda x: torch.tensor(x, device="cuda", dtype=torch.int32)
+table, lens, path = i32([[0, 1, 2, 3], [4, 5, 6, 7]]), i32([50, 7]), i32([[0, 2, 3, 0]] * 2)
+pools = rnd(8, 16, 2, 64), rnd(8, 16, 2, 64)
+def calls():
+    out = [*xattn.attention_fwd(q, k, v), *xattn.attention_bwd(q, k, v, o, dO, lse)[1:],
+           *xattn.attention_bwd(q, k, v, o, dO, lse, deterministic=True), *xattn.attention_decode(one, k, v),
+           *xattn.attention_fwd(qf, kf, vf), *xattn.attention_bwd(qf, kf, vf, of, dOf, lse),
+           *xattn.attention_window_fwd(qf, kf, vf, 70, 3), *xattn.attention_window_bwd(qf, kf, vf, of, dOf, lse, 70, 3)]
+    xattn.cache_append(new, new, *pools, table, lens)
+    xattn.cache_compact(*pools, table, lens, path, i)
+    return *out, pools[0].clone(), pools[1].clone()
+i = i32([3, 2])
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+eager = calls()
+torch.cuda.synchronize()
+assert xattn.xattn_check_device_status() == 0
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+print("same")
+"""
+
+
+def test_the_other_calls_as_a_process_s_first_captured():
+    """The same of the causal calls, the decode step, the fp32 forms and the page calls."""
+    run = subprocess.run([sys.executable, "-c", EVERY_CALL_FIRST_IN_CAPTURE], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stderr[-2000:]
