@@ -268,11 +268,14 @@ def test_the_scratch_can_be_given_back():
     side.wait_stream(torch.cuda.current_stream())
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
-        c = xattn.attention_window_fwd(x["q"], x["k"], x["v"], 700, 4, 0.125)
+        o, lse = xattn.attention_window_fwd(x["q"], x["k"], x["v"], 700, 4, 0.125)
         xattn.xattn_trim_scratch()                         # takes no part in the capture
-    graph.replay()
-    torch.cuda.synchronize()
-    assert torch.equal(c[0], a["o"])
+        c = xattn.attention_window_bwd(x["q"], x["k"], x["v"], o, x["dO"], lse, 700, 4, 0.125)
+    for _ in range(2):                                     # the graph's scratch is its own
+        graph.replay()
+        torch.cuda.synchronize()
+        xattn.xattn_trim_scratch()
+        assert torch.equal(o, a["o"]) and torch.equal(c[1], a["dk"]) and torch.equal(c[2], a["dv"])
 
 
 EVERY_CALL_FIRST_IN_CAPTURE = """
