@@ -15,7 +15,8 @@
 //   P  = exp2(S scale log2e - LSE_i log2e)   (LSE_i and D_i of the thread's query row
 //   dS = P (dP - D_i)                          are registers) -> bf16 into TMEM
 //   dQ_m += dS K_n            (A = dS from TMEM, B = K_n from shared memory)
-// dQ = scale * accumulator (the softmax scale is applied once, at the end).
+// dQ = scale * accumulator (the softmax scale is applied once, at the end). dS is rounded to bf16,
+// K's type, as in attn_bwd_sm103.cu; P stays fp32 in registers.
 // Window with sinks (kWin): query i sees key j <= i only if i - j < window or j < sinks;
 // the CTA walks the sink tiles and the tiles from the first one its window reaches.
 #include "sm103_ptx.cuh"

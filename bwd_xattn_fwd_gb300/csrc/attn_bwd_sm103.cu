@@ -23,6 +23,10 @@
 //                                                      and one query head per kv head,
 //                                                      dK reads dS^T from shared memory)
 //      The softmax scale of dS is applied once, to dK_n in the epilogue.
+//      P and dS are rounded to bf16 because their products' other operands (dO, Q, K) are bf16 and
+//      a product takes two operands of one type; accumulators, LSE and D stay fp32 (D and LSE
+//      enter the products as three bf16 terms). dQ and dK are then 0.0030 (relative, rms)
+//      from the exact values where fp32 products give 0.0017, bf16's own rounding of the result.
 //      Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer of S^T and dV,
 //      3 = MMA issuer of dP^T and dK, 4-7 = P, 8-11 = dS (one thread per key row).
 //   3. dQ: by default the main kernel also computes dQ_m = dS K_n per iteration and
