@@ -342,6 +342,8 @@ def attention_decode(q, k_cache, v_cache, scale=None, stream=None):
 
 
 # ---- tensor-level calls that check their tensors (csrc/xattn_torch.cpp) ------------------
+# A stream given to one of them is as torch.cuda.stream(stream) around the call: the outputs
+# belong to it, and tensors of another stream are the caller's to order and to keep.
 
 def _load_calls():
     """The native part of the calls below, bound to this library's entry points."""

@@ -332,7 +332,8 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
 /*
  * Writes n new tokens' rows k_new, v_new [B, n, nkv, hd] to positions ctx_b .. ctx_b + n - 1 of
  * each sequence. Positions outside the table, or whose entry is no page, are dropped; no
- * other row is touched. Two sequences must not append to one page. hd a multiple of 8 (else
+ * other row is touched. Two sequences must not append to one page, and none must have it twice
+ * in its table there. hd a multiple of 8 (else
  * XATTN_ERR_UNSUPPORTED_HD); any n that the table can hold. No scratch.
  */
 xattn_status xattn_cache_append(const void *k_new, const void *v_new, void *k_pages,
@@ -355,7 +356,7 @@ xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_t
                                  int max_pages, void *stream);
 
 /*
- * Gives back to the driver what the library's scratch pool of the current device holds beyond
+ * Gives back to CUDA what the library's scratch pool of the current device holds beyond
  * keep_bytes and no call still uses (a call uses its scratch until its work on its stream is
  * over: synchronise first to have all of it given back). The next call that takes scratch maps it
  * again. Memory of captured graphs belongs to the graphs and is not touched.
