@@ -295,6 +295,31 @@ xattn_status bf16_device(DeviceInfo **dev) {
   return get_encode();
 }
 
+// Sizes of an expanded latent attention; every row's vectors are whole 16-number pieces.
+xattn_status check_latent(int B, int S, int nh, int dn, int dr, int dv, float scale) {
+  if (dn <= 0 || dr <= 0 || dv <= 0) return XATTN_ERR_BAD_SHAPE;
+  if (dn > 128 || dr > 64 || dv > 128 || dn % 16 != 0 || dr % 16 != 0 || dv % 16 != 0) return XATTN_ERR_UNSUPPORTED_HD;
+  XATTN_TRY(check_shape(B, S, nh, nh, dn + 128, scale));
+  if (S > (1 << 30)) return XATTN_ERR_BAD_SHAPE;   // tile sums stay inside int32
+  return check_bf16_scale(scale);
+}
+
+// A page table [B, max_pages] over num_pages pages, for calls that move no rows.
+xattn_status check_table(int B, int num_pages, int page_size, int max_pages) {
+  return check_pages(B, 1, 1, 1, num_pages, page_size, max_pages);
+}
+
+// Rows of a slot map and the pool that they go to.
+xattn_status check_slots(long long rows, int a, int b, int num_pages, int page_size) {
+  if (rows < 0 || a <= 0 || b <= 0 || num_pages <= 0 || page_size <= 0) return XATTN_ERR_BAD_SHAPE;
+  if (static_cast<double>(a) + b > 0x1p30 || static_cast<double>(num_pages) * page_size * (static_cast<double>(a) + b) > 0x1p60 ||
+      static_cast<double>(rows) * (static_cast<double>(a) + b) > 0x1p38)
+    return XATTN_ERR_BAD_SHAPE;
+  return a % 8 != 0 || b % 8 != 0 ? XATTN_ERR_UNSUPPORTED_HD : XATTN_OK;
+}
+
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
 xattn_status check_workspace(void *ws, size_t bytes, int B, int S, int nh, int hd) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return XATTN_ERR_WORKSPACE;
   if (bytes < bwd_workspace_bytes(B, S, nh, hd, true)) return XATTN_ERR_WORKSPACE;
@@ -733,13 +758,164 @@ xattn_status xattn_bwd_f32(const float *q, const float *k, const float *v, const
                                     static_cast<cudaStream_t>(stream)));
 }
 
+xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope, int B, int S, int nh, int dn, int dr,
+                              int dv, float scale, void *o, float *lse, void *stream) {
+  if (!q || !kv || !k_rope || !o || !lse) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_latent(B, S, nh, dn, dr, dv, scale));
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) || !aligned4(lse)) return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  LatentArgs a = {};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.kv = static_cast<const __nv_bfloat16 *>(kv);
+  a.k_rope = static_cast<const __nv_bfloat16 *>(k_rope);
+  a.o = static_cast<__nv_bfloat16 *>(o);
+  a.lse = lse;
+  a.B = B, a.S = S, a.nh = nh, a.dn = dn, a.dr = dr, a.dv = dv, a.scale = scale;
+  a.status = dev->status, a.timeout_ns = wait_limit_ns();
+  return cuda_status(launch_latent_fwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope, const void *o, const void *dO,
+                              const float *lse, int B, int S, int nh, int dn, int dr, int dv, float scale, void *dq,
+                              void *dkv, void *dk_rope, void *stream) {
+  if (!q || !kv || !k_rope || !o || !dO || !lse || !dq || !dkv || !dk_rope) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_latent(B, S, nh, dn, dr, dv, scale));
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) ||
+      !aligned16(dkv) || !aligned16(dk_rope) || !aligned4(lse))
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  LatentArgs a = {};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.kv = static_cast<const __nv_bfloat16 *>(kv);
+  a.k_rope = static_cast<const __nv_bfloat16 *>(k_rope);
+  a.dO = static_cast<const __nv_bfloat16 *>(dO);
+  a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(o));   // (read only here)
+  a.lse = const_cast<float *>(lse);
+  a.dq = static_cast<__nv_bfloat16 *>(dq);
+  a.dkv = static_cast<__nv_bfloat16 *>(dkv);
+  a.dk_rope = static_cast<__nv_bfloat16 *>(dk_rope);
+  a.B = B, a.S = S, a.nh = nh, a.dn = dn, a.dr = dr, a.dv = dv, a.scale = scale;
+  a.status = dev->status, a.timeout_ns = wait_limit_ns();
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void *base = nullptr;
+  XATTN_TRY(scratch_alloc(*dev, latent_bwd_workspace_bytes(a), st, &base));
+  latent_bwd_workspace_carve(a, base);
+  xattn_status r = cuda_status(launch_latent_bwd(a, st));
+  const cudaError_t fe = cudaFreeAsync(base, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
+}
+
+xattn_status xattn_latent_decode(const void *q, const void *pages, const int *page_table, const int *ctx_lens, int B,
+                                 int n, int nh, int dc, int dr, int num_pages, int page_size, int max_pages, float scale,
+                                 void *o, float *lse, void *stream) {
+  if (!q || !pages || !page_table || !ctx_lens || !o || !lse) return XATTN_ERR_NULL_PTR;
+  if (nh <= 0 || dc <= 0 || dr <= 0) return XATTN_ERR_BAD_SHAPE;
+  if (dc > 512 || dc % 128 != 0 || dr > 64 || dr % 16 != 0) return XATTN_ERR_UNSUPPORTED_HD;
+  XATTN_TRY(check_pages(B, n, 1, dc + dr, num_pages, page_size, max_pages));
+  if (n > XATTN_TREE_MAX || static_cast<double>(B) * n * nh > 0x1p28) return XATTN_ERR_BAD_SHAPE;
+  if (!std::isfinite(scale)) return XATTN_ERR_BAD_SCALE;
+  XATTN_TRY(check_bf16_scale(scale));
+  if (!aligned16(q) || !aligned16(pages) || !aligned16(o) || !aligned4(page_table, ctx_lens) || !aligned4(lse))
+    return XATTN_ERR_MISALIGNED;
+  LatentDecodeArgs a = {};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.pages = static_cast<const __nv_bfloat16 *>(pages);
+  a.page_table = page_table, a.ctx_lens = ctx_lens;
+  a.o = static_cast<__nv_bfloat16 *>(o);
+  a.lse = lse;
+  a.B = B, a.n = n, a.nh = nh, a.dc = dc, a.dr = dr;
+  a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
+  a.scale_log2 = scale * kLog2e;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  a.status = dev->status, a.timeout_ns = wait_limit_ns();
+  return cuda_status(launch_latent_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+xattn_status xattn_cache_reserve(int *page_table, const int *ctx_lens, const int *new_lens, const int *free_pages,
+                                 int *free_count, int B, int num_pages, int page_size, int max_pages, int tokens,
+                                 long long *slots, int *offsets, int *granted, void *stream) {
+  if (!page_table || !ctx_lens || !new_lens || !free_pages || !free_count || !offsets || !granted ||
+      (!slots && tokens > 0))
+    return XATTN_ERR_NULL_PTR;
+  if (tokens < 0) return XATTN_ERR_BAD_SHAPE;
+  XATTN_TRY(check_table(B, num_pages, page_size, max_pages));
+  if (!aligned4(page_table, ctx_lens, new_lens, free_pages, free_count, offsets, granted) || !aligned8(slots))
+    return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void *base = nullptr;
+  XATTN_TRY(scratch_alloc(*dev, (static_cast<size_t>(B) + 1) * sizeof(int), st, &base));
+  const ReserveArgs a = {page_table, ctx_lens, new_lens, free_pages, free_count, slots, offsets, granted,
+                         static_cast<int *>(base), B, max_pages, page_size, num_pages, tokens};
+  xattn_status r = cuda_status(launch_cache_reserve(a, st));
+  const cudaError_t fe = cudaFreeAsync(base, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
+}
+
+xattn_status xattn_cache_release(int *page_table, const int *held_lens, const int *keep_lens, int *free_pages,
+                                 int *free_count, int B, int num_pages, int page_size, int max_pages, void *stream) {
+  if (!page_table || !held_lens || !keep_lens || !free_pages || !free_count) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_table(B, num_pages, page_size, max_pages));
+  if (!aligned4(page_table, held_lens, keep_lens, free_pages, free_count)) return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void *base = nullptr;
+  XATTN_TRY(scratch_alloc(*dev, (static_cast<size_t>(B) + 1) * sizeof(int), st, &base));
+  const ReleaseArgs a = {page_table, held_lens, keep_lens, free_pages, free_count, static_cast<int *>(base), B, max_pages,
+                         page_size, num_pages};
+  xattn_status r = cuda_status(launch_cache_release(a, st));
+  const cudaError_t fe = cudaFreeAsync(base, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
+}
+
+xattn_status xattn_cache_write(const void *k_new, const void *v_new, void *k_pages, void *v_pages, const long long *slots,
+                               int rows, int nkv, int hd, int num_pages, int page_size, void *stream) {
+  if (!k_pages || !v_pages || (rows != 0 && (!k_new || !v_new || !slots))) return XATTN_ERR_NULL_PTR;
+  if (nkv <= 0 || hd <= 0 || static_cast<double>(nkv) * hd > 0x1p28) return XATTN_ERR_BAD_SHAPE;
+  if (hd % 8 != 0) return XATTN_ERR_UNSUPPORTED_HD;
+  XATTN_TRY(check_slots(rows, nkv * hd, nkv * hd, num_pages, page_size));
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned8(slots))
+    return XATTN_ERR_MISALIGNED;
+  if (rows == 0) return XATTN_OK;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const int vecs = nkv * hd / 8;
+  const WriteArgs a = {{static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new)},
+                       {static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages)},
+                       {vecs, vecs}, {vecs, vecs}, slots, rows, static_cast<long long>(num_pages) * page_size};
+  return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+}
+
+xattn_status xattn_latent_write(const void *c, const void *k_rope, void *pages, const long long *slots, int rows, int dc,
+                                int dr, int num_pages, int page_size, void *stream) {
+  if (!pages || (rows != 0 && (!c || !k_rope || !slots))) return XATTN_ERR_NULL_PTR;
+  XATTN_TRY(check_slots(rows, dc, dr, num_pages, page_size));
+  if (!aligned16(c) || !aligned16(k_rope) || !aligned16(pages) || !aligned8(slots)) return XATTN_ERR_MISALIGNED;
+  if (rows == 0) return XATTN_OK;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(device_info(&dev));
+  const WriteArgs a = {{static_cast<const uint4 *>(c), static_cast<const uint4 *>(k_rope)},
+                       {static_cast<uint4 *>(pages), static_cast<uint4 *>(pages) + dc / 8},
+                       {dc / 8, dr / 8}, {(dc + dr) / 8, (dc + dr) / 8}, slots, rows,
+                       static_cast<long long>(num_pages) * page_size};
+  return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+}
+
 const char *xattn_status_string(xattn_status s) {
   switch (s) {
     case XATTN_OK: return "ok";
     case XATTN_ERR_NULL_PTR: return "a required pointer is NULL";
     case XATTN_ERR_BAD_SHAPE: return "B, S, nh, nkv and hd must be positive and within size limits";
     case XATTN_ERR_GROUP: return "nh must be a multiple of nkv";
-    case XATTN_ERR_UNSUPPORTED_HD: return "unsupported head dimension (bf16: 32, 64 or 128; the backward's stage calls and xattn_bwd_noalloc: 32 or 64; fp32: <= 128)";
+    case XATTN_ERR_UNSUPPORTED_HD: return "unsupported head dimension (bf16: 32, 64 or 128; the backward's stage calls and xattn_bwd_noalloc: 32 or 64; fp32: <= 128; latent attention: dn, dr, dv multiples of 16 up to 128, 64, 128, dc of 128 up to 512; rows of pages: multiples of 8)";
     case XATTN_ERR_MISALIGNED: return "a bf16 tensor pointer is not 16-byte aligned, or a float or int array not 4-byte";
     case XATTN_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case XATTN_ERR_NO_DEVICE_SUPPORT: return "the current device is not compute capability 10.3 (sm_103)";

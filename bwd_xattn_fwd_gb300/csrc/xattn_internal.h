@@ -212,4 +212,68 @@ struct PageArgs {
 cudaError_t launch_cache_append(const PageArgs &a, const void *k_new, const void *v_new, cudaStream_t stream);
 cudaError_t launch_cache_compact(const PageArgs &a, const int *path, const int *accepted, cudaStream_t stream);
 
+// Latent attention, expanded form (attn_latent.cu): head h's key of token j is (kv[j, h, :dn],
+// k_rope[j]), its value kv[j, h, dn:].
+struct LatentArgs {
+  const __nv_bfloat16 *q, *kv, *k_rope, *dO;   // [B,S,nh,dn+dr], [B,S,nh,dn+dv], [B,S,dr], [B,S,nh,dv]
+  __nv_bfloat16 *o;                            // [B,S,nh,dv]: written by the forward, read by the backward
+  float *lse;                                  // [B,S,nh], likewise
+  __nv_bfloat16 *dq, *dkv, *dk_rope;
+  float *D, *rope_parts;                       // the backward's scratch
+  int B, S, nh, dn, dr, dv;
+  float scale;
+  int *status;
+  unsigned long long timeout_ns;
+};
+size_t latent_bwd_workspace_bytes(const LatentArgs &a);
+void latent_bwd_workspace_carve(LatentArgs &a, void *base);
+cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
+cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
+
+// Absorbed form: n new tokens a sequence over a paged cache of rows of dc + dr numbers.
+struct LatentDecodeArgs {
+  const __nv_bfloat16 *q, *pages;              // [B,n,nh,dc+dr], [num_pages,page_size,dc+dr]
+  const int *page_table, *ctx_lens;
+  __nv_bfloat16 *o;                            // [B,n,nh,dc]
+  float *lse;
+  int B, n, nh, dc, dr, num_pages, page_size, max_pages;
+  float scale_log2;
+  int *status;
+  unsigned long long timeout_ns;
+};
+cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream);
+
+// Page tables, slot maps and rows written by slot (cache_tables.cu).
+struct ReserveArgs {
+  int *page_table;
+  const int *ctx_lens, *new_lens, *free_pages;
+  int *free_count;
+  long long *slots;
+  int *offsets, *granted;
+  int *first;                                  // scratch: [B] pages taken before each sequence's; [B]: free pages before
+  int B, max_pages, page_size, num_pages;
+  long long tokens;
+};
+cudaError_t launch_cache_reserve(const ReserveArgs &a, cudaStream_t stream);
+
+struct ReleaseArgs {
+  int *page_table;
+  const int *held_lens, *keep_lens;
+  int *free_pages, *free_count;
+  int *counts;                                 // scratch: [B] pages given back; [B]: free pages before
+  int B, max_pages, page_size, num_pages;
+};
+cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream);
+
+// Two sources' rows to the rows `slots` of their places: 16-byte vectors, of a row src_vecs[x] go to
+// dst[x] + slot * dst_stride[x].
+struct WriteArgs {
+  const uint4 *src[2];
+  uint4 *dst[2];
+  int vecs[2], stride[2];
+  const long long *slots;
+  long long rows, num_slots;
+};
+cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream);
+
 }  // namespace xattn

@@ -30,6 +30,14 @@ decltype(&xattn_tree_decode) g_tree_decode;
 decltype(&xattn_cache_append) g_cache_append;
 decltype(&xattn_cache_compact) g_cache_compact;
 
+decltype(&xattn_latent_fwd) g_latent_fwd;
+decltype(&xattn_latent_bwd) g_latent_bwd;
+decltype(&xattn_latent_decode) g_latent_decode;
+decltype(&xattn_cache_reserve) g_cache_reserve;
+decltype(&xattn_cache_release) g_cache_release;
+decltype(&xattn_cache_write) g_cache_write;
+decltype(&xattn_latent_write) g_latent_write;
+
 using at::IntArrayRef;
 using at::ScalarType;
 using at::Tensor;
@@ -261,17 +269,229 @@ PyObject *cache_compact(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(seven addresses): the entry points to call.
+struct Latent {
+  const Tensor *q, *kv, *rope;
+  int64_t B, S, nh, dn, dr, dv;
+  int device;
+  bool ok;
+  explicit Latent(PyObject *const *args) : q(tensor(args, 0)), kv(tensor(args, 1)), rope(tensor(args, 2)), ok(false) {
+    if (!q || !kv || !rope || !q->is_cuda() || q->dim() != 4 || kv->dim() != 4 || rope->dim() != 3 || !ints(q->sizes()) ||
+        !ints(kv->sizes()))
+      return;
+    device = q->get_device();
+    B = q->size(0), S = q->size(1), nh = q->size(2), dr = rope->size(2), dn = q->size(3) - dr, dv = kv->size(3) - dn;
+    ok = dn > 0 && dv > 0 && fits(q, at::kBFloat16, {B, S, nh, dn + dr}, device) &&
+         fits(kv, at::kBFloat16, {B, S, nh, dn + dv}, device) && fits(rope, at::kBFloat16, {B, S, dr}, device);
+  }
+};
+
+// latent_fwd(q, kv, k_rope, scale) -> (o, lse)
+PyObject *latent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(4)
+  const Latent x(args);
+  if (!x.ok) Py_RETURN_NONE;
+  XATTN_HERE(x.device);
+  const float scale = scale_of(args[3], x.dn + x.dr);
+  if (PyErr_Occurred()) return nullptr;
+  const Tensor o = at::empty({x.B, x.S, x.nh, x.dv}, x.q->options());
+  const Tensor lse = at::empty({x.B, x.S, x.nh}, x.q->options().dtype(at::kFloat));
+  const void *q = x.q->data_ptr(), *kv = x.kv->data_ptr(), *rope = x.rope->data_ptr();
+  void *op = o.data_ptr();
+  float *l = lse.data_ptr<float>();
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_latent_fwd(q, kv, rope, x.B, x.S, x.nh, x.dn, x.dr, x.dv, scale, op, l, stream);
+  Py_END_ALLOW_THREADS
+  return result(status, {o, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// latent_bwd(q, kv, k_rope, o, dO, lse, scale) -> (dq, dkv, dk_rope)
+PyObject *latent_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(7)
+  const Latent x(args);
+  const Tensor *o = tensor(args, 3), *dO = tensor(args, 4), *lse = tensor(args, 5);
+  if (!x.ok || !fits(o, at::kBFloat16, {x.B, x.S, x.nh, x.dv}, x.device) ||
+      !fits(dO, at::kBFloat16, {x.B, x.S, x.nh, x.dv}, x.device) || !fits(lse, at::kFloat, {x.B, x.S, x.nh}, x.device))
+    Py_RETURN_NONE;
+  XATTN_HERE(x.device);
+  const float scale = scale_of(args[6], x.dn + x.dr);
+  if (PyErr_Occurred()) return nullptr;
+  const Tensor dq = at::empty(x.q->sizes(), x.q->options()), dkv = at::empty(x.kv->sizes(), x.kv->options()),
+               drope = at::empty(x.rope->sizes(), x.rope->options());
+  const void *in[5] = {x.q->data_ptr(), x.kv->data_ptr(), x.rope->data_ptr(), o->data_ptr(), dO->data_ptr()};
+  const float *l = lse->data_ptr<float>();
+  void *out[3] = {dq.data_ptr(), dkv.data_ptr(), drope.data_ptr()};
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_latent_bwd(in[0], in[1], in[2], in[3], in[4], l, x.B, x.S, x.nh, x.dn, x.dr, x.dv, scale, out[0], out[1],
+                        out[2], stream);
+  Py_END_ALLOW_THREADS
+  return result(status, {dq, dkv, drope});
+  END_HANDLE_TH_ERRORS
+}
+
+// latent_decode(q, pages, page_table, ctx_lens, dc, scale) -> (o, lse)
+PyObject *latent_decode(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(6)
+  const Tensor *q = tensor(args, 0), *pages = tensor(args, 1), *table = tensor(args, 2), *lens = tensor(args, 3);
+  if (!q || !pages || !table || !q->is_cuda() || q->dim() != 4 || pages->dim() != 3 || table->dim() != 2 ||
+      !ints(q->sizes()) || !ints(pages->sizes()) || !ints(table->sizes()))
+    Py_RETURN_NONE;
+  const int device = q->get_device();
+  const int64_t B = table->size(0), tokens = q->size(1), nh = q->size(2), width = pages->size(2);
+  const int64_t dc = PyLong_AsLongLong(args[4]);
+  const float scale = static_cast<float>(PyFloat_AsDouble(args[5]));
+  if (PyErr_Occurred()) return nullptr;
+  if (dc <= 0 || dc >= width || !fits(q, at::kBFloat16, {B, tokens, nh, width}, device) ||
+      !fits(pages, at::kBFloat16, pages->sizes(), device) || !fits(table, at::kInt, table->sizes(), device) ||
+      !fits(lens, at::kInt, {B}, device))
+    Py_RETURN_NONE;
+  XATTN_HERE(device);
+  const Tensor o = at::empty({B, tokens, nh, dc}, q->options());
+  const Tensor lse = at::empty({B, tokens, nh}, q->options().dtype(at::kFloat));
+  const void *qp = q->data_ptr(), *pp = pages->data_ptr();
+  const int *tp = table->data_ptr<int>(), *lp = lens->data_ptr<int>();
+  void *op = o.data_ptr();
+  float *l = lse.data_ptr<float>();
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_latent_decode(qp, pp, tp, lp, B, tokens, nh, dc, width - dc, pages->size(0), pages->size(1), table->size(1),
+                           scale, op, l, stream);
+  Py_END_ALLOW_THREADS
+  return result(status, {o, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// A page table, two arrays of lengths, and the stack of free pages.
+struct Tables {
+  const Tensor *table, *from, *to, *pages, *count;
+  int64_t B, max_pages, num_pages;
+  int device;
+  bool ok;
+  explicit Tables(PyObject *const *args)
+      : table(tensor(args, 0)), from(tensor(args, 1)), to(tensor(args, 2)), pages(tensor(args, 3)), count(tensor(args, 4)),
+        ok(false) {
+    if (!table || !pages || !table->is_cuda() || table->dim() != 2 || pages->dim() != 1 || !ints(table->sizes()) ||
+        !ints(pages->sizes()))
+      return;
+    device = table->get_device();
+    B = table->size(0), max_pages = table->size(1), num_pages = pages->size(0);
+    ok = fits(table, at::kInt, table->sizes(), device) && fits(from, at::kInt, {B}, device) &&
+         fits(to, at::kInt, {B}, device) && fits(pages, at::kInt, pages->sizes(), device) &&
+         fits(count, at::kInt, {1}, device);
+  }
+};
+
+// cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_size, tokens) -> (slots, offsets, granted)
+PyObject *cache_reserve(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(7)
+  const Tables x(args);
+  const int page_size = clamped(args[5]), tokens = clamped(args[6]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!x.ok) Py_RETURN_NONE;
+  XATTN_HERE(x.device);
+  if (tokens < 0) return PyLong_FromLong(XATTN_ERR_BAD_SHAPE);
+  const Tensor slots = at::empty({tokens}, x.table->options().dtype(at::kLong)),
+               offsets = at::empty({x.B + 1}, x.table->options()), granted = at::empty({x.B}, x.table->options());
+  int *table = x.table->data_ptr<int>(), *count = x.count->data_ptr<int>(), *op = offsets.data_ptr<int>(),
+      *gp = granted.data_ptr<int>();
+  const int *ctx = x.from->data_ptr<int>(), *fresh = x.to->data_ptr<int>(), *pages = x.pages->data_ptr<int>();
+  auto *sp = reinterpret_cast<long long *>(slots.data_ptr<int64_t>());
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_cache_reserve(table, ctx, fresh, pages, count, x.B, x.num_pages, page_size, x.max_pages, tokens, sp, op, gp,
+                           stream);
+  Py_END_ALLOW_THREADS
+  if (status == XATTN_OK) {
+    PyObject *done = written(status, {x.table, x.count});
+    Py_XDECREF(done);
+  }
+  return result(status, {slots, offsets, granted});
+  END_HANDLE_TH_ERRORS
+}
+
+// cache_release(page_table, held_lens, keep_lens, free_pages, free_count, page_size) -> True
+PyObject *cache_release(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(6)
+  const Tables x(args);
+  const int page_size = clamped(args[5]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!x.ok) Py_RETURN_NONE;
+  XATTN_HERE(x.device);
+  int *table = x.table->data_ptr<int>(), *pages = x.pages->data_ptr<int>(), *count = x.count->data_ptr<int>();
+  const int *held = x.from->data_ptr<int>(), *keep = x.to->data_ptr<int>();
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_cache_release(table, held, keep, pages, count, x.B, x.num_pages, page_size, x.max_pages, stream);
+  Py_END_ALLOW_THREADS
+  return written(status, {x.table, x.pages, x.count});
+  END_HANDLE_TH_ERRORS
+}
+
+// cache_write(k_new, v_new, k_pages, v_pages, slots) -> True
+PyObject *cache_write(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(5)
+  const Tensor *k = tensor(args, 0), *v = tensor(args, 1), *kp = tensor(args, 2), *vp = tensor(args, 3), *slots = tensor(args, 4);
+  if (!kp || !slots || !kp->is_cuda() || kp->dim() != 4 || slots->dim() != 1 || !ints(kp->sizes()) || !ints(slots->sizes()))
+    Py_RETURN_NONE;
+  const int device = kp->get_device();
+  const int64_t rows = slots->size(0), nkv = kp->size(2), hd = kp->size(3);
+  if (!fits(kp, at::kBFloat16, kp->sizes(), device) || !fits(vp, at::kBFloat16, kp->sizes(), device) ||
+      !fits(slots, at::kLong, {rows}, device) || !fits(k, at::kBFloat16, {rows, nkv, hd}, device) ||
+      !fits(v, at::kBFloat16, {rows, nkv, hd}, device))
+    Py_RETURN_NONE;
+  XATTN_HERE(device);
+  const void *kn = k->data_ptr(), *vn = v->data_ptr();
+  void *kd = kp->data_ptr(), *vd = vp->data_ptr();
+  const auto *sp = reinterpret_cast<const long long *>(slots->data_ptr<int64_t>());
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_cache_write(kn, vn, kd, vd, sp, rows, nkv, hd, kp->size(0), kp->size(1), stream);
+  Py_END_ALLOW_THREADS
+  return written(status, {kp, vp});
+  END_HANDLE_TH_ERRORS
+}
+
+// latent_write(c, k_rope, pages, slots) -> True
+PyObject *latent_write(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  XATTN_CALL(4)
+  const Tensor *c = tensor(args, 0), *rope = tensor(args, 1), *pages = tensor(args, 2), *slots = tensor(args, 3);
+  if (!c || !rope || !pages || !slots || !pages->is_cuda() || c->dim() != 2 || rope->dim() != 2 || pages->dim() != 3 ||
+      slots->dim() != 1 || !ints(pages->sizes()) || !ints(slots->sizes()))
+    Py_RETURN_NONE;
+  const int device = pages->get_device();
+  const int64_t rows = slots->size(0), dc = c->size(1), dr = rope->size(1);
+  if (!fits(pages, at::kBFloat16, {pages->size(0), pages->size(1), dc + dr}, device) || !fits(slots, at::kLong, {rows}, device) ||
+      !fits(c, at::kBFloat16, {rows, dc}, device) || !fits(rope, at::kBFloat16, {rows, dr}, device))
+    Py_RETURN_NONE;
+  XATTN_HERE(device);
+  const void *cp = c->data_ptr(), *rp = rope->data_ptr();
+  void *pp = pages->data_ptr();
+  const auto *sp = reinterpret_cast<const long long *>(slots->data_ptr<int64_t>());
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = g_latent_write(cp, rp, pp, sp, rows, dc, dr, pages->size(0), pages->size(1), stream);
+  Py_END_ALLOW_THREADS
+  return written(status, {pages});
+  END_HANDLE_TH_ERRORS
+}
+
+// bind(fourteen addresses): the entry points to call.
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
   void **const targets[] = {reinterpret_cast<void **>(&g_window_fwd),  reinterpret_cast<void **>(&g_window_fwd_f32),
                             reinterpret_cast<void **>(&g_window_bwd),  reinterpret_cast<void **>(&g_window_bwd_f32),
                             reinterpret_cast<void **>(&g_tree_decode), reinterpret_cast<void **>(&g_cache_append),
-                            reinterpret_cast<void **>(&g_cache_compact)};
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+                            reinterpret_cast<void **>(&g_cache_compact), reinterpret_cast<void **>(&g_latent_fwd),
+                            reinterpret_cast<void **>(&g_latent_bwd),  reinterpret_cast<void **>(&g_latent_decode),
+                            reinterpret_cast<void **>(&g_cache_reserve), reinterpret_cast<void **>(&g_cache_release),
+                            reinterpret_cast<void **>(&g_cache_write), reinterpret_cast<void **>(&g_latent_write)};
+  constexpr int kTargets = sizeof(targets) / sizeof(targets[0]);
+  if (n != kTargets) {
+    PyErr_SetString(PyExc_TypeError, "bind takes fourteen addresses");
     return nullptr;
   }
-  for (int i = 0; i < 7; ++i) *targets[i] = PyLong_AsVoidPtr(args[i]);
+  for (int i = 0; i < kTargets; ++i) *targets[i] = PyLong_AsVoidPtr(args[i]);
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -279,7 +499,10 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define XATTN_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {XATTN_METHOD(window_fwd),   XATTN_METHOD(window_bwd),    XATTN_METHOD(tree_decode),
-                           XATTN_METHOD(cache_append), XATTN_METHOD(cache_compact), XATTN_METHOD(bind),
+                           XATTN_METHOD(cache_append), XATTN_METHOD(cache_compact), XATTN_METHOD(latent_fwd),
+                           XATTN_METHOD(latent_bwd),   XATTN_METHOD(latent_decode), XATTN_METHOD(cache_reserve),
+                           XATTN_METHOD(cache_release), XATTN_METHOD(cache_write),  XATTN_METHOD(latent_write),
+                           XATTN_METHOD(bind),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "xattn_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

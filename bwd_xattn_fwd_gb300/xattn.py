@@ -79,6 +79,13 @@ _SIGS = {
     "xattn_tree_decode": [_vp] * 6 + [_i] * 10 + [_f] + [_vp] * 3,
     "xattn_cache_append": [_vp] * 6 + [_i] * 7 + [_vp],
     "xattn_cache_compact": [_vp] * 6 + [_i] * 7 + [_vp],
+    "xattn_latent_fwd": [_vp] * 3 + [_i] * 6 + [_f] + [_vp] * 3,
+    "xattn_latent_bwd": [_vp] * 6 + [_i] * 6 + [_f] + [_vp] * 4,
+    "xattn_latent_decode": [_vp] * 4 + [_i] * 8 + [_f] + [_vp] * 3,
+    "xattn_cache_reserve": [_vp] * 5 + [_i] * 5 + [_vp] * 4,
+    "xattn_cache_release": [_vp] * 5 + [_i] * 4 + [_vp],
+    "xattn_cache_write": [_vp] * 5 + [_i] * 5 + [_vp],
+    "xattn_latent_write": [_vp] * 4 + [_i] * 5 + [_vp],
     "xattn_trim_scratch": [_sz],
     "xattn_check_device_status": [_vp],
 }
@@ -252,6 +259,45 @@ def xattn_cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, 
           _addr(accepted), B, n, nkv, hd, num_pages, page_size, max_pages, _stream(stream))
 
 
+def xattn_latent_fwd(q, kv, k_rope, B, S, nh, dn, dr, dv, scale, o, lse, stream=None):
+    _call("xattn_latent_fwd", _addr(q), _addr(kv), _addr(k_rope), B, S, nh, dn, dr, dv, scale, _addr(o), _addr(lse),
+          _stream(stream))
+
+
+def xattn_latent_bwd(q, kv, k_rope, o, dO, lse, B, S, nh, dn, dr, dv, scale, dq, dkv, dk_rope, stream=None):
+    _call("xattn_latent_bwd", _addr(q), _addr(kv), _addr(k_rope), _addr(o), _addr(dO), _addr(lse), B, S, nh, dn, dr, dv,
+          scale, _addr(dq), _addr(dkv), _addr(dk_rope), _stream(stream))
+
+
+def xattn_latent_decode(q, pages, page_table, ctx_lens, B, n, nh, dc, dr, num_pages, page_size, max_pages, scale, o, lse,
+                        stream=None):
+    _call("xattn_latent_decode", _addr(q), _addr(pages), _addr(page_table), _addr(ctx_lens), B, n, nh, dc, dr, num_pages,
+          page_size, max_pages, scale, _addr(o), _addr(lse), _stream(stream))
+
+
+def xattn_cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, B, num_pages, page_size, max_pages, tokens,
+                        slots, offsets, granted, stream=None):
+    _call("xattn_cache_reserve", _addr(page_table), _addr(ctx_lens), _addr(new_lens), _addr(free_pages),
+          _addr(free_count), B, num_pages, page_size, max_pages, tokens, _addr(slots), _addr(offsets), _addr(granted),
+          _stream(stream))
+
+
+def xattn_cache_release(page_table, held_lens, keep_lens, free_pages, free_count, B, num_pages, page_size, max_pages,
+                        stream=None):
+    _call("xattn_cache_release", _addr(page_table), _addr(held_lens), _addr(keep_lens), _addr(free_pages),
+          _addr(free_count), B, num_pages, page_size, max_pages, _stream(stream))
+
+
+def xattn_cache_write(k_new, v_new, k_pages, v_pages, slots, rows, nkv, hd, num_pages, page_size, stream=None):
+    _call("xattn_cache_write", _addr(k_new), _addr(v_new), _addr(k_pages), _addr(v_pages), _addr(slots), rows, nkv, hd,
+          num_pages, page_size, _stream(stream))
+
+
+def xattn_latent_write(c, k_rope, pages, slots, rows, dc, dr, num_pages, page_size, stream=None):
+    _call("xattn_latent_write", _addr(c), _addr(k_rope), _addr(pages), _addr(slots), rows, dc, dr, num_pages, page_size,
+          _stream(stream))
+
+
 def xattn_trim_scratch(keep_bytes=0):
     """Gives back what the current device's scratch pool holds beyond keep_bytes and no call still
     uses."""
@@ -358,7 +404,9 @@ def _load_calls():
     spec.loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
                   ("xattn_window_fwd", "xattn_window_fwd_f32", "xattn_window_bwd", "xattn_window_bwd_f32",
-                   "xattn_tree_decode", "xattn_cache_append", "xattn_cache_compact")))
+                   "xattn_tree_decode", "xattn_cache_append", "xattn_cache_compact", "xattn_latent_fwd", "xattn_latent_bwd",
+                   "xattn_latent_decode", "xattn_cache_reserve", "xattn_cache_release", "xattn_cache_write",
+                   "xattn_latent_write")))
     return module
 
 
@@ -536,3 +584,149 @@ def cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted, stream
     return _again(name, out, lambda: cache_compact(k_pages, v_pages, page_table, ctx_lens, path, accepted), k_pages,
                   None, (*tensors, ("path", path, (B, path.shape[1]), torch.int32),
                          ("accepted", accepted, (B,), torch.int32)))
+
+
+def attention_latent_fwd(q, kv, k_rope, scale=None, stream=None):
+    """(o [B,S,nh,dv], lse [B,S,nh]) of latent attention in its expanded form, causal: q [B,S,nh,dn+dr], kv
+    [B,S,nh,dn+dv] (each head's key part, then its value), k_rope [B,S,dr], the part of the keys that
+    the heads share (bf16). scale: (dn + dr) ** -0.5 unless given."""
+    if stream is not None:
+        with _Elsewhere(q, stream):
+            return attention_latent_fwd(q, kv, k_rope, scale)
+    out = _calls.latent_fwd(q, kv, k_rope, scale)
+    if type(out) is tuple:
+        return out
+    name = "attention_latent_fwd"
+    return _again(name, out, lambda: attention_latent_fwd(q, kv, k_rope, scale), q, None, _latent(name, q, kv, k_rope))
+
+
+def attention_latent_bwd(q, kv, k_rope, o, dO, lse, scale=None, stream=None):
+    """(dq, dkv, dk_rope) for the tensors of attention_latent_fwd and the output gradient dO; k_rope's is
+    the sum over the heads."""
+    if stream is not None:
+        with _Elsewhere(q, stream):
+            return attention_latent_bwd(q, kv, k_rope, o, dO, lse, scale)
+    out = _calls.latent_bwd(q, kv, k_rope, o, dO, lse, scale)
+    if type(out) is tuple:
+        return out
+    import torch
+    name = "attention_latent_bwd"
+    tensors = _latent(name, q, kv, k_rope)
+    outs = (*q.shape[:3], kv.shape[3] - q.shape[3] + k_rope.shape[2])
+    return _again(name, out, lambda: attention_latent_bwd(q, kv, k_rope, o, dO, lse, scale), q, None,
+                  (*tensors, ("o", o, outs, torch.bfloat16), ("dO", dO, outs, torch.bfloat16),
+                   ("lse", lse, q.shape[:3], torch.float32)))
+
+
+def _latent(name, q, kv, k_rope):
+    import torch
+    _need_dims(name, q=(q, 4), kv=(kv, 4), k_rope=(k_rope, 3))
+    dn, dr = q.shape[3] - k_rope.shape[2], k_rope.shape[2]
+    if dn < 1 or kv.shape[3] <= dn:
+        raise ValueError(f"{name}: q has dn + dr numbers a head, kv dn + dv and k_rope dr: dn, dv >= 1 do not fit "
+                         f"{q.shape[3]}, {kv.shape[3]} and {dr}")
+    return (("q", q, q.shape, torch.bfloat16), ("kv", kv, (*q.shape[:3], kv.shape[3]), torch.bfloat16),
+            ("k_rope", k_rope, (*q.shape[:2], dr), torch.bfloat16))
+
+
+def attention_latent_decode(q, pages, page_table, ctx_lens, dc, scale, stream=None):
+    """(o [B,n,nh,dc], lse [B,n,nh]) of latent attention in its absorbed form, n <= 64 new tokens a sequence over
+    a paged cache: q [B,n,nh,dc+dr] against the rows of pages [num_pages,page_size,dc+dr] (bf16), whose first dc
+    numbers are the values too, through page_table [B,max_pages] and ctx_lens [B] (int32). The new tokens' rows
+    are already at positions ctx_lens .. ctx_lens + n - 1 (latent_write); token i sees positions 0 .. ctx_lens + i.
+    scale: that of the expanded heads."""
+    if stream is not None:
+        with _Elsewhere(q, stream):
+            return attention_latent_decode(q, pages, page_table, ctx_lens, dc, scale)
+    out = _calls.latent_decode(q, pages, page_table, ctx_lens, dc, scale)
+    if type(out) is tuple:
+        return out
+    import torch
+    name = "attention_latent_decode"
+    _need_dims(name, q=(q, 4), pages=(pages, 3), page_table=(page_table, 2))
+    if not 0 < dc < pages.shape[2]:
+        raise ValueError(f"{name}: dc = {dc} does not fit rows of {pages.shape[2]}")
+    B = page_table.shape[0]
+    return _again(name, out, lambda: attention_latent_decode(q, pages, page_table, ctx_lens, dc, scale), q, None,
+                  (("q", q, (B, *q.shape[1:3], pages.shape[2]), torch.bfloat16),
+                   ("pages", pages, pages.shape, torch.bfloat16), ("page_table", page_table, page_table.shape, torch.int32),
+                   ("ctx_lens", ctx_lens, (B,), torch.int32)))
+
+
+def cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_size, tokens, stream=None):
+    """Takes the pages for new_lens positions a sequence, from ctx_lens on, from the stack of free pages
+    (free_pages [num_pages], free_count [1]) into page_table [B,max_pages] (all int32; table and count in place).
+    Returns (slots [tokens] int64, offsets [B+1], granted [B]): the pool rows of a ragged batch's tokens (-1:
+    none), where each sequence's tokens begin, and the positions that it got (0 when the pages or `tokens` do
+    not reach)."""
+    if stream is not None:
+        with _Elsewhere(page_table, stream):
+            return cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_size, tokens)
+    out = _calls.cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_size, tokens)
+    if type(out) is tuple:
+        return out
+    name = "cache_reserve"
+    return _again(name, out, lambda: cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_size,
+                                                   tokens), page_table, None,
+                  _tables(name, page_table, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages,
+                          free_count=free_count))
+
+
+def cache_release(page_table, held_lens, keep_lens, free_pages, free_count, page_size, stream=None):
+    """Gives the pages that hold only positions from keep_lens to held_lens - 1 back to the stack, and sets
+    their entries of page_table to -1 (table, stack and count in place; tensors as for cache_reserve)."""
+    if stream is not None:
+        with _Elsewhere(page_table, stream):
+            return cache_release(page_table, held_lens, keep_lens, free_pages, free_count, page_size)
+    out = _calls.cache_release(page_table, held_lens, keep_lens, free_pages, free_count, page_size)
+    if out is True:
+        return None
+    name = "cache_release"
+    return _again(name, out, lambda: cache_release(page_table, held_lens, keep_lens, free_pages, free_count, page_size),
+                  page_table, None, _tables(name, page_table, held_lens=held_lens, keep_lens=keep_lens,
+                                            free_pages=free_pages, free_count=free_count))
+
+
+def _tables(name, page_table, free_pages, free_count, **lens):
+    import torch
+    _need_dims(name, page_table=(page_table, 2), free_pages=(free_pages, 1))
+    return (("page_table", page_table, page_table.shape, torch.int32),
+            *((label, t, page_table.shape[:1], torch.int32) for label, t in lens.items()),
+            ("free_pages", free_pages, free_pages.shape, torch.int32), ("free_count", free_count, (1,), torch.int32))
+
+
+def cache_write(k_new, v_new, k_pages, v_pages, slots, stream=None):
+    """Writes the rows k_new, v_new [rows,nkv,hd] to the pool rows that slots [rows] (int64) names, in place
+    (the slots of cache_reserve; a slot outside the pool drops its row)."""
+    if stream is not None:
+        with _Elsewhere(k_pages, stream):
+            return cache_write(k_new, v_new, k_pages, v_pages, slots)
+    out = _calls.cache_write(k_new, v_new, k_pages, v_pages, slots)
+    if out is True:
+        return None
+    import torch
+    name = "cache_write"
+    _need_dims(name, k_pages=(k_pages, 4), slots=(slots, 1))
+    rows = (slots.shape[0], *k_pages.shape[2:])
+    return _again(name, out, lambda: cache_write(k_new, v_new, k_pages, v_pages, slots), k_pages, None,
+                  (("k_pages", k_pages, k_pages.shape, torch.bfloat16), ("v_pages", v_pages, k_pages.shape, torch.bfloat16),
+                   ("slots", slots, slots.shape, torch.int64), ("k_new", k_new, rows, torch.bfloat16),
+                   ("v_new", v_new, rows, torch.bfloat16)))
+
+
+def latent_write(c, k_rope, pages, slots, stream=None):
+    """Writes the rows (c, k_rope) [rows,dc], [rows,dr] to the rows of pages [num_pages,page_size,dc+dr] that
+    slots [rows] (int64) names, in place (the slots of cache_reserve; a slot outside the pool drops its row)."""
+    if stream is not None:
+        with _Elsewhere(pages, stream):
+            return latent_write(c, k_rope, pages, slots)
+    out = _calls.latent_write(c, k_rope, pages, slots)
+    if out is True:
+        return None
+    import torch
+    name = "latent_write"
+    _need_dims(name, c=(c, 2), k_rope=(k_rope, 2), pages=(pages, 3), slots=(slots, 1))
+    return _again(name, out, lambda: latent_write(c, k_rope, pages, slots), pages, None,
+                  (("pages", pages, (*pages.shape[:2], c.shape[1] + k_rope.shape[1]), torch.bfloat16),
+                   ("slots", slots, slots.shape, torch.int64), ("c", c, (slots.shape[0], c.shape[1]), torch.bfloat16),
+                   ("k_rope", k_rope, (slots.shape[0], k_rope.shape[1]), torch.bfloat16)))

@@ -59,7 +59,8 @@ typedef enum {
     XATTN_ERR_GROUP = 3,              /* nh is not a multiple of nkv */
     XATTN_ERR_UNSUPPORTED_HD = 4,     /* bf16: hd not in {32, 64, 128} (the backward's
                                          stage calls and xattn_bwd_noalloc: {32, 64});
-                                         fp32: hd > 128 */
+                                         fp32: hd > 128; latent and page calls:
+                                         the sizes that their comments give */
     XATTN_ERR_MISALIGNED = 5,         /* a bf16 tensor pointer is not 16-byte aligned, or a float
                                          or int array not 4-byte (xattn_tree_decode's words: 8) */
     XATTN_ERR_CUDA = 6,               /* a CUDA runtime or driver call failed */
@@ -354,6 +355,95 @@ xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_t
                                  const int *ctx_lens, const int *path, const int *accepted,
                                  int B, int n, int nkv, int hd, int num_pages, int page_size,
                                  int max_pages, void *stream);
+
+/*
+ * Latent attention: the keys and values of all heads come from one latent vector c_j [dc] a token, and
+ * a part k_rope_j [dr] of every key (the one that carries the position) is shared by the heads. With
+ * up-projections W_k, W_v [nh, dc, dn], [nh, dc, dv]:
+ *   key of head h, token j: (c_j W_k[h], k_rope_j), value: c_j W_v[h].
+ * The pages have no counterpart. Two forms of the one operation:
+ *   expanded (training, prompts): the caller multiplies kv = c [W_k | W_v], and the attention runs over heads of
+ *     dn + dr and dv numbers, causal as in xattn_fwd;
+ *   absorbed (serving): with q_h W_k[h]^T for the query's dn part, every head's key is the cached row
+ *     (c_j, k_rope_j) itself and its value c_j; the caller multiplies the output by W_v[h]. A cached position
+ *     is dc + dr numbers however many heads there are.
+ *
+ * Expanded form, bf16, contiguous:
+ *   q [B, S, nh, dn + dr], kv [B, S, nh, dn + dv] (a head's key part, then its value), k_rope [B, S, dr],
+ *   o, dO [B, S, nh, dv], lse [B, S, nh] float; dq, dkv, dk_rope like q, kv, k_rope
+ *   s_ij = scale (q_i[:dn] . kv_j[:dn] + q_i[dn:] . k_rope_j) (j <= i), and with P, dS as at the top:
+ *   dq_i = scale sum_j dS_ij (kv_j[:dn], k_rope_j), dkv_j = (scale sum_i dS_ij q_i[:dn], sum_i P_ij dO_i),
+ *   dk_rope_j = scale sum_h sum_i dS_ij q_i[dn:].
+ * dn, dv multiples of 16 up to 128, dr of 16 up to 64 (else XATTN_ERR_UNSUPPORTED_HD); any S >= 1 up to 2^30;
+ * any finite scale whose product with log2 e is finite (the backward too). bf16 tensors 16-byte aligned, lse
+ * 4-byte. Arithmetic as in xattn_fwd and xattn_bwd; k_rope's gradient is summed over the heads in fp32. Every
+ * output is bit-for-bit reproducible. Scratch of the backward is stream-ordered, from the library's pool.
+ */
+xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope, int B, int S, int nh, int dn, int dr,
+                              int dv, float scale, void *o, float *lse, void *stream);
+xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope, const void *o, const void *dO,
+                              const float *lse, int B, int S, int nh, int dn, int dr, int dv, float scale, void *dq,
+                              void *dkv, void *dk_rope, void *stream);
+
+/*
+ * Absorbed form: n new tokens per sequence over a paged cache of latent rows, pages [num_pages, page_size,
+ * dc + dr] (bf16), with a page table and lengths as for xattn_tree_decode. The new tokens' rows are already in
+ * the cache, at positions ctx_b .. ctx_b + n - 1 (xattn_latent_write); token i sees positions 0 .. ctx_b + i.
+ *   q [B, n, nh, dc + dr] bf16;  o [B, n, nh, dc] bf16 out;  lse [B, n, nh] float out
+ * scale multiplies the scores; it is that of the expanded heads (1 / sqrt(dn + dr)).
+ * dc 128, 256, 384 or 512, dr a multiple of 16 up to 64 (else XATTN_ERR_UNSUPPORTED_HD); n <= XATTN_TREE_MAX, any
+ * nh with B * n * nh <= 2^28 (else XATTN_ERR_BAD_SHAPE). A table entry that is no page: its positions are not
+ * visible. A token that sees nothing gives o = 0 and lse = -infinity. Positions from ctx_b + n on are never used
+ * and may hold anything, NaN included; rows that some token of the sequence sees must be finite. Alignment,
+ * arithmetic, scratch and reproducibility as for xattn_tree_decode.
+ */
+xattn_status xattn_latent_decode(const void *q, const void *pages, const int *page_table, const int *ctx_lens, int B,
+                                 int n, int nh, int dc, int dr, int num_pages, int page_size, int max_pages, float scale,
+                                 void *o, float *lse, void *stream);
+
+/*
+ * The page tables of a paged cache, kept on the device. The free pages are a stack: free_pages [num_pages]
+ * (int) holds free_count[0] page numbers, the last of them on top; the rest of the array means nothing.
+ *
+ * xattn_cache_reserve gives each sequence b the pages for new_lens[b] positions from ctx_lens[b] on, and says
+ * where the rows of a ragged batch go whose tokens lie one sequence after the other:
+ *   page_table [B, max_pages]: the entries of the new pages are written, no other
+ *   free_count: less the pages taken; the k-th page taken is free_pages[free_count - 1 - k]
+ *   offsets [B + 1]: sequence b's tokens are offsets[b] .. offsets[b + 1] - 1 (sums of new_lens)
+ *   granted [B]: positions that sequence b got: new_lens[b], less what its table cannot hold; 0 when the
+ *     free pages do not reach to the end of its need, or the `tokens` entries of the slot map to the end of its
+ *     tokens (sequences before it are served first; one that needs no new page is served all the same)
+ *   slots [tokens]: token t's row of the pool, page * page_size + row in the page; -1 for tokens that got
+ *     none, and behind the last one
+ * The pages below ctx_lens[b] are the sequence's already (a partly filled one goes on being filled). The lengths
+ * are taken within [0, max_pages * page_size].
+ *
+ * xattn_cache_release gives the pages that hold only positions from keep_lens[b] to held_lens[b] - 1 back (a
+ * finished request: keep 0; rejected drafts: what was accepted) and sets their table entries to -1; entries
+ * that are no page are skipped. A release of what a reserve granted restores the stack. What would not
+ * fit the stack (a page given back twice) is dropped.
+ *
+ * page_size as above (else XATTN_ERR_PAGES); int arrays 4-byte aligned, slots 8-byte. Two sequences must not
+ * share a page that is released. Scratch is stream-ordered, from the library's pool.
+ */
+xattn_status xattn_cache_reserve(int *page_table, const int *ctx_lens, const int *new_lens, const int *free_pages,
+                                 int *free_count, int B, int num_pages, int page_size, int max_pages, int tokens,
+                                 long long *slots, int *offsets, int *granted, void *stream);
+xattn_status xattn_cache_release(int *page_table, const int *held_lens, const int *keep_lens, int *free_pages,
+                                 int *free_count, int B, int num_pages, int page_size, int max_pages, void *stream);
+
+/*
+ * Writes the rows of a ragged batch to the rows of the pool that slots [rows] names (xattn_cache_reserve).
+ * A slot outside [0, num_pages * page_size) is no place: its row is dropped. No slot twice. rows may be 0.
+ *   xattn_cache_write : k_new, v_new [rows, nkv, hd] into k_pages, v_pages; hd a multiple of 8
+ *   xattn_latent_write: c [rows, dc] and k_rope [rows, dr] side by side into pages [num_pages, page_size, dc + dr];
+ *                       dc and dr multiples of 8 (else XATTN_ERR_UNSUPPORTED_HD)
+ * Any page_size. bf16 tensors 16-byte aligned, slots 8-byte. No scratch.
+ */
+xattn_status xattn_cache_write(const void *k_new, const void *v_new, void *k_pages, void *v_pages, const long long *slots,
+                               int rows, int nkv, int hd, int num_pages, int page_size, void *stream);
+xattn_status xattn_latent_write(const void *c, const void *k_rope, void *pages, const long long *slots, int rows, int dc,
+                                int dr, int num_pages, int page_size, void *stream);
 
 /*
  * Gives back to CUDA what the library's scratch pool of the current device holds beyond
