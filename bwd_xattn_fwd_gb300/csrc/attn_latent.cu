@@ -136,48 +136,6 @@ __global__ void __launch_bounds__(kPlain) latent_rope_plain(const LatentArgs a) 
   a.dk_rope[t] = __float2bfloat16(g);
 }
 
-__global__ void __launch_bounds__(kPlain) latent_decode_plain(const LatentDecodeArgs a) {
-  __shared__ float qs[576], ps[kPlain], part[kPlain / 32];
-  __shared__ long long at[kPlain];
-  const int rows = a.n * a.nh, r = static_cast<int>(blockIdx.x % rows), b = static_cast<int>(blockIdx.x / rows);
-  const int dq = a.dc + a.dr, tid = threadIdx.x;
-  const size_t row = static_cast<size_t>(b) * rows + r;
-  for (int d = tid; d < dq; d += kPlain) qs[d] = __bfloat162float(a.q[row * dq + d]);
-  __syncthreads();
-  const int ctx = min(max(a.ctx_lens[b], 0), a.max_pages * a.page_size - a.n), end = ctx + r / a.nh + 1;
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int j0 = 0; j0 < end; j0 += kPlain) {
-    const int j = j0 + tid;
-    long long place = -1;
-    if (j < end) {
-      const int id = a.page_table[static_cast<size_t>(b) * a.max_pages + j / a.page_size];
-      if (id >= 0 && id < a.num_pages) place = static_cast<long long>(id) * a.page_size + j % a.page_size;
-    }
-    float s = -INFINITY;
-    if (place >= 0) {
-      s = 0.f;
-      for (int d = 0; d < dq; ++d) s = fmaf(qs[d], __bfloat162float(a.pages[place * dq + d]), s);
-      s *= a.scale_log2;
-    }
-    at[tid] = place;
-    const float mn = fmaxf(m, block_reduce(s, true, part)), base = mn == -INFINITY ? 0.f : mn, alpha = exp2f(m - base);
-    const float p = exp2f(s - base);
-    ps[tid] = p;
-    l = l * alpha + block_reduce(p, false, part);
-    m = mn;
-    for (int e = 0; e < 2; ++e) {
-      o[e] *= alpha;
-      if (tid + e * kPlain < a.dc)
-        for (int x = 0; x < kPlain; ++x)
-          if (j0 + x < end && at[x] >= 0) o[e] = fmaf(ps[x], __bfloat162float(a.pages[at[x] * dq + tid + e * kPlain]), o[e]);
-    }
-    __syncthreads();
-  }
-  for (int e = 0; e < 2; ++e)
-    if (tid + e * kPlain < a.dc) a.o[row * a.dc + tid + e * kPlain] = __float2bfloat16(l != 0.f ? o[e] / l : 0.f);
-  if (tid == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
 }  // namespace
 
 size_t latent_bwd_workspace_bytes(const LatentArgs &a) {
@@ -198,9 +156,4 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream) {
   latent_rope_plain<<<static_cast<unsigned>((static_cast<size_t>(a.B) * a.S * a.dr + kPlain - 1) / kPlain), kPlain, 0, stream>>>(a);
   return cudaGetLastError();
 }
-cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
-  latent_decode_plain<<<static_cast<unsigned>(a.B) * a.n * a.nh, kPlain, 0, stream>>>(a);
-  return cudaGetLastError();
-}
-
 }  // namespace xattn

@@ -1,0 +1,677 @@
+// Latent attention in its absorbed form: a few new tokens per sequence over a paged cache whose rows
+// (c, k_rope) are the keys of every head, and whose c are the values.
+//
+// GB300 mapping. A cached position is 2 (dc + dr) bytes for all heads, and 2 (2 dc + dr) flops a query row:
+// with 16 rows HBM bounds the operation, with 128 the tensor cores come near to it. The cache is read once per
+// row tile, in tiles of 64 positions:
+//   * S^T = C Q^T : positions are the M = 64 rows, the query rows (token, head) the N columns, so that a few
+//     heads do not cost the 128 rows that a query tile has; and O^T += C^T P^T with the 128 numbers of a latent
+//     block as M. One copy of the tile in shared memory is K-major for the first product and MN-major for the
+//     second. O^T [dc, N] fp32 takes dc / 128 x N of the 512 TMEM columns, so N is at most 64: 16, 32 or 64
+//     query rows a row tile, and several row tiles where there are more.
+//   * Rings: a tile is dc / 128 pairs of 64-column sub-tiles (16 KB) and the shared part (8 KB); a pair is free
+//     again as soon as its block of O^T has been added, so loads go on while a tile is worked on.
+//   * Softmax: a thread has one position and half of the columns; a column's maximum over the positions would be a
+//     reduction over lanes. It is needed only where some score exceeds the column's running maximum by more than
+//     2^8 (the stale one is exact because the final division uses the same): each tile asks just that, in one vote,
+//     and only where the answer is yes are the maxima taken and O^T rescaled. Sums stay with the threads
+//     until the end.
+//   * Work: the sequences' tiles form one line that is cut into equal runs, one per group of CTAs, a CTA of the
+//     group per row tile (they read the same tiles at the same time, the second from L2); lengths are read on the
+//     device, so a captured graph follows them. A run's end cuts a sequence: such pieces write (max, sum, O)
+//     records, and latent_combine_kernel merges them in order.
+//   * Roundings: scores, maxima, sums and O are fp32; P is rounded to bf16, C's type.
+//   * Pages as in attn_tree.cu: a box whose table entry is no page is loaded from outside the pool (zeros).
+// Warps: 0 TMA producer; 1 TMEM owner and MMA issuer; 2-9 softmax (warp & 3: lane quarter; two halves of the columns).
+// TMEM: S^T buffers [0, N), [N, 2N); O^T block j [2N + j N, 2N + (j + 1) N).
+#include <cfloat>
+#include <type_traits>
+
+#include "sm103_ptx.cuh"
+#include "xattn_internal.h"
+
+namespace xattn {
+namespace {
+
+constexpr int kTilePos = 64;                       // positions of a tile
+constexpr int kLatThreads = 320;
+constexpr int kSoftWarps = 8;
+
+// N: query rows (columns) of a row tile.
+template <int N>
+struct LatLayout {
+  static constexpr uint32_t kSub = kTilePos * 128;               // a sub-tile of 64 columns
+  static constexpr uint32_t kPair = 2 * kSub;
+  static constexpr int kPairs = N == 64 ? 8 : (N == 32 ? 10 : 11);
+  static constexpr int kRopes = N == 64 ? 2 : 3;
+  static constexpr uint32_t kQSub = N * 128;                     // 64 columns of the query rows
+  static constexpr uint32_t kPRow = N * 2;
+  static constexpr uint32_t kSwizzleP = N == 64 ? kSwizzle128 : (N == 32 ? kSwizzle64 : kSwizzle32);
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kP = kQ + 9 * kQSub;
+  static constexpr uint32_t kC = kP + kTilePos * kPRow;
+  static constexpr uint32_t kR = kC + kPairs * kPair;
+  static constexpr uint32_t kBars = kR + kRopes * kSub;
+  static constexpr int kNumBars = 2 * kPairs + 2 * kRopes + 9;
+  static constexpr uint32_t kBase = (kBars + 8 * kNumBars + 15) / 16 * 16;   // float [N] maxima, [N] factors, [4][N] parts
+  static constexpr uint32_t kFlags = kBase + 6 * N * 4;
+  static constexpr uint32_t kHeld = kFlags + 2 * kSoftWarps * 4;             // per rope slot: boxes that hold a page
+  static constexpr uint32_t kMisc = (kHeld + 4 * kRopes + 15) / 16 * 16;
+  static constexpr uint32_t kUsed = kMisc + 32;
+  static constexpr uint32_t kDynBytes = kUsed + 1024;
+  static_assert(kP % 1024 == 0 && kC % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+  static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
+  static_assert(kDynBytes > 114 * 1024, "one CTA an SM: each holds all TMEM columns");
+};
+
+__device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+  const bool ok = mbar_wait(bar, parity, ctl);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void lat_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ int lat_ctx(const LatentDecodeArgs &a, int b) {
+  return min(max(a.ctx_lens[b], 0), a.max_pages * a.page_size - a.n);
+}
+__device__ __forceinline__ int lat_tiles(const LatentDecodeArgs &a, int b) {
+  return (lat_ctx(a, b) + a.n + kTilePos - 1) / kTilePos;
+}
+
+// The line of `length` tiles in `runs` runs: the first length % runs have one more.
+struct LatRuns {
+  int each, more;
+  __device__ LatRuns(int length, int runs) : each(length / runs), more(length - length / runs * runs) {}
+  __device__ int start(int c) const { return c * each + min(c, more); }
+  __device__ int of(int pos) const {
+    const int head = more * (each + 1);
+    return pos < head ? pos / (each + 1) : more + (pos - head) / each;
+  }
+};
+
+// A run of the line, walked piece by piece; warp-uniform, every role walks the same pieces.
+struct LatWalk {
+  int pos, stop;           // next tile and end of the run, on the line
+  int first;               // where sequence b starts on it
+  int b, ctx, count;       // sequence, its committed positions and tiles
+  int e0, e1;              // the piece: tiles [e0, e1) of the sequence
+};
+
+__device__ __forceinline__ bool lat_piece(LatWalk &w, const LatentDecodeArgs &a) {
+  if (w.pos >= w.stop) return false;
+  if (w.pos - w.first >= w.count) {
+    w.first += w.count;
+    if (++w.b >= a.B) return false;                              // (only if the lengths change under the call)
+    w.ctx = lat_ctx(a, w.b);
+    w.count = (w.ctx + a.n + kTilePos - 1) / kTilePos;
+  }
+  w.e0 = w.pos - w.first;
+  w.e1 = min(w.count, w.e0 + (w.stop - w.pos));
+  w.pos += w.e1 - w.e0;
+  return true;
+}
+
+// The line's length, and this group's run of it. Lane l takes B / 32 sequences in a row.
+__device__ __forceinline__ LatRuns lat_start(const LatentDecodeArgs &a, int group, int groups, int lane, LatWalk &w) {
+  const int each = (a.B + 31) / 32, b0 = lane * each, b1 = min(a.B, b0 + each);
+  int mine = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) mine += lat_tiles(a, b);
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += up;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  const LatRuns runs(total, min(groups, total));
+  w.pos = w.stop = 0;
+  if (group >= total) return runs;
+  w.pos = runs.start(group);
+  w.stop = runs.start(group + 1);
+  const unsigned past = __ballot_sync(0xffffffffu, incl > w.pos);
+  const int l = __ffs(past) - 1;
+  int b = b0, at = incl - mine;
+  if (lane == l) {
+    for (int c = lat_tiles(a, b); at + c <= w.pos; c = lat_tiles(a, b)) at += c, ++b;
+  }
+  w.b = __shfl_sync(0xffffffffu, b, l);
+  w.first = __shfl_sync(0xffffffffu, at, l);
+  w.ctx = lat_ctx(a, w.b);
+  w.count = (w.ctx + a.n + kTilePos - 1) / kTilePos;
+  return runs;
+}
+
+// Order of floats as integers (for a maximum over lanes in one instruction).
+__device__ __forceinline__ int float_key(float x) {
+  const int k = __float_as_int(x);
+  return k ^ ((k >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t *r) {
+  if constexpr (C == 32) tmem_ld_x32(addr, r);
+  else if constexpr (C == 16) tmem_ld_x16(addr, r);
+  else tmem_ld_x8(addr, r);
+}
+__device__ __forceinline__ void tmem_st_x8_words(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <int C>
+__device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t *r) {
+  if constexpr (C == 32) tmem_st_x32(addr, r);
+  else if constexpr (C == 16) tmem_st_x16(addr, r);
+  else tmem_st_x8_words(addr, r);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kLatThreads, 1)
+    latent_decode_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mc,
+                         const LatentDecodeArgs a) {
+  using L = LatLayout<N>;
+  constexpr int kPairs = L::kPairs, kRopes = L::kRopes;
+  extern __shared__ uint8_t latent_smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t sQ = smem_u32(smem + L::kQ), sP = smem_u32(smem + L::kP), sC = smem_u32(smem + L::kC),
+                 sR = smem_u32(smem + L::kR), bar0 = smem_u32(smem + L::kBars);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  auto c_full = [&](int s) { return bar(s); };
+  auto c_empty = [&](int s) { return bar(kPairs + s); };
+  auto r_full = [&](int s) { return bar(2 * kPairs + s); };
+  auto r_empty = [&](int s) { return bar(2 * kPairs + kRopes + s); };
+  constexpr int kB = 2 * kPairs + 2 * kRopes;
+  auto s_full = [&](int x) { return bar(kB + x); };
+  auto s_free = [&](int x) { return bar(kB + 2 + x); };
+  const uint32_t p_full = bar(kB + 4), o_done = bar(kB + 5), q_full = bar(kB + 6), q_empty = bar(kB + 7), meet = bar(kB + 8);
+  float *base = reinterpret_cast<float *>(smem + L::kBase), *factor = base + N, *parts = base + 2 * N;
+  volatile int *flags = reinterpret_cast<volatile int *>(smem + L::kFlags);
+  volatile uint32_t *held_boxes = reinterpret_cast<volatile uint32_t *>(smem + L::kHeld);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
+  const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
+  XATTN_DCHECK(smem + L::kUsed <= latent_smem_raw + L::kDynBytes, a.status);
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < kB; ++s) mbar_init(bar(s), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full(x), 1);
+      mbar_init(s_free(x), kSoftWarps);
+    }
+    mbar_init(p_full, kSoftWarps);
+    mbar_init(o_done, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(meet, kSoftWarps);
+    fence_mbar_init();
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mc);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch();
+  grid_dep_wait();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+  const uint32_t tS = tmem, tO = tmem + 2 * N;
+
+  const int group = static_cast<int>(blockIdx.x) / a.row_tiles, rt = static_cast<int>(blockIdx.x) - group * a.row_tiles;
+  const int groups = static_cast<int>(gridDim.x) / a.row_tiles, blocks = a.dc / 128;
+  LatWalk walk;
+  const LatRuns runs = lat_start(a, group, groups, lane, walk);
+
+  if (warp == 0) {
+    // ---------------- TMA producer: lane l finds box l of each tile ----------------
+    const int box_rows = min(a.page_size, kTilePos), boxes = kTilePos / box_rows;
+    const uint32_t box_bytes = box_rows * 128u;
+    int R = 0, Rj = 0, issued_c = 0, issued_r = 0, pieces = 0;
+    bool ok = true;
+    while (ok && lat_piece(walk, a)) {
+      if (!lat_wait(q_empty, (pieces & 1) ^ 1, ctl)) break;
+      mbar_expect_tx_elect(q_full, (2 * blocks + 1) * L::kQSub);
+      for (int c = 0; c <= 2 * blocks; ++c) tma_load_4d_elect(sQ + c * L::kQSub, &mq, q_full, 64 * c, rt * N, walk.b, 0);
+      ++pieces;
+      const int *table = a.page_table + static_cast<size_t>(walk.b) * a.max_pages;
+      const int end = walk.ctx + a.n;
+      // This lane's box of tile e: its table entry (-1 past the end), read one tile ahead.
+      auto box_of = [&](int e, int *row) -> int {
+        const int p0 = e * kTilePos + lane * box_rows, at = p0 / a.page_size;
+        *row = p0 - at * a.page_size;
+        if (lane >= boxes || e >= walk.e1 || p0 >= end) return -1;
+        return __ldg(table + at);
+      };
+      int row_next = 0, id_next = box_of(walk.e0, &row_next);
+#pragma unroll 1
+      for (int e = walk.e0; ok && e < walk.e1; ++e, ++R) {
+        const int page = id_next >= 0 && id_next < a.num_pages ? id_next : a.num_pages, row = row_next;
+        id_next = box_of(e + 1, &row_next);
+        const unsigned held = __ballot_sync(0xffffffffu, page != a.num_pages);
+        int pg[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pg[x] = __shfl_sync(0xffffffffu, page, x);
+        const int rw = __shfl_sync(0xffffffffu, row, 0);
+        XATTN_DCHECK(page >= 0 && page <= a.num_pages && row >= 0 && row + box_rows <= a.page_size && boxes <= 4, a.status);
+        auto load_sub = [&](uint32_t dst, uint32_t full, int col) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (x < boxes) tma_load_4d(dst + x * box_bytes, &mc, full, col, x == 0 ? rw : 0, pg[x], 0);
+        };
+#pragma unroll 1
+        for (int j = 0; j < blocks; ++j, ++Rj) {
+          const int s = Rj % kPairs;
+          if (!lat_wait(c_empty(s), ((Rj / kPairs) & 1) ^ 1, ctl)) { ok = false; break; }
+          if (elect_one()) {
+            mbar_expect_tx(c_full(s), L::kPair);
+            load_sub(sC + s * L::kPair, c_full(s), 128 * j);
+            load_sub(sC + s * L::kPair + L::kSub, c_full(s), 128 * j + 64);
+          }
+          __syncwarp();
+          issued_c = Rj + 1;
+        }
+        if (!ok) break;
+        const int s = R % kRopes;
+        if (!lat_wait(r_empty(s), ((R / kRopes) & 1) ^ 1, ctl)) { ok = false; break; }
+        if (elect_one()) {
+          held_boxes[s] = held;                                  // read by the softmax warps before the slot's next use
+          mbar_expect_tx(r_full(s), L::kSub);
+          load_sub(sR + s * L::kSub, r_full(s), a.dc);
+        }
+        __syncwarp();
+        issued_r = R + 1;
+      }
+    }
+    __syncwarp();
+    // Every copy in flight has landed before the CTA can exit.
+    if (pieces > 0) mbar_drain(q_full, (pieces - 1) & 1, ctl);
+    for (int r = max(issued_c - kPairs, 0); r < issued_c; ++r) mbar_drain(c_full(r % kPairs), (r / kPairs) & 1, ctl);
+    for (int r = max(issued_r - kRopes, 0); r < issued_r; ++r) mbar_drain(r_full(r % kRopes), (r / kRopes) & 1, ctl);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    constexpr uint32_t idesc_s = idesc_bf16_f32(64, N, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, true, true);
+    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
+    const uint64_t dC = smem_desc(sC, 16, 1024, kSwizzle128), dR = smem_desc(sR, 16, 1024, kSwizzle128);
+    const uint64_t dCt = smem_desc(sC, L::kSub, 1024, kSwizzle128);      // MN-major: 64 columns a sub-tile
+    const uint64_t dP = smem_desc(sP, 16, 8 * L::kPRow, L::kSwizzleP);   // MN-major
+    const int rope_steps = a.dr / 16;
+    // S^T of ring tile R (pairs from Rj on): after its last reader has read the buffer.
+    auto scores = [&](int R, int Rj, bool last) -> bool {
+      if (!lat_wait(s_free(R & 1), ((R >> 1) & 1) ^ 1, ctl)) return false;
+      const uint32_t d = tS + (R & 1) * N;
+#pragma unroll 1
+      for (int j = 0; j < blocks; ++j) {
+        const int s = (Rj + j) % kPairs;
+        if (!lat_wait(c_full(s), ((Rj + j) / kPairs) & 1, ctl)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(d, dC + s * (L::kPair >> 4) + (kk / 4) * (L::kSub >> 4) + (kk % 4) * 2,
+                   dQ + (2 * j + kk / 4) * (L::kQSub >> 4) + (kk % 4) * 2, idesc_s, (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+      }
+      const int s = R % kRopes;
+      if (!lat_wait(r_full(s), (R / kRopes) & 1, ctl)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        for (int kk = 0; kk < rope_steps; ++kk)
+          mma_ss(d, dR + s * (L::kSub >> 4) + kk * 2, dQ + 2 * blocks * (L::kQSub >> 4) + kk * 2, idesc_s, 1u);
+        mma_commit(s_full(R & 1));
+        if (last) mma_commit(q_empty);
+      }
+      __syncwarp();
+      return true;
+    };
+    int R = 0, Rj = 0, piece = 0, scored = 0;
+    bool ok = true;
+    while (ok && lat_piece(walk, a)) {
+      ok = lat_wait(q_full, piece & 1, ctl) && scores(R, Rj, walk.e0 + 1 == walk.e1);
+      if (!ok) break;
+      scored = R + 1;
+#pragma unroll 1
+      for (int e = walk.e0; e < walk.e1; ++e, ++R, Rj += blocks) {
+        if (e + 1 < walk.e1) {
+          if (!scores(R + 1, Rj + blocks, e + 2 == walk.e1)) { ok = false; break; }
+          scored = R + 2;
+        }
+        if (!lat_wait(p_full, R & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          for (int j = 0; j < blocks; ++j) {
+            const int s = (Rj + j) % kPairs;
+#pragma unroll
+            for (int kk = 0; kk < kTilePos / 16; ++kk)
+              mma_ss(tO + j * N, dCt + s * (L::kPair >> 4) + kk * 128, dP + kk * L::kPRow, idesc_o,
+                     (e > walk.e0 || kk > 0) ? 1u : 0u);
+            mma_commit(c_empty(s));
+          }
+          mma_commit(o_done);
+        }
+        __syncwarp();
+      }
+      ++piece;
+    }
+    __syncwarp();
+    // The last products are done before TMEM goes.
+    if (scored > 0) mbar_drain(s_full((scored - 1) & 1), ((scored - 1) >> 1) & 1, ctl);
+    if (R > 0) mbar_drain(o_done, (R - 1) & 1, ctl);
+  } else {
+    // ---------------- softmax: thread = one position, half of the columns ----------------
+    constexpr int C = N / 2;
+    const int quarter = warp & 3, half = (warp - 2) >> 2, tid = static_cast<int>(threadIdx.x) - 64;
+    const int pos = quarter * 16 + (lane & 15);                    // M = 64: 16 rows in each quarter's lanes 0-15
+    const bool live = lane < 16;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int box_rows = min(a.page_size, kTilePos);
+    const unsigned all_boxes = (1u << (kTilePos / box_rows)) - 1u;
+    const int rows_all = a.n * a.nh, row0 = rt * N, rows = min(rows_all - row0, N);
+    int R = 0, meets = 0;
+    bool ok = true;
+    auto meet_all = [&]() -> bool {
+      lat_arrive(meet, lane);
+      return lat_wait(meet, meets++ & 1, ctl);
+    };
+    if (warp == 2 && lane == 0 && rt == 0) a.plan[group] = make_int2(0, 0);
+    while (ok && lat_piece(walk, a)) {
+      const int e0 = walk.e0, e1 = walk.e1, b = walk.b, ctx = walk.ctx, end = ctx + a.n;
+      const bool whole = e0 == 0 && e1 == walk.count;
+      // A run that ends inside the sequence it started last says so to the combine.
+      if (warp == 2 && lane == 0 && rt == 0 && e0 == 0 && e1 < walk.count)
+        a.plan[group] = make_int2(b, runs.of(walk.first + walk.count - 1) + 1);
+      float l[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) l[c] = 0.f;
+#pragma unroll 1
+      for (int e = e0; e < e1; ++e, ++R) {
+        const bool first = e == e0;
+        if (!lat_wait(s_full(R & 1), (R >> 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        const unsigned held = held_boxes[R % kRopes];
+        float x[C];
+        uint32_t *xr = reinterpret_cast<uint32_t *>(x);
+        tmem_ld_cols<C>(tS + (R & 1) * N + half * C + lane_off, xr);
+        tmem_wait_ld();
+        reg_fence<C>(xr);
+        tc_fence_before();
+        lat_arrive(s_free(R & 1), lane);
+        // (Scores carry held_boxes' slot: the copy that overwrites it waits for r_empty, below.)
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] *= a.scale_log2;
+        const int p = e * kTilePos + pos;
+        if (e * kTilePos + kTilePos > ctx + 1 || held != all_boxes) {
+          // Positions that some row does not see: new ones, those behind the last, missing pages.
+          const bool there = (held >> (pos / box_rows)) & 1u;
+          int token = (row0 + half * C) / a.nh, left = (token + 1) * a.nh - (row0 + half * C);
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            if (!there || p >= end || p > ctx + token) x[c] = -INFINITY;
+            if (--left == 0) ++token, left = a.nh;
+          }
+          // Rows behind the last position may hold anything and are zeroed before P meets them (0 x NaN would not
+          // be 0).
+          if (live && p >= end) {
+            const int Rj = R * blocks;
+            for (int j = half; j < 2 * blocks; j += 2) {
+              uint8_t *row = smem + L::kC + ((Rj + j / 2) % kPairs) * L::kPair + (j & 1) * L::kSub + pos * 128;
+#pragma unroll
+              for (int v = 0; v < 8; ++v) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        if (!live) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) x[c] = -INFINITY;
+        }
+        // Does some score pass its column's base by more than 2^8? A piece's first tile always asks.
+        bool grow = first;
+        if (!first) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < C; c += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(base + half * C + c);
+            top = fmax3(top, x[c] - m.x, x[c + 1] - m.y);
+            top = fmax3(top, x[c + 2] - m.z, x[c + 3] - m.w);
+          }
+          grow = top > 8.f;
+        }
+        const bool warp_grows = __any_sync(0xffffffffu, grow);
+        if (lane == 0) flags[(R & 1) * kSoftWarps + warp - 2] = warp_grows;
+        if (!meet_all()) { ok = false; break; }
+        int any = 0;
+#pragma unroll
+        for (int w = 0; w < kSoftWarps; ++w) any |= flags[(R & 1) * kSoftWarps + w];
+        if (any) {
+          // The columns' maxima: over a warp's positions, then over the four quarters.
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int k = __reduce_max_sync(0xffffffffu, float_key(x[c]));
+            if (lane == (c & 31)) parts[quarter * N + half * C + c] = key_float(k);
+          }
+          if (!meet_all()) { ok = false; break; }
+          if (tid < N) {
+            // (-FLT_MAX stands for nothing seen: any score is far above it, and differences stay numbers.)
+            const float old = first ? -FLT_MAX : base[tid];
+            float m = old;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = parts[q * N + tid] > m || parts[q * N + tid] != parts[q * N + tid] ? parts[q * N + tid] : m;
+            factor[tid] = ex2_approx(old - m);
+            base[tid] = m;
+          }
+          if (!meet_all()) { ok = false; break; }
+        }
+        // P over the last tile's, which its product has read then; O^T is at rest too.
+        if (!lat_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (any && !first) {
+          const float *f = factor + half * C;
+#pragma unroll
+          for (int c = 0; c < C; ++c) l[c] *= f[c];
+#pragma unroll 1
+          for (int j = 0; j < blocks; ++j) {
+            uint32_t ov[C];
+            const uint32_t at = tO + j * N + half * C + lane_off;
+            tmem_ld_cols<C>(at, ov);
+            tmem_wait_ld();
+            reg_fence<C>(ov);
+#pragma unroll
+            for (int c = 0; c < C; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * f[c]);
+            tmem_st_cols<C>(at, ov);
+          }
+          tmem_wait_st();
+        }
+        uint32_t pk[C / 2];
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          const float4 m = *reinterpret_cast<const float4 *>(base + half * C + c);
+          const float p0 = ex2_approx(x[c] - m.x), p1 = ex2_approx(x[c + 1] - m.y);
+          const float p2 = ex2_approx(x[c + 2] - m.z), p3 = ex2_approx(x[c + 3] - m.w);
+          l[c] += p0, l[c + 1] += p1, l[c + 2] += p2, l[c + 3] += p3;
+          pk[c / 2] = pack_bf16x2(p0, p1);
+          pk[c / 2 + 1] = pack_bf16x2(p2, p3);
+        }
+        if (live) {
+#pragma unroll
+          for (int v = 0; v < C / 8; ++v) {
+            const int chunk = half * (C / 8) + v;
+            const int sw = N == 64 ? (chunk ^ (pos & 7)) : (N == 32 ? (chunk ^ ((pos >> 1) & 3)) : (chunk ^ ((pos >> 2) & 1)));
+            *reinterpret_cast<uint4 *>(smem + L::kP + pos * L::kPRow + (sw << 4)) =
+                make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (warp == 2 && lane == 0) mbar_arrive(r_empty(R % kRopes));
+        lat_arrive(p_full, lane);
+      }
+      if (!ok) break;
+      // The piece's sums meet in `parts`; its O^T and LSE, or its record (O not divided by the sum).
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float s = live ? l[c] : 0.f;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (lane == (c & 31)) parts[quarter * N + half * C + c] = s;
+      }
+      if (!meet_all()) { ok = false; break; }
+      const size_t rec = (2 * static_cast<size_t>(blockIdx.x) + (e0 == 0 ? 1 : 0)) * N;
+      const size_t out = static_cast<size_t>(b) * rows_all + row0;
+      if (tid < N) {
+        const float sum = (parts[tid] + parts[N + tid]) + (parts[2 * N + tid] + parts[3 * N + tid]), m = base[tid];
+        factor[tid] = !whole ? 1.f : (sum != 0.f ? 1.f / sum : 0.f);
+        if (tid < rows) {
+          if (whole)
+            a.lse[out + tid] = sum != 0.f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+          else
+            a.ws_ml[rec + tid] = make_float2(m, sum);
+        }
+      }
+      if (!meet_all() || !lat_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; j < blocks; ++j) {
+        uint32_t ov[C];
+        tmem_ld_cols<C>(tO + j * N + half * C + lane_off, ov);
+        tmem_wait_ld();
+        reg_fence<C>(ov);
+        const int d = j * 128 + quarter * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int r = half * C + c;
+          if (r < rows) {
+            const float f = factor[r], v = __uint_as_float(ov[c]);
+            if (whole)
+              a.o[(out + r) * a.dc + d] = __float2bfloat16_rn(f != 0.f ? v * f : 0.f);
+            else
+              a.ws_o[(rec + r) * a.dc + d] = v;
+          }
+        }
+        __syncwarp();                                            // (the reads of TMEM are the warp's)
+      }
+      tc_fence_before();
+      if (!meet_all()) { ok = false; break; }                    // factor and parts are read
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merges the records of the cut sequences: block (c, row) takes one query row of the sequence that run c starts and
+// does not finish, if there is one (plan[c]: sequence, past the last run). Half of the block takes every second
+// record, four columns a thread.
+constexpr int kCombineThreads = 256;
+__global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const LatentDecodeArgs a, int tile_rows) {
+  __shared__ float weight[kMaxLatentRuns];
+  __shared__ float4 other[kCombineThreads / 2];
+  __shared__ float stats[2];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int c0 = blockIdx.x;
+  const int2 plan = a.plan[c0];
+  if (plan.y == 0) return;
+  const int row = blockIdx.y, rt = row / tile_rows, r = row - rt * tile_rows, records = plan.y - c0;
+  auto rec_of = [&](int k) {
+    return (2 * (static_cast<size_t>(c0 + k) * a.row_tiles + rt) + (k == 0 ? 1 : 0)) * tile_rows + r;
+  };
+  if (threadIdx.x < 32) {
+    float M = -FLT_MAX, sum = 0.f;
+    for (int k = threadIdx.x; k < records; k += 32) {
+      const float2 ml = a.ws_ml[rec_of(k)];
+      if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    }
+    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int k = threadIdx.x; k < records; k += 32) {
+      const float2 ml = a.ws_ml[rec_of(k)];
+      const float w = ml.y != 0.f ? ex2_approx(ml.x - M) : 0.f;   // a record that saw nothing counts 0
+      weight[k] = w;
+      sum = fmaf(ml.y, w, sum);
+    }
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (threadIdx.x == 0) stats[0] = M, stats[1] = sum;
+  }
+  __syncthreads();
+  const int half = threadIdx.x / (kCombineThreads / 2), i = threadIdx.x % (kCombineThreads / 2);
+  const bool mine = 4 * i < a.dc;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mine) {
+#pragma unroll 4
+    for (int k = half; k < records; k += 2) {
+      const float w = weight[k];
+      const float4 x = *reinterpret_cast<const float4 *>(a.ws_o + rec_of(k) * a.dc + 4 * i);
+      if (w != 0.f) acc.x = fmaf(x.x, w, acc.x), acc.y = fmaf(x.y, w, acc.y), acc.z = fmaf(x.z, w, acc.z), acc.w = fmaf(x.w, w, acc.w);
+    }
+  }
+  if (half == 1) other[i] = acc;
+  __syncthreads();
+  if (half == 1) return;
+  const size_t out = static_cast<size_t>(plan.x) * a.n * a.nh + row;
+  const float sum = stats[1], inv = sum != 0.f ? 1.f / sum : 0.f;
+  if (mine) {
+    const float4 z = other[i];
+    *reinterpret_cast<uint2 *>(a.o + out * a.dc + 4 * i) = make_uint2(pack_bf16x2((acc.x + z.x) * inv, (acc.y + z.y) * inv),
+                                                                    pack_bf16x2((acc.z + z.z) * inv, (acc.w + z.w) * inv));
+  }
+  if (i == 0) a.lse[out] = sum != 0.f ? (stats[0] + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int N>
+cudaError_t launch_latent_n(const CUtensorMap &mq, const CUtensorMap &mc, const LatentDecodeArgs &a, int groups,
+                            cudaStream_t stream) {
+  using L = LatLayout<N>;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t err = allow_smem(latent_decode_kernel<N>, L::kDynBytes, allowed);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(latent_decode_kernel<N>, static_cast<unsigned>(groups) * a.row_tiles, kLatThreads, L::kDynBytes, stream,
+                   mq, mc, a);
+  if (err != cudaSuccess || groups == 1) return err;
+  return launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(groups - 1), static_cast<unsigned>(a.n * a.nh)),
+                    kCombineThreads, 0, stream, a, N);
+}
+
+}  // namespace
+
+int latent_tile_rows(int n, int nh) {
+  const long long rows = static_cast<long long>(n) * nh;
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+}
+
+// Groups of CTAs (runs of the line), a CTA of each per row tile: as many as the GPU holds at once, and no more than
+// the tables allow tiles. With more row tiles than SMs one group, whose CTAs come in waves.
+int latent_groups(const LatentDecodeArgs &a, int sms) {
+  const long long most = static_cast<long long>(a.B) * ((static_cast<long long>(a.max_pages) * a.page_size + kTilePos - 1) / kTilePos);
+  long long groups = sms / a.row_tiles;
+  if (groups > kMaxLatentRuns) groups = kMaxLatentRuns;
+  if (groups > most) groups = most;
+  return groups < 1 ? 1 : static_cast<int>(groups);
+}
+
+size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int tile_rows) {
+  return static_cast<size_t>(groups) * a.row_tiles * 2 * tile_rows * (a.dc * sizeof(float) + sizeof(float2)) +
+         static_cast<size_t>(groups) * sizeof(int2);
+}
+
+cudaError_t launch_latent_decode(const CUtensorMap &mq, const CUtensorMap &mc, const LatentDecodeArgs &a, int groups,
+                                 int tile_rows, cudaStream_t stream) {
+  if (tile_rows == 16) return launch_latent_n<16>(mq, mc, a, groups, stream);
+  if (tile_rows == 32) return launch_latent_n<32>(mq, mc, a, groups, stream);
+  return launch_latent_n<64>(mq, mc, a, groups, stream);
+}
+
+}  // namespace xattn

@@ -284,6 +284,19 @@ xattn_status make_map_pages(CUtensorMap *map, const void *ptr, int num_pages, in
   return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
+// Map over [outer, rows, width] bf16: box = 64 columns of box_rows rows. What lies outside reads as zeros.
+xattn_status make_map_rows(CUtensorMap *map, const void *ptr, int outer, int rows, int width, int box_rows) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer), 1};
+  const cuuint64_t row = static_cast<cuuint64_t>(width) * 2;
+  const cuuint64_t strides[3] = {row, row * rows, row * rows * outer};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
+}
+
 // The fp32 window kernels' largest grid: four blocks per 32 rows of a head.
 bool window_f32_grid_ok(int B, int S, int nh) {
   return static_cast<double>(B) * nh * ((S + 31) / 32) * 4 < 0x1p31;
@@ -815,24 +828,41 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
   if (nh <= 0 || dc <= 0 || dr <= 0) return XATTN_ERR_BAD_SHAPE;
   if (dc > 512 || dc % 128 != 0 || dr > 64 || dr % 16 != 0) return XATTN_ERR_UNSUPPORTED_HD;
   XATTN_TRY(check_pages(B, n, 1, dc + dr, num_pages, page_size, max_pages));
-  if (n > XATTN_TREE_MAX || static_cast<double>(B) * n * nh > 0x1p28) return XATTN_ERR_BAD_SHAPE;
+  // Tiles of the line, rows of the outputs and query coordinates stay inside int32.
+  if (n > XATTN_TREE_MAX || static_cast<double>(B) * n * nh > 0x1p28 ||
+      static_cast<double>(B) * ((static_cast<double>(max_pages) * page_size + 63) / 64) > 0x1p30)
+    return XATTN_ERR_BAD_SHAPE;
   if (!std::isfinite(scale)) return XATTN_ERR_BAD_SCALE;
   XATTN_TRY(check_bf16_scale(scale));
   if (!aligned16(q) || !aligned16(pages) || !aligned16(o) || !aligned4(page_table, ctx_lens) || !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
+  DeviceInfo *dev = nullptr;
+  XATTN_TRY(bf16_device(&dev));
+  const int tile_rows = latent_tile_rows(n, nh);
   LatentDecodeArgs a = {};
-  a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.pages = static_cast<const __nv_bfloat16 *>(pages);
   a.page_table = page_table, a.ctx_lens = ctx_lens;
   a.o = static_cast<__nv_bfloat16 *>(o);
   a.lse = lse;
   a.B = B, a.n = n, a.nh = nh, a.dc = dc, a.dr = dr;
   a.num_pages = num_pages, a.page_size = page_size, a.max_pages = max_pages;
+  a.row_tiles = (n * nh + tile_rows - 1) / tile_rows;
   a.scale_log2 = scale * kLog2e;
-  DeviceInfo *dev = nullptr;
-  XATTN_TRY(bf16_device(&dev));
   a.status = dev->status, a.timeout_ns = wait_limit_ns();
-  return cuda_status(launch_latent_decode(a, static_cast<cudaStream_t>(stream)));
+  CUtensorMap mq, mc;
+  XATTN_TRY(make_map_rows(&mq, q, B, n * nh, dc + dr, tile_rows));
+  XATTN_TRY(make_map_rows(&mc, pages, num_pages, page_size, dc + dr, page_size < 64 ? page_size : 64));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int groups = latent_groups(a, dev->sms);
+  void *base = nullptr;
+  XATTN_TRY(scratch_alloc(*dev, latent_decode_workspace_bytes(a, groups, tile_rows), st, &base));
+  const size_t records = static_cast<size_t>(groups) * a.row_tiles * 2 * tile_rows;
+  a.ws_o = static_cast<float *>(base);
+  a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + records * dc);
+  a.plan = reinterpret_cast<int2 *>(a.ws_ml + records);
+  xattn_status r = cuda_status(launch_latent_decode(mq, mc, a, groups, tile_rows, st));
+  const cudaError_t fe = cudaFreeAsync(base, st);
+  if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
+  return r;
 }
 
 xattn_status xattn_cache_reserve(int *page_table, const int *ctx_lens, const int *new_lens, const int *free_pages,

@@ -230,18 +230,27 @@ void latent_bwd_workspace_carve(LatentArgs &a, void *base);
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
 
-// Absorbed form: n new tokens a sequence over a paged cache of rows of dc + dr numbers.
+// Absorbed form (attn_latent_decode.cu): n new tokens a sequence over a paged cache of rows of dc + dr numbers. mq: map
+// over the queries, boxes of 64 columns of tile_rows rows of one sequence; mc: over the pool, boxes of 64 columns of
+// min(page_size, 64) rows of one page. The scratch, latent_decode_workspace_bytes(), is ws_o, ws_ml and plan.
+constexpr int kMaxLatentRuns = 256;
 struct LatentDecodeArgs {
-  const __nv_bfloat16 *q, *pages;              // [B,n,nh,dc+dr], [num_pages,page_size,dc+dr]
   const int *page_table, *ctx_lens;
   __nv_bfloat16 *o;                            // [B,n,nh,dc]
-  float *lse;
+  float *lse, *ws_o;
+  float2 *ws_ml;
+  int2 *plan;                                  // [groups] what each run leaves to the combine
   int B, n, nh, dc, dr, num_pages, page_size, max_pages;
+  int row_tiles;                               // tiles of latent_tile_rows(n, nh) of a sequence's n nh query rows
   float scale_log2;
   int *status;
   unsigned long long timeout_ns;
 };
-cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream);
+int latent_tile_rows(int n, int nh);
+int latent_groups(const LatentDecodeArgs &a, int sms);
+size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int tile_rows);
+cudaError_t launch_latent_decode(const CUtensorMap &mq, const CUtensorMap &mc, const LatentDecodeArgs &a, int groups,
+                                 int tile_rows, cudaStream_t stream);
 
 // Page tables, slot maps and rows written by slot (cache_tables.cu).
 struct ReserveArgs {
