@@ -22,7 +22,8 @@
 //     records, and latent_combine_kernel merges them in order.
 //   * Roundings: scores, maxima, sums and O are fp32; P is rounded to bf16, C's type.
 //   * Pages as in attn_tree.cu: a box whose table entry is no page is loaded from outside the pool (zeros).
-// Warps: 0 TMA producer; 1 TMEM owner and MMA issuer; 2-9 softmax (warp & 3: lane quarter; two halves of the columns).
+// Warps: 0 TMA producer; 1 TMEM owner and issuer of S^T; 10 issuer of O^T (apart, so that a tile's P is not kept waiting
+// behind scores whose tile has not landed); 2-9 softmax (warp & 3: lane quarter; two halves of the columns).
 // TMEM: S^T buffers [0, N), [N, 2N); O^T block j [2N + j N, 2N + (j + 1) N).
 #include <cfloat>
 #include <type_traits>
@@ -34,7 +35,7 @@ namespace xattn {
 namespace {
 
 constexpr int kTilePos = 64;                       // positions of a tile
-constexpr int kLatThreads = 320;
+constexpr int kLatThreads = 352;
 constexpr int kSoftWarps = 8;
 
 // N: query rows (columns) of a row tile.
@@ -145,12 +146,35 @@ __device__ __forceinline__ LatRuns lat_start(const LatentDecodeArgs &a, int grou
   return runs;
 }
 
-// Order of floats as integers (for a maximum over lanes in one instruction).
-__device__ __forceinline__ int float_key(float x) {
-  const int k = __float_as_int(x);
-  return k ^ ((k >> 31) & 0x7fffffff);
+// Sixteen TMEM lanes (S^T with M = 64 has 16 of its rows in the first lanes of each quarter) by 8 K columns: thread t
+// gets rows t / 4 (x[4 i], x[4 i + 1]) and t / 4 + 8 (x[4 i + 2], x[4 i + 3]) of columns 8 i + 2 (t % 4), + 1.
+template <int K>
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t addr, uint32_t *r) {
+  if constexpr (K == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+  } else if constexpr (K == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  }
 }
-__device__ __forceinline__ float key_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// Eight-by-eight matrices of 16-bit numbers in that layout into rows of 16 bytes: lane l gives row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_x2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 
 template <int C>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t *r) {
@@ -298,58 +322,62 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     for (int r = max(issued_c - kPairs, 0); r < issued_c; ++r) mbar_drain(c_full(r % kPairs), (r / kPairs) & 1, ctl);
     for (int r = max(issued_r - kRopes, 0); r < issued_r; ++r) mbar_drain(r_full(r % kRopes), (r / kRopes) & 1, ctl);
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
+    // ---------------- issuer of S^T = C Q^T ----------------
     constexpr uint32_t idesc_s = idesc_bf16_f32(64, N, false, false);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, true, true);
     const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
     const uint64_t dC = smem_desc(sC, 16, 1024, kSwizzle128), dR = smem_desc(sR, 16, 1024, kSwizzle128);
-    const uint64_t dCt = smem_desc(sC, L::kSub, 1024, kSwizzle128);      // MN-major: 64 columns a sub-tile
-    const uint64_t dP = smem_desc(sP, 16, 8 * L::kPRow, L::kSwizzleP);   // MN-major
     const int rope_steps = a.dr / 16;
-    // S^T of ring tile R (pairs from Rj on): after its last reader has read the buffer.
-    auto scores = [&](int R, int Rj, bool last) -> bool {
-      if (!lat_wait(s_free(R & 1), ((R >> 1) & 1) ^ 1, ctl)) return false;
-      const uint32_t d = tS + (R & 1) * N;
-#pragma unroll 1
-      for (int j = 0; j < blocks; ++j) {
-        const int s = (Rj + j) % kPairs;
-        if (!lat_wait(c_full(s), ((Rj + j) / kPairs) & 1, ctl)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss(d, dC + s * (L::kPair >> 4) + (kk / 4) * (L::kSub >> 4) + (kk % 4) * 2,
-                   dQ + (2 * j + kk / 4) * (L::kQSub >> 4) + (kk % 4) * 2, idesc_s, (j > 0 || kk > 0) ? 1u : 0u);
-        }
-        __syncwarp();
-      }
-      const int s = R % kRopes;
-      if (!lat_wait(r_full(s), (R / kRopes) & 1, ctl)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        for (int kk = 0; kk < rope_steps; ++kk)
-          mma_ss(d, dR + s * (L::kSub >> 4) + kk * 2, dQ + 2 * blocks * (L::kQSub >> 4) + kk * 2, idesc_s, 1u);
-        mma_commit(s_full(R & 1));
-        if (last) mma_commit(q_empty);
-      }
-      __syncwarp();
-      return true;
-    };
-    int R = 0, Rj = 0, piece = 0, scored = 0;
+    int R = 0, Rj = 0, piece = 0;
     bool ok = true;
     while (ok && lat_piece(walk, a)) {
-      ok = lat_wait(q_full, piece & 1, ctl) && scores(R, Rj, walk.e0 + 1 == walk.e1);
-      if (!ok) break;
-      scored = R + 1;
+      if (!lat_wait(q_full, piece & 1, ctl)) break;
 #pragma unroll 1
-      for (int e = walk.e0; e < walk.e1; ++e, ++R, Rj += blocks) {
-        if (e + 1 < walk.e1) {
-          if (!scores(R + 1, Rj + blocks, e + 2 == walk.e1)) { ok = false; break; }
-          scored = R + 2;
+      for (int e = walk.e0; e < walk.e1; ++e) {
+        if (!lat_wait(s_free(R & 1), ((R >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
+        const uint32_t d = tS + (R & 1) * N;
+#pragma unroll 1
+        for (int j = 0; j < blocks; ++j, ++Rj) {
+          const int s = Rj % kPairs;
+          if (!lat_wait(c_full(s), (Rj / kPairs) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ss(d, dC + s * (L::kPair >> 4) + (kk / 4) * (L::kSub >> 4) + (kk % 4) * 2,
+                     dQ + (2 * j + kk / 4) * (L::kQSub >> 4) + (kk % 4) * 2, idesc_s, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
         }
+        const int s = R % kRopes;
+        if (!ok || !lat_wait(r_full(s), (R / kRopes) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          for (int kk = 0; kk < rope_steps; ++kk)
+            mma_ss(d, dR + s * (L::kSub >> 4) + kk * 2, dQ + 2 * blocks * (L::kQSub >> 4) + kk * 2, idesc_s, 1u);
+          mma_commit(s_full(R & 1));
+          if (e + 1 == walk.e1) mma_commit(q_empty);
+        }
+        __syncwarp();
+        ++R;
+      }
+      ++piece;
+    }
+    __syncwarp();
+    if (R > 0) mbar_drain(s_full((R - 1) & 1), ((R - 1) >> 1) & 1, ctl);   // the products are done before TMEM goes
+  } else if (warp == 10) {
+    // ---------------- issuer of O^T += C^T P^T ----------------
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, true, true);
+    const uint64_t dCt = smem_desc(sC, L::kSub, 1024, kSwizzle128);      // MN-major: 64 columns a sub-tile
+    const uint64_t dP = smem_desc(sP, 16, 8 * L::kPRow, L::kSwizzleP);   // MN-major
+    int R = 0, Rj = 0;
+    bool ok = true;
+    while (ok && lat_piece(walk, a)) {
+#pragma unroll 1
+      for (int e = walk.e0; e < walk.e1; ++e, ++R) {
         if (!lat_wait(p_full, R & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
+#pragma unroll 1
           for (int j = 0; j < blocks; ++j) {
             const int s = (Rj + j) % kPairs;
 #pragma unroll
@@ -361,23 +389,27 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           mma_commit(o_done);
         }
         __syncwarp();
+        Rj += blocks;
       }
-      ++piece;
     }
     __syncwarp();
-    // The last products are done before TMEM goes.
-    if (scored > 0) mbar_drain(s_full((scored - 1) & 1), ((scored - 1) >> 1) & 1, ctl);
     if (R > 0) mbar_drain(o_done, (R - 1) & 1, ctl);
   } else {
-    // ---------------- softmax: thread = one position, half of the columns ----------------
-    constexpr int C = N / 2;
+    // ---------------- softmax: thread = two positions, a quarter of its warp's columns ----------------
+    constexpr int C = N / 2, K = C / 8;
     const int quarter = warp & 3, half = (warp - 2) >> 2, tid = static_cast<int>(threadIdx.x) - 64;
-    const int pos = quarter * 16 + (lane & 15);                    // M = 64: 16 rows in each quarter's lanes 0-15
-    const bool live = lane < 16;
+    const int pos = quarter * 16 + (lane >> 2);                    // and pos + 8 (M = 64: a quarter's first 16 lanes)
+    const int col = half * C + 2 * (lane & 3);                     // and + 1, + 8, + 9, ..
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int box_rows = min(a.page_size, kTilePos);
     const unsigned all_boxes = (1u << (kTilePos / box_rows)) - 1u;
     const int rows_all = a.n * a.nh, row0 = rt * N, rows = min(rows_all - row0, N);
+    // Where this lane's row of the P matrices goes: rows pos, chunks of 8 columns, swizzled.
+    auto p_chunk = [&](int k) -> uint32_t {
+      const int at = quarter * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), chunk = half * K + k;
+      const int sw = N == 64 ? (chunk ^ (at & 7)) : (N == 32 ? (chunk ^ ((at >> 1) & 3)) : (chunk ^ ((at >> 2) & 1)));
+      return sP + at * L::kPRow + (sw << 4);
+    };
     int R = 0, meets = 0;
     bool ok = true;
     auto meet_all = [&]() -> bool {
@@ -391,59 +423,58 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       // A run that ends inside the sequence it started last says so to the combine.
       if (warp == 2 && lane == 0 && rt == 0 && e0 == 0 && e1 < walk.count)
         a.plan[group] = make_int2(b, runs.of(walk.first + walk.count - 1) + 1);
-      float l[C];
+      float l[2 * K];
 #pragma unroll
-      for (int c = 0; c < C; ++c) l[c] = 0.f;
+      for (int k = 0; k < 2 * K; ++k) l[k] = 0.f;
 #pragma unroll 1
       for (int e = e0; e < e1; ++e, ++R) {
         const bool first = e == e0;
         if (!lat_wait(s_full(R & 1), (R >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         const unsigned held = held_boxes[R % kRopes];
-        float x[C];
+        float x[4 * K];
         uint32_t *xr = reinterpret_cast<uint32_t *>(x);
-        tmem_ld_cols<C>(tS + (R & 1) * N + half * C + lane_off, xr);
+        tmem_ld_16x256b<K>(tS + (R & 1) * N + half * C + lane_off, xr);
         tmem_wait_ld();
-        reg_fence<C>(xr);
+        reg_fence<4 * K>(xr);
         tc_fence_before();
         lat_arrive(s_free(R & 1), lane);
-        // (Scores carry held_boxes' slot: the copy that overwrites it waits for r_empty, below.)
 #pragma unroll
-        for (int c = 0; c < C; ++c) x[c] *= a.scale_log2;
-        const int p = e * kTilePos + pos;
+        for (int k = 0; k < 2 * K; ++k) fmul2(x[2 * k], x[2 * k + 1], x[2 * k], x[2 * k + 1], a.scale_log2, a.scale_log2);
         if (e * kTilePos + kTilePos > ctx + 1 || held != all_boxes) {
           // Positions that some row does not see: new ones, those behind the last, missing pages.
-          const bool there = (held >> (pos / box_rows)) & 1u;
-          int token = (row0 + half * C) / a.nh, left = (token + 1) * a.nh - (row0 + half * C);
+          const int p = e * kTilePos + pos;
+          const bool there0 = (held >> (pos / box_rows)) & 1u, there1 = (held >> ((pos + 8) / box_rows)) & 1u;
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            if (!there || p >= end || p > ctx + token) x[c] = -INFINITY;
-            if (--left == 0) ++token, left = a.nh;
-          }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int last = min(ctx + (row0 + col + 8 * k + h) / a.nh, end - 1);
+              if (!there0 || p > last) x[4 * k + h] = -INFINITY;
+              if (!there1 || p + 8 > last) x[4 * k + 2 + h] = -INFINITY;
+            }
           // Rows behind the last position may hold anything and are zeroed before P meets them (0 x NaN would not
           // be 0).
-          if (live && p >= end) {
-            const int Rj = R * blocks;
-            for (int j = half; j < 2 * blocks; j += 2) {
-              uint8_t *row = smem + L::kC + ((Rj + j / 2) % kPairs) * L::kPair + (j & 1) * L::kSub + pos * 128;
+          const int r = tid >> 2;
+          if (e * kTilePos + r >= end) {
+            for (int j = tid & 3; j < 2 * blocks; j += 4) {
+              uint8_t *row = smem + L::kC + ((R * blocks + j / 2) % kPairs) * L::kPair + (j & 1) * L::kSub + r * 128;
 #pragma unroll
               for (int v = 0; v < 8; ++v) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
             }
           }
-        }
-        if (!live) {
-#pragma unroll
-          for (int c = 0; c < C; ++c) x[c] = -INFINITY;
         }
         // Does some score pass its column's base by more than 2^8? A piece's first tile always asks.
         bool grow = first;
         if (!first) {
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < C; c += 4) {
-            const float4 m = *reinterpret_cast<const float4 *>(base + half * C + c);
-            top = fmax3(top, x[c] - m.x, x[c + 1] - m.y);
-            top = fmax3(top, x[c + 2] - m.z, x[c + 3] - m.w);
+          for (int k = 0; k < K; ++k) {
+            const float2 m = *reinterpret_cast<const float2 *>(base + col + 8 * k);
+            float d0, d1, d2, d3;
+            fadd2(d0, d1, x[4 * k], x[4 * k + 1], m.x, m.y);
+            fadd2(d2, d3, x[4 * k + 2], x[4 * k + 3], m.x, m.y);
+            top = fmax3(fmax3(top, d0, d1), d2, d3);
           }
           grow = top > 8.f;
         }
@@ -456,29 +487,46 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         if (any) {
           // The columns' maxima: over a warp's positions, then over the four quarters.
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const int k = __reduce_max_sync(0xffffffffu, float_key(x[c]));
-            if (lane == (c & 31)) parts[quarter * N + half * C + c] = key_float(k);
-          }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float m = fmaxf(x[4 * k + h], x[4 * k + 2 + h]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+              if (lane < 4) parts[quarter * N + col + 8 * k + h] = m;
+            }
           if (!meet_all()) { ok = false; break; }
           if (tid < N) {
             // (-FLT_MAX stands for nothing seen: any score is far above it, and differences stay numbers.)
-            const float old = first ? -FLT_MAX : base[tid];
-            float m = old;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m = parts[q * N + tid] > m || parts[q * N + tid] != parts[q * N + tid] ? parts[q * N + tid] : m;
+            const float old = first ? -FLT_MAX : -base[tid];
+            const float m = fmaxf(fmax3(old, parts[tid], parts[N + tid]), fmaxf(parts[2 * N + tid], parts[3 * N + tid]));
             factor[tid] = ex2_approx(old - m);
-            base[tid] = m;
+            base[tid] = -m;
           }
           if (!meet_all()) { ok = false; break; }
+        }
+        uint32_t pk[2 * K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float2 m = *reinterpret_cast<const float2 *>(base + col + 8 * k);
+          if (any) {
+            const float2 f = *reinterpret_cast<const float2 *>(factor + col + 8 * k);
+            if (!first) l[2 * k] *= f.x, l[2 * k + 1] *= f.y;
+          }
+          float d0, d1, d2, d3;
+          fadd2(d0, d1, x[4 * k], x[4 * k + 1], m.x, m.y);
+          fadd2(d2, d3, x[4 * k + 2], x[4 * k + 3], m.x, m.y);
+          d0 = ex2_approx(d0), d1 = ex2_approx(d1), d2 = ex2_approx(d2), d3 = ex2_approx(d3);
+          fadd2(l[2 * k], l[2 * k + 1], l[2 * k], l[2 * k + 1], d0, d1);
+          fadd2(l[2 * k], l[2 * k + 1], l[2 * k], l[2 * k + 1], d2, d3);
+          pk[2 * k] = pack_bf16x2(d0, d1);
+          pk[2 * k + 1] = pack_bf16x2(d2, d3);
         }
         // P over the last tile's, which its product has read then; O^T is at rest too.
         if (!lat_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         if (any && !first) {
           const float *f = factor + half * C;
-#pragma unroll
-          for (int c = 0; c < C; ++c) l[c] *= f[c];
 #pragma unroll 1
           for (int j = 0; j < blocks; ++j) {
             uint32_t ov[C];
@@ -492,24 +540,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           }
           tmem_wait_st();
         }
-        uint32_t pk[C / 2];
+        if constexpr (K == 1) {
+          stmatrix_x2(p_chunk(0), pk[0], pk[1]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const float4 m = *reinterpret_cast<const float4 *>(base + half * C + c);
-          const float p0 = ex2_approx(x[c] - m.x), p1 = ex2_approx(x[c + 1] - m.y);
-          const float p2 = ex2_approx(x[c + 2] - m.z), p3 = ex2_approx(x[c + 3] - m.w);
-          l[c] += p0, l[c + 1] += p1, l[c + 2] += p2, l[c + 3] += p3;
-          pk[c / 2] = pack_bf16x2(p0, p1);
-          pk[c / 2 + 1] = pack_bf16x2(p2, p3);
-        }
-        if (live) {
-#pragma unroll
-          for (int v = 0; v < C / 8; ++v) {
-            const int chunk = half * (C / 8) + v;
-            const int sw = N == 64 ? (chunk ^ (pos & 7)) : (N == 32 ? (chunk ^ ((pos >> 1) & 3)) : (chunk ^ ((pos >> 2) & 1)));
-            *reinterpret_cast<uint4 *>(smem + L::kP + pos * L::kPRow + (sw << 4)) =
-                make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-          }
+          for (int k = 0; k < K; k += 2) stmatrix_x4(p_chunk(k + (lane >> 4)), pk[2 * k], pk[2 * k + 1], pk[2 * k + 2], pk[2 * k + 3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -519,17 +554,17 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       if (!ok) break;
       // The piece's sums meet in `parts`; its O^T and LSE, or its record (O not divided by the sum).
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float s = live ? l[c] : 0.f;
+      for (int k = 0; k < 2 * K; ++k) {
+        float s = l[k];
 #pragma unroll
-        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == (c & 31)) parts[quarter * N + half * C + c] = s;
+        for (int off = 4; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (lane < 4) parts[quarter * N + col + 8 * (k / 2) + (k & 1)] = s;
       }
       if (!meet_all()) { ok = false; break; }
       const size_t rec = (2 * static_cast<size_t>(blockIdx.x) + (e0 == 0 ? 1 : 0)) * N;
       const size_t out = static_cast<size_t>(b) * rows_all + row0;
       if (tid < N) {
-        const float sum = (parts[tid] + parts[N + tid]) + (parts[2 * N + tid] + parts[3 * N + tid]), m = base[tid];
+        const float sum = (parts[tid] + parts[N + tid]) + (parts[2 * N + tid] + parts[3 * N + tid]), m = -base[tid];
         factor[tid] = !whole ? 1.f : (sum != 0.f ? 1.f / sum : 0.f);
         if (tid < rows) {
           if (whole)
@@ -540,23 +575,28 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       }
       if (!meet_all() || !lat_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
       tc_fence_after();
+      // Eight rows of a block at a time, a lane a number of the latent.
+      const int d = quarter * 32 + lane;
 #pragma unroll 1
-      for (int j = 0; j < blocks; ++j) {
-        uint32_t ov[C];
-        tmem_ld_cols<C>(tO + j * N + half * C + lane_off, ov);
+      for (int x = 0; x < blocks * K; ++x) {
+        const int j = x / K, r0 = half * C + (x - j * K) * 8;
+        if (r0 >= rows) continue;
+        uint32_t ov[8];
+        tmem_ld_x8(tO + j * N + r0 + lane_off, ov);
         tmem_wait_ld();
-        reg_fence<C>(ov);
-        const int d = j * 128 + quarter * 32 + lane;
+        reg_fence<8>(ov);
+        if (whole) {
+          __nv_bfloat16 *to = a.o + (out + r0) * a.dc + j * 128 + d;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int r = half * C + c;
-          if (r < rows) {
-            const float f = factor[r], v = __uint_as_float(ov[c]);
-            if (whole)
-              a.o[(out + r) * a.dc + d] = __float2bfloat16_rn(f != 0.f ? v * f : 0.f);
-            else
-              a.ws_o[(rec + r) * a.dc + d] = v;
+          for (int c = 0; c < 8; ++c, to += a.dc) {
+            const float f = factor[r0 + c];
+            if (r0 + c < rows) *to = __float2bfloat16_rn(f != 0.f ? __uint_as_float(ov[c]) * f : 0.f);
           }
+        } else {
+          float *to = a.ws_o + (rec + r0) * a.dc + j * 128 + d;
+#pragma unroll
+          for (int c = 0; c < 8; ++c, to += a.dc)
+            if (r0 + c < rows) *to = __uint_as_float(ov[c]);
         }
         __syncwarp();                                            // (the reads of TMEM are the warp's)
       }
