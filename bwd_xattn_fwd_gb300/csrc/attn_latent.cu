@@ -1,4 +1,4 @@
-// Latent attention, plainly: one block a query row (forward, dQ, decode) or a key row (dK, dV), products on
+// Latent attention, plainly: one block a query row (dQ) or a key row (dK, dV), products on
 // the CUDA cores in fp32.
 #include "sm103_ptx.cuh"
 #include "xattn_internal.h"
@@ -34,32 +34,6 @@ __device__ __forceinline__ float value_dot(const LatentArgs &a, const float *x, 
   float s = 0.f;
   for (int d = 0; d < a.dv; ++d) s = fmaf(x[d], __bfloat162float(v[d]), s);
   return s;
-}
-
-__global__ void __launch_bounds__(kPlain) latent_fwd_plain(const LatentArgs a) {
-  __shared__ float qs[192], ps[kPlain], part[kPlain / 32];
-  const int h = blockIdx.x % a.nh, i = static_cast<int>(blockIdx.x / a.nh % a.S);
-  const size_t b = blockIdx.x / a.nh / a.S, tok = b * a.S + i;
-  const int dq = a.dn + a.dr, tid = threadIdx.x;
-  for (int d = tid; d < dq; d += kPlain) qs[d] = __bfloat162float(a.q[(tok * a.nh + h) * dq + d]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j0 = 0; j0 <= i; j0 += kPlain) {
-    const int j = j0 + tid;
-    const float s = j <= i ? key_dot(a, qs, b * a.S + j, h) * a.scale * kLog2e : -INFINITY;
-    const float mn = fmaxf(m, block_reduce(s, true, part)), alpha = exp2f(m - mn);
-    const float p = j <= i ? exp2f(s - mn) : 0.f;
-    ps[tid] = p;
-    l = l * alpha + block_reduce(p, false, part);
-    m = mn;
-    o *= alpha;
-    if (tid < a.dv)
-      for (int x = 0; x < kPlain && j0 + x <= i; ++x)
-        o = fmaf(ps[x], __bfloat162float(a.kv[((b * a.S + j0 + x) * a.nh + h) * (a.dn + a.dv) + a.dn + tid]), o);
-    __syncthreads();
-  }
-  if (tid < a.dv) a.o[(tok * a.nh + h) * a.dv + tid] = __float2bfloat16(o / l);
-  if (tid == 0) a.lse[tok * a.nh + h] = (m + log2f(l)) * kLn2;
 }
 
 __global__ void __launch_bounds__(kPlain) latent_dq_plain(const LatentArgs a) {
@@ -146,10 +120,6 @@ void latent_bwd_workspace_carve(LatentArgs &a, void *base) {
   a.rope_parts = a.D + static_cast<size_t>(a.B) * a.S * a.nh;
 }
 
-cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream) {
-  latent_fwd_plain<<<static_cast<unsigned>(a.B) * a.S * a.nh, kPlain, 0, stream>>>(a);
-  return cudaGetLastError();
-}
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream) {
   latent_dq_plain<<<static_cast<unsigned>(a.B) * a.S * a.nh, kPlain, 0, stream>>>(a);
   latent_dkv_plain<<<static_cast<unsigned>(a.B) * a.S * a.nh, kPlain, 0, stream>>>(a);

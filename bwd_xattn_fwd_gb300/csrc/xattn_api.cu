@@ -284,6 +284,21 @@ xattn_status make_map_pages(CUtensorMap *map, const void *ptr, int num_pages, in
   return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
+// Map over [B, S, H, width] bf16 for tiles of 64-column sub-tiles: box = 64 columns of `rows` rows of one head; what lies
+// outside (columns behind the last too) reads as zeros.
+xattn_status make_map_subtiles(CUtensorMap *map, const void *ptr, int B, int S, int H, int width, int rows) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(S),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t row = static_cast<cuuint64_t>(width) * 2;
+  const cuuint64_t strides[3] = {row, row * H, row * H * S};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
+}
+
 // Map over [outer, rows, width] bf16: box = 64 columns of box_rows rows. What lies outside reads as zeros.
 xattn_status make_map_rows(CUtensorMap *map, const void *ptr, int outer, int rows, int width, int box_rows) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer), 1};
@@ -305,6 +320,12 @@ bool window_f32_grid_ok(int B, int S, int nh) {
 xattn_status bf16_device(DeviceInfo **dev) {
   XATTN_TRY(device_info(dev));
   if (!(*dev)->sm103) return XATTN_ERR_NO_DEVICE_SUPPORT;
+  // Encoding a map needs the thread's context, which a thread whose first CUDA call this is does not have yet.
+  static thread_local const DeviceInfo *bound = nullptr;
+  if (bound != *dev) {
+    if (cudaSetDevice(static_cast<int>(*dev - g_dev)) != cudaSuccess) return XATTN_ERR_CUDA;
+    bound = *dev;
+  }
   return get_encode();
 }
 
@@ -786,7 +807,11 @@ xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope,
   a.lse = lse;
   a.B = B, a.S = S, a.nh = nh, a.dn = dn, a.dr = dr, a.dv = dv, a.scale = scale;
   a.status = dev->status, a.timeout_ns = wait_limit_ns();
-  return cuda_status(launch_latent_fwd(a, static_cast<cudaStream_t>(stream)));
+  CUtensorMap mq, mkv, mrope;
+  XATTN_TRY(make_map_subtiles(&mq, q, B, S, nh, dn + dr, kTileRows));
+  XATTN_TRY(make_map_subtiles(&mkv, kv, B, S, nh, dn + dv, kTileRows));
+  XATTN_TRY(make_map_subtiles(&mrope, k_rope, B, S, 1, dr, kTileRows));
+  return cuda_status(launch_latent_fwd(mq, mkv, mrope, a, dev->sms, static_cast<cudaStream_t>(stream)));
 }
 
 xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope, const void *o, const void *dO,

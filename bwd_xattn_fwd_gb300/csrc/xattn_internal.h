@@ -212,7 +212,7 @@ struct PageArgs {
 cudaError_t launch_cache_append(const PageArgs &a, const void *k_new, const void *v_new, cudaStream_t stream);
 cudaError_t launch_cache_compact(const PageArgs &a, const int *path, const int *accepted, cudaStream_t stream);
 
-// Latent attention, expanded form (attn_latent.cu): head h's key of token j is (kv[j, h, :dn],
+// Latent attention, expanded form (attn_latent_fwd.cu, attn_latent.cu); maps: boxes of 64 columns of 128 rows of a head. Head h's key of token j is (kv[j, h, :dn],
 // k_rope[j]), its value kv[j, h, dn:].
 struct LatentArgs {
   const __nv_bfloat16 *q, *kv, *k_rope, *dO;   // [B,S,nh,dn+dr], [B,S,nh,dn+dv], [B,S,dr], [B,S,nh,dv]
@@ -227,7 +227,8 @@ struct LatentArgs {
 };
 size_t latent_bwd_workspace_bytes(const LatentArgs &a);
 void latent_bwd_workspace_carve(LatentArgs &a, void *base);
-cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
+cudaError_t launch_latent_fwd(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrope, const LatentArgs &a,
+                              int sms, cudaStream_t stream);
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
 
 // Absorbed form (attn_latent_decode.cu): n new tokens a sequence over a paged cache of rows of dc + dr numbers. mq: map

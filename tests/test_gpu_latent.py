@@ -415,6 +415,25 @@ def test_two_graphs_and_two_threads():
     assert xattn.xattn_check_device_status() == 0
 
 
+def test_a_thread_whose_first_cuda_call_is_the_library_s():
+    """A host thread may call without having used CUDA before."""
+    from bwd_xattn_fwd_gb300 import xattn
+    x = latent_inputs(1, 100, 2, 64, 32, 64, seed=1)
+    q, kv, rope = x["q"], x["kv"], x["k_rope"]
+    k = torch.randn(1, 100, 2, 64, device="cuda").bfloat16()
+    calls = [lambda: xattn.attention_latent_fwd(q, kv, rope, 0.1), lambda: xattn.attention_fwd(k, k, k),
+             lambda: xattn.attention_window_fwd(k, k, k, 9)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(calls, want):
+        got = []
+        t = threading.Thread(target=lambda: got.append(c()))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert got and torch.equal(got[0][0], o) and torch.equal(got[0][1], lse)
+
+
 FIRST_IN_CAPTURE = """
 import torch
 from bwd_xattn_fwd_gb300 import xattn
