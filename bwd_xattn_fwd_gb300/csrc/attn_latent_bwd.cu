@@ -1,0 +1,782 @@
+// Latent attention in its expanded form, backward, on sm_103a tensor cores: the scores are recomputed, D = rowsum(dO * O)
+// stands for the softmax Jacobian, and the gradient of the shared part k_rope is the sum over the heads.
+//   P = exp(scale S - LSE), dS = P (dO V^T - D);
+//   dV = P^T dO, dK = scale dS^T Q (its first dn numbers to dkv, the others summed over the heads to dk_rope), dQ = scale dS K.
+//
+// Four kernels:
+//   1. latent_bwd_rows_kernel: per query row -LSE log2 e and -D, transposed to [B, nh, S_pad] so that a tile's 64 (128) of a
+//      head are one contiguous copy.
+//   2. latent_dkv_kernel (key-stationary): a unit is (batch, head, 128 keys); dV [128, dv] and dK [128, dn + dr] stay in TMEM,
+//      320 of its 512 columns, so queries come in tiles of 64 and three 64-column places hold the scores: S^T(t) in place
+//      t % 2 (P^T over it), dP^T(t) in the third (dS^T over it). S^T is issued two tiles ahead, so it runs while the warps
+//      work on P and dS. A score product of 64 columns takes 48 cycles a K step where its arithmetic is 32 (shared memory
+//      feeds 128 + 64 rows); with 128 columns the places would not fit. Per 64 queries 576 (S) + 384 (dP) + 256 (dV) + 384 (dK).
+//   3. latent_dq_kernel (query-stationary, as attn_bwd_dq_sm103.cu): S and dP once more, dQ += dS K in TMEM over the key
+//      tiles. dQ [., dn + dr] does not fit beside dV and dK, and summed with atomics it would not be reproducible.
+//   4. latent_rope_kernel: k_rope's gradient from the heads' fp32 parts, in order.
+// Every output is bit-for-bit reproducible. Roundings: P and dS to bf16, Q's, K's and dO's type, before their products; dS is
+// made of the rounded P (in the third kernel of the unrounded one). Bound by the tensor cores.
+#include "sm103_ptx.cuh"
+#include "xattn_internal.h"
+
+namespace xattn {
+namespace {
+
+constexpr int kBwdThreads = 384;                       // 12 warps
+constexpr int kQRows = 64;                             // queries of a tile (dkv)
+constexpr uint32_t kKeySub = kTileRows * 128;          // 64 columns of 128 rows
+constexpr uint32_t kQuerySub = kQRows * 128;           // 64 columns of 64 rows
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+  const bool ok = mbar_wait(bar, parity, ctl);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// One warp a row (b, i, h) of o and dO. Rows S .. S_pad - 1: a weight of 0 (their Q and dO are read as zeros).
+__global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, S_pad = padded_rows(a.S);
+  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<size_t>(a.B) * S_pad * a.nh) return;
+  const int h = static_cast<int>(row % a.nh);
+  const size_t rest = row / a.nh;
+  const int i = static_cast<int>(rest % S_pad);
+  const size_t b = rest / S_pad, to = (b * a.nh + h) * S_pad + i;
+  if (i >= a.S) {
+    if (lane == 0) a.nlse[to] = -INFINITY, a.nD[to] = 0.f;
+    return;
+  }
+  const size_t from = (b * a.S + i) * a.nh + h;
+  float dot = 0.f;
+  if (4 * lane < a.dv) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(a.o + from * a.dv + 4 * lane);
+    const uint2 y = *reinterpret_cast<const uint2 *>(a.dO + from * a.dv + 4 * lane);
+    dot = bf16lo_to_f32(x.x) * bf16lo_to_f32(y.x) + bf16hi_to_f32(x.x) * bf16hi_to_f32(y.x);
+    dot = fmaf(bf16lo_to_f32(x.y), bf16lo_to_f32(y.y), dot);
+    dot = fmaf(bf16hi_to_f32(x.y), bf16hi_to_f32(y.y), dot);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+  if (lane == 0) a.nlse[to] = -a.lse[from] * kLog2e, a.nD[to] = -dot;
+}
+
+// NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS).
+template <int NS>
+struct DkvLayout {
+  static constexpr int kStages = 3;
+  static constexpr uint32_t kK = 0;                                  // NS sub-tiles and the shared part
+  static constexpr uint32_t kV = kK + (NS + 1) * kKeySub;
+  static constexpr uint32_t kQ = kV + NS * kKeySub;                  // stages of Q (NS + 1 sub-tiles)
+  static constexpr uint32_t kdO = kQ + kStages * (NS + 1) * kQuerySub;
+  static constexpr uint32_t kRows = kdO + kStages * NS * kQuerySub;  // stages of -LSE log2 e and -D
+  static constexpr uint32_t kBars = kRows + kStages * 2 * kQRows * 4;
+  static constexpr int kNumBars = 2 * kStages + 13;
+  static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
+  static constexpr uint32_t kUsed = kMisc + 32;
+  static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
+  static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
+};
+
+// Warps: 0 TMA; 1 issuer of S^T and dV (and TMEM owner); 3 issuer of dP^T and dK; 4-7 P^T; 8-11 dS^T; a thread is a key row.
+// TMEM: dV [0, 128) | dK [128, 320), its shared part from 256 on | S^T places [320, 384), [384, 448) | dP^T [448, 512).
+template <int NS>
+__global__ void __maxnreg__(168)
+    latent_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
+                      const __grid_constant__ CUtensorMap mrope, const __grid_constant__ CUtensorMap mdo, const LatentArgs a) {
+  using L = DkvLayout<NS>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t latent_dkv_smem[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dkv_smem) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int S = a.S, nh = a.nh, dn = a.dn, dr = a.dr, dv = a.dv;
+  const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
+  const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
+  const int num_n = (S + kTileRows - 1) / kTileRows, num_q = (S + kQRows - 1) / kQRows, BH = a.B * nh;
+  const int S_pad = padded_rows(S);
+  // Units, most query tiles first; CTA c of G takes unit k G + c in even rounds and k G + G - 1 - c in odd ones.
+  const int num_units = num_n * BH, G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  auto unit_at = [G, cta](int k) { return k * G + ((k & 1) ? G - 1 - cta : cta); };
+#define XATTN_DKV_UNIT(u)                                          \
+  const int n = (u) / BH, bh = (u) - n * BH;                       \
+  const int b = bh / nh, h = bh - b * nh;                          \
+  const int m0 = 2 * n, T = num_q - m0; /* query tiles */          \
+  (void)b;                                                         \
+  (void)h
+
+  const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV), sQ = smem_u32(smem + L::kQ),
+                 sdO = smem_u32(smem + L::kdO), sRows = smem_u32(smem + L::kRows), bar0 = smem_u32(smem + L::kBars);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  auto q_full = [&](int s) { return bar(s); };                       // Q, dO and the rows' numbers of a tile
+  auto q_empty = [&](int s) { return bar(kStages + s); };
+  constexpr int kB = 2 * kStages;
+  const uint32_t kv_full = bar(kB), acc_done = bar(kB + 1), acc_free = bar(kB + 2), dp_full = bar(kB + 3),
+                 ds_full = bar(kB + 4);
+  auto s_full = [&](int x) { return bar(kB + 5 + x); };
+  auto p_full = [&](int x) { return bar(kB + 7 + x); };
+  auto p_free = [&](int x) { return bar(kB + 9 + x); };               // the dS warps have read P^T
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
+  const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 2);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(acc_done, 2);
+    mbar_init(acc_free, 256);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 128);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full(x), 1);
+      mbar_init(p_full(x), 128);
+      mbar_init(p_free(x), 128);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mkv);
+    tma_prefetch_desc(&mrope);
+    tma_prefetch_desc(&mdo);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch();
+  grid_dep_wait();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+  const uint32_t tdV = tmem, tdK = tmem + 128, tdKr = tmem + 256, tdP = tmem + 448;
+  auto tS = [&](int x) { return tmem + 320u + 64u * x; };
+
+  if (warp == 0) {
+    // ---------------- TMA producer (converged warp, one elected lane issues) ----------------
+    auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int col, int head, int row0, int bb) {
+      XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && bb >= 0 && bb < a.B && dst >= sK &&
+                       dst < sRows,
+                   a.status);
+      tma_load_4d_elect(dst, map, full, col, head, row0, bb);
+    };
+    int g = 0, units = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DKV_UNIT(u);
+      const size_t rows = static_cast<size_t>(bh) * S_pad;
+      auto load_tile = [&](int t) -> bool {
+        const int s = g % kStages, q0 = (m0 + t) * kQRows;
+        if (!warp_wait(q_empty(s), ((g / kStages) & 1) ^ 1, ctl)) return false;
+        mbar_expect_tx_elect(q_full(s), (k_subs + 1 + v_subs) * kQuerySub + 2 * kQRows * 4);
+        const uint32_t dq = sQ + s * (NS + 1) * kQuerySub, ddo = sdO + s * NS * kQuerySub, dr0 = sRows + s * 2 * kQRows * 4;
+        for (int c = 0; c < k_subs; ++c) load(dq + c * kQuerySub, &mq, q_full(s), 64 * c, h, q0, b);
+        load(dq + NS * kQuerySub, &mq, q_full(s), dn, h, q0, b);
+        for (int c = 0; c < v_subs; ++c) load(ddo + c * kQuerySub, &mdo, q_full(s), 64 * c, h, q0, b);
+        XATTN_DCHECK(q0 + kQRows <= S_pad, a.status);
+        bulk_load_elect(dr0, a.nlse + rows + q0, kQRows * 4, q_full(s));
+        bulk_load_elect(dr0 + kQRows * 4, a.nD + rows + q0, kQRows * 4, q_full(s));
+        ++g;
+        return true;
+      };
+      // The first tiles do not wait for the unit before, whose K and V are still read.
+      const int pre = T < kStages ? T : kStages;
+      for (int t = 0; ok && t < pre; ++t) ok = load_tile(t);
+      if (!ok || !warp_wait(acc_done, (units & 1) ^ 1, ctl)) break;
+      mbar_expect_tx_elect(kv_full, (k_subs + 1 + v_subs) * kKeySub);
+      for (int c = 0; c < k_subs; ++c) load(sK + c * kKeySub, &mkv, kv_full, 64 * c, h, n * kTileRows, b);
+      load(sK + NS * kKeySub, &mrope, kv_full, 0, 0, n * kTileRows, b);
+      for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, kv_full, dn + 64 * c, h, n * kTileRows, b);
+      ++units;
+      for (int t = pre; ok && t < T; ++t) ok = load_tile(t);
+    }
+    // Every copy in flight has landed before the CTA can exit.
+    if (units > 0) mbar_drain(kv_full, (units - 1) & 1, ctl);
+    for (int r = max(g - kStages, 0); r < g; ++r) mbar_drain(q_full(r % kStages), (r / kStages) & 1, ctl);
+  } else if (warp == 1) {
+    // ---------------- issuer of S^T and dV ----------------
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
+    const uint32_t idesc_dv = idesc_bf16_f32(128, dv, false, true);
+    const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
+    const uint64_t ddO = smem_desc(sdO, kQuerySub, 1024, kSwizzle128);   // MN-major: 64 columns a sub-tile
+    auto scores = [&](int g) -> bool {                                   // S^T of tile g (over all units)
+      const int s = g % kStages;
+      if (!warp_wait(q_full(s), (g / kStages) & 1, ctl) || !warp_wait(p_free(g & 1), ((g >> 1) & 1) ^ 1, ctl)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t q = dQ + s * (NS + 1) * (kQuerySub >> 4);
+        const uint32_t d = tS(g & 1);
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (4 * c + kk < dn_steps)
+              mma_ss(d, dK + c * (kKeySub >> 4) + kk * 2, q + c * (kQuerySub >> 4) + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < dr_steps) mma_ss(d, dK + NS * (kKeySub >> 4) + kk * 2, q + NS * (kQuerySub >> 4) + kk * 2, idesc_s, 1u);
+        mma_commit(s_full(g & 1));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int units = 0, g = 0;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DKV_UNIT(u);
+      ok = warp_wait(kv_full, units & 1, ctl) && scores(g) && (T < 2 || scores(g + 1));
+      // The first dV overwrites the accumulator, which the unit before has read.
+      if (!ok || !warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
+#pragma unroll 1
+      for (int t = 0; t < T; ++t, ++g) {
+        const int s = g % kStages;
+        if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t o = ddO + s * NS * (kQuerySub >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kQRows / 16; ++kk)
+            mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(q_empty(s));
+          if (t + 1 == T) mma_commit(acc_done);
+        }
+        __syncwarp();
+        if (t + 2 < T && !scores(g + 2)) { ok = false; break; }
+      }
+      ++units;
+    }
+    if (ok && units > 0) mbar_drain(acc_done, (units - 1) & 1, ctl);
+  } else if (warp == 3) {
+    // ---------------- issuer of dP^T and dK ----------------
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
+    const uint32_t idesc_dk = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
+    const uint64_t dV = smem_desc(sV, 16, 1024, kSwizzle128), ddO = smem_desc(sdO, 16, 1024, kSwizzle128);
+    const uint64_t dQ = smem_desc(sQ, kQuerySub, 1024, kSwizzle128);     // MN-major
+    auto scores = [&](int g) -> bool {
+      const int s = g % kStages;
+      if (!warp_wait(q_full(s), (g / kStages) & 1, ctl)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t o = ddO + s * NS * (kQuerySub >> 4);
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (4 * c + kk < dv_steps)
+              mma_ss(tdP, dV + c * (kKeySub >> 4) + kk * 2, o + c * (kQuerySub >> 4) + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+        mma_commit(dp_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int units = 0, g = 0;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DKV_UNIT(u);
+      // (dP^T's place: the dK before, issued by this thread, reads dS^T there first, and the dS warps had read dP^T.)
+      ok = warp_wait(kv_full, units & 1, ctl) && scores(g);
+      if (!ok || !warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
+#pragma unroll 1
+      for (int t = 0; t < T; ++t, ++g) {
+        const int s = g % kStages;
+        if (!warp_wait(ds_full, g & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t q = dQ + s * (NS + 1) * (kQuerySub >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kQRows / 16; ++kk) {
+            mma_ts(tdK, tdP + kk * 8, q + kk * 128, idesc_dk, (t > 0 || kk > 0) ? 1u : 0u);
+            mma_ts(tdKr, tdP + kk * 8, q + NS * (kQuerySub >> 4) + kk * 128, idesc_dr, (t > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(q_empty(s));
+          if (t + 1 == T) mma_commit(acc_done);
+        }
+        __syncwarp();
+        if (t + 1 < T && !scores(g + 1)) { ok = false; break; }
+      }
+      ++units;
+    }
+    if (ok && units > 0) mbar_drain(acc_done, (units - 1) & 1, ctl);
+  } else if (warp >= 4) {
+    const bool p_side = warp < 8;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const float scale_log2 = a.scale * kLog2e;
+    bool ok = true;
+    int units = 0, g = 0;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DKV_UNIT(u);
+      if (p_side) {
+        // ---------------- P^T = exp2(S^T scale log2 e - LSE log2 e) ----------------
+#pragma unroll 1
+        for (int t = 0; t < T; ++t, ++g) {
+          if (!warp_wait(s_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t at = tS(g & 1) + lane_off;
+          uint32_t r[64];
+          tmem_ld_x32(at, r);
+          tmem_ld_x32(at + 32, r + 32);
+          tmem_wait_ld();
+          reg_fence<64>(r);
+          const float4 *nl = reinterpret_cast<const float4 *>(smem + L::kRows + (g % kStages) * 2 * kQRows * 4);
+          // Queries before the key (of the first two tiles) do not see it.
+          const int hidden = row - t * kQRows;                     // columns below it
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 m = nl[c / 4];
+            float x0, x1, x2, x3;
+            ffma2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), scale_log2, scale_log2, m.x, m.y);
+            ffma2(x2, x3, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]), scale_log2, scale_log2, m.z, m.w);
+            pk[c / 2] = pack_bf16x2(ex2_approx(x0), ex2_approx(x1));
+            pk[c / 2 + 1] = pack_bf16x2(ex2_approx(x2), ex2_approx(x3));
+          }
+          if (t < 2) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (2 * c < hidden) pk[c] &= 0xffff0000u;
+              if (2 * c + 1 < hidden) pk[c] &= 0x0000ffffu;
+            }
+          }
+          tmem_st_x32(at, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_full(g & 1));
+        }
+      } else {
+        // ---------------- dS^T = P^T (dP^T - D) ----------------
+#pragma unroll 1
+        for (int t = 0; t < T; ++t, ++g) {
+          if (!warp_wait(dp_full, g & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+          uint32_t r[64], p[32];
+          tmem_ld_x32(tdP + lane_off, r);
+          tmem_ld_x32(tdP + lane_off + 32, r + 32);
+          if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) {
+            tmem_wait_ld();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          tmem_ld_x32(tS(g & 1) + lane_off, p);
+          tmem_wait_ld();
+          reg_fence<64>(r);
+          reg_fence<32>(p);
+          tc_fence_before();
+          mbar_arrive(p_free(g & 1));
+          const float4 *nd = reinterpret_cast<const float4 *>(smem + L::kRows + (g % kStages) * 2 * kQRows * 4 + kQRows * 4);
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 d = nd[c / 4];
+            float x0, x1, x2, x3;
+            fadd2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), d.x, d.y);
+            fadd2(x2, x3, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]), d.z, d.w);
+            fmul2(x0, x1, x0, x1, bf16lo_to_f32(p[c / 2]), bf16hi_to_f32(p[c / 2]));
+            fmul2(x2, x3, x2, x3, bf16lo_to_f32(p[c / 2 + 1]), bf16hi_to_f32(p[c / 2 + 1]));
+            p[c / 2] = pack_bf16x2(x0, x1);
+            p[c / 2 + 1] = pack_bf16x2(x2, x3);
+          }
+          tmem_st_x32(tdP + lane_off, p);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(ds_full);
+        }
+      }
+      // The unit's sums: the P warps write dV, the dS warps dK and this head's part of k_rope's gradient.
+      if (!ok || !warp_wait(acc_done, units & 1, ctl)) break;
+      tc_fence_after();
+      const int j = n * kTileRows + row;
+      const size_t tok = (static_cast<size_t>(b) * S + j) * nh + h;
+      XATTN_DCHECK(j >= S || tok < static_cast<size_t>(a.B) * S * nh, a.status);
+      auto put = [&](uint32_t from, int cols, float mult, __nv_bfloat16 *to) {
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t v[16];
+          tmem_ld_x16(from + lane_off + c, v);
+          tmem_wait_ld();
+          reg_fence<16>(v);
+          if (j < S) {
+            uint4 *dst = reinterpret_cast<uint4 *>(to + c);
+            auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * mult, __uint_as_float(v[e + 1]) * mult); };
+            dst[0] = make_uint4(pair(0), pair(2), pair(4), pair(6));
+            dst[1] = make_uint4(pair(8), pair(10), pair(12), pair(14));
+          }
+          __syncwarp();
+        }
+      };
+      if (p_side) {
+        put(tdV, dv, 1.f, a.dkv + tok * (dn + dv) + dn);
+      } else {
+        put(tdK, dn, a.scale, a.dkv + tok * (dn + dv));
+#pragma unroll 1
+        for (int c = 0; c < dr; c += 16) {
+          uint32_t v[16];
+          tmem_ld_x16(tdKr + lane_off + c, v);
+          tmem_wait_ld();
+          reg_fence<16>(v);
+          if (j < S) {
+            float4 *dst = reinterpret_cast<float4 *>(a.rope_parts + tok * dr + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                                   __uint_as_float(v[4 * e + 3]));
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(acc_free);
+      ++units;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+#undef XATTN_DKV_UNIT
+
+// dQ: a CTA per (batch, head, 128 queries). Q and dO stay; K in two stages, V in one (it is read only by dP, early in a
+// tile's step, and there is no room for more).
+template <int NS>
+struct LatentDqLayout {
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kdO = kQ + (NS + 1) * kKeySub;
+  static constexpr uint32_t kK = kdO + NS * kKeySub;
+  static constexpr uint32_t kV = kK + 2 * (NS + 1) * kKeySub;
+  static constexpr uint32_t kBars = kV + NS * kKeySub;
+  static constexpr int kNumBars = 14;
+  static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
+  static constexpr uint32_t kUsed = kMisc + 32;
+  static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
+  static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
+};
+
+// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
+// TMEM: S [0, 128) | dP [128, 256) | dS bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448 on.
+template <int NS>
+__global__ void __maxnreg__(168)
+    latent_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
+                     const __grid_constant__ CUtensorMap mrope, const __grid_constant__ CUtensorMap mdo, const LatentArgs a) {
+  using L = LatentDqLayout<NS>;
+  extern __shared__ uint8_t latent_dq_smem[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dq_smem) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int S = a.S, nh = a.nh, dn = a.dn, dr = a.dr, dv = a.dv;
+  const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
+  const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
+  const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh;
+  const int m = num_m - 1 - static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) % BH;
+  const int b = bh / nh, h = bh - b * nh, T = m + 1;                 // key tiles
+  const uint32_t sQ = smem_u32(smem + L::kQ), sdO = smem_u32(smem + L::kdO), sK = smem_u32(smem + L::kK),
+                 sV = smem_u32(smem + L::kV), bar0 = smem_u32(smem + L::kBars);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  auto k_full = [&](int s) { return bar(s); };
+  auto k_empty = [&](int s) { return bar(2 + s); };
+  const uint32_t v_full = bar(4), v_empty = bar(5), q_full = bar(6), s_full = bar(7), s_free = bar(8), dp_full = bar(9),
+                 dp_free = bar(10), ds_full = bar(11), dq_done = bar(12), acc_done = bar(13);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
+  const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), (i == 8 || i == 10 || i == 11) ? 256 : 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mkv);
+    tma_prefetch_desc(&mrope);
+    tma_prefetch_desc(&mdo);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch();
+  grid_dep_wait();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+  const uint32_t tS = tmem, tdP = tmem + 128, tdS = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int col, int head, int row0) {
+      XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && dst >= sQ && dst + kKeySub <= bar0, a.status);
+      tma_load_4d_elect(dst, map, full, col, head, row0, b);
+    };
+    mbar_expect_tx_elect(q_full, (k_subs + 1 + v_subs) * kKeySub);
+    for (int c = 0; c < k_subs; ++c) load(sQ + c * kKeySub, &mq, q_full, 64 * c, h, m * kTileRows);
+    load(sQ + NS * kKeySub, &mq, q_full, dn, h, m * kTileRows);
+    for (int c = 0; c < v_subs; ++c) load(sdO + c * kKeySub, &mdo, q_full, 64 * c, h, m * kTileRows);
+    int issued_k = 0, issued_v = 0;
+    for (int n = 0; n < T; ++n) {
+      const int s = n & 1;
+      if (!warp_wait(k_empty(s), ((n >> 1) & 1) ^ 1, ctl)) break;
+      mbar_expect_tx_elect(k_full(s), (k_subs + 1) * kKeySub);
+      const uint32_t dk = sK + s * (NS + 1) * kKeySub;
+      for (int c = 0; c < k_subs; ++c) load(dk + c * kKeySub, &mkv, k_full(s), 64 * c, h, n * kTileRows);
+      load(dk + NS * kKeySub, &mrope, k_full(s), 0, 0, n * kTileRows);
+      issued_k = n + 1;
+      if (!warp_wait(v_empty, (n & 1) ^ 1, ctl)) break;
+      mbar_expect_tx_elect(v_full, v_subs * kKeySub);
+      for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, v_full, dn + 64 * c, h, n * kTileRows);
+      issued_v = n + 1;
+    }
+    // Every copy in flight has landed before the CTA can exit.
+    mbar_drain(q_full, 0, ctl);
+    for (int n = max(issued_k - 2, 0); n < issued_k; ++n) mbar_drain(k_full(n & 1), (n >> 1) & 1, ctl);
+    if (issued_v > 0) mbar_drain(v_full, (issued_v - 1) & 1, ctl);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
+    constexpr uint32_t kSubDesc = kKeySub >> 4;
+    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128), ddO = smem_desc(sdO, 16, 1024, kSwizzle128);
+    const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dV = smem_desc(sV, 16, 1024, kSwizzle128);
+    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
+    auto issue_s = [&](int s) {
+      if (elect_one()) {
+        const uint64_t kd = dK + s * (NS + 1) * kSubDesc;
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (4 * c + kk < dn_steps) mma_ss(tS, dQ + c * kSubDesc + kk * 2, kd + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < dr_steps) mma_ss(tS, dQ + NS * kSubDesc + kk * 2, kd + NS * kSubDesc + kk * 2, idesc_s, 1u);
+        mma_commit(s_full);
+      }
+      __syncwarp();
+    };
+    auto issue_dp = [&]() {
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (4 * c + kk < dv_steps) mma_ss(tdP, ddO + c * kSubDesc + kk * 2, dV + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+        mma_commit(dp_full);
+        mma_commit(v_empty);
+      }
+      __syncwarp();
+    };
+    bool ok = warp_wait(q_full, 0, ctl) && warp_wait(k_full(0), 0, ctl);
+    if (ok) {
+      tc_fence_after();
+      issue_s(0);
+      ok = warp_wait(v_full, 0, ctl);
+    }
+    if (ok) {
+      tc_fence_after();
+      issue_dp();
+    }
+#pragma unroll 1
+    for (int n = 0; ok && n < T; ++n) {
+      const int s = n & 1, s1 = s ^ 1;
+      const uint32_t ph = n & 1;
+      if (n + 1 < T) {
+        // The next tile's products as soon as the compute warps have read this tile's.
+        if (!warp_wait(k_full(s1), ((n + 1) >> 1) & 1, ctl) || !warp_wait(s_free, ph, ctl)) break;
+        tc_fence_after();
+        issue_s(s1);
+        if (!warp_wait(v_full, (n + 1) & 1, ctl) || !warp_wait(dp_free, ph, ctl)) break;
+        tc_fence_after();
+        issue_dp();
+      }
+      if (!warp_wait(ds_full, ph, ctl)) break;
+      tc_fence_after();
+      if (elect_one()) {                                            // dQ += dS K_n
+        const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
+#pragma unroll
+        for (int kk = 0; kk < kTileRows / 16; ++kk) {
+          mma_ts(tdQ, tdS + kk * 8, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
+          mma_ts(tdQr, tdS + kk * 8, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(dq_done);
+        mma_commit(k_empty(s));
+      }
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(acc_done);
+    __syncwarp();
+    mbar_drain(acc_done, 0, ctl);
+  } else if (warp >= 4) {
+    // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
+    const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int i = quarter * 32 + lane, ig = m * kTileRows + i;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int c0 = 64 * g;                              // first key column of this group
+    const float scale_log2 = a.scale * kLog2e;
+    const size_t at = static_cast<size_t>(bh) * padded_rows(S) + ig;
+    const float nlse2 = a.nlse[at], nD = a.nD[at];
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; n < T; ++n) {
+      if (!warp_wait(s_full, n & 1, ctl)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t p[64];
+      tmem_ld_x32(tS + lane_off + c0, p);
+      tmem_ld_x32(tS + lane_off + c0 + 32, p + 32);
+      tmem_wait_ld();
+      reg_fence<64>(p);
+      tc_fence_before();
+      mbar_arrive(s_free);
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        float x0, x1;
+        ffma2(x0, x1, __uint_as_float(p[e]), __uint_as_float(p[e + 1]), scale_log2, scale_log2, nlse2, nlse2);
+        p[e] = __float_as_uint(ex2_approx(x0));
+        p[e + 1] = __float_as_uint(ex2_approx(x1));
+      }
+      if (n == m) {                                     // keys behind the query
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (c0 + e > i) p[e] = 0u;
+      }
+      // dS = P (dP - D) in two 32-column halves, bf16 into the dS slot.
+      if (!warp_wait(dp_full, n & 1, ctl)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t d[32];
+        tmem_ld_x32(tdP + lane_off + c0 + 32 * half, d);
+        tmem_wait_ld();
+        reg_fence<32>(d);
+        if (half == 1) {                                // dP(n) fully read
+          tc_fence_before();
+          mbar_arrive(dp_free);
+        }
+        uint32_t ds[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float t0, t1;
+          fadd2(t0, t1, __uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), nD, nD);
+          fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * half + 2 * e]), __uint_as_float(p[32 * half + 2 * e + 1]));
+          ds[e] = pack_bf16x2(t0, t1);
+        }
+        if (half == 0 && n > 0) {
+          // dQ(n - 1) has finished reading the dS slot.
+          if (!warp_wait(dq_done, (n - 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+        }
+        tmem_st_x16(tdS + lane_off + c0 / 2 + 16 * half, ds);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    // Epilogue: dq = bf16(scale * sum); group g writes every second 16 columns of the thread's row.
+    if (ok && warp_wait(acc_done, 0, ctl)) {
+      tc_fence_after();
+      const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
+      XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
+#pragma unroll 1
+      for (int c = 16 * g; c < dn + dr; c += 32) {
+        uint32_t v[16];
+        tmem_ld_x16((c < dn ? tdQ + c : tdQr + (c - dn)) + lane_off, v);
+        tmem_wait_ld();
+        reg_fence<16>(v);
+        if (ig < S) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.dq + row * (dn + dr) + c);
+          auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale); };
+          dst[0] = make_uint4(pair(0), pair(2), pair(4), pair(6));
+          dst[1] = make_uint4(pair(8), pair(10), pair(12), pair(14));
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// k_rope's gradient: the heads' parts added in order, four columns a thread.
+__global__ void __launch_bounds__(256) latent_rope_kernel(const LatentArgs a) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const size_t t = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int quads = a.dr / 4;
+  const size_t tok = t / quads;
+  if (tok >= static_cast<size_t>(a.B) * a.S) return;
+  const int c = static_cast<int>(t - tok * quads) * 4;
+  const float *from = a.rope_parts + tok * a.nh * a.dr + c;
+  float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int h = 0; h < a.nh; ++h) {
+    const float4 x = *reinterpret_cast<const float4 *>(from + static_cast<size_t>(h) * a.dr);
+    g.x += x.x, g.y += x.y, g.z += x.z, g.w += x.w;
+  }
+  *reinterpret_cast<uint2 *>(a.dk_rope + tok * a.dr + c) =
+      make_uint2(pack_bf16x2(g.x * a.scale, g.y * a.scale), pack_bf16x2(g.z * a.scale, g.w * a.scale));
+}
+
+template <int NS>
+cudaError_t launch_latent_bwd_ns(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
+                                 cudaStream_t stream) {
+  using LK = DkvLayout<NS>;
+  using LQ = LatentDqLayout<NS>;
+  static std::atomic<unsigned long long> allowed_k{0}, allowed_q{0};
+  cudaError_t err = allow_smem(latent_dkv_kernel<NS>, LK::kDynBytes, allowed_k);
+  if (err == cudaSuccess) err = allow_smem(latent_dq_kernel<NS>, LQ::kDynBytes, allowed_q);
+  if (err != cudaSuccess) return err;
+  const long long num_n = (a.S + kTileRows - 1) / kTileRows, units = num_n * a.B * a.nh;
+  err = launch_pdl(latent_dkv_kernel<NS>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LK::kDynBytes, stream,
+                   q64.q, q128.kv, q128.rope, q64.dO, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(latent_dq_kernel<NS>, static_cast<unsigned>(units), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
+                    q128.rope, q128.dO, a);
+}
+
+}  // namespace
+
+size_t latent_bwd_workspace_bytes(const LatentArgs &a) {
+  return (2 * static_cast<size_t>(a.B) * a.nh * padded_rows(a.S) + static_cast<size_t>(a.B) * a.S * a.nh * a.dr) * sizeof(float);
+}
+void latent_bwd_workspace_carve(LatentArgs &a, void *base) {
+  const size_t rows = static_cast<size_t>(a.B) * a.nh * padded_rows(a.S);
+  a.nlse = static_cast<float *>(base);
+  a.nD = a.nlse + rows;
+  a.rope_parts = a.nD + rows;
+}
+
+cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
+                              cudaStream_t stream) {
+  const size_t rows = static_cast<size_t>(a.B) * a.nh * padded_rows(a.S);
+  cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0, stream, a);
+  if (err != cudaSuccess) return err;
+  err = a.dn <= 64 && a.dv <= 64 ? launch_latent_bwd_ns<1>(q64, q128, a, sms, stream)
+                                 : launch_latent_bwd_ns<2>(q64, q128, a, sms, stream);
+  if (err != cudaSuccess) return err;
+  const size_t threads = static_cast<size_t>(a.B) * a.S * (a.dr / 4);
+  return launch_pdl(latent_rope_kernel, static_cast<unsigned>((threads + 255) / 256), 256, 0, stream, a);
+}
+
+}  // namespace xattn

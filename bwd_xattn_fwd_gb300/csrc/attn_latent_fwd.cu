@@ -11,8 +11,8 @@
 //     sub-tiles in the order K(0) V(0) K(1) V(1) ..: V(n) takes the place of K(n - 1)'s first two as soon as both scores
 //     have read them, K(n) that of V(n - 2). (Two stages of K and one of V are as much memory, but V(n) could only be
 //     fetched when P V(n - 1) has ended, right before it is needed.) Where dn, dv <= 64: three whole stages.
-//   * P V is one product over all dv columns: two of 64 cost nearly twice as much (a product of 128 x 64 x 16 takes some 60
-//     cycles where 128 x 128 x 16 takes 64). Only a V whose second sub-tile lies at the ring's start is taken in two.
+//   * P V is a product a sub-tile (P from TMEM: 32 cycles a K step and 64 columns, as much as half of one over 128), so V's
+//     two may lie anywhere in the ring.
 // Roundings: P to bf16, V's type, before P V; o to bf16. Exponentials as in attn_fwd_sm103.cu.
 // TMEM: S_A [0,128) S_B [128,256) fp32, P over each one's first 64 columns | O_A [256,384) O_B [384,512).
 #include <type_traits>
@@ -208,12 +208,12 @@ __global__ void __maxnreg__(168)
     // phases behind (a barrier tells only its last two apart).
     const int x = warp == 1 ? 0 : 1;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
-    const uint32_t idesc_pv = idesc_bf16_f32(128, dv, false, true), idesc_pv0 = idesc_bf16_f32(128, 64, false, true),
+    const uint32_t idesc_pv0 = idesc_bf16_f32(128, min(dv, 64), false, true),
                    idesc_pv1 = idesc_bf16_f32(128, max(dv - 64, 16), false, true);
     constexpr uint32_t kSubDesc = kSubTile >> 4, kRowStep = (16 * 128) >> 4;
     const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128) + x * (NS + 1) * kSubDesc;
     const uint64_t dK = smem_desc(sRing, 16, 1024, kSwizzle128);
-    const uint64_t dV = smem_desc(sRing, kSubTile, 1024, kSwizzle128);   // MN-major: the next 64 columns a sub-tile on
+    const uint64_t dV = smem_desc(sRing, 8192, 1024, kSwizzle128);       // MN-major
     const uint32_t tSx = tS(x), tOx = tO(x);
     auto issue_qk = [&](int R) {
       if (elect_one()) {
@@ -234,19 +234,12 @@ __global__ void __maxnreg__(168)
       __syncwarp();
     };
     auto issue_pv = [&](int R, bool first) {
-      const int v0 = v_block(R, 0);
-      const uint64_t vd = dV + v0 * kSubDesc;
+      const uint64_t v0 = dV + v_block(R, 0) * kSubDesc, v1 = dV + v_block(R, NS - 1) * kSubDesc;
       if (elect_one()) {
-        if (NS == 1 || v0 + 1 < kBlocks || dv <= 64) {
 #pragma unroll
-          for (int kk = 0; kk < kTileRows / 16; ++kk)
-            mma_ts(tOx, tSx + kk * 8, vd + kk * kRowStep, idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < kTileRows / 16; ++kk) {
-            mma_ts(tOx, tSx + kk * 8, vd + kk * kRowStep, idesc_pv0, (!first || kk > 0) ? 1u : 0u);
-            mma_ts(tOx + 64, tSx + kk * 8, dV + kk * kRowStep, idesc_pv1, (!first || kk > 0) ? 1u : 0u);
-          }
+        for (int kk = 0; kk < kTileRows / 16; ++kk) {
+          mma_ts(tOx, tSx + kk * 8, v0 + kk * kRowStep, idesc_pv0, (!first || kk > 0) ? 1u : 0u);
+          if (NS == 2 && dv > 64) mma_ts(tOx + 64, tSx + kk * 8, v1 + kk * kRowStep, idesc_pv1, (!first || kk > 0) ? 1u : 0u);
         }
         mma_commit(o_done(x));
         mma_commit(v_empty(R % kDepth));
@@ -490,8 +483,7 @@ __global__ void __maxnreg__(168)
 #undef XATTN_LATENT_UNIT
 
 template <int NS, bool kNegScale>
-cudaError_t launch_latent_fwd_ns(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrope,
-                                 const LatentArgs &a, int sms, cudaStream_t stream) {
+cudaError_t launch_latent_fwd_ns(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream) {
   using L = LatentFwdLayout<NS>;
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t err = allow_smem(latent_fwd_kernel<NS, kNegScale>, L::kDynBytes, allowed);
@@ -499,18 +491,17 @@ cudaError_t launch_latent_fwd_ns(const CUtensorMap &mq, const CUtensorMap &mkv, 
   const int num_m = (a.S + kTileRows - 1) / kTileRows;
   const long long units = static_cast<long long>(a.B) * a.nh * ((num_m + 1) / 2);
   return launch_pdl(latent_fwd_kernel<NS, kNegScale>, static_cast<unsigned>(units < sms ? units : sms), kFwdThreads,
-                    L::kDynBytes, stream, mq, mkv, mrope, a);
+                    L::kDynBytes, stream, maps.q, maps.kv, maps.rope, a);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_fwd(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrope, const LatentArgs &a,
-                              int sms, cudaStream_t stream) {
+cudaError_t launch_latent_fwd(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream) {
   if (a.dn <= 64 && a.dv <= 64)
-    return a.scale < 0.f ? launch_latent_fwd_ns<1, true>(mq, mkv, mrope, a, sms, stream)
-                         : launch_latent_fwd_ns<1, false>(mq, mkv, mrope, a, sms, stream);
-  return a.scale < 0.f ? launch_latent_fwd_ns<2, true>(mq, mkv, mrope, a, sms, stream)
-                       : launch_latent_fwd_ns<2, false>(mq, mkv, mrope, a, sms, stream);
+    return a.scale < 0.f ? launch_latent_fwd_ns<1, true>(maps, a, sms, stream)
+                         : launch_latent_fwd_ns<1, false>(maps, a, sms, stream);
+  return a.scale < 0.f ? launch_latent_fwd_ns<2, true>(maps, a, sms, stream)
+                       : launch_latent_fwd_ns<2, false>(maps, a, sms, stream);
 }
 
 }  // namespace xattn

@@ -556,7 +556,6 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   const int grid = tree_grid(a, hd, dev->sms);
   void *ws = nullptr;
   if (!a.whole) XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
-  a.q = static_cast<const __nv_bfloat16 *>(q);
   a.page_table = page_table;
   a.ctx_lens = ctx_lens;
   a.tree = tree;
@@ -800,18 +799,15 @@ xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope,
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
   LatentArgs a = {};
-  a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.kv = static_cast<const __nv_bfloat16 *>(kv);
-  a.k_rope = static_cast<const __nv_bfloat16 *>(k_rope);
   a.o = static_cast<__nv_bfloat16 *>(o);
   a.lse = lse;
   a.B = B, a.S = S, a.nh = nh, a.dn = dn, a.dr = dr, a.dv = dv, a.scale = scale;
   a.status = dev->status, a.timeout_ns = wait_limit_ns();
-  CUtensorMap mq, mkv, mrope;
-  XATTN_TRY(make_map_subtiles(&mq, q, B, S, nh, dn + dr, kTileRows));
-  XATTN_TRY(make_map_subtiles(&mkv, kv, B, S, nh, dn + dv, kTileRows));
-  XATTN_TRY(make_map_subtiles(&mrope, k_rope, B, S, 1, dr, kTileRows));
-  return cuda_status(launch_latent_fwd(mq, mkv, mrope, a, dev->sms, static_cast<cudaStream_t>(stream)));
+  LatentMaps maps;
+  XATTN_TRY(make_map_subtiles(&maps.q, q, B, S, nh, dn + dr, kTileRows));
+  XATTN_TRY(make_map_subtiles(&maps.kv, kv, B, S, nh, dn + dv, kTileRows));
+  XATTN_TRY(make_map_subtiles(&maps.rope, k_rope, B, S, 1, dr, kTileRows));
+  return cuda_status(launch_latent_fwd(maps, a, dev->sms, static_cast<cudaStream_t>(stream)));
 }
 
 xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope, const void *o, const void *dO,
@@ -825,9 +821,6 @@ xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope,
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
   LatentArgs a = {};
-  a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.kv = static_cast<const __nv_bfloat16 *>(kv);
-  a.k_rope = static_cast<const __nv_bfloat16 *>(k_rope);
   a.dO = static_cast<const __nv_bfloat16 *>(dO);
   a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(o));   // (read only here)
   a.lse = const_cast<float *>(lse);
@@ -838,9 +831,16 @@ xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope,
   a.status = dev->status, a.timeout_ns = wait_limit_ns();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   void *base = nullptr;
+  LatentMaps q64, q128;
+  XATTN_TRY(make_map_subtiles(&q128.q, q, B, S, nh, dn + dr, kTileRows));
+  XATTN_TRY(make_map_subtiles(&q128.kv, kv, B, S, nh, dn + dv, kTileRows));
+  XATTN_TRY(make_map_subtiles(&q128.rope, k_rope, B, S, 1, dr, kTileRows));
+  XATTN_TRY(make_map_subtiles(&q128.dO, dO, B, S, nh, dv, kTileRows));
+  XATTN_TRY(make_map_subtiles(&q64.q, q, B, S, nh, dn + dr, 64));
+  XATTN_TRY(make_map_subtiles(&q64.dO, dO, B, S, nh, dv, 64));
   XATTN_TRY(scratch_alloc(*dev, latent_bwd_workspace_bytes(a), st, &base));
   latent_bwd_workspace_carve(a, base);
-  xattn_status r = cuda_status(launch_latent_bwd(a, st));
+  xattn_status r = cuda_status(launch_latent_bwd(q64, q128, a, dev->sms, st));
   const cudaError_t fe = cudaFreeAsync(base, st);
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
   return r;

@@ -212,24 +212,29 @@ struct PageArgs {
 cudaError_t launch_cache_append(const PageArgs &a, const void *k_new, const void *v_new, cudaStream_t stream);
 cudaError_t launch_cache_compact(const PageArgs &a, const int *path, const int *accepted, cudaStream_t stream);
 
-// Latent attention, expanded form (attn_latent_fwd.cu, attn_latent.cu); maps: boxes of 64 columns of 128 rows of a head. Head h's key of token j is (kv[j, h, :dn],
+// Latent attention, expanded form (attn_latent_fwd.cu, attn_latent_bwd.cu): head h's key of token j is (kv[j, h, :dn],
 // k_rope[j]), its value kv[j, h, dn:].
 struct LatentArgs {
-  const __nv_bfloat16 *q, *kv, *k_rope, *dO;   // [B,S,nh,dn+dr], [B,S,nh,dn+dv], [B,S,dr], [B,S,nh,dv]
+  const __nv_bfloat16 *dO;                     // [B,S,nh,dv]
   __nv_bfloat16 *o;                            // [B,S,nh,dv]: written by the forward, read by the backward
   float *lse;                                  // [B,S,nh], likewise
-  __nv_bfloat16 *dq, *dkv, *dk_rope;
-  float *D, *rope_parts;                       // the backward's scratch
+  __nv_bfloat16 *dq, *dkv, *dk_rope;           // [B,S,nh,dn+dr], [B,S,nh,dn+dv], [B,S,dr]
+  float *nlse, *nD, *rope_parts;               // the backward's scratch: [B,nh,S_pad] twice, [B,S,nh,dr]
   int B, S, nh, dn, dr, dv;
   float scale;
   int *status;
   unsigned long long timeout_ns;
 };
+// Maps over the tensors: boxes of 64 columns of 128 (or 64) rows of one head.
+struct LatentMaps {
+  CUtensorMap q, kv, rope, dO;
+};
 size_t latent_bwd_workspace_bytes(const LatentArgs &a);
 void latent_bwd_workspace_carve(LatentArgs &a, void *base);
-cudaError_t launch_latent_fwd(const CUtensorMap &mq, const CUtensorMap &mkv, const CUtensorMap &mrope, const LatentArgs &a,
-                              int sms, cudaStream_t stream);
-cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
+cudaError_t launch_latent_fwd(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream);
+// q64: q and dO by 64 rows; q128: all four by 128.
+cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
+                              cudaStream_t stream);
 
 // Absorbed form (attn_latent_decode.cu): n new tokens a sequence over a paged cache of rows of dc + dr numbers. mq: map
 // over the queries, boxes of 64 columns of tile_rows rows of one sequence; mc: over the pool, boxes of 64 columns of
