@@ -8,8 +8,8 @@
 //      head are one contiguous copy.
 //   2. latent_dkv_kernel (key-stationary): a unit is (batch, head, 128 keys); dV [128, dv] and dK [128, dn + dr] stay in TMEM,
 //      320 of its 512 columns, so queries come in tiles of 64 and three 64-column places hold the scores: S^T(t) in place
-//      t % 2 (P^T over it), dP^T(t) in the third (dS^T over it). S^T is issued two tiles ahead, so it runs while the warps
-//      work on P and dS. A score product of 64 columns takes 48 cycles a K step where its arithmetic is 32 (shared memory
+//      t % 2 (P^T over it), dP^T(t) in the third (dS^T over it). S^T(t + 1) is issued before dV(t), so it runs while the
+//      warps work on P and dS (two tiles ahead it waited for a stage of the ring). A score product of 64 columns takes 48 cycles a K step where its arithmetic is 32 (shared memory
 //      feeds 128 + 64 rows); with 128 columns the places would not fit. Per 64 queries 576 (S) + 384 (dP) + 256 (dV) + 384 (dK).
 //   3. latent_dq_kernel (query-stationary, as attn_bwd_dq_sm103.cu): S and dP once more, dQ += dS K in TMEM over the key
 //      tiles. dQ [., dn + dr] does not fit beside dV and dK, and summed with atomics it would not be reproducible.
@@ -32,33 +32,47 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok);
 }
 
-// One warp a row (b, i, h) of o and dO. Rows S .. S_pad - 1: a weight of 0 (their Q and dO are read as zeros).
+// Sixteen lanes a row (b, i, h) of o and dO, eight numbers each; kRowsEach rows a group of lanes, their loads together. Rows
+// S .. S_pad - 1 get a weight of 0 (their Q and dO are read as zeros).
+constexpr int kRowsEach = 4, kRowsBlock = 256 / 16 * kRowsEach;
 __global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a) {
   grid_dep_launch();
   grid_dep_wait();
-  const int lane = threadIdx.x & 31, S_pad = padded_rows(a.S);
-  const size_t row = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<size_t>(a.B) * S_pad * a.nh) return;
-  const int h = static_cast<int>(row % a.nh);
-  const size_t rest = row / a.nh;
-  const int i = static_cast<int>(rest % S_pad);
-  const size_t b = rest / S_pad, to = (b * a.nh + h) * S_pad + i;
-  if (i >= a.S) {
-    if (lane == 0) a.nlse[to] = -INFINITY, a.nD[to] = 0.f;
-    return;
-  }
-  const size_t from = (b * a.S + i) * a.nh + h;
-  float dot = 0.f;
-  if (4 * lane < a.dv) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(a.o + from * a.dv + 4 * lane);
-    const uint2 y = *reinterpret_cast<const uint2 *>(a.dO + from * a.dv + 4 * lane);
-    dot = bf16lo_to_f32(x.x) * bf16lo_to_f32(y.x) + bf16hi_to_f32(x.x) * bf16hi_to_f32(y.x);
-    dot = fmaf(bf16lo_to_f32(x.y), bf16lo_to_f32(y.y), dot);
-    dot = fmaf(bf16hi_to_f32(x.y), bf16hi_to_f32(y.y), dot);
+  const int part = threadIdx.x & 15, group = threadIdx.x >> 4, S_pad = padded_rows(a.S);
+  const unsigned nh = a.nh;
+  const size_t rows = static_cast<size_t>(a.B) * S_pad * nh;
+  size_t row = static_cast<size_t>(blockIdx.x) * kRowsBlock + group, from[kRowsEach], to[kRowsEach];
+  bool live[kRowsEach], real[kRowsEach];
+  uint4 x[kRowsEach], y[kRowsEach];
+#pragma unroll
+  for (int e = 0; e < kRowsEach; ++e, row += 16) {
+    const size_t rest = row / nh, b = rest / S_pad;
+    const int h = static_cast<int>(row - rest * nh), i = static_cast<int>(rest - b * S_pad);
+    live[e] = row < rows;
+    real[e] = live[e] && i < a.S;
+    to[e] = (b * nh + h) * S_pad + i;
+    from[e] = (b * a.S + i) * nh + h;
+    x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (real[e] && 8 * part < a.dv) {
+      x[e] = *reinterpret_cast<const uint4 *>(a.o + from[e] * a.dv + 8 * part);
+      y[e] = *reinterpret_cast<const uint4 *>(a.dO + from[e] * a.dv + 8 * part);
+    }
   }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-  if (lane == 0) a.nlse[to] = -a.lse[from] * kLog2e, a.nD[to] = -dot;
+  for (int e = 0; e < kRowsEach; ++e) {
+    float dot = 0.f;
+    auto add = [&](uint32_t u, uint32_t v) {
+      dot = fmaf(bf16lo_to_f32(u), bf16lo_to_f32(v), dot);
+      dot = fmaf(bf16hi_to_f32(u), bf16hi_to_f32(v), dot);
+    };
+    add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
+#pragma unroll
+    for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (live[e] && part == 0) {
+      a.nlse[to[e]] = real[e] ? -a.lse[from[e]] * kLog2e : -INFINITY;
+      a.nD[to[e]] = -dot;
+    }
+  }
 }
 
 // NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS).
@@ -195,6 +209,13 @@ __global__ void __maxnreg__(168)
       for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, kv_full, dn + 64 * c, h, n * kTileRows, b);
       ++units;
       for (int t = pre; ok && t < T; ++t) ok = load_tile(t);
+      // The next unit's K and V into L2: they are fetched when this one's products have ended, with nothing to do meanwhile.
+      const int u1 = unit_at(k + 1);
+      if (ok && u1 < num_units) {
+        const int n1 = u1 / BH, bh1 = u1 - n1 * BH, b1 = bh1 / nh, h1 = bh1 - b1 * nh;
+        for (int c = 0; c < k_subs; ++c) tma_prefetch_4d_elect(&mkv, 64 * c, h1, n1 * kTileRows, b1);
+        for (int c = 0; c < v_subs; ++c) tma_prefetch_4d_elect(&mkv, dn + 64 * c, h1, n1 * kTileRows, b1);
+      }
     }
     // Every copy in flight has landed before the CTA can exit.
     if (units > 0) mbar_drain(kv_full, (units - 1) & 1, ctl);
@@ -233,13 +254,13 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       XATTN_DKV_UNIT(u);
-      ok = warp_wait(kv_full, units & 1, ctl) && scores(g) && (T < 2 || scores(g + 1));
+      ok = warp_wait(kv_full, units & 1, ctl) && scores(g);
       // The first dV overwrites the accumulator, which the unit before has read.
       if (!ok || !warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
         const int s = g % kStages;
-        if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+        if ((t + 1 < T && !scores(g + 1)) || !warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           const uint64_t o = ddO + s * NS * (kQuerySub >> 4);
@@ -250,7 +271,6 @@ __global__ void __maxnreg__(168)
           if (t + 1 == T) mma_commit(acc_done);
         }
         __syncwarp();
-        if (t + 2 < T && !scores(g + 2)) { ok = false; break; }
       }
       ++units;
     }
@@ -411,10 +431,8 @@ __global__ void __maxnreg__(168)
           tmem_wait_ld();
           reg_fence<16>(v);
           if (j < S) {
-            uint4 *dst = reinterpret_cast<uint4 *>(to + c);
             auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * mult, __uint_as_float(v[e + 1]) * mult); };
-            dst[0] = make_uint4(pair(0), pair(2), pair(4), pair(6));
-            dst[1] = make_uint4(pair(8), pair(10), pair(12), pair(14));
+            store_32(to + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
           }
           __syncwarp();
         }
@@ -430,11 +448,9 @@ __global__ void __maxnreg__(168)
           tmem_wait_ld();
           reg_fence<16>(v);
           if (j < S) {
-            float4 *dst = reinterpret_cast<float4 *>(a.rope_parts + tok * dr + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
-                                   __uint_as_float(v[4 * e + 3]));
+            float *dst = a.rope_parts + tok * dr + c;
+            store_32(dst, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+            store_32(dst + 8, v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]);
           }
           __syncwarp();
         }
@@ -463,14 +479,14 @@ struct LatentDqLayout {
   static constexpr uint32_t kK = kdO + NS * kKeySub;
   static constexpr uint32_t kV = kK + 2 * (NS + 1) * kKeySub;
   static constexpr uint32_t kBars = kV + NS * kKeySub;
-  static constexpr int kNumBars = 14;
+  static constexpr int kNumBars = 13;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
   static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
 };
 
-// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
+// Warps: 0 TMA; 1 issuer of S and dP (and TMEM owner); 3 issuer of dQ; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
 // TMEM: S [0, 128) | dP [128, 256) | dS bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448 on.
 template <int NS>
 __global__ void __maxnreg__(168)
@@ -493,7 +509,7 @@ __global__ void __maxnreg__(168)
   auto k_full = [&](int s) { return bar(s); };
   auto k_empty = [&](int s) { return bar(2 + s); };
   const uint32_t v_full = bar(4), v_empty = bar(5), q_full = bar(6), s_full = bar(7), s_free = bar(8), dp_full = bar(9),
-                 dp_free = bar(10), ds_full = bar(11), dq_done = bar(12), acc_done = bar(13);
+                 dp_free = bar(10), ds_full = bar(11), dq_done = bar(12);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
@@ -548,13 +564,12 @@ __global__ void __maxnreg__(168)
     for (int n = max(issued_k - 2, 0); n < issued_k; ++n) mbar_drain(k_full(n & 1), (n >> 1) & 1, ctl);
     if (issued_v > 0) mbar_drain(v_full, (issued_v - 1) & 1, ctl);
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
+    // ---------------- issuer of S and dP ----------------
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
+    bool scored = false;
     constexpr uint32_t kSubDesc = kKeySub >> 4;
     const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128), ddO = smem_desc(sdO, 16, 1024, kSwizzle128);
     const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dV = smem_desc(sV, 16, 1024, kSwizzle128);
-    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
     auto issue_s = [&](int s) {
       if (elect_one()) {
         const uint64_t kd = dK + s * (NS + 1) * kSubDesc;
@@ -582,32 +597,31 @@ __global__ void __maxnreg__(168)
       }
       __syncwarp();
     };
-    bool ok = warp_wait(q_full, 0, ctl) && warp_wait(k_full(0), 0, ctl);
-    if (ok) {
-      tc_fence_after();
-      issue_s(0);
-      ok = warp_wait(v_full, 0, ctl);
-    }
-    if (ok) {
-      tc_fence_after();
-      issue_dp();
-    }
+    // The next tile's products as soon as the compute warps have read this tile's.
+    bool ok = warp_wait(q_full, 0, ctl);
 #pragma unroll 1
     for (int n = 0; ok && n < T; ++n) {
-      const int s = n & 1, s1 = s ^ 1;
-      const uint32_t ph = n & 1;
-      if (n + 1 < T) {
-        // The next tile's products as soon as the compute warps have read this tile's.
-        if (!warp_wait(k_full(s1), ((n + 1) >> 1) & 1, ctl) || !warp_wait(s_free, ph, ctl)) break;
-        tc_fence_after();
-        issue_s(s1);
-        if (!warp_wait(v_full, (n + 1) & 1, ctl) || !warp_wait(dp_free, ph, ctl)) break;
-        tc_fence_after();
-        issue_dp();
-      }
-      if (!warp_wait(ds_full, ph, ctl)) break;
+      if (!warp_wait(k_full(n & 1), (n >> 1) & 1, ctl) || !warp_wait(s_free, (n & 1) ^ 1, ctl)) break;
       tc_fence_after();
-      if (elect_one()) {                                            // dQ += dS K_n
+      issue_s(n & 1);
+      if (!warp_wait(v_full, n & 1, ctl) || !warp_wait(dp_free, (n & 1) ^ 1, ctl)) break;
+      tc_fence_after();
+      issue_dp();
+      if (n + 1 == T) scored = true;
+    }
+    if (scored) mbar_drain(dp_full, (T - 1) & 1, ctl);
+  } else if (warp == 3) {
+    // ---------------- issuer of dQ += dS K (apart, so that it does not wait behind scores whose K has not landed) --------
+    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
+    constexpr uint32_t kSubDesc = kKeySub >> 4;
+    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
+    int done = 0;
+#pragma unroll 1
+    for (int n = 0; n < T; ++n) {
+      const int s = n & 1;
+      if (!warp_wait(ds_full, n & 1, ctl)) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
 #pragma unroll
         for (int kk = 0; kk < kTileRows / 16; ++kk) {
@@ -618,10 +632,9 @@ __global__ void __maxnreg__(168)
         mma_commit(k_empty(s));
       }
       __syncwarp();
+      done = n + 1;
     }
-    if (elect_one()) mma_commit(acc_done);
-    __syncwarp();
-    mbar_drain(acc_done, 0, ctl);
+    if (done > 0) mbar_drain(dq_done, (done - 1) & 1, ctl);
   } else if (warp >= 4) {
     // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
     const int g = (warp - 4) >> 2, quarter = warp & 3;
@@ -689,7 +702,7 @@ __global__ void __maxnreg__(168)
       mbar_arrive(ds_full);
     }
     // Epilogue: dq = bf16(scale * sum); group g writes every second 16 columns of the thread's row.
-    if (ok && warp_wait(acc_done, 0, ctl)) {
+    if (ok && warp_wait(dq_done, (T - 1) & 1, ctl)) {
       tc_fence_after();
       const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
       XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
@@ -700,10 +713,8 @@ __global__ void __maxnreg__(168)
         tmem_wait_ld();
         reg_fence<16>(v);
         if (ig < S) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.dq + row * (dn + dr) + c);
           auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale); };
-          dst[0] = make_uint4(pair(0), pair(2), pair(4), pair(6));
-          dst[1] = make_uint4(pair(8), pair(10), pair(12), pair(14));
+          store_32(a.dq + row * (dn + dr) + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
         }
         __syncwarp();
       }
@@ -770,7 +781,7 @@ void latent_bwd_workspace_carve(LatentArgs &a, void *base) {
 cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
                               cudaStream_t stream) {
   const size_t rows = static_cast<size_t>(a.B) * a.nh * padded_rows(a.S);
-  cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0, stream, a);
+  cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>((rows + kRowsBlock - 1) / kRowsBlock), 256, 0, stream, a);
   if (err != cudaSuccess) return err;
   err = a.dn <= 64 && a.dv <= 64 ? launch_latent_bwd_ns<1>(q64, q128, a, sms, stream)
                                  : launch_latent_bwd_ns<2>(q64, q128, a, sms, stream);

@@ -460,10 +460,8 @@ __global__ void __maxnreg__(168)
         tmem_wait_ld();
         reg_fence<16>(ov);
         if (i < S) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.o + at * dv + c);
           auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv); };
-          dst[0] = make_uint4(pair(0), pair(2), pair(4), pair(6));
-          dst[1] = make_uint4(pair(8), pair(10), pair(12), pair(14));
+          store_32(a.o + at * dv + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
         }
         __syncwarp();
       }

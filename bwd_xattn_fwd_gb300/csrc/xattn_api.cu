@@ -194,6 +194,7 @@ xattn_status make_map_aux(CUtensorMap *map, void *ptr, int B, int S, int nh) {
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }   // outputs stored by sectors
 template <typename... T>
 bool aligned4(const T *...p) {
   return (((reinterpret_cast<uintptr_t>(p) & 3u) == 0) && ...);
@@ -795,7 +796,7 @@ xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope,
                               int dv, float scale, void *o, float *lse, void *stream) {
   if (!q || !kv || !k_rope || !o || !lse) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_latent(B, S, nh, dn, dr, dv, scale));
-  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) || !aligned4(lse)) return XATTN_ERR_MISALIGNED;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned32(o) || !aligned4(lse)) return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));
   LatentArgs a = {};
@@ -815,8 +816,8 @@ xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope,
                               void *dkv, void *dk_rope, void *stream) {
   if (!q || !kv || !k_rope || !o || !dO || !lse || !dq || !dkv || !dk_rope) return XATTN_ERR_NULL_PTR;
   XATTN_TRY(check_latent(B, S, nh, dn, dr, dv, scale));
-  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) ||
-      !aligned16(dkv) || !aligned16(dk_rope) || !aligned4(lse))
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o) || !aligned16(dO) || !aligned32(dq) ||
+      !aligned32(dkv) || !aligned16(dk_rope) || !aligned4(lse))
     return XATTN_ERR_MISALIGNED;
   DeviceInfo *dev = nullptr;
   XATTN_TRY(bf16_device(&dev));

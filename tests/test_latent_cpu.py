@@ -25,8 +25,8 @@ def _fwd(lib, q=16, kv=32, rope=48, B=1, S=5, nh=3, dn=64, dr=32, dv=64, scale=0
     return f(q, kv, rope, B, S, nh, dn, dr, dv, scale, o, lse, None)
 
 
-def _bwd(lib, q=16, kv=32, rope=48, o=64, dO=80, lse=96, B=1, S=5, nh=3, dn=64, dr=32, dv=64, scale=0.1, dq=112,
-         dkv=128, drope=144):
+def _bwd(lib, q=16, kv=32, rope=48, o=64, dO=80, lse=96, B=1, S=5, nh=3, dn=64, dr=32, dv=64, scale=0.1, dq=128,
+         dkv=160, drope=144):
     f = lib.xattn_latent_bwd
     f.restype, f.argtypes = I, [P] * 6 + [I] * 6 + [F] + [P] * 4
     return f(q, kv, rope, o, dO, lse, B, S, nh, dn, dr, dv, scale, dq, dkv, drope, None)
@@ -38,6 +38,8 @@ def test_expanded_checks(lib, call, more):
         assert call(lib, **{name: None}) == 1, name
     for name in ("q", "kv", "rope", *more):
         assert call(lib, **{name: 24}) == 5, name
+    for name in ("o",) if call is _fwd else ("dq", "dkv"):
+        assert call(lib, **{name: 48}) == 5, name                         # written by whole 32-byte sectors
     assert call(lib, lse=98) == 5
     for name in ("B", "S", "nh", "dn", "dr", "dv"):
         assert call(lib, **{name: 0}) == 2, name
