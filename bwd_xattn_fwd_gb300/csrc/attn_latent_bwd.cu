@@ -8,8 +8,8 @@
 //      head are one contiguous copy.
 //   2. latent_dkv_kernel (key-stationary): a unit is (batch, head, 128 keys); dV [128, dv] and dK [128, dn + dr] stay in TMEM,
 //      320 of its 512 columns, so queries come in tiles of 64 and three 64-column places hold the scores: S^T(t) in place
-//      t % 2 (P^T over it), dP^T(t) in the third (dS^T over it). S^T(t + 1) is issued before dV(t), so it runs while the
-//      warps work on P and dS (two tiles ahead it waited for a stage of the ring). A score product of 64 columns takes 48 cycles a K step where its arithmetic is 32 (shared memory
+//      t % 2 (P^T over it), dP^T(t) in the third (dS^T over it). S^T is issued two tiles ahead, so it runs while the warps
+//      work on P and dS. A score product of 64 columns takes 48 cycles a K step where its arithmetic is 32 (shared memory
 //      feeds 128 + 64 rows); with 128 columns the places would not fit. Per 64 queries 576 (S) + 384 (dP) + 256 (dV) + 384 (dK).
 //   3. latent_dq_kernel (query-stationary, as attn_bwd_dq_sm103.cu): S and dP once more, dQ += dS K in TMEM over the key
 //      tiles. dQ [., dn + dr] does not fit beside dV and dK, and summed with atomics it would not be reproducible.
@@ -32,47 +32,57 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok);
 }
 
-// Sixteen lanes a row (b, i, h) of o and dO, eight numbers each; kRowsEach rows a group of lanes, their loads together. Rows
-// S .. S_pad - 1 get a weight of 0 (their Q and dO are read as zeros).
-constexpr int kRowsEach = 4, kRowsBlock = 256 / 16 * kRowsEach;
-__global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a) {
+// A block takes 32 positions of up to 8 heads: sixteen lanes a row (b, i, h) of o and dO, eight numbers each, and the results by
+// way of shared memory, so that a head's 32 are written together (one by one, each to a line of its own, they took longer than
+// the reads). Rows S .. S_pad - 1 get a weight of 0 (their Q and dO are read as zeros).
+constexpr int kRowsPos = 32, kRowsHeads = 8;
+__global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a, int head_blocks) {
+  __shared__ float2 sums[kRowsHeads][kRowsPos + 1];
   grid_dep_launch();
   grid_dep_wait();
-  const int part = threadIdx.x & 15, group = threadIdx.x >> 4, S_pad = padded_rows(a.S);
-  const unsigned nh = a.nh;
-  const size_t rows = static_cast<size_t>(a.B) * S_pad * nh;
-  size_t row = static_cast<size_t>(blockIdx.x) * kRowsBlock + group, from[kRowsEach], to[kRowsEach];
-  bool live[kRowsEach], real[kRowsEach];
-  uint4 x[kRowsEach], y[kRowsEach];
+  const int part = threadIdx.x & 15, group = threadIdx.x >> 4, S_pad = padded_rows(a.S), tiles = S_pad / kRowsPos;
+  const unsigned hb = blockIdx.x % head_blocks, rest = blockIdx.x / head_blocks;
+  const int b = static_cast<int>(rest / tiles), i0 = static_cast<int>(rest - static_cast<unsigned>(b) * tiles) * kRowsPos;
+  const int h0 = static_cast<int>(hb) * kRowsHeads;
+  constexpr int kOnce = 4;                                           // rows a group of lanes has in flight
+#pragma unroll 1
+  for (int r0 = group; r0 < kRowsPos * kRowsHeads; r0 += 16 * kOnce) {
+    uint4 x[kOnce], y[kOnce];
+    float lse[kOnce];
 #pragma unroll
-  for (int e = 0; e < kRowsEach; ++e, row += 16) {
-    const size_t rest = row / nh, b = rest / S_pad;
-    const int h = static_cast<int>(row - rest * nh), i = static_cast<int>(rest - b * S_pad);
-    live[e] = row < rows;
-    real[e] = live[e] && i < a.S;
-    to[e] = (b * nh + h) * S_pad + i;
-    from[e] = (b * a.S + i) * nh + h;
-    x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
-    if (real[e] && 8 * part < a.dv) {
-      x[e] = *reinterpret_cast<const uint4 *>(a.o + from[e] * a.dv + 8 * part);
-      y[e] = *reinterpret_cast<const uint4 *>(a.dO + from[e] * a.dv + 8 * part);
+    for (int e = 0; e < kOnce; ++e) {
+      const int r = r0 + 16 * e, i = i0 + r / kRowsHeads, h = h0 + r % kRowsHeads;
+      x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
+      lse[e] = INFINITY;
+      if (i >= a.S || h >= a.nh) continue;
+      const size_t from = (static_cast<size_t>(b) * a.S + i) * a.nh + h;
+      lse[e] = a.lse[from];
+      if (8 * part < a.dv) {
+        x[e] = *reinterpret_cast<const uint4 *>(a.o + from * a.dv + 8 * part);
+        y[e] = *reinterpret_cast<const uint4 *>(a.dO + from * a.dv + 8 * part);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kOnce; ++e) {
+      float dot = 0.f;
+      auto add = [&](uint32_t u, uint32_t v) {
+        dot = fmaf(bf16lo_to_f32(u), bf16lo_to_f32(v), dot);
+        dot = fmaf(bf16hi_to_f32(u), bf16hi_to_f32(v), dot);
+      };
+      add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
+#pragma unroll
+      for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      const int r = r0 + 16 * e;
+      if (part == 0) sums[r % kRowsHeads][r / kRowsHeads] = make_float2(-lse[e] * kLog2e, -dot);
     }
   }
-#pragma unroll
-  for (int e = 0; e < kRowsEach; ++e) {
-    float dot = 0.f;
-    auto add = [&](uint32_t u, uint32_t v) {
-      dot = fmaf(bf16lo_to_f32(u), bf16lo_to_f32(v), dot);
-      dot = fmaf(bf16hi_to_f32(u), bf16hi_to_f32(v), dot);
-    };
-    add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
-#pragma unroll
-    for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    if (live[e] && part == 0) {
-      a.nlse[to[e]] = real[e] ? -a.lse[from[e]] * kLog2e : -INFINITY;
-      a.nD[to[e]] = -dot;
-    }
-  }
+  __syncthreads();
+  const int h = threadIdx.x >> 5, i = threadIdx.x & 31;
+  if (h0 + h >= a.nh) return;
+  const size_t to = (static_cast<size_t>(b) * a.nh + h0 + h) * S_pad + i0 + i;
+  const float2 v = sums[h][i];
+  a.nlse[to] = v.x;
+  a.nD[to] = v.y;
 }
 
 // NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS).
@@ -85,14 +95,14 @@ struct DkvLayout {
   static constexpr uint32_t kdO = kQ + kStages * (NS + 1) * kQuerySub;
   static constexpr uint32_t kRows = kdO + kStages * NS * kQuerySub;  // stages of -LSE log2 e and -D
   static constexpr uint32_t kBars = kRows + kStages * 2 * kQRows * 4;
-  static constexpr int kNumBars = 2 * kStages + 13;
+  static constexpr int kNumBars = 2 * kStages + 9;
   static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
   static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
 };
 
-// Warps: 0 TMA; 1 issuer of S^T and dV (and TMEM owner); 3 issuer of dP^T and dK; 4-7 P^T; 8-11 dS^T; a thread is a key row.
+// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 P^T; 8-11 dS^T; a thread is a key row.
 // TMEM: dV [0, 128) | dK [128, 320), its shared part from 256 on | S^T places [320, 384), [384, 448) | dP^T [448, 512).
 template <int NS>
 __global__ void __maxnreg__(168)
@@ -129,7 +139,6 @@ __global__ void __maxnreg__(168)
                  ds_full = bar(kB + 4);
   auto s_full = [&](int x) { return bar(kB + 5 + x); };
   auto p_full = [&](int x) { return bar(kB + 7 + x); };
-  auto p_free = [&](int x) { return bar(kB + 9 + x); };               // the dS warps have read P^T
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
@@ -138,17 +147,16 @@ __global__ void __maxnreg__(168)
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 2);
+      mbar_init(q_empty(s), 1);
     }
     mbar_init(kv_full, 1);
-    mbar_init(acc_done, 2);
+    mbar_init(acc_done, 1);
     mbar_init(acc_free, 256);
     mbar_init(dp_full, 1);
     mbar_init(ds_full, 128);
     for (int x = 0; x < 2; ++x) {
       mbar_init(s_full(x), 1);
       mbar_init(p_full(x), 128);
-      mbar_init(p_free(x), 128);
     }
     fence_mbar_init();
     tma_prefetch_desc(&mq);
@@ -221,17 +229,22 @@ __global__ void __maxnreg__(168)
     if (units > 0) mbar_drain(kv_full, (units - 1) & 1, ctl);
     for (int r = max(g - kStages, 0); r < g; ++r) mbar_drain(q_full(r % kStages), (r / kStages) & 1, ctl);
   } else if (warp == 1) {
-    // ---------------- issuer of S^T and dV ----------------
+    // ---------------- MMA issuer ----------------
+    // One thread, so one order: dV(t), dK(t), dP^T(t + 1), S^T(t + 2). dK -> dP^T -> dS^T -> dK is the longest chain (dP^T and
+    // dS^T have one place), and S^T, dV fill the time that the dS warps take. (With two issuers the pipe took S^T between dK
+    // and dP^T: 2430 cycles a tile.)
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
-    const uint32_t idesc_dv = idesc_bf16_f32(128, dv, false, true);
+    const uint32_t idesc_dv = idesc_bf16_f32(128, dv, false, true), idesc_dk = idesc_bf16_f32(128, dn, false, true),
+                   idesc_dr = idesc_bf16_f32(128, dr, false, true);
     const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
-    const uint64_t ddO = smem_desc(sdO, kQuerySub, 1024, kSwizzle128);   // MN-major: 64 columns a sub-tile
-    auto scores = [&](int g) -> bool {                                   // S^T of tile g (over all units)
-      const int s = g % kStages;
-      if (!warp_wait(q_full(s), (g / kStages) & 1, ctl) || !warp_wait(p_free(g & 1), ((g >> 1) & 1) ^ 1, ctl)) return false;
-      tc_fence_after();
+    const uint64_t dV = smem_desc(sV, 16, 1024, kSwizzle128), ddO = smem_desc(sdO, 16, 1024, kSwizzle128);
+    const uint64_t dQt = smem_desc(sQ, kQuerySub, 1024, kSwizzle128);    // MN-major: 64 columns a sub-tile
+    const uint64_t ddOt = smem_desc(sdO, kQuerySub, 1024, kSwizzle128);
+    auto landed = [&](int g) { return warp_wait(q_full(g % kStages), (g / kStages) & 1, ctl); };
+    // S^T of tile g (over all units); its place's P^T and the dS warps' reading of it lie two tiles back.
+    auto issue_s = [&](int g) {
       if (elect_one()) {
-        const uint64_t q = dQ + s * (NS + 1) * (kQuerySub >> 4);
+        const uint64_t q = dQ + (g % kStages) * (NS + 1) * (kQuerySub >> 4);
         const uint32_t d = tS(g & 1);
 #pragma unroll
         for (int c = 0; c < NS; ++c)
@@ -245,48 +258,10 @@ __global__ void __maxnreg__(168)
         mma_commit(s_full(g & 1));
       }
       __syncwarp();
-      return true;
     };
-    bool ok = true;
-    int units = 0, g = 0;
-#pragma unroll 1
-    for (int k = 0; ok; ++k) {
-      const int u = unit_at(k);
-      if (u >= num_units) break;
-      XATTN_DKV_UNIT(u);
-      ok = warp_wait(kv_full, units & 1, ctl) && scores(g);
-      // The first dV overwrites the accumulator, which the unit before has read.
-      if (!ok || !warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
-#pragma unroll 1
-      for (int t = 0; t < T; ++t, ++g) {
-        const int s = g % kStages;
-        if ((t + 1 < T && !scores(g + 1)) || !warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t o = ddO + s * NS * (kQuerySub >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kQRows / 16; ++kk)
-            mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(q_empty(s));
-          if (t + 1 == T) mma_commit(acc_done);
-        }
-        __syncwarp();
-      }
-      ++units;
-    }
-    if (ok && units > 0) mbar_drain(acc_done, (units - 1) & 1, ctl);
-  } else if (warp == 3) {
-    // ---------------- issuer of dP^T and dK ----------------
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
-    const uint32_t idesc_dk = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
-    const uint64_t dV = smem_desc(sV, 16, 1024, kSwizzle128), ddO = smem_desc(sdO, 16, 1024, kSwizzle128);
-    const uint64_t dQ = smem_desc(sQ, kQuerySub, 1024, kSwizzle128);     // MN-major
-    auto scores = [&](int g) -> bool {
-      const int s = g % kStages;
-      if (!warp_wait(q_full(s), (g / kStages) & 1, ctl)) return false;
-      tc_fence_after();
+    auto issue_dp = [&](int g) {
       if (elect_one()) {
-        const uint64_t o = ddO + s * NS * (kQuerySub >> 4);
+        const uint64_t o = ddO + (g % kStages) * NS * (kQuerySub >> 4);
 #pragma unroll
         for (int c = 0; c < NS; ++c)
 #pragma unroll
@@ -296,7 +271,6 @@ __global__ void __maxnreg__(168)
         mma_commit(dp_full);
       }
       __syncwarp();
-      return true;
     };
     bool ok = true;
     int units = 0, g = 0;
@@ -305,16 +279,33 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       XATTN_DKV_UNIT(u);
-      // (dP^T's place: the dK before, issued by this thread, reads dS^T there first, and the dS warps had read dP^T.)
-      ok = warp_wait(kv_full, units & 1, ctl) && scores(g);
-      if (!ok || !warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
+      if (!warp_wait(kv_full, units & 1, ctl) || !landed(g)) break;
+      tc_fence_after();
+      issue_s(g);
+      issue_dp(g);
+      if (T > 1) {
+        if (!landed(g + 1)) break;
+        tc_fence_after();
+        issue_s(g + 1);
+      }
+      // The first dV and dK overwrite the accumulators, which the unit before has read.
+      if (!warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
         const int s = g % kStages;
+        if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t o = ddOt + s * NS * (kQuerySub >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kQRows / 16; ++kk)
+            mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
+        }
+        __syncwarp();
         if (!warp_wait(ds_full, g & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t q = dQ + s * (NS + 1) * (kQuerySub >> 4);
+          const uint64_t q = dQt + s * (NS + 1) * (kQuerySub >> 4);
 #pragma unroll
           for (int kk = 0; kk < kQRows / 16; ++kk) {
             mma_ts(tdK, tdP + kk * 8, q + kk * 128, idesc_dk, (t > 0 || kk > 0) ? 1u : 0u);
@@ -324,7 +315,14 @@ __global__ void __maxnreg__(168)
           if (t + 1 == T) mma_commit(acc_done);
         }
         __syncwarp();
-        if (t + 1 < T && !scores(g + 1)) { ok = false; break; }
+        if (t + 1 < T) {
+          issue_dp(g + 1);                                          // (tile g + 1 has landed: its S^T went before)
+          if (t + 2 < T) {
+            if (!landed(g + 2)) { ok = false; break; }
+            tc_fence_after();
+            issue_s(g + 2);
+          }
+        }
       }
       ++units;
     }
@@ -397,8 +395,6 @@ __global__ void __maxnreg__(168)
           tmem_wait_ld();
           reg_fence<64>(r);
           reg_fence<32>(p);
-          tc_fence_before();
-          mbar_arrive(p_free(g & 1));
           const float4 *nd = reinterpret_cast<const float4 *>(smem + L::kRows + (g % kStages) * 2 * kQRows * 4 + kQRows * 4);
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
@@ -423,16 +419,18 @@ __global__ void __maxnreg__(168)
       const int j = n * kTileRows + row;
       const size_t tok = (static_cast<size_t>(b) * S + j) * nh + h;
       XATTN_DCHECK(j >= S || tok < static_cast<size_t>(a.B) * S * nh, a.status);
+      // 32 columns at once (they may end after 16: the rest is read and dropped).
       auto put = [&](uint32_t from, int cols, float mult, __nv_bfloat16 *to) {
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 16) {
-          uint32_t v[16];
-          tmem_ld_x16(from + lane_off + c, v);
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t r[32];
+          tmem_ld_x32(from + lane_off + c, r);
           tmem_wait_ld();
-          reg_fence<16>(v);
+          reg_fence<32>(r);
+          auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(r[e]) * mult, __uint_as_float(r[e + 1]) * mult); };
           if (j < S) {
-            auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * mult, __uint_as_float(v[e + 1]) * mult); };
             store_32(to + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
+            if (c + 32 <= cols) store_32(to + c + 16, pair(16), pair(18), pair(20), pair(22), pair(24), pair(26), pair(28), pair(30));
           }
           __syncwarp();
         }
@@ -780,8 +778,9 @@ void latent_bwd_workspace_carve(LatentArgs &a, void *base) {
 
 cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
                               cudaStream_t stream) {
-  const size_t rows = static_cast<size_t>(a.B) * a.nh * padded_rows(a.S);
-  cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>((rows + kRowsBlock - 1) / kRowsBlock), 256, 0, stream, a);
+  const int head_blocks = (a.nh + kRowsHeads - 1) / kRowsHeads;
+  cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>(a.B) * (padded_rows(a.S) / kRowsPos) * head_blocks,
+                               256, 0, stream, a, head_blocks);
   if (err != cudaSuccess) return err;
   err = a.dn <= 64 && a.dv <= 64 ? launch_latent_bwd_ns<1>(q64, q128, a, sms, stream)
                                  : launch_latent_bwd_ns<2>(q64, q128, a, sms, stream);
