@@ -95,7 +95,7 @@ struct DkvLayout {
   static constexpr uint32_t kdO = kQ + kStages * (NS + 1) * kQuerySub;
   static constexpr uint32_t kRows = kdO + kStages * NS * kQuerySub;  // stages of -LSE log2 e and -D
   static constexpr uint32_t kBars = kRows + kStages * 2 * kQRows * 4;
-  static constexpr int kNumBars = 2 * kStages + 9;
+  static constexpr int kNumBars = 2 * kStages + 12;
   static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
@@ -135,10 +135,10 @@ __global__ void __maxnreg__(168)
   auto q_full = [&](int s) { return bar(s); };                       // Q, dO and the rows' numbers of a tile
   auto q_empty = [&](int s) { return bar(kStages + s); };
   constexpr int kB = 2 * kStages;
-  const uint32_t kv_full = bar(kB), acc_done = bar(kB + 1), acc_free = bar(kB + 2), dp_full = bar(kB + 3),
-                 ds_full = bar(kB + 4);
-  auto s_full = [&](int x) { return bar(kB + 5 + x); };
-  auto p_full = [&](int x) { return bar(kB + 7 + x); };
+  const uint32_t k_full = bar(kB), v_full = bar(kB + 1), k_empty = bar(kB + 2), v_empty = bar(kB + 3), acc_done = bar(kB + 4),
+                 acc_free = bar(kB + 5), dp_full = bar(kB + 6), ds_full = bar(kB + 7);
+  auto s_full = [&](int x) { return bar(kB + 8 + x); };
+  auto p_full = [&](int x) { return bar(kB + 10 + x); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
@@ -149,7 +149,10 @@ __global__ void __maxnreg__(168)
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1);
     }
-    mbar_init(kv_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(v_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_empty, 1);
     mbar_init(acc_done, 1);
     mbar_init(acc_free, 256);
     mbar_init(dp_full, 1);
@@ -185,7 +188,7 @@ __global__ void __maxnreg__(168)
                    a.status);
       tma_load_4d_elect(dst, map, full, col, head, row0, bb);
     };
-    int g = 0, units = 0;
+    int g = 0, units = 0, units_k = 0;
     bool ok = true;
 #pragma unroll 1
     for (int k = 0; ok; ++k) {
@@ -207,16 +210,20 @@ __global__ void __maxnreg__(168)
         ++g;
         return true;
       };
-      // The first tiles do not wait for the unit before, whose K and V are still read.
-      const int pre = T < kStages ? T : kStages;
-      for (int t = 0; ok && t < pre; ++t) ok = load_tile(t);
-      if (!ok || !warp_wait(acc_done, (units & 1) ^ 1, ctl)) break;
-      mbar_expect_tx_elect(kv_full, (k_subs + 1 + v_subs) * kKeySub);
-      for (int c = 0; c < k_subs; ++c) load(sK + c * kKeySub, &mkv, kv_full, 64 * c, h, n * kTileRows, b);
-      load(sK + NS * kKeySub, &mrope, kv_full, 0, 0, n * kTileRows, b);
-      for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, kv_full, dn + 64 * c, h, n * kTileRows, b);
+      // In the order in which the unit before frees the places: K's with its last S^T, V's with its last dP^T (before its sums
+      // are written), a stage with each tile.
+      ok = load_tile(0) && warp_wait(k_empty, (units & 1) ^ 1, ctl);
+      if (!ok) break;
+      mbar_expect_tx_elect(k_full, (k_subs + 1) * kKeySub);
+      for (int c = 0; c < k_subs; ++c) load(sK + c * kKeySub, &mkv, k_full, 64 * c, h, n * kTileRows, b);
+      load(sK + NS * kKeySub, &mrope, k_full, 0, 0, n * kTileRows, b);
+      ++units_k;
+      ok = (T < 2 || load_tile(1)) && warp_wait(v_empty, (units & 1) ^ 1, ctl);
+      if (!ok) break;
+      mbar_expect_tx_elect(v_full, v_subs * kKeySub);
+      for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, v_full, dn + 64 * c, h, n * kTileRows, b);
       ++units;
-      for (int t = pre; ok && t < T; ++t) ok = load_tile(t);
+      for (int t = 2; ok && t < T; ++t) ok = load_tile(t);
       // The next unit's K and V into L2: they are fetched when this one's products have ended, with nothing to do meanwhile.
       const int u1 = unit_at(k + 1);
       if (ok && u1 < num_units) {
@@ -226,7 +233,8 @@ __global__ void __maxnreg__(168)
       }
     }
     // Every copy in flight has landed before the CTA can exit.
-    if (units > 0) mbar_drain(kv_full, (units - 1) & 1, ctl);
+    if (units_k > 0) mbar_drain(k_full, (units_k - 1) & 1, ctl);
+    if (units > 0) mbar_drain(v_full, (units - 1) & 1, ctl);
     for (int r = max(g - kStages, 0); r < g; ++r) mbar_drain(q_full(r % kStages), (r / kStages) & 1, ctl);
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -242,7 +250,8 @@ __global__ void __maxnreg__(168)
     const uint64_t ddOt = smem_desc(sdO, kQuerySub, 1024, kSwizzle128);
     auto landed = [&](int g) { return warp_wait(q_full(g % kStages), (g / kStages) & 1, ctl); };
     // S^T of tile g (over all units); its place's P^T and the dS warps' reading of it lie two tiles back.
-    auto issue_s = [&](int g) {
+    auto issue_s = [&](int g, bool last) {
+
       if (elect_one()) {
         const uint64_t q = dQ + (g % kStages) * (NS + 1) * (kQuerySub >> 4);
         const uint32_t d = tS(g & 1);
@@ -256,10 +265,12 @@ __global__ void __maxnreg__(168)
         for (int kk = 0; kk < 4; ++kk)
           if (kk < dr_steps) mma_ss(d, dK + NS * (kKeySub >> 4) + kk * 2, q + NS * (kQuerySub >> 4) + kk * 2, idesc_s, 1u);
         mma_commit(s_full(g & 1));
+        if (last) mma_commit(k_empty);
       }
       __syncwarp();
     };
-    auto issue_dp = [&](int g) {
+    auto issue_dp = [&](int g, bool last) {
+
       if (elect_one()) {
         const uint64_t o = ddO + (g % kStages) * NS * (kQuerySub >> 4);
 #pragma unroll
@@ -269,6 +280,7 @@ __global__ void __maxnreg__(168)
             if (4 * c + kk < dv_steps)
               mma_ss(tdP, dV + c * (kKeySub >> 4) + kk * 2, o + c * (kQuerySub >> 4) + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
         mma_commit(dp_full);
+        if (last) mma_commit(v_empty);
       }
       __syncwarp();
     };
@@ -279,14 +291,16 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       XATTN_DKV_UNIT(u);
-      if (!warp_wait(kv_full, units & 1, ctl) || !landed(g)) break;
+      if (!warp_wait(k_full, units & 1, ctl) || !landed(g)) break;
       tc_fence_after();
-      issue_s(g);
-      issue_dp(g);
+      issue_s(g, T == 1);
+      if (!warp_wait(v_full, units & 1, ctl)) break;
+      tc_fence_after();
+      issue_dp(g, T == 1);
       if (T > 1) {
         if (!landed(g + 1)) break;
         tc_fence_after();
-        issue_s(g + 1);
+        issue_s(g + 1, T == 2);
       }
       // The first dV and dK overwrite the accumulators, which the unit before has read.
       if (!warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
@@ -316,11 +330,11 @@ __global__ void __maxnreg__(168)
         }
         __syncwarp();
         if (t + 1 < T) {
-          issue_dp(g + 1);                                          // (tile g + 1 has landed: its S^T went before)
+          issue_dp(g + 1, t + 2 == T);                              // (tile g + 1 has landed: its S^T went before)
           if (t + 2 < T) {
             if (!landed(g + 2)) { ok = false; break; }
             tc_fence_after();
-            issue_s(g + 2);
+            issue_s(g + 2, t + 3 == T);
           }
         }
       }
@@ -413,7 +427,7 @@ __global__ void __maxnreg__(168)
           mbar_arrive(ds_full);
         }
       }
-      // The unit's sums: the P warps write dV, the dS warps dK and this head's part of k_rope's gradient.
+      // The unit's sums: the P warps write dV, the dS warps dK.
       if (!ok || !warp_wait(acc_done, units & 1, ctl)) break;
       tc_fence_after();
       const int j = n * kTileRows + row;
@@ -435,23 +449,21 @@ __global__ void __maxnreg__(168)
           __syncwarp();
         }
       };
-      if (p_side) {
-        put(tdV, dv, 1.f, a.dkv + tok * (dn + dv) + dn);
-      } else {
-        put(tdK, dn, a.scale, a.dkv + tok * (dn + dv));
+      if (p_side) put(tdV, dv, 1.f, a.dkv + tok * (dn + dv) + dn);
+      else put(tdK, dn, a.scale, a.dkv + tok * (dn + dv));
+      // This head's part of k_rope's gradient, every second 16 columns a group.
 #pragma unroll 1
-        for (int c = 0; c < dr; c += 16) {
-          uint32_t v[16];
-          tmem_ld_x16(tdKr + lane_off + c, v);
-          tmem_wait_ld();
-          reg_fence<16>(v);
-          if (j < S) {
-            float *dst = a.rope_parts + tok * dr + c;
-            store_32(dst, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-            store_32(dst + 8, v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]);
-          }
-          __syncwarp();
+      for (int c = p_side ? 0 : 16; c < dr; c += 32) {
+        uint32_t v[16];
+        tmem_ld_x16(tdKr + lane_off + c, v);
+        tmem_wait_ld();
+        reg_fence<16>(v);
+        if (j < S) {
+          float *dst = a.rope_parts + tok * dr + c;
+          store_32(dst, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+          store_32(dst + 8, v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]);
         }
+        __syncwarp();
       }
       tc_fence_before();
       mbar_arrive(acc_free);
@@ -468,29 +480,31 @@ __global__ void __maxnreg__(168)
 }
 #undef XATTN_DKV_UNIT
 
-// dQ: a CTA per (batch, head, 128 queries). Q and dO stay; K in two stages, V in one (it is read only by dP, early in a
-// tile's step, and there is no room for more).
+// dQ: a CTA per (batch, head, 128 queries). Q stays in shared memory and dO in TMEM (the A operand of dP), which leaves room
+// for three stages of K: K(n) is needed from S(n) to dQ(n), and with two the next scores waited for it. V has one stage: only
+// dP(n) reads it.
 template <int NS>
 struct LatentDqLayout {
+  static constexpr int kStages = 3;
   static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kdO = kQ + (NS + 1) * kKeySub;
-  static constexpr uint32_t kK = kdO + NS * kKeySub;
-  static constexpr uint32_t kV = kK + 2 * (NS + 1) * kKeySub;
+  static constexpr uint32_t kK = kQ + (NS + 1) * kKeySub;
+  static constexpr uint32_t kV = kK + kStages * (NS + 1) * kKeySub;
   static constexpr uint32_t kBars = kV + NS * kKeySub;
-  static constexpr int kNumBars = 13;
+  static constexpr int kNumBars = 2 * kStages + 9;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
   static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
 };
 
-// Warps: 0 TMA; 1 issuer of S and dP (and TMEM owner); 3 issuer of dQ; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
-// TMEM: S [0, 128) | dP [128, 256) | dS bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448 on.
+// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
+// TMEM: S [0, 128) | dP [128, 256), dS bf16 over [128, 160) and [192, 224) | dO bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448.
 template <int NS>
 __global__ void __maxnreg__(168)
     latent_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
-                     const __grid_constant__ CUtensorMap mrope, const __grid_constant__ CUtensorMap mdo, const LatentArgs a) {
+                     const __grid_constant__ CUtensorMap mrope, const LatentArgs a) {
   using L = LatentDqLayout<NS>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t latent_dq_smem[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dq_smem) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -501,25 +515,25 @@ __global__ void __maxnreg__(168)
   const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh;
   const int m = num_m - 1 - static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) % BH;
   const int b = bh / nh, h = bh - b * nh, T = m + 1;                 // key tiles
-  const uint32_t sQ = smem_u32(smem + L::kQ), sdO = smem_u32(smem + L::kdO), sK = smem_u32(smem + L::kK),
-                 sV = smem_u32(smem + L::kV), bar0 = smem_u32(smem + L::kBars);
+  const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV),
+                 bar0 = smem_u32(smem + L::kBars);
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   auto k_full = [&](int s) { return bar(s); };
-  auto k_empty = [&](int s) { return bar(2 + s); };
-  const uint32_t v_full = bar(4), v_empty = bar(5), q_full = bar(6), s_full = bar(7), s_free = bar(8), dp_full = bar(9),
-                 dp_free = bar(10), ds_full = bar(11), dq_done = bar(12);
+  auto k_empty = [&](int s) { return bar(kStages + s); };
+  constexpr int kB = 2 * kStages;
+  const uint32_t v_full = bar(kB), v_empty = bar(kB + 1), q_full = bar(kB + 2), s_full = bar(kB + 3), dp_full = bar(kB + 4),
+                 dq_done = bar(kB + 5), s_free = bar(kB + 6), ds_full = bar(kB + 7), do_full = bar(kB + 8);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), (i == 8 || i == 10 || i == 11) ? 256 : 1);
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i >= kB + 6 ? 256 : 1);
     fence_mbar_init();
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mkv);
     tma_prefetch_desc(&mrope);
-    tma_prefetch_desc(&mdo);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), 512);
@@ -531,7 +545,7 @@ __global__ void __maxnreg__(168)
   grid_dep_launch();
   grid_dep_wait();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
-  const uint32_t tS = tmem, tdP = tmem + 128, tdS = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
+  const uint32_t tS = tmem, tdP = tmem + 128, tdO = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -539,14 +553,13 @@ __global__ void __maxnreg__(168)
       XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && dst >= sQ && dst + kKeySub <= bar0, a.status);
       tma_load_4d_elect(dst, map, full, col, head, row0, b);
     };
-    mbar_expect_tx_elect(q_full, (k_subs + 1 + v_subs) * kKeySub);
+    mbar_expect_tx_elect(q_full, (k_subs + 1) * kKeySub);
     for (int c = 0; c < k_subs; ++c) load(sQ + c * kKeySub, &mq, q_full, 64 * c, h, m * kTileRows);
     load(sQ + NS * kKeySub, &mq, q_full, dn, h, m * kTileRows);
-    for (int c = 0; c < v_subs; ++c) load(sdO + c * kKeySub, &mdo, q_full, 64 * c, h, m * kTileRows);
     int issued_k = 0, issued_v = 0;
     for (int n = 0; n < T; ++n) {
-      const int s = n & 1;
-      if (!warp_wait(k_empty(s), ((n >> 1) & 1) ^ 1, ctl)) break;
+      const int s = n % kStages;
+      if (!warp_wait(k_empty(s), ((n / kStages) & 1) ^ 1, ctl)) break;
       mbar_expect_tx_elect(k_full(s), (k_subs + 1) * kKeySub);
       const uint32_t dk = sK + s * (NS + 1) * kKeySub;
       for (int c = 0; c < k_subs; ++c) load(dk + c * kKeySub, &mkv, k_full(s), 64 * c, h, n * kTileRows);
@@ -559,16 +572,20 @@ __global__ void __maxnreg__(168)
     }
     // Every copy in flight has landed before the CTA can exit.
     mbar_drain(q_full, 0, ctl);
-    for (int n = max(issued_k - 2, 0); n < issued_k; ++n) mbar_drain(k_full(n & 1), (n >> 1) & 1, ctl);
+    for (int n = max(issued_k - kStages, 0); n < issued_k; ++n) mbar_drain(k_full(n % kStages), (n / kStages) & 1, ctl);
     if (issued_v > 0) mbar_drain(v_full, (issued_v - 1) & 1, ctl);
   } else if (warp == 1) {
-    // ---------------- issuer of S and dP ----------------
+    // ---------------- MMA issuer: S(n + 1) before dQ(n), dP(n + 1) behind it (dS(n) lies in dP's place) ----------------
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-    bool scored = false;
+    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
     constexpr uint32_t kSubDesc = kKeySub >> 4;
-    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128), ddO = smem_desc(sdO, 16, 1024, kSwizzle128);
+    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
     const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dV = smem_desc(sV, 16, 1024, kSwizzle128);
-    auto issue_s = [&](int s) {
+    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
+    auto scores = [&](int n) -> bool {
+      const int s = n % kStages;
+      if (!warp_wait(k_full(s), (n / kStages) & 1, ctl) || !warp_wait(s_free, (n & 1) ^ 1, ctl)) return false;
+      tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = dK + s * (NS + 1) * kSubDesc;
 #pragma unroll
@@ -582,56 +599,46 @@ __global__ void __maxnreg__(168)
         mma_commit(s_full);
       }
       __syncwarp();
+      return true;
     };
-    auto issue_dp = [&]() {
+    auto issue_dp = [&](int n) -> bool {
+      if (!warp_wait(v_full, n & 1, ctl)) return false;
+      tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < NS; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            if (4 * c + kk < dv_steps) mma_ss(tdP, ddO + c * kSubDesc + kk * 2, dV + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+            if (4 * c + kk < dv_steps) mma_ts(tdP, tdO + 32 * c + 8 * kk, dV + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
         mma_commit(dp_full);
         mma_commit(v_empty);
       }
       __syncwarp();
+      return true;
     };
-    // The next tile's products as soon as the compute warps have read this tile's.
-    bool ok = warp_wait(q_full, 0, ctl);
+    int done = 0;
+    bool ok = warp_wait(q_full, 0, ctl) && scores(0) && warp_wait(do_full, 0, ctl) && issue_dp(0);
 #pragma unroll 1
     for (int n = 0; ok && n < T; ++n) {
-      if (!warp_wait(k_full(n & 1), (n >> 1) & 1, ctl) || !warp_wait(s_free, (n & 1) ^ 1, ctl)) break;
+      const int s = n % kStages;
+      if ((n + 1 < T && !scores(n + 1)) || !warp_wait(ds_full, n & 1, ctl)) break;
       tc_fence_after();
-      issue_s(n & 1);
-      if (!warp_wait(v_full, n & 1, ctl) || !warp_wait(dp_free, (n & 1) ^ 1, ctl)) break;
-      tc_fence_after();
-      issue_dp();
-      if (n + 1 == T) scored = true;
-    }
-    if (scored) mbar_drain(dp_full, (T - 1) & 1, ctl);
-  } else if (warp == 3) {
-    // ---------------- issuer of dQ += dS K (apart, so that it does not wait behind scores whose K has not landed) --------
-    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
-    constexpr uint32_t kSubDesc = kKeySub >> 4;
-    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
-    int done = 0;
-#pragma unroll 1
-    for (int n = 0; n < T; ++n) {
-      const int s = n & 1;
-      if (!warp_wait(ds_full, n & 1, ctl)) break;
-      tc_fence_after();
-      if (elect_one()) {
+      if (elect_one()) {                                            // dQ += dS K_n
         const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
 #pragma unroll
         for (int kk = 0; kk < kTileRows / 16; ++kk) {
-          mma_ts(tdQ, tdS + kk * 8, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
-          mma_ts(tdQr, tdS + kk * 8, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
+          const uint32_t ds = tdP + (kk / 4) * 64 + (kk % 4) * 8;
+          mma_ts(tdQ, ds, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
+          mma_ts(tdQr, ds, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
         }
-        mma_commit(dq_done);
         mma_commit(k_empty(s));
+        mma_commit(dq_done);
       }
       __syncwarp();
       done = n + 1;
+      if (n + 1 < T && !issue_dp(n + 1)) break;
     }
+    __syncwarp();
     if (done > 0) mbar_drain(dq_done, (done - 1) & 1, ctl);
   } else if (warp >= 4) {
     // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
@@ -641,6 +648,21 @@ __global__ void __maxnreg__(168)
     const int c0 = 64 * g;                              // first key column of this group
     const float scale_log2 = a.scale * kLog2e;
     const size_t at = static_cast<size_t>(bh) * padded_rows(S) + ig;
+    const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
+    XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
+    // dO of this thread's row, 64 columns a group, into TMEM (rows behind the last, and columns behind dv: zeros).
+    if (NS == 2 || g == 0) {
+      uint32_t x[32];
+      uint4 *v = reinterpret_cast<uint4 *>(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = ig < S && c0 + 8 * e < dv ? __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + c0 + 8 * e))
+                                         : make_uint4(0u, 0u, 0u, 0u);
+      tmem_st_x32(tdO + lane_off + 32 * g, x);
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    mbar_arrive(do_full);
     const float nlse2 = a.nlse[at], nD = a.nD[at];
     bool ok = true;
 #pragma unroll 1
@@ -666,44 +688,33 @@ __global__ void __maxnreg__(168)
         for (int e = 0; e < 64; ++e)
           if (c0 + e > i) p[e] = 0u;
       }
-      // dS = P (dP - D) in two 32-column halves, bf16 into the dS slot.
+      // dS = P (dP - D), bf16 over the first half of this group's dP.
       if (!warp_wait(dp_full, n & 1, ctl)) { ok = false; break; }
       tc_fence_after();
+      uint32_t ds[32];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int part = 0; part < 2; ++part) {
         uint32_t d[32];
-        tmem_ld_x32(tdP + lane_off + c0 + 32 * half, d);
+        tmem_ld_x32(tdP + lane_off + c0 + 32 * part, d);
         tmem_wait_ld();
         reg_fence<32>(d);
-        if (half == 1) {                                // dP(n) fully read
-          tc_fence_before();
-          mbar_arrive(dp_free);
-        }
-        uint32_t ds[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float t0, t1;
           fadd2(t0, t1, __uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), nD, nD);
-          fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * half + 2 * e]), __uint_as_float(p[32 * half + 2 * e + 1]));
-          ds[e] = pack_bf16x2(t0, t1);
+          fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * part + 2 * e]), __uint_as_float(p[32 * part + 2 * e + 1]));
+          ds[16 * part + e] = pack_bf16x2(t0, t1);
         }
-        if (half == 0 && n > 0) {
-          // dQ(n - 1) has finished reading the dS slot.
-          if (!warp_wait(dq_done, (n - 1) & 1, ctl)) { ok = false; break; }
-          tc_fence_after();
-        }
-        tmem_st_x16(tdS + lane_off + c0 / 2 + 16 * half, ds);
       }
-      if (!ok) break;
+      tmem_st_x32(tdP + lane_off + c0, ds);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(ds_full);
     }
+
     // Epilogue: dq = bf16(scale * sum); group g writes every second 16 columns of the thread's row.
     if (ok && warp_wait(dq_done, (T - 1) & 1, ctl)) {
       tc_fence_after();
-      const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
-      XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
 #pragma unroll 1
       for (int c = 16 * g; c < dn + dr; c += 32) {
         uint32_t v[16];
@@ -761,7 +772,7 @@ cudaError_t launch_latent_bwd_ns(const LatentMaps &q64, const LatentMaps &q128, 
                    q64.q, q128.kv, q128.rope, q64.dO, a);
   if (err != cudaSuccess) return err;
   return launch_pdl(latent_dq_kernel<NS>, static_cast<unsigned>(units), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
-                    q128.rope, q128.dO, a);
+                    q128.rope, a);
 }
 
 }  // namespace

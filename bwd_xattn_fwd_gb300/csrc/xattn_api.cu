@@ -836,7 +836,6 @@ xattn_status xattn_latent_bwd(const void *q, const void *kv, const void *k_rope,
   XATTN_TRY(make_map_subtiles(&q128.q, q, B, S, nh, dn + dr, kTileRows));
   XATTN_TRY(make_map_subtiles(&q128.kv, kv, B, S, nh, dn + dv, kTileRows));
   XATTN_TRY(make_map_subtiles(&q128.rope, k_rope, B, S, 1, dr, kTileRows));
-  XATTN_TRY(make_map_subtiles(&q128.dO, dO, B, S, nh, dv, kTileRows));
   XATTN_TRY(make_map_subtiles(&q64.q, q, B, S, nh, dn + dr, 64));
   XATTN_TRY(make_map_subtiles(&q64.dO, dO, B, S, nh, dv, 64));
   XATTN_TRY(scratch_alloc(*dev, latent_bwd_workspace_bytes(a), st, &base));

@@ -232,7 +232,7 @@ struct LatentMaps {
 size_t latent_bwd_workspace_bytes(const LatentArgs &a);
 void latent_bwd_workspace_carve(LatentArgs &a, void *base);
 cudaError_t launch_latent_fwd(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream);
-// q64: q and dO by 64 rows; q128: all four by 128.
+// q64: q and dO by 64 rows; q128: q, kv and rope by 128.
 cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
                               cudaStream_t stream);
 
