@@ -557,6 +557,7 @@ xattn_status xattn_tree_decode(const void *q, const void *k_pages, const void *v
   const int grid = tree_grid(a, hd, dev->sms);
   void *ws = nullptr;
   if (!a.whole) XATTN_TRY(scratch_alloc(*dev, tree_workspace_bytes(grid, a.rec_rows, hd), st, &ws));
+  a.q = static_cast<const __nv_bfloat16 *>(q);
   a.page_table = page_table;
   a.ctx_lens = ctx_lens;
   a.tree = tree;
