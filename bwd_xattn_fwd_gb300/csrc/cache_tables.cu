@@ -44,81 +44,179 @@ __device__ __forceinline__ int pages_of(int positions, int page_size) { return (
 
 __device__ __forceinline__ int clamp_len(int len, int most) { return min(max(len, 0), most); }
 
-// Sequences in order, 1024 at a time: what each needs, whether it gets it, and where its tokens start.
+// One thread a sequence: what sequence b needs (y: its tokens), and what it may get at most.
+__device__ __forceinline__ Pair reserve_need(const ReserveArgs &a, int b, int *room) {
+  *room = 0;
+  if (b >= a.B) return {0, 0};
+  const int most = a.max_pages * a.page_size;                // (at most 2^30)
+  const int ctx = clamp_len(a.ctx_lens[b], most), fresh = max(a.new_lens[b], 0);
+  *room = min(fresh, most - ctx);
+  return {pages_of(ctx + *room, a.page_size) - pages_of(ctx, a.page_size), fresh};
+}
+
+// The slot of token t, the at-th of sequence b, whose new pages begin `first` below the stack's top `count`; the page that
+// begins with it goes into the table.
+__device__ __forceinline__ long long reserve_slot(const ReserveArgs &a, int b, int at, int first, int count) {
+  const int ctx = clamp_len(a.ctx_lens[b], a.max_pages * a.page_size), pos = ctx + at, page = pos / a.page_size;
+  const int row = pos - page * a.page_size, held = pages_of(ctx, a.page_size);
+  int *entry = a.page_table + static_cast<size_t>(b) * a.max_pages + page;
+  int id;
+  if (page >= held) {
+    const int place = count - 1 - (first + page - held);
+    id = place >= 0 && place < a.num_pages ? a.free_pages[place] : -1;   // (outside only if the lengths change)
+    if (row == 0) *entry = id;
+  } else {
+    id = *entry;
+  }
+  return id >= 0 && id < a.num_pages ? static_cast<long long>(id) * a.page_size + row : -1;
+}
+
+// Sequences in order, 1024 at a time: what each needs, whether it gets it, and where its tokens start. With kFill the block
+// also does what reserve_fill_kernel does (B <= 1024; what it needs for that stays in shared memory).
+template <bool kFill>
 __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const ReserveArgs a) {
   __shared__ Pair part[kPlanThreads / 32];
-  __shared__ long long taken_part[kPlanThreads / 32];
+  __shared__ int taken_part[kPlanThreads / 32];
+  __shared__ int starts[kFill ? kPlanThreads + 1 : 1], got[kFill ? kPlanThreads : 1], firsts[kFill ? kPlanThreads : 1];
   grid_dep_launch();
   grid_dep_wait();
-  const int most = a.max_pages * a.page_size;                // (at most 2^30)
   const int count = clamp_len(a.free_count[0], a.num_pages);
   Pair base{0, 0};
-  long long taken = 0;
+  int taken = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    int need = 0, room = 0, fresh = 0;
-    if (b < a.B) {
-      const int ctx = clamp_len(a.ctx_lens[b], most);
-      fresh = max(a.new_lens[b], 0);
-      room = min(fresh, most - ctx);
-      need = pages_of(ctx + room, a.page_size) - pages_of(ctx, a.page_size);
-    }
+    int room;
+    const Pair need = reserve_need(a, b, &room);
     Pair total;
-    Pair upto = block_scan<kPlanThreads>({need, fresh}, part, &total);
+    Pair upto = block_scan<kPlanThreads>(need, part, &total);
     upto.x += base.x, upto.y += base.y;
     base.x += total.x, base.y += total.y;
     if (b < a.B) {
-      const bool ok = (need == 0 || upto.x <= count) && upto.y <= a.tokens;
-      if (ok && need > 0) taken = upto.x;
-      a.first[b] = ok ? static_cast<int>(min(upto.x - need, static_cast<long long>(a.num_pages))) : 0;
+      const bool ok = (need.x == 0 || upto.x <= count) && upto.y <= a.tokens;
+      if (ok && need.x > 0) taken = static_cast<int>(upto.x);
+      const int first = ok ? static_cast<int>(min(upto.x - need.x, static_cast<long long>(a.num_pages))) : 0;
+      const int end = static_cast<int>(min(upto.y, 0x7fffffffll));
       a.granted[b] = ok ? room : 0;
-      a.offsets[b + 1] = static_cast<int>(min(upto.y, 0x7fffffffll));
+      a.offsets[b + 1] = end;
+      if constexpr (kFill)
+        starts[b + 1] = end, got[b] = ok ? room : 0, firsts[b] = first;
+      else
+        a.first[b] = first;
     }
   }
   // The pages taken: the largest running need that was met (each thread's last is its largest).
-#pragma unroll
-  for (int off = 16; off; off >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, off));
+  taken = __reduce_max_sync(0xffffffffu, taken);
   if ((threadIdx.x & 31) == 0) taken_part[threadIdx.x >> 5] = taken;
+  if (kFill && threadIdx.x == 0) starts[0] = 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kPlanThreads / 32; ++w) taken = max(taken, taken_part[w]);
-    a.offsets[0] = 0;
-    a.first[a.B] = count;
-    a.free_count[0] = count - static_cast<int>(taken);
+  if (threadIdx.x < 32) {
+    taken = __reduce_max_sync(0xffffffffu, taken_part[threadIdx.x]);
+    if (threadIdx.x == 0) {
+      a.offsets[0] = 0;
+      if (!kFill) a.first[a.B] = count;
+      a.free_count[0] = count - taken;
+    }
+  }
+  if constexpr (kFill) {
+    for (int t = threadIdx.x; t < a.tokens; t += kPlanThreads) {
+      long long slot = -1;
+      if (t < starts[a.B]) {
+        int lo = 0, hi = a.B;                                // starts[lo] <= t < starts[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (starts[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+        if (t - starts[lo] < got[lo]) slot = reserve_slot(a, lo, t - starts[lo], firsts[lo], count);
+      }
+      a.slots[t] = slot;
+    }
   }
 }
 
-// One thread a token: its slot, and the table entry of a page that begins with it.
+// One thread a token: its slot, and the table entry of a page that begins with it. A warp looks for its first token's
+// sequence 32 places at a time (two steps for 1024 sequences; a binary search of each thread's own took a third of the
+// kernel), and its threads go on from there.
 __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const ReserveArgs a) {
   grid_dep_launch();
   grid_dep_wait();
-  const long long t = static_cast<long long>(blockIdx.x) * kFillThreads + threadIdx.x;
-  if (t >= a.tokens) return;
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * kFillThreads + threadIdx.x, t0 = t - lane;
+  const int end = a.offsets[a.B], count = a.first[a.B];
   long long slot = -1;
-  if (t < a.offsets[a.B]) {
-    int lo = 0, hi = a.B;                                    // offsets[lo] <= t < offsets[hi]
+  if (t0 < end) {                                            // (warp-uniform)
+    int lo = 0, hi = a.B;                                    // offsets[lo] <= t0 < offsets[hi]
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.offsets[mid] <= t) lo = mid;
-      else hi = mid;
+      const int step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi);
+      const unsigned below = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= t0);   // lanes 0 .. k
+      const int k = 31 - __clz(below);
+      lo += k * step;
+      hi = min(lo + step, hi);
     }
-    const int at = static_cast<int>(t - a.offsets[lo]);
-    if (at < a.granted[lo]) {
-      const int ctx = clamp_len(a.ctx_lens[lo], a.max_pages * a.page_size), pos = ctx + at, page = pos / a.page_size;
-      const int row = pos - page * a.page_size, held = pages_of(ctx, a.page_size);
-      int *entry = a.page_table + static_cast<size_t>(lo) * a.max_pages + page;
-      int id;
-      if (page >= held) {
-        const int place = a.first[a.B] - 1 - (a.first[lo] + page - held);
-        id = place >= 0 && place < a.num_pages ? a.free_pages[place] : -1;   // (outside only if the lengths change)
-        if (row == 0) *entry = id;
-      } else {
-        id = *entry;
-      }
-      if (id >= 0 && id < a.num_pages) slot = static_cast<long long>(id) * a.page_size + row;
+    if (t < end) {
+      int next = a.offsets[lo + 1];
+      while (next <= t) next = a.offsets[++lo + 1];
+      const int at = static_cast<int>(t) - a.offsets[lo];
+      if (at < a.granted[lo]) slot = reserve_slot(a, lo, at, a.first[lo], count);
     }
   }
-  a.slots[t] = slot;
+  if (t < a.tokens) a.slots[t] = slot;
+}
+
+// Pages that sequence b gives back: entries [from, to) of its row.
+__device__ __forceinline__ int *release_row(const ReleaseArgs &a, int b, int *from, int *to) {
+  const int most = a.max_pages * a.page_size;
+  *from = pages_of(clamp_len(a.keep_lens[b], most), a.page_size);
+  *to = pages_of(clamp_len(a.held_lens[b], most), a.page_size);
+  return a.page_table + static_cast<size_t>(b) * a.max_pages;
+}
+
+// (warp) How many pages sequence b gives back.
+__device__ __forceinline__ int release_count(const ReleaseArgs &a, int b, int lane) {
+  int from, to, n = 0;
+  const int *row = release_row(a, b, &from, &to);
+#pragma unroll 4
+  for (int j = from + lane; j < to; j += 32) n += row[j] >= 0 && row[j] < a.num_pages;
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// (warp) Sequence b's pages onto the stack, downwards from place top - 1 - rank.
+__device__ __forceinline__ void release_push(const ReleaseArgs &a, int b, long long top, long long rank, int lane) {
+  int from, to;
+  int *row = release_row(a, b, &from, &to);
+  for (int j0 = from; j0 < to; j0 += 32) {
+    const int j = j0 + lane, id = j < to ? row[j] : -1;
+    const bool real = id >= 0 && id < a.num_pages;
+    const unsigned all = __ballot_sync(0xffffffffu, real);
+    const long long place = top - 1 - (rank + __popc(all & ((1u << lane) - 1u)));
+    if (real && place >= 0 && place < a.num_pages) a.free_pages[place] = id;
+    if (j < to) row[j] = -1;
+    rank += __popc(all);
+  }
+}
+
+// Few sequences with short rows: all in one block. The first sequence's first page ends topmost, so that a release undoes
+// the reserve before it.
+__global__ void __launch_bounds__(kPlanThreads) release_small_kernel(const ReleaseArgs a) {
+  __shared__ Pair part[kPlanThreads / 32];
+  __shared__ int ranks[kPlanThreads];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int count = clamp_len(a.free_count[0], a.num_pages);
+  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+    const int n = release_count(a, b, lane);
+    if (lane == 0) ranks[b] = n;
+  }
+  __syncthreads();
+  const int mine = tid < a.B ? ranks[tid] : 0;
+  Pair total;
+  const Pair upto = block_scan<kPlanThreads>({mine, 0}, part, &total);
+  if (tid < a.B) ranks[tid] = static_cast<int>(upto.x) - mine;
+  const long long top = count + total.x;                     // one past the stack's new top
+  __syncthreads();
+  if (tid == 0) a.free_count[0] = static_cast<int>(min(top, static_cast<long long>(a.num_pages)));
+  for (int b = warp; b < a.B; b += kPlanThreads / 32) release_push(a, b, top, ranks[b], lane);
 }
 
 // One warp a sequence: how many pages it gives back.
@@ -128,17 +226,11 @@ __global__ void __launch_bounds__(kFillThreads) release_count_kernel(const Relea
   const int lane = threadIdx.x & 31, b = static_cast<int>(blockIdx.x) * (kFillThreads / 32) + (threadIdx.x >> 5);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.counts[a.B] = clamp_len(a.free_count[0], a.num_pages);
   if (b >= a.B) return;
-  const int most = a.max_pages * a.page_size;
-  const int from = pages_of(clamp_len(a.keep_lens[b], most), a.page_size), to = pages_of(clamp_len(a.held_lens[b], most), a.page_size);
-  const int *row = a.page_table + static_cast<size_t>(b) * a.max_pages;
-  int n = 0;
-  for (int j = from + lane; j < to; j += 32) n += row[j] >= 0 && row[j] < a.num_pages;
-  n = __reduce_add_sync(0xffffffffu, n);
+  const int n = release_count(a, b, lane);
   if (lane == 0) a.counts[b] = n;
 }
 
-// One warp a sequence, `each` sequences a block: its pages onto the stack, the first sequence's first page
-// topmost, so that a release undoes the reserve before it.
+// One warp a sequence, `each` sequences a block, which adds up for itself what the sequences before it give back.
 __global__ void __launch_bounds__(kFillThreads) release_push_kernel(const ReleaseArgs a, int each) {
   __shared__ Pair part[kFillThreads / 32];
   __shared__ int before[kFillThreads / 32];
@@ -153,10 +245,8 @@ __global__ void __launch_bounds__(kFillThreads) release_push_kernel(const Releas
     if (b < b0) mine.y += n;
   }
   block_scan<kFillThreads>(mine, part, &total);
-  const int count = a.counts[a.B];
-  const long long top = count + total.x;                     // one past the stack's new top
+  const long long top = a.counts[a.B] + total.x;             // one past the stack's new top
   if (blockIdx.x == 0 && threadIdx.x == 0) a.free_count[0] = static_cast<int>(min(top, static_cast<long long>(a.num_pages)));
-  const int most = a.max_pages * a.page_size;
   long long rank = total.y;
   for (int g = 0; g < each; g += kWarps) {
     const int b = b0 + g + warp;
@@ -170,66 +260,78 @@ __global__ void __launch_bounds__(kFillThreads) release_push_kernel(const Releas
       if (w < warp) r += before[w];
       rank += before[w];
     }
-    if (!live) continue;
-    const int from = pages_of(clamp_len(a.keep_lens[b], most), a.page_size), to = pages_of(clamp_len(a.held_lens[b], most), a.page_size);
-    int *row = a.page_table + static_cast<size_t>(b) * a.max_pages;
-    for (int j0 = from; j0 < to; j0 += 32) {
-      const int j = j0 + lane, id = j < to ? row[j] : -1;
-      const bool real = id >= 0 && id < a.num_pages;
-      const unsigned all = __ballot_sync(0xffffffffu, real);
-      const long long place = top - 1 - (r + __popc(all & ((1u << lane) - 1u)));
-      if (real && place >= 0 && place < a.num_pages) a.free_pages[place] = id;
-      if (j < to) row[j] = -1;
-      r += __popc(all);
-    }
+    if (live) release_push(a, b, top, r, lane);
   }
 }
 
-// One thread a 16-byte vector of a row of either source.
+// A thread has kVecsEach 16-byte vectors of the rows of both sources, a block's width apart; what it reads of the source does
+// not wait for the slot. (The slot first, then the row: 41 us for 65536 rows of 576, 3.7 TB/s.)
+constexpr int kVecsEach = 4;
 __global__ void __launch_bounds__(kFillThreads) cache_write_kernel(const WriteArgs a) {
   grid_dep_launch();
   grid_dep_wait();
-  const long long t = static_cast<long long>(blockIdx.x) * kFillThreads + threadIdx.x;
-  const int each = a.vecs[0] + a.vecs[1];
-  long long r;
-  int v;
-  if (t >> 32) {
-    r = t / each;
-    v = static_cast<int>(t - r * each);
-  } else {                                                   // division in 32 bits
-    r = static_cast<unsigned>(t) / static_cast<unsigned>(each);
-    v = static_cast<int>(static_cast<unsigned>(t) - static_cast<unsigned>(r) * each);
+  const long long t0 = static_cast<long long>(blockIdx.x) * (kFillThreads * kVecsEach) + threadIdx.x;
+  const unsigned each = a.vecs0 + a.vecs1;
+  uint4 x[kVecsEach];
+  uint4 *to[kVecsEach];
+#pragma unroll
+  for (int e = 0; e < kVecsEach; ++e) {
+    const long long t = t0 + e * kFillThreads;
+    long long r;
+    unsigned v;
+    if (t >> 32) {
+      r = t / each;
+      v = static_cast<unsigned>(t - r * each);
+    } else {                                                 // division in 32 bits
+      r = static_cast<unsigned>(t) / each;
+      v = static_cast<unsigned>(t) - static_cast<unsigned>(r) * each;
+    }
+    to[e] = nullptr;
+    if (r >= a.rows) continue;
+    const long long slot = a.slots[r];
+    const bool second = v >= a.vecs0;
+    if (second) v -= a.vecs0;
+    x[e] = second ? a.src1[r * a.vecs1 + v] : a.src0[r * a.vecs0 + v];
+    if (slot >= 0 && slot < a.num_slots) to[e] = second ? a.dst1 + slot * a.stride1 + v : a.dst0 + slot * a.stride0 + v;
   }
-  if (r >= a.rows) return;
-  const long long slot = a.slots[r];
-  if (slot < 0 || slot >= a.num_slots) return;
-  const int x = v < a.vecs[0] ? 0 : 1;
-  if (x) v -= a.vecs[0];
-  a.dst[x][slot * a.stride[x] + v] = a.src[x][r * a.vecs[x] + v];
+#pragma unroll
+  for (int e = 0; e < kVecsEach; ++e)
+    if (to[e]) *to[e] = x[e];
 }
 
 unsigned blocks_for(long long threads) { return static_cast<unsigned>((threads + kFillThreads - 1) / kFillThreads); }
 
+// One block does all of a small call: no scratch and no second kernel.
+constexpr int kSmallTokens = 8192, kSmallEntries = 16384;
+
 }  // namespace
 
+bool reserve_small(int B, long long tokens) { return B <= kPlanThreads && tokens <= kSmallTokens; }
+bool release_small(int B, int max_pages) {
+  return B <= kPlanThreads && static_cast<long long>(B) * max_pages <= kSmallEntries;
+}
+
 cudaError_t launch_cache_reserve(const ReserveArgs &a, cudaStream_t stream) {
-  const cudaError_t err = launch_pdl(reserve_plan_kernel, 1, kPlanThreads, 0, stream, a);
+  if (reserve_small(a.B, a.tokens)) return launch_pdl(reserve_plan_kernel<true>, 1, kPlanThreads, 0, stream, a);
+  const cudaError_t err = launch_pdl(reserve_plan_kernel<false>, 1, kPlanThreads, 0, stream, a);
   if (err != cudaSuccess || a.tokens == 0) return err;
   return launch_pdl(reserve_fill_kernel, blocks_for(a.tokens), kFillThreads, 0, stream, a);
 }
 
 cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream) {
+  if (release_small(a.B, a.max_pages)) return launch_pdl(release_small_kernel, 1, kPlanThreads, 0, stream, a);
   constexpr int kWarps = kFillThreads / 32;
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.B) + kWarps - 1) / kWarps);
   const cudaError_t err = launch_pdl(release_count_kernel, blocks, kFillThreads, 0, stream, a);
   if (err != cudaSuccess) return err;
   const int each = (static_cast<int>((blocks + 511) / 512)) * kWarps;
-  return launch_pdl(release_push_kernel, static_cast<unsigned>((static_cast<long long>(a.B) + each - 1) / each), kFillThreads, 0, stream, a,
-                    each);
+  return launch_pdl(release_push_kernel, static_cast<unsigned>((static_cast<long long>(a.B) + each - 1) / each), kFillThreads, 0,
+                    stream, a, each);
 }
 
 cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream) {
-  return launch_pdl(cache_write_kernel, blocks_for(a.rows * (a.vecs[0] + a.vecs[1])), kFillThreads, 0, stream, a);
+  const long long threads = (a.rows * (a.vecs0 + a.vecs1) + kVecsEach - 1) / kVecsEach;
+  return launch_pdl(cache_write_kernel, blocks_for(threads), kFillThreads, 0, stream, a);
 }
 
 }  // namespace xattn

@@ -269,6 +269,7 @@ struct ReserveArgs {
   int B, max_pages, page_size, num_pages;
   long long tokens;
 };
+bool reserve_small(int B, long long tokens);   // needs no scratch
 cudaError_t launch_cache_reserve(const ReserveArgs &a, cudaStream_t stream);
 
 struct ReleaseArgs {
@@ -278,14 +279,15 @@ struct ReleaseArgs {
   int *counts;                                 // scratch: [B] pages given back; [B]: free pages before
   int B, max_pages, page_size, num_pages;
 };
+bool release_small(int B, int max_pages);      // needs no scratch
 cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream);
 
-// Two sources' rows to the rows `slots` of their places: 16-byte vectors, of a row src_vecs[x] go to
-// dst[x] + slot * dst_stride[x].
+// Rows of two sources to their places: row r of source x, vecs_x 16-byte vectors, to dst_x + slots[r] * stride_x.
 struct WriteArgs {
-  const uint4 *src[2];
-  uint4 *dst[2];
-  int vecs[2], stride[2];
+  const uint4 *src0, *src1;
+  uint4 *dst0, *dst1;
+  unsigned vecs0, vecs1;
+  int stride0, stride1;
   const long long *slots;
   long long rows, num_slots;
 };
