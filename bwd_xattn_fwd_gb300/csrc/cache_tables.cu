@@ -11,7 +11,7 @@
 namespace xattn {
 namespace {
 
-constexpr int kPlanThreads = 1024, kFillThreads = 256;
+constexpr int kPlanThreads = 1024, kFewThreads = 256, kFillThreads = 256;
 
 struct Pair {
   long long x, y;
@@ -71,38 +71,42 @@ __device__ __forceinline__ long long reserve_slot(const ReserveArgs &a, int b, i
   return id >= 0 && id < a.num_pages ? static_cast<long long>(id) * a.page_size + row : -1;
 }
 
-// Sequences in order, 1024 at a time: what each needs, whether it gets it, and where its tokens start. With kFill the block
-// also does what reserve_fill_kernel does (B <= 1024; what it needs for that stays in shared memory).
-template <bool kFill>
-__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const ReserveArgs a) {
-  __shared__ Pair part[kPlanThreads / 32];
-  __shared__ int taken_part[kPlanThreads / 32];
-  __shared__ int starts[kFill ? kPlanThreads + 1 : 1], got[kFill ? kPlanThreads : 1], firsts[kFill ? kPlanThreads : 1];
+// What each sequence needs, whether it gets it, and where its tokens start. A thread takes ceil(B / kThreads) sequences in a row:
+// their sums, then, behind one scan of the block, each in its place. With kFill the block also does what reserve_fill_kernel
+// does (B <= kThreads; what it needs for that stays in shared memory).
+template <bool kFill, int kThreads>
+__global__ void __launch_bounds__(kThreads) reserve_plan_kernel(const ReserveArgs a) {
+  __shared__ Pair part[kThreads / 32];
+  __shared__ int taken_part[kThreads / 32];
+  __shared__ int starts[kFill ? kThreads + 1 : 1], got[kFill ? kThreads : 1], firsts[kFill ? kThreads : 1];
   grid_dep_launch();
   grid_dep_wait();
   const int count = clamp_len(a.free_count[0], a.num_pages);
-  Pair base{0, 0};
-  int taken = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    int room;
+  const int each = kFill ? 1 : (a.B + kThreads - 1) / kThreads, b0 = static_cast<int>(threadIdx.x) * each;
+  const int b1 = min(b0 + each, a.B);
+  int room;
+  Pair mine{0, 0}, total;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) {
     const Pair need = reserve_need(a, b, &room);
-    Pair total;
-    Pair upto = block_scan<kPlanThreads>(need, part, &total);
-    upto.x += base.x, upto.y += base.y;
-    base.x += total.x, base.y += total.y;
-    if (b < a.B) {
-      const bool ok = (need.x == 0 || upto.x <= count) && upto.y <= a.tokens;
-      if (ok && need.x > 0) taken = static_cast<int>(upto.x);
-      const int first = ok ? static_cast<int>(min(upto.x - need.x, static_cast<long long>(a.num_pages))) : 0;
-      const int end = static_cast<int>(min(upto.y, 0x7fffffffll));
-      a.granted[b] = ok ? room : 0;
-      a.offsets[b + 1] = end;
-      if constexpr (kFill)
-        starts[b + 1] = end, got[b] = ok ? room : 0, firsts[b] = first;
-      else
-        a.first[b] = first;
-    }
+    mine.x += need.x, mine.y += need.y;
+  }
+  Pair upto = block_scan<kThreads>(mine, part, &total);
+  upto.x -= mine.x, upto.y -= mine.y;
+  int taken = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Pair need = reserve_need(a, b, &room);
+    upto.x += need.x, upto.y += need.y;
+    const bool ok = (need.x == 0 || upto.x <= count) && upto.y <= a.tokens;
+    if (ok && need.x > 0) taken = static_cast<int>(upto.x);
+    const int first = ok ? static_cast<int>(min(upto.x - need.x, static_cast<long long>(a.num_pages))) : 0;
+    const int end = static_cast<int>(min(upto.y, 0x7fffffffll));
+    a.granted[b] = ok ? room : 0;
+    a.offsets[b + 1] = end;
+    if constexpr (kFill)
+      starts[b + 1] = end, got[b] = ok ? room : 0, firsts[b] = first;
+    else
+      a.first[b] = first;
   }
   // The pages taken: the largest running need that was met (each thread's last is its largest).
   taken = __reduce_max_sync(0xffffffffu, taken);
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
   if (kFill && threadIdx.x == 0) starts[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
-    taken = __reduce_max_sync(0xffffffffu, taken_part[threadIdx.x]);
+    taken = __reduce_max_sync(0xffffffffu, threadIdx.x < kThreads / 32 ? taken_part[threadIdx.x] : 0);
     if (threadIdx.x == 0) {
       a.offsets[0] = 0;
       if (!kFill) a.first[a.B] = count;
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
     }
   }
   if constexpr (kFill) {
-    for (int t = threadIdx.x; t < a.tokens; t += kPlanThreads) {
+    for (int t = threadIdx.x; t < a.tokens; t += kThreads) {
       long long slot = -1;
       if (t < starts[a.B]) {
         int lo = 0, hi = a.B;                                // starts[lo] <= t < starts[hi]
@@ -134,18 +138,18 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
   }
 }
 
-// One thread a token: its slot, and the table entry of a page that begins with it. A warp looks for its first token's
-// sequence 32 places at a time (two steps for 1024 sequences; a binary search of each thread's own took a third of the
-// kernel), and its threads go on from there.
+// A warp has kTokensEach x 32 tokens in a row: their slots, and the table entries of pages that begin with them. It looks for
+// its first token's sequence 32 places at a time (two steps for 1024 sequences), and each thread goes on from there.
+constexpr int kTokensEach = 4;
 __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const ReserveArgs a) {
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
-  const long long t = static_cast<long long>(blockIdx.x) * kFillThreads + threadIdx.x, t0 = t - lane;
+  const long long t0 = (static_cast<long long>(blockIdx.x) * (kFillThreads / 32) + (threadIdx.x >> 5)) * (32 * kTokensEach);
   const int end = a.offsets[a.B], count = a.first[a.B];
-  long long slot = -1;
+  int lo = 0;
   if (t0 < end) {                                            // (warp-uniform)
-    int lo = 0, hi = a.B;                                    // offsets[lo] <= t0 < offsets[hi]
+    int hi = a.B;                                            // offsets[lo] <= t0 < offsets[hi]
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi);
       const unsigned below = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= t0);   // lanes 0 .. k
@@ -153,14 +157,24 @@ __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const Reserv
       lo += k * step;
       hi = min(lo + step, hi);
     }
+  }
+  int next = t0 < end ? a.offsets[lo + 1] : 0;
+  long long slot[kTokensEach];
+#pragma unroll
+  for (int e = 0; e < kTokensEach; ++e) {
+    const long long t = t0 + 32 * e + lane;
+    slot[e] = -1;
     if (t < end) {
-      int next = a.offsets[lo + 1];
       while (next <= t) next = a.offsets[++lo + 1];
       const int at = static_cast<int>(t) - a.offsets[lo];
-      if (at < a.granted[lo]) slot = reserve_slot(a, lo, at, a.first[lo], count);
+      if (at < a.granted[lo]) slot[e] = reserve_slot(a, lo, at, a.first[lo], count);
     }
   }
-  if (t < a.tokens) a.slots[t] = slot;
+#pragma unroll
+  for (int e = 0; e < kTokensEach; ++e) {
+    const long long t = t0 + 32 * e + lane;
+    if (t < a.tokens) a.slots[t] = slot[e];
+  }
 }
 
 // Pages that sequence b gives back: entries [from, to) of its row.
@@ -197,26 +211,27 @@ __device__ __forceinline__ void release_push(const ReleaseArgs &a, int b, long l
 
 // Few sequences with short rows: all in one block. The first sequence's first page ends topmost, so that a release undoes
 // the reserve before it.
-__global__ void __launch_bounds__(kPlanThreads) release_small_kernel(const ReleaseArgs a) {
-  __shared__ Pair part[kPlanThreads / 32];
-  __shared__ int ranks[kPlanThreads];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleaseArgs a) {
+  __shared__ Pair part[kThreads / 32];
+  __shared__ int ranks[kThreads];
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const int count = clamp_len(a.free_count[0], a.num_pages);
-  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+  for (int b = warp; b < a.B; b += kThreads / 32) {
     const int n = release_count(a, b, lane);
     if (lane == 0) ranks[b] = n;
   }
   __syncthreads();
   const int mine = tid < a.B ? ranks[tid] : 0;
   Pair total;
-  const Pair upto = block_scan<kPlanThreads>({mine, 0}, part, &total);
+  const Pair upto = block_scan<kThreads>({mine, 0}, part, &total);
   if (tid < a.B) ranks[tid] = static_cast<int>(upto.x) - mine;
   const long long top = count + total.x;                     // one past the stack's new top
   __syncthreads();
   if (tid == 0) a.free_count[0] = static_cast<int>(min(top, static_cast<long long>(a.num_pages)));
-  for (int b = warp; b < a.B; b += kPlanThreads / 32) release_push(a, b, top, ranks[b], lane);
+  for (int b = warp; b < a.B; b += kThreads / 32) release_push(a, b, top, ranks[b], lane);
 }
 
 // One warp a sequence: how many pages it gives back.
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(kFillThreads) release_push_kernel(const Releas
 
 // A thread has kVecsEach 16-byte vectors of the rows of both sources, a block's width apart; what it reads of the source does
 // not wait for the slot. (The slot first, then the row: 41 us for 65536 rows of 576, 3.7 TB/s.)
-constexpr int kVecsEach = 4;
+template <int kVecsEach>
 __global__ void __launch_bounds__(kFillThreads) cache_write_kernel(const WriteArgs a) {
   grid_dep_launch();
   grid_dep_wait();
@@ -312,14 +327,21 @@ bool release_small(int B, int max_pages) {
 }
 
 cudaError_t launch_cache_reserve(const ReserveArgs &a, cudaStream_t stream) {
-  if (reserve_small(a.B, a.tokens)) return launch_pdl(reserve_plan_kernel<true>, 1, kPlanThreads, 0, stream, a);
-  const cudaError_t err = launch_pdl(reserve_plan_kernel<false>, 1, kPlanThreads, 0, stream, a);
+  if (reserve_small(a.B, a.tokens)) {
+    if (a.B <= kFewThreads && a.tokens <= 2 * kFewThreads)
+      return launch_pdl(reserve_plan_kernel<true, kFewThreads>, 1, kFewThreads, 0, stream, a);
+    return launch_pdl(reserve_plan_kernel<true, kPlanThreads>, 1, kPlanThreads, 0, stream, a);
+  }
+  const cudaError_t err = launch_pdl(reserve_plan_kernel<false, kPlanThreads>, 1, kPlanThreads, 0, stream, a);
   if (err != cudaSuccess || a.tokens == 0) return err;
-  return launch_pdl(reserve_fill_kernel, blocks_for(a.tokens), kFillThreads, 0, stream, a);
+  return launch_pdl(reserve_fill_kernel, blocks_for((a.tokens + kTokensEach - 1) / kTokensEach), kFillThreads, 0, stream, a);
 }
 
 cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream) {
-  if (release_small(a.B, a.max_pages)) return launch_pdl(release_small_kernel, 1, kPlanThreads, 0, stream, a);
+  if (release_small(a.B, a.max_pages)) {
+    if (a.B <= kFewThreads / 32) return launch_pdl(release_small_kernel<kFewThreads>, 1, kFewThreads, 0, stream, a);
+    return launch_pdl(release_small_kernel<kPlanThreads>, 1, kPlanThreads, 0, stream, a);
+  }
   constexpr int kWarps = kFillThreads / 32;
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.B) + kWarps - 1) / kWarps);
   const cudaError_t err = launch_pdl(release_count_kernel, blocks, kFillThreads, 0, stream, a);
@@ -330,8 +352,12 @@ cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream) {
-  const long long threads = (a.rows * (a.vecs0 + a.vecs1) + kVecsEach - 1) / kVecsEach;
-  return launch_pdl(cache_write_kernel, blocks_for(threads), kFillThreads, 0, stream, a);
+  // One vector a thread where that is less than the GPU holds at once (64 rows of 576: 1.3 us, 2.5 with four), else two (65536
+  // rows: 24.6 us, 6.2 TB/s; one 25.6, four 26.8, eight 32.2).
+  const long long vecs = a.rows * (a.vecs0 + a.vecs1);
+  constexpr int kMany = 2;
+  if (vecs <= 152 * 2048) return launch_pdl(cache_write_kernel<1>, blocks_for(vecs), kFillThreads, 0, stream, a);
+  return launch_pdl(cache_write_kernel<kMany>, blocks_for((vecs + kMany - 1) / kMany), kFillThreads, 0, stream, a);
 }
 
 }  // namespace xattn
