@@ -101,12 +101,17 @@ struct LatWalk {
   int e0, e1;              // the piece: tiles [e0, e1) of the sequence
 };
 
+// What a walk holds is the same in every lane; the broadcasts let the compiler see it, so that loops over it keep the counters, and the
+// descriptors made of them, in uniform registers. With those issued from a converged warp, a product of 64 x 64 x 16 takes its
+// 33 cycles; with loop bounds as loaded 47, and issued by one lane in a branch of its own 53.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ bool lat_piece(LatWalk &w, const LatentDecodeArgs &a) {
   if (w.pos >= w.stop) return false;
   if (w.pos - w.first >= w.count) {
     w.first += w.count;
     if (++w.b >= a.B) return false;                              // (only if the lengths change under the call)
-    w.ctx = lat_ctx(a, w.b);
+    w.ctx = uniform(lat_ctx(a, w.b));
     w.count = (w.ctx + a.n + kTilePos - 1) / kTilePos;
   }
   w.e0 = w.pos - w.first;
@@ -127,7 +132,7 @@ __device__ __forceinline__ LatRuns lat_start(const LatentDecodeArgs &a, int grou
     const int up = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += up;
   }
-  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  const int total = uniform(__shfl_sync(0xffffffffu, incl, 31));
   const LatRuns runs(total, min(groups, total));
   w.pos = w.stop = 0;
   if (group >= total) return runs;
@@ -139,9 +144,9 @@ __device__ __forceinline__ LatRuns lat_start(const LatentDecodeArgs &a, int grou
   if (lane == l) {
     for (int c = lat_tiles(a, b); at + c <= w.pos; c = lat_tiles(a, b)) at += c, ++b;
   }
-  w.b = __shfl_sync(0xffffffffu, b, l);
-  w.first = __shfl_sync(0xffffffffu, at, l);
-  w.ctx = lat_ctx(a, w.b);
+  w.b = uniform(__shfl_sync(0xffffffffu, b, l));
+  w.first = uniform(__shfl_sync(0xffffffffu, at, l));
+  w.ctx = uniform(lat_ctx(a, w.b));
   w.count = (w.ctx + a.n + kTilePos - 1) / kTilePos;
   return runs;
 }
@@ -197,6 +202,7 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t *r) {
 template <int N>
 __global__ void __launch_bounds__(kLatThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mc,
+                         const __grid_constant__ CUtensorMap mqc, const __grid_constant__ CUtensorMap mpair,
                          const LatentDecodeArgs a) {
   using L = LatLayout<N>;
   constexpr int kPairs = L::kPairs, kRopes = L::kRopes;
@@ -238,6 +244,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mc);
+    tma_prefetch_desc(&mqc);
+    tma_prefetch_desc(&mpair);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), 512);
@@ -254,7 +262,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   const int group = static_cast<int>(blockIdx.x) / a.row_tiles, rt = static_cast<int>(blockIdx.x) - group * a.row_tiles;
   const int groups = static_cast<int>(gridDim.x) / a.row_tiles, blocks = a.dc / 128;
   LatWalk walk;
+
   const LatRuns runs = lat_start(a, group, groups, lane, walk);
+
 
   if (warp == 0) {
     // ---------------- TMA producer: lane l finds box l of each tile ----------------
@@ -265,7 +275,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     while (ok && lat_piece(walk, a)) {
       if (!lat_wait(q_empty, (pieces & 1) ^ 1, ctl)) break;
       mbar_expect_tx_elect(q_full, (2 * blocks + 1) * L::kQSub);
-      for (int c = 0; c <= 2 * blocks; ++c) tma_load_4d_elect(sQ + c * L::kQSub, &mq, q_full, 64 * c, rt * N, walk.b, 0);
+      tma_load_4d_elect(sQ, &mqc, q_full, 0, rt * N, 0, walk.b);
+      tma_load_4d_elect(sQ + 2 * blocks * L::kQSub, &mq, q_full, a.dc, rt * N, walk.b, 0);
       ++pieces;
       const int *table = a.page_table + static_cast<size_t>(walk.b) * a.max_pages;
       const int end = walk.ctx + a.n;
@@ -296,7 +307,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         for (int j = 0; j < blocks; ++j, ++Rj) {
           const int s = Rj % kPairs;
           if (!lat_wait(c_empty(s), ((Rj / kPairs) & 1) ^ 1, ctl)) { ok = false; break; }
-          if (elect_one()) {
+          if (boxes == 1) {                                     // both sub-tiles in one box
+            mbar_expect_tx_elect(c_full(s), L::kPair);
+            tma_load_4d_elect(sC + s * L::kPair, &mpair, c_full(s), 0, rw, 2 * j, pg[0]);
+          } else if (elect_one()) {
             mbar_expect_tx(c_full(s), L::kPair);
             load_sub(sC + s * L::kPair, c_full(s), 128 * j);
             load_sub(sC + s * L::kPair + L::kSub, c_full(s), 128 * j + 64);
@@ -340,24 +354,18 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           const int s = Rj % kPairs;
           if (!lat_wait(c_full(s), (Rj / kPairs) & 1, ctl)) { ok = false; break; }
           tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ss(d, dC + s * (L::kPair >> 4) + (kk / 4) * (L::kSub >> 4) + (kk % 4) * 2,
-                     dQ + (2 * j + kk / 4) * (L::kQSub >> 4) + (kk % 4) * 2, idesc_s, (j > 0 || kk > 0) ? 1u : 0u);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss_elect(d, dC + s * (L::kPair >> 4) + (kk / 4) * (L::kSub >> 4) + (kk % 4) * 2,
+                         dQ + (2 * j + kk / 4) * (L::kQSub >> 4) + (kk % 4) * 2, idesc_s, (j > 0 || kk > 0) ? 1u : 0u);
         }
         const int s = R % kRopes;
         if (!ok || !lat_wait(r_full(s), (R / kRopes) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        if (elect_one()) {
-          for (int kk = 0; kk < rope_steps; ++kk)
-            mma_ss(d, dR + s * (L::kSub >> 4) + kk * 2, dQ + 2 * blocks * (L::kQSub >> 4) + kk * 2, idesc_s, 1u);
-          mma_commit(s_full(R & 1));
-          if (e + 1 == walk.e1) mma_commit(q_empty);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < rope_steps; ++kk)
+          mma_ss_elect(d, dR + s * (L::kSub >> 4) + kk * 2, dQ + 2 * blocks * (L::kQSub >> 4) + kk * 2, idesc_s, 1u);
+        mma_commit_elect(s_full(R & 1));
+        if (e + 1 == walk.e1) mma_commit_elect(q_empty);
         ++R;
       }
       ++piece;
@@ -376,20 +384,16 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       for (int e = walk.e0; e < walk.e1; ++e, ++R) {
         if (!lat_wait(p_full, R & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        if (elect_one()) {
 #pragma unroll 1
-          for (int j = 0; j < blocks; ++j) {
-            const int s = (Rj + j) % kPairs;
+        for (int j = 0; j < blocks; ++j, ++Rj) {
+          const int s = Rj % kPairs;
 #pragma unroll
-            for (int kk = 0; kk < kTilePos / 16; ++kk)
-              mma_ss(tO + j * N, dCt + s * (L::kPair >> 4) + kk * 128, dP + kk * L::kPRow, idesc_o,
-                     (e > walk.e0 || kk > 0) ? 1u : 0u);
-            mma_commit(c_empty(s));
-          }
-          mma_commit(o_done);
+          for (int kk = 0; kk < kTilePos / 16; ++kk)
+            mma_ss_elect(tO + j * N, dCt + s * (L::kPair >> 4) + kk * 128, dP + kk * L::kPRow, idesc_o,
+                         (e > walk.e0 || kk > 0) ? 1u : 0u);
+          mma_commit_elect(c_empty(s));
         }
-        __syncwarp();
-        Rj += blocks;
+        mma_commit_elect(o_done);
       }
     }
     __syncwarp();
@@ -505,6 +509,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           }
           if (!meet_all()) { ok = false; break; }
         }
+
         uint32_t pk[2 * K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -549,9 +554,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         if (warp == 2 && lane == 0) mbar_arrive(r_empty(R % kRopes));
+
         lat_arrive(p_full, lane);
       }
       if (!ok) break;
+
       // The piece's sums meet in `parts`; its O^T and LSE, or its record (O not divided by the sum).
 #pragma unroll
       for (int k = 0; k < 2 * K; ++k) {
@@ -575,6 +582,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       }
       if (!meet_all() || !lat_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
       tc_fence_after();
+
       // Eight rows of a block at a time, a lane a number of the latent.
       const int d = quarter * 32 + lane;
 #pragma unroll 1
@@ -601,6 +609,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         __syncwarp();                                            // (the reads of TMEM are the warp's)
       }
       tc_fence_before();
+
       if (!meet_all()) { ok = false; break; }                    // factor and parts are read
     }
   }
@@ -613,76 +622,126 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   }
 }
 
-// Merges the records of the cut sequences: block (c, row) takes one query row of the sequence that run c starts and
-// does not finish, if there is one (plan[c]: sequence, past the last run). Half of the block takes every second
-// record, four columns a thread.
-constexpr int kCombineThreads = 256;
-__global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const LatentDecodeArgs a, int tile_rows) {
-  __shared__ float weight[kMaxLatentRuns];
-  __shared__ float4 other[kCombineThreads / 2];
-  __shared__ float stats[2];
+// Merges the records of the cut sequences: block (c, y) takes rows of the sequence that run c starts and does not finish, if
+// there is one (plan[c]: sequence, past the last run). dc / 4 threads hold a row, four columns each, and add the records in
+// order, the next one's numbers on their way while one is added; `passes` rows a thread. kWide, for calls whose sequences spread
+// over many runs: with more than kFewRecords records the block's warps take every eighth each, and add up in the order of the
+// warps. (The other form has no shared memory, so that its blocks are there before the decode kernel's leave the SM.)
+constexpr int kCombineThreads = 256, kFewRecords = 8;
+__device__ __forceinline__ void merge_record(float &M, float &sum, float4 &acc, float2 ml, float4 x) {
+  if (ml.y == 0.f) return;                                      // a record that saw nothing holds anything but this
+  const float m = fmaxf(M, ml.x), f0 = ex2_approx(M - m), f1 = ex2_approx(ml.x - m);
+  M = m;
+  sum = sum * f0 + ml.y * f1;
+  acc.x = acc.x * f0 + x.x * f1, acc.y = acc.y * f0 + x.y * f1, acc.z = acc.z * f0 + x.z * f1, acc.w = acc.w * f0 + x.w * f1;
+}
+template <bool kWide>
+__global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const LatentDecodeArgs a, int tile_rows, int passes) {
   grid_dep_launch();
   grid_dep_wait();
   const int c0 = blockIdx.x;
   const int2 plan = a.plan[c0];
   if (plan.y == 0) return;
-  const int row = blockIdx.y, rt = row / tile_rows, r = row - rt * tile_rows, records = plan.y - c0;
-  auto rec_of = [&](int k) {
-    return (2 * (static_cast<size_t>(c0 + k) * a.row_tiles + rt) + (k == 0 ? 1 : 0)) * tile_rows + r;
+  const int records = plan.y - c0, quads = a.dc / 4, rows = a.n * a.nh;
+  auto rec_of = [&](int k, int row) {
+    const int rt = row / tile_rows;
+    return (2 * (static_cast<size_t>(c0 + k) * a.row_tiles + rt) + (k == 0 ? 1 : 0)) * tile_rows + (row - rt * tile_rows);
   };
-  if (threadIdx.x < 32) {
-    float M = -FLT_MAX, sum = 0.f;
-    for (int k = threadIdx.x; k < records; k += 32) {
-      const float2 ml = a.ws_ml[rec_of(k)];
-      if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  auto put = [&](int row, int i, float M, float sum, float4 acc) {
+    const size_t out = static_cast<size_t>(plan.x) * rows + row;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint2 *>(a.o + out * a.dc + 4 * i) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (i == 0) a.lse[out] = sum != 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+  };
+  const int each = kCombineThreads / quads, row0 = static_cast<int>(blockIdx.y) * each * passes;
+  if (!kWide || records <= kFewRecords) {
+    const int sub = threadIdx.x / quads, i = threadIdx.x - sub * quads;
+    if (sub >= each) return;                                    // (dc = 384: some threads are over)
+#pragma unroll 2
+    for (int p = 0; p < passes; ++p) {
+      const int row = row0 + p * each + sub;
+      if (row >= rows) break;
+      float M = -FLT_MAX, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      size_t rec = rec_of(0, row);
+      float2 ml = a.ws_ml[rec];
+      float4 x = *reinterpret_cast<const float4 *>(a.ws_o + rec * a.dc + 4 * i);
+#pragma unroll 1
+      for (int k = 0; k < records; ++k) {
+        const float2 ml_here = ml;
+        const float4 x_here = x;
+        if (k + 1 < records) {
+          rec = rec_of(k + 1, row);
+          ml = a.ws_ml[rec];
+          x = *reinterpret_cast<const float4 *>(a.ws_o + rec * a.dc + 4 * i);
+        }
+        merge_record(M, sum, acc, ml_here, x_here);
+      }
+      put(row, i, M, sum, acc);
     }
-    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    for (int k = threadIdx.x; k < records; k += 32) {
-      const float2 ml = a.ws_ml[rec_of(k)];
-      const float w = ml.y != 0.f ? ex2_approx(ml.x - M) : 0.f;   // a record that saw nothing counts 0
-      weight[k] = w;
-      sum = fmaf(ml.y, w, sum);
+    return;
+  }
+  if constexpr (kWide) {
+    __shared__ float4 part[8][128];
+    __shared__ float2 part_ml[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int row = row0; row < min(row0 + each * passes, rows); ++row) {
+      float M = -FLT_MAX, sum = 0.f;
+      float4 acc[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int k = warp; k < records; k += 8) {
+        const size_t rec = rec_of(k, row);
+        const float2 ml = a.ws_ml[rec];
+        float4 x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          x[q] = lane + 32 * q < quads ? *reinterpret_cast<const float4 *>(a.ws_o + rec * a.dc + 4 * (lane + 32 * q))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        float m1 = M, s1 = sum;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          m1 = M, s1 = sum;
+          merge_record(m1, s1, acc[q], ml, x[q]);
+        }
+        M = m1, sum = s1;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part[warp][lane + 32 * q] = acc[q];
+      if (lane == 0) part_ml[warp] = make_float2(M, sum);
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < quads) {
+        M = -FLT_MAX, sum = 0.f;
+        float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) merge_record(M, sum, all, part_ml[w], part[w][threadIdx.x]);
+        put(row, threadIdx.x, M, sum, all);
+      }
+      __syncthreads();                                            // before the next row's parts
     }
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (threadIdx.x == 0) stats[0] = M, stats[1] = sum;
   }
-  __syncthreads();
-  const int half = threadIdx.x / (kCombineThreads / 2), i = threadIdx.x % (kCombineThreads / 2);
-  const bool mine = 4 * i < a.dc;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (mine) {
-#pragma unroll 4
-    for (int k = half; k < records; k += 2) {
-      const float w = weight[k];
-      const float4 x = *reinterpret_cast<const float4 *>(a.ws_o + rec_of(k) * a.dc + 4 * i);
-      if (w != 0.f) acc.x = fmaf(x.x, w, acc.x), acc.y = fmaf(x.y, w, acc.y), acc.z = fmaf(x.z, w, acc.z), acc.w = fmaf(x.w, w, acc.w);
-    }
-  }
-  if (half == 1) other[i] = acc;
-  __syncthreads();
-  if (half == 1) return;
-  const size_t out = static_cast<size_t>(plan.x) * a.n * a.nh + row;
-  const float sum = stats[1], inv = sum != 0.f ? 1.f / sum : 0.f;
-  if (mine) {
-    const float4 z = other[i];
-    *reinterpret_cast<uint2 *>(a.o + out * a.dc + 4 * i) = make_uint2(pack_bf16x2((acc.x + z.x) * inv, (acc.y + z.y) * inv),
-                                                                    pack_bf16x2((acc.z + z.z) * inv, (acc.w + z.w) * inv));
-  }
-  if (i == 0) a.lse[out] = sum != 0.f ? (stats[0] + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int N>
-cudaError_t launch_latent_n(const CUtensorMap &mq, const CUtensorMap &mc, const LatentDecodeArgs &a, int groups,
-                            cudaStream_t stream) {
+cudaError_t launch_latent_n(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, cudaStream_t stream) {
   using L = LatLayout<N>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t err = allow_smem(latent_decode_kernel<N>, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
   err = launch_pdl(latent_decode_kernel<N>, static_cast<unsigned>(groups) * a.row_tiles, kLatThreads, L::kDynBytes, stream,
-                   mq, mc, a);
+                   maps.q, maps.pages, maps.q_latents, maps.latents, a);
   if (err != cudaSuccess || groups == 1) return err;
-  return launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(groups - 1), static_cast<unsigned>(a.n * a.nh)),
-                    kCombineThreads, 0, stream, a, N);
+  // Rows a thread: as many as make one wave of blocks; one where sequences spread over many runs.
+  const int rows = a.n * a.nh, each = kCombineThreads / (a.dc / 4);
+  const long long blocks = static_cast<long long>(groups - 1) * ((rows + each - 1) / each);
+  const bool wide = groups >= 4 * a.B;
+  const int passes = wide ? 1 : static_cast<int>(min(max(blocks / (152 * 8), 1ll), 8ll));
+  return launch_pdl(wide ? latent_combine_kernel<true> : latent_combine_kernel<false>,
+                    dim3(static_cast<unsigned>(groups - 1), static_cast<unsigned>((rows + each * passes - 1) / (each * passes))),
+                    kCombineThreads, 0, stream, a, N, passes);
 }
 
 }  // namespace
@@ -707,11 +766,11 @@ size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int 
          static_cast<size_t>(groups) * sizeof(int2);
 }
 
-cudaError_t launch_latent_decode(const CUtensorMap &mq, const CUtensorMap &mc, const LatentDecodeArgs &a, int groups,
-                                 int tile_rows, cudaStream_t stream) {
-  if (tile_rows == 16) return launch_latent_n<16>(mq, mc, a, groups, stream);
-  if (tile_rows == 32) return launch_latent_n<32>(mq, mc, a, groups, stream);
-  return launch_latent_n<64>(mq, mc, a, groups, stream);
+cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int tile_rows,
+                                 cudaStream_t stream) {
+  if (tile_rows == 16) return launch_latent_n<16>(maps, a, groups, stream);
+  if (tile_rows == 32) return launch_latent_n<32>(maps, a, groups, stream);
+  return launch_latent_n<64>(maps, a, groups, stream);
 }
 
 }  // namespace xattn

@@ -313,6 +313,20 @@ xattn_status make_map_rows(CUtensorMap *map, const void *ptr, int outer, int row
   return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
+// Map over the first dc columns of [outer, rows, width] as [outer, dc / 64, rows, 64]: box = 64 columns by box_rows rows, `subs`
+// times (sub-tiles one behind the other).
+xattn_status make_map_latents(CUtensorMap *map, const void *ptr, int outer, int rows, int dc, int width, int box_rows, int subs) {
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(dc / 64), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t row = static_cast<cuuint64_t>(width) * 2;
+  const cuuint64_t strides[3] = {row, 128, row * rows};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(subs), 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
+}
+
 // The fp32 window kernels' largest grid: four blocks per 32 rows of a head.
 bool window_f32_grid_ok(int B, int S, int nh) {
   return static_cast<double>(B) * nh * ((S + 31) / 32) * 4 < 0x1p31;
@@ -874,9 +888,12 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
   a.row_tiles = (n * nh + tile_rows - 1) / tile_rows;
   a.scale_log2 = scale * kLog2e;
   a.status = dev->status, a.timeout_ns = wait_limit_ns();
-  CUtensorMap mq, mc;
-  XATTN_TRY(make_map_rows(&mq, q, B, n * nh, dc + dr, tile_rows));
-  XATTN_TRY(make_map_rows(&mc, pages, num_pages, page_size, dc + dr, page_size < 64 ? page_size : 64));
+  const int box_rows = page_size < 64 ? page_size : 64;
+  LatentDecodeMaps maps;
+  XATTN_TRY(make_map_rows(&maps.q, q, B, n * nh, dc + dr, tile_rows));
+  XATTN_TRY(make_map_latents(&maps.q_latents, q, B, n * nh, dc, dc + dr, tile_rows, dc / 64));
+  XATTN_TRY(make_map_rows(&maps.pages, pages, num_pages, page_size, dc + dr, box_rows));
+  XATTN_TRY(make_map_latents(&maps.latents, pages, num_pages, page_size, dc, dc + dr, box_rows, 2));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int groups = latent_groups(a, dev->sms);
   void *base = nullptr;
@@ -885,7 +902,7 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
   a.ws_o = static_cast<float *>(base);
   a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + records * dc);
   a.plan = reinterpret_cast<int2 *>(a.ws_ml + records);
-  xattn_status r = cuda_status(launch_latent_decode(mq, mc, a, groups, tile_rows, st));
+  xattn_status r = cuda_status(launch_latent_decode(maps, a, groups, tile_rows, st));
   const cudaError_t fe = cudaFreeAsync(base, st);
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
   return r;

@@ -236,9 +236,13 @@ cudaError_t launch_latent_fwd(const LatentMaps &maps, const LatentArgs &a, int s
 cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
                               cudaStream_t stream);
 
-// Absorbed form (attn_latent_decode.cu): n new tokens a sequence over a paged cache of rows of dc + dr numbers. mq: map
-// over the queries, boxes of 64 columns of tile_rows rows of one sequence; mc: over the pool, boxes of 64 columns of
-// min(page_size, 64) rows of one page. The scratch, latent_decode_workspace_bytes(), is ws_o, ws_ml and plan.
+// Absorbed form (attn_latent_decode.cu): n new tokens a sequence over a paged cache of rows of dc + dr numbers. Maps: over the
+// queries, boxes of 64 columns of tile_rows rows of one sequence, and (q_latents) of all dc columns of them; over the pool, boxes
+// of 64 columns of min(page_size, 64) rows of one page, and (latents) of two such side by side in the first dc columns. The
+// scratch, latent_decode_workspace_bytes(), is ws_o, ws_ml and plan.
+struct LatentDecodeMaps {
+  CUtensorMap q, q_latents, pages, latents;
+};
 constexpr int kMaxLatentRuns = 256;
 struct LatentDecodeArgs {
   const int *page_table, *ctx_lens;
@@ -255,8 +259,8 @@ struct LatentDecodeArgs {
 int latent_tile_rows(int n, int nh);
 int latent_groups(const LatentDecodeArgs &a, int sms);
 size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int tile_rows);
-cudaError_t launch_latent_decode(const CUtensorMap &mq, const CUtensorMap &mc, const LatentDecodeArgs &a, int groups,
-                                 int tile_rows, cudaStream_t stream);
+cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int tile_rows,
+                                 cudaStream_t stream);
 
 // Page tables, slot maps and rows written by slot (cache_tables.cu).
 struct ReserveArgs {
