@@ -43,17 +43,18 @@ template <int N>
 struct LatLayout {
   static constexpr uint32_t kSub = kTilePos * 128;               // a sub-tile of 64 columns
   static constexpr uint32_t kPair = 2 * kSub;
-  static constexpr int kPairs = N == 64 ? 8 : (N == 32 ? 10 : 11);
+  static constexpr int kPairs = N == 64 ? 8 : 10;
+  static constexpr int kQBufs = N == 16 ? 2 : 1;                 // query rows of this piece, and of the next
   static constexpr int kRopes = N == 64 ? 2 : 3;
   static constexpr uint32_t kQSub = N * 128;                     // 64 columns of the query rows
   static constexpr uint32_t kPRow = N * 2;
   static constexpr uint32_t kSwizzleP = N == 64 ? kSwizzle128 : (N == 32 ? kSwizzle64 : kSwizzle32);
   static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kP = kQ + 9 * kQSub;
+  static constexpr uint32_t kP = kQ + kQBufs * 9 * kQSub;
   static constexpr uint32_t kC = kP + kTilePos * kPRow;
   static constexpr uint32_t kR = kC + kPairs * kPair;
   static constexpr uint32_t kBars = kR + kRopes * kSub;
-  static constexpr int kNumBars = 2 * kPairs + 2 * kRopes + 9;
+  static constexpr int kNumBars = 2 * kPairs + 2 * kRopes + 7 + 2 * kQBufs;
   static constexpr uint32_t kBase = (kBars + 8 * kNumBars + 15) / 16 * 16;   // float [N] maxima, [N] factors, [4][N] parts
   static constexpr uint32_t kFlags = kBase + 6 * N * 4;
   static constexpr uint32_t kHeld = kFlags + 2 * kSoftWarps * 4;             // per rope slot: boxes that hold a page
@@ -220,7 +221,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   constexpr int kB = 2 * kPairs + 2 * kRopes;
   auto s_full = [&](int x) { return bar(kB + x); };
   auto s_free = [&](int x) { return bar(kB + 2 + x); };
-  const uint32_t p_full = bar(kB + 4), o_done = bar(kB + 5), q_full = bar(kB + 6), q_empty = bar(kB + 7), meet = bar(kB + 8);
+  const uint32_t p_full = bar(kB + 4), o_done = bar(kB + 5), meet = bar(kB + 6);
+  constexpr int kQBufs = L::kQBufs;
+  auto q_full = [&](int x) { return bar(kB + 7 + x); };
+  auto q_empty = [&](int x) { return bar(kB + 7 + kQBufs + x); };
   float *base = reinterpret_cast<float *>(smem + L::kBase), *factor = base + N, *parts = base + 2 * N;
   volatile int *flags = reinterpret_cast<volatile int *>(smem + L::kFlags);
   volatile uint32_t *held_boxes = reinterpret_cast<volatile uint32_t *>(smem + L::kHeld);
@@ -238,8 +242,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     }
     mbar_init(p_full, kSoftWarps);
     mbar_init(o_done, 1);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int x = 0; x < kQBufs; ++x) {
+      mbar_init(q_full(x), 1);
+      mbar_init(q_empty(x), 1);
+    }
     mbar_init(meet, kSoftWarps);
     fence_mbar_init();
     tma_prefetch_desc(&mq);
@@ -262,7 +268,6 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   const int group = static_cast<int>(blockIdx.x) / a.row_tiles, rt = static_cast<int>(blockIdx.x) - group * a.row_tiles;
   const int groups = static_cast<int>(gridDim.x) / a.row_tiles, blocks = a.dc / 128;
   LatWalk walk;
-
   const LatRuns runs = lat_start(a, group, groups, lane, walk);
 
 
@@ -273,10 +278,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     int R = 0, Rj = 0, issued_c = 0, issued_r = 0, pieces = 0;
     bool ok = true;
     while (ok && lat_piece(walk, a)) {
-      if (!lat_wait(q_empty, (pieces & 1) ^ 1, ctl)) break;
-      mbar_expect_tx_elect(q_full, (2 * blocks + 1) * L::kQSub);
-      tma_load_4d_elect(sQ, &mqc, q_full, 0, rt * N, 0, walk.b);
-      tma_load_4d_elect(sQ + 2 * blocks * L::kQSub, &mq, q_full, a.dc, rt * N, walk.b, 0);
+      const int qb = pieces % kQBufs;
+      if (!lat_wait(q_empty(qb), ((pieces / kQBufs) & 1) ^ 1, ctl)) break;
+      mbar_expect_tx_elect(q_full(qb), (2 * blocks + 1) * L::kQSub);
+      tma_load_4d_elect(sQ + qb * 9 * L::kQSub, &mqc, q_full(qb), 0, rt * N, 0, walk.b);
+      tma_load_4d_elect(sQ + (9 * qb + 2 * blocks) * L::kQSub, &mq, q_full(qb), a.dc, rt * N, walk.b, 0);
       ++pieces;
       const int *table = a.page_table + static_cast<size_t>(walk.b) * a.max_pages;
       const int end = walk.ctx + a.n;
@@ -332,19 +338,21 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     }
     __syncwarp();
     // Every copy in flight has landed before the CTA can exit.
-    if (pieces > 0) mbar_drain(q_full, (pieces - 1) & 1, ctl);
+    for (int r = max(pieces - kQBufs, 0); r < pieces; ++r) mbar_drain(q_full(r % kQBufs), (r / kQBufs) & 1, ctl);
     for (int r = max(issued_c - kPairs, 0); r < issued_c; ++r) mbar_drain(c_full(r % kPairs), (r / kPairs) & 1, ctl);
     for (int r = max(issued_r - kRopes, 0); r < issued_r; ++r) mbar_drain(r_full(r % kRopes), (r / kRopes) & 1, ctl);
   } else if (warp == 1) {
     // ---------------- issuer of S^T = C Q^T ----------------
     constexpr uint32_t idesc_s = idesc_bf16_f32(64, N, false, false);
-    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
+    const uint64_t dQ0 = smem_desc(sQ, 16, 1024, kSwizzle128);
     const uint64_t dC = smem_desc(sC, 16, 1024, kSwizzle128), dR = smem_desc(sR, 16, 1024, kSwizzle128);
     const int rope_steps = a.dr / 16;
     int R = 0, Rj = 0, piece = 0;
     bool ok = true;
     while (ok && lat_piece(walk, a)) {
-      if (!lat_wait(q_full, piece & 1, ctl)) break;
+      const int qb = piece % kQBufs;
+      if (!lat_wait(q_full(qb), (piece / kQBufs) & 1, ctl)) break;
+      const uint64_t dQ = dQ0 + qb * 9 * (L::kQSub >> 4);
 #pragma unroll 1
       for (int e = walk.e0; e < walk.e1; ++e) {
         if (!lat_wait(s_free(R & 1), ((R >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         for (int kk = 0; kk < rope_steps; ++kk)
           mma_ss_elect(d, dR + s * (L::kSub >> 4) + kk * 2, dQ + 2 * blocks * (L::kQSub >> 4) + kk * 2, idesc_s, 1u);
         mma_commit_elect(s_full(R & 1));
-        if (e + 1 == walk.e1) mma_commit_elect(q_empty);
+        if (e + 1 == walk.e1) mma_commit_elect(q_empty(qb));
         ++R;
       }
       ++piece;
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             for (int j = tid & 3; j < 2 * blocks; j += 4) {
               uint8_t *row = smem + L::kC + ((R * blocks + j / 2) % kPairs) * L::kPair + (j & 1) * L::kSub + r * 128;
 #pragma unroll
-              for (int v = 0; v < 8; ++v) reinterpret_cast<uint4 *>(row)[v] = make_uint4(0u, 0u, 0u, 0u);
+              for (int v = 0; v < 8; ++v) reinterpret_cast<uint4 *>(row)[(v + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);   // (banks)
             }
           }
         }
@@ -509,7 +517,6 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           }
           if (!meet_all()) { ok = false; break; }
         }
-
         uint32_t pk[2 * K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -554,11 +561,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         if (warp == 2 && lane == 0) mbar_arrive(r_empty(R % kRopes));
-
         lat_arrive(p_full, lane);
       }
       if (!ok) break;
-
       // The piece's sums meet in `parts`; its O^T and LSE, or its record (O not divided by the sum).
 #pragma unroll
       for (int k = 0; k < 2 * K; ++k) {
@@ -582,34 +587,39 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       }
       if (!meet_all() || !lat_wait(o_done, (R - 1) & 1, ctl)) { ok = false; break; }
       tc_fence_after();
-
-      // Eight rows of a block at a time, a lane a number of the latent.
+      // Eight rows of a block a load, a lane a number of the latent; with few rows four loads together.
+      constexpr int kOnce = N == 64 ? 1 : 4;
       const int d = quarter * 32 + lane;
 #pragma unroll 1
-      for (int x = 0; x < blocks * K; ++x) {
-        const int j = x / K, r0 = half * C + (x - j * K) * 8;
-        if (r0 >= rows) continue;
-        uint32_t ov[8];
-        tmem_ld_x8(tO + j * N + r0 + lane_off, ov);
+      for (int x0 = 0; x0 < blocks * K; x0 += kOnce) {
+        uint32_t ov[kOnce][8];
+        auto row_of = [&](int x) { return half * C + (x - x / K * K) * 8; };
+#pragma unroll
+        for (int y = 0; y < kOnce; ++y)
+          if (x0 + y < blocks * K) tmem_ld_x8(tO + (x0 + y) / K * N + row_of(x0 + y) + lane_off, ov[y]);
         tmem_wait_ld();
-        reg_fence<8>(ov);
-        if (whole) {
-          __nv_bfloat16 *to = a.o + (out + r0) * a.dc + j * 128 + d;
 #pragma unroll
-          for (int c = 0; c < 8; ++c, to += a.dc) {
-            const float f = factor[r0 + c];
-            if (r0 + c < rows) *to = __float2bfloat16_rn(f != 0.f ? __uint_as_float(ov[c]) * f : 0.f);
+        for (int y = 0; y < kOnce; ++y) {
+          reg_fence<8>(ov[y]);
+          const int x = x0 + y, j = x / K, r0 = row_of(x);
+          if (x >= blocks * K || r0 >= rows) continue;
+          if (whole) {
+            __nv_bfloat16 *to = a.o + (out + r0) * a.dc + j * 128 + d;
+#pragma unroll
+            for (int c = 0; c < 8; ++c, to += a.dc) {
+              const float f = factor[r0 + c];
+              if (r0 + c < rows) *to = __float2bfloat16_rn(f != 0.f ? __uint_as_float(ov[y][c]) * f : 0.f);
+            }
+          } else {
+            float *to = a.ws_o + (rec + r0) * a.dc + j * 128 + d;
+#pragma unroll
+            for (int c = 0; c < 8; ++c, to += a.dc)
+              if (r0 + c < rows) *to = __uint_as_float(ov[y][c]);
           }
-        } else {
-          float *to = a.ws_o + (rec + r0) * a.dc + j * 128 + d;
-#pragma unroll
-          for (int c = 0; c < 8; ++c, to += a.dc)
-            if (r0 + c < rows) *to = __uint_as_float(ov[c]);
         }
         __syncwarp();                                            // (the reads of TMEM are the warp's)
       }
       tc_fence_before();
-
       if (!meet_all()) { ok = false; break; }                    // factor and parts are read
     }
   }
