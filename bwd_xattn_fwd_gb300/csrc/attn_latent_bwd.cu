@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a
   a.nD[to] = v.y;
 }
 
-// NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS).
+// NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS). kFull: they are full (dn = dv = 64 NS), so that the
+// products' steps have no conditions (B8 S1024, 12 heads of 64 + 32 / 64: dkv 62 -> 59 us, dq 47 -> 45).
 template <int NS>
 struct DkvLayout {
   static constexpr int kStages = 3;
@@ -95,7 +96,8 @@ struct DkvLayout {
   static constexpr uint32_t kdO = kQ + kStages * (NS + 1) * kQuerySub;
   static constexpr uint32_t kRows = kdO + kStages * NS * kQuerySub;  // stages of -LSE log2 e and -D
   static constexpr uint32_t kBars = kRows + kStages * 2 * kQRows * 4;
-  static constexpr int kNumBars = 2 * kStages + 12;
+  static constexpr int kPlaces = NS == 1 ? 2 : 1;                    // of dP^T and dS^T
+  static constexpr int kNumBars = 2 * kStages + 14;
   static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
@@ -103,8 +105,8 @@ struct DkvLayout {
 };
 
 // Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 P^T; 8-11 dS^T; a thread is a key row.
-// TMEM: dV [0, 128) | dK [128, 320), its shared part from 256 on | S^T places [320, 384), [384, 448) | dP^T [448, 512).
-template <int NS>
+// TMEM (columns): dV 64 NS | dK 64 NS, its shared part 64 | two places of S^T, 64 each | one (NS = 1: two) of dP^T.
+template <int NS, bool kFull>
 __global__ void __maxnreg__(168)
     latent_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
                       const __grid_constant__ CUtensorMap mrope, const __grid_constant__ CUtensorMap mdo, const LatentArgs a) {
@@ -114,7 +116,7 @@ __global__ void __maxnreg__(168)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dkv_smem) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int S = a.S, nh = a.nh, dn = a.dn, dr = a.dr, dv = a.dv;
+  const int S = a.S, nh = a.nh, dn = kFull ? 64 * NS : a.dn, dr = a.dr, dv = kFull ? 64 * NS : a.dv;
   const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
   const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
   const int num_n = (S + kTileRows - 1) / kTileRows, num_q = (S + kQRows - 1) / kQRows, BH = a.B * nh;
@@ -136,9 +138,14 @@ __global__ void __maxnreg__(168)
   auto q_empty = [&](int s) { return bar(kStages + s); };
   constexpr int kB = 2 * kStages;
   const uint32_t k_full = bar(kB), v_full = bar(kB + 1), k_empty = bar(kB + 2), v_empty = bar(kB + 3), acc_done = bar(kB + 4),
-                 acc_free = bar(kB + 5), dp_full = bar(kB + 6), ds_full = bar(kB + 7);
-  auto s_full = [&](int x) { return bar(kB + 8 + x); };
-  auto p_full = [&](int x) { return bar(kB + 10 + x); };
+                 acc_free = bar(kB + 5);
+  auto s_full = [&](int x) { return bar(kB + 6 + x); };
+  auto p_full = [&](int x) { return bar(kB + 8 + x); };
+  // dP^T's (and dS^T's) place and its phase, of tile g.
+  constexpr int kPlaces = L::kPlaces;
+  auto dp_full = [&](int g) { return bar(kB + 10 + g % kPlaces); };
+  auto ds_full = [&](int g) { return bar(kB + 12 + g % kPlaces); };
+  auto dp_phase = [](int g) { return static_cast<uint32_t>((g / kPlaces) & 1); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
@@ -155,9 +162,9 @@ __global__ void __maxnreg__(168)
     mbar_init(v_empty, 1);
     mbar_init(acc_done, 1);
     mbar_init(acc_free, 256);
-    mbar_init(dp_full, 1);
-    mbar_init(ds_full, 128);
     for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(kB + 10 + x), 1);
+      mbar_init(bar(kB + 12 + x), 128);
       mbar_init(s_full(x), 1);
       mbar_init(p_full(x), 128);
     }
@@ -177,8 +184,10 @@ __global__ void __maxnreg__(168)
   grid_dep_launch();
   grid_dep_wait();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
-  const uint32_t tdV = tmem, tdK = tmem + 128, tdKr = tmem + 256, tdP = tmem + 448;
-  auto tS = [&](int x) { return tmem + 320u + 64u * x; };
+  constexpr uint32_t kAcc = 64 * NS;                                  // columns of dV, and of dK
+  const uint32_t tdV = tmem, tdK = tmem + kAcc, tdKr = tmem + 2 * kAcc;
+  auto tS = [&](int x) { return tmem + 2 * kAcc + 64u + 64u * x; };
+  auto tdP = [&](int g) { return tmem + 2 * kAcc + 192u + 64u * (g % kPlaces); };
 
   if (warp == 0) {
     // ---------------- TMA producer (converged warp, one elected lane issues) ----------------
@@ -240,7 +249,7 @@ __global__ void __maxnreg__(168)
     // ---------------- MMA issuer ----------------
     // One thread, so one order: dV(t), dK(t), dP^T(t + 1), S^T(t + 2). dK -> dP^T -> dS^T -> dK is the longest chain (dP^T and
     // dS^T have one place), and S^T, dV fill the time that the dS warps take. (With two issuers the pipe took S^T between dK
-    // and dP^T: 2430 cycles a tile.)
+    // and dP^T: 2430 cycles a tile, 2200 so.) With two places dP^T(t + 1) goes first: it need not wait for dK(t).
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
     const uint32_t idesc_dv = idesc_bf16_f32(128, dv, false, true), idesc_dk = idesc_bf16_f32(128, dn, false, true),
                    idesc_dr = idesc_bf16_f32(128, dr, false, true);
@@ -278,8 +287,8 @@ __global__ void __maxnreg__(168)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (4 * c + kk < dv_steps)
-              mma_ss(tdP, dV + c * (kKeySub >> 4) + kk * 2, o + c * (kQuerySub >> 4) + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
-        mma_commit(dp_full);
+              mma_ss(tdP(g), dV + c * (kKeySub >> 4) + kk * 2, o + c * (kQuerySub >> 4) + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+        mma_commit(dp_full(g));
         if (last) mma_commit(v_empty);
       }
       __syncwarp();
@@ -307,6 +316,7 @@ __global__ void __maxnreg__(168)
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
         const int s = g % kStages;
+        if (kPlaces == 2 && t + 1 < T) issue_dp(g + 1, t + 2 == T);   // (its place's dK went before; the tile has landed)
         if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
@@ -316,26 +326,24 @@ __global__ void __maxnreg__(168)
             mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
         }
         __syncwarp();
-        if (!warp_wait(ds_full, g & 1, ctl)) { ok = false; break; }
+        if (!warp_wait(ds_full(g), dp_phase(g), ctl)) { ok = false; break; }
         tc_fence_after();
         if (elect_one()) {
           const uint64_t q = dQt + s * (NS + 1) * (kQuerySub >> 4);
 #pragma unroll
           for (int kk = 0; kk < kQRows / 16; ++kk) {
-            mma_ts(tdK, tdP + kk * 8, q + kk * 128, idesc_dk, (t > 0 || kk > 0) ? 1u : 0u);
-            mma_ts(tdKr, tdP + kk * 8, q + NS * (kQuerySub >> 4) + kk * 128, idesc_dr, (t > 0 || kk > 0) ? 1u : 0u);
+            mma_ts(tdK, tdP(g) + kk * 8, q + kk * 128, idesc_dk, (t > 0 || kk > 0) ? 1u : 0u);
+            mma_ts(tdKr, tdP(g) + kk * 8, q + NS * (kQuerySub >> 4) + kk * 128, idesc_dr, (t > 0 || kk > 0) ? 1u : 0u);
           }
           mma_commit(q_empty(s));
           if (t + 1 == T) mma_commit(acc_done);
         }
         __syncwarp();
-        if (t + 1 < T) {
-          issue_dp(g + 1, t + 2 == T);                              // (tile g + 1 has landed: its S^T went before)
-          if (t + 2 < T) {
-            if (!landed(g + 2)) { ok = false; break; }
-            tc_fence_after();
-            issue_s(g + 2, t + 3 == T);
-          }
+        if (kPlaces == 1 && t + 1 < T) issue_dp(g + 1, t + 2 == T);   // (the tile has landed: its S^T went before)
+        if (t + 2 < T) {
+          if (!landed(g + 2)) { ok = false; break; }
+          tc_fence_after();
+          issue_s(g + 2, t + 3 == T);
         }
       }
       ++units;
@@ -394,11 +402,12 @@ __global__ void __maxnreg__(168)
         // ---------------- dS^T = P^T (dP^T - D) ----------------
 #pragma unroll 1
         for (int t = 0; t < T; ++t, ++g) {
-          if (!warp_wait(dp_full, g & 1, ctl)) { ok = false; break; }
+          if (!warp_wait(dp_full(g), dp_phase(g), ctl)) { ok = false; break; }
           tc_fence_after();
           uint32_t r[64], p[32];
-          tmem_ld_x32(tdP + lane_off, r);
-          tmem_ld_x32(tdP + lane_off + 32, r + 32);
+          const uint32_t at = tdP(g) + lane_off;
+          tmem_ld_x32(at, r);
+          tmem_ld_x32(at + 32, r + 32);
           if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) {
             tmem_wait_ld();
             ok = false;
@@ -421,10 +430,10 @@ __global__ void __maxnreg__(168)
             p[c / 2] = pack_bf16x2(x0, x1);
             p[c / 2 + 1] = pack_bf16x2(x2, x3);
           }
-          tmem_st_x32(tdP + lane_off, p);
+          tmem_st_x32(at, p);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(ds_full);
+          mbar_arrive(ds_full(g));
         }
       }
       // The unit's sums: the P warps write dV, the dS warps dK.
@@ -499,7 +508,7 @@ struct LatentDqLayout {
 
 // Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
 // TMEM: S [0, 128) | dP [128, 256), dS bf16 over [128, 160) and [192, 224) | dO bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448.
-template <int NS>
+template <int NS, bool kFull>
 __global__ void __maxnreg__(168)
     latent_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
                      const __grid_constant__ CUtensorMap mrope, const LatentArgs a) {
@@ -509,7 +518,7 @@ __global__ void __maxnreg__(168)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dq_smem) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int S = a.S, nh = a.nh, dn = a.dn, dr = a.dr, dv = a.dv;
+  const int S = a.S, nh = a.nh, dn = kFull ? 64 * NS : a.dn, dr = a.dr, dv = kFull ? 64 * NS : a.dv;
   const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
   const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
   const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh;
@@ -758,20 +767,20 @@ __global__ void __launch_bounds__(256) latent_rope_kernel(const LatentArgs a) {
       make_uint2(pack_bf16x2(g.x * a.scale, g.y * a.scale), pack_bf16x2(g.z * a.scale, g.w * a.scale));
 }
 
-template <int NS>
+template <int NS, bool kFull>
 cudaError_t launch_latent_bwd_ns(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
                                  cudaStream_t stream) {
   using LK = DkvLayout<NS>;
   using LQ = LatentDqLayout<NS>;
   static std::atomic<unsigned long long> allowed_k{0}, allowed_q{0};
-  cudaError_t err = allow_smem(latent_dkv_kernel<NS>, LK::kDynBytes, allowed_k);
-  if (err == cudaSuccess) err = allow_smem(latent_dq_kernel<NS>, LQ::kDynBytes, allowed_q);
+  cudaError_t err = allow_smem(latent_dkv_kernel<NS, kFull>, LK::kDynBytes, allowed_k);
+  if (err == cudaSuccess) err = allow_smem(latent_dq_kernel<NS, kFull>, LQ::kDynBytes, allowed_q);
   if (err != cudaSuccess) return err;
   const long long num_n = (a.S + kTileRows - 1) / kTileRows, units = num_n * a.B * a.nh;
-  err = launch_pdl(latent_dkv_kernel<NS>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LK::kDynBytes, stream,
+  err = launch_pdl(latent_dkv_kernel<NS, kFull>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LK::kDynBytes, stream,
                    q64.q, q128.kv, q128.rope, q64.dO, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(latent_dq_kernel<NS>, static_cast<unsigned>(units), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
+  return launch_pdl(latent_dq_kernel<NS, kFull>, static_cast<unsigned>(units), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
                     q128.rope, a);
 }
 
@@ -793,8 +802,11 @@ cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, con
   cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>(a.B) * (padded_rows(a.S) / kRowsPos) * head_blocks,
                                256, 0, stream, a, head_blocks);
   if (err != cudaSuccess) return err;
-  err = a.dn <= 64 && a.dv <= 64 ? launch_latent_bwd_ns<1>(q64, q128, a, sms, stream)
-                                 : launch_latent_bwd_ns<2>(q64, q128, a, sms, stream);
+  const bool one = a.dn <= 64 && a.dv <= 64;
+  if (a.dn == (one ? 64 : 128) && a.dv == a.dn)
+    err = one ? launch_latent_bwd_ns<1, true>(q64, q128, a, sms, stream) : launch_latent_bwd_ns<2, true>(q64, q128, a, sms, stream);
+  else
+    err = one ? launch_latent_bwd_ns<1, false>(q64, q128, a, sms, stream) : launch_latent_bwd_ns<2, false>(q64, q128, a, sms, stream);
   if (err != cudaSuccess) return err;
   const size_t threads = static_cast<size_t>(a.B) * a.S * (a.dr / 4);
   return launch_pdl(latent_rope_kernel, static_cast<unsigned>((threads + 255) / 256), 256, 0, stream, a);

@@ -13,8 +13,10 @@
 //     fetched when P V(n - 1) has ended, right before it is needed.) Where dn, dv <= 64: three whole stages.
 //   * P V is a product a sub-tile (P from TMEM: 32 cycles a K step and 64 columns, as much as half of one over 128), so V's
 //     two may lie anywhere in the ring.
-// Roundings: P to bf16, V's type, before P V; o to bf16. Exponentials as in attn_fwd_sm103.cu.
-// TMEM: S_A [0,128) S_B [128,256) fp32, P over each one's first 64 columns | O_A [256,384) O_B [384,512).
+// Roundings: P to bf16, V's type, before P V; o to bf16. All exponentials on the special-function unit: one pair in eight on the FMA
+// pipe, as in attn_fwd_sm103.cu, was 1 % slower here, one in four 5 %.
+// TMEM: S_A [0,128) S_B [128,256) fp32 | O_A, O_B from 256, 64 NS columns each | NS = 1: P_A [384,448) P_B [448,512), so that the
+// next scores are issued as soon as these are read; NS = 2: P_X over the first half of S_X, the next scores behind P V.
 #include <type_traits>
 
 #include "sm103_ptx.cuh"
@@ -32,6 +34,7 @@ struct LatentFwdLayout {
   static constexpr int kBlocks = NS == 2 ? 8 : 9;                  // ring of sub-tiles
   static constexpr int kEach = 2 * NS + 1;                         // of one K and V tile
   static constexpr int kDepth = NS == 2 ? 2 : 3;                   // barriers of K, and of V
+  static constexpr bool kAliasP = NS == 2;
   static constexpr uint32_t kQ = 0;                                // Q_A, Q_B
   static constexpr uint32_t kRing = 2 * (NS + 1) * kSubTile;
   static constexpr uint32_t kBars = kRing + kBlocks * kSubTile;
@@ -43,34 +46,13 @@ struct LatentFwdLayout {
   static_assert(kDynBytes > 114 * 1024, "one CTA an SM: each holds all TMEM columns");
 };
 
-// 2^x for a pair on the FMA pipe: x = j + f with j = rint(x) and |f| <= 1/2 (x clamped
-// at -126), 2^f from a cubic fitted to it on [-1/2, 1/2] by least squares on Chebyshev
-// nodes (relative error below 8e-5), and j added into the exponent field.
-__device__ __forceinline__ void exp2_fma2(float x0, float x1, float &y0, float &y1) {
-  constexpr float kRound = 12582912.f;   // 1.5 * 2^23: x + kRound is rint(x) in the low bits
-  constexpr float c0 = 0.9999279975891113f, c1 = 0.6932597756385803f;
-  constexpr float c2 = 0.24261167645454407f, c3 = 0.05517822131514549f;
-  x0 = fmaxf(x0, -126.f);
-  x1 = fmaxf(x1, -126.f);
-  float j0, j1, t0, t1, f0, f1, p0, p1;
-  fadd2(j0, j1, x0, x1, kRound, kRound);
-  fadd2(t0, t1, j0, j1, -kRound, -kRound);
-  ffma2(f0, f1, t0, t1, -1.f, -1.f, x0, x1);
-  ffma2(p0, p1, f0, f1, c3, c3, c2, c2);
-  ffma2(p0, p1, p0, p1, f0, f1, c1, c1);
-  ffma2(p0, p1, p0, p1, f0, f1, c0, c0);
-  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(j0) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(j1) << 23));
-}
-
-
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
   const bool ok = mbar_wait(bar, parity, ctl);
   return __all_sync(0xffffffffu, ok);
 }
 
 // kNegScale: scale < 0, so the row maximum of the scaled scores is the scaled minimum of the raw ones.
-template <int NS, bool kNegScale>
+template <int NS, bool kFull, bool kNegScale>
 __global__ void __maxnreg__(168)
     latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
                       const __grid_constant__ CUtensorMap mrope, const LatentArgs a) {
@@ -80,7 +62,7 @@ __global__ void __maxnreg__(168)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_fwd_smem) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int S = a.S, nh = a.nh, dn = a.dn, dv = a.dv;
+  const int S = a.S, nh = a.nh, dn = kFull ? 64 * NS : a.dn, dv = kFull ? 64 * NS : a.dv;
   const int dn_steps = dn / 16, dr_steps = a.dr / 16;
   const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
 
@@ -150,7 +132,8 @@ __global__ void __maxnreg__(168)
   grid_dep_wait();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   auto tS = [&](int x) { return tmem + 128u * x; };
-  auto tO = [&](int x) { return tmem + 256u + 128u * x; };
+  auto tO = [&](int x) { return tmem + 256u + 64u * NS * x; };
+  auto tP = [&](int x) { return L::kAliasP ? tS(x) : tmem + 384u + 64u * x; };
   // Ring position of K(R) and V(R), R counting tiles over all units.
   auto k_block = [](int R, int c) { return (R * L::kEach + c) % kBlocks; };
   auto v_block = [](int R, int c) { return (R * L::kEach + NS + 1 + c) % kBlocks; };
@@ -214,7 +197,7 @@ __global__ void __maxnreg__(168)
     const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128) + x * (NS + 1) * kSubDesc;
     const uint64_t dK = smem_desc(sRing, 16, 1024, kSwizzle128);
     const uint64_t dV = smem_desc(sRing, 8192, 1024, kSwizzle128);       // MN-major
-    const uint32_t tSx = tS(x), tOx = tO(x);
+    const uint32_t tSx = tS(x), tOx = tO(x), tPx = tP(x);
     auto issue_qk = [&](int R) {
       if (elect_one()) {
 #pragma unroll
@@ -238,8 +221,8 @@ __global__ void __maxnreg__(168)
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTileRows / 16; ++kk) {
-          mma_ts(tOx, tSx + kk * 8, v0 + kk * kRowStep, idesc_pv0, (!first || kk > 0) ? 1u : 0u);
-          if (NS == 2 && dv > 64) mma_ts(tOx + 64, tSx + kk * 8, v1 + kk * kRowStep, idesc_pv1, (!first || kk > 0) ? 1u : 0u);
+          mma_ts(tOx, tPx + kk * 8, v0 + kk * kRowStep, idesc_pv0, (!first || kk > 0) ? 1u : 0u);
+          if (NS == 2 && dv > 64) mma_ts(tOx + 64, tPx + kk * 8, v1 + kk * kRowStep, idesc_pv1, (!first || kk > 0) ? 1u : 0u);
         }
         mma_commit(o_done(x));
         mma_commit(v_empty(R % kDepth));
@@ -276,14 +259,24 @@ __global__ void __maxnreg__(168)
         if (!warp_wait(o_free(x), (unitsx - 1) & 1, ctl)) break;
 #pragma unroll 1
         for (int n = 0; n < used; ++n, ++gx) {
-          // P_X(n) lies in S_X's columns: its product first, then the next scores over them.
+          const bool more = n + 1 < used;
+          if constexpr (!L::kAliasP) {
+            if (more) {
+              if (!warp_wait(s_free(x), gx & 1, ctl) || !landed_k(R + n + 1)) { ok = false; break; }
+              tc_fence_after();
+              issue_qk(R + n + 1);
+            }
+          }
           if (!landed_v(R + n) || !warp_wait(p_full(x), gx & 1, ctl)) { ok = false; break; }
           tc_fence_after();
           issue_pv(R + n, n == 0);
-          if (n + 1 < used) {
-            if (!landed_k(R + n + 1)) { ok = false; break; }
-            tc_fence_after();
-            issue_qk(R + n + 1);
+          if constexpr (L::kAliasP) {
+            // P_X(n) lies in S_X's columns: the next scores over them behind its product.
+            if (more) {
+              if (!landed_k(R + n + 1)) { ok = false; break; }
+              tc_fence_after();
+              issue_qk(R + n + 1);
+            }
           }
         }
         if (!ok) break;
@@ -303,7 +296,7 @@ __global__ void __maxnreg__(168)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tSx = tS(x) + lane_off, tOx = tO(x) + lane_off, tPx = tSx;
+    const uint32_t tSx = tS(x) + lane_off, tOx = tO(x) + lane_off, tPx = tP(x) + lane_off;
     const float scale_log2 = a.scale * kLog2e;
     bool ok = true;
 #pragma unroll 1
@@ -369,9 +362,6 @@ __global__ void __maxnreg__(168)
         const float neg_m = -m_use;
         // Exponents, the causal mask on them (-inf -> exact zeros for any scale, 0
         // included), the exponentials, row sums and bf16 P, packed in place into r[0, 64).
-        // One pair in eight of the other tiles' chunks is exponentiated on the FMA pipe
-        // (exp2_fma2) instead of MUFU, which both tiles' softmax warps share (the diagonal
-        // copy keeps MUFU: measured slightly faster there).
         // The first three quarters of P are computed before waiting for the previous PV_X
         // (which still reads P_X), so that product's latency overlaps the exponentials;
         // storing them before the last quarter keeps the register peak at one S row.
@@ -387,13 +377,7 @@ __global__ void __maxnreg__(168)
               if (c > row) x0 = -INFINITY;
               if (c + 1 > row) x1 = -INFINITY;
             }
-            float p0, p1;
-            if (!kDiag && !decltype(mask_chunk)::value && (e & 7) == 7) {
-              exp2_fma2(x0, x1, p0, p1);
-            } else {
-              p0 = ex2_approx(x0);
-              p1 = ex2_approx(x1);
-            }
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             const int a = (e & 1) * 2;
             fadd2(ps[a], ps[a + 1], ps[a], ps[a + 1], p0, p1);
             r[c32 / 2 + e] = pack_bf16x2(p0, p1);
@@ -480,26 +464,30 @@ __global__ void __maxnreg__(168)
 }
 #undef XATTN_LATENT_UNIT
 
-template <int NS, bool kNegScale>
+template <int NS, bool kFull, bool kNegScale>
 cudaError_t launch_latent_fwd_ns(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream) {
   using L = LatentFwdLayout<NS>;
   static std::atomic<unsigned long long> allowed{0};
-  const cudaError_t err = allow_smem(latent_fwd_kernel<NS, kNegScale>, L::kDynBytes, allowed);
+  const cudaError_t err = allow_smem(latent_fwd_kernel<NS, kFull, kNegScale>, L::kDynBytes, allowed);
   if (err != cudaSuccess) return err;
   const int num_m = (a.S + kTileRows - 1) / kTileRows;
   const long long units = static_cast<long long>(a.B) * a.nh * ((num_m + 1) / 2);
-  return launch_pdl(latent_fwd_kernel<NS, kNegScale>, static_cast<unsigned>(units < sms ? units : sms), kFwdThreads,
+  return launch_pdl(latent_fwd_kernel<NS, kFull, kNegScale>, static_cast<unsigned>(units < sms ? units : sms), kFwdThreads,
                     L::kDynBytes, stream, maps.q, maps.kv, maps.rope, a);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_fwd(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream) {
+  // One sub-tile that is full: products without conditions (B8 S1024, 12 heads of 64 + 32 / 64: 35.5 -> 32.2 us). With two the
+  // same is slower: S and P V of one query tile then go out in a row and keep the other's waiting (B4 S4093, 16 heads of 128 + 64 /
+  // 128: 250 -> 278 us).
+  if (a.dn == 64 && a.dv == 64 && a.scale >= 0.f) return launch_latent_fwd_ns<1, true, false>(maps, a, sms, stream);
   if (a.dn <= 64 && a.dv <= 64)
-    return a.scale < 0.f ? launch_latent_fwd_ns<1, true>(maps, a, sms, stream)
-                         : launch_latent_fwd_ns<1, false>(maps, a, sms, stream);
-  return a.scale < 0.f ? launch_latent_fwd_ns<2, true>(maps, a, sms, stream)
-                       : launch_latent_fwd_ns<2, false>(maps, a, sms, stream);
+    return a.scale < 0.f ? launch_latent_fwd_ns<1, false, true>(maps, a, sms, stream)
+                         : launch_latent_fwd_ns<1, false, false>(maps, a, sms, stream);
+  return a.scale < 0.f ? launch_latent_fwd_ns<2, false, true>(maps, a, sms, stream)
+                       : launch_latent_fwd_ns<2, false, false>(maps, a, sms, stream);
 }
 
 }  // namespace xattn
