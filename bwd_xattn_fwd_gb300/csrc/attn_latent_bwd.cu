@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a
 // products' steps have no conditions (B8 S1024, 12 heads of 64 + 32 / 64: dkv 62 -> 59 us, dq 47 -> 45).
 template <int NS>
 struct DkvLayout {
-  static constexpr int kStages = 3;
+  static constexpr int kStages = NS == 1 ? 6 : 3;                    // (NS = 1 with three: 1850 cycles a tile, bound by their turn)
   static constexpr uint32_t kK = 0;                                  // NS sub-tiles and the shared part
   static constexpr uint32_t kV = kK + (NS + 1) * kKeySub;
   static constexpr uint32_t kQ = kV + NS * kKeySub;                  // stages of Q (NS + 1 sub-tiles)
@@ -97,6 +97,7 @@ struct DkvLayout {
   static constexpr uint32_t kRows = kdO + kStages * NS * kQuerySub;  // stages of -LSE log2 e and -D
   static constexpr uint32_t kBars = kRows + kStages * 2 * kQRows * 4;
   static constexpr int kPlaces = NS == 1 ? 2 : 1;                    // of dP^T and dS^T
+  static constexpr int kIssuers = NS == 1 ? 2 : 1;
   static constexpr int kNumBars = 2 * kStages + 14;
   static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kUsed = kMisc + 32;
@@ -104,7 +105,7 @@ struct DkvLayout {
   static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
 };
 
-// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 P^T; 8-11 dS^T; a thread is a key row.
+// Warps: 0 TMA; 1 MMA issuer and TMEM owner (NS = 1: 3 another issuer); 4-7 P^T; 8-11 dS^T; a thread is a key row.
 // TMEM (columns): dV 64 NS | dK 64 NS, its shared part 64 | two places of S^T, 64 each | one (NS = 1: two) of dP^T.
 template <int NS, bool kFull>
 __global__ void __maxnreg__(168)
@@ -154,13 +155,13 @@ __global__ void __maxnreg__(168)
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 1);
+      mbar_init(q_empty(s), L::kIssuers);
     }
     mbar_init(k_full, 1);
     mbar_init(v_full, 1);
     mbar_init(k_empty, 1);
     mbar_init(v_empty, 1);
-    mbar_init(acc_done, 1);
+    mbar_init(acc_done, L::kIssuers);
     mbar_init(acc_free, 256);
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kB + 10 + x), 1);
@@ -245,11 +246,14 @@ __global__ void __maxnreg__(168)
     if (units_k > 0) mbar_drain(k_full, (units_k - 1) & 1, ctl);
     if (units > 0) mbar_drain(v_full, (units - 1) & 1, ctl);
     for (int r = max(g - kStages, 0); r < g; ++r) mbar_drain(q_full(r % kStages), (r / kStages) & 1, ctl);
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    // One thread, so one order: dV(t), dK(t), dP^T(t + 1), S^T(t + 2). dK -> dP^T -> dS^T -> dK is the longest chain (dP^T and
+  } else if (warp == 1 || (L::kIssuers == 2 && warp == 3)) {
+    // ---------------- MMA issuers: of S^T and dV (p_side), and of dP^T and dK (s_side) ----------------
+    // NS = 2: one thread, so one order: dV(t), dK(t), dP^T(t + 1), S^T(t + 2). dK -> dP^T -> dS^T -> dK is the longest chain (dP^T and
     // dS^T have one place), and S^T, dV fill the time that the dS warps take. (With two issuers the pipe took S^T between dK
-    // and dP^T: 2430 cycles a tile, 2200 so.) With two places dP^T(t + 1) goes first: it need not wait for dK(t).
+    // and dP^T: 2430 cycles a tile, 2200 so.)
+    // NS = 1: the products are short and their issue is what takes time (1750 cycles a tile by one thread), so two threads;
+    // dP^T has two places and need not wait for dK.
+    const bool p_side = warp == 1, s_side = L::kIssuers == 1 || warp == 3;
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
     const uint32_t idesc_dv = idesc_bf16_f32(128, dv, false, true), idesc_dk = idesc_bf16_f32(128, dn, false, true),
                    idesc_dr = idesc_bf16_f32(128, dr, false, true);
@@ -300,50 +304,64 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       XATTN_DKV_UNIT(u);
-      if (!warp_wait(k_full, units & 1, ctl) || !landed(g)) break;
-      tc_fence_after();
-      issue_s(g, T == 1);
-      if (!warp_wait(v_full, units & 1, ctl)) break;
-      tc_fence_after();
-      issue_dp(g, T == 1);
+      if (!landed(g)) break;
+      if (p_side) {
+        if (!warp_wait(k_full, units & 1, ctl)) break;
+        tc_fence_after();
+        issue_s(g, T == 1);
+      }
+      if (s_side) {
+        if (!warp_wait(v_full, units & 1, ctl)) break;
+        tc_fence_after();
+        issue_dp(g, T == 1);
+      }
       if (T > 1) {
         if (!landed(g + 1)) break;
         tc_fence_after();
-        issue_s(g + 1, T == 2);
+        if (p_side) issue_s(g + 1, T == 2);
       }
       // The first dV and dK overwrite the accumulators, which the unit before has read.
       if (!warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
 #pragma unroll 1
       for (int t = 0; t < T; ++t, ++g) {
         const int s = g % kStages;
-        if (kPlaces == 2 && t + 1 < T) issue_dp(g + 1, t + 2 == T);   // (its place's dK went before; the tile has landed)
-        if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t o = ddOt + s * NS * (kQuerySub >> 4);
+        const bool last = t + 1 == T;
+        if (kPlaces == 2 && s_side && !last) issue_dp(g + 1, t + 2 == T);   // (its place's dK went before; the tile has landed)
+        if (p_side) {
+          if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t o = ddOt + s * NS * (kQuerySub >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kQRows / 16; ++kk)
-            mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kQRows / 16; ++kk)
+              mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
+            if (L::kIssuers == 2) {
+              mma_commit(q_empty(s));
+              if (last) mma_commit(acc_done);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
         if (!warp_wait(ds_full(g), dp_phase(g), ctl)) { ok = false; break; }
         tc_fence_after();
-        if (elect_one()) {
-          const uint64_t q = dQt + s * (NS + 1) * (kQuerySub >> 4);
+        if (s_side) {
+          if (elect_one()) {
+            const uint64_t q = dQt + s * (NS + 1) * (kQuerySub >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kQRows / 16; ++kk) {
-            mma_ts(tdK, tdP(g) + kk * 8, q + kk * 128, idesc_dk, (t > 0 || kk > 0) ? 1u : 0u);
-            mma_ts(tdKr, tdP(g) + kk * 8, q + NS * (kQuerySub >> 4) + kk * 128, idesc_dr, (t > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kQRows / 16; ++kk) {
+              mma_ts(tdK, tdP(g) + kk * 8, q + kk * 128, idesc_dk, (t > 0 || kk > 0) ? 1u : 0u);
+              mma_ts(tdKr, tdP(g) + kk * 8, q + NS * (kQuerySub >> 4) + kk * 128, idesc_dr, (t > 0 || kk > 0) ? 1u : 0u);
+            }
+            mma_commit(q_empty(s));
+            if (last) mma_commit(acc_done);
           }
-          mma_commit(q_empty(s));
-          if (t + 1 == T) mma_commit(acc_done);
+          __syncwarp();
+          if (kPlaces == 1 && !last) issue_dp(g + 1, t + 2 == T);    // (the tile has landed: its S^T went before)
         }
-        __syncwarp();
-        if (kPlaces == 1 && t + 1 < T) issue_dp(g + 1, t + 2 == T);   // (the tile has landed: its S^T went before)
         if (t + 2 < T) {
           if (!landed(g + 2)) { ok = false; break; }
           tc_fence_after();
-          issue_s(g + 2, t + 3 == T);
+          if (p_side) issue_s(g + 2, t + 3 == T);
         }
       }
       ++units;

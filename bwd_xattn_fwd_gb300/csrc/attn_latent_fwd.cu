@@ -94,7 +94,7 @@ __global__ void __maxnreg__(168)
   auto o_done = [&](int x) { return bar(kB + 4 + x); };
   auto s_free = [&](int x) { return bar(kB + 6 + x); };
   auto o_free = [&](int x) { return bar(kB + 8 + x); };
-  const uint32_t q_full = bar(kB + 10), mma_final = bar(kB + 11);
+  const uint32_t q_full = bar(kB + 10), q_empty = bar(kB + 11);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
@@ -115,7 +115,7 @@ __global__ void __maxnreg__(168)
       mbar_init(o_free(x), 128);
     }
     mbar_init(q_full, 1);
-    mbar_init(mma_final, 2);
+    mbar_init(q_empty, 2);                   // both issuers' last scores of a unit
     fence_mbar_init();
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mkv);
@@ -153,7 +153,7 @@ __global__ void __maxnreg__(168)
       const int u = unit_at(k);
       if (u >= num_units) break;
       XATTN_LATENT_UNIT(u);
-      if (!warp_wait(mma_final, (units & 1) ^ 1, ctl)) break;      // the unit before has read its query tiles
+      if (!warp_wait(q_empty, (units & 1) ^ 1, ctl)) break;        // the unit before has taken its last scores
       mbar_expect_tx_elect(q_full, (hasB ? 2 : 1) * (k_subs + 1) * kSubTile);
       for (int x = 0; x < (hasB ? 2 : 1); ++x) {
         for (int c = 0; c < k_subs; ++c)
@@ -198,7 +198,7 @@ __global__ void __maxnreg__(168)
     const uint64_t dK = smem_desc(sRing, 16, 1024, kSwizzle128);
     const uint64_t dV = smem_desc(sRing, 8192, 1024, kSwizzle128);       // MN-major
     const uint32_t tSx = tS(x), tOx = tO(x), tPx = tP(x);
-    auto issue_qk = [&](int R) {
+    auto issue_qk = [&](int R, bool last) {
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < NS; ++c) {
@@ -213,6 +213,7 @@ __global__ void __maxnreg__(168)
           if (kk < dr_steps) mma_ss(tSx, q + kk * 2, kd + kk * 2, idesc_qk, 1u);
         mma_commit(s_full(x));
         mma_commit(k_empty(R % kDepth));
+        if (last) mma_commit(q_empty);
       }
       __syncwarp();
     };
@@ -241,7 +242,7 @@ __global__ void __maxnreg__(168)
       return true;
     };
     bool ok = true;
-    int units = 0, unitsx = 0;
+    int units = 0, unitsx = 0, steps = 0;
 #pragma unroll 1
     for (int k = 0, R = 0, gx = 0; ok; ++k) {
       const int u = unit_at(k);
@@ -255,7 +256,7 @@ __global__ void __maxnreg__(168)
         ok = landed_k(R) && warp_wait(s_free(x), (gx - 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        issue_qk(R);
+        issue_qk(R, used == 1);
         if (!warp_wait(o_free(x), (unitsx - 1) & 1, ctl)) break;
 #pragma unroll 1
         for (int n = 0; n < used; ++n, ++gx) {
@@ -264,7 +265,7 @@ __global__ void __maxnreg__(168)
             if (more) {
               if (!warp_wait(s_free(x), gx & 1, ctl) || !landed_k(R + n + 1)) { ok = false; break; }
               tc_fence_after();
-              issue_qk(R + n + 1);
+              issue_qk(R + n + 1, n + 2 == used);
             }
           }
           if (!landed_v(R + n) || !warp_wait(p_full(x), gx & 1, ctl)) { ok = false; break; }
@@ -275,21 +276,23 @@ __global__ void __maxnreg__(168)
             if (more) {
               if (!landed_k(R + n + 1)) { ok = false; break; }
               tc_fence_after();
-              issue_qk(R + n + 1);
+              issue_qk(R + n + 1, n + 2 == used);
             }
           }
         }
         if (!ok) break;
         ++unitsx;
+      } else {
+        if (elect_one()) mbar_arrive(q_empty);
+        __syncwarp();
       }
       for (int n = used; ok && n < count; ++n) ok = pass_tile(R + n);
       if (!ok) break;
-      if (elect_one()) mma_commit(mma_final);       // covers every MMA of this unit
-      __syncwarp();
       R += count;
       ++units;
+      steps = gx;
     }
-    if (units > 0) mbar_drain(mma_final, (units - 1) & 1, ctl);
+    if (steps > 0) mbar_drain(o_done(x), (steps - 1) & 1, ctl);      // covers every MMA of this issuer
   } else if (warp >= 4) {
     // ---------------- softmax + epilogue: one thread per query row of tile X ----------------
     const int x = (warp - 4) >> 2;          // 0 = tile A, 1 = tile B
