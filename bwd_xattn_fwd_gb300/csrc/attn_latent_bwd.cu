@@ -98,7 +98,7 @@ struct DkvLayout {
   static constexpr uint32_t kBars = kRows + kStages * 2 * kQRows * 4;
   static constexpr int kPlaces = NS == 1 ? 2 : 1;                    // of dP^T and dS^T
   static constexpr int kIssuers = NS == 1 ? 2 : 1;
-  static constexpr int kNumBars = 2 * kStages + 14;
+  static constexpr int kNumBars = 2 * kStages + 16;
   static constexpr uint32_t kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
@@ -142,6 +142,7 @@ __global__ void __maxnreg__(168)
                  acc_free = bar(kB + 5);
   auto s_full = [&](int x) { return bar(kB + 6 + x); };
   auto p_full = [&](int x) { return bar(kB + 8 + x); };
+  auto s_read = [&](int x) { return bar(kB + 14 + x); };             // by the dS warps: P^T may overwrite S^T
   // dP^T's (and dS^T's) place and its phase, of tile g.
   constexpr int kPlaces = L::kPlaces;
   auto dp_full = [&](int g) { return bar(kB + 10 + g % kPlaces); };
@@ -168,6 +169,7 @@ __global__ void __maxnreg__(168)
       mbar_init(bar(kB + 12 + x), 128);
       mbar_init(s_full(x), 1);
       mbar_init(p_full(x), 128);
+      mbar_init(s_read(x), 128);
     }
     fence_mbar_init();
     tma_prefetch_desc(&mq);
@@ -342,9 +344,9 @@ __global__ void __maxnreg__(168)
           }
           __syncwarp();
         }
-        if (!warp_wait(ds_full(g), dp_phase(g), ctl)) { ok = false; break; }
-        tc_fence_after();
         if (s_side) {
+          if (!warp_wait(ds_full(g), dp_phase(g), ctl)) { ok = false; break; }
+          tc_fence_after();
           if (elect_one()) {
             const uint64_t q = dQt + s * (NS + 1) * (kQuerySub >> 4);
 #pragma unroll
@@ -372,6 +374,15 @@ __global__ void __maxnreg__(168)
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float scale_log2 = a.scale * kLog2e;
+    auto probabilities = [&](uint32_t *s, float4 m) {              // of four queries; m: -LSE log2 e
+      float x0, x1, x2, x3;
+      ffma2(x0, x1, __uint_as_float(s[0]), __uint_as_float(s[1]), scale_log2, scale_log2, m.x, m.y);
+      ffma2(x2, x3, __uint_as_float(s[2]), __uint_as_float(s[3]), scale_log2, scale_log2, m.z, m.w);
+      s[0] = __float_as_uint(ex2_approx(x0));
+      s[1] = __float_as_uint(ex2_approx(x1));
+      s[2] = __float_as_uint(ex2_approx(x2));
+      s[3] = __float_as_uint(ex2_approx(x3));
+    };
     bool ok = true;
     int units = 0, g = 0;
 #pragma unroll 1
@@ -397,12 +408,9 @@ __global__ void __maxnreg__(168)
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
-            const float4 m = nl[c / 4];
-            float x0, x1, x2, x3;
-            ffma2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), scale_log2, scale_log2, m.x, m.y);
-            ffma2(x2, x3, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]), scale_log2, scale_log2, m.z, m.w);
-            pk[c / 2] = pack_bf16x2(ex2_approx(x0), ex2_approx(x1));
-            pk[c / 2 + 1] = pack_bf16x2(ex2_approx(x2), ex2_approx(x3));
+            probabilities(r + c, nl[c / 4]);
+            pk[c / 2] = pack_bf16x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+            pk[c / 2 + 1] = pack_bf16x2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
           }
           if (t < 2) {
 #pragma unroll
@@ -411,6 +419,8 @@ __global__ void __maxnreg__(168)
               if (2 * c + 1 < hidden) pk[c] &= 0x0000ffffu;
             }
           }
+          if (!warp_wait(s_read(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
           tmem_st_x32(at, pk);
           tmem_wait_st();
           tc_fence_before();
@@ -420,31 +430,41 @@ __global__ void __maxnreg__(168)
         // ---------------- dS^T = P^T (dP^T - D) ----------------
 #pragma unroll 1
         for (int t = 0; t < T; ++t, ++g) {
+          // P in fp32, by these warps too: with the P warps' bf16 numbers dK had one rounding more, 2.9e-3 of its norm for 2.5e-3.
+          // It takes no time that the walk waits for: S^T is there before dP^T.
+          if (!warp_wait(s_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+          tc_fence_after();
+          uint32_t p[64], r[64];
+          tmem_ld_x32(tS(g & 1) + lane_off, p);
+          tmem_ld_x32(tS(g & 1) + lane_off + 32, p + 32);
+          tmem_wait_ld();
+          reg_fence<64>(p);
+          tc_fence_before();
+          mbar_arrive(s_read(g & 1));
+          const float4 *nl = reinterpret_cast<const float4 *>(smem + L::kRows + (g % kStages) * 2 * kQRows * 4),
+                       *nd = nl + kQRows / 4;
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) probabilities(p + c, nl[c / 4]);
+          if (t < 2) {
+            const int hidden = row - t * kQRows;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) p[c] = c < hidden ? 0u : p[c];
+          }
           if (!warp_wait(dp_full(g), dp_phase(g), ctl)) { ok = false; break; }
           tc_fence_after();
-          uint32_t r[64], p[32];
           const uint32_t at = tdP(g) + lane_off;
           tmem_ld_x32(at, r);
           tmem_ld_x32(at + 32, r + 32);
-          if (!warp_wait(p_full(g & 1), (g >> 1) & 1, ctl)) {
-            tmem_wait_ld();
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          tmem_ld_x32(tS(g & 1) + lane_off, p);
           tmem_wait_ld();
           reg_fence<64>(r);
-          reg_fence<32>(p);
-          const float4 *nd = reinterpret_cast<const float4 *>(smem + L::kRows + (g % kStages) * 2 * kQRows * 4 + kQRows * 4);
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
             const float4 d = nd[c / 4];
             float x0, x1, x2, x3;
             fadd2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), d.x, d.y);
             fadd2(x2, x3, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]), d.z, d.w);
-            fmul2(x0, x1, x0, x1, bf16lo_to_f32(p[c / 2]), bf16hi_to_f32(p[c / 2]));
-            fmul2(x2, x3, x2, x3, bf16lo_to_f32(p[c / 2 + 1]), bf16hi_to_f32(p[c / 2 + 1]));
+            fmul2(x0, x1, x0, x1, __uint_as_float(p[c]), __uint_as_float(p[c + 1]));
+            fmul2(x2, x3, x2, x3, __uint_as_float(p[c + 2]), __uint_as_float(p[c + 3]));
             p[c / 2] = pack_bf16x2(x0, x1);
             p[c / 2 + 1] = pack_bf16x2(x2, x3);
           }
