@@ -106,7 +106,8 @@ struct DkvLayout {
 };
 
 // Warps: 0 TMA; 1 MMA issuer and TMEM owner (NS = 1: 3 another issuer); 4-7 P^T; 8-11 dS^T; a thread is a key row.
-// TMEM (columns): dV 64 NS | dK 64 NS, its shared part 64 | two places of S^T, 64 each | one (NS = 1: two) of dP^T.
+// TMEM (columns): dV 64 NS | dK 64 NS, its shared part 64 | two places of S^T, 64 each | one (NS = 1: two) of dP^T |
+// NS = 1: two of P^T, 32 each.
 template <int NS, bool kFull>
 __global__ void __maxnreg__(168)
     latent_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
@@ -142,7 +143,7 @@ __global__ void __maxnreg__(168)
                  acc_free = bar(kB + 5);
   auto s_full = [&](int x) { return bar(kB + 6 + x); };
   auto p_full = [&](int x) { return bar(kB + 8 + x); };
-  auto s_read = [&](int x) { return bar(kB + 14 + x); };             // by the dS warps: P^T may overwrite S^T
+  auto s_read = [&](int x) { return bar(kB + 14 + x); };             // by the dS warps: its place may be overwritten
   // dP^T's (and dS^T's) place and its phase, of tile g.
   constexpr int kPlaces = L::kPlaces;
   auto dp_full = [&](int g) { return bar(kB + 10 + g % kPlaces); };
@@ -190,6 +191,7 @@ __global__ void __maxnreg__(168)
   constexpr uint32_t kAcc = 64 * NS;                                  // columns of dV, and of dK
   const uint32_t tdV = tmem, tdK = tmem + kAcc, tdKr = tmem + 2 * kAcc;
   auto tS = [&](int x) { return tmem + 2 * kAcc + 64u + 64u * x; };
+  auto tP = [&](int x) { return NS == 1 ? tmem + 448u + 32u * x : tS(x); };      // bf16; NS = 2: over S^T
   auto tdP = [&](int g) { return tmem + 2 * kAcc + 192u + 64u * (g % kPlaces); };
 
   if (warp == 0) {
@@ -265,8 +267,10 @@ __global__ void __maxnreg__(168)
     const uint64_t ddOt = smem_desc(sdO, kQuerySub, 1024, kSwizzle128);
     auto landed = [&](int g) { return warp_wait(q_full(g % kStages), (g / kStages) & 1, ctl); };
     // S^T of tile g (over all units); its place's P^T and the dS warps' reading of it lie two tiles back.
+    // NS = 2: P^T was written after that reading; NS = 1 waits for it here.
     auto issue_s = [&](int g, bool last) {
-
+      if (NS == 1 && g >= 2 && !warp_wait(s_read(g & 1), ((g - 2) >> 1) & 1, ctl)) return false;
+      if (NS == 1) tc_fence_after();
       if (elect_one()) {
         const uint64_t q = dQ + (g % kStages) * (NS + 1) * (kQuerySub >> 4);
         const uint32_t d = tS(g & 1);
@@ -283,6 +287,7 @@ __global__ void __maxnreg__(168)
         if (last) mma_commit(k_empty);
       }
       __syncwarp();
+      return true;
     };
     auto issue_dp = [&](int g, bool last) {
 
@@ -310,7 +315,7 @@ __global__ void __maxnreg__(168)
       if (p_side) {
         if (!warp_wait(k_full, units & 1, ctl)) break;
         tc_fence_after();
-        issue_s(g, T == 1);
+        if (!issue_s(g, T == 1)) break;
       }
       if (s_side) {
         if (!warp_wait(v_full, units & 1, ctl)) break;
@@ -320,7 +325,7 @@ __global__ void __maxnreg__(168)
       if (T > 1) {
         if (!landed(g + 1)) break;
         tc_fence_after();
-        if (p_side) issue_s(g + 1, T == 2);
+        if (p_side && !issue_s(g + 1, T == 2)) break;
       }
       // The first dV and dK overwrite the accumulators, which the unit before has read.
       if (!warp_wait(acc_free, (units & 1) ^ 1, ctl)) break;
@@ -336,7 +341,7 @@ __global__ void __maxnreg__(168)
             const uint64_t o = ddOt + s * NS * (kQuerySub >> 4);
 #pragma unroll
             for (int kk = 0; kk < kQRows / 16; ++kk)
-              mma_ts(tdV, tS(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
+              mma_ts(tdV, tP(g & 1) + kk * 8, o + kk * 128, idesc_dv, (t > 0 || kk > 0) ? 1u : 0u);
             if (L::kIssuers == 2) {
               mma_commit(q_empty(s));
               if (last) mma_commit(acc_done);
@@ -363,7 +368,7 @@ __global__ void __maxnreg__(168)
         if (t + 2 < T) {
           if (!landed(g + 2)) { ok = false; break; }
           tc_fence_after();
-          if (p_side) issue_s(g + 2, t + 3 == T);
+          if (p_side && !issue_s(g + 2, t + 3 == T)) { ok = false; break; }
         }
       }
       ++units;
@@ -419,9 +424,11 @@ __global__ void __maxnreg__(168)
               if (2 * c + 1 < hidden) pk[c] &= 0x0000ffffu;
             }
           }
-          if (!warp_wait(s_read(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
-          tc_fence_after();
-          tmem_st_x32(at, pk);
+          if (NS == 2) {
+            if (!warp_wait(s_read(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+            tc_fence_after();
+          }
+          tmem_st_x32(tP(g & 1) + lane_off, pk);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_full(g & 1));
@@ -434,7 +441,7 @@ __global__ void __maxnreg__(168)
           // It takes no time that the walk waits for: S^T is there before dP^T.
           if (!warp_wait(s_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
           tc_fence_after();
-          uint32_t p[64], r[64];
+          uint32_t p[64], r[32];
           tmem_ld_x32(tS(g & 1) + lane_off, p);
           tmem_ld_x32(tS(g & 1) + lane_off + 32, p + 32);
           tmem_wait_ld();
@@ -453,20 +460,23 @@ __global__ void __maxnreg__(168)
           if (!warp_wait(dp_full(g), dp_phase(g), ctl)) { ok = false; break; }
           tc_fence_after();
           const uint32_t at = tdP(g) + lane_off;
-          tmem_ld_x32(at, r);
-          tmem_ld_x32(at + 32, r + 32);
-          tmem_wait_ld();
-          reg_fence<64>(r);
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float4 d = nd[c / 4];
-            float x0, x1, x2, x3;
-            fadd2(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), d.x, d.y);
-            fadd2(x2, x3, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]), d.z, d.w);
-            fmul2(x0, x1, x0, x1, __uint_as_float(p[c]), __uint_as_float(p[c + 1]));
-            fmul2(x2, x3, x2, x3, __uint_as_float(p[c + 2]), __uint_as_float(p[c + 3]));
-            p[c / 2] = pack_bf16x2(x0, x1);
-            p[c / 2 + 1] = pack_bf16x2(x2, x3);
+          for (int half = 0; half < 64; half += 32) {
+            tmem_ld_x32(at + half, r);
+            tmem_wait_ld();
+            reg_fence<32>(r);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const int c = half + e;
+              const float4 d = nd[c / 4];
+              float x0, x1, x2, x3;
+              fadd2(x0, x1, __uint_as_float(r[e]), __uint_as_float(r[e + 1]), d.x, d.y);
+              fadd2(x2, x3, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]), d.z, d.w);
+              fmul2(x0, x1, x0, x1, __uint_as_float(p[c]), __uint_as_float(p[c + 1]));
+              fmul2(x2, x3, x2, x3, __uint_as_float(p[c + 2]), __uint_as_float(p[c + 3]));
+              p[c / 2] = pack_bf16x2(x0, x1);
+              p[c / 2 + 1] = pack_bf16x2(x2, x3);
+            }
           }
           tmem_st_x32(at, p);
           tmem_wait_st();
