@@ -423,8 +423,15 @@ __global__ void __maxnreg__(168)
               if (2 * c < hidden) pk[c] &= 0xffff0000u;
               if (2 * c + 1 < hidden) pk[c] &= 0x0000ffffu;
             }
+            if (NS == 1) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) r[c] = c < hidden ? 0u : r[c];
+            }
           }
-          if (NS == 2) {
+          if (NS == 1) {
+            tmem_st_x32(at, r);
+            tmem_st_x32(at + 32, r + 32);
+          } else {
             if (!warp_wait(s_read(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
             tc_fence_after();
           }
@@ -437,9 +444,10 @@ __global__ void __maxnreg__(168)
         // ---------------- dS^T = P^T (dP^T - D) ----------------
 #pragma unroll 1
         for (int t = 0; t < T; ++t, ++g) {
-          // P in fp32, by these warps too: with the P warps' bf16 numbers dK had one rounding more, 2.9e-3 of its norm for 2.5e-3.
-          // It takes no time that the walk waits for: S^T is there before dP^T.
-          if (!warp_wait(s_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
+          // P in fp32 (from the bf16 numbers dK had one rounding more, 2.9e-3 of its norm for 2.4e-3). NS = 1: the P warps leave
+          // it over S^T. NS = 2 has no room for both and takes the exponentials here again, while dP^T is on its way. (NS = 1
+          // so: B4 S4096, 16 heads of 64 + 32 / 64 668 us, from the P warps 651.)
+          if (!warp_wait(NS == 1 ? p_full(g & 1) : s_full(g & 1), (g >> 1) & 1, ctl)) { ok = false; break; }
           tc_fence_after();
           uint32_t p[64], r[32];
           tmem_ld_x32(tS(g & 1) + lane_off, p);
@@ -450,12 +458,14 @@ __global__ void __maxnreg__(168)
           mbar_arrive(s_read(g & 1));
           const float4 *nl = reinterpret_cast<const float4 *>(smem + L::kRows + (g % kStages) * 2 * kQRows * 4),
                        *nd = nl + kQRows / 4;
+          if (NS == 2) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) probabilities(p + c, nl[c / 4]);
-          if (t < 2) {
-            const int hidden = row - t * kQRows;
+            for (int c = 0; c < 64; c += 4) probabilities(p + c, nl[c / 4]);
+            if (t < 2) {
+              const int hidden = row - t * kQRows;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) p[c] = c < hidden ? 0u : p[c];
+              for (int c = 0; c < 64; ++c) p[c] = c < hidden ? 0u : p[c];
+            }
           }
           if (!warp_wait(dp_full(g), dp_phase(g), ctl)) { ok = false; break; }
           tc_fence_after();
