@@ -557,7 +557,7 @@ struct LatentDqLayout {
   static constexpr uint32_t kK = kQ + (NS + 1) * kKeySub;
   static constexpr uint32_t kV = kK + kStages * (NS + 1) * kKeySub;
   static constexpr uint32_t kBars = kV + NS * kKeySub;
-  static constexpr int kNumBars = 2 * kStages + 9;
+  static constexpr int kNumBars = 2 * kStages + 10;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kUsed = kMisc + 32;
   static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
@@ -579,9 +579,17 @@ __global__ void __maxnreg__(168)
   const int S = a.S, nh = a.nh, dn = kFull ? 64 * NS : a.dn, dr = a.dr, dv = kFull ? 64 * NS : a.dv;
   const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
   const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
-  const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh;
-  const int m = num_m - 1 - static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) % BH;
-  const int b = bh / nh, h = bh - b * nh, T = m + 1;                 // key tiles
+  const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh, num_units = num_m * BH;
+  // Units, most key tiles first, dealt to and fro as in the kernel before.
+  auto unit_at = [&](int k) {
+    const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    return k * G + ((k & 1) ? G - 1 - c : c);
+  };
+#define XATTN_DQ_UNIT(u)                                             \
+  const int m = num_m - 1 - (u) / BH, bh = (u) % BH;                 \
+  const int b = bh / nh, h = bh - b * nh, T = m + 1; /* key tiles */ \
+  (void)b;                                                           \
+  (void)h
   const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV),
                  bar0 = smem_u32(smem + L::kBars);
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -589,14 +597,14 @@ __global__ void __maxnreg__(168)
   auto k_empty = [&](int s) { return bar(kStages + s); };
   constexpr int kB = 2 * kStages;
   const uint32_t v_full = bar(kB), v_empty = bar(kB + 1), q_full = bar(kB + 2), s_full = bar(kB + 3), dp_full = bar(kB + 4),
-                 dq_done = bar(kB + 5), s_free = bar(kB + 6), ds_full = bar(kB + 7), do_full = bar(kB + 8);
+                 dq_done = bar(kB + 5), q_empty = bar(kB + 6), s_free = bar(kB + 7), ds_full = bar(kB + 8), do_full = bar(kB + 9);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i >= kB + 6 ? 256 : 1);
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i >= kB + 7 ? 256 : 1);
     fence_mbar_init();
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mkv);
@@ -616,29 +624,41 @@ __global__ void __maxnreg__(168)
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int col, int head, int row0) {
-      XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && dst >= sQ && dst + kKeySub <= bar0, a.status);
-      tma_load_4d_elect(dst, map, full, col, head, row0, b);
-    };
-    mbar_expect_tx_elect(q_full, (k_subs + 1) * kKeySub);
-    for (int c = 0; c < k_subs; ++c) load(sQ + c * kKeySub, &mq, q_full, 64 * c, h, m * kTileRows);
-    load(sQ + NS * kKeySub, &mq, q_full, dn, h, m * kTileRows);
-    int issued_k = 0, issued_v = 0;
-    for (int n = 0; n < T; ++n) {
-      const int s = n % kStages;
-      if (!warp_wait(k_empty(s), ((n / kStages) & 1) ^ 1, ctl)) break;
-      mbar_expect_tx_elect(k_full(s), (k_subs + 1) * kKeySub);
-      const uint32_t dk = sK + s * (NS + 1) * kKeySub;
-      for (int c = 0; c < k_subs; ++c) load(dk + c * kKeySub, &mkv, k_full(s), 64 * c, h, n * kTileRows);
-      load(dk + NS * kKeySub, &mrope, k_full(s), 0, 0, n * kTileRows);
-      issued_k = n + 1;
-      if (!warp_wait(v_empty, (n & 1) ^ 1, ctl)) break;
-      mbar_expect_tx_elect(v_full, v_subs * kKeySub);
-      for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, v_full, dn + 64 * c, h, n * kTileRows);
-      issued_v = n + 1;
+    bool ok = true;
+    int units = 0, issued_k = 0, issued_v = 0;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DQ_UNIT(u);
+      auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int col, int head, int row0) {
+        XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && dst >= sQ && dst + kKeySub <= bar0, a.status);
+        tma_load_4d_elect(dst, map, full, col, head, row0, b);
+      };
+      // The unit's first K before its Q: a stage is free sooner.
+      for (int n = 0; n < T; ++n) {
+        const int s = issued_k % kStages;
+        if (!warp_wait(k_empty(s), ((issued_k / kStages) & 1) ^ 1, ctl)) { ok = false; break; }
+        mbar_expect_tx_elect(k_full(s), (k_subs + 1) * kKeySub);
+        const uint32_t dk = sK + s * (NS + 1) * kKeySub;
+        for (int c = 0; c < k_subs; ++c) load(dk + c * kKeySub, &mkv, k_full(s), 64 * c, h, n * kTileRows);
+        load(dk + NS * kKeySub, &mrope, k_full(s), 0, 0, n * kTileRows);
+        ++issued_k;
+        if (n == 0) {
+          if (!warp_wait(q_empty, (units & 1) ^ 1, ctl)) { ok = false; break; }
+          mbar_expect_tx_elect(q_full, (k_subs + 1) * kKeySub);
+          for (int c = 0; c < k_subs; ++c) load(sQ + c * kKeySub, &mq, q_full, 64 * c, h, m * kTileRows);
+          load(sQ + NS * kKeySub, &mq, q_full, dn, h, m * kTileRows);
+          ++units;
+        }
+        if (!warp_wait(v_empty, (issued_v & 1) ^ 1, ctl)) { ok = false; break; }
+        mbar_expect_tx_elect(v_full, v_subs * kKeySub);
+        for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, v_full, dn + 64 * c, h, n * kTileRows);
+        ++issued_v;
+      }
     }
     // Every copy in flight has landed before the CTA can exit.
-    mbar_drain(q_full, 0, ctl);
+    if (units > 0) mbar_drain(q_full, (units - 1) & 1, ctl);
     for (int n = max(issued_k - kStages, 0); n < issued_k; ++n) mbar_drain(k_full(n % kStages), (n / kStages) & 1, ctl);
     if (issued_v > 0) mbar_drain(v_full, (issued_v - 1) & 1, ctl);
   } else if (warp == 1) {
@@ -649,9 +669,10 @@ __global__ void __maxnreg__(168)
     const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
     const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dV = smem_desc(sV, 16, 1024, kSwizzle128);
     const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
-    auto scores = [&](int n) -> bool {
-      const int s = n % kStages;
-      if (!warp_wait(k_full(s), (n / kStages) & 1, ctl) || !warp_wait(s_free, (n & 1) ^ 1, ctl)) return false;
+    // (t counts the tiles of all units.)
+    auto scores = [&](int t, bool last) -> bool {
+      const int s = t % kStages;
+      if (!warp_wait(k_full(s), (t / kStages) & 1, ctl) || !warp_wait(s_free, (t & 1) ^ 1, ctl)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = dK + s * (NS + 1) * kSubDesc;
@@ -664,12 +685,13 @@ __global__ void __maxnreg__(168)
         for (int kk = 0; kk < 4; ++kk)
           if (kk < dr_steps) mma_ss(tS, dQ + NS * kSubDesc + kk * 2, kd + NS * kSubDesc + kk * 2, idesc_s, 1u);
         mma_commit(s_full);
+        if (last) mma_commit(q_empty);
       }
       __syncwarp();
       return true;
     };
-    auto issue_dp = [&](int n) -> bool {
-      if (!warp_wait(v_full, n & 1, ctl)) return false;
+    auto issue_dp = [&](int t) -> bool {
+      if (!warp_wait(v_full, t & 1, ctl)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -683,105 +705,135 @@ __global__ void __maxnreg__(168)
       __syncwarp();
       return true;
     };
-    int done = 0;
-    bool ok = warp_wait(q_full, 0, ctl) && scores(0) && warp_wait(do_full, 0, ctl) && issue_dp(0);
+    bool ok = true;
+    int units = 0, t = 0;
 #pragma unroll 1
-    for (int n = 0; ok && n < T; ++n) {
-      const int s = n % kStages;
-      if ((n + 1 < T && !scores(n + 1)) || !warp_wait(ds_full, n & 1, ctl)) break;
-      tc_fence_after();
-      if (elect_one()) {                                            // dQ += dS K_n
-        const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DQ_UNIT(u);
+      (void)bh;
+      ok = warp_wait(q_full, units & 1, ctl) && scores(t, T == 1) && warp_wait(do_full, units & 1, ctl) && issue_dp(t);
+#pragma unroll 1
+      for (int n = 0; ok && n < T; ++n, ++t) {
+        const int s = t % kStages;
+        const bool more = n + 1 < T;
+        // (dS of the unit's first tile comes from threads that have read the dQ before: it may be overwritten.)
+        ok = (!more || scores(t + 1, n + 2 == T)) && warp_wait(ds_full, t & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {                                          // dQ += dS K_n
+          const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
 #pragma unroll
-        for (int kk = 0; kk < kTileRows / 16; ++kk) {
-          const uint32_t ds = tdP + (kk / 4) * 64 + (kk % 4) * 8;
-          mma_ts(tdQ, ds, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
-          mma_ts(tdQr, ds, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kTileRows / 16; ++kk) {
+            const uint32_t ds = tdP + (kk / 4) * 64 + (kk % 4) * 8;
+            mma_ts(tdQ, ds, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
+            mma_ts(tdQr, ds, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(k_empty(s));
+          if (!more) mma_commit(dq_done);
         }
-        mma_commit(k_empty(s));
-        mma_commit(dq_done);
+        __syncwarp();
+        ok = !more || issue_dp(t + 1);
       }
-      __syncwarp();
-      done = n + 1;
-      if (n + 1 < T && !issue_dp(n + 1)) break;
+      if (ok) ++units;
     }
     __syncwarp();
-    if (done > 0) mbar_drain(dq_done, (done - 1) & 1, ctl);
+    if (units > 0) mbar_drain(dq_done, (units - 1) & 1, ctl);
   } else if (warp >= 4) {
     // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
     const int g = (warp - 4) >> 2, quarter = warp & 3;
-    const int i = quarter * 32 + lane, ig = m * kTileRows + i;
+    const int i = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int c0 = 64 * g;                              // first key column of this group
     const float scale_log2 = a.scale * kLog2e;
-    const size_t at = static_cast<size_t>(bh) * padded_rows(S) + ig;
-    const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
-    XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
-    // dO of this thread's row, 64 columns a group, into TMEM (rows behind the last, and columns behind dv: zeros).
-    if (NS == 2 || g == 0) {
-      uint32_t x[32];
-      uint4 *v = reinterpret_cast<uint4 *>(x);
+    float nlse2 = 0.f, nD = 0.f;
+    // A unit's dO of this thread's row, 64 columns a group, into TMEM (rows behind the last, and columns behind dv: zeros), and
+    // the row's numbers.
+    auto begin = [&](int u) {
+      XATTN_DQ_UNIT(u);
+      (void)T;
+      const int ig = m * kTileRows + i;
+      const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h, at = static_cast<size_t>(bh) * padded_rows(S) + ig;
+      XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
+      nlse2 = a.nlse[at], nD = a.nD[at];
+      if (NS == 2 || g == 0) {
+        uint32_t x[32];
+        uint4 *v = reinterpret_cast<uint4 *>(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = ig < S && c0 + 8 * e < dv ? __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + c0 + 8 * e))
-                                         : make_uint4(0u, 0u, 0u, 0u);
-      tmem_st_x32(tdO + lane_off + 32 * g, x);
-      tmem_wait_st();
-    }
-    tc_fence_before();
-    mbar_arrive(do_full);
-    const float nlse2 = a.nlse[at], nD = a.nD[at];
-    bool ok = true;
+        for (int e = 0; e < 8; ++e)
+          v[e] = ig < S && c0 + 8 * e < dv ? __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + c0 + 8 * e))
+                                           : make_uint4(0u, 0u, 0u, 0u);
+        tmem_st_x32(tdO + lane_off + 32 * g, x);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(do_full);
+    };
+    int units = 0, t = 0;
+    if (unit_at(0) < num_units) begin(unit_at(0));
 #pragma unroll 1
-    for (int n = 0; n < T; ++n) {
-      if (!warp_wait(s_full, n & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t p[64];
-      tmem_ld_x32(tS + lane_off + c0, p);
-      tmem_ld_x32(tS + lane_off + c0 + 32, p + 32);
-      tmem_wait_ld();
-      reg_fence<64>(p);
-      tc_fence_before();
-      mbar_arrive(s_free);
-#pragma unroll
-      for (int e = 0; e < 64; e += 2) {
-        float x0, x1;
-        ffma2(x0, x1, __uint_as_float(p[e]), __uint_as_float(p[e + 1]), scale_log2, scale_log2, nlse2, nlse2);
-        p[e] = __float_as_uint(ex2_approx(x0));
-        p[e + 1] = __float_as_uint(ex2_approx(x1));
-      }
-      if (n == m) {                                     // keys behind the query
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (c0 + e > i) p[e] = 0u;
-      }
-      // dS = P (dP - D), bf16 over the first half of this group's dP.
-      if (!warp_wait(dp_full, n & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t ds[32];
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        uint32_t d[32];
-        tmem_ld_x32(tdP + lane_off + c0 + 32 * part, d);
+    for (int k = 0;; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DQ_UNIT(u);
+      bool ok = true;
+#pragma unroll 1
+      for (int n = 0; n < T; ++n, ++t) {
+        if (!warp_wait(s_full, t & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t p[64];
+        tmem_ld_x32(tS + lane_off + c0, p);
+        tmem_ld_x32(tS + lane_off + c0 + 32, p + 32);
         tmem_wait_ld();
-        reg_fence<32>(d);
+        reg_fence<64>(p);
+        tc_fence_before();
+        mbar_arrive(s_free);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float t0, t1;
-          fadd2(t0, t1, __uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), nD, nD);
-          fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * part + 2 * e]), __uint_as_float(p[32 * part + 2 * e + 1]));
-          ds[16 * part + e] = pack_bf16x2(t0, t1);
+        for (int e = 0; e < 64; e += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(p[e]), __uint_as_float(p[e + 1]), scale_log2, scale_log2, nlse2, nlse2);
+          p[e] = __float_as_uint(ex2_approx(x0));
+          p[e + 1] = __float_as_uint(ex2_approx(x1));
         }
+        if (n == m) {                                     // keys behind the query
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (c0 + e > i) p[e] = 0u;
+        }
+        // dS = P (dP - D), bf16 over the first half of this group's dP.
+        if (!warp_wait(dp_full, t & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t ds[32];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t d[32];
+          tmem_ld_x32(tdP + lane_off + c0 + 32 * part, d);
+          tmem_wait_ld();
+          reg_fence<32>(d);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float t0, t1;
+            fadd2(t0, t1, __uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), nD, nD);
+            fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * part + 2 * e]), __uint_as_float(p[32 * part + 2 * e + 1]));
+            ds[16 * part + e] = pack_bf16x2(t0, t1);
+          }
+        }
+        tmem_st_x32(tdP + lane_off + c0, ds);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(ds_full);
       }
-      tmem_st_x32(tdP + lane_off + c0, ds);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(ds_full);
-    }
 
-    // Epilogue: dq = bf16(scale * sum); group g writes every second 16 columns of the thread's row.
-    if (ok && warp_wait(dq_done, (T - 1) & 1, ctl)) {
+      if (!ok) break;
+      // The next unit's dO (its place was read by dP of the last tile), then dq = bf16(scale * sum) while its S and dP are
+      // made; group g writes every second 16 columns of the thread's row.
+      if (unit_at(k + 1) < num_units) begin(unit_at(k + 1));
+      if (!warp_wait(dq_done, units & 1, ctl)) break;
+      ++units;
       tc_fence_after();
+      const int ig = m * kTileRows + i;
+      __nv_bfloat16 *to = a.dq + ((static_cast<size_t>(b) * S + ig) * nh + h) * (dn + dr);
 #pragma unroll 1
       for (int c = 16 * g; c < dn + dr; c += 32) {
         uint32_t v[16];
@@ -790,10 +842,11 @@ __global__ void __maxnreg__(168)
         reg_fence<16>(v);
         if (ig < S) {
           auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale); };
-          store_32(a.dq + row * (dn + dr) + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
+          store_32(to + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
         }
         __syncwarp();
       }
+      tc_fence_before();
     }
   }
 
@@ -804,6 +857,7 @@ __global__ void __maxnreg__(168)
     tmem_dealloc(tmem, 512);
   }
 }
+#undef XATTN_DQ_UNIT
 
 // k_rope's gradient: the heads' parts added in order, four columns a thread.
 __global__ void __launch_bounds__(256) latent_rope_kernel(const LatentArgs a) {
@@ -838,7 +892,7 @@ cudaError_t launch_latent_bwd_ns(const LatentMaps &q64, const LatentMaps &q128, 
   err = launch_pdl(latent_dkv_kernel<NS, kFull>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LK::kDynBytes, stream,
                    q64.q, q128.kv, q128.rope, q64.dO, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(latent_dq_kernel<NS, kFull>, static_cast<unsigned>(units), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
+  return launch_pdl(latent_dq_kernel<NS, kFull>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
                     q128.rope, a);
 }
 
