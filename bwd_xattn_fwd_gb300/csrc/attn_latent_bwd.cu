@@ -3,19 +3,19 @@
 //   P = exp(scale S - LSE), dS = P (dO V^T - D);
 //   dV = P^T dO, dK = scale dS^T Q (its first dn numbers to dkv, the others summed over the heads to dk_rope), dQ = scale dS K.
 //
-// Four kernels:
-//   1. latent_bwd_rows_kernel: per query row -LSE log2 e and -D, transposed to [B, nh, S_pad] so that a tile's 64 (128) of a
-//      head are one contiguous copy.
+// Three kernels:
+//   1. latent_dq_kernel (query-stationary): S and dP, dQ += dS K in TMEM over the key tiles. It also makes -LSE log2 e and -D of
+//      its rows and leaves them, transposed to [B, nh, S_pad] (a tile's 64 of a head are one contiguous copy), for the next.
 //   2. latent_dkv_kernel (key-stationary): a unit is (batch, head, 128 keys); dV [128, dv] and dK [128, dn + dr] stay in TMEM,
 //      320 of its 512 columns, so queries come in tiles of 64 and three 64-column places hold the scores: S^T(t) in place
 //      t % 2 (P^T over it), dP^T(t) in the third (dS^T over it). S^T is issued two tiles ahead, so it runs while the warps
 //      work on P and dS. A score product of 64 columns takes 48 cycles a K step where its arithmetic is 32 (shared memory
 //      feeds 128 + 64 rows); with 128 columns the places would not fit. Per 64 queries 576 (S) + 384 (dP) + 256 (dV) + 384 (dK).
-//   3. latent_dq_kernel (query-stationary, as attn_bwd_dq_sm103.cu): S and dP once more, dQ += dS K in TMEM over the key
-//      tiles. dQ [., dn + dr] does not fit beside dV and dK, and summed with atomics it would not be reproducible.
-//   4. latent_rope_kernel: k_rope's gradient from the heads' fp32 parts, in order.
+//      S and dP are made twice: dQ [., dn + dr] does not fit beside dV and dK, and summed with atomics it would not be
+//      reproducible.
+//   3. latent_rope_kernel: k_rope's gradient from the heads' fp32 parts, in order.
 // Every output is bit-for-bit reproducible. Roundings: P and dS to bf16, Q's, K's and dO's type, before their products; dS is
-// made of the rounded P (in the third kernel of the unrounded one). Bound by the tensor cores.
+// made of the unrounded P. Bound by the tensor cores.
 #include "sm103_ptx.cuh"
 #include "xattn_internal.h"
 
@@ -32,61 +32,380 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok);
 }
 
-// A block takes 32 positions of up to 8 heads: sixteen lanes a row (b, i, h) of o and dO, eight numbers each, and the results by
-// way of shared memory, so that a head's 32 are written together (one by one, each to a line of its own, they took longer than
-// the reads). Rows S .. S_pad - 1 get a weight of 0 (their Q and dO are read as zeros).
-constexpr int kRowsPos = 32, kRowsHeads = 8;
-__global__ void __launch_bounds__(256) latent_bwd_rows_kernel(const LatentArgs a, int head_blocks) {
-  __shared__ float2 sums[kRowsHeads][kRowsPos + 1];
-  grid_dep_launch();
-  grid_dep_wait();
-  const int part = threadIdx.x & 15, group = threadIdx.x >> 4, S_pad = padded_rows(a.S), tiles = S_pad / kRowsPos;
-  const unsigned hb = blockIdx.x % head_blocks, rest = blockIdx.x / head_blocks;
-  const int b = static_cast<int>(rest / tiles), i0 = static_cast<int>(rest - static_cast<unsigned>(b) * tiles) * kRowsPos;
-  const int h0 = static_cast<int>(hb) * kRowsHeads;
-  constexpr int kOnce = 4;                                           // rows a group of lanes has in flight
-#pragma unroll 1
-  for (int r0 = group; r0 < kRowsPos * kRowsHeads; r0 += 16 * kOnce) {
-    uint4 x[kOnce], y[kOnce];
-    float lse[kOnce];
-#pragma unroll
-    for (int e = 0; e < kOnce; ++e) {
-      const int r = r0 + 16 * e, i = i0 + r / kRowsHeads, h = h0 + r % kRowsHeads;
-      x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
-      lse[e] = INFINITY;
-      if (i >= a.S || h >= a.nh) continue;
-      const size_t from = (static_cast<size_t>(b) * a.S + i) * a.nh + h;
-      lse[e] = a.lse[from];
-      if (8 * part < a.dv) {
-        x[e] = *reinterpret_cast<const uint4 *>(a.o + from * a.dv + 8 * part);
-        y[e] = *reinterpret_cast<const uint4 *>(a.dO + from * a.dv + 8 * part);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kOnce; ++e) {
-      float dot = 0.f;
-      auto add = [&](uint32_t u, uint32_t v) {
-        dot = fmaf(bf16lo_to_f32(u), bf16lo_to_f32(v), dot);
-        dot = fmaf(bf16hi_to_f32(u), bf16hi_to_f32(v), dot);
-      };
-      add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
-#pragma unroll
-      for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-      const int r = r0 + 16 * e;
-      if (part == 0) sums[r % kRowsHeads][r / kRowsHeads] = make_float2(-lse[e] * kLog2e, -dot);
-    }
-  }
-  __syncthreads();
-  const int h = threadIdx.x >> 5, i = threadIdx.x & 31;
-  if (h0 + h >= a.nh) return;
-  const size_t to = (static_cast<size_t>(b) * a.nh + h0 + h) * S_pad + i0 + i;
-  const float2 v = sums[h][i];
-  a.nlse[to] = v.x;
-  a.nD[to] = v.y;
-}
-
 // NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS). kFull: they are full (dn = dv = 64 NS), so that the
 // products' steps have no conditions (B8 S1024, 12 heads of 64 + 32 / 64: dkv 62 -> 59 us, dq 47 -> 45).
+
+// dQ: a unit is (batch, head, 128 queries). Q stays in shared memory and dO in TMEM (the A operand of dP), which leaves room
+// for three stages of K: K(n) is needed from S(n) to dQ(n), and with two the next scores waited for it. V has one stage: only
+// dP(n) reads it.
+template <int NS>
+struct LatentDqLayout {
+  static constexpr int kStages = 3;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + (NS + 1) * kKeySub;
+  static constexpr uint32_t kV = kK + kStages * (NS + 1) * kKeySub;
+  static constexpr uint32_t kBars = kV + NS * kKeySub;
+  static constexpr int kNumBars = 2 * kStages + 12;
+  static constexpr uint32_t kRows = (kBars + 8 * kNumBars + 15) / 16 * 16;   // -LSE log2 e and -D
+  static constexpr uint32_t kMisc = kRows + kTileRows * 8;
+  static constexpr uint32_t kUsed = kMisc + 32;
+  static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
+  static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
+};
+
+// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 2-3 the rows' numbers; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns
+// a group.
+// TMEM: S [0, 128) | dP [128, 256), dS bf16 over [128, 160) and [192, 224) | dO bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448.
+template <int NS, bool kFull>
+__global__ void __maxnreg__(168)
+    latent_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
+                     const __grid_constant__ CUtensorMap mrope, const LatentArgs a) {
+  using L = LatentDqLayout<NS>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t latent_dq_smem[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dq_smem) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int S = a.S, nh = a.nh, dn = kFull ? 64 * NS : a.dn, dr = a.dr, dv = kFull ? 64 * NS : a.dv;
+  const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
+  const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
+  const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh, num_units = num_m * BH;
+  // Units, most key tiles first, dealt to and fro as in the kernel before.
+  auto unit_at = [&](int k) {
+    const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    return k * G + ((k & 1) ? G - 1 - c : c);
+  };
+#define XATTN_DQ_UNIT(u)                                             \
+  const int m = num_m - 1 - (u) / BH, bh = (u) % BH;                 \
+  const int b = bh / nh, h = bh - b * nh, T = m + 1; /* key tiles */ \
+  (void)b;                                                           \
+  (void)h
+  const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV),
+                 bar0 = smem_u32(smem + L::kBars);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  auto k_full = [&](int s) { return bar(s); };
+  auto k_empty = [&](int s) { return bar(kStages + s); };
+  constexpr int kB = 2 * kStages;
+  const uint32_t v_full = bar(kB), v_empty = bar(kB + 1), q_full = bar(kB + 2), s_full = bar(kB + 3), dp_full = bar(kB + 4),
+                 dq_done = bar(kB + 5), q_empty = bar(kB + 6), s_free = bar(kB + 7), ds_full = bar(kB + 8), do_full = bar(kB + 9),
+                 rows_empty = bar(kB + 10), rows_full = bar(kB + 11);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
+  const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i == kB + 11 ? 64 : (i >= kB + 7 ? 256 : 1));
+    fence_mbar_init();
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mkv);
+    tma_prefetch_desc(&mrope);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch();
+  grid_dep_wait();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+  const uint32_t tS = tmem, tdP = tmem + 128, tdO = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    bool ok = true;
+    int units = 0, issued_k = 0, issued_v = 0;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DQ_UNIT(u);
+      auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int col, int head, int row0) {
+        XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && dst >= sQ && dst + kKeySub <= bar0, a.status);
+        tma_load_4d_elect(dst, map, full, col, head, row0, b);
+      };
+      // The unit's first K before its Q: a stage is free sooner.
+      for (int n = 0; n < T; ++n) {
+        const int s = issued_k % kStages;
+        if (!warp_wait(k_empty(s), ((issued_k / kStages) & 1) ^ 1, ctl)) { ok = false; break; }
+        mbar_expect_tx_elect(k_full(s), (k_subs + 1) * kKeySub);
+        const uint32_t dk = sK + s * (NS + 1) * kKeySub;
+        for (int c = 0; c < k_subs; ++c) load(dk + c * kKeySub, &mkv, k_full(s), 64 * c, h, n * kTileRows);
+        load(dk + NS * kKeySub, &mrope, k_full(s), 0, 0, n * kTileRows);
+        ++issued_k;
+        if (n == 0) {
+          if (!warp_wait(q_empty, (units & 1) ^ 1, ctl)) { ok = false; break; }
+          mbar_expect_tx_elect(q_full, (k_subs + 1) * kKeySub);
+          for (int c = 0; c < k_subs; ++c) load(sQ + c * kKeySub, &mq, q_full, 64 * c, h, m * kTileRows);
+          load(sQ + NS * kKeySub, &mq, q_full, dn, h, m * kTileRows);
+          ++units;
+        }
+        if (!warp_wait(v_empty, (issued_v & 1) ^ 1, ctl)) { ok = false; break; }
+        mbar_expect_tx_elect(v_full, v_subs * kKeySub);
+        for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, v_full, dn + 64 * c, h, n * kTileRows);
+        ++issued_v;
+      }
+    }
+    // Every copy in flight has landed before the CTA can exit.
+    if (units > 0) mbar_drain(q_full, (units - 1) & 1, ctl);
+    for (int n = max(issued_k - kStages, 0); n < issued_k; ++n) mbar_drain(k_full(n % kStages), (n / kStages) & 1, ctl);
+    if (issued_v > 0) mbar_drain(v_full, (issued_v - 1) & 1, ctl);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: S(n + 1) before dQ(n), dP(n + 1) behind it (dS(n) lies in dP's place) ----------------
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
+    constexpr uint32_t kSubDesc = kKeySub >> 4;
+    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
+    const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dV = smem_desc(sV, 16, 1024, kSwizzle128);
+    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
+    // (t counts the tiles of all units.)
+    auto scores = [&](int t, bool last) -> bool {
+      const int s = t % kStages;
+      if (!warp_wait(k_full(s), (t / kStages) & 1, ctl) || !warp_wait(s_free, (t & 1) ^ 1, ctl)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = dK + s * (NS + 1) * kSubDesc;
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (4 * c + kk < dn_steps) mma_ss(tS, dQ + c * kSubDesc + kk * 2, kd + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < dr_steps) mma_ss(tS, dQ + NS * kSubDesc + kk * 2, kd + NS * kSubDesc + kk * 2, idesc_s, 1u);
+        mma_commit(s_full);
+        if (last) mma_commit(q_empty);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto issue_dp = [&](int t) -> bool {
+      if (!warp_wait(v_full, t & 1, ctl)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (4 * c + kk < dv_steps) mma_ts(tdP, tdO + 32 * c + 8 * kk, dV + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
+        mma_commit(dp_full);
+        mma_commit(v_empty);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int units = 0, t = 0;
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DQ_UNIT(u);
+      (void)bh;
+      ok = warp_wait(q_full, units & 1, ctl) && scores(t, T == 1) && warp_wait(do_full, units & 1, ctl) && issue_dp(t);
+#pragma unroll 1
+      for (int n = 0; ok && n < T; ++n, ++t) {
+        const int s = t % kStages;
+        const bool more = n + 1 < T;
+        // (dS of the unit's first tile comes from threads that have read the dQ before: it may be overwritten.)
+        ok = (!more || scores(t + 1, n + 2 == T)) && warp_wait(ds_full, t & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {                                          // dQ += dS K_n
+          const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
+#pragma unroll
+          for (int kk = 0; kk < kTileRows / 16; ++kk) {
+            const uint32_t ds = tdP + (kk / 4) * 64 + (kk % 4) * 8;
+            mma_ts(tdQ, ds, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
+            mma_ts(tdQr, ds, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(k_empty(s));
+          if (!more) mma_commit(dq_done);
+        }
+        __syncwarp();
+        ok = !more || issue_dp(t + 1);
+      }
+      if (ok) ++units;
+    }
+    __syncwarp();
+    if (units > 0) mbar_drain(dq_done, (units - 1) & 1, ctl);
+  } else if (warp < 4) {
+    // ---------------- A unit's -LSE log2 e and -D, a unit ahead: 64 rows a warp, sixteen lanes a row of o and dO ----------------
+    // (A kernel of its own for them took 10 us of B8 S1024, 12 heads of 64 + 32 / 64; by the threads whose rows they are, a row
+    // a thread, a unit began 2 us later.)
+    const int part = lane & 15;
+    float2 *rows = reinterpret_cast<float2 *>(smem + L::kRows);
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units || !warp_wait(rows_empty, (k & 1) ^ 1, ctl)) break;
+      XATTN_DQ_UNIT(u);
+      (void)T;
+      constexpr int kOnce = 8;                                        // rows a half warp has in flight
+#pragma unroll 1
+      for (int r0 = 64 * (warp - 2) + (lane >> 4); r0 < 64 * (warp - 1); r0 += 2 * kOnce) {
+        uint4 x[kOnce], y[kOnce];
+        float lse[kOnce];
+#pragma unroll
+        for (int e = 0; e < kOnce; ++e) {
+          const int ig = m * kTileRows + r0 + 2 * e;
+          const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
+          x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
+          lse[e] = INFINITY;                                          // rows behind the last get a weight of 0
+          if (ig >= S) continue;
+          lse[e] = a.lse[row];
+          if (8 * part < dv) {
+            x[e] = __ldg(reinterpret_cast<const uint4 *>(a.o + row * dv + 8 * part));
+            y[e] = __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + 8 * part));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kOnce; ++e) {
+          float dot = 0.f;
+          auto add = [&](uint32_t v, uint32_t w) {
+            dot = fmaf(bf16lo_to_f32(v), bf16lo_to_f32(w), dot);
+            dot = fmaf(bf16hi_to_f32(v), bf16hi_to_f32(w), dot);
+          };
+          add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
+#pragma unroll
+          for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+          if (part == 0) rows[r0 + 2 * e] = make_float2(-lse[e] * kLog2e, -dot);
+        }
+      }
+      __syncwarp();
+      mbar_arrive(rows_full);
+#pragma unroll
+      for (int r = 64 * (warp - 2) + lane; r < 64 * (warp - 1); r += 32) {
+        const size_t at = static_cast<size_t>(bh) * padded_rows(S) + m * kTileRows + r;
+        const float2 v = rows[r];
+        a.nlse[at] = v.x;
+        a.nD[at] = v.y;
+      }
+    }
+  } else {
+    // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
+    const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int i = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int c0 = 64 * g;                              // first key column of this group
+    const float scale_log2 = a.scale * kLog2e;
+    float nlse2 = 0.f, nD = 0.f;
+    // A unit's dO of this thread's row, 64 columns a group, into TMEM (rows behind the last, and columns behind dv: zeros), and
+    // the row's numbers.
+    auto begin = [&](int u, int k) -> bool {
+      XATTN_DQ_UNIT(u);
+      (void)T;
+      const int ig = m * kTileRows + i;
+      const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
+      XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
+      if (NS == 2 || g == 0) {
+        uint32_t x[32];
+        uint4 *v = reinterpret_cast<uint4 *>(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = ig < S && c0 + 8 * e < dv ? __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + c0 + 8 * e))
+                                           : make_uint4(0u, 0u, 0u, 0u);
+        tmem_st_x32(tdO + lane_off + 32 * g, x);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(do_full);
+      if (!warp_wait(rows_full, k & 1, ctl)) return false;
+      const float2 r = reinterpret_cast<const float2 *>(smem + L::kRows)[i];
+      nlse2 = r.x, nD = r.y;
+      mbar_arrive(rows_empty);
+      return true;
+    };
+    int units = 0, t = 0;
+    bool ok = unit_at(0) < num_units && begin(unit_at(0), 0);
+#pragma unroll 1
+    for (int k = 0; ok; ++k) {
+      const int u = unit_at(k);
+      if (u >= num_units) break;
+      XATTN_DQ_UNIT(u);
+#pragma unroll 1
+      for (int n = 0; n < T; ++n, ++t) {
+        if (!warp_wait(s_full, t & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t p[64];
+        tmem_ld_x32(tS + lane_off + c0, p);
+        tmem_ld_x32(tS + lane_off + c0 + 32, p + 32);
+        tmem_wait_ld();
+        reg_fence<64>(p);
+        tc_fence_before();
+        mbar_arrive(s_free);
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(p[e]), __uint_as_float(p[e + 1]), scale_log2, scale_log2, nlse2, nlse2);
+          p[e] = __float_as_uint(ex2_approx(x0));
+          p[e + 1] = __float_as_uint(ex2_approx(x1));
+        }
+        if (n == m) {                                     // keys behind the query
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (c0 + e > i) p[e] = 0u;
+        }
+        // dS = P (dP - D), bf16 over the first half of this group's dP.
+        if (!warp_wait(dp_full, t & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t ds[32];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t d[32];
+          tmem_ld_x32(tdP + lane_off + c0 + 32 * part, d);
+          tmem_wait_ld();
+          reg_fence<32>(d);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float t0, t1;
+            fadd2(t0, t1, __uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), nD, nD);
+            fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * part + 2 * e]), __uint_as_float(p[32 * part + 2 * e + 1]));
+            ds[16 * part + e] = pack_bf16x2(t0, t1);
+          }
+        }
+        tmem_st_x32(tdP + lane_off + c0, ds);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(ds_full);
+      }
+
+      if (!ok) break;
+      // The next unit's dO (its place was read by dP of the last tile), then dq = bf16(scale * sum) while its S and dP are
+      // made; group g writes every second 16 columns of the thread's row.
+      ok = (unit_at(k + 1) >= num_units || begin(unit_at(k + 1), k + 1)) && warp_wait(dq_done, units & 1, ctl);
+      if (!ok) break;
+      ++units;
+      tc_fence_after();
+      const int ig = m * kTileRows + i;
+      __nv_bfloat16 *to = a.dq + ((static_cast<size_t>(b) * S + ig) * nh + h) * (dn + dr);
+#pragma unroll 1
+      for (int c = 16 * g; c < dn + dr; c += 32) {
+        uint32_t v[16];
+        tmem_ld_x16((c < dn ? tdQ + c : tdQr + (c - dn)) + lane_off, v);
+        tmem_wait_ld();
+        reg_fence<16>(v);
+        if (ig < S) {
+          auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale); };
+          store_32(to + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+#undef XATTN_DQ_UNIT
+
 template <int NS>
 struct DkvLayout {
   static constexpr int kStages = NS == 1 ? 6 : 3;                    // (NS = 1 with three: 1850 cycles a tile, bound by their turn)
@@ -547,318 +866,6 @@ __global__ void __maxnreg__(168)
 }
 #undef XATTN_DKV_UNIT
 
-// dQ: a CTA per (batch, head, 128 queries). Q stays in shared memory and dO in TMEM (the A operand of dP), which leaves room
-// for three stages of K: K(n) is needed from S(n) to dQ(n), and with two the next scores waited for it. V has one stage: only
-// dP(n) reads it.
-template <int NS>
-struct LatentDqLayout {
-  static constexpr int kStages = 3;
-  static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = kQ + (NS + 1) * kKeySub;
-  static constexpr uint32_t kV = kK + kStages * (NS + 1) * kKeySub;
-  static constexpr uint32_t kBars = kV + NS * kKeySub;
-  static constexpr int kNumBars = 2 * kStages + 10;
-  static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
-  static constexpr uint32_t kUsed = kMisc + 32;
-  static constexpr uint32_t kDynBytes = kUsed + 1024 > 116 * 1024 ? kUsed + 1024 : 116 * 1024;   // one CTA an SM (TMEM)
-  static_assert(kDynBytes <= 227 * 1024, "exceeds the opt-in shared memory of one CTA");
-};
-
-// Warps: 0 TMA; 1 MMA issuer and TMEM owner; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns a group.
-// TMEM: S [0, 128) | dP [128, 256), dS bf16 over [128, 160) and [192, 224) | dO bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448.
-template <int NS, bool kFull>
-__global__ void __maxnreg__(168)
-    latent_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
-                     const __grid_constant__ CUtensorMap mrope, const LatentArgs a) {
-  using L = LatentDqLayout<NS>;
-  constexpr int kStages = L::kStages;
-  extern __shared__ uint8_t latent_dq_smem[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(latent_dq_smem) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int S = a.S, nh = a.nh, dn = kFull ? 64 * NS : a.dn, dr = a.dr, dv = kFull ? 64 * NS : a.dv;
-  const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
-  const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
-  const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh, num_units = num_m * BH;
-  // Units, most key tiles first, dealt to and fro as in the kernel before.
-  auto unit_at = [&](int k) {
-    const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-    return k * G + ((k & 1) ? G - 1 - c : c);
-  };
-#define XATTN_DQ_UNIT(u)                                             \
-  const int m = num_m - 1 - (u) / BH, bh = (u) % BH;                 \
-  const int b = bh / nh, h = bh - b * nh, T = m + 1; /* key tiles */ \
-  (void)b;                                                           \
-  (void)h
-  const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV),
-                 bar0 = smem_u32(smem + L::kBars);
-  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
-  auto k_full = [&](int s) { return bar(s); };
-  auto k_empty = [&](int s) { return bar(kStages + s); };
-  constexpr int kB = 2 * kStages;
-  const uint32_t v_full = bar(kB), v_empty = bar(kB + 1), q_full = bar(kB + 2), s_full = bar(kB + 3), dp_full = bar(kB + 4),
-                 dq_done = bar(kB + 5), q_empty = bar(kB + 6), s_free = bar(kB + 7), ds_full = bar(kB + 8), do_full = bar(kB + 9);
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
-  const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
-
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i >= kB + 7 ? 256 : 1);
-    fence_mbar_init();
-    tma_prefetch_desc(&mq);
-    tma_prefetch_desc(&mkv);
-    tma_prefetch_desc(&mrope);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  grid_dep_launch();
-  grid_dep_wait();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
-  const uint32_t tS = tmem, tdP = tmem + 128, tdO = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
-
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    bool ok = true;
-    int units = 0, issued_k = 0, issued_v = 0;
-#pragma unroll 1
-    for (int k = 0; ok; ++k) {
-      const int u = unit_at(k);
-      if (u >= num_units) break;
-      XATTN_DQ_UNIT(u);
-      auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int col, int head, int row0) {
-        XATTN_DCHECK(col % 8 == 0 && head >= 0 && head < nh && row0 >= 0 && row0 < S && dst >= sQ && dst + kKeySub <= bar0, a.status);
-        tma_load_4d_elect(dst, map, full, col, head, row0, b);
-      };
-      // The unit's first K before its Q: a stage is free sooner.
-      for (int n = 0; n < T; ++n) {
-        const int s = issued_k % kStages;
-        if (!warp_wait(k_empty(s), ((issued_k / kStages) & 1) ^ 1, ctl)) { ok = false; break; }
-        mbar_expect_tx_elect(k_full(s), (k_subs + 1) * kKeySub);
-        const uint32_t dk = sK + s * (NS + 1) * kKeySub;
-        for (int c = 0; c < k_subs; ++c) load(dk + c * kKeySub, &mkv, k_full(s), 64 * c, h, n * kTileRows);
-        load(dk + NS * kKeySub, &mrope, k_full(s), 0, 0, n * kTileRows);
-        ++issued_k;
-        if (n == 0) {
-          if (!warp_wait(q_empty, (units & 1) ^ 1, ctl)) { ok = false; break; }
-          mbar_expect_tx_elect(q_full, (k_subs + 1) * kKeySub);
-          for (int c = 0; c < k_subs; ++c) load(sQ + c * kKeySub, &mq, q_full, 64 * c, h, m * kTileRows);
-          load(sQ + NS * kKeySub, &mq, q_full, dn, h, m * kTileRows);
-          ++units;
-        }
-        if (!warp_wait(v_empty, (issued_v & 1) ^ 1, ctl)) { ok = false; break; }
-        mbar_expect_tx_elect(v_full, v_subs * kKeySub);
-        for (int c = 0; c < v_subs; ++c) load(sV + c * kKeySub, &mkv, v_full, dn + 64 * c, h, n * kTileRows);
-        ++issued_v;
-      }
-    }
-    // Every copy in flight has landed before the CTA can exit.
-    if (units > 0) mbar_drain(q_full, (units - 1) & 1, ctl);
-    for (int n = max(issued_k - kStages, 0); n < issued_k; ++n) mbar_drain(k_full(n % kStages), (n / kStages) & 1, ctl);
-    if (issued_v > 0) mbar_drain(v_full, (issued_v - 1) & 1, ctl);
-  } else if (warp == 1) {
-    // ---------------- MMA issuer: S(n + 1) before dQ(n), dP(n + 1) behind it (dS(n) lies in dP's place) ----------------
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
-    const uint32_t idesc_dq = idesc_bf16_f32(128, dn, false, true), idesc_dr = idesc_bf16_f32(128, dr, false, true);
-    constexpr uint32_t kSubDesc = kKeySub >> 4;
-    const uint64_t dQ = smem_desc(sQ, 16, 1024, kSwizzle128);
-    const uint64_t dK = smem_desc(sK, 16, 1024, kSwizzle128), dV = smem_desc(sV, 16, 1024, kSwizzle128);
-    const uint64_t dKt = smem_desc(sK, kKeySub, 1024, kSwizzle128);       // MN-major: 64 columns a sub-tile
-    // (t counts the tiles of all units.)
-    auto scores = [&](int t, bool last) -> bool {
-      const int s = t % kStages;
-      if (!warp_wait(k_full(s), (t / kStages) & 1, ctl) || !warp_wait(s_free, (t & 1) ^ 1, ctl)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t kd = dK + s * (NS + 1) * kSubDesc;
-#pragma unroll
-        for (int c = 0; c < NS; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (4 * c + kk < dn_steps) mma_ss(tS, dQ + c * kSubDesc + kk * 2, kd + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk < dr_steps) mma_ss(tS, dQ + NS * kSubDesc + kk * 2, kd + NS * kSubDesc + kk * 2, idesc_s, 1u);
-        mma_commit(s_full);
-        if (last) mma_commit(q_empty);
-      }
-      __syncwarp();
-      return true;
-    };
-    auto issue_dp = [&](int t) -> bool {
-      if (!warp_wait(v_full, t & 1, ctl)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int c = 0; c < NS; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (4 * c + kk < dv_steps) mma_ts(tdP, tdO + 32 * c + 8 * kk, dV + c * kSubDesc + kk * 2, idesc_s, c + kk > 0 ? 1u : 0u);
-        mma_commit(dp_full);
-        mma_commit(v_empty);
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = true;
-    int units = 0, t = 0;
-#pragma unroll 1
-    for (int k = 0; ok; ++k) {
-      const int u = unit_at(k);
-      if (u >= num_units) break;
-      XATTN_DQ_UNIT(u);
-      (void)bh;
-      ok = warp_wait(q_full, units & 1, ctl) && scores(t, T == 1) && warp_wait(do_full, units & 1, ctl) && issue_dp(t);
-#pragma unroll 1
-      for (int n = 0; ok && n < T; ++n, ++t) {
-        const int s = t % kStages;
-        const bool more = n + 1 < T;
-        // (dS of the unit's first tile comes from threads that have read the dQ before: it may be overwritten.)
-        ok = (!more || scores(t + 1, n + 2 == T)) && warp_wait(ds_full, t & 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {                                          // dQ += dS K_n
-          const uint64_t kd = dKt + s * (NS + 1) * kSubDesc;
-#pragma unroll
-          for (int kk = 0; kk < kTileRows / 16; ++kk) {
-            const uint32_t ds = tdP + (kk / 4) * 64 + (kk % 4) * 8;
-            mma_ts(tdQ, ds, kd + kk * 128, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
-            mma_ts(tdQr, ds, kd + NS * kSubDesc + kk * 128, idesc_dr, (n > 0 || kk > 0) ? 1u : 0u);
-          }
-          mma_commit(k_empty(s));
-          if (!more) mma_commit(dq_done);
-        }
-        __syncwarp();
-        ok = !more || issue_dp(t + 1);
-      }
-      if (ok) ++units;
-    }
-    __syncwarp();
-    if (units > 0) mbar_drain(dq_done, (units - 1) & 1, ctl);
-  } else if (warp >= 4) {
-    // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
-    const int g = (warp - 4) >> 2, quarter = warp & 3;
-    const int i = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int c0 = 64 * g;                              // first key column of this group
-    const float scale_log2 = a.scale * kLog2e;
-    float nlse2 = 0.f, nD = 0.f;
-    // A unit's dO of this thread's row, 64 columns a group, into TMEM (rows behind the last, and columns behind dv: zeros), and
-    // the row's numbers.
-    auto begin = [&](int u) {
-      XATTN_DQ_UNIT(u);
-      (void)T;
-      const int ig = m * kTileRows + i;
-      const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h, at = static_cast<size_t>(bh) * padded_rows(S) + ig;
-      XATTN_DCHECK(ig >= S || row < static_cast<size_t>(a.B) * S * nh, a.status);
-      nlse2 = a.nlse[at], nD = a.nD[at];
-      if (NS == 2 || g == 0) {
-        uint32_t x[32];
-        uint4 *v = reinterpret_cast<uint4 *>(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = ig < S && c0 + 8 * e < dv ? __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + c0 + 8 * e))
-                                           : make_uint4(0u, 0u, 0u, 0u);
-        tmem_st_x32(tdO + lane_off + 32 * g, x);
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      mbar_arrive(do_full);
-    };
-    int units = 0, t = 0;
-    if (unit_at(0) < num_units) begin(unit_at(0));
-#pragma unroll 1
-    for (int k = 0;; ++k) {
-      const int u = unit_at(k);
-      if (u >= num_units) break;
-      XATTN_DQ_UNIT(u);
-      bool ok = true;
-#pragma unroll 1
-      for (int n = 0; n < T; ++n, ++t) {
-        if (!warp_wait(s_full, t & 1, ctl)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t p[64];
-        tmem_ld_x32(tS + lane_off + c0, p);
-        tmem_ld_x32(tS + lane_off + c0 + 32, p + 32);
-        tmem_wait_ld();
-        reg_fence<64>(p);
-        tc_fence_before();
-        mbar_arrive(s_free);
-#pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float x0, x1;
-          ffma2(x0, x1, __uint_as_float(p[e]), __uint_as_float(p[e + 1]), scale_log2, scale_log2, nlse2, nlse2);
-          p[e] = __float_as_uint(ex2_approx(x0));
-          p[e + 1] = __float_as_uint(ex2_approx(x1));
-        }
-        if (n == m) {                                     // keys behind the query
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (c0 + e > i) p[e] = 0u;
-        }
-        // dS = P (dP - D), bf16 over the first half of this group's dP.
-        if (!warp_wait(dp_full, t & 1, ctl)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t ds[32];
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t d[32];
-          tmem_ld_x32(tdP + lane_off + c0 + 32 * part, d);
-          tmem_wait_ld();
-          reg_fence<32>(d);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float t0, t1;
-            fadd2(t0, t1, __uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), nD, nD);
-            fmul2(t0, t1, t0, t1, __uint_as_float(p[32 * part + 2 * e]), __uint_as_float(p[32 * part + 2 * e + 1]));
-            ds[16 * part + e] = pack_bf16x2(t0, t1);
-          }
-        }
-        tmem_st_x32(tdP + lane_off + c0, ds);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(ds_full);
-      }
-
-      if (!ok) break;
-      // The next unit's dO (its place was read by dP of the last tile), then dq = bf16(scale * sum) while its S and dP are
-      // made; group g writes every second 16 columns of the thread's row.
-      if (unit_at(k + 1) < num_units) begin(unit_at(k + 1));
-      if (!warp_wait(dq_done, units & 1, ctl)) break;
-      ++units;
-      tc_fence_after();
-      const int ig = m * kTileRows + i;
-      __nv_bfloat16 *to = a.dq + ((static_cast<size_t>(b) * S + ig) * nh + h) * (dn + dr);
-#pragma unroll 1
-      for (int c = 16 * g; c < dn + dr; c += 32) {
-        uint32_t v[16];
-        tmem_ld_x16((c < dn ? tdQ + c : tdQr + (c - dn)) + lane_off, v);
-        tmem_wait_ld();
-        reg_fence<16>(v);
-        if (ig < S) {
-          auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale); };
-          store_32(to + c, pair(0), pair(2), pair(4), pair(6), pair(8), pair(10), pair(12), pair(14));
-        }
-        __syncwarp();
-      }
-      tc_fence_before();
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
-}
-#undef XATTN_DQ_UNIT
-
 // k_rope's gradient: the heads' parts added in order, four columns a thread.
 __global__ void __launch_bounds__(256) latent_rope_kernel(const LatentArgs a) {
   grid_dep_launch();
@@ -889,11 +896,10 @@ cudaError_t launch_latent_bwd_ns(const LatentMaps &q64, const LatentMaps &q128, 
   if (err == cudaSuccess) err = allow_smem(latent_dq_kernel<NS, kFull>, LQ::kDynBytes, allowed_q);
   if (err != cudaSuccess) return err;
   const long long num_n = (a.S + kTileRows - 1) / kTileRows, units = num_n * a.B * a.nh;
-  err = launch_pdl(latent_dkv_kernel<NS, kFull>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LK::kDynBytes, stream,
-                   q64.q, q128.kv, q128.rope, q64.dO, a);
+  const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+  err = launch_pdl(latent_dq_kernel<NS, kFull>, grid, kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv, q128.rope, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(latent_dq_kernel<NS, kFull>, static_cast<unsigned>(units < sms ? units : sms), kBwdThreads, LQ::kDynBytes, stream, q128.q, q128.kv,
-                    q128.rope, a);
+  return launch_pdl(latent_dkv_kernel<NS, kFull>, grid, kBwdThreads, LK::kDynBytes, stream, q64.q, q128.kv, q128.rope, q64.dO, a);
 }
 
 }  // namespace
@@ -910,10 +916,7 @@ void latent_bwd_workspace_carve(LatentArgs &a, void *base) {
 
 cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, const LatentArgs &a, int sms,
                               cudaStream_t stream) {
-  const int head_blocks = (a.nh + kRowsHeads - 1) / kRowsHeads;
-  cudaError_t err = launch_pdl(latent_bwd_rows_kernel, static_cast<unsigned>(a.B) * (padded_rows(a.S) / kRowsPos) * head_blocks,
-                               256, 0, stream, a, head_blocks);
-  if (err != cudaSuccess) return err;
+  cudaError_t err;
   const bool one = a.dn <= 64 && a.dv <= 64;
   if (a.dn == (one ? 64 : 128) && a.dv == a.dn)
     err = one ? launch_latent_bwd_ns<1, true>(q64, q128, a, sms, stream) : launch_latent_bwd_ns<2, true>(q64, q128, a, sms, stream);
