@@ -45,7 +45,7 @@ struct LatentDqLayout {
   static constexpr uint32_t kK = kQ + (NS + 1) * kKeySub;
   static constexpr uint32_t kV = kK + kStages * (NS + 1) * kKeySub;
   static constexpr uint32_t kBars = kV + NS * kKeySub;
-  static constexpr int kNumBars = 2 * kStages + 12;
+  static constexpr int kNumBars = 2 * kStages + 13;
   static constexpr uint32_t kRows = (kBars + 8 * kNumBars + 15) / 16 * 16;   // -LSE log2 e and -D
   static constexpr uint32_t kMisc = kRows + kTileRows * 8;
   static constexpr uint32_t kUsed = kMisc + 32;
@@ -88,14 +88,14 @@ __global__ void __maxnreg__(168)
   constexpr int kB = 2 * kStages;
   const uint32_t v_full = bar(kB), v_empty = bar(kB + 1), q_full = bar(kB + 2), s_full = bar(kB + 3), dp_full = bar(kB + 4),
                  dq_done = bar(kB + 5), q_empty = bar(kB + 6), s_free = bar(kB + 7), ds_full = bar(kB + 8), do_full = bar(kB + 9),
-                 rows_empty = bar(kB + 10), rows_full = bar(kB + 11);
+                 rows_empty = bar(kB + 10), rows_first = bar(kB + 11), rows_full = bar(kB + 12);
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 16);
   const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i == kB + 11 ? 64 : (i >= kB + 7 ? 256 : 1));
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i == kB + 12 ? 64 : (i >= kB + 7 ? 256 : 1));
     fence_mbar_init();
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mkv);
@@ -112,6 +112,53 @@ __global__ void __maxnreg__(168)
   grid_dep_wait();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   const uint32_t tS = tmem, tdP = tmem + 128, tdO = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
+
+  // -LSE log2 e and -D of a unit's rows r0 .. r0 + count - 1, by a warp, sixteen lanes a row of o and dO. (A kernel of its own
+  // for them took 10 us of B8 S1024, 12 heads of 64 + 32 / 64; by the threads whose rows they are a unit began 2 us later.)
+  auto row_numbers = [&](int u, int r0, int count) {
+    XATTN_DQ_UNIT(u);
+    (void)T;
+    const int part = lane & 15;
+    float2 *rows = reinterpret_cast<float2 *>(smem + L::kRows) + r0;
+    constexpr int kOnce = 8;                                          // rows a half warp has in flight
+#pragma unroll 1
+    for (int from = lane >> 4; from < count; from += 2 * kOnce) {
+      uint4 x[kOnce], y[kOnce];
+      float lse[kOnce];
+#pragma unroll
+      for (int e = 0; e < kOnce; ++e) {
+        const int ig = m * kTileRows + r0 + from + 2 * e;
+        const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
+        x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
+        lse[e] = INFINITY;                                            // rows behind the last get a weight of 0
+        if (ig >= S) continue;
+        lse[e] = a.lse[row];
+        if (8 * part < dv) {
+          x[e] = __ldg(reinterpret_cast<const uint4 *>(a.o + row * dv + 8 * part));
+          y[e] = __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + 8 * part));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kOnce; ++e) {
+        float dot = 0.f;
+        auto add = [&](uint32_t v, uint32_t w) {
+          dot = fmaf(bf16lo_to_f32(v), bf16lo_to_f32(w), dot);
+          dot = fmaf(bf16hi_to_f32(v), bf16hi_to_f32(w), dot);
+        };
+        add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
+#pragma unroll
+        for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        if (part == 0) rows[from + 2 * e] = make_float2(-lse[e] * kLog2e, -dot);
+      }
+    }
+    __syncwarp();
+    for (int r = lane; r < count; r += 32) {
+      const size_t at = static_cast<size_t>(bh) * padded_rows(S) + m * kTileRows + r0 + r;
+      const float2 v = rows[r];
+      a.nlse[at] = v.x;
+      a.nD[at] = v.y;
+    }
+  };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -232,57 +279,13 @@ __global__ void __maxnreg__(168)
     __syncwarp();
     if (units > 0) mbar_drain(dq_done, (units - 1) & 1, ctl);
   } else if (warp < 4) {
-    // ---------------- A unit's -LSE log2 e and -D, a unit ahead: 64 rows a warp, sixteen lanes a row of o and dO ----------------
-    // (A kernel of its own for them took 10 us of B8 S1024, 12 heads of 64 + 32 / 64; by the threads whose rows they are, a row
-    // a thread, a unit began 2 us later.)
-    const int part = lane & 15;
-    float2 *rows = reinterpret_cast<float2 *>(smem + L::kRows);
+    // ---------------- The rows' numbers, a unit ahead ----------------
 #pragma unroll 1
-    for (int k = 0;; ++k) {
+    for (int k = 1;; ++k) {
       const int u = unit_at(k);
       if (u >= num_units || !warp_wait(rows_empty, (k & 1) ^ 1, ctl)) break;
-      XATTN_DQ_UNIT(u);
-      (void)T;
-      constexpr int kOnce = 8;                                        // rows a half warp has in flight
-#pragma unroll 1
-      for (int r0 = 64 * (warp - 2) + (lane >> 4); r0 < 64 * (warp - 1); r0 += 2 * kOnce) {
-        uint4 x[kOnce], y[kOnce];
-        float lse[kOnce];
-#pragma unroll
-        for (int e = 0; e < kOnce; ++e) {
-          const int ig = m * kTileRows + r0 + 2 * e;
-          const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
-          x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
-          lse[e] = INFINITY;                                          // rows behind the last get a weight of 0
-          if (ig >= S) continue;
-          lse[e] = a.lse[row];
-          if (8 * part < dv) {
-            x[e] = __ldg(reinterpret_cast<const uint4 *>(a.o + row * dv + 8 * part));
-            y[e] = __ldg(reinterpret_cast<const uint4 *>(a.dO + row * dv + 8 * part));
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kOnce; ++e) {
-          float dot = 0.f;
-          auto add = [&](uint32_t v, uint32_t w) {
-            dot = fmaf(bf16lo_to_f32(v), bf16lo_to_f32(w), dot);
-            dot = fmaf(bf16hi_to_f32(v), bf16hi_to_f32(w), dot);
-          };
-          add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
-#pragma unroll
-          for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-          if (part == 0) rows[r0 + 2 * e] = make_float2(-lse[e] * kLog2e, -dot);
-        }
-      }
-      __syncwarp();
+      row_numbers(u, 64 * (warp - 2), 64);
       mbar_arrive(rows_full);
-#pragma unroll
-      for (int r = 64 * (warp - 2) + lane; r < 64 * (warp - 1); r += 32) {
-        const size_t at = static_cast<size_t>(bh) * padded_rows(S) + m * kTileRows + r;
-        const float2 v = rows[r];
-        a.nlse[at] = v.x;
-        a.nD[at] = v.y;
-      }
     }
   } else {
     // ---------------- P and dS: one query row per thread, 64 key columns per group ----------------
@@ -312,14 +315,20 @@ __global__ void __maxnreg__(168)
       }
       tc_fence_before();
       mbar_arrive(do_full);
-      if (!warp_wait(rows_full, k & 1, ctl)) return false;
+      if (!(k == 0 ? warp_wait(rows_first, 0, ctl) : warp_wait(rows_full, (k & 1) ^ 1, ctl))) return false;
       const float2 r = reinterpret_cast<const float2 *>(smem + L::kRows)[i];
       nlse2 = r.x, nD = r.y;
       mbar_arrive(rows_empty);
       return true;
     };
     int units = 0, t = 0;
-    bool ok = unit_at(0) < num_units && begin(unit_at(0), 0);
+    // (The first unit's numbers by these warps: by the two that make them later a short call took 1.5 us more.)
+    bool ok = unit_at(0) < num_units;
+    if (ok) {
+      row_numbers(unit_at(0), 16 * (warp - 4), 16);
+      mbar_arrive(rows_first);
+      ok = begin(unit_at(0), 0);
+    }
 #pragma unroll 1
     for (int k = 0; ok; ++k) {
       const int u = unit_at(k);
