@@ -20,6 +20,9 @@
 //     group per row tile (they read the same tiles at the same time, the second from L2); lengths are read on the
 //     device, so a captured graph follows them. A run's end cuts a sequence: such pieces write (max, sum, O)
 //     records, and latent_combine_kernel merges them in order.
+//   * Measured: 64 sequences of 8192 positions, one token of 16 heads, 512 + 64: 106 us, 5.7 TB/s; of 4096 62 us, and 79 with 64
+//     heads, 115 with 128 (two row tiles: 2560 cycles of shared-memory reads a tile of 64 rows, 3200 taken); one
+//     sequence of 1000 11 us. 14 us do not grow with the cache.
 //   * Roundings: scores, maxima, sums and O are fp32; P is rounded to bf16, C's type.
 //   * Pages as in attn_tree.cu: a box whose table entry is no page is loaded from outside the pool (zeros).
 // Warps: 0 TMA producer; 1 TMEM owner and issuer of S^T; 10 issuer of O^T (apart, so that a tile's P is not kept waiting
@@ -756,6 +759,8 @@ cudaError_t launch_latent_n(const LatentDecodeMaps &maps, const LatentDecodeArgs
 
 }  // namespace
 
+// The fewest columns that hold the rows: 64 sequences of 4096, 16 rows 62 us (by 32 columns 63, by 64 66 to 68), 32 rows 66 (by 64
+// 70).
 int latent_tile_rows(int n, int nh) {
   const long long rows = static_cast<long long>(n) * nh;
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);

@@ -15,6 +15,8 @@
 //     two may lie anywhere in the ring.
 // Roundings: P to bf16, V's type, before P V; o to bf16. All exponentials on the special-function unit: one pair in eight on the FMA
 // pipe, as in attn_fwd_sm103.cu, was 1 % slower here, one in four 5 %.
+// Bound by the tensor cores, and between units by the softmax's turn: B4 S4093, 16 heads of 128 + 64 / 128 243 us, 1411 TFLOP/s of
+// visible pairs (71 % of the measured peak); 64 + 32 / 64 at S4096 133 us, 1293, at B8 S1024, 12 heads 24 us, 665.
 // TMEM: S_A [0,128) S_B [128,256) fp32 | O_A, O_B from 256, 64 NS columns each | NS = 1: P_A [384,448) P_B [448,512), so that the
 // next scores are issued as soon as these are read; NS = 2: P_X over the first half of S_X, the next scores behind P V.
 #include <type_traits>
@@ -482,7 +484,8 @@ cudaError_t launch_latent_fwd_ns(const LatentMaps &maps, const LatentArgs &a, in
 }  // namespace
 
 cudaError_t launch_latent_fwd(const LatentMaps &maps, const LatentArgs &a, int sms, cudaStream_t stream) {
-  // One sub-tile that is full: products without conditions (B8 S1024, 12 heads of 64 + 32 / 64: 35.5 -> 32.2 us). With two the
+  // One sub-tile that is full: products without conditions (B8 S1024, 12 heads of 64 + 32 / 64: 27.5 -> 24.5 us, B4 S4096, 16
+  // heads 144 -> 133). With two the
   // same is slower: S and P V of one query tile then go out in a row and keep the other's waiting (B4 S4093, 16 heads of 128 + 64 /
   // 128: 250 -> 278 us).
   if (a.dn == 64 && a.dv == 64 && a.scale >= 0.f) return launch_latent_fwd_ns<1, true, false>(maps, a, sms, stream);
