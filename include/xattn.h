@@ -37,8 +37,8 @@
  *     two seconds) gives up, records XATTN_ERR_DEVICE_TIMEOUT in a device status word
  *     and finishes; xattn_check_device_status reports it.
  *   - Scratch is stream-ordered: taken on `stream` and released on it when the call's work
- *     is enqueued. The window, tree and fp32 window calls take it from a memory pool of the
- *     library's own (one per device), which keeps what it has grown to (xattn_trim_scratch).
+ *     is enqueued. The window, tree, latent, page-table and fp32 window calls take it from a memory pool
+ *     of the library's own (one per device), which keeps what it has grown to (xattn_trim_scratch).
  *   - CUDA graphs: the calls may be captured on a stream and replayed, a process's first
  *     call on a device among them (but xattn_bwd_noalloc's, see there). Scratch is recorded
  *     in the graph as stream-ordered allocation nodes.
@@ -61,8 +61,9 @@ typedef enum {
                                          stage calls and xattn_bwd_noalloc: {32, 64});
                                          fp32: hd > 128; latent and page calls:
                                          the sizes that their comments give */
-    XATTN_ERR_MISALIGNED = 5,         /* a bf16 tensor pointer is not 16-byte aligned, or a float
-                                         or int array not 4-byte (xattn_tree_decode's words: 8) */
+    XATTN_ERR_MISALIGNED = 5,         /* a bf16 tensor pointer is not 16-byte aligned (some latent
+                                         outputs: 32), or a float or int array not 4-byte
+                                         (xattn_tree_decode's words, slot maps: 8) */
     XATTN_ERR_CUDA = 6,               /* a CUDA runtime or driver call failed */
     XATTN_ERR_NO_DEVICE_SUPPORT = 7,  /* the current device is not compute capability 10.3 */
     XATTN_ERR_DEVICE_TIMEOUT = 8,     /* a bounded on-device wait expired (reported later) */
@@ -376,7 +377,8 @@ xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_t
  *   dk_rope_j = scale sum_h sum_i dS_ij q_i[dn:].
  * dn, dv multiples of 16 up to 128, dr of 16 up to 64 (else XATTN_ERR_UNSUPPORTED_HD); any S >= 1 up to 2^30;
  * any finite scale whose product with log2 e is finite (the backward too). bf16 tensors 16-byte aligned (the
- * forward's o, and dq and dkv: 32-byte), lse 4-byte. Arithmetic as in xattn_fwd and xattn_bwd; k_rope's gradient is summed over the heads in fp32. Every
+ * forward's o, and dq and dkv: 32-byte), lse 4-byte. Arithmetic as in xattn_fwd and xattn_bwd; k_rope's
+ * gradient is summed over the heads in fp32. Every
  * output is bit-for-bit reproducible. Scratch of the backward is stream-ordered, from the library's pool.
  */
 xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope, int B, int S, int nh, int dn, int dr,

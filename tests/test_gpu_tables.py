@@ -51,6 +51,10 @@ CASES = [
     (20000, 2, 16, 20, 2, 3000, 100),
     (7, 300, 16, 0, 4700, 2500, 2),     # long prompts
     (2, 3, 256, 300, 400, 0, 4),        # no page at all
+    (64, 20, 16, 200, 80, 3000, 0),     # a plan and a fill, a release by one block
+    (700, 10, 16, 80, 2, 700, 4),       # the other way round
+    (9, 40, 16, 300, 40, 100, 2),
+    (64, 300, 16, 40, 30, 500, 1),      # few sequences, wide tables
 ]
 
 
