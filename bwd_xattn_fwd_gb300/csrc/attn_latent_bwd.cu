@@ -116,25 +116,26 @@ __global__ void __maxnreg__(168)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   const uint32_t tS = tmem, tdP = tmem + 128, tdO = tmem + 256, tdQ = tmem + 320, tdQr = tmem + 448;
 
-  // -LSE log2 e and -D of a unit's rows r0 .. r0 + count - 1, by a warp, sixteen lanes a row of o and dO. (A kernel of its own
+  // -LSE log2 e and -D of a unit's rows r0 .. r0 + count - 1, by a warp, 8 NS lanes a row of o and dO. (A kernel of its own
   // for them took 10 us of B8 S1024, 12 heads of 64 + 32 / 64; by the threads whose rows they are a unit began 2 us later.)
   auto row_numbers = [&](int u, int r0, int count) {
     XATTN_DQ_UNIT(u);
     (void)T;
-    const int part = lane & 15;
+    constexpr int kLanes = 8 * NS, kAtOnce = 32 / kLanes;
+    const int part = lane % kLanes;
     float2 *rows = reinterpret_cast<float2 *>(smem + L::kRows) + r0;
-    constexpr int kOnce = 8;                                          // rows a half warp has in flight
+    constexpr int kOnce = 8;                                          // rows that kLanes lanes have in flight
 #pragma unroll 1
-    for (int from = lane >> 4; from < count; from += 2 * kOnce) {
+    for (int from = lane / kLanes; from < count; from += kAtOnce * kOnce) {
       uint4 x[kOnce], y[kOnce];
       float lse[kOnce];
 #pragma unroll
       for (int e = 0; e < kOnce; ++e) {
-        const int ig = m * kTileRows + r0 + from + 2 * e;
+        const int at = from + kAtOnce * e, ig = m * kTileRows + r0 + at;
         const size_t row = (static_cast<size_t>(b) * S + ig) * nh + h;
         x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
         lse[e] = INFINITY;                                            // rows behind the last get a weight of 0
-        if (ig >= S) continue;
+        if (ig >= S || at >= count) continue;
         lse[e] = a.lse[row];
         if (8 * part < dv) {
           x[e] = __ldg(reinterpret_cast<const uint4 *>(a.o + row * dv + 8 * part));
@@ -150,8 +151,8 @@ __global__ void __maxnreg__(168)
         };
         add(x[e].x, y[e].x), add(x[e].y, y[e].y), add(x[e].z, y[e].z), add(x[e].w, y[e].w);
 #pragma unroll
-        for (int off = 8; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        if (part == 0) rows[from + 2 * e] = make_float2(-lse[e] * kLog2e, -dot);
+        for (int off = kLanes / 2; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        if (part == 0 && from + kAtOnce * e < count) rows[from + kAtOnce * e] = make_float2(-lse[e] * kLog2e, -dot);
       }
     }
     __syncwarp();
