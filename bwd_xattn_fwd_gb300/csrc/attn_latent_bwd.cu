@@ -17,7 +17,7 @@
 // Every output is bit-for-bit reproducible. Roundings: P and dS to bf16, Q's, K's and dO's type, before their products; dS is
 // made of the unrounded P. B2 S4001, 16 heads of 128 + 64 / 128: dQ 181 us, 1445 TFLOP/s of its products (73 % of the measured
 // peak; tensor cores), dK/dV 273 us, 1203 (61 %; the shared-memory reads of its products and their
-// chain), k_rope 8. B8 S1024, 12 heads of 64 + 32 / 64: 39, 57 and 5 us (units' starts and ends, the P / dS chain).
+// chain), k_rope 8. B8 S1024, 12 heads of 64 + 32 / 64: 41, 56 and 5 us (units' starts and ends, the P / dS chain).
 #include "sm103_ptx.cuh"
 #include "xattn_internal.h"
 
@@ -35,8 +35,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
 }
 
 // NS: sub-tiles of dn, and of dv, that there is room for (dn, dv <= 64 NS). kFull: they are full (dn = dv = 64 NS), so that the
-// products' steps have no conditions (backward of B8 S1024, 12 heads of 64 + 32 / 64: 108 -> 104 us, B4 S4096,
-// 16 heads 653 -> 632; of 128 + 64 / 128 at B8 S2048 575 -> 572).
+// products' steps have no conditions (backward of B8 S1024, 12 heads of 64 + 32 / 64: 101 -> 99 us, B4 S4096,
+// 16 heads 646 -> 632; of 128 + 64 / 128 at B4 S4093 940 -> 936).
 
 // dQ: a unit is (batch, head, 128 queries). Q stays in shared memory and dO in TMEM (the A operand of dP), which leaves room
 // for three stages of K: K(n) is needed from S(n) to dQ(n), and with two the next scores waited for it. V has one stage: only
@@ -421,7 +421,7 @@ __global__ void __maxnreg__(168)
 
 template <int NS>
 struct DkvLayout {
-  static constexpr int kStages = NS == 1 ? 6 : 3;                    // (NS = 1 with three: B4 S4096, 16 heads 668 us for 632)
+  static constexpr int kStages = NS == 1 ? 6 : 3;                    // (NS = 1 with three: B4 S4096, 16 heads 661 us for 632)
   static constexpr uint32_t kK = 0;                                  // NS sub-tiles and the shared part
   static constexpr uint32_t kV = kK + (NS + 1) * kKeySub;
   static constexpr uint32_t kQ = kV + NS * kKeySub;                  // stages of Q (NS + 1 sub-tiles)
@@ -588,7 +588,7 @@ __global__ void __maxnreg__(168)
     // dS^T have one place), and S^T, dV fill the time that the dS warps take. (With two issuers the pipe took S^T between dK
     // and dP^T: 2430 cycles a tile, 2200 so.)
     // NS = 1: the products are short and their issue is what takes time (1750 cycles a tile by one thread), so two threads (B4 S4096,
-    // 16 heads of 64 + 32 / 64: 700 -> 632 us);
+    // 16 heads of 64 + 32 / 64: 695 -> 632 us);
     // dP^T has two places and need not wait for dK.
     const bool p_side = warp == 1, s_side = L::kIssuers == 1 || warp == 3;
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kQRows, false, false);
