@@ -58,7 +58,8 @@ struct LatentDqLayout {
 
 // Warps: 0 TMA; 1 MMA issuer and TMEM owner; 2-3 the rows' numbers; 4-7 and 8-11 P and dS, a query row a thread, 64 key columns
 // a group.
-// TMEM: S [0, 128) | dP [128, 256), dS bf16 over [128, 160) and [192, 224) | dO bf16 [256, 320) | dQ [320, 512), its part for k_rope from 448.
+// TMEM: S [0, 128) | dP [128, 256), dS bf16 over [128, 160) and [192, 224) | dO bf16 [256, 320) | dQ [320, 512), its part for
+// k_rope from 448.
 template <int NS, bool kFull>
 __global__ void __maxnreg__(168)
     latent_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,

@@ -316,9 +316,9 @@ __global__ void __launch_bounds__(kFillThreads) cache_write_kernel(const WriteAr
 
 unsigned blocks_for(long long threads) { return static_cast<unsigned>((threads + kFillThreads - 1) / kFillThreads); }
 
-// One block does all of a small call: no scratch and no second kernel. A reserve of 1000 tokens of 1000 sequences takes 6 us so
-// (two kernels 14), of 2048 of 128 7.4 (9.3), of 4000 of 4 8.1 (7.4), of 8192 of 512 12.4 (7.9). A release of 64 sequences takes 3.7 us on the GPU (3.3) and
-// less of the host's time (2.2 for 4.9), of 8 1.8 (3.3), of 256 7.8 (3.4).
+// One block does all of a small call: no scratch and no second kernel. A reserve of 1000 tokens of 1000 sequences takes 6 us
+// so (two kernels 14), of 2048 of 128 7.4 (9.3), of 4000 of 4 8.1 (7.4), of 8192 of 512 12.4 (7.9). A release of 64
+// sequences takes 3.7 us on the GPU (3.3) and less of the host's time (2.2 for 4.9), of 8 1.8 (3.3), of 256 7.8 (3.4).
 constexpr int kSmallTokens = 2048, kSmallSeqs = 64, kSmallEntries = 16384;
 
 }  // namespace
