@@ -633,7 +633,8 @@ def attention_latent_decode(q, pages, page_table, ctx_lens, dc, scale, stream=No
     """(o [B,n,nh,dc], lse [B,n,nh]) of latent attention in its absorbed form, n <= 64 new tokens a sequence over
     a paged cache: q [B,n,nh,dc+dr] against the rows of pages [num_pages,page_size,dc+dr] (bf16), whose first dc
     numbers are the values too, through page_table [B,max_pages] and ctx_lens [B] (int32). The new tokens' rows
-    are already at positions ctx_lens .. ctx_lens + n - 1 (latent_write); token i sees positions 0 .. ctx_lens + i.
+    are already at positions ctx_lens .. ctx_lens + n - 1 (latent_write; of a sequence that got no places for them
+    the outputs mean nothing); token i sees positions 0 .. ctx_lens + i.
     scale: that of the expanded heads."""
     if stream is not None:
         with _Elsewhere(q, stream):
@@ -658,7 +659,8 @@ def cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_s
     (free_pages [num_pages], free_count [1]) into page_table [B,max_pages] (all int32; table and count in place).
     Returns (slots [tokens] int64, offsets [B+1], granted [B]): the pool rows of a ragged batch's tokens (-1:
     none), where each sequence's tokens begin, and the positions that it got (0 when the pages or `tokens` do
-    not reach)."""
+    not reach). What an attention call gives for a sequence that got less than it asked for means nothing: it sees rows
+    that were not written."""
     if stream is not None:
         with _Elsewhere(page_table, stream):
             return cache_reserve(page_table, ctx_lens, new_lens, free_pages, free_count, page_size, tokens)

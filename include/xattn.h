@@ -417,6 +417,9 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
  *     tokens (sequences before it are served first; one that needs no new page is served all the same)
  *   slots [tokens]: token t's row of the pool, page * page_size + row in the page; -1 for tokens that got
  *     none, and behind the last one
+ * A sequence that got less than it asked for has new tokens without a row. Attention calls for its new_lens[b] tokens would
+ * see rows there that were not written (what another request left in its last page, NaN perhaps): leave it out of them, or
+ * drop its outputs, which mean nothing. The other sequences' do not depend on it.
  * The pages below ctx_lens[b] are the sequence's already (a partly filled one goes on being filled). The lengths
  * are taken within [0, max_pages * page_size].
  *
