@@ -33,7 +33,8 @@ struct DeviceInfo {
 DeviceInfo g_dev[kMaxDevices];
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
+PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
+std::once_flag g_driver_once;
 
 uint64_t wait_limit_ns() {
   static const uint64_t v = [] {
@@ -129,16 +130,20 @@ xattn_status scratch_alloc(DeviceInfo &d, size_t bytes, cudaStream_t stream, voi
   return XATTN_ERR_CUDA;
 }
 
-xattn_status get_encode() {
-  std::call_once(g_encode_once, [] {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+// The driver's functions that the library calls by themselves.
+xattn_status get_driver() {
+  std::call_once(g_driver_once, [] {
+    auto entry = [](const char *name, unsigned version) -> void * {
+      void *fn = nullptr;
+      cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+      const bool found = cudaGetDriverEntryPointByVersion(name, &fn, version, cudaEnableDefault, &q) == cudaSuccess &&
+                         q == cudaDriverEntryPointSuccess;
+      return found ? fn : nullptr;
+    };
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(entry("cuTensorMapEncodeTiled", 12000));
+    g_ctx_current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(entry("cuCtxGetCurrent", 4000));
   });
-  return g_encode ? XATTN_OK : XATTN_ERR_CUDA;
+  return g_encode && g_ctx_current ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
 // 4-D map over a contiguous [B, S, H, hd] bf16 tensor; box = one head's 128-row tile, or
@@ -335,13 +340,13 @@ bool window_f32_grid_ok(int B, int S, int nh) {
 xattn_status bf16_device(DeviceInfo **dev) {
   XATTN_TRY(device_info(dev));
   if (!(*dev)->sm103) return XATTN_ERR_NO_DEVICE_SUPPORT;
-  // Encoding a map needs the thread's context, which a thread whose first CUDA call this is does not have yet.
-  static thread_local const DeviceInfo *bound = nullptr;
-  if (bound != *dev) {
-    if (cudaSetDevice(static_cast<int>(*dev - g_dev)) != cudaSuccess) return XATTN_ERR_CUDA;
-    bound = *dev;
-  }
-  return get_encode();
+  XATTN_TRY(get_driver());
+  // Encoding a map needs a current context. A thread may have none (this is its first CUDA call, or its context was popped): it
+  // gets the device's primary one, as from any runtime call that needs one. A context that is current stays so.
+  CUcontext current = nullptr;
+  if (g_ctx_current(&current) != CUDA_SUCCESS) return XATTN_ERR_CUDA;
+  if (!current && cudaSetDevice(static_cast<int>(*dev - g_dev)) != cudaSuccess) return XATTN_ERR_CUDA;
+  return XATTN_OK;
 }
 
 // Sizes of an expanded latent attention; every row's vectors are whole 16-number pieces.

@@ -31,6 +31,9 @@
  *   - stream is a cudaStream_t (NULL = the legacy default stream) of the current
  *     device. Calls enqueue work and return; none synchronises the device (xtrain
  *     docs/06-performance.md, "Phase T7", design decision 3: no per-op synchronisation).
+ *   - A call runs in the calling thread's current context, which stays current. A thread without
+ *     one gets the device's primary context. The status word and the scratch pool belong to the
+ *     context of a process's first call on a device; use one context per device and process.
  *   - Argument checks run before any launch. On a check failure nothing is enqueued
  *     and the outputs are untouched. Launch failures return XATTN_ERR_CUDA.
  *   - A kernel that waits on an on-chip barrier longer than a bounded time (about
