@@ -431,12 +431,13 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       lat_arrive(meet, lane);
       return lat_wait(meet, meets++ & 1, ctl);
     };
-    if (warp == 2 && lane == 0 && rt == 0) a.plan[group] = make_int2(0, 0);
+    // (One group has no plan and no records: its one run cuts no sequence.)
+    if (warp == 2 && lane == 0 && rt == 0 && groups > 1) a.plan[group] = make_int2(0, 0);
     while (ok && lat_piece(walk, a)) {
       const int e0 = walk.e0, e1 = walk.e1, b = walk.b, ctx = walk.ctx, end = ctx + a.n;
-      const bool whole = e0 == 0 && e1 == walk.count;
+      const bool whole = groups == 1 || (e0 == 0 && e1 == walk.count);
       // A run that ends inside the sequence it started last says so to the combine.
-      if (warp == 2 && lane == 0 && rt == 0 && e0 == 0 && e1 < walk.count)
+      if (warp == 2 && lane == 0 && rt == 0 && !whole && e0 == 0)
         a.plan[group] = make_int2(b, runs.of(walk.first + walk.count - 1) + 1);
       float l[2 * K];
 #pragma unroll
@@ -777,6 +778,7 @@ int latent_groups(const LatentDecodeArgs &a, int sms) {
 }
 
 size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int tile_rows) {
+  if (groups == 1) return 0;
   return static_cast<size_t>(groups) * a.row_tiles * 2 * tile_rows * (a.dc * sizeof(float) + sizeof(float2)) +
          static_cast<size_t>(groups) * sizeof(int2);
 }

@@ -901,14 +901,17 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
   XATTN_TRY(make_map_latents(&maps.latents, pages, num_pages, page_size, dc, dc + dr, box_rows, 2));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int groups = latent_groups(a, dev->sms);
+  const size_t scratch = latent_decode_workspace_bytes(a, groups, tile_rows);
   void *base = nullptr;
-  XATTN_TRY(scratch_alloc(*dev, latent_decode_workspace_bytes(a, groups, tile_rows), st, &base));
-  const size_t records = static_cast<size_t>(groups) * a.row_tiles * 2 * tile_rows;
-  a.ws_o = static_cast<float *>(base);
-  a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + records * dc);
-  a.plan = reinterpret_cast<int2 *>(a.ws_ml + records);
+  if (scratch) {
+    XATTN_TRY(scratch_alloc(*dev, scratch, st, &base));
+    const size_t records = static_cast<size_t>(groups) * a.row_tiles * 2 * tile_rows;
+    a.ws_o = static_cast<float *>(base);
+    a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + records * dc);
+    a.plan = reinterpret_cast<int2 *>(a.ws_ml + records);
+  }
   xattn_status r = cuda_status(launch_latent_decode(maps, a, groups, tile_rows, st));
-  const cudaError_t fe = cudaFreeAsync(base, st);
+  const cudaError_t fe = scratch ? cudaFreeAsync(base, st) : cudaSuccess;
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
   return r;
 }

@@ -239,7 +239,7 @@ cudaError_t launch_latent_bwd(const LatentMaps &q64, const LatentMaps &q128, con
 // Absorbed form (attn_latent_decode.cu): n new tokens a sequence over a paged cache of rows of dc + dr numbers. Maps: over the
 // queries, boxes of 64 columns of tile_rows rows of one sequence, and (q_latents) of all dc columns of them; over the pool, boxes
 // of 64 columns of min(page_size, 64) rows of one page, and (latents) of two such side by side in the first dc columns. The
-// scratch, latent_decode_workspace_bytes(), is ws_o, ws_ml and plan.
+// scratch, latent_decode_workspace_bytes(), is ws_o, ws_ml and plan; with one group there is none.
 struct LatentDecodeMaps {
   CUtensorMap q, q_latents, pages, latents;
 };
