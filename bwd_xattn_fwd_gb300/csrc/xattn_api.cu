@@ -358,8 +358,10 @@ xattn_status check_latent(int B, int S, int nh, int dn, int dr, int dv, float sc
   return check_bf16_scale(scale);
 }
 
-// A page table [B, max_pages] over num_pages pages, for calls that move no rows.
+// A page table [B, max_pages] over num_pages pages, for calls that move no rows. (Sums of B and a block's or
+// a warp's width stay inside int32.)
 xattn_status check_table(int B, int num_pages, int page_size, int max_pages) {
+  if (B > (1 << 30)) return XATTN_ERR_BAD_SHAPE;
   return check_pages(B, 1, 1, 1, num_pages, page_size, max_pages);
 }
 

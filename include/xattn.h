@@ -431,7 +431,8 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
  * that are no page are skipped. A release of what a reserve granted restores the stack. What would not
  * fit the stack (a page given back twice) is dropped.
  *
- * page_size as above (else XATTN_ERR_PAGES); int arrays 4-byte aligned, slots 8-byte. Two sequences must not
+ * B at most 2^30 (else XATTN_ERR_BAD_SHAPE), page_size as above (else XATTN_ERR_PAGES); int arrays 4-byte aligned,
+ * slots 8-byte. Two sequences must not
  * share a page that is released. Scratch is stream-ordered, from the library's pool.
  */
 xattn_status xattn_cache_reserve(int *page_table, const int *ctx_lens, const int *new_lens, const int *free_pages,

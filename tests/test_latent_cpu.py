@@ -226,3 +226,12 @@ def test_plain_reserve_and_release():
     assert count == 1 and granted == [20, 3, 0] and t[2] == [-1, -1, -1] and slots[23:] == [-1] * 19
     # The slot map ends inside sequence 1's tokens.
     assert reserve_reference(table, [5, 20, 0], [20, 3, 17], free, 5, 16, 22, 8)[4] == [20, 0, 0]
+
+
+def test_more_sequences_than_the_tables_count(lib):
+    """Beyond 2^30 sequences sums of their number and a block's width would wrap: the plan would serve nobody, the search in
+    the offsets start before them."""
+    for B in (2**30 + 1, 2**31 - 1024, 2**31 - 1):
+        assert _reserve(lib, B=B, width=1) == 2 and _release(lib, B=B, width=1) == 2
+    if not torch.cuda.is_available():
+        assert _reserve(lib, B=2**30, width=1) == NO_GPU and _release(lib, B=2**30, width=1) == NO_GPU
