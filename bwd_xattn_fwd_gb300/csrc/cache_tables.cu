@@ -59,6 +59,7 @@ __device__ __forceinline__ Pair reserve_need(const ReserveArgs &a, int b, int *r
 __device__ __forceinline__ long long reserve_slot(const ReserveArgs &a, int b, int at, int first, int count) {
   const int ctx = clamp_len(a.ctx_lens[b], a.max_pages * a.page_size), pos = ctx + at, page = pos / a.page_size;
   const int row = pos - page * a.page_size, held = pages_of(ctx, a.page_size);
+  XATTN_DCHECK(b >= 0 && b < a.B && at >= 0 && pos >= ctx && page < a.max_pages && first >= 0 && first <= a.num_pages, a.status);
   int *entry = a.page_table + static_cast<size_t>(b) * a.max_pages + page;
   int id;
   if (page >= held) {
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(kThreads) reserve_plan_kernel(const ReserveArg
     if (ok && need.x > 0) taken = static_cast<int>(upto.x);
     const int first = ok ? static_cast<int>(min(upto.x - need.x, static_cast<long long>(a.num_pages))) : 0;
     const int end = static_cast<int>(min(upto.y, 0x7fffffffll));
+    XATTN_DCHECK(b >= 0 && room >= 0 && upto.x >= need.x && end >= 0 && (!kFill || a.B <= kThreads), a.status);
     a.granted[b] = ok ? room : 0;
     a.offsets[b + 1] = end;
     if constexpr (kFill)
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kThreads) reserve_plan_kernel(const ReserveArg
           if (starts[mid] <= t) lo = mid;
           else hi = mid;
         }
+        XATTN_DCHECK(lo < a.B && starts[lo] <= t && t < starts[lo + 1], a.status);
         if (t - starts[lo] < got[lo]) slot = reserve_slot(a, lo, t - starts[lo], firsts[lo], count);
       }
       a.slots[t] = slot;
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const Reserv
     int hi = a.B;                                            // offsets[lo] <= t0 < offsets[hi]
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi);
+      XATTN_DCHECK(at >= 0 && at <= a.B, a.status);
       const unsigned below = __ballot_sync(0xffffffffu, at < hi && a.offsets[at] <= t0);   // lanes 0 .. k
       const int k = 31 - __clz(below);
       lo += k * step;
@@ -167,6 +171,7 @@ __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const Reserv
     if (t < end) {
       while (next <= t) next = a.offsets[++lo + 1];
       const int at = static_cast<int>(t) - a.offsets[lo];
+      XATTN_DCHECK(lo < a.B && at >= 0, a.status);
       if (at < a.granted[lo]) slot[e] = reserve_slot(a, lo, at, a.first[lo], count);
     }
   }
@@ -182,6 +187,7 @@ __device__ __forceinline__ int *release_row(const ReleaseArgs &a, int b, int *fr
   const int most = a.max_pages * a.page_size;
   *from = pages_of(clamp_len(a.keep_lens[b], most), a.page_size);
   *to = pages_of(clamp_len(a.held_lens[b], most), a.page_size);
+  XATTN_DCHECK(b >= 0 && b < a.B && *from >= 0 && *to <= a.max_pages, a.status);
   return a.page_table + static_cast<size_t>(b) * a.max_pages;
 }
 
@@ -219,6 +225,7 @@ __global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleaseAr
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const int count = clamp_len(a.free_count[0], a.num_pages);
+  XATTN_DCHECK(a.B <= kThreads, a.status);
   for (int b = warp; b < a.B; b += kThreads / 32) {
     const int n = release_count(a, b, lane);
     if (lane == 0) ranks[b] = n;
@@ -307,6 +314,9 @@ __global__ void __launch_bounds__(kFillThreads) cache_write_kernel(const WriteAr
     const bool second = v >= a.vecs0;
     if (second) v -= a.vecs0;
     x[e] = second ? a.src1[r * a.vecs1 + v] : a.src0[r * a.vecs0 + v];
+    XATTN_DCHECK(r >= 0 && v < (second ? a.vecs1 : a.vecs0) && static_cast<int>(a.vecs0) <= a.stride0 &&
+                     static_cast<int>(a.vecs1) <= a.stride1,
+                 a.status);
     if (slot >= 0 && slot < a.num_slots) to[e] = second ? a.dst1 + slot * a.stride1 + v : a.dst0 + slot * a.stride0 + v;
   }
 #pragma unroll

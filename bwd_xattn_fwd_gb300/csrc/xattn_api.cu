@@ -935,7 +935,7 @@ xattn_status xattn_cache_reserve(int *page_table, const int *ctx_lens, const int
   void *base = nullptr;
   if (!small) XATTN_TRY(scratch_alloc(*dev, (static_cast<size_t>(B) + 1) * sizeof(int), st, &base));
   const ReserveArgs a = {page_table, ctx_lens, new_lens, free_pages, free_count, slots, offsets, granted,
-                         static_cast<int *>(base), B, max_pages, page_size, num_pages, tokens};
+                         static_cast<int *>(base), B, max_pages, page_size, num_pages, tokens, dev->status};
   xattn_status r = cuda_status(launch_cache_reserve(a, st));
   const cudaError_t fe = small ? cudaSuccess : cudaFreeAsync(base, st);
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
@@ -954,7 +954,7 @@ xattn_status xattn_cache_release(int *page_table, const int *held_lens, const in
   void *base = nullptr;
   if (!small) XATTN_TRY(scratch_alloc(*dev, (static_cast<size_t>(B) + 1) * sizeof(int), st, &base));
   const ReleaseArgs a = {page_table, held_lens, keep_lens, free_pages, free_count, static_cast<int *>(base), B, max_pages,
-                         page_size, num_pages};
+                         page_size, num_pages, dev->status};
   xattn_status r = cuda_status(launch_cache_release(a, st));
   const cudaError_t fe = small ? cudaSuccess : cudaFreeAsync(base, st);
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
@@ -975,7 +975,8 @@ xattn_status xattn_cache_write(const void *k_new, const void *v_new, void *k_pag
   const int vecs = nkv * hd / 8;
   const WriteArgs a = {static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k_pages),
                        static_cast<uint4 *>(v_pages), static_cast<unsigned>(vecs), static_cast<unsigned>(vecs), vecs, vecs,
-                       slots, rows, static_cast<long long>(num_pages) * page_size};
+                       slots, rows, static_cast<long long>(num_pages) * page_size,
+                       dev->status};
   return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -990,7 +991,8 @@ xattn_status xattn_latent_write(const void *c, const void *k_rope, void *pages, 
   const int vecs = (dc + dr) / 8;
   const WriteArgs a = {static_cast<const uint4 *>(c), static_cast<const uint4 *>(k_rope), static_cast<uint4 *>(pages),
                        static_cast<uint4 *>(pages) + dc / 8, static_cast<unsigned>(dc / 8), static_cast<unsigned>(dr / 8),
-                       vecs, vecs, slots, rows, static_cast<long long>(num_pages) * page_size};
+                       vecs, vecs, slots, rows, static_cast<long long>(num_pages) * page_size,
+                       dev->status};
   return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
 }
 

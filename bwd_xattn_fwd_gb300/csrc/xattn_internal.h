@@ -272,6 +272,7 @@ struct ReserveArgs {
   int *first;                                  // scratch: [B] pages taken before each sequence's; [B]: free pages before
   int B, max_pages, page_size, num_pages;
   long long tokens;
+  int *status;
 };
 bool reserve_small(int B, long long tokens);   // needs no scratch
 cudaError_t launch_cache_reserve(const ReserveArgs &a, cudaStream_t stream);
@@ -282,6 +283,7 @@ struct ReleaseArgs {
   int *free_pages, *free_count;
   int *counts;                                 // scratch: [B] pages given back; [B]: free pages before
   int B, max_pages, page_size, num_pages;
+  int *status;
 };
 bool release_small(int B, int max_pages);      // needs no scratch
 cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream);
@@ -294,6 +296,7 @@ struct WriteArgs {
   int stride0, stride1;
   const long long *slots;
   long long rows, num_slots;
+  int *status;
 };
 cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream);
 
