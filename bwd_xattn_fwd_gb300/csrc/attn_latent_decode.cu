@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const L
 }
 
 template <int N>
-cudaError_t launch_latent_n(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, cudaStream_t stream) {
+cudaError_t launch_latent_n(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int sms, cudaStream_t stream) {
   using L = LatLayout<N>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t err = allow_smem(latent_decode_kernel<N>, L::kDynBytes, allowed);
@@ -752,7 +752,7 @@ cudaError_t launch_latent_n(const LatentDecodeMaps &maps, const LatentDecodeArgs
   const int rows = a.n * a.nh, each = kCombineThreads / (a.dc / 4);
   const long long blocks = static_cast<long long>(groups - 1) * ((rows + each - 1) / each);
   const bool wide = groups >= 4 * a.B;
-  const int passes = wide ? 1 : static_cast<int>(min(max(blocks / (152 * 8), 1ll), 8ll));
+  const int passes = wide ? 1 : static_cast<int>(min(max(blocks / (sms * 8), 1ll), 8ll));
   return launch_pdl(wide ? latent_combine_kernel<true> : latent_combine_kernel<false>,
                     dim3(static_cast<unsigned>(groups - 1), static_cast<unsigned>((rows + each * passes - 1) / (each * passes))),
                     kCombineThreads, 0, stream, a, N, passes);
@@ -783,11 +783,11 @@ size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int 
          static_cast<size_t>(groups) * sizeof(int2);
 }
 
-cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int tile_rows,
+cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int tile_rows, int sms,
                                  cudaStream_t stream) {
-  if (tile_rows == 16) return launch_latent_n<16>(maps, a, groups, stream);
-  if (tile_rows == 32) return launch_latent_n<32>(maps, a, groups, stream);
-  return launch_latent_n<64>(maps, a, groups, stream);
+  if (tile_rows == 16) return launch_latent_n<16>(maps, a, groups, sms, stream);
+  if (tile_rows == 32) return launch_latent_n<32>(maps, a, groups, sms, stream);
+  return launch_latent_n<64>(maps, a, groups, sms, stream);
 }
 
 }  // namespace xattn

@@ -365,12 +365,12 @@ cudaError_t launch_cache_release(const ReleaseArgs &a, cudaStream_t stream) {
                     stream, a, each);
 }
 
-cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream) {
+cudaError_t launch_cache_write(const WriteArgs &a, int sms, cudaStream_t stream) {
   // One vector a thread where that is less than the GPU holds at once (64 rows of 576: 1.3 us, 2.5 with four), else two (65536
   // rows: 24.6 us, 6.2 TB/s; one 25.6, four 26.8, eight 32.2).
   const long long vecs = a.rows * (a.vecs0 + a.vecs1);
   constexpr int kMany = 2;
-  if (vecs <= 152 * 2048) return launch_pdl(cache_write_kernel<1>, blocks_for(vecs), kFillThreads, 0, stream, a);
+  if (vecs <= static_cast<long long>(sms) * 2048) return launch_pdl(cache_write_kernel<1>, blocks_for(vecs), kFillThreads, 0, stream, a);
   return launch_pdl(cache_write_kernel<kMany>, blocks_for((vecs + kMany - 1) / kMany), kFillThreads, 0, stream, a);
 }
 

@@ -912,7 +912,7 @@ xattn_status xattn_latent_decode(const void *q, const void *pages, const int *pa
     a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + records * dc);
     a.plan = reinterpret_cast<int2 *>(a.ws_ml + records);
   }
-  xattn_status r = cuda_status(launch_latent_decode(maps, a, groups, tile_rows, st));
+  xattn_status r = cuda_status(launch_latent_decode(maps, a, groups, tile_rows, dev->sms, st));
   const cudaError_t fe = scratch ? cudaFreeAsync(base, st) : cudaSuccess;
   if (r == XATTN_OK && fe != cudaSuccess) r = XATTN_ERR_CUDA;
   return r;
@@ -977,7 +977,7 @@ xattn_status xattn_cache_write(const void *k_new, const void *v_new, void *k_pag
                        static_cast<uint4 *>(v_pages), static_cast<unsigned>(vecs), static_cast<unsigned>(vecs), vecs, vecs,
                        slots, rows, static_cast<long long>(num_pages) * page_size,
                        dev->status};
-  return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_cache_write(a, dev->sms, static_cast<cudaStream_t>(stream)));
 }
 
 xattn_status xattn_latent_write(const void *c, const void *k_rope, void *pages, const long long *slots, int rows, int dc,
@@ -993,7 +993,7 @@ xattn_status xattn_latent_write(const void *c, const void *k_rope, void *pages, 
                        static_cast<uint4 *>(pages) + dc / 8, static_cast<unsigned>(dc / 8), static_cast<unsigned>(dr / 8),
                        vecs, vecs, slots, rows, static_cast<long long>(num_pages) * page_size,
                        dev->status};
-  return cuda_status(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_cache_write(a, dev->sms, static_cast<cudaStream_t>(stream)));
 }
 
 const char *xattn_status_string(xattn_status s) {

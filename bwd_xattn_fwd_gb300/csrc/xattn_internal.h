@@ -259,7 +259,7 @@ struct LatentDecodeArgs {
 int latent_tile_rows(int n, int nh);
 int latent_groups(const LatentDecodeArgs &a, int sms);
 size_t latent_decode_workspace_bytes(const LatentDecodeArgs &a, int groups, int tile_rows);
-cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int tile_rows,
+cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeArgs &a, int groups, int tile_rows, int sms,
                                  cudaStream_t stream);
 
 // Page tables, slot maps and rows written by slot (cache_tables.cu).
@@ -298,6 +298,6 @@ struct WriteArgs {
   long long rows, num_slots;
   int *status;
 };
-cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_write(const WriteArgs &a, int sms, cudaStream_t stream);
 
 }  // namespace xattn
