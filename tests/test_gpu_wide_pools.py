@@ -9,6 +9,14 @@ from paged_ref import check_tree
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _give_back():
+    yield
+    from bwd_xattn_fwd_gb300 import xattn
+    torch.cuda.empty_cache()
+    xattn.xattn_trim_scratch(0)
+
+
 def _need(gigabytes):
     if not torch.cuda.is_available():
         pytest.fail("CUDA device required for -m gpu tests")
@@ -69,3 +77,50 @@ def test_kv_rows_behind_2_to_the_31_numbers(rows):
         assert torch.equal(flat[slots], new)
         assert int((flat[:, 0, 0] != 0).sum()) == int((new[:, 0, 0] != 0).sum())
     assert xattn.xattn_check_device_status() == 0
+
+
+def test_expanded_tensors_of_more_than_2_to_the_31_numbers():
+    """1024 heads: the last heads of the last sequence, behind 2^31 numbers of every tensor and of the backward's scratch, have the
+    bits that they have in a call of their own."""
+    from bwd_xattn_fwd_gb300 import xattn
+    _need(90)
+    B, S, nh, dn, dr, dv = 9, 2050, 1024, 64, 64, 64
+    g = torch.Generator("cuda").manual_seed(0)
+
+    def fill(*shape, times=0.5):
+        t = torch.empty(*shape, dtype=torch.bfloat16, device="cuda")
+        for b in range(shape[0]):
+            t[b] = (torch.randn(shape[1:], generator=g, device="cuda") * times).bfloat16()
+        return t
+
+    q, kv, rope, dO = fill(B, S, nh, dn + dr), fill(B, S, nh, dn + dv), fill(B, S, dr), fill(B, S, nh, dv, times=1.0)
+    assert q[:-1].numel() > 2 ** 31 and B * S * nh * dr > 2 ** 30
+    o, lse = xattn.attention_latent_fwd(q, kv, rope)
+    dq, dkv, _ = xattn.attention_latent_bwd(q, kv, rope, o, dO, lse)
+    torch.cuda.synchronize()
+    assert xattn.xattn_check_device_status() == 0
+    cut = lambda t: t[-1:, :, -3:].contiguous()
+    o1, lse1 = xattn.attention_latent_fwd(cut(q), cut(kv), rope[-1:].contiguous())
+    dq1, dkv1, _ = xattn.attention_latent_bwd(cut(q), cut(kv), rope[-1:].contiguous(), o1, cut(dO), lse1)
+    for a, b in ((o, o1), (lse, lse1), (dq, dq1), (dkv, dkv1)):
+        assert torch.equal(cut(a), b)
+
+
+def test_absorbed_queries_of_more_than_2_to_the_31_numbers():
+    """64 tokens of 65536 heads, 65536 row tiles: the last heads of the last token against the definition."""
+    from bwd_xattn_fwd_gb300 import xattn
+    _need(40)
+    n, nh, dc, dr, page, ctx = 64, 65536, 512, 64, 16, 30
+    q = torch.empty(1, n, nh, dc + dr, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator("cuda").manual_seed(0)
+    for i in range(n):
+        q[0, i] = (torch.randn(nh, dc + dr, generator=g, device="cuda") * 0.5).bfloat16()
+    pages = (torch.randn(6, page, dc + dr, generator=g, device="cuda") * 0.5).bfloat16()
+    table = [[3, 1, 5, 0, 2, 4]]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    o, lse = xattn.attention_latent_decode(q, pages, i32(table), i32([ctx]), dc, 0.07)
+    torch.cuda.synchronize()
+    assert o[0, :-1].numel() > 2 ** 31 - 2 ** 26 and q.numel() > 2 ** 31 and xattn.xattn_check_device_status() == 0
+    for heads in (slice(0, 2), slice(nh - 3, nh)):
+        check_tree(o[:, :, heads], lse[:, :, heads],
+                   latent_decode_reference(q[:, :, heads].contiguous(), pages, table, [ctx], dc, 0.07), str(heads))
