@@ -1003,7 +1003,7 @@ const char *xattn_status_string(xattn_status s) {
     case XATTN_ERR_BAD_SHAPE: return "B, S, nh, nkv and hd must be positive and within size limits";
     case XATTN_ERR_GROUP: return "nh must be a multiple of nkv";
     case XATTN_ERR_UNSUPPORTED_HD: return "unsupported head dimension (bf16: 32, 64 or 128; the backward's stage calls and xattn_bwd_noalloc: 32 or 64; fp32: <= 128; latent attention: dn, dr, dv multiples of 16 up to 128, 64, 128, dc of 128 up to 512; rows of pages: multiples of 8)";
-    case XATTN_ERR_MISALIGNED: return "a bf16 tensor pointer is not 16-byte aligned, or a float or int array not 4-byte";
+    case XATTN_ERR_MISALIGNED: return "a pointer is not aligned: bf16 tensors to 16 bytes (latent attention's o, dq and dkv as outputs to 32), float and int arrays to 4, tree words and slot maps to 8";
     case XATTN_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case XATTN_ERR_NO_DEVICE_SUPPORT: return "the current device is not compute capability 10.3 (sm_103)";
     case XATTN_ERR_DEVICE_TIMEOUT: return "a bounded on-device wait expired";
