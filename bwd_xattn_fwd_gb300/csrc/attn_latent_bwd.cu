@@ -74,7 +74,7 @@ __global__ void __maxnreg__(168)
   const int dn_steps = dn / 16, dr_steps = dr / 16, dv_steps = dv / 16;
   const int k_subs = (dn + 63) / 64, v_subs = (dv + 63) / 64;
   const int num_m = (S + kTileRows - 1) / kTileRows, BH = a.B * nh, num_units = num_m * BH;
-  // Units, most key tiles first, dealt to and fro as in the kernel before.
+  // Units, most key tiles first; CTA c of G takes unit k G + c in even rounds and k G + G - 1 - c in odd ones.
   auto unit_at = [&](int k) {
     const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
     return k * G + ((k & 1) ? G - 1 - c : c);

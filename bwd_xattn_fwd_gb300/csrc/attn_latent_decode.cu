@@ -21,8 +21,9 @@
 //     device, so a captured graph follows them. A run's end cuts a sequence: such pieces write (max, sum, O)
 //     records, and latent_combine_kernel merges them in order.
 //   * Measured: 64 sequences of 8192 positions, one token of 16 heads, 512 + 64: 106 us, 5.7 TB/s; of 4096 62 us, and 79 with 64
-//     heads, 115 with 128 (two row tiles: 2560 cycles of shared-memory reads a tile of 64 rows, 3200 taken); one
-//     sequence of 1000 11 us. 14 us do not grow with the cache.
+//     heads, 115 with 128 (two row tiles: 2560 cycles of shared-memory reads a tile of 64 rows, 3200 taken). A batch of
+//     64 takes 15 us and 10.7 us for every 1000 positions beyond 2048 (7 TB/s; 9.5 us with 16 positions): the 15 are the start, the last
+//     tiles' chain, records and the combine. One sequence of 16 positions takes 9.5 us, of 1000 11.
 //   * Roundings: scores, maxima, sums and O are fp32; P is rounded to bf16, C's type.
 //   * Pages as in attn_tree.cu: a box whose table entry is no page is loaded from outside the pool (zeros).
 // Warps: 0 TMA producer; 1 TMEM owner and issuer of S^T; 10 issuer of O^T (apart, so that a tile's P is not kept waiting

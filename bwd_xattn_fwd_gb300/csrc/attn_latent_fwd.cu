@@ -17,6 +17,7 @@
 // pipe, as in attn_fwd_sm103.cu, was 1 % slower here, one in four 5 %.
 // Bound by the tensor cores, and between units by the softmax's turn: B4 S4093, 16 heads of 128 + 64 / 128 243 us, 1411 TFLOP/s of
 // visible pairs (71 % of the measured peak); 64 + 32 / 64 at S4096 133 us, 1293, at B8 S1024, 12 heads 24 us, 665.
+// Registers: a softmax thread holds a row of S (128). At the cap of 168 that 384 threads leave, NS = 2 spills 16 bytes and NS = 1 none.
 // TMEM: S_A [0,128) S_B [128,256) fp32 | O_A, O_B from 256, 64 NS columns each | NS = 1: P_A [384,448) P_B [448,512), so that the
 // next scores are issued as soon as these are read; NS = 2: P_X over the first half of S_X, the next scores behind P V.
 #include <type_traits>

@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kThreads) reserve_plan_kernel(const ReserveArg
 }
 
 // A warp has kTokensEach x 32 tokens in a row: their slots, and the table entries of pages that begin with them. It looks for
-// its first token's sequence 32 places at a time (two steps for 1024 sequences), and each thread goes on from there.
+// its first token's sequence 32 places at a time (two steps for 1024 sequences), and each thread goes on from there. (32 registers;
+// 8 bytes are spilled.)
 constexpr int kTokensEach = 4;
 __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const ReserveArgs a) {
   grid_dep_launch();

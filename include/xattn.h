@@ -378,11 +378,12 @@ xattn_status xattn_cache_compact(void *k_pages, void *v_pages, const int *page_t
  *   s_ij = scale (q_i[:dn] . kv_j[:dn] + q_i[dn:] . k_rope_j) (j <= i), and with P, dS as at the top:
  *   dq_i = scale sum_j dS_ij (kv_j[:dn], k_rope_j), dkv_j = (scale sum_i dS_ij q_i[:dn], sum_i P_ij dO_i),
  *   dk_rope_j = scale sum_h sum_i dS_ij q_i[dn:].
- * dn, dv multiples of 16 up to 128, dr of 16 up to 64 (else XATTN_ERR_UNSUPPORTED_HD); any S >= 1 up to 2^30;
- * any finite scale whose product with log2 e is finite (the backward too). bf16 tensors 16-byte aligned (the
- * forward's o, and dq and dkv: 32-byte), lse 4-byte. Arithmetic as in xattn_fwd and xattn_bwd; k_rope's
- * gradient is summed over the heads in fp32. Every
- * output is bit-for-bit reproducible. Scratch of the backward is stream-ordered, from the library's pool.
+ * kv and k_rope must be finite, as for the causal calls (rows behind a shorter sequence's end too: a hidden key's
+ * weight of 0 meets its value in the products). dn, dv multiples of 16 up to 128, dr of 16 up to 64 (else
+ * XATTN_ERR_UNSUPPORTED_HD); any S >= 1 up to 2^30; any finite scale whose product with log2 e is finite (the backward
+ * too). bf16 tensors 16-byte aligned (the forward's o, and dq and dkv: 32-byte), lse 4-byte. Arithmetic as in xattn_fwd
+ * and xattn_bwd; k_rope's gradient is summed over the heads in fp32. Every output is bit-for-bit reproducible. Scratch of
+ * the backward is stream-ordered, from the library's pool.
  */
 xattn_status xattn_latent_fwd(const void *q, const void *kv, const void *k_rope, int B, int S, int nh, int dn, int dr,
                               int dv, float scale, void *o, float *lse, void *stream);
